@@ -249,6 +249,131 @@ PA_API pa_status pa_copy_blocks(const void *src_k, const void *src_v, void *dst_
                                 const int32_t *pairs, int num_pairs, int32_t *dev_status,
                                 pa_stream_t stream);
 
+/*
+ * Position rotation (rotary embedding) of a step's queries and keys, with the
+ * cache write on the way: for token t with slot = slot_mapping[t] >= 0 and
+ * p = positions[t], R = rot_dim / 2, every head row x of q and key and every
+ * pair (a, b) = (x[i], x[i + R]) (interleaved = 0) or (x[2i], x[2i + 1])
+ * (interleaved = 1), i < R:
+ *     a' = a cos_sin[p][i] - b cos_sin[p][R + i],
+ *     b' = b cos_sin[p][i] + a cos_sin[p][R + i];
+ * dims from rot_dim on keep their values.  The products and sums are fp32 (or
+ * exact, rounded once to fp32), the result is rounded once to `dtype`.  Then
+ * q_out[t] holds the rotated queries, and the rotated key row and the value
+ * row are stored at the slot as pa_reshape_and_cache stores them.
+ *  q_out          device [num_tokens][num_heads][head_dim], what the attention
+ *                 calls take; q itself (in place) when q's rows are contiguous,
+ *                 else memory that q, key and value do not touch
+ *  q, key, value  device rows, token strides in elements (views of one fused
+ *                 QKV projection output, say); num_heads 0: no queries (q and
+ *                 q_out unused)
+ *  cos_sin        device fp32 [max_position][rot_dim]: R cosines, then R sines
+ *                 per position (the caller's frequencies and scaling)
+ *  positions      device int32 [num_tokens]
+ *  rot_dim        even, 0 .. head_dim; 0: no rotation (cos_sin, positions and
+ *                 max_position unused)
+ * A token with a negative slot is padding: its q_out row and the pools are left
+ * as they are and its position is not read.  A slot past the pool or a
+ * position outside [0, max_position) sets PA_ERR_OUT_OF_RANGE, and the token
+ * is skipped.  Any head_dim and block_size >= 1.  Precondition (not checked on
+ * the device): live slots are pairwise distinct, as for pa_reshape_and_cache.
+ */
+PA_API pa_status pa_rope_and_cache(void *q_out, const void *q, const void *key, const void *value,
+                                   int64_t q_stride_tok, int64_t key_stride_tok,
+                                   int64_t value_stride_tok, const float *cos_sin,
+                                   const int32_t *positions, int max_position, int rot_dim,
+                                   int interleaved, void *k_cache, void *v_cache,
+                                   const int64_t *slot_mapping, int num_tokens, int num_heads,
+                                   int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                   pa_dtype dtype, int32_t *dev_status, pa_stream_t stream);
+
+/*
+ * The cache held in 4 bits.  A 4-bit pool is device memory of num_blocks
+ * blocks of pa_q4_block_bytes(...) bytes, 16-byte aligned, laid out
+ * [num_blocks][num_kv_heads] slabs; a slab is B = block_size token rows of
+ * head_dim / 2 code bytes, then B rows of head_dim / 32 bf16 scales.  A group
+ * is 32 consecutive dims of one token and kv-head; with amax its largest
+ * magnitude,
+ *     s = bf16(amax / 7),  n = 8 + clamp(rint(x / s), -7, 7)  (n = 8 when s = 0),
+ * fp32 division, ties to even; nibble n stands for (n - 8) s.  A group with a
+ * NaN or an infinity takes a NaN scale and reads back as NaN.  Byte layout of
+ * a row (low nibble first, NG = head_dim / 32 groups):
+ *     K pool  32-bit words [4][NG], word (c, g): dims 32 g + 8 c .. + 7;
+ *     V pool  16-bit units [8][NG], unit (r, g): dims 32 g + 4 r .. + 3.
+ * Blocks, block tables, slots, sharing and pa_copy_blocks (block_bytes =
+ * pa_q4_block_bytes) work as for the 16/32-bit pools: 4.5 bits a value instead
+ * of 16.  block_size 8, 16 or 32 and head_dim 64 or 128 (PA_ERR_UNSUPPORTED
+ * otherwise).
+ */
+
+/* Bytes of one block of one 4-bit pool, or -1 for a shape that has none.  Host-only. */
+PA_API int64_t pa_q4_block_bytes(int block_size, int num_kv_heads, int head_dim);
+
+/*
+ * pa_rope_and_cache into 4-bit pools: the same rotation, q_out and token rules;
+ * the key row (rotated and rounded to `dtype`) and the value row are quantised
+ * into the slot's row.  The result equals pa_rope_and_cache into 16/32-bit
+ * pools followed by pa_quantize_blocks_q4, bit for bit.
+ *  k_cache, v_cache  4-bit pools, 16-byte aligned
+ */
+PA_API pa_status pa_rope_and_cache_q4(void *q_out, const void *q, const void *key, const void *value,
+                                      int64_t q_stride_tok, int64_t key_stride_tok,
+                                      int64_t value_stride_tok, const float *cos_sin,
+                                      const int32_t *positions, int max_position, int rot_dim,
+                                      int interleaved, void *k_cache, void *v_cache,
+                                      const int64_t *slot_mapping, int num_tokens, int num_heads,
+                                      int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                      pa_dtype dtype, int32_t *dev_status, pa_stream_t stream);
+
+/*
+ * Whole blocks from 16/32-bit pools to 4-bit pools: for each pair i, (src, dst)
+ * = (pairs[2i], pairs[2i+1]), every row of block src of src_k / src_v is
+ * quantised into block dst of dst_k / dst_v.  Pairs behave as in
+ * pa_copy_blocks (a negative entry skips the pair; one past its pool sets
+ * PA_ERR_OUT_OF_RANGE and skips it; destinations are distinct).  A prompt
+ * prefilled in a bf16 pool moves to the pool that its decode steps read.
+ *  src_k, src_v  [src_num_blocks][block_size][num_kv_heads][head_dim] of `dtype`
+ * All pools 16-byte aligned.
+ */
+PA_API pa_status pa_quantize_blocks_q4(const void *src_k, const void *src_v, void *dst_k, void *dst_v,
+                                       int block_size, int num_kv_heads, int head_dim,
+                                       int src_num_blocks, int dst_num_blocks, const int32_t *pairs,
+                                       int num_pairs, pa_dtype dtype, int32_t *dev_status,
+                                       pa_stream_t stream);
+
+/*
+ * The other way: blocks of 4-bit pools written out as (n - 8) s, rounded to
+ * `dtype`, into 16/32-bit pools -- for pa_varlen_prefill over a cached 4-bit
+ * prefix, or to hand a block to code that reads the wide layout.  Rows of a
+ * block that were never written come out as whatever their bytes stand for.
+ */
+PA_API pa_status pa_dequantize_blocks_q4(const void *src_k, const void *src_v, void *dst_k, void *dst_v,
+                                         int block_size, int num_kv_heads, int head_dim,
+                                         int src_num_blocks, int dst_num_blocks, const int32_t *pairs,
+                                         int num_pairs, pa_dtype dtype, int32_t *dev_status,
+                                         pa_stream_t stream);
+
+/* Workspace bytes pa_decode_q4 needs for these sizes (0 is never returned). */
+PA_API size_t pa_decode_q4_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                          int block_size, int max_blocks);
+
+/*
+ * Paged decode attention over 4-bit pools: pa_decode with K and V the values
+ * that the pools' codes and scales stand for.  Arguments, GQA mapping, error
+ * behaviour and workspace rules as pa_decode's; `dtype` is that of q and out
+ * (fp32 accumulation and softmax for both; with F32 the products are fp32 to
+ * the last few bits, with BF16 the softmax weights enter the second product
+ * in bf16 as in pa_decode).  Deterministic: results depend on the inputs and
+ * the device's SM count, never on which blocks hold the data.
+ *  k_cache, v_cache  4-bit pools, 16-byte aligned
+ */
+PA_API pa_status pa_decode_q4(void *out, const void *q, const void *k_cache, const void *v_cache,
+                              const int32_t *block_tables, const int32_t *context_lens, int num_seqs,
+                              int num_heads, int num_kv_heads, int head_dim, int block_size,
+                              int max_blocks, int num_blocks, float scale, pa_dtype dtype,
+                              void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                              pa_stream_t stream);
+
 /* Workspace bytes pa_varlen_prefill needs for these sizes. */
 PA_API size_t pa_varlen_prefill_workspace_size(int num_seqs, int total_q, int num_heads,
                                         int num_kv_heads, int head_dim, int block_size,

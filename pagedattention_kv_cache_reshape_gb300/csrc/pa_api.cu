@@ -8,6 +8,7 @@
 
 #include "pa.h"
 #include "pa_internal.h"
+#include "q4_format.cuh"
 
 namespace pa {
 
@@ -275,6 +276,155 @@ pa_status pa_copy_blocks(const void *src_k, const void *src_v, void *dst_k, void
     return from_cuda(launch_copy_blocks(src_k, src_v, dst_k, dst_v, block_bytes, src_num_blocks,
                                         dst_num_blocks, pairs, num_pairs, dev_status,
                                         (cudaStream_t)stream));
+}
+
+}  // extern "C"
+
+namespace {
+// Whether [a, a + an) and [b, b + bn) share a byte.
+bool overlaps(const void *a, int64_t an, const void *b, int64_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
+
+// The 4-bit pools' shapes: those the decode over them reads.
+pa_status check_q4_shape(int num_kv_heads, int head_dim, int block_size) {
+    if (num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0) return PA_ERR_INVALID_ARG;
+    if (block_size != 8 && block_size != 16 && block_size != 32) return PA_ERR_UNSUPPORTED;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+pa_status rope_and_cache(const RopeArgs &a, bool q4, pa_stream_t stream) {
+    const int eb = elem_bytes(a.dtype);
+    if (eb == 0 || a.num_tokens < 0 || a.num_heads < 0 || a.num_kv_heads <= 0 || a.head_dim <= 0 ||
+        a.block_size <= 0 || a.num_blocks <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (a.rot_dim < 0 || a.rot_dim % 2 != 0 || a.rot_dim > a.head_dim) return PA_ERR_INVALID_ARG;
+    if (a.rot_dim > 0 && a.max_position <= 0) return PA_ERR_INVALID_ARG;
+    if (a.interleaved != 0 && a.interleaved != 1) return PA_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)a.num_kv_heads * a.head_dim, q_row = (int64_t)a.num_heads * a.head_dim;
+    if (a.key_stride < row || a.value_stride < row) return PA_ERR_INVALID_ARG;
+    if (a.num_heads > 0 && a.q_stride < q_row) return PA_ERR_INVALID_ARG;
+    if (q4) {
+        const pa_status st = check_q4_shape(a.num_kv_heads, a.head_dim, a.block_size);
+        if (st != PA_OK) return st;
+    }
+    if (a.num_tokens == 0) return PA_OK;
+    if (!a.key || !a.value || !a.k_cache || !a.v_cache || !a.slot_mapping) return PA_ERR_INVALID_ARG;
+    if (a.num_heads > 0 && (!a.q || !a.q_out)) return PA_ERR_INVALID_ARG;
+    if (a.rot_dim > 0 && (!a.cos_sin || !a.positions)) return PA_ERR_INVALID_ARG;
+    const uintptr_t pool_align = q4 ? 16 : eb;
+    if (!aligned(a.key, eb) || !aligned(a.value, eb) || !aligned(a.k_cache, pool_align) ||
+        !aligned(a.v_cache, pool_align) || !aligned(a.slot_mapping, 8))
+        return PA_ERR_INVALID_ARG;
+    if (a.rot_dim > 0 && (!aligned(a.cos_sin, 4) || !aligned(a.positions, 4))) return PA_ERR_INVALID_ARG;
+    if (a.num_heads > 0) {
+        if (!aligned(a.q, eb) || !aligned(a.q_out, eb)) return PA_ERR_INVALID_ARG;
+        // in place (the same contiguous rows) or apart; nothing between
+        const int64_t n = a.num_tokens - 1, out_bytes = (n + 1) * q_row * eb;
+        const bool in_place = a.q_out == a.q && a.q_stride == q_row;
+        if (!in_place && overlaps(a.q_out, out_bytes, a.q, (n * a.q_stride + q_row) * eb))
+            return PA_ERR_INVALID_ARG;
+        if (overlaps(a.q_out, out_bytes, a.key, (n * a.key_stride + row) * eb) ||
+            overlaps(a.q_out, out_bytes, a.value, (n * a.value_stride + row) * eb))
+            return PA_ERR_INVALID_ARG;
+    }
+    return from_cuda(launch_rope_and_cache(a, q4, (cudaStream_t)stream));
+}
+
+pa_status q4_blocks(const Q4BlocksArgs &a, bool quantize, pa_stream_t stream) {
+    const int eb = elem_bytes(a.dtype);
+    if (eb == 0 || a.num_pairs < 0 || a.src_num_blocks < 0 || a.dst_num_blocks < 0) return PA_ERR_INVALID_ARG;
+    const pa_status st = check_q4_shape(a.num_kv_heads, a.head_dim, a.block_size);
+    if (st != PA_OK) return st;
+    if (a.num_pairs == 0) return PA_OK;
+    if (!a.src_k || !a.src_v || !a.dst_k || !a.dst_v || !a.pairs) return PA_ERR_INVALID_ARG;
+    if (!aligned(a.src_k, 16) || !aligned(a.src_v, 16) || !aligned(a.dst_k, 16) || !aligned(a.dst_v, 16) ||
+        !aligned(a.pairs, 4))
+        return PA_ERR_INVALID_ARG;
+    return from_cuda(launch_q4_blocks(a, quantize, (cudaStream_t)stream));
+}
+}  // namespace
+
+extern "C" {
+
+int64_t pa_q4_block_bytes(int block_size, int num_kv_heads, int head_dim) {
+    if (check_q4_shape(num_kv_heads, head_dim, block_size) != PA_OK) return -1;
+    return (int64_t)num_kv_heads * q4_slab_bytes(block_size, head_dim);
+}
+
+pa_status pa_rope_and_cache(void *q_out, const void *q, const void *key, const void *value,
+                            int64_t q_stride_tok, int64_t key_stride_tok, int64_t value_stride_tok,
+                            const float *cos_sin, const int32_t *positions, int max_position, int rot_dim,
+                            int interleaved, void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                            int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                            int num_blocks, pa_dtype dtype, int32_t *dev_status, pa_stream_t stream) {
+    const RopeArgs a{q_out, q, key, value, q_stride_tok, key_stride_tok, value_stride_tok, cos_sin, positions,
+                     max_position, rot_dim, interleaved, k_cache, v_cache, slot_mapping, num_tokens, num_heads,
+                     num_kv_heads, head_dim, block_size, num_blocks, dtype, dev_status};
+    return rope_and_cache(a, false, stream);
+}
+
+pa_status pa_rope_and_cache_q4(void *q_out, const void *q, const void *key, const void *value,
+                               int64_t q_stride_tok, int64_t key_stride_tok, int64_t value_stride_tok,
+                               const float *cos_sin, const int32_t *positions, int max_position, int rot_dim,
+                               int interleaved, void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                               int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                               int num_blocks, pa_dtype dtype, int32_t *dev_status, pa_stream_t stream) {
+    const RopeArgs a{q_out, q, key, value, q_stride_tok, key_stride_tok, value_stride_tok, cos_sin, positions,
+                     max_position, rot_dim, interleaved, k_cache, v_cache, slot_mapping, num_tokens, num_heads,
+                     num_kv_heads, head_dim, block_size, num_blocks, dtype, dev_status};
+    return rope_and_cache(a, true, stream);
+}
+
+pa_status pa_quantize_blocks_q4(const void *src_k, const void *src_v, void *dst_k, void *dst_v, int block_size,
+                                int num_kv_heads, int head_dim, int src_num_blocks, int dst_num_blocks,
+                                const int32_t *pairs, int num_pairs, pa_dtype dtype, int32_t *dev_status,
+                                pa_stream_t stream) {
+    const Q4BlocksArgs a{src_k, src_v, dst_k, dst_v, block_size, num_kv_heads, head_dim, src_num_blocks,
+                         dst_num_blocks, pairs, num_pairs, dtype, dev_status};
+    return q4_blocks(a, true, stream);
+}
+
+pa_status pa_dequantize_blocks_q4(const void *src_k, const void *src_v, void *dst_k, void *dst_v, int block_size,
+                                  int num_kv_heads, int head_dim, int src_num_blocks, int dst_num_blocks,
+                                  const int32_t *pairs, int num_pairs, pa_dtype dtype, int32_t *dev_status,
+                                  pa_stream_t stream) {
+    const Q4BlocksArgs a{src_k, src_v, dst_k, dst_v, block_size, num_kv_heads, head_dim, src_num_blocks,
+                         dst_num_blocks, pairs, num_pairs, dtype, dev_status};
+    return q4_blocks(a, false, stream);
+}
+
+size_t pa_decode_q4_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                   int max_blocks) {
+    (void)block_size;
+    (void)max_blocks;
+    return decode_q4_workspace(num_seqs < 0 ? 0 : num_seqs, num_heads < 1 ? 1 : num_heads,
+                               num_kv_heads < 1 ? 1 : num_kv_heads, head_dim < 1 ? 1 : head_dim);
+}
+
+pa_status pa_decode_q4(void *out, const void *q, const void *k_cache, const void *v_cache,
+                       const int32_t *block_tables, const int32_t *context_lens, int num_seqs, int num_heads,
+                       int num_kv_heads, int head_dim, int block_size, int max_blocks, int num_blocks,
+                       float scale, pa_dtype dtype, void *workspace, size_t workspace_bytes,
+                       int32_t *dev_status, pa_stream_t stream) {
+    const pa_status st = check_attention_shape(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                               max_blocks, num_blocks, dtype, scale);
+    if (st != PA_OK) return st;
+    if (num_seqs == 0) return PA_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens) return PA_ERR_INVALID_ARG;
+    const int eb = elem_bytes(dtype);
+    if (!aligned(out, eb) || !aligned(q, eb) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(block_tables, 4) || !aligned(context_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    const size_t need = pa_decode_q4_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                                    max_blocks);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return PA_ERR_WORKSPACE;
+    const AttnArgs a{out, q, k_cache, v_cache, block_tables, context_lens, nullptr, num_seqs, num_seqs, 1,
+                     num_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks, scale, dtype,
+                     dev_status};
+    return from_cuda(launch_decode_q4(a, workspace, workspace_bytes, (cudaStream_t)stream));
 }
 
 size_t pa_varlen_prefill_workspace_size(int num_seqs, int total_q, int num_heads,

@@ -135,6 +135,58 @@ PrefillPlanJob prefill_plan_job(const AttnArgs &a, void *workspace);
 cudaError_t launch_prefill_tc(const AttnArgs &a, void *workspace, size_t workspace_bytes,
                               cudaStream_t stream, bool planned = false);
 
+// Position rotation of queries and keys, and the cache write of the step's rows
+// (strides in elements).  num_heads 0: no queries; rot_dim 0: no rotation.
+struct RopeArgs {
+    void *q_out;
+    const void *q;
+    const void *key;
+    const void *value;
+    int64_t q_stride;
+    int64_t key_stride;
+    int64_t value_stride;
+    const float *cos_sin;       // [max_position][rot_dim]: cosines, then sines
+    const int32_t *positions;
+    int max_position;
+    int rot_dim;
+    int interleaved;
+    void *k_cache;
+    void *v_cache;
+    const int64_t *slot_mapping;
+    int num_tokens;
+    int num_heads;
+    int num_kv_heads;
+    int head_dim;
+    int block_size;
+    int num_blocks;
+    pa_dtype dtype;
+    int32_t *status;
+};
+// q4: the pools hold 4-bit rows (q4_format.cuh); head_dim 64 or 128 then.
+cudaError_t launch_rope_and_cache(const RopeArgs &a, bool q4, cudaStream_t stream);
+
+// Whole blocks between wide pools and 4-bit pools, along (source, destination) pairs.
+struct Q4BlocksArgs {
+    const void *src_k;
+    const void *src_v;
+    void *dst_k;
+    void *dst_v;
+    int block_size;
+    int num_kv_heads;
+    int head_dim;
+    int src_num_blocks;
+    int dst_num_blocks;
+    const int32_t *pairs;
+    int num_pairs;
+    pa_dtype dtype;             // of the wide pools
+    int32_t *status;
+};
+cudaError_t launch_q4_blocks(const Q4BlocksArgs &a, bool quantize, cudaStream_t stream);
+
+// Paged decode over 4-bit pools (a.cu_seqlens_q is not used).
+size_t decode_q4_workspace(int num_seqs, int num_heads, int num_kv_heads, int head_dim);
+cudaError_t launch_decode_q4(const AttnArgs &a, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 // Launch as a programmatic dependent of the previous kernel in the stream:
 // the kernel calls griddepcontrol.wait before it reads that kernel's output.
 template <typename... KArgs, typename... Args>

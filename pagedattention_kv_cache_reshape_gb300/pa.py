@@ -30,6 +30,8 @@ EXPORTS = (
     "pa_block_manager_create", "pa_block_manager_destroy", "pa_block_manager_num_free",
     "pa_block_manager_refcount", "pa_allocate_slots", "pa_free_sequence", "pa_share_prefix",
     "pa_block_manager_tables", "pa_validate_inputs", "pa_allocate_slots_batch", "pa_set_wait_test",
+    "pa_rope_and_cache", "pa_q4_block_bytes", "pa_rope_and_cache_q4", "pa_quantize_blocks_q4",
+    "pa_dequantize_blocks_q4", "pa_decode_q4_workspace_size", "pa_decode_q4",
 )
 STATIC_SCRATCH_BYTES = 24 << 20
 STALL_NONE, STALL_PRODUCER, STALL_CONSUMER = 0, 1, 2
@@ -116,6 +118,21 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         L.pa_decode_static_scratch.restype = i32
         L.pa_decode_static_scratch.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32,
                                                f32, i32, vp, vp]
+        L.pa_rope_and_cache.restype = i32
+        L.pa_rope_and_cache.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp, i32, i32, i32, vp, vp, vp, i32, i32,
+                                        i32, i32, i32, i32, i32, vp, vp]
+        L.pa_rope_and_cache_q4.restype = i32
+        L.pa_rope_and_cache_q4.argtypes = L.pa_rope_and_cache.argtypes
+        L.pa_q4_block_bytes.restype = i64
+        L.pa_q4_block_bytes.argtypes = [i32, i32, i32]
+        L.pa_quantize_blocks_q4.restype = i32
+        L.pa_quantize_blocks_q4.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, i32, i32, vp, vp]
+        L.pa_dequantize_blocks_q4.restype = i32
+        L.pa_dequantize_blocks_q4.argtypes = L.pa_quantize_blocks_q4.argtypes
+        L.pa_decode_q4_workspace_size.restype = sz
+        L.pa_decode_q4_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
+        L.pa_decode_q4.restype = i32
+        L.pa_decode_q4.argtypes = L.pa_decode.argtypes
         L.pa_validate_inputs.restype = i32
         L.pa_validate_inputs.argtypes = [vp, i32, i32, vp, vp, i32, i32, i32, ctypes.POINTER(ctypes.c_int),
                                          ctypes.POINTER(ctypes.c_int64)]
@@ -347,6 +364,158 @@ def varlen_step(q, key, value, k_cache, v_cache, cu_seqlens_q, block_tables, con
         workspace.numel() * workspace.element_size(), _opt(dev_status), _stream(stream))
     _check(rc, "pa_varlen_step")
     return slot_mapping, out
+
+
+def _rows(t, name: str, tokens: int, heads: int, d: int, dtype) -> None:
+    if t.dim() != 3 or t.shape != (tokens, heads, d) or t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {d}] with contiguous rows")
+    if t.dtype != dtype:
+        raise TypeError("q, key, value and the 16/32-bit pools must share one dtype")
+
+
+def _current(*tensors) -> None:
+    # launches go to the current device's stream: a tensor of another device is refused, not reached across
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
+
+
+def _tok_stride(t) -> int:
+    # one token: any stride will do, and torch may report one shorter than a row
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _q4_pool_shape(k_cache, v_cache, head_dim: int):
+    """(num_blocks, block_size, num_kv_heads) of a pair of 4-bit pools."""
+    if k_cache.dim() != 3 or k_cache.shape != v_cache.shape:
+        raise ValueError("4-bit pools must be uint8 [num_blocks, num_kv_heads, slab] of one shape")
+    num_blocks, hkv, slab = k_cache.shape
+    row = head_dim // 2 + head_dim // 32 * 2
+    if row <= 0 or slab % row:
+        raise ValueError(f"a slab of {slab} bytes does not hold token rows of head_dim {head_dim}")
+    return num_blocks, slab // row, hkv
+
+
+def _rope(fn, q, key, value, cos_sin, positions, pools, num_blocks, block_size, slot_mapping, interleaved, q_out,
+          dev_status, stream):
+    n, hkv, d = key.shape
+    _rows(key, "key", n, hkv, d, key.dtype)
+    _rows(value, "value", n, hkv, d, key.dtype)
+    heads = 0
+    if q is not None:
+        heads = q.shape[1] if q.dim() == 3 else 0
+        _rows(q, "q", n, heads, d, key.dtype)
+        if q_out is None:
+            q_out = torch.empty((n, heads, d), dtype=q.dtype, device=q.device)
+        _rows(q_out, "q_out", n, heads, d, key.dtype)
+        _contig(q_out, "q_out")
+    if slot_mapping.numel() < n or (cos_sin is not None and positions.numel() < n):
+        raise ValueError("slot_mapping and positions must have an entry per token")
+    _current(q, q_out, key, value, cos_sin, positions, slot_mapping, *pools)
+    rot = max_pos = 0
+    if cos_sin is not None:
+        max_pos, rot = cos_sin.shape
+    rc = getattr(load(), fn)(
+        None if q is None else _dev(q_out, "q_out"), None if q is None else _dev(q, "q"), _dev(key, "key"),
+        _dev(value, "value"), 0 if q is None else _tok_stride(q), _tok_stride(key), _tok_stride(value),
+        None if cos_sin is None else _contig(cos_sin, "cos_sin", torch.float32),
+        None if cos_sin is None else _contig(positions, "positions", torch.int32), max_pos, rot,
+        1 if interleaved else 0, pools[0].data_ptr(), pools[1].data_ptr(), _contig(slot_mapping, "slot_mapping", torch.int64), n, heads,
+        hkv, d, block_size, num_blocks, _dtype_code(key), _opt(dev_status), _stream(stream))
+    _check(rc, fn)
+    return q_out
+
+
+def rope_and_cache(q, key, value, cos_sin, positions, k_cache, v_cache, slot_mapping, interleaved: bool = False,
+                   q_out=None, dev_status=None, stream=None):
+    """pa_rope_and_cache: q [tokens, H, D] (or None) and key rotated by position, K/V rows written to the pools;
+    returns q_out.  q, key and value may be token-strided views; cos_sin is fp32 [max_position, rot_dim] (None: no
+    rotation) and positions int32 [tokens]."""
+    num_blocks, block_size, hkv, d = k_cache.shape
+    if k_cache.shape != v_cache.shape or key.dim() != 3 or key.shape[1:] != (hkv, d):
+        raise ValueError("key, value and the pools disagree on heads or head_dim")
+    if not (key.dtype == k_cache.dtype == v_cache.dtype):
+        raise TypeError("q, key, value and the 16/32-bit pools must share one dtype")
+    _contig(k_cache, "k_cache"), _contig(v_cache, "v_cache")
+    return _rope("pa_rope_and_cache", q, key, value, cos_sin, positions, (k_cache, v_cache), num_blocks, block_size,
+                 slot_mapping, interleaved, q_out, dev_status, stream)
+
+
+def q4_block_bytes(block_size: int, num_kv_heads: int, head_dim: int) -> int:
+    return int(load().pa_q4_block_bytes(int(block_size), int(num_kv_heads), int(head_dim)))
+
+
+def rope_and_cache_q4(q, key, value, cos_sin, positions, k_cache, v_cache, slot_mapping, interleaved: bool = False,
+                      q_out=None, dev_status=None, stream=None):
+    """pa_rope_and_cache_q4: rope_and_cache into 4-bit pools (uint8 [num_blocks, num_kv_heads,
+    q4_block_bytes(block_size, 1, head_dim)])."""
+    if key.dim() != 3:
+        raise ValueError("key must be [tokens, num_kv_heads, head_dim]")
+    num_blocks, block_size, hkv = _q4_pool_shape(k_cache, v_cache, key.shape[2])
+    if key.shape[1] != hkv:
+        raise ValueError("key and the pools disagree on num_kv_heads")
+    _contig(k_cache, "k_cache", torch.uint8), _contig(v_cache, "v_cache", torch.uint8)
+    return _rope("pa_rope_and_cache_q4", q, key, value, cos_sin, positions, (k_cache, v_cache), num_blocks, block_size,
+                 slot_mapping, interleaved, q_out, dev_status, stream)
+
+
+def _q4_blocks(fn, wide_k, wide_v, q4_k, q4_v, quantize, pairs, dev_status, stream):
+    num_wide, block_size, hkv, d = wide_k.shape
+    num_q4, b4, h4 = _q4_pool_shape(q4_k, q4_v, d)
+    if wide_k.shape != wide_v.shape or (b4, h4) != (block_size, hkv):
+        raise ValueError("the 16/32-bit and 4-bit pools must share block size, heads and head_dim")
+    if wide_k.dtype != wide_v.dtype:
+        raise TypeError("the 16/32-bit pools must share one dtype")
+    wide = (_contig(wide_k, "16/32-bit pool"), _contig(wide_v, "16/32-bit pool"))
+    q4 = (_contig(q4_k, "4-bit pool", torch.uint8), _contig(q4_v, "4-bit pool", torch.uint8))
+    pairs = pairs.reshape(-1, 2)
+    _current(wide_k, wide_v, q4_k, q4_v, pairs)
+    src, dst = (wide, q4) if quantize else (q4, wide)
+    n_src, n_dst = (num_wide, num_q4) if quantize else (num_q4, num_wide)
+    rc = getattr(load(), fn)(*src, *dst, block_size, hkv, d, n_src, n_dst, _contig(pairs, "pairs", torch.int32),
+                             int(pairs.shape[0]), _dtype_code(wide_k), _opt(dev_status), _stream(stream))
+    _check(rc, fn)
+
+
+def quantize_blocks_q4(src_k, src_v, dst_k, dst_v, pairs, dev_status=None, stream=None):
+    """pa_quantize_blocks_q4: blocks of 16/32-bit pools [n, B, Hkv, D] into 4-bit pools; pairs device int32 [n, 2]."""
+    _q4_blocks("pa_quantize_blocks_q4", src_k, src_v, dst_k, dst_v, True, pairs, dev_status, stream)
+
+
+def dequantize_blocks_q4(src_k, src_v, dst_k, dst_v, pairs, dev_status=None, stream=None):
+    """pa_dequantize_blocks_q4: blocks of 4-bit pools into 16/32-bit pools [n, B, Hkv, D]; pairs device int32 [n, 2]."""
+    _q4_blocks("pa_dequantize_blocks_q4", dst_k, dst_v, src_k, src_v, False, pairs, dev_status, stream)
+
+
+def decode_q4_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks) -> int:
+    return int(load().pa_decode_q4_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                                  max_blocks))
+
+
+def decode_q4(q, k_cache, v_cache, block_tables, context_lens, scale: float, out=None, workspace=None,
+              dev_status=None, stream=None):
+    """pa_decode_q4: q [num_seqs, H, D] over 4-bit pools -> out [num_seqs, H, D]."""
+    num_seqs, H, D = q.shape
+    num_blocks, block_size, hkv = _q4_pool_shape(k_cache, v_cache, D)
+    if block_tables.shape[0] != num_seqs or context_lens.numel() != num_seqs:
+        raise ValueError("block_tables and context_lens must have a row per sequence")
+    max_blocks = block_tables.shape[1]
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and dtype")
+    _current(q, out, k_cache, v_cache, block_tables, context_lens, workspace)
+    if workspace is None:
+        workspace = _ws(None, decode_q4_workspace_size(num_seqs, H, hkv, D, block_size, max_blocks), q.device)
+    rc = load().pa_decode_q4(
+        _contig(out, "out"), _contig(q, "q"), _contig(k_cache, "k_cache", torch.uint8),
+        _contig(v_cache, "v_cache", torch.uint8), _contig(block_tables, "block_tables", torch.int32),
+        _contig(context_lens, "context_lens", torch.int32), num_seqs, H, hkv, D, block_size, max_blocks, num_blocks,
+        float(scale), _dtype_code(q), _contig(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+        _opt(dev_status), _stream(stream))
+    _check(rc, "pa_decode_q4")
+    return out
 
 
 def validate_inputs(block_tables, context_lens, slot_mapping, block_size: int, num_blocks: int):
