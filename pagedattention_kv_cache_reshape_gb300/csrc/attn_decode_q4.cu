@@ -1,6 +1,36 @@
 // attn_decode_q4.cu -- paged decode attention over 4-bit pools (q4_format.cuh):
 //     out[s][h] = sum_j softmax_j(scale <q[s][h], K_s[j][g]>) V_s[j][g]
 // with K and V the values their codes and scales stand for.
+//
+// What it has to move is 4.5 bits a cached value, 3.6 times less than a bf16
+// cache; the bound that comes up before HBM is the instruction issue of turning
+// nibbles into matrix operands, so the kernel is built to spend little there:
+//  * A nibble n becomes a bf16 operand with one and-or per pair: 0x4300 | n is
+//    128 + n exactly.  Scales are never multiplied into elements.  For the
+//    first product (S = K Q^T, tokens in M, q-heads in N, m16n8k16) the k steps
+//    of a group of 32 dims share their accumulator, and the group's scale is
+//    applied to the 4 sums of a lane; the surplus of 136 a code is taken off
+//    by starting the accumulator at -136 sum(q) of the group.  For the second
+//    (O^T += V^T P^T) the token's scale of V goes into the weight p, once per
+//    group, and the codes are brought to n - 8 exactly, because sums over many
+//    tokens would lose the small result under a surplus.
+//  * The softmax reference of a head moves only when a logit passes it by 8
+//    (base 2), found by one warp vote a unit: weights stay below 2^8 and sums
+//    are rescaled a few times a sequence instead of every unit.
+//  * A warp takes units of 16 tokens of one sequence and kv-head through a ring
+//    of its own in shared memory (16-byte asynchronous copies): nothing is
+//    shared between warps until their pieces are merged.
+//
+// The batch is one stream of units, (sequence, kv-head, 16 tokens); every CTA
+// takes an equal contiguous share and every warp of it an equal part, whatever
+// the mix of lengths.  A (sequence, kv-head) inside one warp is normalised and
+// stored; cut ones leave (m, l, o) pieces, merged first between the warps of a
+// CTA (shared memory), then by the last arriving CTA (workspace), always in
+// stream order, so results do not depend on timing.
+//
+// fp32 queries: q and the weights are split into three bf16 parts each (24
+// bits), whose products with the exact codes are summed in fp32; the codes of
+// K are brought to n - 8 too.
 #include <math.h>
 
 #include "pa_device.cuh"
@@ -10,80 +40,697 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kU = 16;              // tokens a unit: the M of the first product, the K of the second
+constexpr int kWarps = 8;
+constexpr int kStages = 4;
+constexpr int kPlanThreads = 1024;
+constexpr int kMaxCtas = 512;
+constexpr float kMoveAt = 8.0f;     // a logit this far (base 2) over the reference moves it
 
-// One CTA per (sequence, q-head); warp w takes tokens w, w + 4, ...; a lane
-// holds D/32 dims (dim 32 g + lane).
-template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) decode_q4_kernel(const AttnArgs a) {
-    constexpr int NG = D / kQ4Group;
-    __shared__ float o_s[kWarps][D], m_s[kWarps], l_s[kWarps];
+struct Q4Params {
+    const void *q;
+    void *out;
+    const uint8_t *k, *v;
+    const int32_t *block_tables, *context_lens;
+    const int64_t *prefix;     // [num_seqs + 1] units of one head before each sequence
+    int32_t *arrivals;         // [kMaxCtas] pieces of the sequence cut at a CTA's end, zeroed by the plan
+    float *part;               // [CTAs][2][heads][D + 2]
+    int num_seqs, num_heads, num_kv_heads;
+    int group;                 // q-heads per kv-head
+    int split;                 // parts a group is split into
+    int hw;                    // q-heads of a part
+    int log2b, max_blocks, num_blocks;
+    int64_t slab;
+    float scale_log2;
+    int vec;                   // q rows and out rows take wide loads and stores
+    int32_t *status;
+};
+
+__device__ __forceinline__ int units_of(int ctx, int max_tokens) {
+    return ctx <= 0 || ctx > max_tokens ? 0 : (ctx - 1) / kU + 1;
+}
+
+// Exclusive prefix of the sequences' units, and the arrival counters' zeros.
+__global__ void __launch_bounds__(kPlanThreads)
+    q4_plan_kernel(const int32_t *__restrict__ context_lens, int num_seqs, int max_tokens,
+                   int64_t *__restrict__ prefix, int32_t *__restrict__ arrivals, int32_t *status) {
+    __shared__ int64_t warp_tot[kPlanThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependency_wait();
     grid_dependents_launch();
-    const int s = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int B = a.block_size, H = a.num_kv_heads, hk = h / (a.num_heads / H);
-    const int ctx = a.context_lens[s];
-    if (ctx <= 0 || (int64_t)ctx > (int64_t)a.max_blocks * B) {
-        if (threadIdx.x == 0) set_status(a.status, PA_ERR_OUT_OF_RANGE);
-        return;
-    }
-    const int64_t slab = q4_slab_bytes(B, D);
-    const int64_t qo = ((int64_t)s * a.num_heads + h) * D;
-    float q[NG], o[NG], m = -INFINITY, l = 0.0f;
-    for (int g = 0; g < NG; ++g) {
-        q[g] = to_float(static_cast<const T *>(a.q)[qo + 32 * g + lane]) * a.scale;
-        o[g] = 0.0f;
-    }
-    for (int j = warp; j < ctx; j += kWarps) {
-        const int32_t blk = a.block_tables[(int64_t)s * a.max_blocks + j / B];
-        if (blk < 0 || blk >= a.num_blocks) {
-            if (lane == 0) set_status(a.status, PA_ERR_OUT_OF_RANGE);
-            continue;
+    if (tid < kMaxCtas) arrivals[tid] = 0;
+    int64_t running = 0;
+    for (int base = 0; base < num_seqs; base += kPlanThreads) {
+        const int s = base + tid;
+        int nu = 0;
+        if (s < num_seqs) {
+            nu = units_of(__ldg(context_lens + s), max_tokens);
+            if (nu == 0) set_status(status, PA_ERR_OUT_OF_RANGE);
         }
-        const int tok = j % B;
-        const int64_t at = ((int64_t)blk * H + hk) * slab;
-        const uint8_t *ks = static_cast<const uint8_t *>(a.k_cache) + at;
-        const uint8_t *vs = static_cast<const uint8_t *>(a.v_cache) + at;
-        float x = 0.0f, v[NG];
-        for (int g = 0; g < NG; ++g) {
-            const int d = 32 * g + lane;
-            const float ksc = q4_scale_value(reinterpret_cast<const uint16_t *>(ks + B * (D / 2))[tok * NG + g]);
-            const float vsc = q4_scale_value(reinterpret_cast<const uint16_t *>(vs + B * (D / 2))[tok * NG + g]);
-            const int kn = (ks[tok * (D / 2) + q4_k_word(d & ~7, D) + ((d & 7) >> 1)] >> (4 * (d & 1))) & 15;
-            const int vn = (vs[tok * (D / 2) + q4_v_unit(d & ~3, D) + ((d & 3) >> 1)] >> (4 * (d & 1))) & 15;
-            x += q[g] * ((kn - 8) * ksc);
-            v[g] = (vn - 8) * vsc;
+        int64_t incl = nu;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += y;
         }
-        for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-        const float mn = fmaxf(m, x), alpha = expf(m - mn), p = expf(x - mn);
-        l = l * alpha + p;
-        for (int g = 0; g < NG; ++g) o[g] = o[g] * alpha + p * v[g];
-        m = mn;
+        if (lane == 31) warp_tot[warp] = incl;
+        __syncthreads();
+        if (warp == 0) {
+            int64_t t = warp_tot[lane];
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, t, off);
+                if (lane >= off) t += y;
+            }
+            warp_tot[lane] = t;
+        }
+        __syncthreads();
+        if (s < num_seqs) prefix[s] = running + (warp ? warp_tot[warp - 1] : 0) + incl - nu;
+        running += warp_tot[kPlanThreads / 32 - 1];
+        __syncthreads();
     }
-    for (int g = 0; g < NG; ++g) o_s[warp][32 * g + lane] = o[g];
-    if (lane == 0) { m_s[warp] = m; l_s[warp] = l; }
+    if (tid == 0) prefix[num_seqs] = running;
+}
+
+__device__ __forceinline__ uint32_t nibbles_128(uint32_t w) {   // 128 + nibble 0 | 128 + nibble 4 << 16, bf16
+    uint32_t r;
+    asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xEA;" : "=r"(r) : "r"(w), "r"(0x43004300u));
+    return r;
+}
+__device__ __forceinline__ uint32_t minus_136(uint32_t a) {     // exact: 128 + n -> n - 8
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x43084308u));
+    return r;
+}
+__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1, float c0, float c1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %10, %11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void cp_async16(void *smem, const void *gmem) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float bf16_part(float &x) {          // the leading bf16 of x, taken off it
+    const float h = __bfloat162float(__float2bfloat16_rn(x));
+    x -= h;
+    return h;
+}
+
+// The last sequence s with prefix[s] <= t, by the warp, 33 ways a step.
+__device__ __forceinline__ int find_seq(const int64_t *prefix, int num_seqs, int64_t t, int lane) {
+    int lo = 0, hi = num_seqs;
+    while (hi - lo > 1) {
+        const int64_t n = hi - lo;
+        const bool le = prefix[lo + (int)(n * (lane + 1) / 33)] <= t;
+        const int c = __popc(__ballot_sync(0xffffffffu, le));
+        hi = c < 32 ? lo + (int)(n * (c + 1) / 33) : hi;
+        lo = c > 0 ? lo + (int)(n * c / 33) : lo;
+    }
+    return lo;
+}
+
+template <typename T, int D, int NT>
+struct Q4Shape {
+    static constexpr bool kF32 = sizeof(T) == 4;
+    static constexpr int NS = kF32 ? 3 : 1;           // bf16 parts of q and of a weight
+    static constexpr int NG = D / kQ4Group;
+    static constexpr int HW = 8 * NT;                 // q-heads a warp has room for
+    static constexpr int kCodes = kU * D / 2;         // bytes of a unit's codes, K or V
+    static constexpr int kScales = kU * NG * 2;
+    static constexpr int kStage = 2 * (kCodes + kScales);
+    static constexpr int kRing = kStages * kStage;
+    static constexpr int kPiece = HW * (D + 2);       // floats: o [HW][D], (m, l) [HW][2]
+    static constexpr int kSmem = kWarps * (kRing + kPiece * 4);
+    static constexpr int kCtasPerSm = NT == 1 && NS == 1 ? 2 : 1;
+    static_assert(kRing >= kPiece * 4, "a drained ring holds a piece");
+};
+
+struct PieceMeta { int seq, vh, u0, u1; };   // seq < 0: none
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4_decode_kernel(const Q4Params p) {
+    using S = Q4Shape<T, D, NT>;
+    constexpr int NG = S::NG, NS = S::NS, HW = S::HW;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ PieceMeta meta[2 * kWarps];
+    __shared__ int last_s[2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
+    uint8_t *ring = smem + warp * S::kRing;
+    float *first_piece = reinterpret_cast<float *>(smem + kWarps * S::kRing) + warp * S::kPiece;
+    const int VH = p.num_kv_heads * p.split, B = 1 << p.log2b, max_tokens = p.max_blocks << p.log2b;
+    if (lane == 0) meta[2 * warp].seq = meta[2 * warp + 1].seq = -1;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int64_t total = p.prefix[p.num_seqs] * VH;
+    // at least a unit a warp: small batches use fewer CTAs and merge in shared memory
+    const int64_t share = max((int64_t)kWarps, (total + gridDim.x - 1) / gridDim.x);
+    const int64_t cta0 = min(total, share * blockIdx.x), cta1 = min(total, cta0 + share);
+    if (cta0 == cta1) return;
+    const int64_t w0 = cta0 + (cta1 - cta0) * warp / kWarps, w1 = cta0 + (cta1 - cta0) * (warp + 1) / kWarps;
+    const int n = (int)(w1 - w0);
+
+    if (n > 0) {
+        // ---- where the warp's part begins
+        int s = find_seq(p.prefix, p.num_seqs, w0 / VH, lane);
+        int ctx = __ldg(p.context_lens + s), nu = units_of(ctx, max_tokens);
+        const int64_t in_seq = w0 - p.prefix[s] * VH;
+        int vh = (int)(in_seq / nu), u = (int)(in_seq - (int64_t)vh * nu);
+        // ---- the copies' own place in the stream, kStages - 1 units ahead
+        int cs = s, cctx = ctx, cnu = nu, cvh = vh, cu = u, left = n, slot = 0;
+        int ids = -1, ids_seq = -1, ids_base = 0;
+        auto issue = [&]() {
+            if (left > 0) {
+                --left;
+                const int b = (int)(((int64_t)cu * kU) >> p.log2b);
+                if (cs != ids_seq || (unsigned)(b - ids_base) >= 32u) {
+                    ids_seq = cs;
+                    ids_base = b & ~31;
+                    const int64_t e = ids_base + lane;
+                    ids = -1;
+                    if ((e << p.log2b) < cctx) {
+                        ids = __ldg(p.block_tables + (int64_t)cs * p.max_blocks + e);
+                        if (ids < 0 || ids >= p.num_blocks) {
+                            set_status(p.status, PA_ERR_OUT_OF_RANGE);
+                            ids = -1;
+                        }
+                    }
+                }
+                // tokens 0..7 and 8..15 of the unit: one block's rows, or two blocks of 8
+                const int id0 = __shfl_sync(0xffffffffu, ids, b - ids_base);
+                const int id1 = __shfl_sync(0xffffffffu, ids, (b - ids_base + (p.log2b == 3)) & 31);
+                const int hk = cvh / p.split, tok = (cu * kU) & (B - 1), tok1 = p.log2b == 3 ? 0 : tok + 8;
+                const int64_t at0 = ((int64_t)id0 * p.num_kv_heads + hk) * p.slab;
+                const int64_t at1 = ((int64_t)id1 * p.num_kv_heads + hk) * p.slab;
+                uint8_t *st = ring + slot * S::kStage;
+#pragma unroll
+                for (int j = lane; j < S::kCodes / 16; j += 32) {   // row j / (D/32)
+                    const int t = j / NG;
+                    const int id = t < 8 ? id0 : id1;
+                    const int64_t at = (t < 8 ? at0 + tok * (D / 2) : at1 + tok1 * (D / 2)) + (j % (8 * NG)) * 16;
+                    const int kd = D == 64 ? j ^ (4 * ((t >> 2) & 1)) : j, vd = j ^ (2 * ((t >> 2) & 3));
+                    if (id >= 0) {
+                        cp_async16(st + kd * 16, p.k + at);
+                        cp_async16(st + S::kCodes + vd * 16, p.v + at);
+                    }
+                }
+                if (lane < 4 * NG) {
+                    const int j = lane % (2 * NG), half = j / NG;
+                    const int64_t at = (half ? at1 + tok1 * (NG * 2) : at0 + tok * (NG * 2)) + B * (D / 2) + (j % NG) * 16;
+                    if ((half ? id1 : id0) >= 0)
+                        cp_async16(st + 2 * S::kCodes + lane * 16, (lane < 2 * NG ? p.k : p.v) + at);
+                }
+                slot = slot + 1 == kStages ? 0 : slot + 1;
+                if (++cu == cnu) {
+                    cu = 0;
+                    if (++cvh == VH && left > 0) {
+                        cvh = 0;
+                        do {
+                            cctx = __ldg(p.context_lens + ++cs);
+                            cnu = units_of(cctx, max_tokens);
+                        } while (cnu == 0);
+                    }
+                }
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) issue();
+
+        uint32_t qf[NT][NS][NG][4];        // the B operand of the first product: pair i holds dims (i, i + 4) of a lane's 8
+        float q0[NT][NG][2];               // -136 sum(q) of a group, for the lane's two columns
+        float o[NT][2 * NG][4], m[NT][2], l[NT][2];
+        bool fresh = true;
+        int u_first = 0, read = 0;
+        for (int i = 0; i < n; ++i) {
+            if (fresh) {
+                fresh = false;
+                u_first = u;
+                const int part = vh % p.split, h0 = (vh / p.split) * p.group + part * p.hw;
+                const int heads = min(p.hw, p.group - part * p.hw);
+                const T *qrow = static_cast<const T *>(p.q) + ((int64_t)s * p.num_heads + h0) * D;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int h = 8 * nt + r;
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        float x[8];
+                        const T *src = qrow + (int64_t)h * D + 32 * g + 8 * c;
+#pragma unroll
+                        for (int d = 0; d < 8; ++d) x[d] = 0.0f;
+                        if (h < heads) {
+                            if (p.vec) {
+                                T y[8];
+#pragma unroll
+                                for (int d = 0; d < (int)sizeof(T) / 2; ++d)
+                                    reinterpret_cast<uint4 *>(y)[d] = __ldg(reinterpret_cast<const uint4 *>(src) + d);
+#pragma unroll
+                                for (int d = 0; d < 8; ++d) x[d] = to_float(y[d]);
+                            } else {
+#pragma unroll
+                                for (int d = 0; d < 8; ++d) x[d] = to_float(src[d]);
+                            }
+                        }
+                        if (NS == 1) {
+                            float sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+                            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                            sum *= -136.0f;
+                            q0[nt][g][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
+                            q0[nt][g][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+                        }
+#pragma unroll
+                        for (int k = 0; k < NS; ++k)
+#pragma unroll
+                            for (int d = 0; d < 4; ++d)
+                                qf[nt][k][g][d] = NS == 1 ? pack_bf16x2(x[d], x[d + 4])
+                                                          : pack_bf16x2(bf16_part(x[d]), bf16_part(x[d + 4]));
+                    }
+#pragma unroll
+                    for (int t = 0; t < 2 * NG; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[nt][t][e] = 0.0f;
+                    m[nt][0] = m[nt][1] = -INFINITY;
+                    l[nt][0] = l[nt][1] = 0.0f;
+                }
+            }
+            cp_async_wait<kStages - 2>();
+            __syncwarp();   // every lane's copies are in, and every lane is done with the slot filled next
+            issue();
+            const uint8_t *st = ring + read * S::kStage;
+            read = read + 1 == kStages ? 0 : read + 1;
+            const int valid = ctx - u * kU;                 // tokens of the unit that exist
+            // row m of the first product is token t(m): its rows (2c, 2c+1) and (2c+8, 2c+9) are the tokens
+            // 4c .. 4c+3 that the lane holds of V
+            const int t0 = 4 * (r >> 1) + (r & 1), t1 = t0 + 2;
+
+            // ---- S = K Q^T
+            float x[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.0f;
+            {
+                uint32_t k0[NG], k1[NG];
+                float s0[NG], s1[NG];
+                const uint16_t *sc = reinterpret_cast<const uint16_t *>(st + 2 * S::kCodes);
+                if constexpr (D == 128) {
+                    *reinterpret_cast<uint4 *>(k0) = *reinterpret_cast<const uint4 *>(st + (t0 * 4 + c) * 16);
+                    *reinterpret_cast<uint4 *>(k1) = *reinterpret_cast<const uint4 *>(st + (t1 * 4 + c) * 16);
+                    const uint2 a = *reinterpret_cast<const uint2 *>(sc + t0 * NG), b = *reinterpret_cast<const uint2 *>(sc + t1 * NG);
+                    s0[0] = __uint_as_float(a.x << 16); s0[1] = __uint_as_float(a.x & 0xffff0000u);
+                    s0[2] = __uint_as_float(a.y << 16); s0[3] = __uint_as_float(a.y & 0xffff0000u);
+                    s1[0] = __uint_as_float(b.x << 16); s1[1] = __uint_as_float(b.x & 0xffff0000u);
+                    s1[2] = __uint_as_float(b.y << 16); s1[3] = __uint_as_float(b.y & 0xffff0000u);
+                } else {
+                    const int j0 = (t0 * 2 + (c >> 1)) ^ (4 * ((t0 >> 2) & 1)), j1 = (t1 * 2 + (c >> 1)) ^ (4 * ((t1 >> 2) & 1));
+                    *reinterpret_cast<uint2 *>(k0) = *reinterpret_cast<const uint2 *>(st + j0 * 16 + (c & 1) * 8);
+                    *reinterpret_cast<uint2 *>(k1) = *reinterpret_cast<const uint2 *>(st + j1 * 16 + (c & 1) * 8);
+                    const uint32_t a = *reinterpret_cast<const uint32_t *>(sc + t0 * NG), b = *reinterpret_cast<const uint32_t *>(sc + t1 * NG);
+                    s0[0] = __uint_as_float(a << 16); s0[1] = __uint_as_float(a & 0xffff0000u);
+                    s1[0] = __uint_as_float(b << 16); s1[1] = __uint_as_float(b & 0xffff0000u);
+                }
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    uint32_t a[4][2];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        a[e][0] = nibbles_128(k0[g] >> (4 * e));
+                        a[e][1] = nibbles_128(k1[g] >> (4 * e));
+                        if (NS > 1) {
+                            a[e][0] = minus_136(a[e][0]);
+                            a[e][1] = minus_136(a[e][1]);
+                        }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float acc[4];
+                        mma_from(acc, a[0][0], a[0][1], a[1][0], a[1][1], qf[nt][0][g][0], qf[nt][0][g][1],
+                                 NS == 1 ? q0[nt][g][0] : 0.0f, NS == 1 ? q0[nt][g][1] : 0.0f);
+                        mma_bf16_16816(acc, a[2][0], a[2][1], a[3][0], a[3][1], qf[nt][0][g][2], qf[nt][0][g][3]);
+#pragma unroll
+                        for (int k = 1; k < NS; ++k) {
+                            mma_bf16_16816(acc, a[0][0], a[0][1], a[1][0], a[1][1], qf[nt][k][g][0], qf[nt][k][g][1]);
+                            mma_bf16_16816(acc, a[2][0], a[2][1], a[3][0], a[3][1], qf[nt][k][g][2], qf[nt][k][g][3]);
+                        }
+                        x[nt][0] = fmaf(s0[g], acc[0], x[nt][0]);
+                        x[nt][1] = fmaf(s0[g], acc[1], x[nt][1]);
+                        x[nt][2] = fmaf(s1[g], acc[2], x[nt][2]);
+                        x[nt][3] = fmaf(s1[g], acc[3], x[nt][3]);
+                    }
+                }
+            }
+            // ---- softmax weights.  Rows behind the sequence may hold anything (NaN scales too): selected away.
+            bool move = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[nt][e] *= p.scale_log2;
+                    if (valid < kU && (e < 2 ? t0 : t1) >= valid) x[nt][e] = -INFINITY;
+                    move |= x[nt][e] > m[nt][e & 1] + kMoveAt;
+                }
+            }
+            if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float y = fmaxf(x[nt][e], x[nt][e + 2]);
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+                        y = fmaxf(y, m[nt][e]);
+                        const float alpha = y == m[nt][e] ? 1.0f : fast_exp2(m[nt][e] - y);
+                        m[nt][e] = y;
+                        l[nt][e] *= alpha;
+#pragma unroll
+                        for (int t = 0; t < 2 * NG; ++t) {
+                            o[nt][t][e] *= alpha;
+                            o[nt][t][e + 2] *= alpha;
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[nt][e] = fast_exp2(x[nt][e] - m[nt][e & 1]);
+                    l[nt][e & 1] += x[nt][e];
+                }
+            // ---- O^T += V^T P^T
+            {
+                const uint8_t *vc = st + S::kCodes;
+                const uint16_t *sc = reinterpret_cast<const uint16_t *>(st + 2 * S::kCodes + S::kScales);
+                float s0[NG], s1[NG];
+                constexpr int NW = NG / 2;       // words of a lane's share of a V row
+                uint32_t w[4][NW];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const int row = 4 * c + t;
+                    if constexpr (D == 128) {
+                        const int j = (row * 4 + (r >> 1)) ^ (2 * c);
+                        *reinterpret_cast<uint2 *>(w[t]) = *reinterpret_cast<const uint2 *>(vc + j * 16 + (r & 1) * 8);
+                    } else {
+                        const int j = (row * 2 + (r >> 2)) ^ (2 * c);
+                        w[t][0] = *reinterpret_cast<const uint32_t *>(vc + j * 16 + (r & 3) * 4);
+                    }
+                }
+#pragma unroll
+                for (int g = 0; g < NG; g += 2) {
+                    uint32_t a = *reinterpret_cast<const uint32_t *>(sc + t0 * NG + g);
+                    uint32_t b = *reinterpret_cast<const uint32_t *>(sc + t1 * NG + g);
+                    if (valid < kU) {
+                        if (t0 >= valid) a = 0;
+                        if (t1 >= valid) b = 0;
+                    }
+                    s0[g] = __uint_as_float(a << 16); s0[g + 1] = __uint_as_float(a & 0xffff0000u);
+                    s1[g] = __uint_as_float(b << 16); s1[g + 1] = __uint_as_float(b & 0xffff0000u);
+                }
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const uint32_t v01 = __byte_perm(w[0][g / 2], w[1][g / 2], g & 1 ? 0x7632 : 0x5410);
+                    const uint32_t v23 = __byte_perm(w[2][g / 2], w[3][g / 2], g & 1 ? 0x7632 : 0x5410);
+                    uint32_t a[4][2];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        a[e][0] = minus_136(nibbles_128(v01 >> (4 * e)));
+                        a[e][1] = minus_136(nibbles_128(v23 >> (4 * e)));
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        // the only rounding of a weight: p times V's scale, to bf16 (fp32 calls: three parts)
+                        float y[4] = {x[nt][0] * s0[g], x[nt][1] * s0[g], x[nt][2] * s1[g], x[nt][3] * s1[g]};
+#pragma unroll
+                        for (int k = 0; k < NS; ++k) {
+                            uint32_t b0, b1;
+                            if (NS == 1) {
+                                b0 = pack_bf16x2(y[0], y[1]);
+                                b1 = pack_bf16x2(y[2], y[3]);
+                            } else {
+                                const float z0 = bf16_part(y[0]), z1 = bf16_part(y[1]);
+                                const float z2 = bf16_part(y[2]), z3 = bf16_part(y[3]);
+                                b0 = pack_bf16x2(z0, z1);
+                                b1 = pack_bf16x2(z2, z3);
+                            }
+                            b0 = movmatrix_trans(b0);
+                            b1 = movmatrix_trans(b1);
+                            mma_bf16_16816(o[nt][2 * g], a[0][0], a[1][0], a[0][1], a[1][1], b0, b1);
+                            mma_bf16_16816(o[nt][2 * g + 1], a[2][0], a[3][0], a[2][1], a[3][1], b0, b1);
+                        }
+                    }
+                }
+            }
+            ++u;
+            if (u < nu && i + 1 < n) continue;
+
+            // ---- the end of a (sequence, head) or of the warp's part
+            const int part = vh % p.split, h0 = (vh / p.split) * p.group + part * p.hw;
+            const int heads = min(p.hw, p.group - part * p.hw);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
+                    l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
+                    l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
+                }
+            if (u_first == 0 && u == nu) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int h = 8 * nt + 2 * c + e;
+                        if (h >= heads) continue;
+                        T *dst = static_cast<T *>(p.out) + ((int64_t)s * p.num_heads + h0 + h) * D + 4 * r;
+                        const float inv = 1.0f / l[nt][e];
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            const float y0 = o[nt][2 * g][e] * inv, y1 = o[nt][2 * g][e + 2] * inv;
+                            const float y2 = o[nt][2 * g + 1][e] * inv, y3 = o[nt][2 * g + 1][e + 2] * inv;
+                            T *d = dst + 32 * g;
+                            if (!p.vec) {
+                                d[0] = from_float<T>(y0); d[1] = from_float<T>(y1);
+                                d[2] = from_float<T>(y2); d[3] = from_float<T>(y3);
+                            } else if constexpr (S::kF32) {
+                                *reinterpret_cast<float4 *>(d) = make_float4(y0, y1, y2, y3);
+                            } else {
+                                *reinterpret_cast<uint2 *>(d) = make_uint2(pack_bf16x2(y0, y1), pack_bf16x2(y2, y3));
+                            }
+                        }
+                    }
+            } else {
+                // the warp's first piece has a place of its own; a later one is its last and takes the drained ring
+                const bool at_start = i + 1 == u - u_first;
+                float *piece = first_piece;
+                if (!at_start) {
+                    cp_async_wait<0>();
+                    __syncwarp();
+                    piece = reinterpret_cast<float *>(ring);
+                }
+                if (lane == 0) meta[2 * warp + (at_start ? 0 : 1)] = {s, vh, u_first, u};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int h = 8 * nt + 2 * c + e;
+#pragma unroll
+                        for (int g = 0; g < NG; ++g)
+                            *reinterpret_cast<float4 *>(piece + h * D + 32 * g + 4 * r) =
+                                make_float4(o[nt][2 * g][e], o[nt][2 * g][e + 2], o[nt][2 * g + 1][e], o[nt][2 * g + 1][e + 2]);
+                        if (r == 0) {
+                            piece[HW * D + 2 * h] = m[nt][e];
+                            piece[HW * D + 2 * h + 1] = l[nt][e];
+                        }
+                    }
+            }
+            fresh = true;
+            if (u == nu) {
+                u = 0;
+                if (++vh == VH && i + 1 < n) {
+                    vh = 0;
+                    do {
+                        ctx = __ldg(p.context_lens + ++s);
+                        nu = units_of(ctx, max_tokens);
+                    } while (nu == 0);
+                }
+            }
+        }
+        cp_async_wait<0>();
+    }
     __syncthreads();
-    float M = -INFINITY, L = 0.0f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, m_s[w]);
-    for (int w = 0; w < kWarps; ++w) L += m_s[w] == -INFINITY ? 0.0f : l_s[w] * expf(m_s[w] - M);
-    for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-        float r = 0.0f;
-        for (int w = 0; w < kWarps; ++w) r += m_s[w] == -INFINITY ? 0.0f : o_s[w][d] * expf(m_s[w] - M);
-        static_cast<T *>(a.out)[qo + d] = from_float<T>(r / L);
+
+    // ---- merge the CTA's pieces: pieces of one (sequence, head) are neighbours in stream order
+    constexpr int PER = D / 32;   // dims a lane
+    auto piece_of = [&](int j) -> const float * {
+        return j & 1 ? reinterpret_cast<const float *>(smem + (j >> 1) * S::kRing)
+                     : reinterpret_cast<const float *>(smem + kWarps * S::kRing) + (j >> 1) * S::kPiece;
+    };
+    auto store_head = [&](int seq, int head, const float (&acc)[PER], float L) {
+        T *dst = static_cast<T *>(p.out) + ((int64_t)seq * p.num_heads + head) * D;
+        const float inv = 1.0f / L;
+#pragma unroll
+        for (int d = 0; d < PER; ++d) dst[d * 32 + lane] = from_float<T>(acc[d] * inv);
+    };
+    PieceMeta cut[2];   // the CTA's pieces of sequences that other CTAs share: cut on the left, cut on the right only
+    cut[0].seq = cut[1].seq = -1;
+    for (int j0 = 0; j0 < 2 * kWarps;) {
+        const PieceMeta a = meta[j0];
+        if (a.seq < 0) { ++j0; continue; }
+        int j1 = j0 + 1, u1 = a.u1;
+        for (; j1 < 2 * kWarps; ++j1) {
+            const PieceMeta b = meta[j1];
+            if (b.seq < 0) continue;
+            if (b.seq != a.seq || b.vh != a.vh) break;
+            u1 = b.u1;
+        }
+        const int nu = units_of(__ldg(p.context_lens + a.seq), max_tokens);
+        const bool whole = a.u0 == 0 && u1 == nu;
+        const int side = a.u0 == 0 ? 1 : 0;
+        if (!whole) cut[side] = {a.seq, a.vh, a.u0, u1};
+        const int part = a.vh % p.split, h0 = (a.vh / p.split) * p.group + part * p.hw;
+        const int heads = min(p.hw, p.group - part * p.hw);
+        float *dst = p.part + ((int64_t)blockIdx.x * 2 + side) * S::kPiece;
+        for (int h = warp; h < heads; h += kWarps) {
+            float M = -INFINITY, L = 0.0f, acc[PER];
+#pragma unroll
+            for (int d = 0; d < PER; ++d) acc[d] = 0.0f;
+            for (int j = j0; j < j1; ++j)
+                if (meta[j].seq >= 0) M = fmaxf(M, piece_of(j)[HW * D + 2 * h]);
+            for (int j = j0; j < j1; ++j) {
+                if (meta[j].seq < 0) continue;
+                const float *pc = piece_of(j);
+                const float f = fast_exp2(pc[HW * D + 2 * h] - M);
+                L += f * pc[HW * D + 2 * h + 1];
+#pragma unroll
+                for (int d = 0; d < PER; ++d) acc[d] += f * pc[h * D + d * 32 + lane];
+            }
+            if (whole) {
+                store_head(a.seq, h0 + h, acc, L);
+            } else {
+#pragma unroll
+                for (int d = 0; d < PER; ++d) __stcg(dst + h * D + d * 32 + lane, acc[d]);
+                if (lane == 0) {
+                    __stcg(dst + HW * D + 2 * h, M);
+                    __stcg(dst + HW * D + 2 * h + 1, L);
+                }
+            }
+        }
+        j0 = j1;
     }
+    if (cut[0].seq < 0 && cut[1].seq < 0) return;
+    // ---- sequences cut between CTAs: the last CTA to arrive merges their pieces, in stream order
+    __threadfence();
+    __syncthreads();
+    auto span = [&](const PieceMeta &a, int64_t &c0, int64_t &c1) {
+        const int nu = units_of(__ldg(p.context_lens + a.seq), max_tokens);
+        const int64_t at = p.prefix[a.seq] * VH + (int64_t)a.vh * nu;
+        c0 = at / share;
+        c1 = (at + nu - 1) / share;
+    };
+    if (tid < 2) {
+        int last = 0;
+        if (cut[tid].seq >= 0) {
+            int64_t c0, c1;
+            span(cut[tid], c0, c1);
+            last = atomic_add_acq_rel_gpu(p.arrivals + c0, 1) == (int)(c1 - c0);
+        }
+        last_s[tid] = last;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        if (!last_s[side]) continue;
+        const PieceMeta a = cut[side];
+        int64_t c0, c1;
+        span(a, c0, c1);
+        const int part = a.vh % p.split, h0 = (a.vh / p.split) * p.group + part * p.hw;
+        const int heads = min(p.hw, p.group - part * p.hw);
+        for (int h = warp; h < heads; h += kWarps) {
+            float M = -INFINITY, L = 0.0f, acc[PER];
+#pragma unroll
+            for (int d = 0; d < PER; ++d) acc[d] = 0.0f;
+            // the first CTA's piece is the one cut on its right
+            auto src = [&](int64_t cta) { return p.part + (cta * 2 + (cta == c0 ? 1 : 0)) * S::kPiece; };
+            for (int64_t cta = c0 + lane; cta <= c1; cta += 32) M = fmaxf(M, __ldcg(src(cta) + HW * D + 2 * h));
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+#pragma unroll 4
+            for (int64_t cta = c0; cta <= c1; ++cta) {
+                const float *pc = src(cta);
+                const float f = fast_exp2(__ldcg(pc + HW * D + 2 * h) - M);
+                L += f * __ldcg(pc + HW * D + 2 * h + 1);
+#pragma unroll
+                for (int d = 0; d < PER; ++d) acc[d] += f * __ldcg(pc + h * D + d * 32 + lane);
+            }
+            store_head(a.seq, h0 + h, acc, L);
+        }
+    }
+}
+
+// q-heads a warp takes: 16 for groups above 8 (K and V codes are then turned into operands once for both
+// tiles of 8), 8 otherwise and for fp32 calls, whose split operands leave no registers for a second tile.
+bool two_tiles(int group, bool f32) { return group > 8 && !f32; }
+
+int64_t prefix_bytes(int num_seqs) { return ((int64_t)(num_seqs + 1) * 8 + 255) / 256 * 256; }
+
+template <typename T, int D, int NT>
+cudaError_t launch_typed(Q4Params p, const AttnArgs &a, cudaStream_t stream) {
+    using S = Q4Shape<T, D, NT>;
+    auto kern = q4_decode_kernel<T, D, NT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    p.split = (p.group + S::HW - 1) / S::HW;
+    p.hw = (p.group + p.split - 1) / p.split;
+    const int grid = min(kMaxCtas, device_sm_count() * S::kCtasPerSm);
+    e = launch_dependent(q4_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a.context_lens, a.num_seqs,
+                         (int)(a.max_blocks * a.block_size), const_cast<int64_t *>(p.prefix), p.arrivals, a.status);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, dim3(grid), dim3(kWarps * 32), S::kSmem, stream, p);
 }
 
 }  // namespace
 
-size_t decode_q4_workspace(int, int, int, int) { return 256; }
+size_t decode_q4_workspace(int num_seqs, int num_heads, int num_kv_heads, int head_dim) {
+    const int hw = two_tiles(num_heads / num_kv_heads, false) ? 16 : 8;
+    const size_t part = (size_t)kMaxCtas * 2 * hw * (head_dim + 2) * sizeof(float);
+    return prefix_bytes(num_seqs) + kMaxCtas * sizeof(int32_t) + (part + 255) / 256 * 256;
+}
 
-cudaError_t launch_decode_q4(const AttnArgs &a, void *, size_t, cudaStream_t stream) {
-    const dim3 grid(a.num_seqs, a.num_heads), block(kWarps * 32);
-    if (a.dtype == PA_DTYPE_BF16)
-        return a.head_dim == 128 ? launch_dependent(decode_q4_kernel<__nv_bfloat16, 128>, grid, block, 0, stream, a)
-                                 : launch_dependent(decode_q4_kernel<__nv_bfloat16, 64>, grid, block, 0, stream, a);
-    return a.head_dim == 128 ? launch_dependent(decode_q4_kernel<float, 128>, grid, block, 0, stream, a)
-                             : launch_dependent(decode_q4_kernel<float, 64>, grid, block, 0, stream, a);
+cudaError_t launch_decode_q4(const AttnArgs &a, void *workspace, size_t, cudaStream_t stream) {
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    Q4Params p = {};
+    p.q = a.q;
+    p.out = a.out;
+    p.k = static_cast<const uint8_t *>(a.k_cache);
+    p.v = static_cast<const uint8_t *>(a.v_cache);
+    p.block_tables = a.block_tables;
+    p.context_lens = a.context_lens;
+    p.prefix = reinterpret_cast<int64_t *>(ws);
+    p.arrivals = reinterpret_cast<int32_t *>(ws + prefix_bytes(a.num_seqs));
+    p.part = reinterpret_cast<float *>(ws + prefix_bytes(a.num_seqs) + kMaxCtas * sizeof(int32_t));
+    p.num_seqs = a.num_seqs;
+    p.num_heads = a.num_heads;
+    p.num_kv_heads = a.num_kv_heads;
+    p.group = a.num_heads / a.num_kv_heads;
+    p.log2b = a.block_size == 8 ? 3 : a.block_size == 16 ? 4 : 5;
+    p.max_blocks = a.max_blocks;
+    p.num_blocks = a.num_blocks;
+    p.slab = q4_slab_bytes(a.block_size, a.head_dim);
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.status = a.status;
+    p.vec = (reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.out)) % 16 == 0;
+    const bool two = two_tiles(p.group, a.dtype == PA_DTYPE_F32), wide = a.head_dim == 128;
+    if (a.dtype == PA_DTYPE_F32)
+        return wide ? launch_typed<float, 128, 1>(p, a, stream) : launch_typed<float, 64, 1>(p, a, stream);
+    if (two)
+        return wide ? launch_typed<__nv_bfloat16, 128, 2>(p, a, stream) : launch_typed<__nv_bfloat16, 64, 2>(p, a, stream);
+    return wide ? launch_typed<__nv_bfloat16, 128, 1>(p, a, stream) : launch_typed<__nv_bfloat16, 64, 1>(p, a, stream);
 }
 
 }  // namespace pa
