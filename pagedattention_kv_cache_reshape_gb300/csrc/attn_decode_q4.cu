@@ -23,7 +23,9 @@
 //
 // The batch is one stream of units, (sequence, kv-head, 16 tokens); every CTA
 // takes an equal contiguous share and every warp of it an equal part, whatever
-// the mix of lengths.  A (sequence, kv-head) inside one warp is normalised and
+// the mix of lengths.  What a new (sequence, kv-head) costs a warp beside its
+// units (queries, first block ids, normalising or leaving a piece) counts as
+// kHeadCost units of the stream in front of it.  A (sequence, kv-head) inside one warp is normalised and
 // stored; cut ones leave (m, l, o) pieces, merged first between the warps of a
 // CTA (shared memory), then by the last arriving CTA (workspace), always in
 // stream order, so results do not depend on timing.
@@ -45,6 +47,7 @@ constexpr int kWarps = 8;
 constexpr int kStages = 4;
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxCtas = 512;
+constexpr int kHeadCost = 2;
 constexpr float kMoveAt = 8.0f;     // a logit this far (base 2) over the reference moves it
 
 struct Q4Params {
@@ -52,7 +55,7 @@ struct Q4Params {
     void *out;
     const uint8_t *k, *v;
     const int32_t *block_tables, *context_lens;
-    const int64_t *prefix;     // [num_seqs + 1] units of one head before each sequence
+    const int64_t *prefix;     // [num_seqs + 1] stream length of one head before each sequence
     int32_t *arrivals;         // [kMaxCtas] pieces of the sequence cut at a CTA's end, zeroed by the plan
     float *part;               // [CTAs][2][heads][D + 2]
     int num_seqs, num_heads, num_kv_heads;
@@ -60,7 +63,7 @@ struct Q4Params {
     int split;                 // parts a group is split into
     int hw;                    // q-heads of a part
     int log2b, max_blocks, num_blocks;
-    int64_t slab;
+    uint32_t slab, block_bytes;
     float scale_log2;
     int vec;                   // q rows and out rows take wide loads and stores
     int32_t *status;
@@ -70,7 +73,10 @@ __device__ __forceinline__ int units_of(int ctx, int max_tokens) {
     return ctx <= 0 || ctx > max_tokens ? 0 : (ctx - 1) / kU + 1;
 }
 
-// Exclusive prefix of the sequences' units, and the arrival counters' zeros.
+// A head of a sequence in the stream: its units and what it costs beside them.
+__device__ __forceinline__ int length_of(int nu) { return nu ? nu + kHeadCost : 0; }
+
+// Exclusive prefix of the sequences' stream lengths, and the arrival counters' zeros.
 __global__ void __launch_bounds__(kPlanThreads)
     q4_plan_kernel(const int32_t *__restrict__ context_lens, int num_seqs, int max_tokens,
                    int64_t *__restrict__ prefix, int32_t *__restrict__ arrivals, int32_t *status) {
@@ -87,7 +93,8 @@ __global__ void __launch_bounds__(kPlanThreads)
             nu = units_of(__ldg(context_lens + s), max_tokens);
             if (nu == 0) set_status(status, PA_ERR_OUT_OF_RANGE);
         }
-        int64_t incl = nu;
+        const int len = length_of(nu);
+        int64_t incl = len;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, incl, off);
@@ -105,7 +112,7 @@ __global__ void __launch_bounds__(kPlanThreads)
             warp_tot[lane] = t;
         }
         __syncthreads();
-        if (s < num_seqs) prefix[s] = running + (warp ? warp_tot[warp - 1] : 0) + incl - nu;
+        if (s < num_seqs) prefix[s] = running + (warp ? warp_tot[warp - 1] : 0) + incl - len;
         running += warp_tot[kPlanThreads / 32 - 1];
         __syncthreads();
     }
@@ -130,12 +137,23 @@ __device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
-__device__ __forceinline__ void cp_async16(void *smem, const void *gmem) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t smem, const void *gmem) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// The NG bf16 scales of a row in shared memory.
+template <int NG> __device__ __forceinline__ void load_scales(float (&s)[NG], const uint8_t *at) {
+    uint32_t w[NG / 2];
+    if constexpr (NG == 4) *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(at);
+    else w[0] = *reinterpret_cast<const uint32_t *>(at);
+#pragma unroll
+    for (int g = 0; g < NG; g += 2) {
+        s[g] = __uint_as_float(w[g / 2] << 16);
+        s[g + 1] = __uint_as_float(w[g / 2] & 0xffff0000u);
+    }
 }
 __device__ __forceinline__ float bf16_part(float &x) {          // the leading bf16 of x, taken off it
     const float h = __bfloat162float(__float2bfloat16_rn(x));
@@ -194,68 +212,80 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
     const int64_t cta0 = min(total, share * blockIdx.x), cta1 = min(total, cta0 + share);
     if (cta0 == cta1) return;
     const int64_t w0 = cta0 + (cta1 - cta0) * warp / kWarps, w1 = cta0 + (cta1 - cta0) * (warp + 1) / kWarps;
-    const int n = (int)(w1 - w0);
 
-    if (n > 0) {
+    if (w1 > w0) {
         // ---- where the warp's part begins
         int s = find_seq(p.prefix, p.num_seqs, w0 / VH, lane);
         int ctx = __ldg(p.context_lens + s), nu = units_of(ctx, max_tokens);
         const int64_t in_seq = w0 - p.prefix[s] * VH;
-        int vh = (int)(in_seq / nu), u = (int)(in_seq - (int64_t)vh * nu);
+        int vh = (int)(in_seq / length_of(nu));
+        const int into = (int)(in_seq - (int64_t)vh * length_of(nu));
+        int u = max(0, into - kHeadCost);
+        int left = (int)(w1 - w0) - max(0, kHeadCost - into);   // of the part, in stream units
         // ---- the copies' own place in the stream, kStages - 1 units ahead
-        int cs = s, cctx = ctx, cnu = nu, cvh = vh, cu = u, left = n, slot = 0;
-        int ids = -1, ids_seq = -1, ids_base = 0;
+        int cs = s, cctx = ctx, cnu = nu, cvh = vh, cu = u;
+        int cleft = left;
+        uint64_t head_at = (uint64_t)(uint32_t)(cvh / p.split) * p.slab;
+        int ids = 0, ids_seq = -1, ids_base = 0;
+        const uint32_t ring_a = smem_u32(ring);
+        uint32_t wr = ring_a;
+        const int v_sw = lane ^ (2 * ((lane / NG >> 2) & 3));                           // swizzled place of V's chunk `lane`
+        const int k_sw = D == 64 ? lane ^ (4 * ((lane / NG >> 2) & 1)) : lane;
+        const uint8_t *sc_src = (lane < 2 * NG ? p.k : p.v) + B * (D / 2) + (lane % NG) * 16;
         auto issue = [&]() {
-            if (left > 0) {
-                --left;
+            if (cleft > 0) {
+                --cleft;
                 const int b = (int)(((int64_t)cu * kU) >> p.log2b);
                 if (cs != ids_seq || (unsigned)(b - ids_base) >= 32u) {
                     ids_seq = cs;
                     ids_base = b & ~31;
                     const int64_t e = ids_base + lane;
-                    ids = -1;
+                    ids = 0;   // behind the sequence or out of range: block 0 is read and not used
                     if ((e << p.log2b) < cctx) {
                         ids = __ldg(p.block_tables + (int64_t)cs * p.max_blocks + e);
                         if (ids < 0 || ids >= p.num_blocks) {
                             set_status(p.status, PA_ERR_OUT_OF_RANGE);
-                            ids = -1;
+                            ids = 0;
                         }
                     }
                 }
-                // tokens 0..7 and 8..15 of the unit: one block's rows, or two blocks of 8
-                const int id0 = __shfl_sync(0xffffffffu, ids, b - ids_base);
-                const int id1 = __shfl_sync(0xffffffffu, ids, (b - ids_base + (p.log2b == 3)) & 31);
-                const int hk = cvh / p.split, tok = (cu * kU) & (B - 1), tok1 = p.log2b == 3 ? 0 : tok + 8;
-                const int64_t at0 = ((int64_t)id0 * p.num_kv_heads + hk) * p.slab;
-                const int64_t at1 = ((int64_t)id1 * p.num_kv_heads + hk) * p.slab;
-                uint8_t *st = ring + slot * S::kStage;
-#pragma unroll
-                for (int j = lane; j < S::kCodes / 16; j += 32) {   // row j / (D/32)
-                    const int t = j / NG;
-                    const int id = t < 8 ? id0 : id1;
-                    const int64_t at = (t < 8 ? at0 + tok * (D / 2) : at1 + tok1 * (D / 2)) + (j % (8 * NG)) * 16;
-                    const int kd = D == 64 ? j ^ (4 * ((t >> 2) & 1)) : j, vd = j ^ (2 * ((t >> 2) & 3));
-                    if (id >= 0) {
-                        cp_async16(st + kd * 16, p.k + at);
-                        cp_async16(st + S::kCodes + vd * 16, p.v + at);
-                    }
+                // tokens 0..7 and 8..15 of the unit: rows of one block, or two blocks of 8
+                const uint32_t id0 = __shfl_sync(0xffffffffu, ids, b - ids_base);
+                const int tok = (cu * kU) & (B - 1);
+                const uint64_t at0 = (uint64_t)id0 * p.block_bytes + head_at;
+                uint64_t at1 = at0;
+                int tok1 = tok + 8;
+                if (p.log2b == 3) {
+                    const uint32_t id1 = __shfl_sync(0xffffffffu, ids, b - ids_base + 1);
+                    at1 = (uint64_t)id1 * p.block_bytes + head_at;
+                    tok1 = 0;
                 }
-                if (lane < 4 * NG) {
-                    const int j = lane % (2 * NG), half = j / NG;
-                    const int64_t at = (half ? at1 + tok1 * (NG * 2) : at0 + tok * (NG * 2)) + B * (D / 2) + (j % NG) * 16;
-                    if ((half ? id1 : id0) >= 0)
-                        cp_async16(st + 2 * S::kCodes + lane * 16, (lane < 2 * NG ? p.k : p.v) + at);
+                const uint64_t c0 = at0 + tok * (D / 2), c1 = at1 + tok1 * (D / 2);
+                if constexpr (D == 128) {   // chunks 0..31: rows 0..7, 32..63: rows 8..15
+                    cp_async16(wr + lane * 16, p.k + c0 + lane * 16);
+                    cp_async16(wr + lane * 16 + 512, p.k + c1 + lane * 16);
+                    cp_async16(wr + S::kCodes + v_sw * 16, p.v + c0 + lane * 16);
+                    cp_async16(wr + S::kCodes + 512 + (v_sw ^ 4) * 16, p.v + c1 + lane * 16);
+                } else {
+                    const uint64_t cc = (lane < 16 ? c0 : c1) + (lane & 15) * 16;
+                    cp_async16(wr + k_sw * 16, p.k + cc);
+                    cp_async16(wr + S::kCodes + v_sw * 16, p.v + cc);
                 }
-                slot = slot + 1 == kStages ? 0 : slot + 1;
+                if (lane < 4 * NG)
+                    cp_async16(wr + 2 * S::kCodes + lane * 16,
+                               sc_src + (lane & NG ? at1 + tok1 * (NG * 2) : at0 + tok * (NG * 2)));
+                wr = wr + S::kStage == ring_a + S::kRing ? ring_a : wr + S::kStage;
                 if (++cu == cnu) {
                     cu = 0;
-                    if (++cvh == VH && left > 0) {
+                    cleft -= kHeadCost;
+                    if (++cvh == VH && cleft > 0) {
                         cvh = 0;
                         do {
                             cctx = __ldg(p.context_lens + ++cs);
                             cnu = units_of(cctx, max_tokens);
                         } while (cnu == 0);
                     }
+                    head_at = (uint64_t)(uint32_t)(cvh / p.split) * p.slab;
                 }
             }
             cp_async_commit();
@@ -266,9 +296,19 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
         uint32_t qf[NT][NS][NG][4];        // the B operand of the first product: pair i holds dims (i, i + 4) of a lane's 8
         float q0[NT][NG][2];               // -136 sum(q) of a group, for the lane's two columns
         float o[NT][2 * NG][4], m[NT][2], l[NT][2];
-        bool fresh = true;
-        int u_first = 0, read = 0;
-        for (int i = 0; i < n; ++i) {
+        bool fresh = true, at_start = true;
+        int u_first = 0;
+        const uint8_t *st = ring;
+        // row m of the first product is token t(m): its rows (2c, 2c+1) and (2c+8, 2c+9) are the tokens
+        // 4c .. 4c+3 that the lane holds of V; its own rows r and r + 8 are the tokens t0 and t0 + 2
+        const int t0 = 4 * (r >> 1) + (r & 1), t1 = t0 + 2;
+        const int k_at = D == 128 ? (t0 * 4 + c) * 16 : ((t0 * 2 + (c >> 1)) ^ (4 * ((t0 >> 2) & 1))) * 16 + (c & 1) * 8;
+        // rows 4c and 4c + 1 of V; 4c + 2 and 4c + 3 lie two rows on
+        const int v_at0 = D == 128 ? ((16 * c + (r >> 1)) ^ (2 * c)) * 16 + (r & 1) * 8 : ((8 * c + (r >> 2)) ^ (2 * c)) * 16 + (r & 3) * 4;
+        const int v_at1 = D == 128 ? ((16 * c + 4 + (r >> 1)) ^ (2 * c)) * 16 + (r & 1) * 8 : ((8 * c + 2 + (r >> 2)) ^ (2 * c)) * 16 + (r & 3) * 4;
+        // a tile's bytes two rows on (head_dim 64: the swizzle turns the step round)
+        const int two_rows_k = D == 128 || !((t0 >> 2) & 1) ? D : -D, two_rows_v = D == 128 || c < 2 ? D : -D;
+        while (left > 0) {
             if (fresh) {
                 fresh = false;
                 u_first = u;
@@ -323,12 +363,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
             cp_async_wait<kStages - 2>();
             __syncwarp();   // every lane's copies are in, and every lane is done with the slot filled next
             issue();
-            const uint8_t *st = ring + read * S::kStage;
-            read = read + 1 == kStages ? 0 : read + 1;
             const int valid = ctx - u * kU;                 // tokens of the unit that exist
-            // row m of the first product is token t(m): its rows (2c, 2c+1) and (2c+8, 2c+9) are the tokens
-            // 4c .. 4c+3 that the lane holds of V
-            const int t0 = 4 * (r >> 1) + (r & 1), t1 = t0 + 2;
 
             // ---- S = K Q^T
             float x[NT][4];
@@ -337,23 +372,15 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
             {
                 uint32_t k0[NG], k1[NG];
                 float s0[NG], s1[NG];
-                const uint16_t *sc = reinterpret_cast<const uint16_t *>(st + 2 * S::kCodes);
                 if constexpr (D == 128) {
-                    *reinterpret_cast<uint4 *>(k0) = *reinterpret_cast<const uint4 *>(st + (t0 * 4 + c) * 16);
-                    *reinterpret_cast<uint4 *>(k1) = *reinterpret_cast<const uint4 *>(st + (t1 * 4 + c) * 16);
-                    const uint2 a = *reinterpret_cast<const uint2 *>(sc + t0 * NG), b = *reinterpret_cast<const uint2 *>(sc + t1 * NG);
-                    s0[0] = __uint_as_float(a.x << 16); s0[1] = __uint_as_float(a.x & 0xffff0000u);
-                    s0[2] = __uint_as_float(a.y << 16); s0[3] = __uint_as_float(a.y & 0xffff0000u);
-                    s1[0] = __uint_as_float(b.x << 16); s1[1] = __uint_as_float(b.x & 0xffff0000u);
-                    s1[2] = __uint_as_float(b.y << 16); s1[3] = __uint_as_float(b.y & 0xffff0000u);
+                    *reinterpret_cast<uint4 *>(k0) = *reinterpret_cast<const uint4 *>(st + k_at);
+                    *reinterpret_cast<uint4 *>(k1) = *reinterpret_cast<const uint4 *>(st + k_at + 128);
                 } else {
-                    const int j0 = (t0 * 2 + (c >> 1)) ^ (4 * ((t0 >> 2) & 1)), j1 = (t1 * 2 + (c >> 1)) ^ (4 * ((t1 >> 2) & 1));
-                    *reinterpret_cast<uint2 *>(k0) = *reinterpret_cast<const uint2 *>(st + j0 * 16 + (c & 1) * 8);
-                    *reinterpret_cast<uint2 *>(k1) = *reinterpret_cast<const uint2 *>(st + j1 * 16 + (c & 1) * 8);
-                    const uint32_t a = *reinterpret_cast<const uint32_t *>(sc + t0 * NG), b = *reinterpret_cast<const uint32_t *>(sc + t1 * NG);
-                    s0[0] = __uint_as_float(a << 16); s0[1] = __uint_as_float(a & 0xffff0000u);
-                    s1[0] = __uint_as_float(b << 16); s1[1] = __uint_as_float(b & 0xffff0000u);
+                    *reinterpret_cast<uint2 *>(k0) = *reinterpret_cast<const uint2 *>(st + k_at);
+                    *reinterpret_cast<uint2 *>(k1) = *reinterpret_cast<const uint2 *>(st + k_at + two_rows_k);
                 }
+                load_scales<NG>(s0, st + 2 * S::kCodes + t0 * (NG * 2));
+                load_scales<NG>(s1, st + 2 * S::kCodes + t0 * (NG * 2) + NG * 4);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     uint32_t a[4][2];
@@ -384,23 +411,35 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
                     }
                 }
             }
-            // ---- softmax weights.  Rows behind the sequence may hold anything (NaN scales too): selected away.
-            bool move = false;
+            // ---- softmax weights (base 2).  Rows behind the sequence may hold anything, NaN scales too: they are
+            // selected away, not multiplied
+            float w[NT][4];
+            auto weigh = [&]() {
+                bool move = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[nt][e] *= p.scale_log2;
-                    if (valid < kU && (e < 2 ? t0 : t1) >= valid) x[nt][e] = -INFINITY;
-                    move |= x[nt][e] > m[nt][e & 1] + kMoveAt;
+                    for (int e = 0; e < 4; ++e) w[nt][e] = fmaf(x[nt][e], p.scale_log2, -m[nt][e & 1]);
+                if (valid < kU) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if ((e < 2 ? t0 : t1) >= valid) w[nt][e] = -INFINITY;
                 }
-            }
-            if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) move |= w[nt][e] > kMoveAt;
+                return move;
+            };
+            if (__any_sync(0xffffffffu, weigh())) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float y = fmaxf(x[nt][e], x[nt][e + 2]);
+                        float y = t0 < valid ? x[nt][e] * p.scale_log2 : -INFINITY;
+                        if (t1 < valid) y = fmaxf(y, x[nt][e + 2] * p.scale_log2);
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
@@ -415,47 +454,40 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
                         }
                     }
                 }
+                weigh();
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    x[nt][e] = fast_exp2(x[nt][e] - m[nt][e & 1]);
+                    x[nt][e] = fast_exp2(w[nt][e]);
                     l[nt][e & 1] += x[nt][e];
                 }
             // ---- O^T += V^T P^T
             {
                 const uint8_t *vc = st + S::kCodes;
-                const uint16_t *sc = reinterpret_cast<const uint16_t *>(st + 2 * S::kCodes + S::kScales);
                 float s0[NG], s1[NG];
                 constexpr int NW = NG / 2;       // words of a lane's share of a V row
-                uint32_t w[4][NW];
+                uint32_t vw[4][NW];
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    const int row = 4 * c + t;
-                    if constexpr (D == 128) {
-                        const int j = (row * 4 + (r >> 1)) ^ (2 * c);
-                        *reinterpret_cast<uint2 *>(w[t]) = *reinterpret_cast<const uint2 *>(vc + j * 16 + (r & 1) * 8);
-                    } else {
-                        const int j = (row * 2 + (r >> 2)) ^ (2 * c);
-                        w[t][0] = *reinterpret_cast<const uint32_t *>(vc + j * 16 + (r & 3) * 4);
-                    }
+                    const uint8_t *at = vc + (t & 1 ? v_at1 : v_at0) + (t < 2 ? 0 : two_rows_v);
+                    if constexpr (D == 128) *reinterpret_cast<uint2 *>(vw[t]) = *reinterpret_cast<const uint2 *>(at);
+                    else vw[t][0] = *reinterpret_cast<const uint32_t *>(at);
                 }
+                load_scales<NG>(s0, st + 2 * S::kCodes + S::kScales + t0 * (NG * 2));
+                load_scales<NG>(s1, st + 2 * S::kCodes + S::kScales + t0 * (NG * 2) + NG * 4);
+                if (valid < kU) {
 #pragma unroll
-                for (int g = 0; g < NG; g += 2) {
-                    uint32_t a = *reinterpret_cast<const uint32_t *>(sc + t0 * NG + g);
-                    uint32_t b = *reinterpret_cast<const uint32_t *>(sc + t1 * NG + g);
-                    if (valid < kU) {
-                        if (t0 >= valid) a = 0;
-                        if (t1 >= valid) b = 0;
+                    for (int g = 0; g < NG; ++g) {
+                        if (t0 >= valid) s0[g] = 0.0f;
+                        if (t1 >= valid) s1[g] = 0.0f;
                     }
-                    s0[g] = __uint_as_float(a << 16); s0[g + 1] = __uint_as_float(a & 0xffff0000u);
-                    s1[g] = __uint_as_float(b << 16); s1[g + 1] = __uint_as_float(b & 0xffff0000u);
                 }
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    const uint32_t v01 = __byte_perm(w[0][g / 2], w[1][g / 2], g & 1 ? 0x7632 : 0x5410);
-                    const uint32_t v23 = __byte_perm(w[2][g / 2], w[3][g / 2], g & 1 ? 0x7632 : 0x5410);
+                    const uint32_t v01 = __byte_perm(vw[0][g / 2], vw[1][g / 2], g & 1 ? 0x7632 : 0x5410);
+                    const uint32_t v23 = __byte_perm(vw[2][g / 2], vw[3][g / 2], g & 1 ? 0x7632 : 0x5410);
                     uint32_t a[4][2];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -486,8 +518,9 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
                     }
                 }
             }
+            st = st + S::kStage == ring + S::kRing ? ring : st + S::kStage;
             ++u;
-            if (u < nu && i + 1 < n) continue;
+            if (--left > 0 && u < nu) continue;
 
             // ---- the end of a (sequence, head) or of the warp's part
             const int part = vh % p.split, h0 = (vh / p.split) * p.group + part * p.hw;
@@ -526,7 +559,6 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
                     }
             } else {
                 // the warp's first piece has a place of its own; a later one is its last and takes the drained ring
-                const bool at_start = i + 1 == u - u_first;
                 float *piece = first_piece;
                 if (!at_start) {
                     cp_async_wait<0>();
@@ -550,15 +582,15 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
                     }
             }
             fresh = true;
-            if (u == nu) {
-                u = 0;
-                if (++vh == VH && i + 1 < n) {
-                    vh = 0;
-                    do {
-                        ctx = __ldg(p.context_lens + ++s);
-                        nu = units_of(ctx, max_tokens);
-                    } while (nu == 0);
-                }
+            at_start = false;
+            u = 0;
+            left -= kHeadCost;
+            if (++vh == VH && left > 0) {
+                vh = 0;
+                do {
+                    ctx = __ldg(p.context_lens + ++s);
+                    nu = units_of(ctx, max_tokens);
+                } while (nu == 0);
             }
         }
         cp_async_wait<0>();
@@ -629,7 +661,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
     __syncthreads();
     auto span = [&](const PieceMeta &a, int64_t &c0, int64_t &c1) {
         const int nu = units_of(__ldg(p.context_lens + a.seq), max_tokens);
-        const int64_t at = p.prefix[a.seq] * VH + (int64_t)a.vh * nu;
+        const int64_t at = p.prefix[a.seq] * VH + (int64_t)a.vh * length_of(nu) + kHeadCost;
         c0 = at / share;
         c1 = (at + nu - 1) / share;
     };
@@ -722,6 +754,7 @@ cudaError_t launch_decode_q4(const AttnArgs &a, void *workspace, size_t, cudaStr
     p.max_blocks = a.max_blocks;
     p.num_blocks = a.num_blocks;
     p.slab = q4_slab_bytes(a.block_size, a.head_dim);
+    p.block_bytes = p.slab * a.num_kv_heads;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.status = a.status;
     p.vec = (reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.out)) % 16 == 0;

@@ -292,6 +292,7 @@ pa_status check_q4_shape(int num_kv_heads, int head_dim, int block_size) {
     if (num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0) return PA_ERR_INVALID_ARG;
     if (block_size != 8 && block_size != 16 && block_size != 32) return PA_ERR_UNSUPPORTED;
     if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)num_kv_heads * q4_slab_bytes(block_size, head_dim) > INT32_MAX) return PA_ERR_UNSUPPORTED;
     return PA_OK;
 }
 
@@ -412,6 +413,8 @@ pa_status pa_decode_q4(void *out, const void *q, const void *k_cache, const void
     const pa_status st = check_attention_shape(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
                                                max_blocks, num_blocks, dtype, scale);
     if (st != PA_OK) return st;
+    const pa_status q4 = check_q4_shape(num_kv_heads, head_dim, block_size);
+    if (q4 != PA_OK) return q4;
     if (num_seqs == 0) return PA_OK;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens) return PA_ERR_INVALID_ARG;
     const int eb = elem_bytes(dtype);
