@@ -4,16 +4,27 @@
 //
 // What it has to move is 4.5 bits a cached value, 3.6 times less than a bf16
 // cache; the bound that comes up before HBM is the instruction issue of turning
-// nibbles into matrix operands, so the kernel is built to spend little there:
-//  * A nibble n becomes a bf16 operand with one and-or per pair: 0x4300 | n is
-//    128 + n exactly.  Scales are never multiplied into elements.  For the
-//    first product (S = K Q^T, tokens in M, q-heads in N, m16n8k16) the k steps
-//    of a group of 32 dims share their accumulator, and the group's scale is
-//    applied to the 4 sums of a lane; the surplus of 136 a code is taken off
-//    by starting the accumulator at -136 sum(q) of the group.  For the second
-//    (O^T += V^T P^T) the token's scale of V goes into the weight p, once per
-//    group, and the codes are brought to n - 8 exactly, because sums over many
-//    tokens would lose the small result under a surplus.
+// nibbles into matrix operands, so the kernel is built to spend little there
+// (bf16 queries; fp32 below):
+//  * A nibble is an operand as it stands: in the low 4 bits of an fp16 it is
+//    the number n 2^-24, in the next 4 bits n 2^-20 (subnormals, which the
+//    matrix instructions take exactly), so an AND makes two of them and one
+//    shift serves four.  Scales are never multiplied into elements, and the 8
+//    in n - 8 is taken off sums, not off elements.  (e4m3 operands would take
+//    a nibble too, but that mma.sync is itself made of conversions and fp16
+//    products: 187 us where fp16 takes FP16TIME, 16 x 32768 tokens.)
+//  * S = K Q^T (tokens in M, q-heads in N, m16n8k16): q in fp16 times a power of
+//    two per head that brings its largest element into [2^14, 2^15): exact
+//    down to 2^-31 of the largest.  The group's scale is applied to the 4 sums
+//    of a lane, and the -8 sum(q) scale of all groups is one more product, of
+//    the scales with -8 sum(q) in three bf16 parts.
+//  * O^T += V^T P^T (dims in M, tokens in K): the token's scale of V goes into
+//    the weight, once per group, and the product is rounded to fp16 (2^-11).
+//    The weights carry a power of two, 2^lift, that brings the largest scale
+//    seen so far into [2^6, 2^7): with weights below 2^8 nothing overflows, and
+//    a product 2^-21 of the largest still has its 11 bits.  The 8 is taken off
+//    by a product of the same weights with -8 right after: a sum over many
+//    tokens would otherwise lose a small result under 8 times its weights.
 //  * The softmax reference of a head moves only when a logit passes it by 8
 //    (base 2), found by one warp vote a unit: weights stay below 2^8 and sums
 //    are rescaled a few times a sequence instead of every unit.
@@ -31,9 +42,11 @@
 // stream order, so results do not depend on timing.
 //
 // fp32 queries: q and the weights are split into three bf16 parts each (24
-// bits), whose products with the exact codes are summed in fp32; the codes of
-// K are brought to n - 8 too.
+// bits), and the codes are brought to n - 8 one by one (0x4300 | n is 128 + n
+// in bf16), so that no sum carries a surplus.
 #include <math.h>
+
+#include <cuda_fp16.h>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -129,13 +142,27 @@ __device__ __forceinline__ uint32_t minus_136(uint32_t a) {     // exact: 128 + 
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x43084308u));
     return r;
 }
-__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1, float c0, float c1) {
+// D = A(16x16, row) * B(16x8, col) + D, fp16 operands, fp32 accumulators.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %10, %11};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+// Nibbles i and i + 4 of w (i = 0..3) as an fp16 pair: n 2^-24 (i even) or n 2^-20 (i odd).
+__device__ __forceinline__ uint32_t nibbles_f16(uint32_t w, int i) {
+    return (i < 2 ? w : w >> 8) & (i & 1 ? 0x00f000f0u : 0x000f000fu);
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 __device__ __forceinline__ void cp_async16(uint32_t smem, const void *gmem) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
@@ -144,16 +171,13 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N> __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// The NG bf16 scales of a row in shared memory.
-template <int NG> __device__ __forceinline__ void load_scales(float (&s)[NG], const uint8_t *at) {
-    uint32_t w[NG / 2];
+// The NG bf16 scales of a row in shared memory, and one of them.
+template <int NG> __device__ __forceinline__ void load_scales(uint32_t (&w)[NG / 2], const uint8_t *at) {
     if constexpr (NG == 4) *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(at);
     else w[0] = *reinterpret_cast<const uint32_t *>(at);
-#pragma unroll
-    for (int g = 0; g < NG; g += 2) {
-        s[g] = __uint_as_float(w[g / 2] << 16);
-        s[g + 1] = __uint_as_float(w[g / 2] & 0xffff0000u);
-    }
+}
+template <int N> __device__ __forceinline__ float scale_of(const uint32_t (&w)[N], int g) {
+    return __uint_as_float(g & 1 ? w[g / 2] & 0xffff0000u : w[g / 2] << 16);
 }
 __device__ __forceinline__ float bf16_part(float &x) {          // the leading bf16 of x, taken off it
     const float h = __bfloat162float(__float2bfloat16_rn(x));
@@ -222,80 +246,107 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
         const int into = (int)(in_seq - (int64_t)vh * length_of(nu));
         int u = max(0, into - kHeadCost);
         int left = (int)(w1 - w0) - max(0, kHeadCost - into);   // of the part, in stream units
-        // ---- the copies' own place in the stream, kStages - 1 units ahead
-        int cs = s, cctx = ctx, cnu = nu, cvh = vh, cu = u;
-        int cleft = left;
-        uint64_t head_at = (uint64_t)(uint32_t)(cvh / p.split) * p.slab;
-        int ids = 0, ids_seq = -1, ids_base = 0;
+        // ---- the copies' own place in the stream, kStages - 1 units ahead: a stretch is the units whose block
+        // ids the lanes hold (id i of the stretch in lane i)
+        int cs = s, cctx = ctx, cnu = nu, cvh = vh, cu = u, cleft = left;
+        int stretch = 0, id_at = 0, half = 0, ids = 0, ids_seq = -1, ids_base = 0;
         const uint32_t ring_a = smem_u32(ring);
         uint32_t wr = ring_a;
-        const int v_sw = lane ^ (2 * ((lane / NG >> 2) & 3));                           // swizzled place of V's chunk `lane`
+        const int v_sw = lane ^ (2 * ((lane / NG >> 2) & 3));      // swizzled place of V's chunk `lane`
         const int k_sw = D == 64 ? lane ^ (4 * ((lane / NG >> 2) & 1)) : lane;
-        const uint8_t *sc_src = (lane < 2 * NG ? p.k : p.v) + B * (D / 2) + (lane % NG) * 16;
+        const int chunk = D == 128 ? lane : lane & 15;
+        const uint8_t *k_src, *v_src, *sc_src;
+        auto at_head = [&]() {
+            const uint64_t at = (uint64_t)(uint32_t)(cvh / p.split) * p.slab;
+            k_src = p.k + at + chunk * 16;
+            v_src = p.v + at + chunk * 16;
+            sc_src = (lane < 2 * NG ? p.k : p.v) + at + B * (D / 2) + (lane % NG) * 16;
+        };
+        at_head();
+        auto next_stretch = [&]() {
+            if (cu == cnu) {
+                cu = 0;
+                cleft -= kHeadCost;
+                if (++cvh == VH && cleft > 0) {
+                    cvh = 0;
+                    do {
+                        cctx = __ldg(p.context_lens + ++cs);
+                        cnu = units_of(cctx, max_tokens);
+                    } while (cnu == 0);
+                }
+                at_head();
+            }
+            stretch = 0;
+            if (cleft <= 0) return;
+            const int b = (int)(((unsigned)cu * kU) >> p.log2b);
+            if (cs != ids_seq || b != ids_base) {
+                ids_seq = cs;
+                ids_base = b;
+                const int64_t e = (int64_t)b + lane;
+                ids = 0;   // behind the sequence or out of range: block 0 is read and not used
+                if ((e << p.log2b) < cctx) {
+                    ids = __ldg(p.block_tables + (int64_t)cs * p.max_blocks + e);
+                    if (ids < 0 || ids >= p.num_blocks) {
+                        set_status(p.status, PA_ERR_OUT_OF_RANGE);
+                        ids = 0;
+                    }
+                }
+            }
+            id_at = 0;
+            half = p.log2b == 5 ? cu & 1 : 0;
+            const int held = p.log2b == 4 ? 32 : p.log2b == 3 ? 16 : 64 - half;
+            stretch = min(min(cnu - cu, held), cleft);
+            cu += stretch;
+            cleft -= stretch;
+        };
         auto issue = [&]() {
-            if (cleft > 0) {
-                --cleft;
-                const int b = (int)(((int64_t)cu * kU) >> p.log2b);
-                if (cs != ids_seq || (unsigned)(b - ids_base) >= 32u) {
-                    ids_seq = cs;
-                    ids_base = b & ~31;
-                    const int64_t e = ids_base + lane;
-                    ids = 0;   // behind the sequence or out of range: block 0 is read and not used
-                    if ((e << p.log2b) < cctx) {
-                        ids = __ldg(p.block_tables + (int64_t)cs * p.max_blocks + e);
-                        if (ids < 0 || ids >= p.num_blocks) {
-                            set_status(p.status, PA_ERR_OUT_OF_RANGE);
-                            ids = 0;
-                        }
-                    }
-                }
-                // tokens 0..7 and 8..15 of the unit: rows of one block, or two blocks of 8
-                const uint32_t id0 = __shfl_sync(0xffffffffu, ids, b - ids_base);
-                const int tok = (cu * kU) & (B - 1);
-                const uint64_t at0 = (uint64_t)id0 * p.block_bytes + head_at;
-                uint64_t at1 = at0;
-                int tok1 = tok + 8;
-                if (p.log2b == 3) {
-                    const uint32_t id1 = __shfl_sync(0xffffffffu, ids, b - ids_base + 1);
-                    at1 = (uint64_t)id1 * p.block_bytes + head_at;
-                    tok1 = 0;
-                }
-                const uint64_t c0 = at0 + tok * (D / 2), c1 = at1 + tok1 * (D / 2);
-                if constexpr (D == 128) {   // chunks 0..31: rows 0..7, 32..63: rows 8..15
-                    cp_async16(wr + lane * 16, p.k + c0 + lane * 16);
-                    cp_async16(wr + lane * 16 + 512, p.k + c1 + lane * 16);
-                    cp_async16(wr + S::kCodes + v_sw * 16, p.v + c0 + lane * 16);
-                    cp_async16(wr + S::kCodes + 512 + (v_sw ^ 4) * 16, p.v + c1 + lane * 16);
+            if (stretch > 0) {
+                const uint32_t id = __shfl_sync(0xffffffffu, ids, id_at);
+                const uint64_t at = (uint64_t)id * p.block_bytes;
+                // tokens 0..7 and 8..15 of the unit: neighbouring rows of one block, or two blocks of 8
+                uint64_t c0 = at, c1 = at + 8 * (D / 2), sc = at + (lane & NG ? 8 * (NG * 2) : 0);
+                if (p.log2b == 4) {
+                    ++id_at;
+                } else if (p.log2b == 3) {
+                    const uint32_t id1 = __shfl_sync(0xffffffffu, ids, id_at + 1);
+                    c1 = (uint64_t)id1 * p.block_bytes;
+                    sc = lane & NG ? c1 : at;
+                    id_at += 2;
                 } else {
-                    const uint64_t cc = (lane < 16 ? c0 : c1) + (lane & 15) * 16;
-                    cp_async16(wr + k_sw * 16, p.k + cc);
-                    cp_async16(wr + S::kCodes + v_sw * 16, p.v + cc);
-                }
-                if (lane < 4 * NG)
-                    cp_async16(wr + 2 * S::kCodes + lane * 16,
-                               sc_src + (lane & NG ? at1 + tok1 * (NG * 2) : at0 + tok * (NG * 2)));
-                wr = wr + S::kStage == ring_a + S::kRing ? ring_a : wr + S::kStage;
-                if (++cu == cnu) {
-                    cu = 0;
-                    cleft -= kHeadCost;
-                    if (++cvh == VH && cleft > 0) {
-                        cvh = 0;
-                        do {
-                            cctx = __ldg(p.context_lens + ++cs);
-                            cnu = units_of(cctx, max_tokens);
-                        } while (cnu == 0);
+                    if (half) {
+                        c0 += kU * (D / 2);
+                        c1 += kU * (D / 2);
+                        sc += kU * (NG * 2);
                     }
-                    head_at = (uint64_t)(uint32_t)(cvh / p.split) * p.slab;
+                    id_at += half;
+                    half ^= 1;
                 }
+                if constexpr (D == 128) {   // chunks 0..31: rows 0..7, 32..63: rows 8..15
+                    cp_async16(wr + lane * 16, k_src + c0);
+                    cp_async16(wr + lane * 16 + 512, k_src + c1);
+                    cp_async16(wr + S::kCodes + v_sw * 16, v_src + c0);
+                    cp_async16(wr + S::kCodes + 512 + (v_sw ^ 4) * 16, v_src + c1);
+                } else {
+                    cp_async16(wr + k_sw * 16, k_src + (lane < 16 ? c0 : c1));
+                    cp_async16(wr + S::kCodes + v_sw * 16, v_src + (lane < 16 ? c0 : c1));
+                }
+                if (lane < 4 * NG) cp_async16(wr + 2 * S::kCodes + lane * 16, sc_src + sc);
+                wr = wr + S::kStage == ring_a + S::kRing ? ring_a : wr + S::kStage;
+                if (--stretch == 0) next_stretch();
             }
             cp_async_commit();
         };
+        next_stretch();
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) issue();
 
-        uint32_t qf[NT][NS][NG][4];        // the B operand of the first product: pair i holds dims (i, i + 4) of a lane's 8
-        float q0[NT][NG][2];               // -136 sum(q) of a group, for the lane's two columns
-        float o[NT][2 * NG][4], m[NT][2], l[NT][2];
+        // q as B operands of the first product, pair i the dims (i, i + 4) of the lane's 8 (bf16 calls: in fp16, odd
+        // pairs divided by the 16 that their codes carry); q8: three bf16 parts of -8 sum(q) of the groups
+        uint32_t qf[NT][NS][NG][4], q8[NT][2];
+        float o[NT][2 * NG][4], m[NT][2], l[NT][2], sl[NT][2];   // sl: what brings the lane's columns to base-2 logits
+        int lift = 0, lift_e = -1;                                // lift_e: the exponent field that lift goes by
+        uint32_t lift_cap = 0xff80ff80u;                          // the largest bf16 of that exponent, twice
+        float move_at = kMoveAt;                                  // kMoveAt + lift
         bool fresh = true, at_start = true;
         int u_first = 0;
         const uint8_t *st = ring;
@@ -318,12 +369,12 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const int h = 8 * nt + r;
+                    float x[NG][8];
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
-                        float x[8];
                         const T *src = qrow + (int64_t)h * D + 32 * g + 8 * c;
 #pragma unroll
-                        for (int d = 0; d < 8; ++d) x[d] = 0.0f;
+                        for (int d = 0; d < 8; ++d) x[g][d] = 0.0f;
                         if (h < heads) {
                             if (p.vec) {
                                 T y[8];
@@ -331,33 +382,86 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
                                 for (int d = 0; d < (int)sizeof(T) / 2; ++d)
                                     reinterpret_cast<uint4 *>(y)[d] = __ldg(reinterpret_cast<const uint4 *>(src) + d);
 #pragma unroll
-                                for (int d = 0; d < 8; ++d) x[d] = to_float(y[d]);
+                                for (int d = 0; d < 8; ++d) x[g][d] = to_float(y[d]);
                             } else {
 #pragma unroll
-                                for (int d = 0; d < 8; ++d) x[d] = to_float(src[d]);
+                                for (int d = 0; d < 8; ++d) x[g][d] = to_float(src[d]);
                             }
                         }
-                        if (NS == 1) {
-                            float sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-                            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                            sum *= -136.0f;
-                            q0[nt][g][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
-                            q0[nt][g][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
-                        }
+                    }
+                    if constexpr (S::kF32) {
 #pragma unroll
-                        for (int k = 0; k < NS; ++k)
+                        for (int g = 0; g < NG; ++g)
+#pragma unroll
+                            for (int k = 0; k < NS; ++k)
+#pragma unroll
+                                for (int d = 0; d < 4; ++d)
+                                    qf[nt][k][g][d] = pack_bf16x2(bf16_part(x[g][d]), bf16_part(x[g][d + 4]));
+                        sl[nt][0] = sl[nt][1] = p.scale_log2;
+                    } else {
+                        float most = 0.0f;
+#pragma unroll
+                        for (int g = 0; g < NG; ++g)
+#pragma unroll
+                            for (int d = 0; d < 8; ++d) most = fmaxf(most, fabsf(x[g][d]));
+                        float any = 0.0f;   // NaN if an element is NaN or infinite
+#pragma unroll
+                        for (int g = 0; g < NG; ++g)
+#pragma unroll
+                            for (int d = 0; d < 8; ++d) any = fmaf(x[g][d], 0.0f, any);
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                        any += __shfl_xor_sync(0xffffffffu, any, 1);
+                        any += __shfl_xor_sync(0xffffffffu, any, 2);
+                        // biased exponents of the factor that brings `most` into [2^14, 2^15) and of its inverse
+                        const int e = (int)(__float_as_uint(most) >> 23);
+                        const float up = __uint_as_float((uint32_t)min(254, 268 - e) << 23) + any;
+                        const float down = __uint_as_float((uint32_t)max(0, e - 14) << 23) * p.scale_log2;
+                        sl[nt][0] = __shfl_sync(0xffffffffu, down, 8 * c) * 0x1p24f;
+                        sl[nt][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4) * 0x1p24f;
+                        float sums[NG];
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            float sum = 0.0f;
+#pragma unroll
+                            for (int d = 0; d < 8; ++d) {
+                                x[g][d] *= up;
+                                sum += x[g][d];
+                            }
 #pragma unroll
                             for (int d = 0; d < 4; ++d)
-                                qf[nt][k][g][d] = NS == 1 ? pack_bf16x2(x[d], x[d + 4])
-                                                          : pack_bf16x2(bf16_part(x[d]), bf16_part(x[d + 4]));
+                                qf[nt][0][g][d] = d & 1 ? pack_f16x2(x[g][d] * 0.0625f, x[g][d + 4] * 0.0625f)
+                                                        : pack_f16x2(x[g][d], x[g][d + 4]);
+                            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                            sums[g] = sum * (-8.0f * 0x1p-24f);
+                        }
+                        // K index i of the product with the scales: part i / NG, group i % NG
+                        q8[nt][0] = q8[nt][1] = 0;
+#pragma unroll
+                        for (int k = 0; k < 3; ++k)
+#pragma unroll
+                            for (int g = 0; g < NG; g += 2) {
+                                const uint32_t y = pack_bf16x2(bf16_part(sums[g]), bf16_part(sums[g + 1]));
+                                const int at = (k * NG + g) / 2;   // word of K: lane c = at % 4, register at / 4
+                                if (c == at % 4) q8[nt][at / 4] = y;
+                            }
                     }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)   // never 0: masked logits are -inf * sl * sl
+                        if (sl[nt][e] == 0.0f) sl[nt][e] = 0x1p-126f;
 #pragma unroll
                     for (int t = 0; t < 2 * NG; ++t)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[nt][t][e] = 0.0f;
                     m[nt][0] = m[nt][1] = -INFINITY;
                     l[nt][0] = l[nt][1] = 0.0f;
+                }
+                if (!S::kF32) {
+                    lift = 0;
+                    lift_e = -1;
+                    lift_cap = 0xff80ff80u;
+                    move_at = kMoveAt;
                 }
             }
             cp_async_wait<kStages - 2>();
@@ -367,11 +471,8 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
 
             // ---- S = K Q^T
             float x[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.0f;
             {
-                uint32_t k0[NG], k1[NG];
-                float s0[NG], s1[NG];
+                uint32_t k0[NG], k1[NG], z0[NG / 2], z1[NG / 2];
                 if constexpr (D == 128) {
                     *reinterpret_cast<uint4 *>(k0) = *reinterpret_cast<const uint4 *>(st + k_at);
                     *reinterpret_cast<uint4 *>(k1) = *reinterpret_cast<const uint4 *>(st + k_at + 128);
@@ -379,71 +480,109 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
                     *reinterpret_cast<uint2 *>(k0) = *reinterpret_cast<const uint2 *>(st + k_at);
                     *reinterpret_cast<uint2 *>(k1) = *reinterpret_cast<const uint2 *>(st + k_at + two_rows_k);
                 }
-                load_scales<NG>(s0, st + 2 * S::kCodes + t0 * (NG * 2));
-                load_scales<NG>(s1, st + 2 * S::kCodes + t0 * (NG * 2) + NG * 4);
+                load_scales<NG>(z0, st + 2 * S::kCodes + t0 * (NG * 2));
+                load_scales<NG>(z1, st + 2 * S::kCodes + t0 * (NG * 2) + NG * 4);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.0f;
+                    if (!S::kF32) {   // K index i of this product: the scale of group i % NG
+                        const uint32_t a0 = NG == 4 && c & 1 ? z0[NG / 2 - 1] : z0[0];
+                        const uint32_t a1 = NG == 4 && c & 1 ? z1[NG / 2 - 1] : z1[0];
+                        mma_bf16_16816(x[nt], a0, a1, a0, a1, q8[nt][0], q8[nt][1]);
+                    }
+                }
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
+                    const float s0 = scale_of(z0, g), s1 = scale_of(z1, g);
                     uint32_t a[4][2];
+                    if constexpr (S::kF32) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        a[e][0] = nibbles_128(k0[g] >> (4 * e));
-                        a[e][1] = nibbles_128(k1[g] >> (4 * e));
-                        if (NS > 1) {
-                            a[e][0] = minus_136(a[e][0]);
-                            a[e][1] = minus_136(a[e][1]);
+                        for (int e = 0; e < 4; ++e) {
+                            a[e][0] = minus_136(nibbles_128(k0[g] >> (4 * e)));
+                            a[e][1] = minus_136(nibbles_128(k1[g] >> (4 * e)));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            a[e][0] = nibbles_f16(k0[g], e);
+                            a[e][1] = nibbles_f16(k1[g], e);
                         }
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float acc[4];
-                        mma_from(acc, a[0][0], a[0][1], a[1][0], a[1][1], qf[nt][0][g][0], qf[nt][0][g][1],
-                                 NS == 1 ? q0[nt][g][0] : 0.0f, NS == 1 ? q0[nt][g][1] : 0.0f);
-                        mma_bf16_16816(acc, a[2][0], a[2][1], a[3][0], a[3][1], qf[nt][0][g][2], qf[nt][0][g][3]);
+                        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        if constexpr (S::kF32) {
 #pragma unroll
-                        for (int k = 1; k < NS; ++k) {
-                            mma_bf16_16816(acc, a[0][0], a[0][1], a[1][0], a[1][1], qf[nt][k][g][0], qf[nt][k][g][1]);
-                            mma_bf16_16816(acc, a[2][0], a[2][1], a[3][0], a[3][1], qf[nt][k][g][2], qf[nt][k][g][3]);
+                            for (int k = 0; k < NS; ++k) {
+                                mma_bf16_16816(acc, a[0][0], a[0][1], a[1][0], a[1][1], qf[nt][k][g][0], qf[nt][k][g][1]);
+                                mma_bf16_16816(acc, a[2][0], a[2][1], a[3][0], a[3][1], qf[nt][k][g][2], qf[nt][k][g][3]);
+                            }
+                        } else {
+                            mma_f16_16816(acc, a[0][0], a[0][1], a[1][0], a[1][1], qf[nt][0][g][0], qf[nt][0][g][1]);
+                            mma_f16_16816(acc, a[2][0], a[2][1], a[3][0], a[3][1], qf[nt][0][g][2], qf[nt][0][g][3]);
                         }
-                        x[nt][0] = fmaf(s0[g], acc[0], x[nt][0]);
-                        x[nt][1] = fmaf(s0[g], acc[1], x[nt][1]);
-                        x[nt][2] = fmaf(s1[g], acc[2], x[nt][2]);
-                        x[nt][3] = fmaf(s1[g], acc[3], x[nt][3]);
+                        x[nt][0] = fmaf(s0, acc[0], x[nt][0]);
+                        x[nt][1] = fmaf(s0, acc[1], x[nt][1]);
+                        x[nt][2] = fmaf(s1, acc[2], x[nt][2]);
+                        x[nt][3] = fmaf(s1, acc[3], x[nt][3]);
                     }
                 }
             }
             // ---- softmax weights (base 2).  Rows behind the sequence may hold anything, NaN scales too: they are
             // selected away, not multiplied
-            float w[NT][4];
-            auto weigh = [&]() {
-                bool move = false;
+            uint32_t vz0[NG / 2], vz1[NG / 2];   // V's scales
+            load_scales<NG>(vz0, st + 2 * S::kCodes + S::kScales + t0 * (NG * 2));
+            load_scales<NG>(vz1, st + 2 * S::kCodes + S::kScales + t0 * (NG * 2) + NG * 4);
+            if (valid < kU) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[nt][e] = fmaf(x[nt][e], p.scale_log2, -m[nt][e & 1]);
-                if (valid < kU) {
+                    for (int e = 0; e < 4; ++e)
+                        if ((e < 2 ? t0 : t1) >= valid) x[nt][e] = -INFINITY * sl[nt][e & 1];   // times sl: -inf
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if ((e < 2 ? t0 : t1) >= valid) w[nt][e] = -INFINITY;
+                for (int g = 0; g < NG / 2; ++g) {
+                    if (t0 >= valid) vz0[g] = 0;
+                    if (t1 >= valid) vz1[g] = 0;
                 }
+            }
+            float w[NT][4];
+            bool move = false;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) move |= w[nt][e] > kMoveAt;
-                return move;
-            };
-            if (__any_sync(0xffffffffu, weigh())) {
+                for (int e = 0; e < 4; ++e) {
+                    w[nt][e] = fmaf(x[nt][e], sl[nt][e & 1], -m[nt][e & 1]);
+                    move |= w[nt][e] > move_at;
+                }
+            uint32_t top = 0;
+            if (!S::kF32) {
+                top = max_bf16x2(vz0[0], vz1[0]);
+                if (NG == 4) top = max_bf16x2(top, max_bf16x2(vz0[NG / 2 - 1], vz1[NG / 2 - 1]));
+                move |= !__hble2(*reinterpret_cast<const __nv_bfloat162 *>(&top),
+                                 *reinterpret_cast<const __nv_bfloat162 *>(&lift_cap));
+            }
+            if (__any_sync(0xffffffffu, move)) {
+                const int old_lift = lift;
+                if (!S::kF32) {
+                    int t0e = (int)(top & 0x7fffu), t = (int)((top >> 16) & 0x7fffu);
+                    t = max(t0e < 0x7f80 ? t0e : 0, t < 0x7f80 ? t : 0);   // (a NaN scale is no size)
+                    t = max(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                    t = max(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                    t = max(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                    lift_e = max(lift_e, t >> 7);
+                    lift_cap = (uint32_t)(lift_e << 7 | 0x7f) * 0x10001u;
+                    lift = min(100, 133 - lift_e);
+                    move_at = kMoveAt + lift;
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float y = t0 < valid ? x[nt][e] * p.scale_log2 : -INFINITY;
-                        if (t1 < valid) y = fmaxf(y, x[nt][e + 2] * p.scale_log2);
+                        float y = fmaxf(x[nt][e] * sl[nt][e], x[nt][e + 2] * sl[nt][e]);
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-                        y = fmaxf(y, m[nt][e]);
+                        y = fmaxf(y, m[nt][e] + old_lift) - lift;
                         const float alpha = y == m[nt][e] ? 1.0f : fast_exp2(m[nt][e] - y);
                         m[nt][e] = y;
                         l[nt][e] *= alpha;
@@ -452,9 +591,10 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
                             o[nt][t][e] *= alpha;
                             o[nt][t][e + 2] *= alpha;
                         }
+                        w[nt][e] = fmaf(x[nt][e], sl[nt][e], -y);
+                        w[nt][e + 2] = fmaf(x[nt][e + 2], sl[nt][e], -y);
                     }
                 }
-                weigh();
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -466,7 +606,6 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
             // ---- O^T += V^T P^T
             {
                 const uint8_t *vc = st + S::kCodes;
-                float s0[NG], s1[NG];
                 constexpr int NW = NG / 2;       // words of a lane's share of a V row
                 uint32_t vw[4][NW];
 #pragma unroll
@@ -475,45 +614,39 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
                     if constexpr (D == 128) *reinterpret_cast<uint2 *>(vw[t]) = *reinterpret_cast<const uint2 *>(at);
                     else vw[t][0] = *reinterpret_cast<const uint32_t *>(at);
                 }
-                load_scales<NG>(s0, st + 2 * S::kCodes + S::kScales + t0 * (NG * 2));
-                load_scales<NG>(s1, st + 2 * S::kCodes + S::kScales + t0 * (NG * 2) + NG * 4);
-                if (valid < kU) {
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        if (t0 >= valid) s0[g] = 0.0f;
-                        if (t1 >= valid) s1[g] = 0.0f;
-                    }
-                }
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
+                    const float s0 = scale_of(vz0, g), s1 = scale_of(vz1, g);
                     const uint32_t v01 = __byte_perm(vw[0][g / 2], vw[1][g / 2], g & 1 ? 0x7632 : 0x5410);
                     const uint32_t v23 = __byte_perm(vw[2][g / 2], vw[3][g / 2], g & 1 ? 0x7632 : 0x5410);
                     uint32_t a[4][2];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        a[e][0] = minus_136(nibbles_128(v01 >> (4 * e)));
-                        a[e][1] = minus_136(nibbles_128(v23 >> (4 * e)));
+                        a[e][0] = S::kF32 ? minus_136(nibbles_128(v01 >> (4 * e))) : nibbles_f16(v01, e);
+                        a[e][1] = S::kF32 ? minus_136(nibbles_128(v23 >> (4 * e))) : nibbles_f16(v23, e);
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        // the only rounding of a weight: p times V's scale, to bf16 (fp32 calls: three parts)
-                        float y[4] = {x[nt][0] * s0[g], x[nt][1] * s0[g], x[nt][2] * s1[g], x[nt][3] * s1[g]};
+                        // the only rounding of a weight: p times V's scale, to fp16 (fp32 calls: three bf16 parts)
+                        float y[4] = {x[nt][0] * s0, x[nt][1] * s0, x[nt][2] * s1, x[nt][3] * s1};
+                        if constexpr (S::kF32) {
 #pragma unroll
-                        for (int k = 0; k < NS; ++k) {
-                            uint32_t b0, b1;
-                            if (NS == 1) {
-                                b0 = pack_bf16x2(y[0], y[1]);
-                                b1 = pack_bf16x2(y[2], y[3]);
-                            } else {
-                                const float z0 = bf16_part(y[0]), z1 = bf16_part(y[1]);
-                                const float z2 = bf16_part(y[2]), z3 = bf16_part(y[3]);
-                                b0 = pack_bf16x2(z0, z1);
-                                b1 = pack_bf16x2(z2, z3);
+                            for (int k = 0; k < NS; ++k) {
+                                const float y0 = bf16_part(y[0]), y1 = bf16_part(y[1]);
+                                const float y2 = bf16_part(y[2]), y3 = bf16_part(y[3]);
+                                const uint32_t b0 = movmatrix_trans(pack_bf16x2(y0, y1));
+                                const uint32_t b1 = movmatrix_trans(pack_bf16x2(y2, y3));
+                                mma_bf16_16816(o[nt][2 * g], a[0][0], a[1][0], a[0][1], a[1][1], b0, b1);
+                                mma_bf16_16816(o[nt][2 * g + 1], a[2][0], a[3][0], a[2][1], a[3][1], b0, b1);
                             }
-                            b0 = movmatrix_trans(b0);
-                            b1 = movmatrix_trans(b1);
-                            mma_bf16_16816(o[nt][2 * g], a[0][0], a[1][0], a[0][1], a[1][1], b0, b1);
-                            mma_bf16_16816(o[nt][2 * g + 1], a[2][0], a[3][0], a[2][1], a[3][1], b0, b1);
+                        } else {
+                            const uint32_t b0 = movmatrix_trans(pack_f16x2(y[0], y[1]));
+                            const uint32_t b1 = movmatrix_trans(pack_f16x2(y[2], y[3]));
+                            constexpr uint32_t e8 = 0x80088008u, f8 = 0x80808080u;   // -8 2^-24 and -8 2^-20, twice
+                            mma_f16_16816(o[nt][2 * g], a[0][0], a[1][0], a[0][1], a[1][1], b0, b1);
+                            mma_f16_16816(o[nt][2 * g + 1], a[2][0], a[3][0], a[2][1], a[3][1], b0, b1);
+                            mma_f16_16816(o[nt][2 * g], e8, f8, e8, f8, b0, b1);
+                            mma_f16_16816(o[nt][2 * g + 1], e8, f8, e8, f8, b0, b1);
                         }
                     }
                 }
@@ -525,6 +658,17 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
             // ---- the end of a (sequence, head) or of the warp's part
             const int part = vh % p.split, h0 = (vh / p.split) * p.group + part * p.hw;
             const int heads = min(p.hw, p.group - part * p.hw);
+            // rows r of a tile carry 2^-24 (bf16 calls), rows r + 8 2^-20
+            constexpr float kUp0 = S::kF32 ? 1.0f : 0x1p24f, kUp1 = S::kF32 ? 1.0f : 0x1p20f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int t = 0; t < 2 * NG; ++t) {
+                    o[nt][t][0] *= kUp0;
+                    o[nt][t][1] *= kUp0;
+                    o[nt][t][2] *= kUp1;
+                    o[nt][t][3] *= kUp1;
+                }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -566,6 +710,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
                     piece = reinterpret_cast<float *>(ring);
                 }
                 if (lane == 0) meta[2 * warp + (at_start ? 0 : 1)] = {s, vh, u_first, u};
+                const float down = __uint_as_float((uint32_t)(127 - lift) << 23);   // 2^-lift
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -574,10 +719,11 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
 #pragma unroll
                         for (int g = 0; g < NG; ++g)
                             *reinterpret_cast<float4 *>(piece + h * D + 32 * g + 4 * r) =
-                                make_float4(o[nt][2 * g][e], o[nt][2 * g][e + 2], o[nt][2 * g + 1][e], o[nt][2 * g + 1][e + 2]);
+                                make_float4(o[nt][2 * g][e] * down, o[nt][2 * g][e + 2] * down,
+                                            o[nt][2 * g + 1][e] * down, o[nt][2 * g + 1][e + 2] * down);
                         if (r == 0) {
-                            piece[HW * D + 2 * h] = m[nt][e];
-                            piece[HW * D + 2 * h + 1] = l[nt][e];
+                            piece[HW * D + 2 * h] = m[nt][e] + lift;
+                            piece[HW * D + 2 * h + 1] = l[nt][e] * down;
                         }
                     }
             }

@@ -95,6 +95,15 @@ def values(pool, kind, B, D):
     return v.reshape(n, H, B, D).transpose(0, 2, 1, 3)
 
 
+def scales(pool, B, D):
+    """The scale of every value of a pool, float64 [n, B, heads, D]."""
+    raw = pool.cpu().numpy()
+    n, H, _ = raw.shape
+    bits = np.ascontiguousarray(raw[:, :, B * D // 2:]).view("<u2").reshape(n, H, B, D // GROUP)
+    s = (bits.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+    return np.repeat(s, GROUP, -1).transpose(0, 2, 1, 3)
+
+
 def attention(q, k, v, scale):
     """q [H, D], k / v [n, Hkv, D] float64 -> (out, sum p |v|, largest logit magnitude sum scale |q||k|)."""
     H, D = q.shape

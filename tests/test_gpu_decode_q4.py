@@ -69,21 +69,35 @@ class Case:
         for s in range(len(self.ctx)) if seqs is None else seqs:
             n = int(self.ctx[s])
             ids = bt[s, :-(-n // self.B)]
-            ref, mean, mag = R.attention(q[s], k[ids].reshape(-1, self.Hkv, self.D)[:n],
-                                         v[ids].reshape(-1, self.Hkv, self.D)[:n], self.scale)
-            # Logits: fp32 sums of exact products.  The codes enter the first product as n + 128 (up to 143, against
-            # 7 for n - 8) with the surplus taken off in the same sum, so its fp32 steps are those of a sum some
-            # 2 * 143 / 7 times the values' own; 16 roundings or truncations (2^-23) at most lie on a sum's way.
+            kr, vr = k[ids].reshape(-1, self.Hkv, self.D)[:n], v[ids].reshape(-1, self.Hkv, self.D)[:n]
+            ref, mean, mag = R.attention(q[s], kr, vr, self.scale)
+            # Logits.  fp32 sums of exact products; with bf16 queries the codes enter as n (up to 15, against 7 for
+            # n - 8) and the surplus is taken off in the same sum, so its fp32 steps are those of a sum some
+            # 2 * 15 / 7 < 5 times the values' own; 16 roundings or truncations (2^-23) at most lie on a sum's way.
             # The base-2 exponential and its fp32 argument add 2^-22 each of their magnitude.
-            wide = 41 if self.dtype == torch.bfloat16 else 1
-            dx = mag * (wide * 16 * 2.0 ** -23 + 2.0 ** -22) + 2.0 ** -21
+            bf16 = self.dtype == torch.bfloat16
+            dx = mag * ((5 if bf16 else 1) * 16 * 2.0 ** -23 + 2.0 ** -22) + 2.0 ** -21
             # Weights: one rounding to bf16 (2^-8 at most, the scale of V folded in before it); fp32 calls split
             # them into three bf16 parts and drop 2^-24.  Both sums round in fp32, at most one step a token block.
-            dp = 2.0 ** -8 if self.dtype == torch.bfloat16 else 2.0 ** -24
+            dp = 2.0 ** -8 if bf16 else 2.0 ** -24
             steps = (n / 16 + 16) * 2.0 ** -23
-            half = 2.0 ** -8 if self.dtype == torch.bfloat16 else 2.0 ** -24
+            half = 2.0 ** -8 if bf16 else 2.0 ** -24
+            extra = 0.0
+            if bf16:
+                # q in two e4m3 parts, its largest element at 2^7 or more: what lies under the smallest step, 2^-9,
+                # is rounded to it, so an element is off by at most 2^-10 / 2^7 of the largest.
+                G = self.H // self.Hkv
+                ksum = np.repeat(np.abs(kr).sum(-1).max(0), G)
+                dx = dx + 2.0 ** -17 * np.abs(q[s]).max(-1) * self.scale * ksum
+                # Codes enter the second product as n too: a block of tokens is added as sum(n w s) and then
+                # -sum(8 w s), each a product whose 16 addends and sum are cut at 2^-24 of the largest, 15 w s at
+                # most: 2 * 17 * 15 * 2^-24 of sum(w s) over the sequence.
+                zero = np.abs(np.repeat(R.scales(self.v4, self.B, self.D)[ids].reshape(-1, self.Hkv, self.D)[:n], G, 1))
+                x = self.scale * np.einsum("hd,nhd->hn", q[s], np.repeat(kr, G, 1))
+                w = np.exp(x - x.max(-1, keepdims=True))
+                extra = 2 * 17 * 15 * 2.0 ** -24 * np.einsum("hn,nhd->hd", w / w.sum(-1, keepdims=True), zero)
             rel = 2 * dx[:, None] + dp + 2 * steps
-            tol = half * np.abs(ref) * (1 + rel) + rel * mean * (1 + half) + 1e-30
+            tol = half * np.abs(ref) * (1 + rel) + rel * mean * (1 + half) + extra + 1e-30
             err = np.abs(o[s] - ref)
             assert np.all(np.isfinite(o[s])), f"{what} seq {s}: non-finite"
             assert np.all(err <= tol), f"{what} seq {s} (ctx {n}): {float((err / tol).max()):.2f} of the bound"
