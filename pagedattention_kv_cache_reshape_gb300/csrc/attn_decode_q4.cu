@@ -151,6 +151,15 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The first of a chain: D = A B.
+__device__ __forceinline__ void mma_f16_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                    uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
@@ -184,6 +193,10 @@ __device__ __forceinline__ float bf16_part(float &x) {          // the leading b
     x -= h;
     return h;
 }
+
+// A value that is the same in all lanes, marked as such: code that depends on it alone then runs on the warp's
+// uniform registers and branches, beside the lanes' arithmetic.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // The last sequence s with prefix[s] <= t, by the warp, 33 ways a step.
 __device__ __forceinline__ int find_seq(const int64_t *prefix, int num_seqs, int64_t t, int lane) {
@@ -223,7 +236,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ PieceMeta meta[2 * kWarps];
     __shared__ int last_s[2];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
+    const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5), r = lane >> 2, c = lane & 3;
     uint8_t *ring = smem + warp * S::kRing;
     float *first_piece = reinterpret_cast<float *>(smem + kWarps * S::kRing) + warp * S::kPiece;
     const int VH = p.num_kv_heads * p.split, B = 1 << p.log2b, max_tokens = p.max_blocks << p.log2b;
@@ -239,13 +252,13 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
 
     if (w1 > w0) {
         // ---- where the warp's part begins
-        int s = find_seq(p.prefix, p.num_seqs, w0 / VH, lane);
-        int ctx = __ldg(p.context_lens + s), nu = units_of(ctx, max_tokens);
+        int s = uniform(find_seq(p.prefix, p.num_seqs, w0 / VH, lane));
+        int ctx = uniform(__ldg(p.context_lens + s)), nu = units_of(ctx, max_tokens);
         const int64_t in_seq = w0 - p.prefix[s] * VH;
-        int vh = (int)(in_seq / length_of(nu));
-        const int into = (int)(in_seq - (int64_t)vh * length_of(nu));
+        int vh = uniform((int)(in_seq / length_of(nu)));
+        const int into = uniform((int)(in_seq - (int64_t)vh * length_of(nu)));
         int u = max(0, into - kHeadCost);
-        int left = (int)(w1 - w0) - max(0, kHeadCost - into);   // of the part, in stream units
+        int left = uniform((int)(w1 - w0)) - max(0, kHeadCost - into);   // of the part, in stream units
         // ---- the copies' own place in the stream, kStages - 1 units ahead: a stretch is the units whose block
         // ids the lanes hold (id i of the stretch in lane i)
         int cs = s, cctx = ctx, cnu = nu, cvh = vh, cu = u, cleft = left;
@@ -261,6 +274,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
             k_src = p.k + at + chunk * 16;
             v_src = p.v + at + chunk * 16;
             sc_src = (lane < 2 * NG ? p.k : p.v) + at + B * (D / 2) + (lane % NG) * 16;
+            if (p.log2b != 3 && lane & NG) sc_src += 8 * (NG * 2);   // the rows 8..15 of a unit
         };
         at_head();
         auto next_stretch = [&]() {
@@ -270,7 +284,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
                 if (++cvh == VH && cleft > 0) {
                     cvh = 0;
                     do {
-                        cctx = __ldg(p.context_lens + ++cs);
+                        cctx = uniform(__ldg(p.context_lens + ++cs));
                         cnu = units_of(cctx, max_tokens);
                     } while (cnu == 0);
                 }
@@ -299,38 +313,38 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
             cu += stretch;
             cleft -= stretch;
         };
+        auto copy = [&](const uint8_t *k0, const uint8_t *v0, const uint8_t *k1, const uint8_t *v1, const uint8_t *sc) {
+            if constexpr (D == 128) {   // chunks 0..31: rows 0..7, 32..63: rows 8..15
+                cp_async16(wr + lane * 16, k0);
+                cp_async16(wr + lane * 16 + 512, k1);
+                cp_async16(wr + S::kCodes + v_sw * 16, v0);
+                cp_async16(wr + S::kCodes + 512 + (v_sw ^ 4) * 16, v1);
+            } else {
+                cp_async16(wr + k_sw * 16, lane < 16 ? k0 : k1);
+                cp_async16(wr + S::kCodes + v_sw * 16, lane < 16 ? v0 : v1);
+            }
+            if (lane < 4 * NG) cp_async16(wr + 2 * S::kCodes + lane * 16, sc);
+        };
         auto issue = [&]() {
             if (stretch > 0) {
+                // tokens 0..7 and 8..15 of the unit: neighbouring rows of one block, or two blocks of 8
+                constexpr int kHalf = 8 * (D / 2);
                 const uint32_t id = __shfl_sync(0xffffffffu, ids, id_at);
                 const uint64_t at = (uint64_t)id * p.block_bytes;
-                // tokens 0..7 and 8..15 of the unit: neighbouring rows of one block, or two blocks of 8
-                uint64_t c0 = at, c1 = at + 8 * (D / 2), sc = at + (lane & NG ? 8 * (NG * 2) : 0);
                 if (p.log2b == 4) {
                     ++id_at;
+                    copy(k_src + at, v_src + at, k_src + at + kHalf, v_src + at + kHalf, sc_src + at);
                 } else if (p.log2b == 3) {
-                    const uint32_t id1 = __shfl_sync(0xffffffffu, ids, id_at + 1);
-                    c1 = (uint64_t)id1 * p.block_bytes;
-                    sc = lane & NG ? c1 : at;
+                    const uint64_t at1 = (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, ids, id_at + 1) * p.block_bytes;
                     id_at += 2;
+                    copy(k_src + at, v_src + at, k_src + at1, v_src + at1, sc_src + (lane & NG ? at1 : at));
                 } else {
-                    if (half) {
-                        c0 += kU * (D / 2);
-                        c1 += kU * (D / 2);
-                        sc += kU * (NG * 2);
-                    }
+                    const uint64_t rows = at + half * (2 * kHalf);
+                    copy(k_src + rows, v_src + rows, k_src + rows + kHalf, v_src + rows + kHalf,
+                         sc_src + at + half * (kU * NG * 2));
                     id_at += half;
                     half ^= 1;
                 }
-                if constexpr (D == 128) {   // chunks 0..31: rows 0..7, 32..63: rows 8..15
-                    cp_async16(wr + lane * 16, k_src + c0);
-                    cp_async16(wr + lane * 16 + 512, k_src + c1);
-                    cp_async16(wr + S::kCodes + v_sw * 16, v_src + c0);
-                    cp_async16(wr + S::kCodes + 512 + (v_sw ^ 4) * 16, v_src + c1);
-                } else {
-                    cp_async16(wr + k_sw * 16, k_src + (lane < 16 ? c0 : c1));
-                    cp_async16(wr + S::kCodes + v_sw * 16, v_src + (lane < 16 ? c0 : c1));
-                }
-                if (lane < 4 * NG) cp_async16(wr + 2 * S::kCodes + lane * 16, sc_src + sc);
                 wr = wr + S::kStage == ring_a + S::kRing ? ring_a : wr + S::kStage;
                 if (--stretch == 0) next_stretch();
             }
@@ -510,15 +524,16 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        float acc[4];
                         if constexpr (S::kF32) {
+                            acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
 #pragma unroll
                             for (int k = 0; k < NS; ++k) {
                                 mma_bf16_16816(acc, a[0][0], a[0][1], a[1][0], a[1][1], qf[nt][k][g][0], qf[nt][k][g][1]);
                                 mma_bf16_16816(acc, a[2][0], a[2][1], a[3][0], a[3][1], qf[nt][k][g][2], qf[nt][k][g][3]);
                             }
                         } else {
-                            mma_f16_16816(acc, a[0][0], a[0][1], a[1][0], a[1][1], qf[nt][0][g][0], qf[nt][0][g][1]);
+                            mma_f16_16816_first(acc, a[0][0], a[0][1], a[1][0], a[1][1], qf[nt][0][g][0], qf[nt][0][g][1]);
                             mma_f16_16816(acc, a[2][0], a[2][1], a[3][0], a[3][1], qf[nt][0][g][2], qf[nt][0][g][3]);
                         }
                         x[nt][0] = fmaf(s0, acc[0], x[nt][0]);
@@ -734,7 +749,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
             if (++vh == VH && left > 0) {
                 vh = 0;
                 do {
-                    ctx = __ldg(p.context_lens + ++s);
+                    ctx = uniform(__ldg(p.context_lens + ++s));
                     nu = units_of(ctx, max_tokens);
                 } while (nu == 0);
             }
