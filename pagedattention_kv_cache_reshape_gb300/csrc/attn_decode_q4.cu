@@ -46,6 +46,8 @@
 // in bf16), so that no sum carries a surplus.
 #include <math.h>
 
+#include <type_traits>
+
 #include <cuda_fp16.h>
 
 #include "pa_device.cuh"
@@ -56,7 +58,6 @@ namespace pa {
 namespace {
 
 constexpr int kU = 16;              // tokens a unit: the M of the first product, the K of the second
-constexpr int kWarps = 8;
 constexpr int kStages = 4;
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxCtas = 512;
@@ -214,6 +215,7 @@ __device__ __forceinline__ int find_seq(const int64_t *prefix, int num_seqs, int
 template <typename T, int D, int NT>
 struct Q4Shape {
     static constexpr bool kF32 = sizeof(T) == 4;
+    static constexpr int kWarps = NT == 1 && !kF32 ? 12 : 8;   // one CTA per SM
     static constexpr int NS = kF32 ? 3 : 1;           // bf16 parts of q and of a weight
     static constexpr int NG = D / kQ4Group;
     static constexpr int HW = 8 * NT;                 // q-heads a warp has room for
@@ -223,16 +225,15 @@ struct Q4Shape {
     static constexpr int kRing = kStages * kStage;
     static constexpr int kPiece = HW * (D + 2);       // floats: o [HW][D], (m, l) [HW][2]
     static constexpr int kSmem = kWarps * (kRing + kPiece * 4);
-    static constexpr int kCtasPerSm = NT == 1 && NS == 1 ? 2 : 1;
     static_assert(kRing >= kPiece * 4, "a drained ring holds a piece");
 };
 
-struct PieceMeta { int seq, vh, u0, u1; };   // seq < 0: none
+struct PieceMeta { int seq, vh, u0, u1, nu; };   // units [u0, u1) of nu; seq < 0: none
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4_decode_kernel(const Q4Params p) {
+__global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_kernel(const Q4Params p) {
     using S = Q4Shape<T, D, NT>;
-    constexpr int NG = S::NG, NS = S::NS, HW = S::HW;
+    constexpr int NG = S::NG, NS = S::NS, HW = S::HW, kWarps = S::kWarps;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ PieceMeta meta[2 * kWarps];
     __shared__ int last_s[2];
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
         const int into = uniform((int)(in_seq - (int64_t)vh * length_of(nu)));
         int u = max(0, into - kHeadCost);
         int left = uniform((int)(w1 - w0)) - max(0, kHeadCost - into);   // of the part, in stream units
-        // ---- the copies' own place in the stream, kStages - 1 units ahead: a stretch is the units whose block
+        // ---- the copies' own place in the stream, kStages units ahead: a stretch is the units whose block
         // ids the lanes hold (id i of the stretch in lane i)
         int cs = s, cctx = ctx, cnu = nu, cvh = vh, cu = u, cleft = left;
         int stretch = 0, id_at = 0, half = 0, ids = 0, ids_seq = -1, ids_base = 0;
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
         };
         next_stretch();
 #pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) issue();
+        for (int i = 0; i < kStages; ++i) issue();
 
         // q as B operands of the first product, pair i the dims (i, i + 4) of the lane's 8 (bf16 calls: in fp16, odd
         // pairs divided by the 16 that their codes carry); q8: three bf16 parts of -8 sum(q) of the groups
@@ -373,6 +374,224 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
         const int v_at1 = D == 128 ? ((16 * c + 4 + (r >> 1)) ^ (2 * c)) * 16 + (r & 1) * 8 : ((8 * c + 2 + (r >> 2)) ^ (2 * c)) * 16 + (r & 3) * 4;
         // a tile's bytes two rows on (head_dim 64: the swizzle turns the step round)
         const int two_rows_k = D == 128 || !((t0 >> 2) & 1) ? D : -D, two_rows_v = D == 128 || c < 2 ? D : -D;
+        // One or two units of the current head.
+        auto step = [&](auto units) {
+            constexpr int NU = decltype(units)::value;
+            // the oldest units' copies are in (kStages are on their way at all times), for every lane
+            cp_async_wait<kStages - NU>();
+            __syncwarp();
+            const uint8_t *at[NU];
+#pragma unroll
+            for (int j = 0; j < NU; ++j) {
+                at[j] = st;
+                st = st + S::kStage == ring + S::kRing ? ring : st + S::kStage;
+            }
+            const int valid = ctx - (u + NU - 1) * kU;      // tokens of the last unit that exist
+            constexpr int L = NU - 1;
+
+            // ---- S = K Q^T
+            float x[NU][NT][4];
+#pragma unroll
+            for (int j = 0; j < NU; ++j) {
+                uint32_t k0[NG], k1[NG], z0[NG / 2], z1[NG / 2];
+                if constexpr (D == 128) {
+                    *reinterpret_cast<uint4 *>(k0) = *reinterpret_cast<const uint4 *>(at[j] + k_at);
+                    *reinterpret_cast<uint4 *>(k1) = *reinterpret_cast<const uint4 *>(at[j] + k_at + 128);
+                } else {
+                    *reinterpret_cast<uint2 *>(k0) = *reinterpret_cast<const uint2 *>(at[j] + k_at);
+                    *reinterpret_cast<uint2 *>(k1) = *reinterpret_cast<const uint2 *>(at[j] + k_at + two_rows_k);
+                }
+                load_scales<NG>(z0, at[j] + 2 * S::kCodes + t0 * (NG * 2));
+                load_scales<NG>(z1, at[j] + 2 * S::kCodes + t0 * (NG * 2) + NG * 4);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    x[j][nt][0] = x[j][nt][1] = x[j][nt][2] = x[j][nt][3] = 0.0f;
+                    if (!S::kF32) {   // K index i of this product: the scale of group i % NG
+                        const uint32_t a0 = NG == 4 && c & 1 ? z0[NG / 2 - 1] : z0[0];
+                        const uint32_t a1 = NG == 4 && c & 1 ? z1[NG / 2 - 1] : z1[0];
+                        mma_bf16_16816(x[j][nt], a0, a1, a0, a1, q8[nt][0], q8[nt][1]);
+                    }
+                }
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const float s0 = scale_of(z0, g), s1 = scale_of(z1, g);
+                    uint32_t a[4][2];
+                    if constexpr (S::kF32) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            a[e][0] = minus_136(nibbles_128(k0[g] >> (4 * e)));
+                            a[e][1] = minus_136(nibbles_128(k1[g] >> (4 * e)));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            a[e][0] = nibbles_f16(k0[g], e);
+                            a[e][1] = nibbles_f16(k1[g], e);
+                        }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float acc[4];
+                        if constexpr (S::kF32) {
+                            acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+#pragma unroll
+                            for (int k = 0; k < NS; ++k) {
+                                mma_bf16_16816(acc, a[0][0], a[0][1], a[1][0], a[1][1], qf[nt][k][g][0], qf[nt][k][g][1]);
+                                mma_bf16_16816(acc, a[2][0], a[2][1], a[3][0], a[3][1], qf[nt][k][g][2], qf[nt][k][g][3]);
+                            }
+                        } else {
+                            mma_f16_16816_first(acc, a[0][0], a[0][1], a[1][0], a[1][1], qf[nt][0][g][0], qf[nt][0][g][1]);
+                            mma_f16_16816(acc, a[2][0], a[2][1], a[3][0], a[3][1], qf[nt][0][g][2], qf[nt][0][g][3]);
+                        }
+                        x[j][nt][0] = fmaf(s0, acc[0], x[j][nt][0]);
+                        x[j][nt][1] = fmaf(s0, acc[1], x[j][nt][1]);
+                        x[j][nt][2] = fmaf(s1, acc[2], x[j][nt][2]);
+                        x[j][nt][3] = fmaf(s1, acc[3], x[j][nt][3]);
+                    }
+                }
+            }
+            // ---- softmax weights (base 2).  Rows behind the sequence may hold anything, NaN scales too: they are
+            // selected away, not multiplied
+            uint32_t vz0[NU][NG / 2], vz1[NU][NG / 2];   // V's scales
+#pragma unroll
+            for (int j = 0; j < NU; ++j) {
+                load_scales<NG>(vz0[j], at[j] + 2 * S::kCodes + S::kScales + t0 * (NG * 2));
+                load_scales<NG>(vz1[j], at[j] + 2 * S::kCodes + S::kScales + t0 * (NG * 2) + NG * 4);
+            }
+            if (valid < kU) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if ((e < 2 ? t0 : t1) >= valid) x[L][nt][e] = -INFINITY * sl[nt][e & 1];   // times sl: -inf
+#pragma unroll
+                for (int g = 0; g < NG / 2; ++g) {
+                    if (t0 >= valid) vz0[L][g] = 0;
+                    if (t1 >= valid) vz1[L][g] = 0;
+                }
+            }
+            float w[NU][NT][4];
+            bool move = false;
+#pragma unroll
+            for (int j = 0; j < NU; ++j)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        w[j][nt][e] = fmaf(x[j][nt][e], sl[nt][e & 1], -m[nt][e & 1]);
+                        move |= w[j][nt][e] > move_at;
+                    }
+            uint32_t top = 0;
+            if (!S::kF32) {
+#pragma unroll
+                for (int j = 0; j < NU; ++j)
+#pragma unroll
+                    for (int g = 0; g < NG / 2; ++g) top = max_bf16x2(top, max_bf16x2(vz0[j][g], vz1[j][g]));
+                move |= !__hble2(*reinterpret_cast<const __nv_bfloat162 *>(&top),
+                                 *reinterpret_cast<const __nv_bfloat162 *>(&lift_cap));
+            }
+            if (__any_sync(0xffffffffu, move)) {
+                const int old_lift = lift;
+                if (!S::kF32) {
+                    int t0e = (int)(top & 0x7fffu), t = (int)((top >> 16) & 0x7fffu);
+                    t = max(t0e < 0x7f80 ? t0e : 0, t < 0x7f80 ? t : 0);   // (a NaN scale is no size)
+                    t = max(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                    t = max(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                    t = uniform(max(t, __shfl_xor_sync(0xffffffffu, t, 16)));
+                    lift_e = max(lift_e, t >> 7);
+                    lift_cap = (uint32_t)(lift_e << 7 | 0x7f) * 0x10001u;
+                    lift = min(100, 133 - lift_e);
+                    move_at = kMoveAt + lift;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float y = m[nt][e] + old_lift;
+#pragma unroll
+                        for (int j = 0; j < NU; ++j)
+                            y = fmaxf(y, fmaxf(x[j][nt][e] * sl[nt][e], x[j][nt][e + 2] * sl[nt][e]));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16)) - lift;
+                        const float alpha = y == m[nt][e] ? 1.0f : fast_exp2(m[nt][e] - y);
+                        m[nt][e] = y;
+                        l[nt][e] *= alpha;
+#pragma unroll
+                        for (int t = 0; t < 2 * NG; ++t) {
+                            o[nt][t][e] *= alpha;
+                            o[nt][t][e + 2] *= alpha;
+                        }
+#pragma unroll
+                        for (int j = 0; j < NU; ++j) {
+                            w[j][nt][e] = fmaf(x[j][nt][e], sl[nt][e], -y);
+                            w[j][nt][e + 2] = fmaf(x[j][nt][e + 2], sl[nt][e], -y);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NU; ++j)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[j][nt][e] = fast_exp2(w[j][nt][e]);
+                        l[nt][e & 1] += x[j][nt][e];
+                    }
+            // ---- O^T += V^T P^T
+#pragma unroll
+            for (int j = 0; j < NU; ++j) {
+                const uint8_t *vc = at[j] + S::kCodes;
+                constexpr int NW = NG / 2;       // words of a lane's share of a V row
+                uint32_t vw[4][NW];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const uint8_t *row = vc + (t & 1 ? v_at1 : v_at0) + (t < 2 ? 0 : two_rows_v);
+                    if constexpr (D == 128) *reinterpret_cast<uint2 *>(vw[t]) = *reinterpret_cast<const uint2 *>(row);
+                    else vw[t][0] = *reinterpret_cast<const uint32_t *>(row);
+                }
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const float s0 = scale_of(vz0[j], g), s1 = scale_of(vz1[j], g);
+                    const uint32_t v01 = __byte_perm(vw[0][g / 2], vw[1][g / 2], g & 1 ? 0x7632 : 0x5410);
+                    const uint32_t v23 = __byte_perm(vw[2][g / 2], vw[3][g / 2], g & 1 ? 0x7632 : 0x5410);
+                    uint32_t a[4][2];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        a[e][0] = S::kF32 ? minus_136(nibbles_128(v01 >> (4 * e))) : nibbles_f16(v01, e);
+                        a[e][1] = S::kF32 ? minus_136(nibbles_128(v23 >> (4 * e))) : nibbles_f16(v23, e);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        // the only rounding of a weight: p times V's scale, to fp16 (fp32 calls: three bf16 parts)
+                        float y[4] = {x[j][nt][0] * s0, x[j][nt][1] * s0, x[j][nt][2] * s1, x[j][nt][3] * s1};
+                        if constexpr (S::kF32) {
+#pragma unroll
+                            for (int k = 0; k < NS; ++k) {
+                                const float y0 = bf16_part(y[0]), y1 = bf16_part(y[1]);
+                                const float y2 = bf16_part(y[2]), y3 = bf16_part(y[3]);
+                                const uint32_t b0 = movmatrix_trans(pack_bf16x2(y0, y1));
+                                const uint32_t b1 = movmatrix_trans(pack_bf16x2(y2, y3));
+                                mma_bf16_16816(o[nt][2 * g], a[0][0], a[1][0], a[0][1], a[1][1], b0, b1);
+                                mma_bf16_16816(o[nt][2 * g + 1], a[2][0], a[3][0], a[2][1], a[3][1], b0, b1);
+                            }
+                        } else {
+                            const uint32_t b0 = movmatrix_trans(pack_f16x2(y[0], y[1]));
+                            const uint32_t b1 = movmatrix_trans(pack_f16x2(y[2], y[3]));
+                            constexpr uint32_t e8 = 0x80088008u, f8 = 0x80808080u;   // -8 2^-24 and -8 2^-20, twice
+                            mma_f16_16816(o[nt][2 * g], a[0][0], a[1][0], a[0][1], a[1][1], b0, b1);
+                            mma_f16_16816(o[nt][2 * g + 1], a[2][0], a[3][0], a[2][1], a[3][1], b0, b1);
+                            mma_f16_16816(o[nt][2 * g], e8, f8, e8, f8, b0, b1);
+                            mma_f16_16816(o[nt][2 * g + 1], e8, f8, e8, f8, b0, b1);
+                        }
+                    }
+                }
+            }
+            __syncwarp();   // every lane is done with the units' places
+#pragma unroll
+            for (int j = 0; j < NU; ++j) issue();
+        };
         while (left > 0) {
             if (fresh) {
                 fresh = false;
@@ -478,197 +697,12 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
                     move_at = kMoveAt;
                 }
             }
-            cp_async_wait<kStages - 2>();
-            __syncwarp();   // every lane's copies are in, and every lane is done with the slot filled next
-            issue();
-            const int valid = ctx - u * kU;                 // tokens of the unit that exist
-
-            // ---- S = K Q^T
-            float x[NT][4];
-            {
-                uint32_t k0[NG], k1[NG], z0[NG / 2], z1[NG / 2];
-                if constexpr (D == 128) {
-                    *reinterpret_cast<uint4 *>(k0) = *reinterpret_cast<const uint4 *>(st + k_at);
-                    *reinterpret_cast<uint4 *>(k1) = *reinterpret_cast<const uint4 *>(st + k_at + 128);
-                } else {
-                    *reinterpret_cast<uint2 *>(k0) = *reinterpret_cast<const uint2 *>(st + k_at);
-                    *reinterpret_cast<uint2 *>(k1) = *reinterpret_cast<const uint2 *>(st + k_at + two_rows_k);
-                }
-                load_scales<NG>(z0, st + 2 * S::kCodes + t0 * (NG * 2));
-                load_scales<NG>(z1, st + 2 * S::kCodes + t0 * (NG * 2) + NG * 4);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.0f;
-                    if (!S::kF32) {   // K index i of this product: the scale of group i % NG
-                        const uint32_t a0 = NG == 4 && c & 1 ? z0[NG / 2 - 1] : z0[0];
-                        const uint32_t a1 = NG == 4 && c & 1 ? z1[NG / 2 - 1] : z1[0];
-                        mma_bf16_16816(x[nt], a0, a1, a0, a1, q8[nt][0], q8[nt][1]);
-                    }
-                }
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const float s0 = scale_of(z0, g), s1 = scale_of(z1, g);
-                    uint32_t a[4][2];
-                    if constexpr (S::kF32) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            a[e][0] = minus_136(nibbles_128(k0[g] >> (4 * e)));
-                            a[e][1] = minus_136(nibbles_128(k1[g] >> (4 * e)));
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            a[e][0] = nibbles_f16(k0[g], e);
-                            a[e][1] = nibbles_f16(k1[g], e);
-                        }
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float acc[4];
-                        if constexpr (S::kF32) {
-                            acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
-#pragma unroll
-                            for (int k = 0; k < NS; ++k) {
-                                mma_bf16_16816(acc, a[0][0], a[0][1], a[1][0], a[1][1], qf[nt][k][g][0], qf[nt][k][g][1]);
-                                mma_bf16_16816(acc, a[2][0], a[2][1], a[3][0], a[3][1], qf[nt][k][g][2], qf[nt][k][g][3]);
-                            }
-                        } else {
-                            mma_f16_16816_first(acc, a[0][0], a[0][1], a[1][0], a[1][1], qf[nt][0][g][0], qf[nt][0][g][1]);
-                            mma_f16_16816(acc, a[2][0], a[2][1], a[3][0], a[3][1], qf[nt][0][g][2], qf[nt][0][g][3]);
-                        }
-                        x[nt][0] = fmaf(s0, acc[0], x[nt][0]);
-                        x[nt][1] = fmaf(s0, acc[1], x[nt][1]);
-                        x[nt][2] = fmaf(s1, acc[2], x[nt][2]);
-                        x[nt][3] = fmaf(s1, acc[3], x[nt][3]);
-                    }
-                }
-            }
-            // ---- softmax weights (base 2).  Rows behind the sequence may hold anything, NaN scales too: they are
-            // selected away, not multiplied
-            uint32_t vz0[NG / 2], vz1[NG / 2];   // V's scales
-            load_scales<NG>(vz0, st + 2 * S::kCodes + S::kScales + t0 * (NG * 2));
-            load_scales<NG>(vz1, st + 2 * S::kCodes + S::kScales + t0 * (NG * 2) + NG * 4);
-            if (valid < kU) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if ((e < 2 ? t0 : t1) >= valid) x[nt][e] = -INFINITY * sl[nt][e & 1];   // times sl: -inf
-#pragma unroll
-                for (int g = 0; g < NG / 2; ++g) {
-                    if (t0 >= valid) vz0[g] = 0;
-                    if (t1 >= valid) vz1[g] = 0;
-                }
-            }
-            float w[NT][4];
-            bool move = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    w[nt][e] = fmaf(x[nt][e], sl[nt][e & 1], -m[nt][e & 1]);
-                    move |= w[nt][e] > move_at;
-                }
-            uint32_t top = 0;
-            if (!S::kF32) {
-                top = max_bf16x2(vz0[0], vz1[0]);
-                if (NG == 4) top = max_bf16x2(top, max_bf16x2(vz0[NG / 2 - 1], vz1[NG / 2 - 1]));
-                move |= !__hble2(*reinterpret_cast<const __nv_bfloat162 *>(&top),
-                                 *reinterpret_cast<const __nv_bfloat162 *>(&lift_cap));
-            }
-            if (__any_sync(0xffffffffu, move)) {
-                const int old_lift = lift;
-                if (!S::kF32) {
-                    int t0e = (int)(top & 0x7fffu), t = (int)((top >> 16) & 0x7fffu);
-                    t = max(t0e < 0x7f80 ? t0e : 0, t < 0x7f80 ? t : 0);   // (a NaN scale is no size)
-                    t = max(t, __shfl_xor_sync(0xffffffffu, t, 4));
-                    t = max(t, __shfl_xor_sync(0xffffffffu, t, 8));
-                    t = max(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                    lift_e = max(lift_e, t >> 7);
-                    lift_cap = (uint32_t)(lift_e << 7 | 0x7f) * 0x10001u;
-                    lift = min(100, 133 - lift_e);
-                    move_at = kMoveAt + lift;
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float y = fmaxf(x[nt][e] * sl[nt][e], x[nt][e + 2] * sl[nt][e]);
-                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
-                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
-                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-                        y = fmaxf(y, m[nt][e] + old_lift) - lift;
-                        const float alpha = y == m[nt][e] ? 1.0f : fast_exp2(m[nt][e] - y);
-                        m[nt][e] = y;
-                        l[nt][e] *= alpha;
-#pragma unroll
-                        for (int t = 0; t < 2 * NG; ++t) {
-                            o[nt][t][e] *= alpha;
-                            o[nt][t][e + 2] *= alpha;
-                        }
-                        w[nt][e] = fmaf(x[nt][e], sl[nt][e], -y);
-                        w[nt][e + 2] = fmaf(x[nt][e + 2], sl[nt][e], -y);
-                    }
-                }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[nt][e] = fast_exp2(w[nt][e]);
-                    l[nt][e & 1] += x[nt][e];
-                }
-            // ---- O^T += V^T P^T
-            {
-                const uint8_t *vc = st + S::kCodes;
-                constexpr int NW = NG / 2;       // words of a lane's share of a V row
-                uint32_t vw[4][NW];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const uint8_t *at = vc + (t & 1 ? v_at1 : v_at0) + (t < 2 ? 0 : two_rows_v);
-                    if constexpr (D == 128) *reinterpret_cast<uint2 *>(vw[t]) = *reinterpret_cast<const uint2 *>(at);
-                    else vw[t][0] = *reinterpret_cast<const uint32_t *>(at);
-                }
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const float s0 = scale_of(vz0, g), s1 = scale_of(vz1, g);
-                    const uint32_t v01 = __byte_perm(vw[0][g / 2], vw[1][g / 2], g & 1 ? 0x7632 : 0x5410);
-                    const uint32_t v23 = __byte_perm(vw[2][g / 2], vw[3][g / 2], g & 1 ? 0x7632 : 0x5410);
-                    uint32_t a[4][2];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        a[e][0] = S::kF32 ? minus_136(nibbles_128(v01 >> (4 * e))) : nibbles_f16(v01, e);
-                        a[e][1] = S::kF32 ? minus_136(nibbles_128(v23 >> (4 * e))) : nibbles_f16(v23, e);
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        // the only rounding of a weight: p times V's scale, to fp16 (fp32 calls: three bf16 parts)
-                        float y[4] = {x[nt][0] * s0, x[nt][1] * s0, x[nt][2] * s1, x[nt][3] * s1};
-                        if constexpr (S::kF32) {
-#pragma unroll
-                            for (int k = 0; k < NS; ++k) {
-                                const float y0 = bf16_part(y[0]), y1 = bf16_part(y[1]);
-                                const float y2 = bf16_part(y[2]), y3 = bf16_part(y[3]);
-                                const uint32_t b0 = movmatrix_trans(pack_bf16x2(y0, y1));
-                                const uint32_t b1 = movmatrix_trans(pack_bf16x2(y2, y3));
-                                mma_bf16_16816(o[nt][2 * g], a[0][0], a[1][0], a[0][1], a[1][1], b0, b1);
-                                mma_bf16_16816(o[nt][2 * g + 1], a[2][0], a[3][0], a[2][1], a[3][1], b0, b1);
-                            }
-                        } else {
-                            const uint32_t b0 = movmatrix_trans(pack_f16x2(y[0], y[1]));
-                            const uint32_t b1 = movmatrix_trans(pack_f16x2(y[2], y[3]));
-                            constexpr uint32_t e8 = 0x80088008u, f8 = 0x80808080u;   // -8 2^-24 and -8 2^-20, twice
-                            mma_f16_16816(o[nt][2 * g], a[0][0], a[1][0], a[0][1], a[1][1], b0, b1);
-                            mma_f16_16816(o[nt][2 * g + 1], a[2][0], a[3][0], a[2][1], a[3][1], b0, b1);
-                            mma_f16_16816(o[nt][2 * g], e8, f8, e8, f8, b0, b1);
-                            mma_f16_16816(o[nt][2 * g + 1], e8, f8, e8, f8, b0, b1);
-                        }
-                    }
-                }
-            }
-            st = st + S::kStage == ring + S::kRing ? ring : st + S::kStage;
-            ++u;
-            if (--left > 0 && u < nu) continue;
+            const int pair = left > 1 && u + 1 < nu ? 2 : 1;
+            if (pair == 2) step(std::integral_constant<int, 2>());
+            else step(std::integral_constant<int, 1>());
+            u += pair;
+            left -= pair;
+            if (left > 0 && u < nu) continue;
 
             // ---- the end of a (sequence, head) or of the warp's part
             const int part = vh % p.split, h0 = (vh / p.split) * p.group + part * p.hw;
@@ -724,7 +758,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
                     __syncwarp();
                     piece = reinterpret_cast<float *>(ring);
                 }
-                if (lane == 0) meta[2 * warp + (at_start ? 0 : 1)] = {s, vh, u_first, u};
+                if (lane == 0) meta[2 * warp + (at_start ? 0 : 1)] = {s, vh, u_first, u, nu};
                 const float down = __uint_as_float((uint32_t)(127 - lift) << 23);   // 2^-lift
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -770,26 +804,26 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
 #pragma unroll
         for (int d = 0; d < PER; ++d) dst[d * 32 + lane] = from_float<T>(acc[d] * inv);
     };
-    PieceMeta cut[2];   // the CTA's pieces of sequences that other CTAs share: cut on the left, cut on the right only
+    PieceMeta cut[2];   // the CTA's part of a head cut on its left, and of one cut on its right only
     cut[0].seq = cut[1].seq = -1;
+    int task = 0;       // (head of a sequence, q-head) pairs go round the warps
     for (int j0 = 0; j0 < 2 * kWarps;) {
-        const PieceMeta a = meta[j0];
+        PieceMeta a = meta[j0];
         if (a.seq < 0) { ++j0; continue; }
-        int j1 = j0 + 1, u1 = a.u1;
+        int j1 = j0 + 1;
         for (; j1 < 2 * kWarps; ++j1) {
-            const PieceMeta b = meta[j1];
-            if (b.seq < 0) continue;
-            if (b.seq != a.seq || b.vh != a.vh) break;
-            u1 = b.u1;
+            if (meta[j1].seq < 0) continue;
+            if (meta[j1].seq != a.seq || meta[j1].vh != a.vh) break;
+            a.u1 = meta[j1].u1;
         }
-        const int nu = units_of(__ldg(p.context_lens + a.seq), max_tokens);
-        const bool whole = a.u0 == 0 && u1 == nu;
+        const bool whole = a.u0 == 0 && a.u1 == a.nu;
         const int side = a.u0 == 0 ? 1 : 0;
-        if (!whole) cut[side] = {a.seq, a.vh, a.u0, u1};
+        if (!whole) cut[side] = a;
         const int part = a.vh % p.split, h0 = (a.vh / p.split) * p.group + part * p.hw;
         const int heads = min(p.hw, p.group - part * p.hw);
         float *dst = p.part + ((int64_t)blockIdx.x * 2 + side) * S::kPiece;
-        for (int h = warp; h < heads; h += kWarps) {
+        for (int h = 0; h < heads; ++h) {
+            if (task++ % kWarps != warp) continue;
             float M = -INFINITY, L = 0.0f, acc[PER];
 #pragma unroll
             for (int d = 0; d < PER; ++d) acc[d] = 0.0f;
@@ -817,20 +851,15 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
         j0 = j1;
     }
     if (cut[0].seq < 0 && cut[1].seq < 0) return;
-    // ---- sequences cut between CTAs: the last CTA to arrive merges their pieces, in stream order
+    // ---- heads cut between CTAs: the last CTA to arrive merges their pieces, in stream order.  The first unit
+    // of the head cut on the left lies u0 before the CTA's share, that of the other u1 before its end.
     __threadfence();
     __syncthreads();
-    auto span = [&](const PieceMeta &a, int64_t &c0, int64_t &c1) {
-        const int nu = units_of(__ldg(p.context_lens + a.seq), max_tokens);
-        const int64_t at = p.prefix[a.seq] * VH + (int64_t)a.vh * length_of(nu) + kHeadCost;
-        c0 = at / share;
-        c1 = (at + nu - 1) / share;
-    };
+    const int64_t at[2] = {cta0 - cut[0].u0, cta1 - cut[1].u1};
     if (tid < 2) {
         int last = 0;
         if (cut[tid].seq >= 0) {
-            int64_t c0, c1;
-            span(cut[tid], c0, c1);
+            const int64_t c0 = at[tid] / share, c1 = (at[tid] + cut[tid].nu - 1) / share;
             last = atomic_add_acq_rel_gpu(p.arrivals + c0, 1) == (int)(c1 - c0);
         }
         last_s[tid] = last;
@@ -840,8 +869,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<T, D, NT>::kCtasPerSm) q4
     for (int side = 0; side < 2; ++side) {
         if (!last_s[side]) continue;
         const PieceMeta a = cut[side];
-        int64_t c0, c1;
-        span(a, c0, c1);
+        const int64_t c0 = at[side] / share, c1 = (at[side] + a.nu - 1) / share;
         const int part = a.vh % p.split, h0 = (a.vh / p.split) * p.group + part * p.hw;
         const int heads = min(p.hw, p.group - part * p.hw);
         for (int h = warp; h < heads; h += kWarps) {
@@ -880,11 +908,11 @@ cudaError_t launch_typed(Q4Params p, const AttnArgs &a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     p.split = (p.group + S::HW - 1) / S::HW;
     p.hw = (p.group + p.split - 1) / p.split;
-    const int grid = min(kMaxCtas, device_sm_count() * S::kCtasPerSm);
+    const int grid = min(kMaxCtas, device_sm_count());
     e = launch_dependent(q4_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a.context_lens, a.num_seqs,
                          (int)(a.max_blocks * a.block_size), const_cast<int64_t *>(p.prefix), p.arrivals, a.status);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3(grid), dim3(kWarps * 32), S::kSmem, stream, p);
+    return launch_dependent(kern, dim3(grid), dim3(S::kWarps * 32), S::kSmem, stream, p);
 }
 
 }  // namespace
