@@ -39,21 +39,105 @@ __host__ __device__ constexpr int q4_v_unit(int dim, int d) {
     return (((dim % kQ4Group) / 4) * (d / kQ4Group) + dim / kQ4Group) * 2;
 }
 
-// The scale of a group whose largest magnitude is amax, in bf16 bits.  A group
-// with a NaN or an infinity (`finite` false) takes a NaN scale: all its values
-// read back as NaN.
-__device__ __forceinline__ uint16_t q4_scale_bits(float amax, bool finite) {
-    if (!finite) return 0x7fc0u;
-    return __bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(amax, 7.0f)));
+// Bits of the scale of a group from the bits of its largest magnitude.  NaN and
+// infinities have the largest bit patterns, so a group that holds one is found
+// by the same integer maximum; it takes a NaN scale and reads back as NaN.
+__device__ __forceinline__ uint16_t q4_scale_bits(uint32_t amax_bits) {
+    if (amax_bits >= 0x7f800000u) return 0x7fc0u;
+    return __bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(__uint_as_float(amax_bits), 7.0f)));
 }
 __device__ __forceinline__ float q4_scale_value(uint16_t bits) {
     return __uint_as_float((uint32_t)bits << 16);
 }
-// The nibble of x in a group of scale s (0 or NaN: every nibble 8).
-__device__ __forceinline__ uint32_t q4_code(float x, float s) {
-    if (!(s > 0.0f)) return 8u;
-    const float n = fminf(fmaxf(rintf(__fdiv_rn(x, s)), -7.0f), 7.0f);
-    return (uint32_t)((int)n + 8);
+
+// The word of 8 values' nibbles (x[0] lowest) in a group of scale s.
+// The quotient x / s is the correctly rounded one, by Markstein's correction
+// of x r, r the correctly rounded 1 / s, with the exact remainder (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990); the range of s keeps the remainders of quotients from 1/4 up normal,
+// and smaller quotients round to 0 either way.  Adding 1.5 2^23 + 8 rounds a
+// quotient to the nearest integer, ties to even, with n + 8 in the low bits;
+// |x / s| <= 7 (1 + 2^-8) there, so no clamp is needed.
+__device__ __forceinline__ uint32_t q4_word(const float (&x)[8], float s) {
+    constexpr float kRound = 12582912.0f + 8.0f;
+    uint32_t w = 0;
+    if (s >= 0x1p-90f && s <= 0x1p90f) {
+        const float r = __frcp_rn(s);
+#pragma unroll
+        for (int i = 7; i >= 0; --i) {
+            const float q0 = __fmul_rn(x[i], r);
+            const float q = __fmaf_rn(__fmaf_rn(-q0, s, x[i]), r, q0);
+            w = w * 16u + __float_as_uint(__fadd_rn(q, kRound));
+        }
+        // the eight sums carry the exponent field of 1.5 2^23 each: 0x4b400000 (1 + 16 + ... + 16^7) mod 2^32
+        return w - 0x3f400000u;
+    }
+    if (!(s > 0.0f)) return 0x88888888u;   // 0 or NaN
+#pragma unroll
+    for (int i = 7; i >= 0; --i) {
+        const float n = fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), -7.0f), 7.0f);
+        w = w * 16u + (uint32_t)((int)n + 8);
+    }
+    return w;
+}
+
+// 8 consecutive values of a row in registers, from 16-byte aligned memory.
+__device__ __forceinline__ void load8(float (&x)[8], const __nv_bfloat16 *p) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void load8(float (&x)[8], const float *p) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *(reinterpret_cast<const float4 *>(p) + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    *(reinterpret_cast<float4 *>(p) + 1) = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// Quantises 8 values, dims 8 k .. 8 k + 7 of a token row, and stores them: called
+// by whole warps in which the D / 8 lanes of a row are neighbours in order of
+// k, a row's first lane a multiple of D / 8.  `row` is the row's code bytes and
+// `scales` its scales; lanes with store = false only take part in the shuffles.
+template <int D>
+__device__ __forceinline__ void q4_store8(const float (&x)[8], int k, bool is_v, uint8_t *row, uint16_t *scales,
+                                          bool store) {
+    constexpr int NG = D / kQ4Group;
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const uint16_t sb = q4_scale_bits(amax);
+    const uint32_t w = q4_word(x, q4_scale_value(sb));
+    // V: a lane holds units r = 2 (k % 4) and r + 1 of group g; with its neighbour group's lane it makes the 4
+    // bytes (r, g), (r, g + 1) or (r + 1, g - 1), (r + 1, g)
+    const int g = k / 4;
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 4);
+    if (!store) return;
+    if (is_v) {
+        const uint32_t pair = g & 1 ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
+        const int r = 2 * (k & 3) + (g & 1);
+        *reinterpret_cast<uint32_t *>(row + (r * NG + (g & ~1)) * 2) = pair;
+    } else {
+        *reinterpret_cast<uint32_t *>(row + q4_k_word(8 * k, D)) = w;
+    }
+    if ((k & 3) == 0) scales[g] = sb;
 }
 
 }  // namespace pa

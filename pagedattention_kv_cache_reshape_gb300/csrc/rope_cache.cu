@@ -7,6 +7,13 @@
 // cos_i = cos_sin[p][i], sin_i = cos_sin[p][R + i]; dims from rot_dim on pass
 // through.  The row is rounded to the inputs' type and stored like
 // reshape_and_cache's, or quantised from there (q4_format.cuh).
+//
+// Bound by HBM: every row is read and written once.  A thread of the fast
+// kernel owns the two vectors of 8 dims whose elements pair up, so it needs 8
+// cosines and 8 sines for 16 values, no exchange with other lanes, and may
+// write q in place; a CTA takes a token's rows in one pass, K and V rows among
+// them.  Rows that do not come in 16-byte pieces (head_dim or rot_dim no
+// multiple of 16, odd addresses or strides) take the element-wise kernel.
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "q4_format.cuh"
@@ -30,6 +37,18 @@ __device__ __forceinline__ float rotate_exact(float a, float c, float b, float s
     return __fadd_rn(sum, __fadd_rn(es, __fadd_rn(ep, ew)));
 }
 
+// A pair turned in place: keys exactly, queries with one rounding more.
+__device__ __forceinline__ void turn(float &a, float &b, float c, float s, bool is_q) {
+    const float x = a, y = b;
+    if (is_q) {
+        a = __fmaf_rn(x, c, -__fmul_rn(y, s));
+        b = __fmaf_rn(y, c, __fmul_rn(x, s));
+    } else {
+        a = rotate_exact(x, c, y, -s);
+        b = rotate_exact(y, c, x, s);
+    }
+}
+
 template <typename T>
 __device__ __forceinline__ float rotated(const RopeArgs &a, const T *row, const float *cs, int d) {
     const int R = a.rot_dim / 2;
@@ -43,7 +62,7 @@ __device__ __forceinline__ float rotated(const RopeArgs &a, const T *row, const 
     return rotate_exact(x, cs[i], y, first ? -cs[R + i] : cs[R + i]);
 }
 
-// One CTA per token.
+// Any shape, element by element: one CTA per token.
 template <typename T, bool kQ4>
 __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) {
     grid_dependency_wait();
@@ -83,45 +102,138 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) 
         }
         return;
     }
-    // one warp per (head, group, K or V), a lane per dim
-    const int ng = D / kQ4Group;
+    // rows of 8 or 16 neighbouring lanes, 8 dims a lane
+    const int lanes = D / 8, k = lane % lanes;
     const int64_t blk = slot / a.block_size;
     const int off = (int)(slot - blk * a.block_size);
     const int64_t slab = q4_slab_bytes(a.block_size, D);
-    for (int j = warp; j < 2 * a.num_kv_heads * ng; j += kThreads / 32) {
-        const int is_v = j & 1, g = (j >> 1) % ng, h = (j >> 1) / ng;
-        const int d = g * kQ4Group + lane;
-        const float x = is_v ? to_float(value[(int64_t)h * D + d])
-                             : to_float(from_float<T>(rotated(a, key + (int64_t)h * D, cs, d)));
-        float amax = fabsf(x);
-        const bool finite = __all_sync(0xffffffffu, amax <= 3.402823466e38f);
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const uint16_t sb = q4_scale_bits(amax, finite);
-        uint32_t w = q4_code(x, q4_scale_value(sb)) << (4 * (lane & 7));
-        for (int o = 1; o < 8; o <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
-        uint8_t *s = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) +
-                     (blk * a.num_kv_heads + h) * slab;
+    for (int j0 = warp * (32 / lanes); j0 < 2 * a.num_kv_heads; j0 += (kThreads / 32) * (32 / lanes)) {
+        const int j = j0 + lane / lanes;
+        const bool in = j < 2 * a.num_kv_heads, is_v = in && j >= a.num_kv_heads;
+        const int h = in ? (is_v ? j - a.num_kv_heads : j) : 0;
+        float x[8];
+        for (int i = 0; i < 8; ++i)
+            x[i] = is_v ? to_float(value[(int64_t)h * D + 8 * k + i])
+                        : to_float(from_float<T>(rotated(a, key + (int64_t)h * D, cs, 8 * k + i)));
+        uint8_t *s = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) + (blk * a.num_kv_heads + h) * slab;
         uint8_t *row = s + off * q4_row_bytes(D);
-        if (!is_v) {
-            if ((lane & 7) == 0) *reinterpret_cast<uint32_t *>(row + q4_k_word(d, D)) = w;
-        } else if ((lane & 3) == 0) {
-            *reinterpret_cast<uint16_t *>(row + q4_v_unit(d, D)) = (uint16_t)((lane & 4) ? w >> 16 : w);
-        }
-        if (lane == 0)
-            reinterpret_cast<uint16_t *>(s + a.block_size * q4_row_bytes(D))[off * ng + g] = sb;
+        uint16_t *scales = reinterpret_cast<uint16_t *>(s + a.block_size * q4_row_bytes(D)) + off * (D / kQ4Group);
+        if (D == 128) q4_store8<128>(x, k, is_v, row, scales, in);
+        else q4_store8<64>(x, k, is_v, row, scales, in);
     }
+}
+
+// One CTA per token, `passes` x `rows` head rows of the token at a time, D / 16 threads a row.  Rows 0 ..
+// num_heads - 1 are queries, then keys, then values.  Thread j of a row, j < rot_dim / 16: the rotated vectors 8 j
+// and R + 8 j (halves) or 16 j and 16 j + 8 (interleaved); the others: the vectors from rot_dim on.  4-bit pools:
+// the rotated keys and the values meet in shared memory, where 8 consecutive dims go to a lane.
+template <typename T, bool kQ4>
+__global__ void __launch_bounds__(512) rope_cache_vec_kernel(const RopeArgs a, int rows, int passes) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    T *kv_s = reinterpret_cast<T *>(smem);   // [2 num_kv_heads][D], 4-bit pools only
+    const int D = a.head_dim, lanes = D / 16, tid = threadIdx.x;
+    const int j = tid % lanes, row0 = tid / lanes, R = a.rot_dim / 2;
+    const int H = a.num_heads, HK = a.num_kv_heads, all = H + 2 * HK;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int t = blockIdx.x;
+    const int64_t slot = __ldg(a.slot_mapping + t);
+    const int pos = a.rot_dim > 0 ? __ldg(a.positions + t) : 0;
+    if (slot < 0) return;   // padding token
+    if (slot >= (int64_t)a.num_blocks * a.block_size || pos < 0 || (a.rot_dim > 0 && pos >= a.max_position)) {
+        if (tid == 0) set_status(a.status, PA_ERR_OUT_OF_RANGE);
+        return;
+    }
+    const bool turns = j < R / 8;
+    const int d0 = turns ? (a.interleaved ? 16 * j : 8 * j) : 16 * j;
+    const int d1 = turns && !a.interleaved ? R + 8 * j : d0 + 8;
+    float c[8], s[8];
+    if (turns) {
+        const float *cs = a.cos_sin + (int64_t)pos * a.rot_dim + 8 * j;
+        load8(c, cs);
+        load8(s, cs + R);
+    }
+    for (int pass = 0; pass < passes; ++pass) {
+        const int row = row0 + pass * rows;
+        if (row0 >= rows || row >= all) break;
+        const bool is_q = row < H, is_v = row >= H + HK;
+        const int h = is_q ? row : is_v ? row - H - HK : row - H;
+        const T *src = is_q ? static_cast<const T *>(a.q) + t * a.q_stride
+                            : is_v ? static_cast<const T *>(a.value) + t * a.value_stride
+                                   : static_cast<const T *>(a.key) + t * a.key_stride;
+        src += (int64_t)h * D;
+        float x[8], y[8];
+        load8(x, src + d0);
+        load8(y, src + d1);
+        if (turns && !is_v) {
+            if (a.interleaved) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {   // pair i is (x[2i], x[2i + 1]) or, from 4 on, y's
+                    float &u = i < 4 ? x[2 * i] : y[2 * i - 8], &v = i < 4 ? x[2 * i + 1] : y[2 * i - 7];
+                    turn(u, v, c[i], s[i], is_q);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) turn(x[i], y[i], c[i], s[i], is_q);
+            }
+        }
+        T *dst;
+        if (is_q) dst = static_cast<T *>(a.q_out) + ((int64_t)t * H + h) * D;
+        else if (kQ4) dst = kv_s + (row - H) * D;
+        else dst = static_cast<T *>(is_v ? a.v_cache : a.k_cache) + (slot * HK + h) * D;
+        store8(dst + d0, x);
+        store8(dst + d1, y);
+    }
+    if (!kQ4) return;
+    __syncthreads();
+    const int per = D / 8, k = tid % per;   // a row's lanes lie in one warp: per is 8 or 16
+    const int64_t blk = slot / a.block_size;
+    const int off = (int)(slot - blk * a.block_size);
+    const int64_t slab = q4_slab_bytes(a.block_size, D);
+    for (int r0 = 0; r0 < 2 * HK; r0 += blockDim.x / per) {
+        const int row = r0 + tid / per;
+        const bool in = row < 2 * HK, is_v = in && row >= HK;
+        float x[8];
+        load8(x, kv_s + (in ? row : 0) * D + 8 * k);
+        uint8_t *sl = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) +
+                      (blk * HK + (in ? row - (is_v ? HK : 0) : 0)) * slab;
+        uint8_t *codes = sl + off * q4_row_bytes(D);
+        uint16_t *scales = reinterpret_cast<uint16_t *>(sl + a.block_size * q4_row_bytes(D)) + off * (D / kQ4Group);
+        if (D == 128) q4_store8<128>(x, k, is_v, codes, scales, in);
+        else q4_store8<64>(x, k, is_v, codes, scales, in);
+    }
+}
+
+template <typename T>
+cudaError_t launch_typed(const RopeArgs &a, bool q4, cudaStream_t stream) {
+    // the fast kernel's rows come in 16-byte pieces; a token's keys and values fit shared memory
+    const int64_t kv_bytes = q4 ? (int64_t)2 * a.num_kv_heads * a.head_dim * sizeof(T) : 0;
+    auto in16 = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+    const int64_t e = sizeof(T);
+    bool vec = a.head_dim % 16 == 0 && a.rot_dim % 16 == 0 && a.head_dim <= 512 && kv_bytes <= 48 * 1024 &&
+               a.key_stride * e % 16 == 0 && a.value_stride * e % 16 == 0 && in16(a.key) && in16(a.value) &&
+               in16(a.k_cache) && in16(a.v_cache) && (a.rot_dim == 0 || in16(a.cos_sin));
+    if (a.num_heads > 0) vec = vec && a.q_stride * e % 16 == 0 && in16(a.q) && in16(a.q_out);
+    if (vec) {
+        const int lanes = a.head_dim / 16;
+        const int64_t all = (int64_t)a.num_heads + 2 * a.num_kv_heads;
+        const int64_t passes = (all * lanes + 511) / 512;
+        const int rows = (int)((all + passes - 1) / passes);
+        const dim3 grid(a.num_tokens), block((rows * lanes + 31) / 32 * 32);
+        return q4 ? launch_dependent(rope_cache_vec_kernel<T, true>, grid, block, (size_t)kv_bytes, stream, a, rows,
+                                     (int)passes)
+                  : launch_dependent(rope_cache_vec_kernel<T, false>, grid, block, 0, stream, a, rows, (int)passes);
+    }
+    const dim3 grid(a.num_tokens), block(kThreads);
+    return q4 ? launch_dependent(rope_cache_kernel<T, true>, grid, block, 0, stream, a)
+              : launch_dependent(rope_cache_kernel<T, false>, grid, block, 0, stream, a);
 }
 
 }  // namespace
 
 cudaError_t launch_rope_and_cache(const RopeArgs &a, bool q4, cudaStream_t stream) {
     if (a.num_tokens == 0) return cudaSuccess;
-    const dim3 grid(a.num_tokens), block(kThreads);
-    if (a.dtype == PA_DTYPE_BF16)
-        return q4 ? launch_dependent(rope_cache_kernel<__nv_bfloat16, true>, grid, block, 0, stream, a)
-                  : launch_dependent(rope_cache_kernel<__nv_bfloat16, false>, grid, block, 0, stream, a);
-    return q4 ? launch_dependent(rope_cache_kernel<float, true>, grid, block, 0, stream, a)
-              : launch_dependent(rope_cache_kernel<float, false>, grid, block, 0, stream, a);
+    return a.dtype == PA_DTYPE_BF16 ? launch_typed<__nv_bfloat16>(a, q4, stream) : launch_typed<float>(a, q4, stream);
 }
 
 }  // namespace pa
