@@ -46,6 +46,7 @@
 // in bf16), so that no sum carries a surplus.
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include <cuda_fp16.h>
@@ -904,15 +905,33 @@ template <typename T, int D, int NT>
 cudaError_t launch_typed(Q4Params p, const AttnArgs &a, cudaStream_t stream) {
     using S = Q4Shape<T, D, NT>;
     auto kern = q4_decode_kernel<T, D, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    // the kernel's shared-memory size is an attribute of each device's context: set at the first call there, and
+    // again should a launch fail (a context made anew has forgotten it)
+    static std::atomic<uint64_t> known{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    auto set = [&] {
+        const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (r == cudaSuccess) known.fetch_or(bit);
+        return r;
+    };
+    const bool had = (known.load() & bit) != 0;
+    if (!had && (e = set()) != cudaSuccess) return e;
     p.split = (p.group + S::HW - 1) / S::HW;
     p.hw = (p.group + p.split - 1) / p.split;
     const int grid = min(kMaxCtas, device_sm_count());
     e = launch_dependent(q4_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a.context_lens, a.num_seqs,
                          (int)(a.max_blocks * a.block_size), const_cast<int64_t *>(p.prefix), p.arrivals, a.status);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3(grid), dim3(S::kWarps * 32), S::kSmem, stream, p);
+    e = launch_dependent(kern, dim3(grid), dim3(S::kWarps * 32), S::kSmem, stream, p);
+    if (e == cudaErrorInvalidValue && had) {
+        cudaGetLastError();
+        if ((e = set()) == cudaSuccess)
+            e = launch_dependent(kern, dim3(grid), dim3(S::kWarps * 32), S::kSmem, stream, p);
+    }
+    return e;
 }
 
 }  // namespace

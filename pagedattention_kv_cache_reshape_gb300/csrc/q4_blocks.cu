@@ -17,9 +17,35 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPerThread = 4;   // loads in flight a thread
 
+// (n - 8) s of a word's 8 nibbles, rounded once.  bf16: 0x4300 | n is 128 + n, and the difference and the product
+// of 4 by 8 bits come out of packed bf16 instructions as if rounded from exact.
+__device__ __forceinline__ void expand8(__nv_bfloat16 *dst, uint32_t w, uint16_t scale) {
+    const uint32_t ss = (uint32_t)scale * 0x10001u;
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {   // nibbles i and i + 4
+        uint32_t t;
+        asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xEA;" : "=r"(t) : "r"(w >> (4 * i)), "r"(0x43004300u));
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(t) : "r"(t), "r"(0x43084308u));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(t), "r"(ss));
+    }
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                                                 __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+}
+__device__ __forceinline__ void expand8(float *dst, uint32_t w, uint16_t scale) {
+    const float s = q4_scale_value(scale);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        y[i] = (__uint_as_float(((w >> (4 * i)) & 15u) | 0x4b000000u) - (8388608.0f + 8.0f)) * s;
+    store8(dst, y);
+}
+
 // grid: (pair, part of the block).  Items of a block: [K, V][head][token][8 dims].
 template <typename T, int D, bool kQuantize>
-__global__ void __launch_bounds__(kThreads) q4_convert_kernel(const Q4BlocksArgs a) {
+__global__ void __launch_bounds__(kThreads) q4_convert_kernel(const Q4BlocksArgs a, int log2b) {
+    constexpr int kRow = D / 8, NG = D / kQ4Group;   // threads and groups of a row
+    const int H = a.num_kv_heads, half = (H * kRow) << log2b, slab = q4_slab_bytes(1 << log2b, D);
     grid_dependency_wait();
     grid_dependents_launch();
     const int i = blockIdx.x;
@@ -29,67 +55,45 @@ __global__ void __launch_bounds__(kThreads) q4_convert_kernel(const Q4BlocksArgs
         if (threadIdx.x == 0 && blockIdx.y == 0) set_status(a.status, PA_ERR_OUT_OF_RANGE);
         return;
     }
-    constexpr int kRow = D / 8, NG = D / kQ4Group;   // threads and groups of a row
-    const int B = a.block_size, H = a.num_kv_heads, half = H * B * kRow;
-    const int64_t slab = q4_slab_bytes(B, D);
-    const int64_t wide_blk = (int64_t)(kQuantize ? src : dst) * B * H * D, q4_blk = (kQuantize ? dst : src) * H * slab;
-    const T *wide_k = static_cast<const T *>(kQuantize ? a.src_k : a.dst_k) + wide_blk;
-    const T *wide_v = static_cast<const T *>(kQuantize ? a.src_v : a.dst_v) + wide_blk;
-    const uint8_t *q4_k = static_cast<const uint8_t *>(kQuantize ? a.dst_k : a.src_k) + q4_blk;
-    const uint8_t *q4_v = static_cast<const uint8_t *>(kQuantize ? a.dst_v : a.src_v) + q4_blk;
+    const int64_t wide_blk = (int64_t)(kQuantize ? src : dst) * half * 8;
+    const int64_t q4_blk = (int64_t)(kQuantize ? dst : src) * H * slab;
+    // the thread's place in a row is the same for all its items; half is a multiple of 32 (B * D / 8 is one of
+    // 64), so a warp's items are all of K, all of V or all outside
+    const int k = threadIdx.x % kRow, g = k / 4, r = 2 * (k & 3) + (g & 1);
     const int first = blockIdx.y * kThreads * kPerThread + threadIdx.x;
-    // half is a multiple of 32 (B * D / 8 is one of 64): a warp's items are all of K, all of V or all outside
-    float x[kPerThread][8];
+    Raw8<T> raw[kQuantize ? kPerThread : 1];
     uint32_t w[kPerThread];
     uint16_t sb[kPerThread];
-    auto place = [&](int u, bool &is_v, int &k, int64_t &wide, int64_t &row, int64_t &scale) {
-        int e = first + u * kThreads;
-        const bool in = e < 2 * half;
-        if (!in) e = 0;
-        is_v = e >= half;
-        if (is_v) e -= half;
-        k = e % kRow;
-        const int t = e / kRow, tok = t % B, h = t / B;
-        wide = ((int64_t)tok * H + h) * D + k * 8;
-        row = h * slab + tok * (D / 2);
-        scale = h * slab + B * (D / 2) + tok * (NG * 2);
-        return in;
-    };
 #pragma unroll
     for (int u = 0; u < kPerThread; ++u) {
-        bool is_v;
-        int k;
-        int64_t wide, row, scale;
-        if (!place(u, is_v, k, wide, row, scale)) continue;
+        const int e = first + u * kThreads;
+        if (e >= 2 * half) break;
+        const bool is_v = e >= half;
+        const int t = (is_v ? e - half : e) / kRow, tok = t & ((1 << log2b) - 1), h = t >> log2b;
         if (kQuantize) {
-            load8(x[u], (is_v ? wide_v : wide_k) + wide);
+            raw[kQuantize ? u : 0] = load_raw8(static_cast<const T *>(is_v ? a.src_v : a.src_k) + wide_blk + (tok * H + h) * D + k * 8);
         } else {
-            const uint8_t *p = is_v ? q4_v : q4_k;
-            const int g = k / 4, r = 2 * (k & 3) + (g & 1);
-            w[u] = *reinterpret_cast<const uint32_t *>(p + row + (is_v ? (r * NG + (g & ~1)) * 2 : q4_k_word(8 * k, D)));
-            sb[u] = *reinterpret_cast<const uint16_t *>(p + scale + 2 * g);
+            const uint8_t *p = static_cast<const uint8_t *>(is_v ? a.src_v : a.src_k) + q4_blk + h * slab;
+            w[u] = *reinterpret_cast<const uint32_t *>(p + tok * (D / 2) + (is_v ? (r * NG + (g & ~1)) * 2 : q4_k_word(8 * k, D)));
+            sb[u] = *reinterpret_cast<const uint16_t *>(p + ((D / 2) << log2b) + tok * (NG * 2) + 2 * g);
         }
     }
 #pragma unroll
     for (int u = 0; u < kPerThread; ++u) {
-        bool is_v;
-        int k;
-        int64_t wide, row, scale;
-        if (!place(u, is_v, k, wide, row, scale)) continue;   // whole warps
+        const int e = first + u * kThreads;
+        if (e >= 2 * half) break;
+        const bool is_v = e >= half;
+        const int t = (is_v ? e - half : e) / kRow, tok = t & ((1 << log2b) - 1), h = t >> log2b;
         if (kQuantize) {
-            uint8_t *p = const_cast<uint8_t *>(is_v ? q4_v : q4_k);
-            q4_store8<D>(x[u], k, is_v, p + row, reinterpret_cast<uint16_t *>(p + scale), true);
+            uint8_t *p = static_cast<uint8_t *>(is_v ? a.dst_v : a.dst_k) + q4_blk + h * slab;
+            q4_store8<D>(raw[kQuantize ? u : 0], k, is_v, p + tok * (D / 2),
+                         reinterpret_cast<uint16_t *>(p + ((D / 2) << log2b) + tok * (NG * 2)), true);
         } else {
-            const int g = k / 4;
             if (is_v) {   // (r, g), (r, g + 1) against the neighbour group's (r + 1, g), (r + 1, g + 1)
                 const uint32_t other = __shfl_xor_sync(0xffffffffu, w[u], 4);
                 w[u] = g & 1 ? __byte_perm(other, w[u], 0x7632) : __byte_perm(w[u], other, 0x5410);
             }
-            const float s = q4_scale_value(sb[u]);
-            float y[8];
-#pragma unroll
-            for (int n = 0; n < 8; ++n) y[n] = (float)((int)((w[u] >> (4 * n)) & 15u) - 8) * s;
-            store8(const_cast<T *>(is_v ? wide_v : wide_k) + wide, y);
+            expand8(static_cast<T *>(is_v ? a.dst_v : a.dst_k) + wide_blk + (tok * H + h) * D + k * 8, w[u], sb[u]);
         }
     }
 }
@@ -98,10 +102,11 @@ template <typename T, int D>
 cudaError_t launch_typed(const Q4BlocksArgs &a, bool quantize, cudaStream_t stream) {
     const int64_t items = (int64_t)2 * a.num_kv_heads * a.block_size * (D / 8);
     const int64_t parts = (items + kThreads * kPerThread - 1) / (kThreads * kPerThread);
-    if (parts > 65535) return cudaErrorNotSupported;
+    if (parts > 65535 || items * 8 > INT32_MAX) return cudaErrorNotSupported;
+    const int log2b = a.block_size == 8 ? 3 : a.block_size == 16 ? 4 : 5;
     const dim3 grid(a.num_pairs, (unsigned)parts), block(kThreads);
-    return quantize ? launch_dependent(q4_convert_kernel<T, D, true>, grid, block, 0, stream, a)
-                    : launch_dependent(q4_convert_kernel<T, D, false>, grid, block, 0, stream, a);
+    return quantize ? launch_dependent(q4_convert_kernel<T, D, true>, grid, block, 0, stream, a, log2b)
+                    : launch_dependent(q4_convert_kernel<T, D, false>, grid, block, 0, stream, a, log2b);
 }
 
 }  // namespace

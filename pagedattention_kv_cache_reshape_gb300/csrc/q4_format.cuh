@@ -81,20 +81,41 @@ __device__ __forceinline__ uint32_t q4_word(const float (&x)[8], float s) {
     return w;
 }
 
-// 8 consecutive values of a row in registers, from 16-byte aligned memory.
-__device__ __forceinline__ void load8(float (&x)[8], const __nv_bfloat16 *p) {
-    const uint4 v = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// 8 consecutive values of a row as they lie in memory (16-byte aligned), and as fp32.
+template <typename T> struct Raw8 { uint4 v[sizeof(T) / 2]; };
+template <typename T> __device__ __forceinline__ Raw8<T> load_raw8(const T *p) {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = *(reinterpret_cast<const uint4 *>(p) + i);
+    return r;
+}
+__device__ __forceinline__ void to_floats(float (&x)[8], const Raw8<__nv_bfloat16> &r) {
+    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         x[2 * i] = __uint_as_float(w[i] << 16);
         x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
 }
-__device__ __forceinline__ void load8(float (&x)[8], const float *p) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *(reinterpret_cast<const float4 *>(p) + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+__device__ __forceinline__ void to_floats(float (&x)[8], const Raw8<float> &r) {
+    const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+}
+// Bits of the largest magnitude of 8 values, as fp32.
+__device__ __forceinline__ uint32_t amax_bits8(const Raw8<__nv_bfloat16> &r) {
+    const uint32_t m = 0x7fff7fffu;
+    const uint32_t t = __vmaxu2(__vmaxu2(r.v[0].x & m, r.v[0].y & m), __vmaxu2(r.v[0].z & m, r.v[0].w & m));
+    return max(t << 16, t & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t amax_bits8(const Raw8<float> &r) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint4 v = r.v[i];
+        a = max(a, max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu)));
+    }
+    return a;
 }
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
     uint32_t w[4];
@@ -114,16 +135,16 @@ __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
 // by whole warps in which the D / 8 lanes of a row are neighbours in order of
 // k, a row's first lane a multiple of D / 8.  `row` is the row's code bytes and
 // `scales` its scales; lanes with store = false only take part in the shuffles.
-template <int D>
-__device__ __forceinline__ void q4_store8(const float (&x)[8], int k, bool is_v, uint8_t *row, uint16_t *scales,
+template <int D, typename T>
+__device__ __forceinline__ void q4_store8(const Raw8<T> &raw, int k, bool is_v, uint8_t *row, uint16_t *scales,
                                           bool store) {
     constexpr int NG = D / kQ4Group;
-    uint32_t amax = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
+    uint32_t amax = amax_bits8(raw);
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const uint16_t sb = q4_scale_bits(amax);
+    float x[8];
+    to_floats(x, raw);
     const uint32_t w = q4_word(x, q4_scale_value(sb));
     // V: a lane holds units r = 2 (k % 4) and r + 1 of group g; with its neighbour group's lane it makes the 4
     // bytes (r, g), (r, g + 1) or (r + 1, g - 1), (r + 1, g)

@@ -111,10 +111,10 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) 
         const int j = j0 + lane / lanes;
         const bool in = j < 2 * a.num_kv_heads, is_v = in && j >= a.num_kv_heads;
         const int h = in ? (is_v ? j - a.num_kv_heads : j) : 0;
-        float x[8];
+        Raw8<T> x;
         for (int i = 0; i < 8; ++i)
-            x[i] = is_v ? to_float(value[(int64_t)h * D + 8 * k + i])
-                        : to_float(from_float<T>(rotated(a, key + (int64_t)h * D, cs, 8 * k + i)));
+            reinterpret_cast<T *>(&x)[i] = is_v ? value[(int64_t)h * D + 8 * k + i]
+                                                : from_float<T>(rotated(a, key + (int64_t)h * D, cs, 8 * k + i));
         uint8_t *s = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) + (blk * a.num_kv_heads + h) * slab;
         uint8_t *row = s + off * q4_row_bytes(D);
         uint16_t *scales = reinterpret_cast<uint16_t *>(s + a.block_size * q4_row_bytes(D)) + off * (D / kQ4Group);
@@ -123,85 +123,131 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) 
     }
 }
 
-// One CTA per token, `passes` x `rows` head rows of the token at a time, D / 16 threads a row.  Rows 0 ..
+// One CTA per U tokens, `passes` x `rows` head rows of a token at a time, D / 16 threads a row.  Rows 0 ..
 // num_heads - 1 are queries, then keys, then values.  Thread j of a row, j < rot_dim / 16: the rotated vectors 8 j
-// and R + 8 j (halves) or 16 j and 16 j + 8 (interleaved); the others: the vectors from rot_dim on.  4-bit pools:
-// the rotated keys and the values meet in shared memory, where 8 consecutive dims go to a lane.
-template <typename T, bool kQ4>
+// and R + 8 j (halves) or 16 j and 16 j + 8 (interleaved); the others: the vectors from rot_dim on.  The rows are
+// requested before the slots and positions that decide what becomes of them.  4-bit pools: the rotated keys and
+// the values meet in shared memory, where 8 consecutive dims go to a lane.
+template <typename T, bool kQ4, int U>
 __global__ void __launch_bounds__(512) rope_cache_vec_kernel(const RopeArgs a, int rows, int passes) {
     extern __shared__ __align__(16) uint8_t smem[];
-    T *kv_s = reinterpret_cast<T *>(smem);   // [2 num_kv_heads][D], 4-bit pools only
+    T *kv_s = reinterpret_cast<T *>(smem);   // [U][2 num_kv_heads][D], 4-bit pools only
     const int D = a.head_dim, lanes = D / 16, tid = threadIdx.x;
-    const int j = tid % lanes, row0 = tid / lanes, R = a.rot_dim / 2;
+    const int row0 = tid / lanes, j = tid - row0 * lanes, R = a.rot_dim / 2;
     const int H = a.num_heads, HK = a.num_kv_heads, all = H + 2 * HK;
-    grid_dependency_wait();
-    grid_dependents_launch();
-    const int t = blockIdx.x;
-    const int64_t slot = __ldg(a.slot_mapping + t);
-    const int pos = a.rot_dim > 0 ? __ldg(a.positions + t) : 0;
-    if (slot < 0) return;   // padding token
-    if (slot >= (int64_t)a.num_blocks * a.block_size || pos < 0 || (a.rot_dim > 0 && pos >= a.max_position)) {
-        if (tid == 0) set_status(a.status, PA_ERR_OUT_OF_RANGE);
-        return;
-    }
     const bool turns = j < R / 8;
     const int d0 = turns ? (a.interleaved ? 16 * j : 8 * j) : 16 * j;
     const int d1 = turns && !a.interleaved ? R + 8 * j : d0 + 8;
-    float c[8], s[8];
-    if (turns) {
-        const float *cs = a.cos_sin + (int64_t)pos * a.rot_dim + 8 * j;
-        load8(c, cs);
-        load8(s, cs + R);
-    }
+    const int t0 = blockIdx.x * U;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    int64_t slot[U];
+    int pos[U];
+    bool live[U];
     for (int pass = 0; pass < passes; ++pass) {
         const int row = row0 + pass * rows;
-        if (row0 >= rows || row >= all) break;
+        const bool mine = row0 < rows && row < all;
         const bool is_q = row < H, is_v = row >= H + HK;
         const int h = is_q ? row : is_v ? row - H - HK : row - H;
-        const T *src = is_q ? static_cast<const T *>(a.q) + t * a.q_stride
-                            : is_v ? static_cast<const T *>(a.value) + t * a.value_stride
-                                   : static_cast<const T *>(a.key) + t * a.key_stride;
-        src += (int64_t)h * D;
-        float x[8], y[8];
-        load8(x, src + d0);
-        load8(y, src + d1);
-        if (turns && !is_v) {
-            if (a.interleaved) {
+        const T *base = static_cast<const T *>(is_q ? a.q : is_v ? a.value : a.key) + (int64_t)h * D;
+        const int64_t stride = is_q ? a.q_stride : is_v ? a.value_stride : a.key_stride;
+        Raw8<T> rx[U], ry[U];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {   // pair i is (x[2i], x[2i + 1]) or, from 4 on, y's
-                    float &u = i < 4 ? x[2 * i] : y[2 * i - 8], &v = i < 4 ? x[2 * i + 1] : y[2 * i - 7];
-                    turn(u, v, c[i], s[i], is_q);
+        for (int u = 0; u < U; ++u)
+            if (mine && t0 + u < a.num_tokens) {
+                rx[u] = load_raw8(base + (t0 + u) * stride + d0);
+                ry[u] = load_raw8(base + (t0 + u) * stride + d1);
+            }
+        if (pass == 0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool in = t0 + u < a.num_tokens;
+                slot[u] = in ? __ldg(a.slot_mapping + t0 + u) : -1;
+                pos[u] = in && a.rot_dim > 0 ? __ldg(a.positions + t0 + u) : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                live[u] = slot[u] >= 0;   // else padding
+                if (live[u] && (slot[u] >= (int64_t)a.num_blocks * a.block_size || pos[u] < 0 ||
+                                (a.rot_dim > 0 && pos[u] >= a.max_position))) {
+                    live[u] = false;
+                    if (tid == 0) set_status(a.status, PA_ERR_OUT_OF_RANGE);
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) turn(x[i], y[i], c[i], s[i], is_q);
             }
         }
-        T *dst;
-        if (is_q) dst = static_cast<T *>(a.q_out) + ((int64_t)t * H + h) * D;
-        else if (kQ4) dst = kv_s + (row - H) * D;
-        else dst = static_cast<T *>(is_v ? a.v_cache : a.k_cache) + (slot * HK + h) * D;
-        store8(dst + d0, x);
-        store8(dst + d1, y);
+        if (!mine) continue;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!live[u]) continue;
+            T *dst;
+            if (is_q) dst = static_cast<T *>(a.q_out) + ((int64_t)(t0 + u) * H + h) * D;
+            else if (kQ4) dst = kv_s + (u * 2 * HK + row - H) * D;
+            else dst = static_cast<T *>(is_v ? a.v_cache : a.k_cache) + (slot[u] * HK + h) * D;
+            if (turns && !is_v) {
+                float c[8], s[8], x[8], y[8];
+                const float *cs = a.cos_sin + (int64_t)pos[u] * a.rot_dim + 8 * j;
+                to_floats(c, load_raw8(cs));
+                to_floats(s, load_raw8(cs + R));
+                to_floats(x, rx[u]);
+                to_floats(y, ry[u]);
+                if (a.interleaved) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {   // pair i is (x[2i], x[2i + 1]) or, from 4 on, y's
+                        float &v = i < 4 ? x[2 * i] : y[2 * i - 8], &w = i < 4 ? x[2 * i + 1] : y[2 * i - 7];
+                        turn(v, w, c[i], s[i], is_q);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) turn(x[i], y[i], c[i], s[i], is_q);
+                }
+                store8(dst + d0, x);
+                store8(dst + d1, y);
+            } else {
+#pragma unroll
+                for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+                    *(reinterpret_cast<uint4 *>(dst + d0) + i) = rx[u].v[i];
+                    *(reinterpret_cast<uint4 *>(dst + d1) + i) = ry[u].v[i];
+                }
+            }
+        }
     }
     if (!kQ4) return;
     __syncthreads();
     const int per = D / 8, k = tid % per;   // a row's lanes lie in one warp: per is 8 or 16
-    const int64_t blk = slot / a.block_size;
-    const int off = (int)(slot - blk * a.block_size);
     const int64_t slab = q4_slab_bytes(a.block_size, D);
-    for (int r0 = 0; r0 < 2 * HK; r0 += blockDim.x / per) {
-        const int row = r0 + tid / per;
-        const bool in = row < 2 * HK, is_v = in && row >= HK;
-        float x[8];
-        load8(x, kv_s + (in ? row : 0) * D + 8 * k);
-        uint8_t *sl = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) +
-                      (blk * HK + (in ? row - (is_v ? HK : 0) : 0)) * slab;
-        uint8_t *codes = sl + off * q4_row_bytes(D);
-        uint16_t *scales = reinterpret_cast<uint16_t *>(sl + a.block_size * q4_row_bytes(D)) + off * (D / kQ4Group);
-        if (D == 128) q4_store8<128>(x, k, is_v, codes, scales, in);
-        else q4_store8<64>(x, k, is_v, codes, scales, in);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (!live[u]) continue;             // the same in every thread
+        const int64_t blk = slot[u] / a.block_size;
+        const int off = (int)(slot[u] - blk * a.block_size);
+        for (int r0 = 0; r0 < 2 * HK; r0 += blockDim.x / per) {
+            if (r0 + (tid & ~31) / per >= 2 * HK) break;   // whole warps
+            const int row = r0 + tid / per;
+            const bool in = row < 2 * HK, is_v = in && row >= HK;
+            const Raw8<T> x = load_raw8(kv_s + (u * 2 * HK + (in ? row : 0)) * D + 8 * k);
+            uint8_t *sl = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) +
+                          (blk * HK + (in ? row - (is_v ? HK : 0) : 0)) * slab;
+            uint8_t *codes = sl + off * q4_row_bytes(D);
+            uint16_t *scales = reinterpret_cast<uint16_t *>(sl + a.block_size * q4_row_bytes(D)) + off * (D / kQ4Group);
+            if (D == 128) q4_store8<128>(x, k, is_v, codes, scales, in);
+            else q4_store8<64>(x, k, is_v, codes, scales, in);
+        }
     }
+}
+
+template <typename T, bool kQ4>
+cudaError_t launch_vec(const RopeArgs &a, int64_t kv_bytes, cudaStream_t stream) {
+    const int lanes = a.head_dim / 16;
+    const int64_t all = (int64_t)a.num_heads + 2 * a.num_kv_heads;
+    const int64_t passes = (all * lanes + 511) / 512;
+    const int rows = (int)((all + passes - 1) / passes);
+    const dim3 block((rows * lanes + 31) / 32 * 32);
+    // two tokens a CTA once one each would fill the GPU several times over: twice the loads in flight
+    if (a.num_tokens >= 8 * device_sm_count() && 2 * kv_bytes <= 48 * 1024)
+        return launch_dependent(rope_cache_vec_kernel<T, kQ4, 2>, dim3((a.num_tokens + 1) / 2), block,
+                                (size_t)(2 * kv_bytes), stream, a, rows, (int)passes);
+    return launch_dependent(rope_cache_vec_kernel<T, kQ4, 1>, dim3(a.num_tokens), block, (size_t)kv_bytes, stream, a,
+                            rows, (int)passes);
 }
 
 template <typename T>
@@ -214,16 +260,7 @@ cudaError_t launch_typed(const RopeArgs &a, bool q4, cudaStream_t stream) {
                a.key_stride * e % 16 == 0 && a.value_stride * e % 16 == 0 && in16(a.key) && in16(a.value) &&
                in16(a.k_cache) && in16(a.v_cache) && (a.rot_dim == 0 || in16(a.cos_sin));
     if (a.num_heads > 0) vec = vec && a.q_stride * e % 16 == 0 && in16(a.q) && in16(a.q_out);
-    if (vec) {
-        const int lanes = a.head_dim / 16;
-        const int64_t all = (int64_t)a.num_heads + 2 * a.num_kv_heads;
-        const int64_t passes = (all * lanes + 511) / 512;
-        const int rows = (int)((all + passes - 1) / passes);
-        const dim3 grid(a.num_tokens), block((rows * lanes + 31) / 32 * 32);
-        return q4 ? launch_dependent(rope_cache_vec_kernel<T, true>, grid, block, (size_t)kv_bytes, stream, a, rows,
-                                     (int)passes)
-                  : launch_dependent(rope_cache_vec_kernel<T, false>, grid, block, 0, stream, a, rows, (int)passes);
-    }
+    if (vec) return q4 ? launch_vec<T, true>(a, kv_bytes, stream) : launch_vec<T, false>(a, kv_bytes, stream);
     const dim3 grid(a.num_tokens), block(kThreads);
     return q4 ? launch_dependent(rope_cache_kernel<T, true>, grid, block, 0, stream, a)
               : launch_dependent(rope_cache_kernel<T, false>, grid, block, 0, stream, a);

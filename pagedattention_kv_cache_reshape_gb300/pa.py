@@ -150,8 +150,8 @@ def _check(rc: int, what: str) -> None:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:   # the current stream's handle, without a torch.cuda.Stream made on the way
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -366,24 +366,38 @@ def varlen_step(q, key, value, k_cache, v_cache, cu_seqlens_q, block_tables, con
     return slot_mapping, out
 
 
-def _rows(t, name: str, tokens: int, heads: int, d: int, dtype) -> None:
-    if t.dim() != 3 or t.shape != (tokens, heads, d) or t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+_CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _refuse(dev: int, *specs):
+    """Raises what is wrong with the first wrong tensor of (tensor, name, dtype or None); the calls below come here
+    only when their one combined check fails.  Launches go to the current device's stream, so a tensor of another
+    device is refused, not reached across."""
+    for t, name, dtype in specs:
+        if t is None:
+            continue
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on the current device cuda:{dev}, got {t.device}")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _rows(t, name: str, tokens: int, heads: int, d: int, dtype, dev: int) -> int:
+    """Checks a token-strided view [tokens, heads, d]; returns its token stride."""
+    if t.shape != (tokens, heads, d):
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {d}] with contiguous rows")
+    st, sh, sd = t.stride()
+    if tokens and ((sd != 1 and d > 1) or (sh != d and heads > 1)):
         raise ValueError(f"{name} must be [{tokens}, {heads}, {d}] with contiguous rows")
     if t.dtype != dtype:
         raise TypeError("q, key, value and the 16/32-bit pools must share one dtype")
-
-
-def _current(*tensors) -> None:
-    # launches go to the current device's stream: a tensor of another device is refused, not reached across
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != dev:
-            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
-
-
-def _tok_stride(t) -> int:
-    # one token: any stride will do, and torch may report one shorter than a row
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor on the current device cuda:{dev}, got {t.device}")
+    return st if tokens > 1 else heads * d   # torch may report any stride for one token
 
 
 def _q4_pool_shape(k_cache, v_cache, head_dim: int):
@@ -397,33 +411,48 @@ def _q4_pool_shape(k_cache, v_cache, head_dim: int):
     return num_blocks, slab // row, hkv
 
 
-def _rope(fn, q, key, value, cos_sin, positions, pools, num_blocks, block_size, slot_mapping, interleaved, q_out,
-          dev_status, stream):
+def _rope(fn, q, key, value, cos_sin, positions, k_cache, v_cache, pool_dtype, num_blocks, block_size, slot_mapping,
+          interleaved, q_out, dev_status, stream):
     n, hkv, d = key.shape
-    _rows(key, "key", n, hkv, d, key.dtype)
-    _rows(value, "value", n, hkv, d, key.dtype)
-    heads = 0
+    dtype, dev = key.dtype, torch.cuda.current_device()
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    ks, vs = _rows(key, "key", n, hkv, d, dtype, dev), _rows(value, "value", n, hkv, d, dtype, dev)
+    heads = qs = q_ptr = out_ptr = 0
     if q is not None:
         heads = q.shape[1] if q.dim() == 3 else 0
-        _rows(q, "q", n, heads, d, key.dtype)
+        qs = _rows(q, "q", n, heads, d, dtype, dev)
         if q_out is None:
-            q_out = torch.empty((n, heads, d), dtype=q.dtype, device=q.device)
-        _rows(q_out, "q_out", n, heads, d, key.dtype)
-        _contig(q_out, "q_out")
-    if slot_mapping.numel() < n or (cos_sin is not None and positions.numel() < n):
-        raise ValueError("slot_mapping and positions must have an entry per token")
-    _current(q, q_out, key, value, cos_sin, positions, slot_mapping, *pools)
-    rot = max_pos = 0
+            q_out = torch.empty((n, heads, d), dtype=dtype, device=q.device)
+        else:
+            _rows(q_out, "q_out", n, heads, d, dtype, dev)
+        if not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous")
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous() and slot_mapping.is_contiguous()
+            and k_cache.get_device() == v_cache.get_device() == slot_mapping.get_device() == dev
+            and k_cache.dtype == v_cache.dtype == pool_dtype and slot_mapping.dtype == torch.int64):
+        _refuse(dev, (k_cache, "k_cache", pool_dtype), (v_cache, "v_cache", pool_dtype),
+                (slot_mapping, "slot_mapping", torch.int64))
+    rot = max_pos = table_ptr = pos_ptr = 0
     if cos_sin is not None:
         max_pos, rot = cos_sin.shape
-    rc = getattr(load(), fn)(
-        None if q is None else _dev(q_out, "q_out"), None if q is None else _dev(q, "q"), _dev(key, "key"),
-        _dev(value, "value"), 0 if q is None else _tok_stride(q), _tok_stride(key), _tok_stride(value),
-        None if cos_sin is None else _contig(cos_sin, "cos_sin", torch.float32),
-        None if cos_sin is None else _contig(positions, "positions", torch.int32), max_pos, rot,
-        1 if interleaved else 0, pools[0].data_ptr(), pools[1].data_ptr(), _contig(slot_mapping, "slot_mapping", torch.int64), n, heads,
-        hkv, d, block_size, num_blocks, _dtype_code(key), _opt(dev_status), _stream(stream))
-    _check(rc, fn)
+        if not (cos_sin.is_contiguous() and positions.is_contiguous()
+                and cos_sin.get_device() == positions.get_device() == dev
+                and cos_sin.dtype == torch.float32 and positions.dtype == torch.int32):
+            _refuse(dev, (cos_sin, "cos_sin", torch.float32), (positions, "positions", torch.int32))
+        if positions.numel() < n:
+            raise ValueError("positions must have an entry per token")
+        table_ptr, pos_ptr = cos_sin.data_ptr(), positions.data_ptr()
+    if slot_mapping.numel() < n:
+        raise ValueError("slot_mapping must have an entry per token")
+    rc = getattr(_lib or load(), fn)(
+        out_ptr, q_ptr, key.data_ptr(), value.data_ptr(), qs, ks, vs, table_ptr, pos_ptr, max_pos, rot,
+        1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), n, heads, hkv, d,
+        block_size, num_blocks, code, 0 if dev_status is None else _opt(dev_status), _stream(stream))
+    if rc != OK:
+        raise PAError(rc, fn)
     return q_out
 
 
@@ -437,9 +466,8 @@ def rope_and_cache(q, key, value, cos_sin, positions, k_cache, v_cache, slot_map
         raise ValueError("key, value and the pools disagree on heads or head_dim")
     if not (key.dtype == k_cache.dtype == v_cache.dtype):
         raise TypeError("q, key, value and the 16/32-bit pools must share one dtype")
-    _contig(k_cache, "k_cache"), _contig(v_cache, "v_cache")
-    return _rope("pa_rope_and_cache", q, key, value, cos_sin, positions, (k_cache, v_cache), num_blocks, block_size,
-                 slot_mapping, interleaved, q_out, dev_status, stream)
+    return _rope("pa_rope_and_cache", q, key, value, cos_sin, positions, k_cache, v_cache, key.dtype, num_blocks,
+                 block_size, slot_mapping, interleaved, q_out, dev_status, stream)
 
 
 def q4_block_bytes(block_size: int, num_kv_heads: int, head_dim: int) -> int:
@@ -455,27 +483,38 @@ def rope_and_cache_q4(q, key, value, cos_sin, positions, k_cache, v_cache, slot_
     num_blocks, block_size, hkv = _q4_pool_shape(k_cache, v_cache, key.shape[2])
     if key.shape[1] != hkv:
         raise ValueError("key and the pools disagree on num_kv_heads")
-    _contig(k_cache, "k_cache", torch.uint8), _contig(v_cache, "v_cache", torch.uint8)
-    return _rope("pa_rope_and_cache_q4", q, key, value, cos_sin, positions, (k_cache, v_cache), num_blocks, block_size,
-                 slot_mapping, interleaved, q_out, dev_status, stream)
+    return _rope("pa_rope_and_cache_q4", q, key, value, cos_sin, positions, k_cache, v_cache, torch.uint8, num_blocks,
+                 block_size, slot_mapping, interleaved, q_out, dev_status, stream)
 
 
 def _q4_blocks(fn, wide_k, wide_v, q4_k, q4_v, quantize, pairs, dev_status, stream):
     num_wide, block_size, hkv, d = wide_k.shape
     num_q4, b4, h4 = _q4_pool_shape(q4_k, q4_v, d)
-    if wide_k.shape != wide_v.shape or (b4, h4) != (block_size, hkv):
+    if wide_k.shape != wide_v.shape or b4 != block_size or h4 != hkv:
         raise ValueError("the 16/32-bit and 4-bit pools must share block size, heads and head_dim")
-    if wide_k.dtype != wide_v.dtype:
+    dtype, dev = wide_k.dtype, torch.cuda.current_device()
+    if wide_v.dtype != dtype:
         raise TypeError("the 16/32-bit pools must share one dtype")
-    wide = (_contig(wide_k, "16/32-bit pool"), _contig(wide_v, "16/32-bit pool"))
-    q4 = (_contig(q4_k, "4-bit pool", torch.uint8), _contig(q4_v, "4-bit pool", torch.uint8))
-    pairs = pairs.reshape(-1, 2)
-    _current(wide_k, wide_v, q4_k, q4_v, pairs)
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    if not (wide_k.is_contiguous() and wide_v.is_contiguous() and q4_k.is_contiguous() and q4_v.is_contiguous()
+            and pairs.is_contiguous() and pairs.dtype == torch.int32 and q4_k.dtype == q4_v.dtype == torch.uint8
+            and wide_k.get_device() == wide_v.get_device() == q4_k.get_device() == q4_v.get_device()
+            == pairs.get_device() == dev):
+        _refuse(dev, (wide_k, "16/32-bit pool", None), (wide_v, "16/32-bit pool", None),
+                (q4_k, "4-bit pool", torch.uint8), (q4_v, "4-bit pool", torch.uint8), (pairs, "pairs", torch.int32))
+    n = pairs.numel()
+    if n % 2:
+        raise ValueError("pairs must be [n, 2]")
+    wide, q4 = (wide_k.data_ptr(), wide_v.data_ptr()), (q4_k.data_ptr(), q4_v.data_ptr())
     src, dst = (wide, q4) if quantize else (q4, wide)
     n_src, n_dst = (num_wide, num_q4) if quantize else (num_q4, num_wide)
-    rc = getattr(load(), fn)(*src, *dst, block_size, hkv, d, n_src, n_dst, _contig(pairs, "pairs", torch.int32),
-                             int(pairs.shape[0]), _dtype_code(wide_k), _opt(dev_status), _stream(stream))
-    _check(rc, fn)
+    rc = getattr(_lib or load(), fn)(src[0], src[1], dst[0], dst[1], block_size, hkv, d, n_src, n_dst,
+                                     pairs.data_ptr(), n // 2, code, 0 if dev_status is None else _opt(dev_status),
+                                     _stream(stream))
+    if rc != OK:
+        raise PAError(rc, fn)
 
 
 def quantize_blocks_q4(src_k, src_v, dst_k, dst_v, pairs, dev_status=None, stream=None):
@@ -498,23 +537,34 @@ def decode_q4(q, k_cache, v_cache, block_tables, context_lens, scale: float, out
     """pa_decode_q4: q [num_seqs, H, D] over 4-bit pools -> out [num_seqs, H, D]."""
     num_seqs, H, D = q.shape
     num_blocks, block_size, hkv = _q4_pool_shape(k_cache, v_cache, D)
-    if block_tables.shape[0] != num_seqs or context_lens.numel() != num_seqs:
+    n, max_blocks = block_tables.shape
+    if n != num_seqs or context_lens.numel() != num_seqs:
         raise ValueError("block_tables and context_lens must have a row per sequence")
-    max_blocks = block_tables.shape[1]
+    dtype, dev = q.dtype, torch.cuda.current_device()
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
     if out is None:
         out = torch.empty_like(q)
-    elif out.shape != q.shape or out.dtype != q.dtype:
+    elif out.shape != q.shape or out.dtype != dtype:
         raise ValueError("out must have q's shape and dtype")
-    _current(q, out, k_cache, v_cache, block_tables, context_lens, workspace)
     if workspace is None:
         workspace = _ws(None, decode_q4_workspace_size(num_seqs, H, hkv, D, block_size, max_blocks), q.device)
-    rc = load().pa_decode_q4(
-        _contig(out, "out"), _contig(q, "q"), _contig(k_cache, "k_cache", torch.uint8),
-        _contig(v_cache, "v_cache", torch.uint8), _contig(block_tables, "block_tables", torch.int32),
-        _contig(context_lens, "context_lens", torch.int32), num_seqs, H, hkv, D, block_size, max_blocks, num_blocks,
-        float(scale), _dtype_code(q), _contig(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-        _opt(dev_status), _stream(stream))
-    _check(rc, "pa_decode_q4")
+    if not (q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and block_tables.is_contiguous() and context_lens.is_contiguous() and workspace.is_contiguous()
+            and k_cache.dtype == v_cache.dtype == torch.uint8
+            and block_tables.dtype == context_lens.dtype == torch.int32
+            and q.get_device() == out.get_device() == k_cache.get_device() == v_cache.get_device()
+            == block_tables.get_device() == context_lens.get_device() == workspace.get_device() == dev):
+        _refuse(dev, (q, "q", None), (out, "out", None), (k_cache, "k_cache", torch.uint8),
+                (v_cache, "v_cache", torch.uint8), (block_tables, "block_tables", torch.int32),
+                (context_lens, "context_lens", torch.int32), (workspace, "workspace", None))
+    rc = (_lib or load()).pa_decode_q4(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), num_seqs, H, hkv, D, block_size, max_blocks, num_blocks, scale, code,
+        workspace.data_ptr(), workspace.nbytes, 0 if dev_status is None else _opt(dev_status), _stream(stream))
+    if rc != OK:
+        raise PAError(rc, "pa_decode_q4")
     return out
 
 
