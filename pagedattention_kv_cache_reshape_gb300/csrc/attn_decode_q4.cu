@@ -38,8 +38,12 @@
 // units (queries, first block ids, normalising or leaving a piece) counts as
 // kHeadCost units of the stream in front of it.  A (sequence, kv-head) inside one warp is normalised and
 // stored; cut ones leave (m, l, o) pieces, merged first between the warps of a
-// CTA (shared memory), then by the last arriving CTA (workspace), always in
-// stream order, so results do not depend on timing.
+// CTA (shared memory), then, where a CTA boundary cuts a head, by a second
+// small kernel (workspace), always in stream order, so results do not depend
+// on timing.  Every CTA finds its share by itself, from a prefix sum over the
+// lengths in shared memory; only batches of more than kScanSeqs sequences
+// have it made by a kernel of its own.  A batch of few heads over short tables
+// takes a CTA a head and needs neither.
 //
 // fp32 queries: q and the weights are split into three bf16 parts each (24
 // bits), and the codes are brought to n - 8 one by one (0x4300 | n is 128 + n
@@ -62,17 +66,24 @@ constexpr int kU = 16;              // tokens a unit: the M of the first product
 constexpr int kStages = 4;
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxCtas = 512;
-constexpr int kHeadCost = 2;
+constexpr int kScanSeqs = 4096;     // sequences whose prefix a CTA makes itself (48 KB of shared memory)
+constexpr int kHeadUnits = 128;     // a CTA a head: up to this many units
+constexpr int kHeadCost = 5;
 constexpr float kMoveAt = 8.0f;     // a logit this far (base 2) over the reference moves it
+
+// A head cut at the end of CTA c (seq < 0: none): its pieces are c's second, then the first of c + 1 .. last.
+struct Cut { int seq, vh, last, pad; };
 
 struct Q4Params {
     const void *q;
     void *out;
     const uint8_t *k, *v;
     const int32_t *block_tables, *context_lens;
-    const int64_t *prefix;     // [num_seqs + 1] stream length of one head before each sequence
-    int32_t *arrivals;         // [kMaxCtas] pieces of the sequence cut at a CTA's end, zeroed by the plan
+    int64_t *prefix;           // [num_seqs + 1] stream length of one head before each sequence (not `scan`)
+    struct Cut *cuts;          // [CTAs] the head cut at each CTA's end
     float *part;               // [CTAs][2][heads][D + 2]
+    int scan;                  // the CTAs make the prefix themselves
+    int by_head;               // CTA i takes head i
     int num_seqs, num_heads, num_kv_heads;
     int group;                 // q-heads per kv-head
     int split;                 // parts a group is split into
@@ -91,24 +102,21 @@ __device__ __forceinline__ int units_of(int ctx, int max_tokens) {
 // A head of a sequence in the stream: its units and what it costs beside them.
 __device__ __forceinline__ int length_of(int nu) { return nu ? nu + kHeadCost : 0; }
 
-// Exclusive prefix of the sequences' stream lengths, and the arrival counters' zeros.
-__global__ void __launch_bounds__(kPlanThreads)
-    q4_plan_kernel(const int32_t *__restrict__ context_lens, int num_seqs, int max_tokens,
-                   int64_t *__restrict__ prefix, int32_t *__restrict__ arrivals, int32_t *status) {
-    __shared__ int64_t warp_tot[kPlanThreads / 32];
+// Exclusive prefix of the sequences' stream lengths, by a CTA of kT threads.  `ctxs`, if set, receives the lengths.
+template <int kT>
+__device__ __forceinline__ void prefix_of(const int32_t *__restrict__ context_lens, int num_seqs, int max_tokens,
+                                          int64_t *prefix, int32_t *ctxs, int64_t *warp_tot, int32_t *status) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    grid_dependency_wait();
-    grid_dependents_launch();
-    if (tid < kMaxCtas) arrivals[tid] = 0;
     int64_t running = 0;
-    for (int base = 0; base < num_seqs; base += kPlanThreads) {
+    for (int base = 0; base < num_seqs; base += kT) {
         const int s = base + tid;
-        int nu = 0;
+        int len = 0;
         if (s < num_seqs) {
-            nu = units_of(__ldg(context_lens + s), max_tokens);
-            if (nu == 0) set_status(status, PA_ERR_OUT_OF_RANGE);
+            const int ctx = __ldg(context_lens + s);
+            len = length_of(units_of(ctx, max_tokens));
+            if (len == 0) set_status(status, PA_ERR_OUT_OF_RANGE);
+            if (ctxs) ctxs[s] = ctx;
         }
-        const int len = length_of(nu);
         int64_t incl = len;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -117,21 +125,27 @@ __global__ void __launch_bounds__(kPlanThreads)
         }
         if (lane == 31) warp_tot[warp] = incl;
         __syncthreads();
-        if (warp == 0) {
-            int64_t t = warp_tot[lane];
+        int64_t before = 0, all = 0;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, t, off);
-                if (lane >= off) t += y;
-            }
-            warp_tot[lane] = t;
+        for (int w = 0; w < kT / 32; ++w) {
+            const int64_t t = warp_tot[w];
+            before += w < warp ? t : 0;
+            all += t;
         }
-        __syncthreads();
-        if (s < num_seqs) prefix[s] = running + (warp ? warp_tot[warp - 1] : 0) + incl - len;
-        running += warp_tot[kPlanThreads / 32 - 1];
+        if (s < num_seqs) prefix[s] = running + before + incl - len;
+        running += all;
         __syncthreads();
     }
     if (tid == 0) prefix[num_seqs] = running;
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+    q4_plan_kernel(const int32_t *__restrict__ context_lens, int num_seqs, int max_tokens, int64_t *prefix,
+                   int32_t *status) {
+    __shared__ int64_t warp_tot[kPlanThreads / 32];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    prefix_of<kPlanThreads>(context_lens, num_seqs, max_tokens, prefix, nullptr, warp_tot, status);
 }
 
 __device__ __forceinline__ uint32_t nibbles_128(uint32_t w) {   // 128 + nibble 0 | 128 + nibble 4 << 16, bf16
@@ -226,6 +240,8 @@ struct Q4Shape {
     static constexpr int kRing = kStages * kStage;
     static constexpr int kPiece = HW * (D + 2);       // floats: o [HW][D], (m, l) [HW][2]
     static constexpr int kSmem = kWarps * (kRing + kPiece * 4);
+    static constexpr int kSmemMost = kSmem + (kScanSeqs + 2) * 12;
+    static_assert(kSmemMost <= 226 * 1024, "fits an SM");
     static_assert(kRing >= kPiece * 4, "a drained ring holds a piece");
 };
 
@@ -237,7 +253,7 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
     constexpr int NG = S::NG, NS = S::NS, HW = S::HW, kWarps = S::kWarps;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ PieceMeta meta[2 * kWarps];
-    __shared__ int last_s[2];
+    __shared__ int64_t warp_tot[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5), r = lane >> 2, c = lane & 3;
     uint8_t *ring = smem + warp * S::kRing;
     float *first_piece = reinterpret_cast<float *>(smem + kWarps * S::kRing) + warp * S::kPiece;
@@ -245,18 +261,36 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
     if (lane == 0) meta[2 * warp].seq = meta[2 * warp + 1].seq = -1;
     grid_dependency_wait();
     grid_dependents_launch();
-    const int64_t total = p.prefix[p.num_seqs] * VH;
+    const int64_t *prefix = p.prefix;
+    const int32_t *ctxs = p.context_lens;
+    if (p.scan) {
+        int64_t *pre = reinterpret_cast<int64_t *>(smem + S::kSmem);
+        int32_t *cx = reinterpret_cast<int32_t *>(pre + p.num_seqs + 1);
+        prefix_of<kWarps * 32>(p.context_lens, p.num_seqs, max_tokens, pre, cx, warp_tot,
+                               blockIdx.x == 0 ? p.status : nullptr);
+        __syncthreads();
+        prefix = pre;
+        ctxs = cx;
+    }
+    const int64_t total = prefix[p.num_seqs] * VH;
     // at least a unit a warp: small batches use fewer CTAs and merge in shared memory
-    const int64_t share = max((int64_t)kWarps, (total + gridDim.x - 1) / gridDim.x);
-    const int64_t cta0 = min(total, share * blockIdx.x), cta1 = min(total, cta0 + share);
+    int64_t share = max((int64_t)kWarps, (total + gridDim.x - 1) / gridDim.x);
+    int64_t cta0 = min(total, share * blockIdx.x), cta1 = min(total, cta0 + share);
+    if (p.by_head) {
+        const int s = blockIdx.x / VH, len = (int)(prefix[s + 1] - prefix[s]);
+        cta0 = prefix[s] * VH + (int64_t)(blockIdx.x - s * VH) * len;
+        cta1 = cta0 + len;
+    } else if (tid == 0) {
+        p.cuts[blockIdx.x].seq = -1;
+    }
     if (cta0 == cta1) return;
     const int64_t w0 = cta0 + (cta1 - cta0) * warp / kWarps, w1 = cta0 + (cta1 - cta0) * (warp + 1) / kWarps;
 
     if (w1 > w0) {
         // ---- where the warp's part begins
-        int s = uniform(find_seq(p.prefix, p.num_seqs, w0 / VH, lane));
-        int ctx = uniform(__ldg(p.context_lens + s)), nu = units_of(ctx, max_tokens);
-        const int64_t in_seq = w0 - p.prefix[s] * VH;
+        int s = uniform(find_seq(prefix, p.num_seqs, w0 / VH, lane));
+        int ctx = uniform(ctxs[s]), nu = units_of(ctx, max_tokens);
+        const int64_t in_seq = w0 - prefix[s] * VH;
         int vh = uniform((int)(in_seq / length_of(nu)));
         const int into = uniform((int)(in_seq - (int64_t)vh * length_of(nu)));
         int u = max(0, into - kHeadCost);
@@ -286,7 +320,7 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                 if (++cvh == VH && cleft > 0) {
                     cvh = 0;
                     do {
-                        cctx = uniform(__ldg(p.context_lens + ++cs));
+                        cctx = uniform(ctxs[++cs]);
                         cnu = units_of(cctx, max_tokens);
                     } while (cnu == 0);
                 }
@@ -784,7 +818,7 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
             if (++vh == VH && left > 0) {
                 vh = 0;
                 do {
-                    ctx = uniform(__ldg(p.context_lens + ++s));
+                    ctx = uniform(ctxs[++s]);
                     nu = units_of(ctx, max_tokens);
                 } while (nu == 0);
             }
@@ -842,56 +876,53 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                 store_head(a.seq, h0 + h, acc, L);
             } else {
 #pragma unroll
-                for (int d = 0; d < PER; ++d) __stcg(dst + h * D + d * 32 + lane, acc[d]);
+                for (int d = 0; d < PER; ++d) dst[h * D + d * 32 + lane] = acc[d];
                 if (lane == 0) {
-                    __stcg(dst + HW * D + 2 * h, M);
-                    __stcg(dst + HW * D + 2 * h + 1, L);
+                    dst[HW * D + 2 * h] = M;
+                    dst[HW * D + 2 * h + 1] = L;
                 }
             }
         }
         j0 = j1;
     }
-    if (cut[0].seq < 0 && cut[1].seq < 0) return;
-    // ---- heads cut between CTAs: the last CTA to arrive merges their pieces, in stream order.  The first unit
-    // of the head cut on the left lies u0 before the CTA's share, that of the other u1 before its end.
-    __threadfence();
-    __syncthreads();
-    const int64_t at[2] = {cta0 - cut[0].u0, cta1 - cut[1].u1};
-    if (tid < 2) {
-        int last = 0;
-        if (cut[tid].seq >= 0) {
-            const int64_t c0 = at[tid] / share, c1 = (at[tid] + cut[tid].nu - 1) / share;
-            last = atomic_add_acq_rel_gpu(p.arrivals + c0, 1) == (int)(c1 - c0);
-        }
-        last_s[tid] = last;
-    }
-    __syncthreads();
+    // the first unit of a head cut on the right only lies u1 before the end of the CTA's share
+    if (tid == 0 && cut[1].seq >= 0)
+        p.cuts[blockIdx.x] = {cut[1].seq, cut[1].vh, (int)((cta1 - cut[1].u1 + cut[1].nu - 1) / share), 0};
+}
+
+// Heads cut between CTAs: CTA c merges the pieces of the one cut at the end of the decode kernel's CTA c, in stream
+// order.
+template <typename T, int D, int HW>
+__global__ void __launch_bounds__(256) q4_merge_kernel(const Q4Params p) {
+    constexpr int PER = D / 32, kPiece = HW * (D + 2);
+    const int c0 = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const Cut a = p.cuts[c0];
+    if (a.seq < 0) return;
+    const int part = a.vh % p.split, h0 = (a.vh / p.split) * p.group + part * p.hw;
+    const int heads = min(p.hw, p.group - part * p.hw);
+    // the first CTA's piece is the one cut on its right
+    auto src = [&](int cta) { return p.part + ((int64_t)cta * 2 + (cta == c0 ? 1 : 0)) * kPiece; };
+    for (int h = warp; h < heads; h += 8) {
+        float M = -INFINITY, L = 0.0f, acc[PER];
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-        if (!last_s[side]) continue;
-        const PieceMeta a = cut[side];
-        const int64_t c0 = at[side] / share, c1 = (at[side] + a.nu - 1) / share;
-        const int part = a.vh % p.split, h0 = (a.vh / p.split) * p.group + part * p.hw;
-        const int heads = min(p.hw, p.group - part * p.hw);
-        for (int h = warp; h < heads; h += kWarps) {
-            float M = -INFINITY, L = 0.0f, acc[PER];
+        for (int d = 0; d < PER; ++d) acc[d] = 0.0f;
+        for (int cta = c0 + lane; cta <= a.last; cta += 32) M = fmaxf(M, src(cta)[HW * D + 2 * h]);
 #pragma unroll
-            for (int d = 0; d < PER; ++d) acc[d] = 0.0f;
-            // the first CTA's piece is the one cut on its right
-            auto src = [&](int64_t cta) { return p.part + (cta * 2 + (cta == c0 ? 1 : 0)) * S::kPiece; };
-            for (int64_t cta = c0 + lane; cta <= c1; cta += 32) M = fmaxf(M, __ldcg(src(cta) + HW * D + 2 * h));
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
 #pragma unroll 4
-            for (int64_t cta = c0; cta <= c1; ++cta) {
-                const float *pc = src(cta);
-                const float f = fast_exp2(__ldcg(pc + HW * D + 2 * h) - M);
-                L += f * __ldcg(pc + HW * D + 2 * h + 1);
+        for (int cta = c0; cta <= a.last; ++cta) {
+            const float *pc = src(cta);
+            const float f = fast_exp2(pc[HW * D + 2 * h] - M);
+            L += f * pc[HW * D + 2 * h + 1];
 #pragma unroll
-                for (int d = 0; d < PER; ++d) acc[d] += f * __ldcg(pc + h * D + d * 32 + lane);
-            }
-            store_head(a.seq, h0 + h, acc, L);
+            for (int d = 0; d < PER; ++d) acc[d] += f * pc[h * D + d * 32 + lane];
         }
+        T *dst = static_cast<T *>(p.out) + ((int64_t)a.seq * p.num_heads + h0 + h) * D;
+        const float inv = 1.0f / L;
+#pragma unroll
+        for (int d = 0; d < PER; ++d) dst[d * 32 + lane] = from_float<T>(acc[d] * inv);
     }
 }
 
@@ -913,7 +944,7 @@ cudaError_t launch_typed(Q4Params p, const AttnArgs &a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? 1ull << dev : 0;
     auto set = [&] {
-        const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemMost);
         if (r == cudaSuccess) known.fetch_or(bit);
         return r;
     };
@@ -921,17 +952,25 @@ cudaError_t launch_typed(Q4Params p, const AttnArgs &a, cudaStream_t stream) {
     if (!had && (e = set()) != cudaSuccess) return e;
     p.split = (p.group + S::HW - 1) / S::HW;
     p.hw = (p.group + p.split - 1) / p.split;
-    const int grid = min(kMaxCtas, device_sm_count());
-    e = launch_dependent(q4_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a.context_lens, a.num_seqs,
-                         (int)(a.max_blocks * a.block_size), const_cast<int64_t *>(p.prefix), p.arrivals, a.status);
-    if (e != cudaSuccess) return e;
-    e = launch_dependent(kern, dim3(grid), dim3(S::kWarps * 32), S::kSmem, stream, p);
+    const int sms = min(kMaxCtas, device_sm_count()), max_tokens = a.max_blocks * a.block_size;
+    const int64_t heads = (int64_t)a.num_seqs * a.num_kv_heads * p.split;
+    p.scan = a.num_seqs <= kScanSeqs;
+    // one CTA a head: nothing is cut between CTAs.  Beyond kHeadUnits units a head the split over all SMs is faster
+    p.by_head = heads <= sms && max_tokens <= kHeadUnits * kU;
+    const int grid = p.by_head ? (int)heads : sms;
+    const size_t smem = S::kSmem + (p.scan ? (size_t)(a.num_seqs + 2) * 12 : 0);
+    if (!p.scan) {
+        e = launch_dependent(q4_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a.context_lens, a.num_seqs,
+                             max_tokens, p.prefix, a.status);
+        if (e != cudaSuccess) return e;
+    }
+    e = launch_dependent(kern, dim3(grid), dim3(S::kWarps * 32), smem, stream, p);
     if (e == cudaErrorInvalidValue && had) {
         cudaGetLastError();
-        if ((e = set()) == cudaSuccess)
-            e = launch_dependent(kern, dim3(grid), dim3(S::kWarps * 32), S::kSmem, stream, p);
+        if ((e = set()) == cudaSuccess) e = launch_dependent(kern, dim3(grid), dim3(S::kWarps * 32), smem, stream, p);
     }
-    return e;
+    if (e != cudaSuccess || p.by_head) return e;
+    return launch_dependent(q4_merge_kernel<T, D, S::HW>, dim3(grid), dim3(256), 0, stream, p);
 }
 
 }  // namespace
@@ -939,7 +978,7 @@ cudaError_t launch_typed(Q4Params p, const AttnArgs &a, cudaStream_t stream) {
 size_t decode_q4_workspace(int num_seqs, int num_heads, int num_kv_heads, int head_dim) {
     const int hw = two_tiles(num_heads / num_kv_heads, false) ? 16 : 8;
     const size_t part = (size_t)kMaxCtas * 2 * hw * (head_dim + 2) * sizeof(float);
-    return prefix_bytes(num_seqs) + kMaxCtas * sizeof(int32_t) + (part + 255) / 256 * 256;
+    return prefix_bytes(num_seqs) + kMaxCtas * sizeof(Cut) + (part + 255) / 256 * 256;
 }
 
 cudaError_t launch_decode_q4(const AttnArgs &a, void *workspace, size_t, cudaStream_t stream) {
@@ -952,8 +991,8 @@ cudaError_t launch_decode_q4(const AttnArgs &a, void *workspace, size_t, cudaStr
     p.block_tables = a.block_tables;
     p.context_lens = a.context_lens;
     p.prefix = reinterpret_cast<int64_t *>(ws);
-    p.arrivals = reinterpret_cast<int32_t *>(ws + prefix_bytes(a.num_seqs));
-    p.part = reinterpret_cast<float *>(ws + prefix_bytes(a.num_seqs) + kMaxCtas * sizeof(int32_t));
+    p.cuts = reinterpret_cast<Cut *>(ws + prefix_bytes(a.num_seqs));
+    p.part = reinterpret_cast<float *>(ws + prefix_bytes(a.num_seqs) + kMaxCtas * sizeof(Cut));
     p.num_seqs = a.num_seqs;
     p.num_heads = a.num_heads;
     p.num_kv_heads = a.num_kv_heads;
