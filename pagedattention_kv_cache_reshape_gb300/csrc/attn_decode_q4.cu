@@ -68,7 +68,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kMaxCtas = 512;
 constexpr int kScanSeqs = 4096;     // sequences whose prefix a CTA makes itself (48 KB of shared memory)
 constexpr int kHeadUnits = 128;     // a CTA a head: up to this many units
-constexpr int kHeadCost = 5;
+constexpr int kHeadCost = 4;
 constexpr float kMoveAt = 8.0f;     // a logit this far (base 2) over the reference moves it
 
 // A head cut at the end of CTA c (seq < 0: none): its pieces are c's second, then the first of c + 1 .. last.
@@ -295,25 +295,18 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
         const int into = uniform((int)(in_seq - (int64_t)vh * length_of(nu)));
         int u = max(0, into - kHeadCost);
         int left = uniform((int)(w1 - w0)) - max(0, kHeadCost - into);   // of the part, in stream units
-        // ---- the copies' own place in the stream, kStages units ahead: a stretch is the units whose block
-        // ids the lanes hold (id i of the stretch in lane i)
-        int cs = s, cctx = ctx, cnu = nu, cvh = vh, cu = u, cleft = left;
-        int stretch = 0, id_at = 0, half = 0, ids = 0, ids_seq = -1, ids_base = 0;
+        // ---- the copies' own place in the stream, kStages units ahead: a stretch is the units whose block ids the
+        // lanes hold (id i of the stretch in lane i); the next stretch's ids are requested one stretch early
+        int cs = s, cctx = ctx, cnu = nu, cvh = vh, cu = u, cleft = left;   // the next stretch
+        int next_len = 0, next_ids = 0, ids_seq = -1, ids_base = 0;
+        int stretch = 0, id_at = 0, half = 0, ids = 0;
         const uint32_t ring_a = smem_u32(ring);
         uint32_t wr = ring_a;
         const int v_sw = lane ^ (2 * ((lane / NG >> 2) & 3));      // swizzled place of V's chunk `lane`
         const int k_sw = D == 64 ? lane ^ (4 * ((lane / NG >> 2) & 1)) : lane;
         const int chunk = D == 128 ? lane : lane & 15;
         const uint8_t *k_src, *v_src, *sc_src;
-        auto at_head = [&]() {
-            const uint64_t at = (uint64_t)(uint32_t)(cvh / p.split) * p.slab;
-            k_src = p.k + at + chunk * 16;
-            v_src = p.v + at + chunk * 16;
-            sc_src = (lane < 2 * NG ? p.k : p.v) + at + B * (D / 2) + (lane % NG) * 16;
-            if (p.log2b != 3 && lane & NG) sc_src += 8 * (NG * 2);   // the rows 8..15 of a unit
-        };
-        at_head();
-        auto next_stretch = [&]() {
+        auto request = [&]() {
             if (cu == cnu) {
                 cu = 0;
                 cleft -= kHeadCost;
@@ -324,30 +317,38 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                         cnu = units_of(cctx, max_tokens);
                     } while (cnu == 0);
                 }
-                at_head();
             }
-            stretch = 0;
+            next_len = 0;
             if (cleft <= 0) return;
             const int b = (int)(((unsigned)cu * kU) >> p.log2b);
             if (cs != ids_seq || b != ids_base) {
                 ids_seq = cs;
                 ids_base = b;
                 const int64_t e = (int64_t)b + lane;
-                ids = 0;   // behind the sequence or out of range: block 0 is read and not used
-                if ((e << p.log2b) < cctx) {
-                    ids = __ldg(p.block_tables + (int64_t)cs * p.max_blocks + e);
-                    if (ids < 0 || ids >= p.num_blocks) {
-                        set_status(p.status, PA_ERR_OUT_OF_RANGE);
-                        ids = 0;
-                    }
-                }
+                next_ids = 0;   // behind the sequence or out of range: block 0 is read and not used
+                if ((e << p.log2b) < cctx) next_ids = __ldg(p.block_tables + (int64_t)cs * p.max_blocks + e);
             }
+            const int held = p.log2b == 4 ? 32 : p.log2b == 3 ? 16 : 64 - (cu & 1);
+            next_len = min(min(cnu - cu, held), cleft);
+            cleft -= next_len;
+        };
+        auto next_stretch = [&]() {
+            stretch = next_len;
+            if (stretch == 0) return;
+            if (next_ids < 0 || next_ids >= p.num_blocks) {
+                set_status(p.status, PA_ERR_OUT_OF_RANGE);
+                next_ids = 0;
+            }
+            ids = next_ids;
             id_at = 0;
             half = p.log2b == 5 ? cu & 1 : 0;
-            const int held = p.log2b == 4 ? 32 : p.log2b == 3 ? 16 : 64 - half;
-            stretch = min(min(cnu - cu, held), cleft);
+            const uint64_t at = (uint64_t)(uint32_t)(cvh / p.split) * p.slab;
+            k_src = p.k + at + chunk * 16;
+            v_src = p.v + at + chunk * 16;
+            sc_src = (lane < 2 * NG ? p.k : p.v) + at + B * (D / 2) + (lane % NG) * 16;
+            if (p.log2b != 3 && lane & NG) sc_src += 8 * (NG * 2);   // the rows 8..15 of a unit
             cu += stretch;
-            cleft -= stretch;
+            request();
         };
         auto copy = [&](const uint8_t *k0, const uint8_t *v0, const uint8_t *k1, const uint8_t *v1, const uint8_t *sc) {
             if constexpr (D == 128) {   // chunks 0..31: rows 0..7, 32..63: rows 8..15
@@ -386,6 +387,33 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
             }
             cp_async_commit();
         };
+        request();
+        // a head's queries as they lie in memory; requested while the head before it is finished (one tile of bf16
+        // queries: the larger forms have no registers for that)
+        constexpr bool kEarly = NT == 1 && !S::kF32;
+        Raw8<T> q_raw[NT][NG];
+        auto request_q = [&](int seq, int head) {
+            const int part = head % p.split, h0 = (head / p.split) * p.group + part * p.hw;
+            const int heads = min(p.hw, p.group - part * p.hw);
+            const T *qrow = static_cast<const T *>(p.q) + ((int64_t)seq * p.num_heads + h0) * D;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const int h = 8 * nt + r;
+                    const T *src = qrow + (int64_t)h * D + 32 * g + 8 * c;
+                    q_raw[nt][g] = {};
+                    if (h < heads) {
+                        if (p.vec) {
+                            q_raw[nt][g] = load_raw8(src);
+                        } else {
+#pragma unroll
+                            for (int d = 0; d < 8; ++d) reinterpret_cast<T *>(&q_raw[nt][g])[d] = src[d];
+                        }
+                    }
+                }
+        };
+        if (kEarly && left > 0) request_q(s, vh);
         next_stretch();
 #pragma unroll
         for (int i = 0; i < kStages; ++i) issue();
@@ -631,32 +659,12 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
             if (fresh) {
                 fresh = false;
                 u_first = u;
-                const int part = vh % p.split, h0 = (vh / p.split) * p.group + part * p.hw;
-                const int heads = min(p.hw, p.group - part * p.hw);
-                const T *qrow = static_cast<const T *>(p.q) + ((int64_t)s * p.num_heads + h0) * D;
+                if (!kEarly) request_q(s, vh);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const int h = 8 * nt + r;
                     float x[NG][8];
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        const T *src = qrow + (int64_t)h * D + 32 * g + 8 * c;
-#pragma unroll
-                        for (int d = 0; d < 8; ++d) x[g][d] = 0.0f;
-                        if (h < heads) {
-                            if (p.vec) {
-                                T y[8];
-#pragma unroll
-                                for (int d = 0; d < (int)sizeof(T) / 2; ++d)
-                                    reinterpret_cast<uint4 *>(y)[d] = __ldg(reinterpret_cast<const uint4 *>(src) + d);
-#pragma unroll
-                                for (int d = 0; d < 8; ++d) x[g][d] = to_float(y[d]);
-                            } else {
-#pragma unroll
-                                for (int d = 0; d < 8; ++d) x[g][d] = to_float(src[d]);
-                            }
-                        }
-                    }
+                    for (int g = 0; g < NG; ++g) to_floats(x[g], q_raw[nt][g]);
                     if constexpr (S::kF32) {
 #pragma unroll
                         for (int g = 0; g < NG; ++g)
@@ -742,6 +750,16 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
             // ---- the end of a (sequence, head) or of the warp's part
             const int part = vh % p.split, h0 = (vh / p.split) * p.group + part * p.hw;
             const int heads = min(p.hw, p.group - part * p.hw);
+            const int s_done = s, vh_done = vh, nu_done = nu;
+            left -= kHeadCost;
+            if (++vh == VH && left > 0) {
+                vh = 0;
+                do {
+                    ctx = uniform(ctxs[++s]);
+                    nu = units_of(ctx, max_tokens);
+                } while (nu == 0);
+            }
+            if (kEarly && left > 0) request_q(s, vh);
             // rows r of a tile carry 2^-24 (bf16 calls), rows r + 8 2^-20
             constexpr float kUp0 = S::kF32 ? 1.0f : 0x1p24f, kUp1 = S::kF32 ? 1.0f : 0x1p20f;
 #pragma unroll
@@ -761,14 +779,14 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                     l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
                     l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
                 }
-            if (u_first == 0 && u == nu) {
+            if (u_first == 0 && u == nu_done) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int h = 8 * nt + 2 * c + e;
                         if (h >= heads) continue;
-                        T *dst = static_cast<T *>(p.out) + ((int64_t)s * p.num_heads + h0 + h) * D + 4 * r;
+                        T *dst = static_cast<T *>(p.out) + ((int64_t)s_done * p.num_heads + h0 + h) * D + 4 * r;
                         const float inv = 1.0f / l[nt][e];
 #pragma unroll
                         for (int g = 0; g < NG; ++g) {
@@ -793,7 +811,7 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                     __syncwarp();
                     piece = reinterpret_cast<float *>(ring);
                 }
-                if (lane == 0) meta[2 * warp + (at_start ? 0 : 1)] = {s, vh, u_first, u, nu};
+                if (lane == 0) meta[2 * warp + (at_start ? 0 : 1)] = {s_done, vh_done, u_first, u, nu_done};
                 const float down = __uint_as_float((uint32_t)(127 - lift) << 23);   // 2^-lift
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -814,14 +832,6 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
             fresh = true;
             at_start = false;
             u = 0;
-            left -= kHeadCost;
-            if (++vh == VH && left > 0) {
-                vh = 0;
-                do {
-                    ctx = uniform(ctxs[++s]);
-                    nu = units_of(ctx, max_tokens);
-                } while (nu == 0);
-            }
         }
         cp_async_wait<0>();
     }
