@@ -3,10 +3,10 @@
 //  quantize:   a prompt prefilled in a bf16 pool goes over to the 4-bit pool
 //              its decode steps read;
 //  dequantize: a cached 4-bit prefix is expanded for a prefill over it.
-// Both move (e + 9/16) bytes a value (e = 2 or 4) and are bound by HBM.  A thread
-// takes 8 consecutive dims of a token row (16 or 32 bytes of the wide pool, 4
-// of the codes), a warp 256 dims: whole 128-byte lines of codes, and rows of
-// the wide pool in pieces of D e bytes.
+// Both move (e + 9/16) bytes a value (e = 2 or 4) and are bound by HBM, with
+// the quantising one near its instruction issue.  A thread takes 16 (quantize)
+// or 8 consecutive dims of a token row, a warp whole lines of the codes, and
+// rows of the wide pool in pieces of D e bytes.
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "q4_format.cuh"
@@ -41,10 +41,11 @@ __device__ __forceinline__ void expand8(float *dst, uint32_t w, uint16_t scale) 
     store8(dst, y);
 }
 
-// grid: (pair, part of the block).  Items of a block: [K, V][head][token][8 dims].
+// grid: (pair, part of the block).  Items of a block: [K, V][head][token][16 or 8 dims].
 template <typename T, int D, bool kQuantize>
 __global__ void __launch_bounds__(kThreads) q4_convert_kernel(const Q4BlocksArgs a, int log2b) {
-    constexpr int kRow = D / 8, NG = D / kQ4Group;   // threads and groups of a row
+    constexpr int kDims = kQuantize ? 16 : 8, kItems = kQuantize ? kPerThread / 2 : kPerThread;
+    constexpr int kRow = D / kDims, NG = D / kQ4Group;   // threads and groups of a row
     const int H = a.num_kv_heads, half = (H * kRow) << log2b, slab = q4_slab_bytes(1 << log2b, D);
     grid_dependency_wait();
     grid_dependents_launch();
@@ -55,23 +56,25 @@ __global__ void __launch_bounds__(kThreads) q4_convert_kernel(const Q4BlocksArgs
         if (threadIdx.x == 0 && blockIdx.y == 0) set_status(a.status, PA_ERR_OUT_OF_RANGE);
         return;
     }
-    const int64_t wide_blk = (int64_t)(kQuantize ? src : dst) * half * 8;
+    const int64_t wide_blk = (int64_t)(kQuantize ? src : dst) * half * kDims;
     const int64_t q4_blk = (int64_t)(kQuantize ? dst : src) * H * slab;
-    // the thread's place in a row is the same for all its items; half is a multiple of 32 (B * D / 8 is one of
-    // 64), so a warp's items are all of K, all of V or all outside
-    const int k = threadIdx.x % kRow, g = k / 4, r = 2 * (k & 3) + (g & 1);
-    const int first = blockIdx.y * kThreads * kPerThread + threadIdx.x;
-    Raw8<T> raw[kQuantize ? kPerThread : 1];
-    uint32_t w[kPerThread];
-    uint16_t sb[kPerThread];
+    // the thread's place in a row is the same for all its items; half is a multiple of 32 (B * D / 16 is one), so
+    // a warp's items are all of K, all of V or all outside
+    const int k = threadIdx.x % kRow, g = k / 4, r = 2 * (k & 3) + (g & 1);   // (g, r: of 8 dims)
+    const int first = blockIdx.y * kThreads * kItems + threadIdx.x;
+    Raw8<T> lo[kQuantize ? kItems : 1], hi[kQuantize ? kItems : 1];
+    uint32_t w[kItems];
+    uint16_t sb[kItems];
 #pragma unroll
-    for (int u = 0; u < kPerThread; ++u) {
+    for (int u = 0; u < kItems; ++u) {
         const int e = first + u * kThreads;
         if (e >= 2 * half) break;
         const bool is_v = e >= half;
         const int t = (is_v ? e - half : e) / kRow, tok = t & ((1 << log2b) - 1), h = t >> log2b;
-        if (kQuantize) {
-            raw[kQuantize ? u : 0] = load_raw8(static_cast<const T *>(is_v ? a.src_v : a.src_k) + wide_blk + (tok * H + h) * D + k * 8);
+        if constexpr (kQuantize) {
+            const T *p = static_cast<const T *>(is_v ? a.src_v : a.src_k) + wide_blk + (tok * H + h) * D + k * 16;
+            lo[u] = load_raw8(p);
+            hi[u] = load_raw8(p + 8);
         } else {
             const uint8_t *p = static_cast<const uint8_t *>(is_v ? a.src_v : a.src_k) + q4_blk + h * slab;
             w[u] = *reinterpret_cast<const uint32_t *>(p + tok * (D / 2) + (is_v ? (r * NG + (g & ~1)) * 2 : q4_k_word(8 * k, D)));
@@ -79,15 +82,15 @@ __global__ void __launch_bounds__(kThreads) q4_convert_kernel(const Q4BlocksArgs
         }
     }
 #pragma unroll
-    for (int u = 0; u < kPerThread; ++u) {
+    for (int u = 0; u < kItems; ++u) {
         const int e = first + u * kThreads;
         if (e >= 2 * half) break;
         const bool is_v = e >= half;
         const int t = (is_v ? e - half : e) / kRow, tok = t & ((1 << log2b) - 1), h = t >> log2b;
-        if (kQuantize) {
+        if constexpr (kQuantize) {
             uint8_t *p = static_cast<uint8_t *>(is_v ? a.dst_v : a.dst_k) + q4_blk + h * slab;
-            q4_store8<D>(raw[kQuantize ? u : 0], k, is_v, p + tok * (D / 2),
-                         reinterpret_cast<uint16_t *>(p + ((D / 2) << log2b) + tok * (NG * 2)), true);
+            q4_store16<D>(lo[u], hi[u], k, is_v, p + tok * (D / 2),
+                          reinterpret_cast<uint16_t *>(p + ((D / 2) << log2b) + tok * (NG * 2)), true);
         } else {
             if (is_v) {   // (r, g), (r, g + 1) against the neighbour group's (r + 1, g), (r + 1, g + 1)
                 const uint32_t other = __shfl_xor_sync(0xffffffffu, w[u], 4);

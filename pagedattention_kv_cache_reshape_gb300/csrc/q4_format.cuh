@@ -34,17 +34,23 @@ __host__ __device__ constexpr int q4_slab_bytes(int block_size, int d) {
 __host__ __device__ constexpr int q4_k_word(int dim, int d) {
     return (((dim % kQ4Group) / 8) * (d / kQ4Group) + dim / kQ4Group) * 4;
 }
-// byte offset of 4 consecutive dims' unit in a V row (dim a multiple of 4)
-__host__ __device__ constexpr int q4_v_unit(int dim, int d) {
-    return (((dim % kQ4Group) / 4) * (d / kQ4Group) + dim / kQ4Group) * 2;
-}
 
 // Bits of the scale of a group from the bits of its largest magnitude.  NaN and
 // infinities have the largest bit patterns, so a group that holds one is found
 // by the same integer maximum; it takes a NaN scale and reads back as NaN.
+// amax / 7 is the correctly rounded quotient, as in q4_word.
 __device__ __forceinline__ uint16_t q4_scale_bits(uint32_t amax_bits) {
-    if (amax_bits >= 0x7f800000u) return 0x7fc0u;
-    return __bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(__uint_as_float(amax_bits), 7.0f)));
+    const float amax = __uint_as_float(amax_bits);
+    float s;
+    if (amax_bits - 0x0d000000u < 0x7f800000u - 0x0d000000u) {   // 2^-101 <= amax < inf
+        constexpr float r = 1.0f / 7.0f;
+        const float q0 = __fmul_rn(amax, r);
+        s = __fmaf_rn(__fmaf_rn(-q0, 7.0f, amax), r, q0);
+    } else {
+        if (amax_bits >= 0x7f800000u) return 0x7fc0u;
+        s = __fdiv_rn(amax, 7.0f);
+    }
+    return __bfloat16_as_ushort(__float2bfloat16_rn(s));
 }
 __device__ __forceinline__ float q4_scale_value(uint16_t bits) {
     return __uint_as_float((uint32_t)bits << 16);
@@ -131,34 +137,37 @@ __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
     *(reinterpret_cast<float4 *>(p) + 1) = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// Quantises 8 values, dims 8 k .. 8 k + 7 of a token row, and stores them: called
-// by whole warps in which the D / 8 lanes of a row are neighbours in order of
-// k, a row's first lane a multiple of D / 8.  `row` is the row's code bytes and
-// `scales` its scales; lanes with store = false only take part in the shuffles.
+// Quantises 16 values, dims 16 k .. 16 k + 15 of a token row (half a group), and
+// stores them: called by whole warps in which the D / 16 lanes of a row are
+// neighbours in order of k, a row's first lane a multiple of D / 16.  `row` is
+// the row's code bytes and `scales` its scales; lanes with store = false only
+// take part in the shuffles.
 template <int D, typename T>
-__device__ __forceinline__ void q4_store8(const Raw8<T> &raw, int k, bool is_v, uint8_t *row, uint16_t *scales,
-                                          bool store) {
+__device__ __forceinline__ void q4_store16(const Raw8<T> &lo, const Raw8<T> &hi, int k, bool is_v, uint8_t *row,
+                                           uint16_t *scales, bool store) {
     constexpr int NG = D / kQ4Group;
-    uint32_t amax = amax_bits8(raw);
+    uint32_t amax = max(amax_bits8(lo), amax_bits8(hi));
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const uint16_t sb = q4_scale_bits(amax);
-    float x[8];
-    to_floats(x, raw);
-    const uint32_t w = q4_word(x, q4_scale_value(sb));
-    // V: a lane holds units r = 2 (k % 4) and r + 1 of group g; with its neighbour group's lane it makes the 4
-    // bytes (r, g), (r, g + 1) or (r + 1, g - 1), (r + 1, g)
-    const int g = k / 4;
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 4);
-    if (!store) return;
-    if (is_v) {
-        const uint32_t pair = g & 1 ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
-        const int r = 2 * (k & 3) + (g & 1);
-        *reinterpret_cast<uint32_t *>(row + (r * NG + (g & ~1)) * 2) = pair;
-    } else {
-        *reinterpret_cast<uint32_t *>(row + q4_k_word(8 * k, D)) = w;
+    const float s = q4_scale_value(sb);
+    const int g = k >> 1, h = k & 1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float x[8];
+        to_floats(x, i ? hi : lo);
+        const uint32_t w = q4_word(x, s);
+        // V: a word holds units r = 4 h + 2 i and r + 1 of group g; with its neighbour group's lane the lane makes
+        // the 4 bytes (r, g), (r, g + 1) or (r + 1, g - 1), (r + 1, g)
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 2);
+        if (!store) continue;
+        if (is_v) {
+            const uint32_t pair = g & 1 ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
+            *reinterpret_cast<uint32_t *>(row + ((4 * h + 2 * i + (g & 1)) * NG + (g & ~1)) * 2) = pair;
+        } else {
+            *reinterpret_cast<uint32_t *>(row + ((2 * h + i) * NG + g) * 4) = w;
+        }
     }
-    if ((k & 3) == 0) scales[g] = sb;
+    if (store && h == 0) scales[g] = sb;
 }
 
 }  // namespace pa

@@ -22,6 +22,7 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kVecThreads = 384;   // 3 CTAs of 56 registers an SM: 36 warps' loads in flight
 
 // a c - b s (sign = -1) or a c + b s (sign = +1), the exact value rounded once to
 // fp32: both products are split into value and error (fma), the sum into value
@@ -102,8 +103,8 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) 
         }
         return;
     }
-    // rows of 8 or 16 neighbouring lanes, 8 dims a lane
-    const int lanes = D / 8, k = lane % lanes;
+    // rows of 4 or 8 neighbouring lanes, 16 dims a lane
+    const int lanes = D / 16, k = lane % lanes;
     const int64_t blk = slot / a.block_size;
     const int off = (int)(slot - blk * a.block_size);
     const int64_t slab = q4_slab_bytes(a.block_size, D);
@@ -111,15 +112,15 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) 
         const int j = j0 + lane / lanes;
         const bool in = j < 2 * a.num_kv_heads, is_v = in && j >= a.num_kv_heads;
         const int h = in ? (is_v ? j - a.num_kv_heads : j) : 0;
-        Raw8<T> x;
-        for (int i = 0; i < 8; ++i)
-            reinterpret_cast<T *>(&x)[i] = is_v ? value[(int64_t)h * D + 8 * k + i]
-                                                : from_float<T>(rotated(a, key + (int64_t)h * D, cs, 8 * k + i));
+        Raw8<T> x[2];
+        for (int i = 0; i < 16; ++i)
+            reinterpret_cast<T *>(x)[i] = is_v ? value[(int64_t)h * D + 16 * k + i]
+                                               : from_float<T>(rotated(a, key + (int64_t)h * D, cs, 16 * k + i));
         uint8_t *s = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) + (blk * a.num_kv_heads + h) * slab;
         uint8_t *row = s + off * q4_row_bytes(D);
         uint16_t *scales = reinterpret_cast<uint16_t *>(s + a.block_size * q4_row_bytes(D)) + off * (D / kQ4Group);
-        if (D == 128) q4_store8<128>(x, k, is_v, row, scales, in);
-        else q4_store8<64>(x, k, is_v, row, scales, in);
+        if (D == 128) q4_store16<128>(x[0], x[1], k, is_v, row, scales, in);
+        else q4_store16<64>(x[0], x[1], k, is_v, row, scales, in);
     }
 }
 
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) 
 // requested before the slots and positions that decide what becomes of them.  4-bit pools: the rotated keys and
 // the values meet in shared memory, where 8 consecutive dims go to a lane.
 template <typename T, bool kQ4, int U>
-__global__ void __launch_bounds__(512) rope_cache_vec_kernel(const RopeArgs a, int rows, int passes) {
+__global__ void __launch_bounds__(kVecThreads, kQ4 ? 2 : 3) rope_cache_vec_kernel(const RopeArgs a, int rows, int passes) {
     extern __shared__ __align__(16) uint8_t smem[];
     T *kv_s = reinterpret_cast<T *>(smem);   // [U][2 num_kv_heads][D], 4-bit pools only
     const int D = a.head_dim, lanes = D / 16, tid = threadIdx.x;
@@ -213,25 +214,22 @@ __global__ void __launch_bounds__(512) rope_cache_vec_kernel(const RopeArgs a, i
     }
     if (!kQ4) return;
     __syncthreads();
-    const int per = D / 8, k = tid % per;   // a row's lanes lie in one warp: per is 8 or 16
+    const int per = D / 16, k = tid % per;   // a row's lanes lie in one warp: per is 4 or 8
     const int64_t slab = q4_slab_bytes(a.block_size, D);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (!live[u]) continue;             // the same in every thread
-        const int64_t blk = slot[u] / a.block_size;
-        const int off = (int)(slot[u] - blk * a.block_size);
-        for (int r0 = 0; r0 < 2 * HK; r0 += blockDim.x / per) {
-            if (r0 + (tid & ~31) / per >= 2 * HK) break;   // whole warps
-            const int row = r0 + tid / per;
-            const bool in = row < 2 * HK, is_v = in && row >= HK;
-            const Raw8<T> x = load_raw8(kv_s + (u * 2 * HK + (in ? row : 0)) * D + 8 * k);
-            uint8_t *sl = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) +
-                          (blk * HK + (in ? row - (is_v ? HK : 0) : 0)) * slab;
-            uint8_t *codes = sl + off * q4_row_bytes(D);
-            uint16_t *scales = reinterpret_cast<uint16_t *>(sl + a.block_size * q4_row_bytes(D)) + off * (D / kQ4Group);
-            if (D == 128) q4_store8<128>(x, k, is_v, codes, scales, in);
-            else q4_store8<64>(x, k, is_v, codes, scales, in);
-        }
+    for (int r0 = 0; r0 < U * 2 * HK; r0 += blockDim.x / per) {
+        if (r0 + (tid & ~31) / per >= U * 2 * HK) break;   // whole warps
+        const int r = r0 + tid / per, u = U > 1 && r >= 2 * HK ? 1 : 0, row = r - u * 2 * HK;
+        const int64_t sl = U > 1 && u ? slot[U - 1] : slot[0];
+        const bool in = r < U * 2 * HK && (U > 1 && u ? live[U - 1] : live[0]), is_v = in && row >= HK;
+        const int64_t blk = in ? sl / a.block_size : 0;
+        const int off = in ? (int)(sl - blk * a.block_size) : 0;
+        const T *src = kv_s + (in ? r : 0) * D + 16 * k;
+        uint8_t *to = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) +
+                      (blk * HK + (in ? row - (is_v ? HK : 0) : 0)) * slab;
+        uint8_t *codes = to + off * q4_row_bytes(D);
+        uint16_t *scales = reinterpret_cast<uint16_t *>(to + a.block_size * q4_row_bytes(D)) + off * (D / kQ4Group);
+        if (D == 128) q4_store16<128>(load_raw8(src), load_raw8(src + 8), k, is_v, codes, scales, in);
+        else q4_store16<64>(load_raw8(src), load_raw8(src + 8), k, is_v, codes, scales, in);
     }
 }
 
@@ -239,7 +237,7 @@ template <typename T, bool kQ4>
 cudaError_t launch_vec(const RopeArgs &a, int64_t kv_bytes, cudaStream_t stream) {
     const int lanes = a.head_dim / 16;
     const int64_t all = (int64_t)a.num_heads + 2 * a.num_kv_heads;
-    const int64_t passes = (all * lanes + 511) / 512;
+    const int64_t passes = (all * lanes + kVecThreads - 1) / kVecThreads;
     const int rows = (int)((all + passes - 1) / passes);
     const dim3 block((rows * lanes + 31) / 32 * 32);
     // two tokens a CTA once one each would fill the GPU several times over: twice the loads in flight
