@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) 
 // requested before the slots and positions that decide what becomes of them.  4-bit pools: the rotated keys and
 // the values meet in shared memory, where 8 consecutive dims go to a lane.
 template <typename T, bool kQ4, int U>
-__global__ void __launch_bounds__(kVecThreads, kQ4 ? 2 : 3) rope_cache_vec_kernel(const RopeArgs a, int rows, int passes) {
+__global__ void __launch_bounds__(kVecThreads, kQ4 || sizeof(T) == 4 ? 2 : 3) rope_cache_vec_kernel(const RopeArgs a, int rows, int passes) {
     extern __shared__ __align__(16) uint8_t smem[];
     T *kv_s = reinterpret_cast<T *>(smem);   // [U][2 num_kv_heads][D], 4-bit pools only
     const int D = a.head_dim, lanes = D / 16, tid = threadIdx.x;

@@ -149,9 +149,13 @@ def _check(rc: int, what: str) -> None:
         raise PAError(rc, what)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _stream(stream) -> int:
-    if stream is None:   # the current stream's handle, without a torch.cuda.Stream made on the way
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:   # the current stream's handle, no torch.cuda.Stream is made
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -386,18 +390,18 @@ def _refuse(dev: int, *specs):
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
-def _rows(t, name: str, tokens: int, heads: int, d: int, dtype, dev: int) -> int:
-    """Checks a token-strided view [tokens, heads, d]; returns its token stride."""
-    if t.shape != (tokens, heads, d):
-        raise ValueError(f"{name} must be [{tokens}, {heads}, {d}] with contiguous rows")
-    st, sh, sd = t.stride()
-    if tokens and ((sd != 1 and d > 1) or (sh != d and heads > 1)):
-        raise ValueError(f"{name} must be [{tokens}, {heads}, {d}] with contiguous rows")
+def _rows(name: str, t, shape, dtype, dev: int) -> None:
+    """Raises what is wrong with a token-strided view [tokens, heads, d]."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)} with contiguous rows")
     if t.dtype != dtype:
         raise TypeError("q, key, value and the 16/32-bit pools must share one dtype")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be a tensor on the current device cuda:{dev}, got {t.device}")
-    return st if tokens > 1 else heads * d   # torch may report any stride for one token
+    tokens, heads, d = shape
+    _, sh, sd = t.stride()
+    if tokens and ((sd != 1 and d > 1) or (sh != d and heads > 1)):
+        raise ValueError(f"{name} must be {list(shape)} with contiguous rows")
 
 
 def _q4_pool_shape(k_cache, v_cache, head_dim: int):
@@ -413,23 +417,32 @@ def _q4_pool_shape(k_cache, v_cache, head_dim: int):
 
 def _rope(fn, q, key, value, cos_sin, positions, k_cache, v_cache, pool_dtype, num_blocks, block_size, slot_mapping,
           interleaved, q_out, dev_status, stream):
-    n, hkv, d = key.shape
-    dtype, dev = key.dtype, torch.cuda.current_device()
+    shape, dtype, dev = key.shape, key.dtype, torch.cuda.current_device()
+    n, hkv, d = shape
     code = _CODES.get(dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
-    ks, vs = _rows(key, "key", n, hkv, d, dtype, dev), _rows(value, "value", n, hkv, d, dtype, dev)
+    (ks, k1, k2), (vs, v1, v2) = key.stride(), value.stride()
+    if not (value.shape == shape and value.dtype == dtype and k2 == 1 and v2 == 1 and k1 == d and v1 == d
+            and key.get_device() == dev and value.get_device() == dev):
+        _rows("key", key, shape, dtype, dev)     # (strides of single rows and heads may be anything)
+        _rows("value", value, shape, dtype, dev)
     heads = qs = q_ptr = out_ptr = 0
     if q is not None:
-        heads = q.shape[1] if q.dim() == 3 else 0
-        qs = _rows(q, "q", n, heads, d, dtype, dev)
+        q_shape = q.shape
+        heads = q_shape[1] if len(q_shape) == 3 else 0
         if q_out is None:
             q_out = torch.empty((n, heads, d), dtype=dtype, device=q.device)
-        else:
-            _rows(q_out, "q_out", n, heads, d, dtype, dev)
+        qs, q1, q2 = q.stride() if heads else (0, 0, 0)
+        if not (q_shape == q_out.shape == (n, heads, d) and q.dtype == q_out.dtype == dtype and q2 == 1 and q1 == d
+                and q.get_device() == dev and q_out.get_device() == dev):
+            _rows("q", q, (n, heads, d), dtype, dev)
+            _rows("q_out", q_out, (n, heads, d), dtype, dev)
         if not q_out.is_contiguous():
             raise ValueError("q_out must be contiguous")
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+    if n == 1:   # torch may report any token stride for one token
+        qs, ks, vs = heads * d, hkv * d, hkv * d
     if not (k_cache.is_contiguous() and v_cache.is_contiguous() and slot_mapping.is_contiguous()
             and k_cache.get_device() == v_cache.get_device() == slot_mapping.get_device() == dev
             and k_cache.dtype == v_cache.dtype == pool_dtype and slot_mapping.dtype == torch.int64):
@@ -450,7 +463,8 @@ def _rope(fn, q, key, value, cos_sin, positions, k_cache, v_cache, pool_dtype, n
     rc = getattr(_lib or load(), fn)(
         out_ptr, q_ptr, key.data_ptr(), value.data_ptr(), qs, ks, vs, table_ptr, pos_ptr, max_pos, rot,
         1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), n, heads, hkv, d,
-        block_size, num_blocks, code, 0 if dev_status is None else _opt(dev_status), _stream(stream))
+        block_size, num_blocks, code, 0 if dev_status is None else _opt(dev_status),
+        _raw_stream(dev) if stream is None else _stream(stream))
     if rc != OK:
         raise PAError(rc, fn)
     return q_out
@@ -461,13 +475,13 @@ def rope_and_cache(q, key, value, cos_sin, positions, k_cache, v_cache, slot_map
     """pa_rope_and_cache: q [tokens, H, D] (or None) and key rotated by position, K/V rows written to the pools;
     returns q_out.  q, key and value may be token-strided views; cos_sin is fp32 [max_position, rot_dim] (None: no
     rotation) and positions int32 [tokens]."""
-    num_blocks, block_size, hkv, d = k_cache.shape
-    if k_cache.shape != v_cache.shape or key.dim() != 3 or key.shape[1:] != (hkv, d):
+    pool, rows, dtype = k_cache.shape, key.shape, key.dtype
+    if len(pool) != 4 or v_cache.shape != pool or len(rows) != 3 or rows[1] != pool[2] or rows[2] != pool[3]:
         raise ValueError("key, value and the pools disagree on heads or head_dim")
-    if not (key.dtype == k_cache.dtype == v_cache.dtype):
+    if k_cache.dtype != dtype or v_cache.dtype != dtype:
         raise TypeError("q, key, value and the 16/32-bit pools must share one dtype")
-    return _rope("pa_rope_and_cache", q, key, value, cos_sin, positions, k_cache, v_cache, key.dtype, num_blocks,
-                 block_size, slot_mapping, interleaved, q_out, dev_status, stream)
+    return _rope("pa_rope_and_cache", q, key, value, cos_sin, positions, k_cache, v_cache, dtype, pool[0],
+                 pool[1], slot_mapping, interleaved, q_out, dev_status, stream)
 
 
 def q4_block_bytes(block_size: int, num_kv_heads: int, head_dim: int) -> int:
@@ -512,7 +526,7 @@ def _q4_blocks(fn, wide_k, wide_v, q4_k, q4_v, quantize, pairs, dev_status, stre
     n_src, n_dst = (num_wide, num_q4) if quantize else (num_q4, num_wide)
     rc = getattr(_lib or load(), fn)(src[0], src[1], dst[0], dst[1], block_size, hkv, d, n_src, n_dst,
                                      pairs.data_ptr(), n // 2, code, 0 if dev_status is None else _opt(dev_status),
-                                     _stream(stream))
+                                     _raw_stream(dev) if stream is None else _stream(stream))
     if rc != OK:
         raise PAError(rc, fn)
 
@@ -562,7 +576,8 @@ def decode_q4(q, k_cache, v_cache, block_tables, context_lens, scale: float, out
     rc = (_lib or load()).pa_decode_q4(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         context_lens.data_ptr(), num_seqs, H, hkv, D, block_size, max_blocks, num_blocks, scale, code,
-        workspace.data_ptr(), workspace.nbytes, 0 if dev_status is None else _opt(dev_status), _stream(stream))
+        workspace.data_ptr(), workspace.nbytes, 0 if dev_status is None else _opt(dev_status),
+        _raw_stream(dev) if stream is None else _stream(stream))
     if rc != OK:
         raise PAError(rc, "pa_decode_q4")
     return out
