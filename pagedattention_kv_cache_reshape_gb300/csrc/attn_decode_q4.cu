@@ -214,6 +214,11 @@ __device__ __forceinline__ float bf16_part(float &x) {          // the leading b
 // uniform registers and branches, beside the lanes' arithmetic.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
+// a / b of non-negative values, with 32-bit division where a allows it (a tenth of the instructions)
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+    return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // The last sequence s with prefix[s] <= t, by the warp, 33 ways a step.
 __device__ __forceinline__ int find_seq(const int64_t *prefix, int num_seqs, int64_t t, int lane) {
     int lo = 0, hi = num_seqs;
@@ -274,7 +279,7 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
     }
     const int64_t total = prefix[p.num_seqs] * VH;
     // at least a unit a warp: small batches use fewer CTAs and merge in shared memory
-    int64_t share = max((int64_t)kWarps, (total + gridDim.x - 1) / gridDim.x);
+    int64_t share = max((int64_t)kWarps, quotient(total + gridDim.x - 1, gridDim.x));
     int64_t cta0 = min(total, share * blockIdx.x), cta1 = min(total, cta0 + share);
     if (p.by_head) {
         const int s = blockIdx.x / VH, len = (int)(prefix[s + 1] - prefix[s]);
@@ -284,14 +289,14 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
         p.cuts[blockIdx.x].seq = -1;
     }
     if (cta0 == cta1) return;
-    const int64_t w0 = cta0 + (cta1 - cta0) * warp / kWarps, w1 = cta0 + (cta1 - cta0) * (warp + 1) / kWarps;
+    const int64_t w0 = cta0 + quotient((cta1 - cta0) * warp, kWarps), w1 = cta0 + quotient((cta1 - cta0) * (warp + 1), kWarps);
 
     if (w1 > w0) {
         // ---- where the warp's part begins
-        int s = uniform(find_seq(prefix, p.num_seqs, w0 / VH, lane));
+        int s = uniform(find_seq(prefix, p.num_seqs, quotient(w0, VH), lane));
         int ctx = uniform(ctxs[s]), nu = units_of(ctx, max_tokens);
         const int64_t in_seq = w0 - prefix[s] * VH;
-        int vh = uniform((int)(in_seq / length_of(nu)));
+        int vh = uniform((int)quotient(in_seq, length_of(nu)));
         const int into = uniform((int)(in_seq - (int64_t)vh * length_of(nu)));
         int u = max(0, into - kHeadCost);
         int left = uniform((int)(w1 - w0)) - max(0, kHeadCost - into);   // of the part, in stream units
@@ -415,8 +420,6 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
         };
         if (kEarly && left > 0) request_q(s, vh);
         next_stretch();
-#pragma unroll
-        for (int i = 0; i < kStages; ++i) issue();
 
         // q as B operands of the first product, pair i the dims (i, i + 4) of the lane's 8 (bf16 calls: in fp16, odd
         // pairs divided by the 16 that their codes carry); q8: three bf16 parts of -8 sum(q) of the groups
@@ -652,10 +655,11 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                 }
             }
             __syncwarp();   // every lane is done with the units' places
-#pragma unroll
-            for (int j = 0; j < NU; ++j) issue();
         };
+        int due = kStages;   // copies to set off: the units' places are free
         while (left > 0) {
+#pragma unroll 1
+            for (; due > 0; --due) issue();
             if (fresh) {
                 fresh = false;
                 u_first = u;
@@ -743,6 +747,7 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
             const int pair = left > 1 && u + 1 < nu ? 2 : 1;
             if (pair == 2) step(std::integral_constant<int, 2>());
             else step(std::integral_constant<int, 1>());
+            due = pair;
             u += pair;
             left -= pair;
             if (left > 0 && u < nu) continue;
@@ -843,97 +848,103 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
         return j & 1 ? reinterpret_cast<const float *>(smem + (j >> 1) * S::kRing)
                      : reinterpret_cast<const float *>(smem + kWarps * S::kRing) + (j >> 1) * S::kPiece;
     };
-    auto store_head = [&](int seq, int head, const float (&acc)[PER], float L) {
-        T *dst = static_cast<T *>(p.out) + ((int64_t)seq * p.num_heads + head) * D;
-        const float inv = 1.0f / L;
+    // lane j of every warp looks at piece j; a run is the pieces of one head, and (run, q-head) pairs go round the warps
+    PieceMeta mine = {-1, 0, 0, 0, 0};
+    if (lane < 2 * kWarps) mine = meta[lane];
+    const bool valid = mine.seq >= 0;
+    const uint32_t some = __ballot_sync(0xffffffffu, valid), below = some & ((1u << lane) - 1u);
+    const int prev = below ? 31 - __clz(below) : lane;
+    const int prev_seq = __shfl_sync(0xffffffffu, mine.seq, prev), prev_vh = __shfl_sync(0xffffffffu, mine.vh, prev);
+    const uint32_t starts = __ballot_sync(0xffffffffu, valid && (!below || prev_seq != mine.seq || prev_vh != mine.vh));
+    const int runs = __popc(starts), run = __popc(starts & (0xffffffffu >> (31 - lane))) - 1;
+    for (int task = warp; task < runs * p.hw; task += kWarps) {
+        const int i = task / p.hw, h = task - i * p.hw;
+        const uint32_t in = __ballot_sync(0xffffffffu, valid && run == i);
+        const int j0 = __ffs(in) - 1, j1 = 31 - __clz(in);
+        const int seq = __shfl_sync(0xffffffffu, mine.seq, j0), vh = __shfl_sync(0xffffffffu, mine.vh, j0);
+        const int u0 = __shfl_sync(0xffffffffu, mine.u0, j0), nu = __shfl_sync(0xffffffffu, mine.nu, j0);
+        const int u1 = __shfl_sync(0xffffffffu, mine.u1, j1);
+        const int part = vh % p.split, h0 = (vh / p.split) * p.group + part * p.hw;
+        if (h >= min(p.hw, p.group - part * p.hw)) continue;
+        const bool member = in >> lane & 1;
+        const float *ml = piece_of(lane < 2 * kWarps ? lane : 0) + HW * D + 2 * h;
+        const float m = member ? ml[0] : -INFINITY;
+        float M = m;
 #pragma unroll
-        for (int d = 0; d < PER; ++d) dst[d * 32 + lane] = from_float<T>(acc[d] * inv);
-    };
-    PieceMeta cut[2];   // the CTA's part of a head cut on its left, and of one cut on its right only
-    cut[0].seq = cut[1].seq = -1;
-    int task = 0;       // (head of a sequence, q-head) pairs go round the warps
-    for (int j0 = 0; j0 < 2 * kWarps;) {
-        PieceMeta a = meta[j0];
-        if (a.seq < 0) { ++j0; continue; }
-        int j1 = j0 + 1;
-        for (; j1 < 2 * kWarps; ++j1) {
-            if (meta[j1].seq < 0) continue;
-            if (meta[j1].seq != a.seq || meta[j1].vh != a.vh) break;
-            a.u1 = meta[j1].u1;
+        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        const float f = member ? fast_exp2(m - M) : 0.0f;
+        float L = member ? f * ml[1] : 0.0f, acc[PER];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+#pragma unroll
+        for (int d = 0; d < PER; ++d) acc[d] = 0.0f;
+        for (int j = j0; j <= j1; ++j) {
+            if (!(in >> j & 1)) continue;
+            const float fj = __shfl_sync(0xffffffffu, f, j);
+            const float *pc = piece_of(j) + h * D + lane;
+#pragma unroll
+            for (int d = 0; d < PER; ++d) acc[d] += fj * pc[d * 32];
         }
-        const bool whole = a.u0 == 0 && a.u1 == a.nu;
-        const int side = a.u0 == 0 ? 1 : 0;
-        if (!whole) cut[side] = a;
-        const int part = a.vh % p.split, h0 = (a.vh / p.split) * p.group + part * p.hw;
-        const int heads = min(p.hw, p.group - part * p.hw);
-        float *dst = p.part + ((int64_t)blockIdx.x * 2 + side) * S::kPiece;
-        for (int h = 0; h < heads; ++h) {
-            if (task++ % kWarps != warp) continue;
-            float M = -INFINITY, L = 0.0f, acc[PER];
+        if (u0 == 0 && u1 == nu) {
+            T *dst = static_cast<T *>(p.out) + ((int64_t)seq * p.num_heads + h0 + h) * D + lane;
+            const float inv = 1.0f / L;
 #pragma unroll
-            for (int d = 0; d < PER; ++d) acc[d] = 0.0f;
-            for (int j = j0; j < j1; ++j)
-                if (meta[j].seq >= 0) M = fmaxf(M, piece_of(j)[HW * D + 2 * h]);
-            for (int j = j0; j < j1; ++j) {
-                if (meta[j].seq < 0) continue;
-                const float *pc = piece_of(j);
-                const float f = fast_exp2(pc[HW * D + 2 * h] - M);
-                L += f * pc[HW * D + 2 * h + 1];
+            for (int d = 0; d < PER; ++d) dst[d * 32] = from_float<T>(acc[d] * inv);
+        } else {   // a head that other CTAs share: cut on its left, or on its right only
+            float *dst = p.part + ((int64_t)blockIdx.x * 2 + (u0 == 0 ? 1 : 0)) * S::kPiece;
 #pragma unroll
-                for (int d = 0; d < PER; ++d) acc[d] += f * pc[h * D + d * 32 + lane];
-            }
-            if (whole) {
-                store_head(a.seq, h0 + h, acc, L);
-            } else {
-#pragma unroll
-                for (int d = 0; d < PER; ++d) dst[h * D + d * 32 + lane] = acc[d];
-                if (lane == 0) {
-                    dst[HW * D + 2 * h] = M;
-                    dst[HW * D + 2 * h + 1] = L;
-                }
+            for (int d = 0; d < PER; ++d) dst[h * D + d * 32 + lane] = acc[d];
+            if (lane == 0) {
+                dst[HW * D + 2 * h] = M;
+                dst[HW * D + 2 * h + 1] = L;
             }
         }
-        j0 = j1;
     }
-    // the first unit of a head cut on the right only lies u1 before the end of the CTA's share
-    if (tid == 0 && cut[1].seq >= 0)
-        p.cuts[blockIdx.x] = {cut[1].seq, cut[1].vh, (int)((cta1 - cut[1].u1 + cut[1].nu - 1) / share), 0};
+    // a head cut on the right only is the last run's; its first unit lies u1 before the end of the CTA's share
+    if (warp == 0 && some) {
+        const int j0 = 31 - __clz(starts), j1 = 31 - __clz(some);
+        const int seq = __shfl_sync(0xffffffffu, mine.seq, j0), vh = __shfl_sync(0xffffffffu, mine.vh, j0);
+        const int u0 = __shfl_sync(0xffffffffu, mine.u0, j0), nu = __shfl_sync(0xffffffffu, mine.nu, j0);
+        const int u1 = __shfl_sync(0xffffffffu, mine.u1, j1);
+        if (lane == 0 && u0 == 0 && u1 < nu) {
+            const int64_t end = cta1 - u1 + nu - 1;
+            p.cuts[blockIdx.x] = {seq, vh, (int)(share >> 31 ? end / share : quotient(end, (int)share)), 0};
+        }
+    }
 }
 
-// Heads cut between CTAs: CTA c merges the pieces of the one cut at the end of the decode kernel's CTA c, in stream
-// order.
+// Heads cut between CTAs: CTA (c, h) merges the pieces of q-head h of the one cut at the end of the decode kernel's
+// CTA c, in stream order.
 template <typename T, int D, int HW>
-__global__ void __launch_bounds__(256) q4_merge_kernel(const Q4Params p) {
+__global__ void __launch_bounds__(32) q4_merge_kernel(const Q4Params p) {
     constexpr int PER = D / 32, kPiece = HW * (D + 2);
-    const int c0 = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c0 = blockIdx.x, h = blockIdx.y, lane = threadIdx.x;
     grid_dependency_wait();
     grid_dependents_launch();
     const Cut a = p.cuts[c0];
     if (a.seq < 0) return;
     const int part = a.vh % p.split, h0 = (a.vh / p.split) * p.group + part * p.hw;
-    const int heads = min(p.hw, p.group - part * p.hw);
+    if (h >= min(p.hw, p.group - part * p.hw)) return;
     // the first CTA's piece is the one cut on its right
     auto src = [&](int cta) { return p.part + ((int64_t)cta * 2 + (cta == c0 ? 1 : 0)) * kPiece; };
-    for (int h = warp; h < heads; h += 8) {
-        float M = -INFINITY, L = 0.0f, acc[PER];
+    float M = -INFINITY, L = 0.0f, acc[PER];
 #pragma unroll
-        for (int d = 0; d < PER; ++d) acc[d] = 0.0f;
-        for (int cta = c0 + lane; cta <= a.last; cta += 32) M = fmaxf(M, src(cta)[HW * D + 2 * h]);
+    for (int d = 0; d < PER; ++d) acc[d] = 0.0f;
+    for (int cta = c0 + lane; cta <= a.last; cta += 32) M = fmaxf(M, src(cta)[HW * D + 2 * h]);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-#pragma unroll 4
-        for (int cta = c0; cta <= a.last; ++cta) {
-            const float *pc = src(cta);
-            const float f = fast_exp2(pc[HW * D + 2 * h] - M);
-            L += f * pc[HW * D + 2 * h + 1];
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+#pragma unroll 2
+    for (int cta = c0; cta <= a.last; ++cta) {
+        const float *pc = src(cta);
+        const float f = fast_exp2(pc[HW * D + 2 * h] - M);
+        L += f * pc[HW * D + 2 * h + 1];
 #pragma unroll
-            for (int d = 0; d < PER; ++d) acc[d] += f * pc[h * D + d * 32 + lane];
-        }
-        T *dst = static_cast<T *>(p.out) + ((int64_t)a.seq * p.num_heads + h0 + h) * D;
-        const float inv = 1.0f / L;
-#pragma unroll
-        for (int d = 0; d < PER; ++d) dst[d * 32 + lane] = from_float<T>(acc[d] * inv);
+        for (int d = 0; d < PER; ++d) acc[d] += f * pc[h * D + d * 32 + lane];
     }
+    T *dst = static_cast<T *>(p.out) + ((int64_t)a.seq * p.num_heads + h0 + h) * D;
+    const float inv = 1.0f / L;
+#pragma unroll
+    for (int d = 0; d < PER; ++d) dst[d * 32 + lane] = from_float<T>(acc[d] * inv);
 }
 
 // q-heads a warp takes: 16 for groups above 8 (K and V codes are then turned into operands once for both
@@ -980,7 +991,7 @@ cudaError_t launch_typed(Q4Params p, const AttnArgs &a, cudaStream_t stream) {
         if ((e = set()) == cudaSuccess) e = launch_dependent(kern, dim3(grid), dim3(S::kWarps * 32), smem, stream, p);
     }
     if (e != cudaSuccess || p.by_head) return e;
-    return launch_dependent(q4_merge_kernel<T, D, S::HW>, dim3(grid), dim3(256), 0, stream, p);
+    return launch_dependent(q4_merge_kernel<T, D, S::HW>, dim3(grid, p.hw), dim3(32), 0, stream, p);
 }
 
 }  // namespace
