@@ -68,7 +68,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kMaxCtas = 512;
 constexpr int kScanSeqs = 4096;     // sequences whose prefix a CTA makes itself (48 KB of shared memory)
 constexpr int kHeadUnits = 128;     // a CTA a head: up to this many units
-constexpr int kHeadCost = 4;
+constexpr int kHeadCost = 3;
 constexpr float kMoveAt = 8.0f;     // a logit this far (base 2) over the reference moves it
 
 // A head cut at the end of CTA c (seq < 0: none): its pieces are c's second, then the first of c + 1 .. last.

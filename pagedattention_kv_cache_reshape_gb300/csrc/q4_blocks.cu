@@ -38,7 +38,7 @@ __device__ __forceinline__ void expand8(float *dst, uint32_t w, uint16_t scale) 
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         y[i] = (__uint_as_float(((w >> (4 * i)) & 15u) | 0x4b000000u) - (8388608.0f + 8.0f)) * s;
-    store8(dst, y);
+    store_raw8(dst, from_floats<float>(y));
 }
 
 // grid: (pair, part of the block).  Items of a block: [K, V][head][token][16 or 8 dims].

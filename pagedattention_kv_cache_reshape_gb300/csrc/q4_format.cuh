@@ -123,18 +123,25 @@ __device__ __forceinline__ uint32_t amax_bits8(const Raw8<float> &r) {
     }
     return a;
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
+template <typename T> __device__ __forceinline__ Raw8<T> from_floats(const float (&x)[8]);
+template <> __device__ __forceinline__ Raw8<__nv_bfloat16> from_floats<__nv_bfloat16>(const float (&x)[8]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
         w[i] = *reinterpret_cast<const uint32_t *>(&v);
     }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    return {{make_uint4(w[0], w[1], w[2], w[3])}};
 }
-__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *(reinterpret_cast<float4 *>(p) + 1) = make_float4(x[4], x[5], x[6], x[7]);
+template <> __device__ __forceinline__ Raw8<float> from_floats<float>(const float (&x)[8]) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[i]);
+    return {{make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])}};
+}
+template <typename T> __device__ __forceinline__ void store_raw8(T *p, const Raw8<T> &r) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) *(reinterpret_cast<uint4 *>(p) + i) = r.v[i];
 }
 
 // Quantises 16 values, dims 16 k .. 16 k + 15 of a token row (half a group), and
@@ -168,6 +175,43 @@ __device__ __forceinline__ void q4_store16(const Raw8<T> &lo, const Raw8<T> &hi,
         }
     }
     if (store && h == 0) scales[g] = sb;
+}
+
+// The same for the 8 values from dim 8 j and the 8 from D / 2 + 8 j, j the lane's
+// place among the D / 16 of its row (what a rotation of halves leaves a lane).
+template <int D, typename T>
+__device__ __forceinline__ void q4_store8x2(const Raw8<T> &lo, const Raw8<T> &hi, int j, bool is_v, uint8_t *row,
+                                            uint16_t *scales, bool store) {
+    constexpr int NG = D / kQ4Group;
+    uint32_t w[2];
+    uint16_t sb[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t amax = amax_bits8(i ? hi : lo);
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        sb[i] = q4_scale_bits(amax);
+        float x[8];
+        to_floats(x, i ? hi : lo);
+        w[i] = q4_word(x, q4_scale_value(sb[i]));
+    }
+    const int c = j & 3, g = j >> 2;   // g: 0 or 1 of the row's half (head_dim 64: 0)
+    if (is_v && NG == 4) {             // units r = 2 c (g = 0) or 2 c + 1 of all four groups: 8 bytes
+        const uint32_t o0 = __shfl_xor_sync(0xffffffffu, w[0], 4), o1 = __shfl_xor_sync(0xffffffffu, w[1], 4);
+        const uint2 v = g ? make_uint2(__byte_perm(o0, w[0], 0x7632), __byte_perm(o1, w[1], 0x7632))
+                          : make_uint2(__byte_perm(w[0], o0, 0x5410), __byte_perm(w[1], o1, 0x5410));
+        if (store) *reinterpret_cast<uint2 *>(row + (2 * c + g) * 8) = v;
+    } else if (is_v) {                 // units 2 c and 2 c + 1 of both groups: 8 bytes
+        if (store)
+            *reinterpret_cast<uint2 *>(row + c * 8) = make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632));
+    } else if (store) {
+        *reinterpret_cast<uint32_t *>(row + (c * NG + g) * 4) = w[0];
+        *reinterpret_cast<uint32_t *>(row + (c * NG + NG / 2 + g) * 4) = w[1];
+    }
+    if (store && c == 0) {
+        scales[g] = sb[0];
+        scales[NG / 2 + g] = sb[1];
+    }
 }
 
 }  // namespace pa

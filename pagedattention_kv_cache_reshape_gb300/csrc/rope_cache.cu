@@ -124,15 +124,40 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) 
     }
 }
 
+// The two vectors of 8 that a thread owns, turned and rounded to T.
+template <typename T>
+__device__ __forceinline__ void turn_rows(Raw8<T> &rx, Raw8<T> &ry, const RopeArgs &a, int pos, int j, bool is_q) {
+    float c[8], s[8], x[8], y[8];
+    const float *cs = a.cos_sin + (int64_t)pos * a.rot_dim + 8 * j;
+    to_floats(c, load_raw8(cs));
+    to_floats(s, load_raw8(cs + a.rot_dim / 2));
+    to_floats(x, rx);
+    to_floats(y, ry);
+    if (a.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {   // pair i is (x[2i], x[2i + 1]) or, from 4 on, y's
+            float &v = i < 4 ? x[2 * i] : y[2 * i - 8], &w = i < 4 ? x[2 * i + 1] : y[2 * i - 7];
+            turn(v, w, c[i], s[i], is_q);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) turn(x[i], y[i], c[i], s[i], is_q);
+    }
+    rx = from_floats<T>(x);
+    ry = from_floats<T>(y);
+}
+
 // One CTA per U tokens, `passes` x `rows` head rows of a token at a time, D / 16 threads a row.  Rows 0 ..
 // num_heads - 1 are queries, then keys, then values.  Thread j of a row, j < rot_dim / 16: the rotated vectors 8 j
 // and R + 8 j (halves) or 16 j and 16 j + 8 (interleaved); the others: the vectors from rot_dim on.  The rows are
-// requested before the slots and positions that decide what becomes of them.  4-bit pools: the rotated keys and
-// the values meet in shared memory, where 8 consecutive dims go to a lane.
-template <typename T, bool kQ4, int U>
+// requested before the slots and positions that decide what becomes of them.  4-bit pools, kQ4 = 1: rows that turn
+// as a whole or not at all are quantised by the lanes that hold them (a group is 2 or 4 neighbouring lanes);
+// kQ4 = 2: with rot_dim between, the rotated keys and the values meet in shared memory, where 16 consecutive dims
+// go to a lane.
+template <typename T, int kQ4, int U>
 __global__ void __launch_bounds__(kVecThreads, kQ4 || sizeof(T) == 4 ? 2 : 3) rope_cache_vec_kernel(const RopeArgs a, int rows, int passes) {
     extern __shared__ __align__(16) uint8_t smem[];
-    T *kv_s = reinterpret_cast<T *>(smem);   // [U][2 num_kv_heads][D], 4-bit pools only
+    T *kv_s = reinterpret_cast<T *>(smem);   // [U][2 num_kv_heads][D], kQ4 = 2 only
     const int D = a.head_dim, lanes = D / 16, tid = threadIdx.x;
     const int row0 = tid / lanes, j = tid - row0 * lanes, R = a.rot_dim / 2;
     const int H = a.num_heads, HK = a.num_kv_heads, all = H + 2 * HK;
@@ -176,43 +201,46 @@ __global__ void __launch_bounds__(kVecThreads, kQ4 || sizeof(T) == 4 ? 2 : 3) ro
                 }
             }
         }
-        if (!mine) continue;
+        const bool quant = kQ4 == 1 && mine && !is_q;
+        if (kQ4 == 1 ? !__any_sync(0xffffffffu, mine) : !mine) continue;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (!live[u]) continue;
+            if (!live[u]) continue;   // the same in every thread
+            if (kQ4 == 1) {
+                if (mine && turns && !is_v) turn_rows(rx[u], ry[u], a, pos[u], j, is_q);
+                if (mine && is_q) {
+                    T *dst = static_cast<T *>(a.q_out) + ((int64_t)(t0 + u) * H + h) * D;
+                    store_raw8(dst + d0, rx[u]);
+                    store_raw8(dst + d1, ry[u]);
+                }
+                if (__any_sync(0xffffffffu, quant)) {
+                    const int64_t blk = slot[u] / a.block_size;
+                    const int off = (int)(slot[u] - blk * a.block_size);
+                    const int64_t slab = q4_slab_bytes(a.block_size, D);
+                    uint8_t *to = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) + (blk * HK + (quant ? h : 0)) * slab;
+                    uint8_t *codes = to + off * q4_row_bytes(D);
+                    uint16_t *scales = reinterpret_cast<uint16_t *>(to + a.block_size * q4_row_bytes(D)) + off * (D / kQ4Group);
+                    const bool v = is_v && quant;
+                    if (a.rot_dim > 0 && !a.interleaved) {
+                        if (D == 128) q4_store8x2<128>(rx[u], ry[u], j, v, codes, scales, quant);
+                        else q4_store8x2<64>(rx[u], ry[u], j, v, codes, scales, quant);
+                    } else {
+                        if (D == 128) q4_store16<128>(rx[u], ry[u], j, v, codes, scales, quant);
+                        else q4_store16<64>(rx[u], ry[u], j, v, codes, scales, quant);
+                    }
+                }
+                continue;
+            }
             T *dst;
             if (is_q) dst = static_cast<T *>(a.q_out) + ((int64_t)(t0 + u) * H + h) * D;
-            else if (kQ4) dst = kv_s + (u * 2 * HK + row - H) * D;
+            else if (kQ4 == 2) dst = kv_s + (u * 2 * HK + row - H) * D;
             else dst = static_cast<T *>(is_v ? a.v_cache : a.k_cache) + (slot[u] * HK + h) * D;
-            if (turns && !is_v) {
-                float c[8], s[8], x[8], y[8];
-                const float *cs = a.cos_sin + (int64_t)pos[u] * a.rot_dim + 8 * j;
-                to_floats(c, load_raw8(cs));
-                to_floats(s, load_raw8(cs + R));
-                to_floats(x, rx[u]);
-                to_floats(y, ry[u]);
-                if (a.interleaved) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {   // pair i is (x[2i], x[2i + 1]) or, from 4 on, y's
-                        float &v = i < 4 ? x[2 * i] : y[2 * i - 8], &w = i < 4 ? x[2 * i + 1] : y[2 * i - 7];
-                        turn(v, w, c[i], s[i], is_q);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) turn(x[i], y[i], c[i], s[i], is_q);
-                }
-                store8(dst + d0, x);
-                store8(dst + d1, y);
-            } else {
-#pragma unroll
-                for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-                    *(reinterpret_cast<uint4 *>(dst + d0) + i) = rx[u].v[i];
-                    *(reinterpret_cast<uint4 *>(dst + d1) + i) = ry[u].v[i];
-                }
-            }
+            if (turns && !is_v) turn_rows(rx[u], ry[u], a, pos[u], j, is_q);
+            store_raw8(dst + d0, rx[u]);
+            store_raw8(dst + d1, ry[u]);
         }
     }
-    if (!kQ4) return;
+    if (kQ4 != 2) return;
     __syncthreads();
     const int per = D / 16, k = tid % per;   // a row's lanes lie in one warp: per is 4 or 8
     const int64_t slab = q4_slab_bytes(a.block_size, D);
@@ -233,7 +261,7 @@ __global__ void __launch_bounds__(kVecThreads, kQ4 || sizeof(T) == 4 ? 2 : 3) ro
     }
 }
 
-template <typename T, bool kQ4>
+template <typename T, int kQ4>
 cudaError_t launch_vec(const RopeArgs &a, int64_t kv_bytes, cudaStream_t stream) {
     const int lanes = a.head_dim / 16;
     const int64_t all = (int64_t)a.num_heads + 2 * a.num_kv_heads;
@@ -251,14 +279,16 @@ cudaError_t launch_vec(const RopeArgs &a, int64_t kv_bytes, cudaStream_t stream)
 template <typename T>
 cudaError_t launch_typed(const RopeArgs &a, bool q4, cudaStream_t stream) {
     // the fast kernel's rows come in 16-byte pieces; a token's keys and values fit shared memory
-    const int64_t kv_bytes = q4 ? (int64_t)2 * a.num_kv_heads * a.head_dim * sizeof(T) : 0;
+    const bool whole = a.rot_dim == 0 || a.rot_dim == a.head_dim;
+    const int64_t kv_bytes = q4 && !whole ? (int64_t)2 * a.num_kv_heads * a.head_dim * sizeof(T) : 0;
     auto in16 = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
     const int64_t e = sizeof(T);
     bool vec = a.head_dim % 16 == 0 && a.rot_dim % 16 == 0 && a.head_dim <= 512 && kv_bytes <= 48 * 1024 &&
                a.key_stride * e % 16 == 0 && a.value_stride * e % 16 == 0 && in16(a.key) && in16(a.value) &&
                in16(a.k_cache) && in16(a.v_cache) && (a.rot_dim == 0 || in16(a.cos_sin));
     if (a.num_heads > 0) vec = vec && a.q_stride * e % 16 == 0 && in16(a.q) && in16(a.q_out);
-    if (vec) return q4 ? launch_vec<T, true>(a, kv_bytes, stream) : launch_vec<T, false>(a, kv_bytes, stream);
+    if (vec && q4) return whole ? launch_vec<T, 1>(a, 0, stream) : launch_vec<T, 2>(a, kv_bytes, stream);
+    if (vec) return launch_vec<T, 0>(a, 0, stream);
     const dim3 grid(a.num_tokens), block(kThreads);
     return q4 ? launch_dependent(rope_cache_kernel<T, true>, grid, block, 0, stream, a)
               : launch_dependent(rope_cache_kernel<T, false>, grid, block, 0, stream, a);
