@@ -22,7 +22,10 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kVecThreads = 384;   // 3 CTAs of 56 registers an SM: 36 warps' loads in flight
+// Threads of a CTA of the fast kernel.  One token a CTA (few tokens): all rows of a usual token at once.  Two: small
+// CTAs, 16 of them with 64 registers an SM, whose loads and stores overlap (8192 tokens of 48 rows: 64 threads 34.4
+// us, 128 35.3, 192 36.9, 384 40.5).
+constexpr int vec_threads(int U) { return U == 1 ? 384 : 64; }
 
 // a c - b s (sign = -1) or a c + b s (sign = +1), the exact value rounded once to
 // fp32: both products are split into value and error (fma), the sum into value
@@ -155,7 +158,7 @@ __device__ __forceinline__ void turn_rows(Raw8<T> &rx, Raw8<T> &ry, const RopeAr
 // kQ4 = 2: with rot_dim between, the rotated keys and the values meet in shared memory, where 16 consecutive dims
 // go to a lane.
 template <typename T, int kQ4, int U>
-__global__ void __launch_bounds__(kVecThreads, kQ4 || sizeof(T) == 4 ? 2 : 3) rope_cache_vec_kernel(const RopeArgs a, int rows, int passes) {
+__global__ void __launch_bounds__(vec_threads(U), U == 1 ? 2 : 16) rope_cache_vec_kernel(const RopeArgs a, int rows, int passes) {
     extern __shared__ __align__(16) uint8_t smem[];
     T *kv_s = reinterpret_cast<T *>(smem);   // [U][2 num_kv_heads][D], kQ4 = 2 only
     const int D = a.head_dim, lanes = D / 16, tid = threadIdx.x;
@@ -265,15 +268,21 @@ template <typename T, int kQ4>
 cudaError_t launch_vec(const RopeArgs &a, int64_t kv_bytes, cudaStream_t stream) {
     const int lanes = a.head_dim / 16;
     const int64_t all = (int64_t)a.num_heads + 2 * a.num_kv_heads;
-    const int64_t passes = (all * lanes + kVecThreads - 1) / kVecThreads;
-    const int rows = (int)((all + passes - 1) / passes);
-    const dim3 block((rows * lanes + 31) / 32 * 32);
+    auto shape = [&](int threads, int &rows, int &passes) {
+        passes = (int)((all * lanes + threads - 1) / threads);
+        rows = (int)((all + passes - 1) / passes);
+        return dim3((rows * lanes + 31) / 32 * 32);
+    };
+    int rows, passes;
     // two tokens a CTA once one each would fill the GPU several times over: twice the loads in flight
-    if (a.num_tokens >= 8 * device_sm_count() && 2 * kv_bytes <= 48 * 1024)
+    if (a.num_tokens >= 8 * device_sm_count() && 2 * kv_bytes <= 48 * 1024) {
+        const dim3 block = shape(vec_threads(2), rows, passes);
         return launch_dependent(rope_cache_vec_kernel<T, kQ4, 2>, dim3((a.num_tokens + 1) / 2), block,
-                                (size_t)(2 * kv_bytes), stream, a, rows, (int)passes);
+                                (size_t)(2 * kv_bytes), stream, a, rows, passes);
+    }
+    const dim3 block = shape(vec_threads(1), rows, passes);
     return launch_dependent(rope_cache_vec_kernel<T, kQ4, 1>, dim3(a.num_tokens), block, (size_t)kv_bytes, stream, a,
-                            rows, (int)passes);
+                            rows, passes);
 }
 
 template <typename T>

@@ -105,12 +105,12 @@ def scales(pool, B, D):
 
 
 def attention(q, k, v, scale):
-    """q [H, D], k / v [n, Hkv, D] float64 -> (out, sum p |v|, largest logit magnitude sum scale |q||k|)."""
+    """q [H, D], k / v [n, Hkv, D] float64 -> (out, sum p |v|, largest sum |scale| |q||k|)."""
     H, D = q.shape
     G = H // k.shape[1]
     kk, vv = np.repeat(k, G, axis=1), np.repeat(v, G, axis=1)
     x = scale * np.einsum("hd,nhd->hn", q, kk)
-    mag = scale * np.einsum("hd,nhd->hn", np.abs(q), np.abs(kk)).max(-1)
+    mag = abs(scale) * np.einsum("hd,nhd->hn", np.abs(q), np.abs(kk)).max(-1)
     p = np.exp(x - x.max(-1, keepdims=True))
     p /= p.sum(-1, keepdims=True)
     return np.einsum("hn,nhd->hd", p, vv), np.einsum("hn,nhd->hd", p, np.abs(vv)), mag

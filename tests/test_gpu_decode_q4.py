@@ -77,18 +77,18 @@ class Case:
             # The base-2 exponential and its fp32 argument add 2^-22 each of their magnitude.
             bf16 = self.dtype == torch.bfloat16
             dx = mag * ((5 if bf16 else 1) * 16 * 2.0 ** -23 + 2.0 ** -22) + 2.0 ** -21
-            # Weights: one rounding to bf16 (2^-8 at most, the scale of V folded in before it); fp32 calls split
+            # Weights: one rounding to fp16 (2^-11 at most, the scale of V folded in before it); fp32 calls split
             # them into three bf16 parts and drop 2^-24.  Both sums round in fp32, at most one step a token block.
-            dp = 2.0 ** -8 if bf16 else 2.0 ** -24
+            dp = 2.0 ** -11 if bf16 else 2.0 ** -24
             steps = (n / 16 + 16) * 2.0 ** -23
             half = 2.0 ** -8 if bf16 else 2.0 ** -24
             extra = 0.0
             if bf16:
-                # q in two e4m3 parts, its largest element at 2^7 or more: what lies under the smallest step, 2^-9,
-                # is rounded to it, so an element is off by at most 2^-10 / 2^7 of the largest.
+                # q in fp16, its largest element at 2^14 or more and half of the elements divided by 16: what lies
+                # under the smallest step, 2^-24, is off by at most 16 * 2^-25 / 2^14 of the largest.
                 G = self.H // self.Hkv
                 ksum = np.repeat(np.abs(kr).sum(-1).max(0), G)
-                dx = dx + 2.0 ** -17 * np.abs(q[s]).max(-1) * self.scale * ksum
+                dx = dx + 2.0 ** -35 * np.abs(q[s]).max(-1) * abs(self.scale) * ksum
                 # Codes enter the second product as n too: a block of tokens is added as sum(n w s) and then
                 # -sum(8 w s), each a product whose 16 addends and sum are cut at 2^-24 of the largest, 15 w s at
                 # most: 2 * 17 * 15 * 2^-24 of sum(w s) over the sequence.
@@ -96,6 +96,9 @@ class Case:
                 x = self.scale * np.einsum("hd,nhd->hn", q[s], np.repeat(kr, G, 1))
                 w = np.exp(x - x.max(-1, keepdims=True))
                 extra = 2 * 17 * 15 * 2.0 ** -24 * np.einsum("hn,nhd->hd", w / w.sum(-1, keepdims=True), zero)
+                # A weight times a scale, the largest scale at 2^6 or more, has the fp16 step 2^-24 at least: half of
+                # it, times |n - 8| <= 8, a token; the weights' sum is 1 or more in units of the largest.
+                extra = extra + n * 8 * 2.0 ** -25 / 2.0 ** 6 * zero.max((0, 2)).reshape(-1, 1)
             rel = 2 * dx[:, None] + dp + 2 * steps
             tol = half * np.abs(ref) * (1 + rel) + rel * mean * (1 + half) + extra + 1e-30
             err = np.abs(o[s] - ref)
@@ -131,6 +134,82 @@ def test_decode_of_many_sequences(H, Hkv, D, B):
     ctx = np.concatenate([rng.integers(1, 40, 700), W.power_law_lengths(rng, 200, 1.2, 1, 1200)])
     c = Case(rng.permutation(ctx), H, Hkv, D, B, torch.bfloat16, seed=6)
     c.check(c.run(), seqs=list(range(0, 900, 7)) + [899], what="many")
+
+
+@pytest.mark.parametrize("S", [4096, 4097, 9000])
+def test_decode_of_thousands_of_sequences(S):
+    """Above 4096 sequences the prefix over the lengths is made by a kernel of its own."""
+    rng = np.random.default_rng(S)
+    ctx = rng.integers(1, 30, S)
+    ctx[S // 2] = 3000
+    c = Case(ctx, 4, 1, 64, 8, torch.bfloat16, seed=S)
+    out = c.run()
+    c.check(out, seqs=[0, 1, S // 2 - 1, S // 2, S // 2 + 1, S - 2, S - 1] + list(range(3, S, 97)), what="thousands")
+    # a sequence without a valid length among them
+    cl = c.cl.clone()
+    cl[S - 1], cl[5] = 0, -3
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = torch.full_like(out, 9.0)
+    pa.decode_q4(c.q, c.k4, c.v4, c.bt, cl, c.scale, out=got, dev_status=st)
+    assert pa.get_device_status(st) == pa.ERR_OUT_OF_RANGE
+    assert torch.all(got[[5, S - 1]] == 9.0)
+    c.check(got, seqs=[0, 4, 6, S // 2, S - 2], what="beside bad lengths")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H,Hkv,D", [(4, 1, 128), (16, 1, 64), (40, 8, 128), (18, 1, 128)])
+@pytest.mark.parametrize("pages", [128, 129])
+def test_one_cta_a_head_and_the_split_agree_with_64_bits(pages, H, Hkv, D, dtype):
+    """Tables of up to 2048 tokens and few heads take a CTA a head; one block more and the work is split."""
+    c = Case([2048, 1, 1999, 17], H, Hkv, D, 16, dtype, seed=pages + H, max_blocks=pages)
+    c.check(c.run(), what=f"{pages} pages")
+
+
+def test_heads_cut_between_many_ctas():
+    """One long sequence of one kv-head: every CTA holds a piece of the same head."""
+    for dtype, H in ((torch.bfloat16, 3), (torch.bfloat16, 12), (torch.float32, 9)):
+        c = Case([16 * 152 * 12 + 5], H, 1, 128, 16, dtype, seed=H)
+        c.check(c.run(), what=f"{H} heads")
+
+
+@pytest.mark.parametrize("H,Hkv,D,B", [(8, 2, 128, 16), (8, 1, 64, 32), (12, 1, 128, 8)])
+def test_every_length_up_to_two_blocks_of_a_step(H, Hkv, D, B):
+    c = Case(list(range(1, 70)), H, Hkv, D, B, torch.bfloat16, seed=40)
+    c.check(c.run(), what="each length")
+
+
+def test_scales_of_v_far_apart():
+    """Scales of V over forty powers of two, rising and falling along the sequence: the lift moves both ways' weights."""
+    for order in (1, -1):
+        c = Case([700], 8, 2, 128, 16, torch.bfloat16, seed=41)
+        e = torch.linspace(-20.0 * order, 20.0 * order, 700, device=DEV)
+        v = torch.randn(c.nb, 16, 2, 128, device=DEV)
+        flat = torch.ones(44 * 16, device=DEV)
+        flat[:700] = torch.exp2(e)
+        v[c.bt[0, :44].long()] *= flat.view(44, 16, 1, 1)
+        k = torch.randn(c.nb, 16, 2, 128, device=DEV)
+        ident = torch.arange(c.nb, dtype=torch.int32, device=DEV)[:, None].repeat(1, 2).contiguous()
+        pa.quantize_blocks_q4(k, v, c.k4, c.v4, ident)
+        c.check(c.run(), what=f"order {order}")
+
+
+def test_zero_queries_and_zero_scale_give_the_mean():
+    for dtype in (torch.bfloat16, torch.float32):
+        c = Case([5, 333, 16], 6, 2, 64, 16, dtype, seed=43)
+        c.q[1] = 0
+        c.check(c.run(), what="zero rows")
+        c.scale = 0.0
+        c.check(c.run(), what="zero scale")
+        c.scale = -0.3
+        c.check(c.run(), what="negative scale")
+
+
+def test_queries_of_extreme_size():
+    for factor in (2.0 ** -60, 2.0 ** 40):
+        c = Case([40, 500], 8, 2, 128, 16, torch.bfloat16, seed=44)
+        c.q *= factor
+        c.scale = 0.1 / factor
+        c.check(c.run(), what=f"q times {factor}")
 
 
 def test_long_single_sequence_and_large_logits():
