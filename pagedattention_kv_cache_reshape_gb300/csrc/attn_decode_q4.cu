@@ -11,8 +11,8 @@
 //    matrix instructions take exactly), so an AND makes two of them and one
 //    shift serves four.  Scales are never multiplied into elements, and the 8
 //    in n - 8 is taken off sums, not off elements.  (e4m3 operands would take
-//    a nibble too, but that mma.sync is itself made of conversions and fp16
-//    products: 187 us where fp16 takes FP16TIME, 16 x 32768 tokens.)
+//    a nibble as well, but that mma.sync is itself made of conversions and
+//    fp16 products: 16 x 32768 tokens took 187 us with it, 151 us with fp16.)
 //  * S = K Q^T (tokens in M, q-heads in N, m16n8k16): q in fp16 times a power of
 //    two per head that brings its largest element into [2^14, 2^15): exact
 //    down to 2^-31 of the largest.  The group's scale is applied to the 4 sums
@@ -67,7 +67,6 @@ constexpr int kStages = 4;
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxCtas = 512;
 constexpr int kScanSeqs = 4096;     // sequences whose prefix a CTA makes itself (48 KB of shared memory)
-constexpr int kHeadUnits = 128;     // a CTA a head: up to this many units
 constexpr int kHeadCost = 3;
 constexpr float kMoveAt = 8.0f;     // a logit this far (base 2) over the reference moves it
 
@@ -452,7 +451,7 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                 at[j] = st;
                 st = st + S::kStage == ring + S::kRing ? ring : st + S::kStage;
             }
-            const int valid = ctx - (u + NU - 1) * kU;      // tokens of the last unit that exist
+            const int valid = ctx - u * kU - (NU - 1) * kU;   // tokens of the last unit that exist
             constexpr int L = NU - 1;
 
             // ---- S = K Q^T
@@ -976,8 +975,11 @@ cudaError_t launch_typed(Q4Params p, const AttnArgs &a, cudaStream_t stream) {
     const int sms = min(kMaxCtas, device_sm_count()), max_tokens = a.max_blocks * a.block_size;
     const int64_t heads = (int64_t)a.num_seqs * a.num_kv_heads * p.split;
     p.scan = a.num_seqs <= kScanSeqs;
-    // one CTA a head: nothing is cut between CTAs.  Beyond kHeadUnits units a head the split over all SMs is faster
-    p.by_head = heads <= sms && max_tokens <= kHeadUnits * kU;
+    // One CTA a head: one launch, and nothing is cut between CTAs.  The split over all SMs costs its second kernel,
+    // some 3 us, and gains the more the fewer heads there are: 8 heads of 512 tokens take 8.0 us this way and 9.5
+    // split, of 1024 10.2 and 10.1, of 2048 14.1 and 11.2; 128 heads of 2048 tokens 14.7 and 16.5, of 4096 22.5 and
+    // 23.1.
+    p.by_head = heads <= sms && max_tokens <= kU * (64 + 128 * heads / sms);
     const int grid = p.by_head ? (int)heads : sms;
     const size_t smem = S::kSmem + (p.scan ? (size_t)(a.num_seqs + 2) * 12 : 0);
     if (!p.scan) {

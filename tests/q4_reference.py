@@ -89,8 +89,8 @@ def values(pool, kind, B, D):
     codes = raw[:, :, :B * D // 2].reshape(n, H, B, D // 2)
     nib = np.stack([codes & 15, codes >> 4], -1).reshape(n, H, B, D)[..., _nibble(kind, D)]
     bits = np.ascontiguousarray(raw[:, :, B * D // 2:]).view("<u2").reshape(n, H, B, D // GROUP)
-    s = (bits.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
     with np.errstate(all="ignore"):
+        s = (bits.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
         v = (nib.astype(np.float64) - 8).reshape(n, H, B, D // GROUP, GROUP) * s[..., None]
     return v.reshape(n, H, B, D).transpose(0, 2, 1, 3)
 
