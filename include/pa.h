@@ -294,8 +294,8 @@ PA_API pa_status pa_rope_and_cache(void *q_out, const void *q, const void *key, 
  * head_dim / 2 code bytes, then B rows of head_dim / 32 bf16 scales.  A group
  * is 32 consecutive dims of one token and kv-head; with amax its largest
  * magnitude,
- *     s = bf16(amax / 7),  n = 8 + clamp(rint(x / s), -7, 7)  (n = 8 when s = 0),
- * fp32 division, ties to even; nibble n stands for (n - 8) s.  A group with a
+ *     s = bf16(amax * fp32(1/7)),  n = 8 + clamp(rint(x / s), -7, 7)  (n = 8 when s = 0),
+ * in fp32, the quotient correctly rounded, ties to even; nibble n stands for (n - 8) s.  A group with a
  * NaN or an infinity takes a NaN scale and reads back as NaN.  Byte layout of
  * a row (low nibble first, NG = head_dim / 32 groups):
  *     K pool  32-bit words [4][NG], word (c, g): dims 32 g + 8 c .. + 7;

@@ -632,14 +632,22 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                         // the only rounding of a weight: p times V's scale, to fp16 (fp32 calls: three bf16 parts)
                         float y[4] = {x[j][nt][0] * s0, x[j][nt][1] * s0, x[j][nt][2] * s1, x[j][nt][3] * s1};
                         if constexpr (S::kF32) {
+                            // summed apart and added with rounding: the matrix sum cuts, and over a long sequence
+                            // its cuts would all point one way
+                            float u0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                             for (int k = 0; k < NS; ++k) {
                                 const float y0 = bf16_part(y[0]), y1 = bf16_part(y[1]);
                                 const float y2 = bf16_part(y[2]), y3 = bf16_part(y[3]);
                                 const uint32_t b0 = movmatrix_trans(pack_bf16x2(y0, y1));
                                 const uint32_t b1 = movmatrix_trans(pack_bf16x2(y2, y3));
-                                mma_bf16_16816(o[nt][2 * g], a[0][0], a[1][0], a[0][1], a[1][1], b0, b1);
-                                mma_bf16_16816(o[nt][2 * g + 1], a[2][0], a[3][0], a[2][1], a[3][1], b0, b1);
+                                mma_bf16_16816(u0, a[0][0], a[1][0], a[0][1], a[1][1], b0, b1);
+                                mma_bf16_16816(u1, a[2][0], a[3][0], a[2][1], a[3][1], b0, b1);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                o[nt][2 * g][e] += u0[e];
+                                o[nt][2 * g + 1][e] += u1[e];
                             }
                         } else {
                             const uint32_t b0 = movmatrix_trans(pack_f16x2(y[0], y[1]));

@@ -5,7 +5,7 @@
 // kv-head: B token rows of D / 2 code bytes, then B rows of D / 32 bf16
 // scales (9 bits per two values: 4.5 bits a value).  A group is 32 consecutive
 // dims of one row; with amax = max |x| over the group,
-//     s = bf16(amax / 7),  n = 8 + clamp(rint(x / s), -7, 7),  value (n - 8) s.
+//     s = bf16(amax fp32(1/7)),  n = 8 + clamp(rint(x / s), -7, 7),  value (n - 8) s.
 // A token's bytes are its own (no byte is shared by two tokens), so tokens of
 // one block can be written by different calls or threads.  A slab keeps one
 // (block, head) contiguous: a decode warp reads it with full-line loads, and
@@ -38,19 +38,9 @@ __host__ __device__ constexpr int q4_k_word(int dim, int d) {
 // Bits of the scale of a group from the bits of its largest magnitude.  NaN and
 // infinities have the largest bit patterns, so a group that holds one is found
 // by the same integer maximum; it takes a NaN scale and reads back as NaN.
-// amax / 7 is the correctly rounded quotient, as in q4_word.
 __device__ __forceinline__ uint16_t q4_scale_bits(uint32_t amax_bits) {
-    const float amax = __uint_as_float(amax_bits);
-    float s;
-    if (amax_bits - 0x0d000000u < 0x7f800000u - 0x0d000000u) {   // 2^-101 <= amax < inf
-        constexpr float r = 1.0f / 7.0f;
-        const float q0 = __fmul_rn(amax, r);
-        s = __fmaf_rn(__fmaf_rn(-q0, 7.0f, amax), r, q0);
-    } else {
-        if (amax_bits >= 0x7f800000u) return 0x7fc0u;
-        s = __fdiv_rn(amax, 7.0f);
-    }
-    return __bfloat16_as_ushort(__float2bfloat16_rn(s));
+    if (amax_bits >= 0x7f800000u) return 0x7fc0u;
+    return __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(__uint_as_float(amax_bits), 1.0f / 7.0f)));
 }
 __device__ __forceinline__ float q4_scale_value(uint16_t bits) {
     return __uint_as_float((uint32_t)bits << 16);

@@ -53,7 +53,7 @@ def quantize(rows):
     g = x.reshape(*x.shape[:-1], -1, GROUP)
     with np.errstate(all="ignore"):
         amax = np.abs(g).max(-1)
-        bits = bf16_bits(amax / np.float32(7))
+        bits = bf16_bits(amax * (np.float32(1) / np.float32(7)))
         bad = ~np.isfinite(g).all(-1)
         bits = np.where(bad, np.uint16(0x7fc0), bits)
         s = (bits.astype(np.uint32) << 16).view(np.float32)[..., None]
