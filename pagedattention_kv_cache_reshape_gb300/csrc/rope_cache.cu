@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(vec_threads(U), U == 1 ? 2 : 16) rope_cache_ve
     const int d0 = turns ? (a.interleaved ? 16 * j : 8 * j) : 16 * j;
     const int d1 = turns && !a.interleaved ? R + 8 * j : d0 + 8;
     const int t0 = blockIdx.x * U;
+    const int log2b = 31 - __clz(a.block_size);   // 4-bit pools: 8, 16 or 32
     grid_dependency_wait();
     grid_dependents_launch();
     int64_t slot[U];
@@ -217,8 +218,8 @@ __global__ void __launch_bounds__(vec_threads(U), U == 1 ? 2 : 16) rope_cache_ve
                     store_raw8(dst + d1, ry[u]);
                 }
                 if (__any_sync(0xffffffffu, quant)) {
-                    const int64_t blk = slot[u] / a.block_size;
-                    const int off = (int)(slot[u] - blk * a.block_size);
+                    const int64_t blk = slot[u] >> log2b;
+                    const int off = (int)slot[u] & (a.block_size - 1);
                     const int64_t slab = q4_slab_bytes(a.block_size, D);
                     uint8_t *to = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) + (blk * HK + (quant ? h : 0)) * slab;
                     uint8_t *codes = to + off * q4_row_bytes(D);
@@ -252,8 +253,8 @@ __global__ void __launch_bounds__(vec_threads(U), U == 1 ? 2 : 16) rope_cache_ve
         const int r = r0 + tid / per, u = U > 1 && r >= 2 * HK ? 1 : 0, row = r - u * 2 * HK;
         const int64_t sl = U > 1 && u ? slot[U - 1] : slot[0];
         const bool in = r < U * 2 * HK && (U > 1 && u ? live[U - 1] : live[0]), is_v = in && row >= HK;
-        const int64_t blk = in ? sl / a.block_size : 0;
-        const int off = in ? (int)(sl - blk * a.block_size) : 0;
+        const int64_t blk = in ? sl >> log2b : 0;
+        const int off = in ? (int)sl & (a.block_size - 1) : 0;
         const T *src = kv_s + (in ? r : 0) * D + 16 * k;
         uint8_t *to = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) +
                       (blk * HK + (in ? row - (is_v ? HK : 0) : 0)) * slab;
