@@ -929,11 +929,13 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
 }
 
 // Heads cut between CTAs: CTA (c, h) merges the pieces of q-head h of the one cut at the end of the decode kernel's
-// CTA c, in stream order.
+// CTA c.  Warp w adds pieces w, w + 4, ... and the four sums are added in order, so the order is fixed.
+constexpr int kMergeWarps = 4;
 template <typename T, int D, int HW>
-__global__ void __launch_bounds__(32) q4_merge_kernel(const Q4Params p) {
+__global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(const Q4Params p) {
     constexpr int PER = D / 32, kPiece = HW * (D + 2);
-    const int c0 = blockIdx.x, h = blockIdx.y, lane = threadIdx.x;
+    __shared__ float sum_s[kMergeWarps][D + 1];
+    const int c0 = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
     grid_dependents_launch();
     const Cut a = p.cuts[c0];
@@ -948,18 +950,37 @@ __global__ void __launch_bounds__(32) q4_merge_kernel(const Q4Params p) {
     for (int cta = c0 + lane; cta <= a.last; cta += 32) M = fmaxf(M, src(cta)[HW * D + 2 * h]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-#pragma unroll 2
-    for (int cta = c0; cta <= a.last; ++cta) {
-        const float *pc = src(cta);
-        const float f = fast_exp2(pc[HW * D + 2 * h] - M);
-        L += f * pc[HW * D + 2 * h + 1];
+    for (int base = c0 + warp; base <= a.last; base += 32 * kMergeWarps) {   // lane i: the warp's i-th piece from here
+        const int cta = base + lane * kMergeWarps, n = min(32, (a.last - base) / kMergeWarps + 1);
+        float f = 0.0f;
+        if (lane < n) {
+            f = fast_exp2(src(cta)[HW * D + 2 * h] - M);
+            L += f * src(cta)[HW * D + 2 * h + 1];
+        }
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float fi = __shfl_sync(0xffffffffu, f, i);
+            const float *pc = src(base + i * kMergeWarps) + h * D + lane;
 #pragma unroll
-        for (int d = 0; d < PER; ++d) acc[d] += f * pc[h * D + d * 32 + lane];
+            for (int d = 0; d < PER; ++d) acc[d] += fi * pc[d * 32];
+        }
     }
-    T *dst = static_cast<T *>(p.out) + ((int64_t)a.seq * p.num_heads + h0 + h) * D;
-    const float inv = 1.0f / L;
 #pragma unroll
-    for (int d = 0; d < PER; ++d) dst[d * 32 + lane] = from_float<T>(acc[d] * inv);
+    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+#pragma unroll
+    for (int d = 0; d < PER; ++d) sum_s[warp][d * 32 + lane] = acc[d];
+    if (lane == 0) sum_s[warp][D] = L;
+    __syncthreads();
+    T *dst = static_cast<T *>(p.out) + ((int64_t)a.seq * p.num_heads + h0 + h) * D;
+    for (int d = threadIdx.x; d < D; d += kMergeWarps * 32) {
+        float o = 0.0f, l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) {
+            o += sum_s[w][d];
+            l += sum_s[w][D];
+        }
+        dst[d] = from_float<T>(o * (1.0f / l));
+    }
 }
 
 // q-heads a warp takes: 16 for groups above 8 (K and V codes are then turned into operands once for both
@@ -1009,7 +1030,7 @@ cudaError_t launch_typed(Q4Params p, const AttnArgs &a, cudaStream_t stream) {
         if ((e = set()) == cudaSuccess) e = launch_dependent(kern, dim3(grid), dim3(S::kWarps * 32), smem, stream, p);
     }
     if (e != cudaSuccess || p.by_head) return e;
-    return launch_dependent(q4_merge_kernel<T, D, S::HW>, dim3(grid, p.hw), dim3(32), 0, stream, p);
+    return launch_dependent(q4_merge_kernel<T, D, S::HW>, dim3(grid, p.hw), dim3(kMergeWarps * 32), 0, stream, p);
 }
 
 }  // namespace
