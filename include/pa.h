@@ -360,11 +360,15 @@ PA_API size_t pa_decode_q4_workspace_size(int num_seqs, int num_heads, int num_k
 /*
  * Paged decode attention over 4-bit pools: pa_decode with K and V the values
  * that the pools' codes and scales stand for.  Arguments, GQA mapping, error
- * behaviour and workspace rules as pa_decode's; `dtype` is that of q and out
- * (fp32 accumulation and softmax for both; with F32 the products are fp32 to
- * the last few bits, with BF16 the softmax weights enter the second product
- * in bf16 as in pa_decode).  Deterministic: results depend on the inputs and
- * the device's SM count, never on which blocks hold the data.
+ * behaviour and workspace rules as pa_decode's (calls that may overlap on the
+ * GPU take workspaces of their own); `dtype` is that of q and out.  Sums and
+ * softmax are fp32.  With BF16 a weight times its scale of V is rounded to
+ * fp16 under a power of two that follows the largest scale of the sequence so
+ * far, so what lies 2^-21 under that keeps fewer bits; with F32 the products
+ * are fp32 to the last few bits.  A NaN in q, or a NaN scale in a visible row,
+ * stays in the heads (for a scale of V: the 32 dims) it belongs to.
+ * Deterministic: results depend on the inputs and the device's SM count,
+ * never on which blocks hold the data.
  *  k_cache, v_cache  4-bit pools, 16-byte aligned
  */
 PA_API pa_status pa_decode_q4(void *out, const void *q, const void *k_cache, const void *v_cache,

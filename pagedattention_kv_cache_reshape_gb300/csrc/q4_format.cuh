@@ -186,8 +186,9 @@ __device__ __forceinline__ void q4_store8x2(const Raw8<T> &lo, const Raw8<T> &hi
         w[i] = q4_word(x, q4_scale_value(sb[i]));
     }
     const int c = j & 3, g = j >> 2;   // g: 0 or 1 of the row's half (head_dim 64: 0)
+    // (a warp may hold rows of K and of V: every lane takes part in the exchange)
+    const uint32_t o0 = __shfl_xor_sync(0xffffffffu, w[0], 4), o1 = __shfl_xor_sync(0xffffffffu, w[1], 4);
     if (is_v && NG == 4) {             // units r = 2 c (g = 0) or 2 c + 1 of all four groups: 8 bytes
-        const uint32_t o0 = __shfl_xor_sync(0xffffffffu, w[0], 4), o1 = __shfl_xor_sync(0xffffffffu, w[1], 4);
         const uint2 v = g ? make_uint2(__byte_perm(o0, w[0], 0x7632), __byte_perm(o1, w[1], 0x7632))
                           : make_uint2(__byte_perm(w[0], o0, 0x5410), __byte_perm(w[1], o1, 0x5410));
         if (store) *reinterpret_cast<uint2 *>(row + (2 * c + g) * 8) = v;

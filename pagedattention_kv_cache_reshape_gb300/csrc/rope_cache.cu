@@ -93,9 +93,11 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) 
         const int R = a.rot_dim / 2;
         if (a.interleaved ? (d & 1) : d >= R) continue;
         const int o = a.interleaved ? d + 1 : d + R;
-        const float y0 = rotated(a, row, cs, d), y1 = rotated(a, row, cs, o);
-        out[d] = from_float<T>(y0);
-        out[o] = from_float<T>(y1);
+        const int i = a.interleaved ? d >> 1 : d;
+        float x = to_float(row[d]), y = to_float(row[o]);
+        turn(x, y, cs[i], cs[R + i], true);
+        out[d] = from_float<T>(x);
+        out[o] = from_float<T>(y);
     }
     const T *key = static_cast<const T *>(a.key) + t * a.key_stride;
     const T *value = static_cast<const T *>(a.value) + t * a.value_stride;

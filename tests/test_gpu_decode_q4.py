@@ -308,6 +308,31 @@ def test_nan_in_visible_rows_stays_in_its_head():
     assert torch.equal(out[0, :2], ref[0, :2]) and torch.all(torch.isnan(out[0, 2:].float()))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_nan_and_infinity_in_a_query_stay_in_its_head(dtype):
+    c = Case([300, 33], 6, 2, 128, 16, dtype, seed=45)
+    ref = c.run()
+    c.q[0, 1, 7] = float("nan")
+    c.q[1, 4, 100] = float("inf")
+    out = c.run()
+    bad = torch.zeros(2, 6, dtype=torch.bool, device=DEV)
+    bad[0, 1] = bad[1, 4] = True
+    assert torch.equal(out[~bad], ref[~bad]) and not torch.isfinite(out[bad].float()).any()
+
+
+def test_nan_scale_of_v_stays_in_its_dims():
+    c = Case([90], 4, 2, 128, 16, torch.bfloat16, seed=46)
+    ref = c.run()
+    B, D = 16, 128
+    at = B * D // 2 + 3 * (D // 16) + 2 * 2            # token 3, group 2
+    c.v4[int(c.bt[0, 2]), 0, at:at + 2] = 0xff
+    out = c.run()
+    assert torch.equal(out[0, 2:], ref[0, 2:]) and torch.isnan(out[0, :2, 64:96].float()).all()
+    other = torch.cat([out[0, :2, :64], out[0, :2, 96:]], 1).float()
+    want = torch.cat([ref[0, :2, :64], ref[0, :2, 96:]], 1).float()
+    assert torch.allclose(other, want, rtol=2.0 ** -7, atol=1e-3)   # the lift may differ: roundings of weights and result
+
+
 def test_workspace_contents_do_not_matter_and_calls_may_share_it_in_order():
     a = Case([700, 20, 5, 3000], 8, 2, 128, 16, torch.bfloat16, seed=19)
     b = Case([9, 4000], 32, 8, 128, 16, torch.bfloat16, seed=20)
@@ -357,6 +382,22 @@ def test_two_streams_with_workspaces_of_their_own():
     torch.cuda.synchronize()
     for o, r in zip(outs, refs):
         assert torch.equal(o, r)
+
+
+def test_blocks_past_32_bits_of_bytes():
+    """Pools of more than 4 GiB: the same blocks at both ends give the same bits."""
+    for B, H, Hkv, D, dtype in ((16, 32, 8, 128, torch.bfloat16), (8, 6, 6, 64, torch.float32)):
+        c = Case([100, 7, 333], H, Hkv, D, B, dtype, seed=47)
+        ref = c.run()
+        per = c.k4[0].numel()
+        nb = (4 << 30) // per + 2 * c.nb
+        far = nb - c.nb
+        for name in ("k4", "v4"):
+            pool = torch.zeros(nb, *getattr(c, name).shape[1:], dtype=torch.uint8, device=DEV)
+            pool[far:] = getattr(c, name)
+            setattr(c, name, pool)
+        out = c.run(bt=torch.where(c.bt >= 0, c.bt + far, c.bt).int())
+        assert far * per > 1 << 32 and torch.equal(out, ref)
 
 
 def test_no_sequences():

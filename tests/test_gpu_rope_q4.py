@@ -180,6 +180,109 @@ def test_rope_into_4_bit_pools_equals_rope_then_quantize(shape, dtype):
     assert np.array_equal(a[s], b[s], equal_nan=True)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("q4,H,Hkv,D,rot,inter", [
+    (False, 32, 8, 128, 128, False), (False, 5, 3, 96, 64, True), (True, 32, 8, 128, 128, False),
+    (True, 7, 3, 64, 64, False), (True, 4, 4, 128, 128, True), (True, 6, 2, 64, 0, False), (True, 8, 2, 128, 64, False),
+    (True, 3, 1, 64, 32, True), (True, 0, 5, 128, 128, False)])
+def test_long_batches_equal_short_ones(q4, H, Hkv, D, rot, inter, dtype):
+    """1301 tokens at once (two a CTA) against the same tokens in calls of 100 (one a CTA), with padding, a bad slot
+    and a bad position among them: every byte."""
+    n, B = 1301, 16
+    q, k, v = inputs(n, H, Hkv, D, dtype, "fused", 51)
+    nb, slots, pos, tab = make_case(n, H, Hkv, D, rot, B, 52, max_pos=3000)
+    slots[[0, 17, 640, 641, n - 1]] = -1
+    slots[33] = nb * B
+    if rot:
+        pos[[50, 900]] = torch.tensor([-7, 3000], dtype=torch.int32, device=DEV)
+    fn = pa.rope_and_cache_q4 if q4 else pa.rope_and_cache
+
+    def run(step):
+        if q4:
+            kc, vc = R.new_pool(nb, B, Hkv, D, DEV, seed=1), R.new_pool(nb, B, Hkv, D, DEV, seed=2)
+        else:
+            kc, vc = (torch.full((nb, B, Hkv, D), 5.0, dtype=dtype, device=DEV) for _ in "kv")
+        out = torch.full((n, H, D), 9.0, dtype=dtype, device=DEV) if H else None
+        st = torch.zeros(1, dtype=torch.int32, device=DEV)
+        for i in range(0, n, step):
+            j = slice(i, i + step)
+            fn(q[j] if H else None, k[j], v[j], tab if rot else None, pos[j] if rot else None, kc, vc, slots[j],
+               interleaved=inter, q_out=out[j] if H else None, dev_status=st)
+        assert pa.get_device_status(st) == pa.ERR_OUT_OF_RANGE
+        return [t.contiguous().view(torch.uint8) for t in (kc, vc, out) if t is not None]
+    for a, b in zip(run(n), run(100)):
+        assert torch.equal(a, b)
+
+
+def test_keys_and_values_of_wide_rows():
+    """More K/V heads than a CTA's shared memory or one pass of its threads holds."""
+    n, H, Hkv, D, B = 3, 150, 75, 128, 16
+    q, k, v = inputs(n, H, Hkv, D, torch.float32, "plain", 61)
+    nb, slots, pos, tab = make_case(n, H, Hkv, D, 64, B, 62)
+    for rot in (0, 64, 128):
+        tab = R.table(5000, rot).to(DEV) if rot else None
+        k4, v4 = R.new_pool(nb, B, Hkv, D, DEV, fill=0), R.new_pool(nb, B, Hkv, D, DEV, fill=0)
+        out4 = pa.rope_and_cache_q4(q, k, v, tab, pos if rot else None, k4, v4, slots)
+        kc = torch.zeros(nb, B, Hkv, D, device=DEV)
+        vc = torch.zeros_like(kc)
+        out = pa.rope_and_cache(q, k, v, tab, pos if rot else None, kc, vc, slots)
+        assert torch.equal(out, out4)
+        k8, v8 = R.new_pool(nb, B, Hkv, D, DEV, fill=0), R.new_pool(nb, B, Hkv, D, DEV, fill=0)
+        pairs = torch.arange(nb, dtype=torch.int32, device=DEV)[:, None].repeat(1, 2).contiguous()
+        pa.quantize_blocks_q4(kc, vc, k8, v8, pairs)
+        s = slots.cpu().numpy()
+        for a, b, kind in ((k4, k8, "k"), (v4, v8, "v")):
+            assert np.array_equal(R.values(a, kind, B, D).reshape(-1, Hkv, D)[s], R.values(b, kind, B, D).reshape(-1, Hkv, D)[s])
+
+
+def test_a_captured_step_follows_its_buffers():
+    """Slot mapping, rotation with append, 4-bit decode and expansion in one graph, replayed with other tokens."""
+    H, Hkv, D, B, S, mb = 8, 2, 128, 16, 3, 4
+    nb = S * mb
+    g = torch.Generator().manual_seed(70)
+    bt = torch.randperm(nb, generator=g).int().view(S, mb).to(DEV)
+    tab = R.table(64, D).to(DEV)
+    qkv = torch.empty(S, (H + 2 * Hkv) * D, dtype=torch.bfloat16, device=DEV)
+    q, k, v = (t.unflatten(1, (-1, D)) for t in qkv.split([H * D, Hkv * D, Hkv * D], 1))
+    start = torch.zeros(S, dtype=torch.int32, device=DEV)
+    ctx = torch.ones(S, dtype=torch.int32, device=DEV)
+    cu = torch.arange(S + 1, dtype=torch.int32, device=DEV)
+    slots = torch.zeros(S, dtype=torch.int64, device=DEV)
+    back = torch.stack([bt.flatten(), torch.arange(nb, device=DEV).int()], 1).contiguous()
+    ws = torch.empty(pa.decode_q4_workspace_size(S, H, Hkv, D, B, mb), dtype=torch.uint8, device=DEV)
+
+    def state():
+        return dict(k4=R.new_pool(nb, B, Hkv, D, DEV, fill=0), v4=R.new_pool(nb, B, Hkv, D, DEV, fill=0),
+                    qo=torch.zeros(S, H, D, dtype=torch.bfloat16, device=DEV), out=torch.zeros(S, H, D, dtype=torch.bfloat16, device=DEV),
+                    wk=torch.zeros(nb, B, Hkv, D, dtype=torch.bfloat16, device=DEV), wv=torch.zeros(nb, B, Hkv, D, dtype=torch.bfloat16, device=DEV))
+
+    def step(z):
+        pa.compute_slot_mapping(bt, start, cu, nb, S, slot_mapping=slots)
+        pa.rope_and_cache_q4(q, k, v, tab, start, z["k4"], z["v4"], slots, q_out=z["qo"])
+        pa.decode_q4(z["qo"], z["k4"], z["v4"], bt, ctx, 0.09, out=z["out"], workspace=ws)
+        pa.dequantize_blocks_q4(z["k4"], z["v4"], z["wk"], z["wv"], back)
+    a, b = state(), state()
+    step(a)
+    a = state()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s), torch.cuda.graph(graph, stream=s):
+        step(a)
+    torch.cuda.synchronize()
+    for t in range(40):
+        qkv.copy_(torch.randn(qkv.shape, generator=g).to(DEV))
+        start.fill_(t)
+        ctx.fill_(t + 1)
+        graph.replay()
+        torch.cuda.synchronize()
+        step(b)
+        torch.cuda.synchronize()
+        assert torch.isfinite(a["out"].float()).all()
+        for name in a:
+            assert torch.equal(a[name].view(torch.uint8), b[name].view(torch.uint8)), (t, name)
+
+
 def rows_with_edges(n, B, H, D, dtype, seed):
     g = torch.Generator().manual_seed(seed)
     x = torch.randn(n, B, H, D, generator=g) * torch.exp(2 * torch.randn(n, B, H, 1, generator=g))
