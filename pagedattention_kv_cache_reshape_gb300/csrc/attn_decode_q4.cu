@@ -45,8 +45,8 @@
 // memory), then, where a CTA boundary cuts a head, by a second small kernel
 // (workspace), always in stream order, so results do not depend on timing.  Every CTA finds its share by itself, from a prefix sum over the
 // lengths in shared memory; only batches of more than kScanSeqs sequences
-// have it made by a kernel of its own.  A batch of few heads over short tables
-// takes a CTA a head and needs neither.
+// have it made by a kernel of its own.  Over short tables a CTA takes whole
+// heads, one or several, and there is no second kernel.
 //
 // Measured (32 / 8 heads of 128, blocks of 16): 256 power-law sequences, 151 MB,
 // 40.3 us; 16 x 32768 tokens, 604 MB, 117 us = 5.2 TB/s, 0.77 of the copy peak,
@@ -91,6 +91,7 @@ struct Q4Params {
     float *part;               // [CTAs][2][heads][D + 2]
     int scan;                  // the CTAs make the prefix themselves
     int by_head;               // CTA i takes head i
+    int whole;                 // the CTAs' shares end between heads
     int num_seqs, num_heads, num_kv_heads;
     int group;                 // q-heads per kv-head
     int split;                 // parts a group is split into
@@ -266,6 +267,7 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ PieceMeta meta[2 * kWarps];
     __shared__ int64_t warp_tot[kWarps];
+    __shared__ int64_t share_s[3];   // of the stream: from, to, and a CTA's usual length
     const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5), r = lane >> 2, c = lane & 3;
     uint8_t *ring = smem + warp * S::kRing;
     float *first_piece = reinterpret_cast<float *>(smem + kWarps * S::kRing) + warp * S::kPiece;
@@ -284,17 +286,37 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
         prefix = pre;
         ctxs = cx;
     }
-    const int64_t total = prefix[p.num_seqs] * VH;
-    // at least a unit a warp: small batches use fewer CTAs and merge in shared memory
-    int64_t share = max((int64_t)kWarps, quotient(total + gridDim.x - 1, gridDim.x));
-    int64_t cta0 = min(total, share * blockIdx.x), cta1 = min(total, cta0 + share);
-    if (p.by_head) {
-        const int s = blockIdx.x / VH, len = (int)(prefix[s + 1] - prefix[s]);
-        cta0 = prefix[s] * VH + (int64_t)(blockIdx.x - s * VH) * len;
-        cta1 = cta0 + len;
-    } else if (tid == 0) {
-        p.cuts[blockIdx.x].seq = -1;
+    if (warp == 0) {   // the CTA's share of the stream
+        const int64_t total = prefix[p.num_seqs] * VH;
+        // at least a unit a warp: small batches use fewer CTAs and merge in shared memory
+        const int64_t share = max((int64_t)kWarps, quotient(total + gridDim.x - 1, gridDim.x));
+        int64_t from = min(total, share * blockIdx.x), to = min(total, from + share);
+        if (p.by_head) {
+            const int s = blockIdx.x / VH, len = (int)(prefix[s + 1] - prefix[s]);
+            from = prefix[s] * VH + (int64_t)(blockIdx.x - s * VH) * len;
+            to = from + len;
+        } else if (p.whole) {   // up to the next head's beginning
+#pragma unroll 1
+            for (int end = 0; end < 2; ++end) {
+                int64_t x = end ? to : from;
+                if (x < total) {
+                    const int s = find_seq(prefix, p.num_seqs, quotient(x, VH), lane);
+                    const int len = (int)(prefix[s + 1] - prefix[s]);
+                    x = prefix[s] * VH + quotient(x - prefix[s] * VH + len - 1, len) * len;
+                }
+                (end ? to : from) = x;
+            }
+        } else if (lane == 0) {
+            p.cuts[blockIdx.x].seq = -1;
+        }
+        if (lane == 0) {
+            share_s[0] = from;
+            share_s[1] = to;
+            share_s[2] = share;
+        }
     }
+    __syncthreads();
+    const int64_t cta0 = share_s[0], cta1 = share_s[1];
     if (cta0 == cta1) return;
     const int64_t w0 = cta0 + quotient((cta1 - cta0) * warp, kWarps), w1 = cta0 + quotient((cta1 - cta0) * (warp + 1), kWarps);
 
@@ -922,7 +944,7 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
         const int u0 = __shfl_sync(0xffffffffu, mine.u0, j0), nu = __shfl_sync(0xffffffffu, mine.nu, j0);
         const int u1 = __shfl_sync(0xffffffffu, mine.u1, j1);
         if (lane == 0 && u0 == 0 && u1 < nu) {
-            const int64_t end = cta1 - u1 + nu - 1;
+            const int64_t end = share_s[1] - u1 + nu - 1, share = share_s[2];
             p.cuts[blockIdx.x] = {seq, vh, (int)(share >> 31 ? end / share : quotient(end, (int)share)), 0};
         }
     }
@@ -1017,6 +1039,10 @@ cudaError_t launch_typed(Q4Params p, const AttnArgs &a, cudaStream_t stream) {
     // split, of 1024 10.2 and 10.1, of 2048 14.1 and 11.2; 128 heads of 2048 tokens 14.7 and 16.5, of 4096 22.5 and
     // 23.1.
     p.by_head = heads <= sms && max_tokens <= kU * (64 + 128 * heads / sms);
+    // Many heads over short tables: shares that end between heads are uneven by a head at most, and nothing is left
+    // to merge (64 x 128-384 tokens of 32 heads 25.7 -> 23.9 us, 50 x 1-500 of 8 heads 13.3 -> 11.7; with tables of
+    // 64 units 100 x 300-1000 of 8 heads 24.8 -> 25.1, with 256 the power-law batch 40.6 -> 49.2).
+    p.whole = !p.by_head && heads >= 2 * sms && max_tokens <= 32 * kU;
     const int grid = p.by_head ? (int)heads : sms;
     const size_t smem = S::kSmem + (p.scan ? (size_t)(a.num_seqs + 2) * 12 : 0);
     if (!p.scan) {
@@ -1029,7 +1055,7 @@ cudaError_t launch_typed(Q4Params p, const AttnArgs &a, cudaStream_t stream) {
         cudaGetLastError();
         if ((e = set()) == cudaSuccess) e = launch_dependent(kern, dim3(grid), dim3(S::kWarps * 32), smem, stream, p);
     }
-    if (e != cudaSuccess || p.by_head) return e;
+    if (e != cudaSuccess || p.by_head || p.whole) return e;
     return launch_dependent(q4_merge_kernel<T, D, S::HW>, dim3(grid, p.hw), dim3(kMergeWarps * 32), 0, stream, p);
 }
 

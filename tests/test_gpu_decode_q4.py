@@ -165,6 +165,29 @@ def test_one_cta_a_head_and_the_split_agree_with_64_bits(pages, H, Hkv, D, dtype
     c.check(c.run(), what=f"{pages} pages")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("S,H,Hkv,D,B,top", [(80, 8, 8, 128, 16, 512), (400, 4, 1, 64, 8, 100), (60, 64, 8, 128, 32, 300),
+                                             (200, 24, 2, 64, 16, 64), (4500, 2, 1, 64, 8, 40)])
+def test_many_heads_over_short_tables(S, H, Hkv, D, B, top, dtype):
+    """Shares that end between heads, with sequences of no valid length among them."""
+    rng = np.random.default_rng(S)
+    ctx = rng.integers(1, top + 1, S)
+    ctx[:3] = top, 1, top
+    c = Case(ctx, H, Hkv, D, B, dtype, seed=S)
+    ref = c.run()
+    some = [0, 1, 2, S - 1] + list(range(3, S, max(1, S // 60)))
+    c.check(ref, seqs=some, what="whole heads")
+    for gone in ([0, 1], [S - 1], list(range(5, S - 5)), list(range(0, S, 2))):
+        cl = c.cl.clone()
+        cl[gone] = 0
+        out = torch.full_like(ref, 9.0)
+        pa.decode_q4(c.q, c.k4, c.v4, c.bt, cl, c.scale, out=out)
+        live = [s for s in range(S) if s not in set(gone)]
+        assert torch.all(out[gone] == 9.0)
+        c.check(out, seqs=[s for s in some if s not in set(gone)], what="some without a length")
+        assert torch.isfinite(out[live].float()).all()
+
+
 def test_heads_cut_between_many_ctas():
     """One long sequence of one kv-head: every CTA holds a piece of the same head."""
     for dtype, H in ((torch.bfloat16, 3), (torch.bfloat16, 12), (torch.float32, 9)):
