@@ -43,15 +43,17 @@
 // none).  A (sequence, kv-head) inside one warp is normalised and stored; cut
 // ones leave (m, l, o) pieces, merged first between the warps of a CTA (shared
 // memory), then, where a CTA boundary cuts a head, by a second small kernel
-// (workspace), always in stream order, so results do not depend on timing.  Every CTA finds its share by itself, from a prefix sum over the
-// lengths in shared memory; only batches of more than kScanSeqs sequences
-// have it made by a kernel of its own.  Over short tables a CTA takes whole
-// heads, one or several, and there is no second kernel.
+// (workspace), always in stream order, so results do not depend on timing.
+// Every CTA finds its share by itself, from a prefix sum over the lengths in
+// shared memory; only batches of more than kScanSeqs sequences have it made by
+// a kernel of its own.  Over short tables a CTA takes whole heads, one or
+// several, and there is no second kernel.
 //
 // Measured (32 / 8 heads of 128, blocks of 16): 256 power-law sequences, 151 MB,
 // 40.4 us; 16 x 32768 tokens, 604 MB, 115 us = 5.3 TB/s, 0.79 of the copy peak,
-// at 60 % of the issue slots and 54 % of the ALU pipe, 305 instructions a unit
-// and warp; its copies alone take 104 us.  A short request takes 5.5 us.
+// at 61 % of the issue slots and 53 % of the ALU pipe, 300 instructions a unit
+// and warp; with the products left out its copies take 96 us.  A short request
+// takes 5.6 us.
 //
 // fp32 queries: q and the weights are split into three bf16 parts each (24
 // bits), and the codes are brought to n - 8 one by one (0x4300 | n is 128 + n

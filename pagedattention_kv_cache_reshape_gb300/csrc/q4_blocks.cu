@@ -8,8 +8,8 @@
 // or 8 consecutive dims of a token row, a warp whole lines of the codes, and
 // rows of the wide pool in pieces of D e bytes.
 // Measured: 2048 pairs of 16 tokens x 8 heads x 128 bf16 (172 MB each way) there
-// and back 62.3 us, 5.5 TB/s; of the two, quantizing takes some 34 us at 65 % of
-// the issue slots and dequantizing 28 us at 76 %.  Five CTAs an SM (62.3 us) beat
+// and back 62.4 us, 5.5 TB/s; each alone from cold caches, quantizing takes 38.4 us
+// at 70 % of the issue slots and dequantizing 28.5 us at 77 %.  Five CTAs an SM (62.3 us) beat
 // four (65.6), eight items a thread 61.8 but slow small calls (256 blocks 9.2
 // against 7.8 us with the append before them).
 #include "pa_device.cuh"
