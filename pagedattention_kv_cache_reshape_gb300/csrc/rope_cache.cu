@@ -275,8 +275,11 @@ template <typename T, int kQ4>
 cudaError_t launch_vec(const RopeArgs &a, int64_t kv_bytes, cudaStream_t stream) {
     const int lanes = a.head_dim / 16;
     const int64_t all = (int64_t)a.num_heads + 2 * a.num_kv_heads;
+    // whole rows a pass, evened out over the passes: rows <= threads / lanes, so that a CTA, rounded up to whole warps,
+    // stays within the kernel's launch bound (`threads` is a multiple of 32) whatever head_dim / 16 is
     auto shape = [&](int threads, int &rows, int &passes) {
-        passes = (int)((all * lanes + threads - 1) / threads);
+        const int most = threads / lanes;
+        passes = (int)((all + most - 1) / most);
         rows = (int)((all + passes - 1) / passes);
         return dim3((rows * lanes + 31) / 32 * 32);
     };
