@@ -31,33 +31,41 @@ constexpr int kThreads = 128;
 // us, 128 35.3, 192 36.9, 384 40.5).
 constexpr int vec_threads(int U) { return U == 1 ? 384 : 64; }
 
-// a c - b s (sign = -1) or a c + b s (sign = +1), the exact value rounded once to
-// fp32: both products are split into value and error (fma), the sum into value
-// and error, and the errors are added last.  The 4-bit code of a key depends
-// on which side of a border its rotated value lies, so the rotation must not
-// add an error of its own there.
+// a c + b s (s negated: a c - b s), the exact value rounded once to fp32, or, where
+// a product or the sum is not finite, what fp32 gives: both products are split
+// into value and error (fma), the sum into value and error, and the errors are
+// added last.  The 4-bit code of a key depends on which side of a border its
+// rotated value lies, so the rotation must not add an error of its own there.
+// kQ4: for 4-bit pools, where a group with an infinity and one with a NaN are
+// the same; the instruction that keeps infinities is left out there (8191
+// tokens with the expansion of their blocks 51.3 us against 52.4).
+template <bool kQ4>
 __device__ __forceinline__ float rotate_exact(float a, float c, float b, float s) {
     const float p = __fmul_rn(a, c), ep = __fmaf_rn(a, c, -p);
     const float w = __fmul_rn(b, s), ew = __fmaf_rn(b, s, -w);
     const float sum = __fadd_rn(p, w);
     const float bb = __fsub_rn(sum, p);
     const float es = __fadd_rn(__fsub_rn(p, __fsub_rn(sum, bb)), __fsub_rn(w, bb));
-    return __fadd_rn(sum, __fadd_rn(es, __fadd_rn(ep, ew)));
+    const float err = __fadd_rn(es, __fadd_rn(ep, ew));
+    // With infinite products or sums err is NaN (inf - inf in es), and the maximum takes its other operand: an
+    // infinite sum stays what it is.  The errors of a finite sum are three half steps, 2^103 each, at most.
+    return __fadd_rn(sum, kQ4 ? err : fmaxf(err, -0x1p105f));
 }
 
 // A pair turned in place: keys exactly, queries with one rounding more.
+template <bool kQ4>
 __device__ __forceinline__ void turn(float &a, float &b, float c, float s, bool is_q) {
     const float x = a, y = b;
     if (is_q) {
         a = __fmaf_rn(x, c, -__fmul_rn(y, s));
         b = __fmaf_rn(y, c, __fmul_rn(x, s));
     } else {
-        a = rotate_exact(x, c, y, -s);
-        b = rotate_exact(y, c, x, s);
+        a = rotate_exact<kQ4>(x, c, y, -s);
+        b = rotate_exact<kQ4>(y, c, x, s);
     }
 }
 
-template <typename T>
+template <typename T, bool kQ4>
 __device__ __forceinline__ float rotated(const RopeArgs &a, const T *row, const float *cs, int d) {
     const int R = a.rot_dim / 2;
     const float x = to_float(row[d]);
@@ -67,7 +75,7 @@ __device__ __forceinline__ float rotated(const RopeArgs &a, const T *row, const 
     if (a.interleaved) { i = d >> 1; first = (d & 1) == 0; o = d ^ 1; }
     else { first = d < R; i = first ? d : d - R; o = first ? d + R : d - R; }
     const float y = to_float(row[o]);
-    return rotate_exact(x, cs[i], y, first ? -cs[R + i] : cs[R + i]);
+    return rotate_exact<kQ4>(x, cs[i], y, first ? -cs[R + i] : cs[R + i]);
 }
 
 // Any shape, element by element: one CTA per token.
@@ -96,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) 
         const int o = a.interleaved ? d + 1 : d + R;
         const int i = a.interleaved ? d >> 1 : d;
         float x = to_float(row[d]), y = to_float(row[o]);
-        turn(x, y, cs[i], cs[R + i], true);
+        turn<kQ4>(x, y, cs[i], cs[R + i], true);
         out[d] = from_float<T>(x);
         out[o] = from_float<T>(y);
     }
@@ -107,7 +115,7 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) 
         T *vd = static_cast<T *>(a.v_cache) + slot * ((int64_t)a.num_kv_heads * D);
         for (int64_t e = tid; e < (int64_t)a.num_kv_heads * D; e += kThreads) {
             const int h = (int)(e / D), d = (int)(e - (int64_t)h * D);
-            kd[e] = from_float<T>(rotated(a, key + (int64_t)h * D, cs, d));
+            kd[e] = from_float<T>(rotated<T, kQ4>(a, key + (int64_t)h * D, cs, d));
             vd[e] = value[e];
         }
         return;
@@ -124,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) 
         Raw8<T> x[2];
         for (int i = 0; i < 16; ++i)
             reinterpret_cast<T *>(x)[i] = is_v ? value[(int64_t)h * D + 16 * k + i]
-                                               : from_float<T>(rotated(a, key + (int64_t)h * D, cs, 16 * k + i));
+                                               : from_float<T>(rotated<T, kQ4>(a, key + (int64_t)h * D, cs, 16 * k + i));
         uint8_t *s = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) + (blk * a.num_kv_heads + h) * slab;
         uint8_t *row = s + off * q4_row_bytes(D);
         uint16_t *scales = reinterpret_cast<uint16_t *>(s + a.block_size * q4_row_bytes(D)) + off * (D / kQ4Group);
@@ -134,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) 
 }
 
 // The two vectors of 8 that a thread owns, turned and rounded to T.
-template <typename T>
+template <typename T, bool kQ4>
 __device__ __forceinline__ void turn_rows(Raw8<T> &rx, Raw8<T> &ry, const RopeArgs &a, int pos, int j, bool is_q) {
     float c[8], s[8], x[8], y[8];
     const float *cs = a.cos_sin + (int64_t)pos * a.rot_dim + 8 * j;
@@ -146,11 +154,11 @@ __device__ __forceinline__ void turn_rows(Raw8<T> &rx, Raw8<T> &ry, const RopeAr
 #pragma unroll
         for (int i = 0; i < 8; ++i) {   // pair i is (x[2i], x[2i + 1]) or, from 4 on, y's
             float &v = i < 4 ? x[2 * i] : y[2 * i - 8], &w = i < 4 ? x[2 * i + 1] : y[2 * i - 7];
-            turn(v, w, c[i], s[i], is_q);
+            turn<kQ4>(v, w, c[i], s[i], is_q);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) turn(x[i], y[i], c[i], s[i], is_q);
+        for (int i = 0; i < 8; ++i) turn<kQ4>(x[i], y[i], c[i], s[i], is_q);
     }
     rx = from_floats<T>(x);
     ry = from_floats<T>(y);
@@ -217,7 +225,7 @@ __global__ void __launch_bounds__(vec_threads(U), U == 1 ? 2 : 16) rope_cache_ve
         for (int u = 0; u < U; ++u) {
             if (!live[u]) continue;   // the same in every thread
             if (kQ4 == 1) {
-                if (mine && turns && !is_v) turn_rows(rx[u], ry[u], a, pos[u], j, is_q);
+                if (mine && turns && !is_v) turn_rows<T, kQ4 != 0>(rx[u], ry[u], a, pos[u], j, is_q);
                 if (mine && is_q) {
                     T *dst = static_cast<T *>(a.q_out) + ((int64_t)(t0 + u) * H + h) * D;
                     store_raw8(dst + d0, rx[u]);
@@ -245,7 +253,7 @@ __global__ void __launch_bounds__(vec_threads(U), U == 1 ? 2 : 16) rope_cache_ve
             if (is_q) dst = static_cast<T *>(a.q_out) + ((int64_t)(t0 + u) * H + h) * D;
             else if (kQ4 == 2) dst = kv_s + (u * 2 * HK + row - H) * D;
             else dst = static_cast<T *>(is_v ? a.v_cache : a.k_cache) + (slot[u] * HK + h) * D;
-            if (turns && !is_v) turn_rows(rx[u], ry[u], a, pos[u], j, is_q);
+            if (turns && !is_v) turn_rows<T, kQ4 != 0>(rx[u], ry[u], a, pos[u], j, is_q);
             store_raw8(dst + d0, rx[u]);
             store_raw8(dst + d1, ry[u]);
         }
