@@ -161,6 +161,25 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _empty(shape, dtype, device, stream, result: bool = False):
+    """Memory that a call on `stream` makes itself.  torch's allocator hands freed memory out again in the order of the
+    stream that it was taken on, so it is taken on the call's own stream.  A result is also marked as used by the
+    current stream, where the caller may read it (after waiting for `stream`)."""
+    if stream is None or device.type != "cuda":   # (tensors off the GPU are refused before the launch)
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    handle = _stream(stream)
+    if handle == here.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):   # 0 and 1 are names of the default stream
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if result:
+        t.record_stream(here)
+    return t
+
+
 def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -202,7 +221,7 @@ def compute_slot_mapping(block_tables, seq_start, cu_seqlens_q, num_blocks: int,
     """pa_compute_slot_mapping; returns the int64 slot_mapping tensor."""
     num_seqs, max_blocks = block_tables.shape
     if slot_mapping is None:
-        slot_mapping = torch.empty(total_new, dtype=torch.int64, device=block_tables.device)
+        slot_mapping = _empty(total_new, torch.int64, block_tables.device, stream, result=True)
     rc = load().pa_compute_slot_mapping(
         _contig(block_tables, "block_tables", torch.int32), num_seqs, max_blocks,
         _contig(seq_start, "seq_start", torch.int32), _contig(cu_seqlens_q, "cu_seqlens_q", torch.int32),
@@ -241,9 +260,9 @@ def varlen_prefill_workspace_size(num_seqs, total_q, num_heads, num_kv_heads, he
                                                        head_dim, block_size, max_blocks))
 
 
-def _ws(workspace, nbytes, device):
+def _ws(workspace, nbytes, device, stream):
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        workspace = _empty(max(nbytes, 16), torch.uint8, device, stream)
     return workspace
 
 
@@ -254,9 +273,9 @@ def decode(q, k_cache, v_cache, block_tables, context_lens, scale: float, out=No
     num_blocks, block_size, hkv, d = k_cache.shape
     max_blocks = block_tables.shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream, result=True)
     need = decode_workspace_size(num_seqs, H, hkv, D, block_size, max_blocks)
-    workspace = _ws(workspace, need, q.device)
+    workspace = _ws(workspace, need, q.device, stream)
     rc = load().pa_decode(
         _contig(out, "out"), _contig(q, "q"), _contig(k_cache, "k_cache"), _contig(v_cache, "v_cache"),
         _contig(block_tables, "block_tables", torch.int32), _contig(context_lens, "context_lens", torch.int32),
@@ -279,11 +298,11 @@ def decode_step(q, key, value, k_cache, v_cache, block_tables, context_lens, seq
         if t.dim() != 3 or t.shape[1:] != (hkv, d) or t.stride(2) != 1 or t.stride(1) != d:
             raise ValueError(f"{name} must be [tokens, {hkv}, {d}] with contiguous rows")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream, result=True)
     if slot_mapping is None:
-        slot_mapping = torch.empty(total_new, dtype=torch.int64, device=q.device)
+        slot_mapping = _empty(total_new, torch.int64, q.device, stream, result=True)
     need = decode_workspace_size(num_seqs, H, hkv, D, block_size, max_blocks)
-    workspace = _ws(workspace, need, q.device)
+    workspace = _ws(workspace, need, q.device, stream)
     rc = load().pa_decode_step(
         _contig(out, "out"), _contig(q, "q"), _dev(key, "key"), _dev(value, "value"), key.stride(0),
         value.stride(0), _contig(k_cache, "k_cache"), _contig(v_cache, "v_cache"),
@@ -325,9 +344,9 @@ def varlen_prefill(q, cu_seqlens_q, k_cache, v_cache, block_tables, context_lens
     num_blocks, block_size, hkv, d = k_cache.shape
     num_seqs, max_blocks = block_tables.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream, result=True)
     need = varlen_prefill_workspace_size(num_seqs, total_q, H, hkv, D, block_size, max_blocks)
-    workspace = _ws(workspace, need, q.device)
+    workspace = _ws(workspace, need, q.device, stream)
     fn = load().pa_varlen_prefill if causal else load().pa_varlen_encode
     rc = fn(
         _contig(out, "out"), _contig(q, "q"), _contig(cu_seqlens_q, "cu_seqlens_q", torch.int32),
@@ -353,11 +372,11 @@ def varlen_step(q, key, value, k_cache, v_cache, cu_seqlens_q, block_tables, con
                 or t.stride(1) != d:
             raise ValueError(f"{name} must be [{total_q}, {hkv}, {d}] with contiguous rows")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream, result=True)
     if slot_mapping is None:
-        slot_mapping = torch.empty(total_q, dtype=torch.int64, device=q.device)
+        slot_mapping = _empty(total_q, torch.int64, q.device, stream, result=True)
     need = varlen_prefill_workspace_size(num_seqs, total_q, H, hkv, D, block_size, max_blocks)
-    workspace = _ws(workspace, need, q.device)
+    workspace = _ws(workspace, need, q.device, stream)
     rc = load().pa_varlen_step(
         _contig(out, "out"), _contig(q, "q"), _dev(key, "key"), _dev(value, "value"), key.stride(0),
         value.stride(0), _contig(k_cache, "k_cache"), _contig(v_cache, "v_cache"),
@@ -432,7 +451,7 @@ def _rope(fn, q, key, value, cos_sin, positions, k_cache, v_cache, pool_dtype, n
         q_shape = q.shape
         heads = q_shape[1] if len(q_shape) == 3 else 0
         if q_out is None:
-            q_out = torch.empty((n, heads, d), dtype=dtype, device=q.device)
+            q_out = _empty((n, heads, d), dtype, q.device, stream, result=True)
         qs, q1, q2 = q.stride() if heads else (0, 0, 0)
         if not (q_shape == q_out.shape == (n, heads, d) and q.dtype == q_out.dtype == dtype and q2 == 1 and q1 == d
                 and q.get_device() == dev and q_out.get_device() == dev):
@@ -559,11 +578,11 @@ def decode_q4(q, k_cache, v_cache, block_tables, context_lens, scale: float, out
     if code is None:
         raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream, result=True)
     elif out.shape != q.shape or out.dtype != dtype:
         raise ValueError("out must have q's shape and dtype")
     if workspace is None:
-        workspace = _ws(None, decode_q4_workspace_size(num_seqs, H, hkv, D, block_size, max_blocks), q.device)
+        workspace = _ws(None, decode_q4_workspace_size(num_seqs, H, hkv, D, block_size, max_blocks), q.device, stream)
     if not (q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
             and block_tables.is_contiguous() and context_lens.is_contiguous() and workspace.is_contiguous()
             and k_cache.dtype == v_cache.dtype == torch.uint8
@@ -648,7 +667,7 @@ def decode_static_scratch(q, k_cache, v_cache, block_tables, context_lens, scale
     num_blocks, block_size, hkv, d = k_cache.shape
     max_blocks = block_tables.shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream, result=True)
     rc = load().pa_decode_static_scratch(
         _contig(out, "out"), _contig(q, "q"), _contig(k_cache, "k_cache"), _contig(v_cache, "v_cache"),
         _contig(block_tables, "block_tables", torch.int32), _contig(context_lens, "context_lens", torch.int32),
