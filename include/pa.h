@@ -363,9 +363,10 @@ PA_API size_t pa_decode_q4_workspace_size(int num_seqs, int num_heads, int num_k
  * behaviour and workspace rules as pa_decode's (calls that may overlap on the
  * GPU take workspaces of their own); `dtype` is that of q and out.  Sums and
  * softmax are fp32.  With BF16 a weight times its scale of V is rounded to
- * fp16 under a power of two that follows the largest scale of the sequence so
- * far, so what lies 2^-21 under that keeps fewer bits; with F32 the products
- * are fp32 to the last few bits.  A NaN in q, or a NaN scale in a visible row,
+ * fp16 under a power of two that follows the largest scale of the same 32 dims
+ * in the sequence so far, so what lies 2^-20 under that keeps fewer bits (other
+ * groups of dims have no part in it); with F32 the products are fp32 to the
+ * last few bits, for scales of V from 2^-100 up.  A NaN in q, or a NaN scale in a visible row,
  * stays in the heads (for a scale of V: the 32 dims) it belongs to.
  * Deterministic: results depend on the inputs and the device's SM count,
  * never on which blocks hold the data.

@@ -20,13 +20,18 @@
 //    the scales with -8 sum(q) in three bf16 parts.
 //  * O^T += V^T P^T (dims in M, tokens in K): the token's scale of V goes into
 //    the weight, once per group, and the product is rounded to fp16 (2^-11).
-//    The weights carry a power of two, 2^lift, that brings the largest scale
-//    seen so far into [2^6, 2^7): with weights below 2^8 nothing overflows, and
-//    a product 2^-21 of the largest still has its 11 bits.  The 8 is taken off
-//    by a product of the same weights with -8 right after: a sum over many
-//    tokens would otherwise lose a small result under 8 times its weights.
-//  * The softmax reference of a head moves only when a logit passes it by 8
-//    (base 2), found by one warp vote a step: weights stay below 2^8 and sums
+//    The scales are first brought up by a power of two of their group (packed
+//    products, two scales each), which took the group's largest scale into
+//    [2^6, 2^7) when it was set and is set anew when one passes 2^8: with
+//    weights up to 2^7 nothing overflows, a product 2^-20 of the group's
+//    largest still has its 11 bits, and no group loses to another, as it did
+//    under one power for all four (16 x 32768 tokens 115.6 us with one, 122.0
+//    with four; groups told apart only where they differ, by a check or a form
+//    of their own, took 119.5 to 125).  The 8 is taken off by a product of the
+//    same weights with -8 right after: a sum over many tokens would otherwise
+//    lose a small result under 8 times its weights.
+//  * The softmax reference of a head moves only when a logit passes it by 7
+//    (base 2), found by one warp vote a step: weights stay below 2^7 and sums
 //    are rescaled a few times a sequence instead of every step.
 //  * A warp takes units of 16 tokens of one sequence and kv-head through a ring
 //    of its own in shared memory (16-byte asynchronous copies), two a step
@@ -78,7 +83,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kMaxCtas = 512;
 constexpr int kScanSeqs = 4096;     // sequences whose prefix a CTA makes itself (48 KB of shared memory)
 constexpr int kHeadCost = 3;
-constexpr float kMoveAt = 8.0f;     // a logit this far (base 2) over the reference moves it
+constexpr float kMoveAt = 7.0f;     // a logit this far (base 2) over the reference moves it
 
 // A head cut at the end of CTA c (seq < 0: none): its pieces are c's second, then the first of c + 1 .. last.
 struct Cut { int seq, vh, last, pad; };
@@ -197,6 +202,11 @@ __device__ __forceinline__ uint32_t nibbles_f16(uint32_t w, int i) {
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 __device__ __forceinline__ void cp_async16(uint32_t smem, const void *gmem) {
@@ -456,9 +466,8 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
         // pairs divided by the 16 that their codes carry); q8: three bf16 parts of -8 sum(q) of the groups
         uint32_t qf[NT][NS][NG][4], q8[NT][2];
         float o[NT][2 * NG][4], m[NT][2], l[NT][2], sl[NT][2];   // sl: what brings the lane's columns to base-2 logits
-        int lift = 0, lift_e = -1;                                // lift_e: the exponent field that lift goes by
-        uint32_t lift_cap = 0xff80ff80u;                          // the largest bf16 of that exponent, twice
-        float move_at = kMoveAt;                                  // kMoveAt + lift
+        uint32_t up[NG / 2], cap[NG / 2];                         // the groups' powers of two for V's scales and the
+                                                                  // largest scales they are good for, bf16 pairs
         bool fresh = true, at_start = true;
         int u_first = 0;
         const uint8_t *st = ring;
@@ -576,48 +585,57 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         w[j][nt][e] = fmaf(x[j][nt][e], sl[nt][e & 1], -m[nt][e & 1]);
-                        move |= w[j][nt][e] > move_at;
+                        move |= w[j][nt][e] > kMoveAt;
                     }
-            uint32_t top = 0;
             if (!S::kF32) {
 #pragma unroll
-                for (int j = 0; j < NU; ++j)
+                for (int g = 0; g < NG / 2; ++g) {
+                    uint32_t top = 0;   // (a NaN scale is no size)
 #pragma unroll
-                    for (int g = 0; g < NG / 2; ++g) top = max_bf16x2(top, max_bf16x2(vz0[j][g], vz1[j][g]));
-                move |= !__hble2(*reinterpret_cast<const __nv_bfloat162 *>(&top),
-                                 *reinterpret_cast<const __nv_bfloat162 *>(&lift_cap));
+                    for (int j = 0; j < NU; ++j) top = max_bf16x2(top, max_bf16x2(vz0[j][g], vz1[j][g]));
+                    move |= !__hble2(*reinterpret_cast<const __nv_bfloat162 *>(&top),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&cap[g]));
+                }
             }
             if (__any_sync(0xffffffffu, move)) {
-                const int old_lift = lift;
+                float beta[NG];   // what the sums of a group are brought down by
                 if (!S::kF32) {
-                    int t0e = (int)(top & 0x7fffu), t = (int)((top >> 16) & 0x7fffu);
-                    t = max(t0e < 0x7f80 ? t0e : 0, t < 0x7f80 ? t : 0);   // (a NaN scale is no size)
-                    t = max(t, __shfl_xor_sync(0xffffffffu, t, 4));
-                    t = max(t, __shfl_xor_sync(0xffffffffu, t, 8));
-                    t = uniform(max(t, __shfl_xor_sync(0xffffffffu, t, 16)));
-                    lift_e = max(lift_e, t >> 7);
-                    lift_cap = (uint32_t)(lift_e << 7 | 0x7f) * 0x10001u;
-                    lift = min(100, 133 - lift_e);
-                    move_at = kMoveAt + lift;
+#pragma unroll
+                    for (int g = 0; g < NG / 2; ++g) {
+                        uint32_t t = 0;
+#pragma unroll
+                        for (int j = 0; j < NU; ++j) t = max_bf16x2(t, max_bf16x2(vz0[j][g], vz1[j][g]));
+                        t = max_bf16x2(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                        t = max_bf16x2(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                        t = max_bf16x2(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                        // exponent fields: of a largest scale e, the power 260 - e takes it to 133 (2^6)
+                        const int old0 = up[g] >> 7 & 0xff, old1 = up[g] >> 23;
+                        const int new0 = min(old0, 260 - (int)(t >> 7 & 0xff)), new1 = min(old1, 260 - (int)(t >> 23 & 0xff));
+                        beta[2 * g] = __uint_as_float((uint32_t)max(1, 127 + new0 - old0) << 23);
+                        beta[2 * g + 1] = __uint_as_float((uint32_t)max(1, 127 + new1 - old1) << 23);
+                        up[g] = (uint32_t)new0 << 7 | (uint32_t)new1 << 23;
+                        cap[g] = (uint32_t)min(254, 261 - new0) << 7 | (uint32_t)min(254, 261 - new1) << 23 | 0x007f007fu;
+                    }
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float y = m[nt][e] + old_lift;
+                        float y = m[nt][e];
 #pragma unroll
                         for (int j = 0; j < NU; ++j)
                             y = fmaxf(y, fmaxf(x[j][nt][e] * sl[nt][e], x[j][nt][e + 2] * sl[nt][e]));
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
-                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16)) - lift;
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
                         const float alpha = y == m[nt][e] ? 1.0f : fast_exp2(m[nt][e] - y);
                         m[nt][e] = y;
                         l[nt][e] *= alpha;
 #pragma unroll
                         for (int t = 0; t < 2 * NG; ++t) {
-                            o[nt][t][e] *= alpha;
-                            o[nt][t][e + 2] *= alpha;
+                            const float f = S::kF32 ? alpha : alpha * beta[t / 2];
+                            o[nt][t][e] *= f;
+                            o[nt][t][e + 2] *= f;
                         }
 #pragma unroll
                         for (int j = 0; j < NU; ++j) {
@@ -626,6 +644,15 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                         }
                     }
                 }
+            }
+            if (!S::kF32) {   // exact: powers of two
+#pragma unroll
+                for (int j = 0; j < NU; ++j)
+#pragma unroll
+                    for (int g = 0; g < NG / 2; ++g) {
+                        vz0[j][g] = mul_bf16x2(vz0[j][g], up[g]);
+                        vz1[j][g] = mul_bf16x2(vz1[j][g], up[g]);
+                    }
             }
 #pragma unroll
             for (int j = 0; j < NU; ++j)
@@ -776,11 +803,10 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                     m[nt][0] = m[nt][1] = -INFINITY;
                     l[nt][0] = l[nt][1] = 0.0f;
                 }
-                if (!S::kF32) {
-                    lift = 0;
-                    lift_e = -1;
-                    lift_cap = 0xff80ff80u;
-                    move_at = kMoveAt;
+#pragma unroll
+                for (int g = 0; g < NG / 2; ++g) {   // 2^126: scales from 2^-118 up bring it down
+                    up[g] = 0x7e807e80u;
+                    cap[g] = 0x047f047fu;
                 }
             }
             const int pair = left > 1 && u + 1 < nu ? 2 : 1;
@@ -804,7 +830,11 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                 } while (nu == 0);
             }
             if (kEarly && left > 0) request_q(s, vh);
-            // rows r of a tile carry 2^-24 (bf16 calls), rows r + 8 2^-20
+            // rows r of a tile carry 2^-24 (bf16 calls), rows r + 8 2^-20; the dims of a group its scales' power of two
+            float down[NG];
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+                down[g] = S::kF32 ? 1.0f : __uint_as_float((254 - (up[g / 2] >> (g & 1 ? 23 : 7) & 0xff)) << 23);
             constexpr float kUp0 = S::kF32 ? 1.0f : 0x1p24f, kUp1 = S::kF32 ? 1.0f : 0x1p20f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -834,8 +864,8 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                         const float inv = 1.0f / l[nt][e];
 #pragma unroll
                         for (int g = 0; g < NG; ++g) {
-                            const float y0 = o[nt][2 * g][e] * inv, y1 = o[nt][2 * g][e + 2] * inv;
-                            const float y2 = o[nt][2 * g + 1][e] * inv, y3 = o[nt][2 * g + 1][e + 2] * inv;
+                            const float y0 = o[nt][2 * g][e] * inv * down[g], y1 = o[nt][2 * g][e + 2] * inv * down[g];
+                            const float y2 = o[nt][2 * g + 1][e] * inv * down[g], y3 = o[nt][2 * g + 1][e + 2] * inv * down[g];
                             T *d = dst + 32 * g;
                             if (!p.vec) {
                                 d[0] = from_float<T>(y0); d[1] = from_float<T>(y1);
@@ -856,7 +886,6 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                     piece = reinterpret_cast<float *>(ring);
                 }
                 if (lane == 0) meta[2 * warp + (at_start ? 0 : 1)] = {s_done, vh_done, u_first, u, nu_done};
-                const float down = __uint_as_float((uint32_t)(127 - lift) << 23);   // 2^-lift
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -865,11 +894,11 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
 #pragma unroll
                         for (int g = 0; g < NG; ++g)
                             *reinterpret_cast<float4 *>(piece + h * D + 32 * g + 4 * r) =
-                                make_float4(o[nt][2 * g][e] * down, o[nt][2 * g][e + 2] * down,
-                                            o[nt][2 * g + 1][e] * down, o[nt][2 * g + 1][e + 2] * down);
+                                make_float4(o[nt][2 * g][e] * down[g], o[nt][2 * g][e + 2] * down[g],
+                                            o[nt][2 * g + 1][e] * down[g], o[nt][2 * g + 1][e + 2] * down[g]);
                         if (r == 0) {
-                            piece[HW * D + 2 * h] = m[nt][e] + lift;
-                            piece[HW * D + 2 * h + 1] = l[nt][e] * down;
+                            piece[HW * D + 2 * h] = m[nt][e];
+                            piece[HW * D + 2 * h + 1] = l[nt][e];
                         }
                     }
             }
