@@ -466,6 +466,7 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
         // pairs divided by the 16 that their codes carry); q8: three bf16 parts of -8 sum(q) of the groups
         uint32_t qf[NT][NS][NG][4], q8[NT][2];
         float o[NT][2 * NG][4], m[NT][2], l[NT][2], sl[NT][2];   // sl: what brings the lane's columns to base-2 logits
+        uint32_t far[NT];                                         // q-heads that leave 2^24 of it to the logits
         uint32_t up[NG / 2], cap[NG / 2];                         // the groups' powers of two for V's scales and the
                                                                   // largest scales they are good for, bf16 pairs
         bool fresh = true, at_start = true;
@@ -556,6 +557,15 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                     }
                 }
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                if (far[nt]) {   // (the same for the warp)
+#pragma unroll
+                    for (int j = 0; j < NU; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (far[nt] >> (8 * c + 4 * (e & 1)) & 1) x[j][nt][e] *= 0x1p24f;
+                }
             // ---- softmax weights (base 2).  Rows behind the sequence may hold anything, NaN scales too: they are
             // selected away, not multiplied
             uint32_t vz0[NU][NG / 2], vz1[NU][NG / 2];   // V's scales
@@ -639,8 +649,9 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                         }
 #pragma unroll
                         for (int j = 0; j < NU; ++j) {
-                            w[j][nt][e] = fmaf(x[j][nt][e], sl[nt][e], -y);
-                            w[j][nt][e + 2] = fmaf(x[j][nt][e + 2], sl[nt][e], -y);
+                            // (products rounded as y was: a fused one leaves y's rounding, past 2^30 or so a large number)
+                            w[j][nt][e] = __fsub_rn(__fmul_rn(x[j][nt][e], sl[nt][e]), y);
+                            w[j][nt][e + 2] = __fsub_rn(__fmul_rn(x[j][nt][e + 2], sl[nt][e]), y);
                         }
                     }
                 }
@@ -735,43 +746,53 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                     float x[NG][8];
 #pragma unroll
                     for (int g = 0; g < NG; ++g) to_floats(x[g], q_raw[nt][g]);
+                    float most = 0.0f;
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+#pragma unroll
+                        for (int d = 0; d < 8; ++d) most = fmaxf(most, fabsf(x[g][d]));
+                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                    // Exponent fields: of the factor that brings `most` into [2^14, 2^15) (fp32 calls: [1, 2)), and of
+                    // its inverse, times the 2^24 that the codes carry.  An inverse with the scale past the largest fp32
+                    // leaves 2^24 of itself to the logits (`far`: the q-heads that do, four bits each).
+                    const int e = (int)(__float_as_uint(most) >> 23);
+                    const int lift_q = S::kF32 ? max(1, min(253, 254 - e)) : min(254, 268 - e);
+                    const int inverse = (S::kF32 ? 254 : 278) - lift_q;
+                    float up_q = __uint_as_float((uint32_t)lift_q << 23);
+                    float back = __uint_as_float((uint32_t)min(254, inverse) << 23) * p.scale_log2;
+                    const bool too_far = inverse > 254 || fabsf(back) > 0x1.fffffep127f;
+                    if (too_far) back = __uint_as_float((uint32_t)(inverse - 24) << 23) * p.scale_log2;
+                    far[nt] = __ballot_sync(0xffffffffu, too_far);
+                    sl[nt][0] = __shfl_sync(0xffffffffu, back, 8 * c);
+                    sl[nt][1] = __shfl_sync(0xffffffffu, back, 8 * c + 4);
                     if constexpr (S::kF32) {
 #pragma unroll
-                        for (int g = 0; g < NG; ++g)
+                        for (int g = 0; g < NG; ++g) {
+#pragma unroll
+                            for (int d = 0; d < 8; ++d) x[g][d] *= up_q;
 #pragma unroll
                             for (int k = 0; k < NS; ++k)
 #pragma unroll
                                 for (int d = 0; d < 4; ++d)
                                     qf[nt][k][g][d] = pack_bf16x2(bf16_part(x[g][d]), bf16_part(x[g][d + 4]));
-                        sl[nt][0] = sl[nt][1] = p.scale_log2;
+                        }
                     } else {
-                        float most = 0.0f;
-#pragma unroll
-                        for (int g = 0; g < NG; ++g)
-#pragma unroll
-                            for (int d = 0; d < 8; ++d) most = fmaxf(most, fabsf(x[g][d]));
                         float any = 0.0f;   // NaN if an element is NaN or infinite
 #pragma unroll
                         for (int g = 0; g < NG; ++g)
 #pragma unroll
                             for (int d = 0; d < 8; ++d) any = fmaf(x[g][d], 0.0f, any);
-                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
                         any += __shfl_xor_sync(0xffffffffu, any, 1);
                         any += __shfl_xor_sync(0xffffffffu, any, 2);
-                        // biased exponents of the factor that brings `most` into [2^14, 2^15) and of its inverse
-                        const int e = (int)(__float_as_uint(most) >> 23);
-                        const float up = __uint_as_float((uint32_t)min(254, 268 - e) << 23) + any;
-                        const float down = __uint_as_float((uint32_t)max(0, e - 14) << 23) * p.scale_log2;
-                        sl[nt][0] = __shfl_sync(0xffffffffu, down, 8 * c) * 0x1p24f;
-                        sl[nt][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4) * 0x1p24f;
+                        up_q += any;
                         float sums[NG];
 #pragma unroll
                         for (int g = 0; g < NG; ++g) {
                             float sum = 0.0f;
 #pragma unroll
                             for (int d = 0; d < 8; ++d) {
-                                x[g][d] *= up;
+                                x[g][d] *= up_q;
                                 sum += x[g][d];
                             }
 #pragma unroll

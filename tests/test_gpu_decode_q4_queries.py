@@ -1,0 +1,69 @@
+"""4-bit decode with queries over the whole range of their type, and with logits past the usual."""
+import numpy as np
+import pytest
+import torch
+
+from pagedattention_kv_cache_reshape_gb300 import pa
+
+import q4_reference as R
+from q4_decode_checks import check
+from test_gpu_decode_q4 import Case, _lib  # noqa: F401  (builds and loads the library)
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def refill(c, factor, seed=7):
+    """Pools anew: K ~ N(0, 1) factor, V ~ N(0, 1)."""
+    g = torch.Generator().manual_seed(seed)
+    k, v = (torch.randn(c.nb, c.B, c.Hkv, c.D, generator=g).to(DEV) for _ in "kv")
+    ident = torch.arange(c.nb, dtype=torch.int32, device=DEV)[:, None].repeat(1, 2).contiguous()
+    pa.quantize_blocks_q4(k * factor, v, c.k4, c.v4, ident)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H,D", [(8, 128), (32, 64)])
+@pytest.mark.parametrize("e", [-118, -100, 100, 118, 121, 124])
+def test_queries_and_keys_of_opposite_size(e, H, D, dtype):
+    """q 2^e over K 2^-e: ordinary logits."""
+    c = Case([40, 500], H, 2, D, 16, dtype, seed=81)
+    refill(c, 2.0 ** -e)
+    c.q *= 2.0 ** e
+    check(c, c.run(), what=f"2^{e}")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_heads_of_all_sizes_side_by_side(dtype):
+    """Heads of one kv-head whose queries differ by powers of two up to 2^224: logits from nothing to several units."""
+    c = Case([300], 8, 1, 128, 16, dtype, seed=82)
+    refill(c, 2.0 ** -122)
+    c.q *= torch.exp2(torch.tensor([122.0, 0.0, 121.0, -100.0, 118.0, 110.0, 124.0, 60.0], device=DEV))[None, :, None].to(dtype)
+    check(c, c.run(), what="mixed")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("e", [30, 60, 110, 121])
+def test_huge_logits_take_the_largest_one(e, dtype):
+    """Logits of 2^e: one token takes all the weight (they lie 2^e 2^-24 apart at least, or they are the same)."""
+    ctx = [1, 40, 300, 900]
+    c = Case(ctx, 8, 2, 128, 16, dtype, seed=83)
+    refill(c, 1.0)
+    c.q *= 2.0 ** e
+    out = c.run()
+    assert torch.isfinite(out).all()
+    k, v = R.values(c.k4, "k", 16, 128), R.values(c.v4, "v", 16, 128)
+    seen = 0
+    for s, n in enumerate(ctx):
+        ids = c.bt[s, :-(-n // 16)].cpu().numpy()
+        kr, vr = k[ids].reshape(-1, 2, 128)[:n], v[ids].reshape(-1, 2, 128)[:n]
+        for h in range(8):
+            x = kr[:, h // 4] @ R.f64(c.q[s, h])
+            top = np.argsort(x)[::-1]
+            # a sum's error: 16 fp32 steps of five times the products' magnitudes, as in the other tests
+            far = 2 * 5 * 16 * 2.0 ** -23 * (np.abs(kr[:, h // 4]) @ np.abs(R.f64(c.q[s, h]))).max()
+            if n > 1 and x[top[0]] - x[top[1]] < far + 2.0 ** 12:
+                continue
+            seen += 1
+            want = torch.from_numpy(vr[top[0], h // 4]).to(dtype)   # (n - 8) s, rounded once
+            assert torch.equal(out[s, h].cpu(), want), (s, h)
+    assert seen >= 24
