@@ -14,8 +14,10 @@
 //    a nibble as well, but that mma.sync is itself made of conversions and
 //    fp16 products: 16 x 32768 tokens took 187 us with it, 151 us with fp16.)
 //  * S = K Q^T (tokens in M, q-heads in N, m16n8k16): q in fp16 times a power of
-//    two per head that brings its largest element into [2^14, 2^15): exact
-//    down to 2^-31 of the largest.  The group's scale is applied to the 4 sums
+//    two per head that brings its largest element into [2^14, 2^15), in the
+//    dims of the upper nibbles (1, 3, 5, 7 mod 8) divided by the 16 that those
+//    carry: elements are exact down to 2^-31 of the head's largest in the even
+//    dims, to 2^-27 in the odd ones.  The group's scale is applied to the 4 sums
 //    of a lane, and the -8 sum(q) scale of all groups is one more product, of
 //    the scales with -8 sum(q) in three bf16 parts.
 //  * O^T += V^T P^T (dims in M, tokens in K): the token's scale of V goes into

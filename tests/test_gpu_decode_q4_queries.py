@@ -67,3 +67,25 @@ def test_huge_logits_take_the_largest_one(e, dtype):
             want = torch.from_numpy(vr[top[0], h // 4]).to(dtype)   # (n - 8) s, rounded once
             assert torch.equal(out[s, h].cpu(), want), (s, h)
     assert seen >= 24
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_small_elements_beside_a_large_one(D):
+    """bf16 queries are held in fp16: elements 2^-30 of the head's largest are exact in the dims 0, 2, 4, 6 (mod 8) and
+    2^-26 of it in the others.  The large element meets keys of zero, so the small ones decide."""
+    c = Case([40, 500], 8, 2, D, 16, torch.bfloat16, seed=84)
+    g = torch.Generator().manual_seed(85)
+    k, v = (torch.randn(c.nb, 16, 2, D, generator=g).to(DEV) for _ in "kv")
+    k[..., :32] = 0                                     # group 0: scale 0
+    ident = torch.arange(c.nb, dtype=torch.int32, device=DEV)[:, None].repeat(1, 2).contiguous()
+    pa.quantize_blocks_q4(k, v, c.k4, c.v4, ident)
+    for odd in (0, 1):
+        q = torch.zeros(2, 8, D, device=DEV)
+        small = torch.randn(2, 8, D // 2, generator=g).clamp(-2, 2).to(DEV)
+        small = torch.where(small.abs() < 1, torch.copysign(torch.ones_like(small), small), small)   # 1 .. 2
+        q[..., odd::2] = small.bfloat16().float() * 2.0 ** (-26 if odd else -30)
+        q[..., :32] = 0
+        q[..., 5] = 1.0
+        c.q = q.bfloat16()
+        c.scale = 0.1 * 2.0 ** (26 if odd else 30)
+        check(c, c.run(), what=f"odd {odd}", exact_q=True)
