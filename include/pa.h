@@ -273,7 +273,7 @@ PA_API pa_status pa_copy_blocks(const void *src_k, const void *src_v, void *dst_
  *  rot_dim        even, 0 .. head_dim; 0: no rotation (cos_sin, positions and
  *                 max_position unused)
  * A token with a negative slot is padding: its q_out row and the pools are left
- * as they are and its position is not read.  A slot past the pool or a
+ * as they are and its position may be anything.  A slot past the pool or a
  * position outside [0, max_position) sets PA_ERR_OUT_OF_RANGE, and the token
  * is skipped.  Any head_dim and block_size >= 1.  Precondition (not checked on
  * the device): live slots are pairwise distinct, as for pa_reshape_and_cache.
