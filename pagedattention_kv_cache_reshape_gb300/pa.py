@@ -469,6 +469,8 @@ def _rope(fn, q, key, value, cos_sin, positions, k_cache, v_cache, pool_dtype, n
                 (slot_mapping, "slot_mapping", torch.int64))
     rot = max_pos = table_ptr = pos_ptr = 0
     if cos_sin is not None:
+        if positions is None:
+            raise ValueError("positions are needed with cos_sin")
         max_pos, rot = cos_sin.shape
         if not (cos_sin.is_contiguous() and positions.is_contiguous()
                 and cos_sin.get_device() == positions.get_device() == dev

@@ -1,0 +1,44 @@
+"""What the Python binding of the rotary and 4-bit calls refuses before the library is called.  Without a GPU: torch
+gives CPU tensors the device number -1, which stands in for the current device here, and a launch would fail the test."""
+import pytest
+import torch
+
+from pagedattention_kv_cache_reshape_gb300 import build as B
+from pagedattention_kv_cache_reshape_gb300 import pa
+
+
+class NoLaunch:
+    def __init__(self, lib):
+        self.lib = lib
+
+    def __getattr__(self, name):
+        if name.endswith("workspace_size"):
+            return getattr(self.lib, name)
+        raise AssertionError(f"{name} was called")
+
+
+@pytest.fixture(autouse=True)
+def _stand_in(monkeypatch):
+    B.build()
+    lib = pa.load()
+    monkeypatch.setattr(pa, "_lib", NoLaunch(lib))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+
+
+def rows(n, h, d=128):
+    return torch.zeros(n, h, d, dtype=torch.bfloat16)
+
+
+def wide():
+    return [torch.zeros(4, 16, 2, 128, dtype=torch.bfloat16) for _ in "kv"]
+
+
+def q4():
+    return [torch.zeros(4, 2, 16 * 72, dtype=torch.uint8) for _ in "kv"]
+
+
+@pytest.mark.parametrize("call,pools", [("rope_and_cache", wide), ("rope_and_cache_q4", q4)])
+def test_a_table_without_positions_is_refused(call, pools):
+    slots = torch.zeros(3, dtype=torch.int64)
+    with pytest.raises(ValueError, match="positions"):
+        getattr(pa, call)(None, rows(3, 2), rows(3, 2), torch.zeros(9, 128), None, *pools(), slots)
