@@ -409,6 +409,13 @@ def _refuse(dev: int, *specs):
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+def _status(t, dev: int) -> int:
+    """The status word's address; like the other tensors it is the current device's."""
+    if t.is_cuda and t.get_device() != dev:
+        raise ValueError(f"dev_status must be on the current device cuda:{dev}, got {t.device}")
+    return _opt(t)
+
+
 def _rows(name: str, t, shape, dtype, dev: int) -> None:
     """Raises what is wrong with a token-strided view [tokens, heads, d]."""
     if t.shape != shape:
@@ -484,7 +491,7 @@ def _rope(fn, q, key, value, cos_sin, positions, k_cache, v_cache, pool_dtype, n
     rc = getattr(_lib or load(), fn)(
         out_ptr, q_ptr, key.data_ptr(), value.data_ptr(), qs, ks, vs, table_ptr, pos_ptr, max_pos, rot,
         1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), n, heads, hkv, d,
-        block_size, num_blocks, code, 0 if dev_status is None else _opt(dev_status),
+        block_size, num_blocks, code, 0 if dev_status is None else _status(dev_status, dev),
         _raw_stream(dev) if stream is None else _stream(stream))
     if rc != OK:
         raise PAError(rc, fn)
@@ -546,7 +553,7 @@ def _q4_blocks(fn, wide_k, wide_v, q4_k, q4_v, quantize, pairs, dev_status, stre
     src, dst = (wide, q4) if quantize else (q4, wide)
     n_src, n_dst = (num_wide, num_q4) if quantize else (num_q4, num_wide)
     rc = getattr(_lib or load(), fn)(src[0], src[1], dst[0], dst[1], block_size, hkv, d, n_src, n_dst,
-                                     pairs.data_ptr(), n // 2, code, 0 if dev_status is None else _opt(dev_status),
+                                     pairs.data_ptr(), n // 2, code, 0 if dev_status is None else _status(dev_status, dev),
                                      _raw_stream(dev) if stream is None else _stream(stream))
     if rc != OK:
         raise PAError(rc, fn)
@@ -597,7 +604,7 @@ def decode_q4(q, k_cache, v_cache, block_tables, context_lens, scale: float, out
     rc = (_lib or load()).pa_decode_q4(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         context_lens.data_ptr(), num_seqs, H, hkv, D, block_size, max_blocks, num_blocks, scale, code,
-        workspace.data_ptr(), workspace.nbytes, 0 if dev_status is None else _opt(dev_status),
+        workspace.data_ptr(), workspace.nbytes, 0 if dev_status is None else _status(dev_status, dev),
         _raw_stream(dev) if stream is None else _stream(stream))
     if rc != OK:
         raise PAError(rc, "pa_decode_q4")
