@@ -211,6 +211,8 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+// The largest scales that powers of two `up` take to less than 2^8 (bf16 pairs): exponent fields 261 - up's.
+__device__ __forceinline__ uint32_t cap_of(uint32_t up) { return 0x82ff82ffu - up; }
 __device__ __forceinline__ void cp_async16(uint32_t smem, const void *gmem) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
 }
@@ -470,6 +472,11 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
         float o[NT][2 * NG][4], m[NT][2], l[NT][2], sl[NT][2];   // sl: what brings the lane's columns to base-2 logits
         uint32_t far[NT];                                         // q-heads that leave 2^24 of it to the logits
         uint32_t up[NG / 2];                                      // the groups' powers of two for V's scales, bf16 pairs
+        uint32_t cap[NG / 2];                                     // the largest scales that `up` takes to less than 2^8
+        // What the compiler makes of the registers differs by form: with the units of a step taken downwards and the
+        // caps made from `up` each time, 16 x 32768 tokens (D = 128, groups up to 8) take 117.4 us, upwards with caps
+        // kept 122.0; for groups of 16 and 32 64 x 18750 tokens take 127 us that way and 121 this, fp32 147 and 141.
+        constexpr bool kDown = !S::kF32 && NT == 1 && D == 128, kKeepCaps = NT == 2;
         bool fresh = true, at_start = true;
         int u_first = 0;
         const uint8_t *st = ring;
@@ -497,11 +504,11 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
             const int valid = ctx - u * kU - (NU - 1) * kU;   // tokens of the last unit that exist
             constexpr int L = NU - 1;
 
-            // ---- S = K Q^T  (units downwards here and in the second product, and the scales of V loaded by a function:
-            // 117.4 us against 122.0 for 16 x 32768 tokens, by the order that comes of it)
+            // ---- S = K Q^T
             float x[NU][NT][4];
 #pragma unroll
-            for (int j = NU - 1; j >= 0; --j) {
+            for (int i = 0; i < NU; ++i) {
+                const int j = kDown ? NU - 1 - i : i;
                 uint32_t k0[NG], k1[NG], z0[NG / 2], z1[NG / 2];
                 if constexpr (D == 128) {
                     *reinterpret_cast<uint4 *>(k0) = *reinterpret_cast<const uint4 *>(at[j] + k_at);
@@ -608,10 +615,9 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                     uint32_t top = 0;   // (a NaN scale is no size)
 #pragma unroll
                     for (int j = 0; j < NU; ++j) top = max_bf16x2(top, max_bf16x2(vz0[j][g], vz1[j][g]));
-                    // exponent fields 261 - up's: the largest scales that `up` takes to less than 2^8
-                    const uint32_t cap = 0x82ff82ffu - up[g];
+                    const uint32_t most = kKeepCaps ? cap[g] : cap_of(up[g]);
                     move |= !__hble2(*reinterpret_cast<const __nv_bfloat162 *>(&top),
-                                     *reinterpret_cast<const __nv_bfloat162 *>(&cap));
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&most));
                 }
             }
             if (__any_sync(0xffffffffu, move)) {
@@ -631,6 +637,7 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                         beta[2 * g] = __uint_as_float((uint32_t)max(1, 127 + new0 - old0) << 23);
                         beta[2 * g + 1] = __uint_as_float((uint32_t)max(1, 127 + new1 - old1) << 23);
                         up[g] = (uint32_t)new0 << 7 | (uint32_t)new1 << 23;
+                        cap[g] = cap_of(up[g]);
                     }
                 }
 #pragma unroll
@@ -682,7 +689,8 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                     }
             // ---- O^T += V^T P^T
 #pragma unroll
-            for (int j = NU - 1; j >= 0; --j) {
+            for (int i = 0; i < NU; ++i) {
+                const int j = kDown ? NU - 1 - i : i;
                 const uint8_t *vc = at[j] + S::kCodes;
                 constexpr int NW = NG / 2;       // words of a lane's share of a V row
                 uint32_t vw[4][NW];
@@ -831,7 +839,10 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                     l[nt][0] = l[nt][1] = 0.0f;
                 }
 #pragma unroll
-                for (int g = 0; g < NG / 2; ++g) up[g] = 0x7e807e80u;   // 2^126: scales from 2^-118 up bring it down
+                for (int g = 0; g < NG / 2; ++g) {
+                    up[g] = 0x7e807e80u;   // 2^126: scales from 2^-118 up bring it down
+                    cap[g] = cap_of(up[g]);
+                }
             }
             const int pair = left > 1 && u + 1 < nu ? 2 : 1;
             if (pair == 2) step(std::integral_constant<int, 2>());
