@@ -57,10 +57,10 @@
 // several, and there is no second kernel.
 //
 // Measured (32 / 8 heads of 128, blocks of 16): 256 power-law sequences, 151 MB,
-// 40.4 us; 16 x 32768 tokens, 604 MB, 115 us = 5.3 TB/s, 0.79 of the copy peak,
-// at 61 % of the issue slots and 53 % of the ALU pipe, 300 instructions a unit
-// and warp; with the products left out its copies take 96 us.  A short request
-// takes 5.6 us.
+// 40.8 us; 16 x 32768 tokens, 604 MB, 116.5 us = 5.2 TB/s, 0.76 of the copy
+// peak, at 62 % of the issue slots and 55 % of the ALU pipe, 310 instructions a
+// unit and warp; with the products left out its copies take 96 us.  A short
+// request takes 5.6 us.
 //
 // fp32 queries: q and the weights are split into three bf16 parts each (24
 // bits), and the codes are brought to n - 8 one by one (0x4300 | n is 128 + n

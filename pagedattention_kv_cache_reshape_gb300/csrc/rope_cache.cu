@@ -15,9 +15,13 @@
 // them.  Rows that do not come in 16-byte pieces (head_dim or rot_dim no
 // multiple of 16, odd addresses or strides) take the element-wise kernel.
 // Measured: 8192 tokens of 32 + 8 + 8 rows of 128 bf16 (204 MB) 34.6 us, 5.9 TB/s;
-// 256 tokens 2.6 us.  Into 4-bit pools 8191 tokens take 43 us from cold caches at
-// 63 % of the issue slots: the keys' exact rotation and the codes cost it half as
-// many instructions again (29.1 M against 19.5 M).
+// 256 tokens 2.6 us; fp32 67 us, 6.0 TB/s.  Into 4-bit pools 8191 tokens take 43
+// us from cold caches at 63 % of the issue slots: the keys' exact rotation and
+// the codes cost it half as many instructions again (29.1 M against 19.5 M);
+// fp32 69 us.  Head sizes of other lanes: 32 + 8 + 8 rows of 96 30.0 us, of 192
+// 55.4.  The element-wise kernel is far slower: with 72 or 36 of the dims turned
+// the 8192 tokens take 165 us (neighbouring pairs 171-175), into 4-bit pools
+// 440-470.
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "q4_format.cuh"
@@ -292,7 +296,9 @@ cudaError_t launch_vec(const RopeArgs &a, int64_t kv_bytes, cudaStream_t stream)
         return dim3((rows * lanes + 31) / 32 * 32);
     };
     int rows, passes;
-    // two tokens a CTA once one each would fill the GPU several times over: twice the loads in flight
+    // Two tokens a CTA once one each would fill the GPU several times over: twice the loads in flight.  32 + 8 + 8
+    // rows of 128 bf16, one a CTA against two: 608 tokens 4.7 and 7.2 us, 912 6.4 and 7.7, 1216 8.1 and 8.1, 1520 9.9
+    // and 8.5, 2432 15.0 and 9.8; into 4-bit pools 912 8.3 and 10.7, 1216 10.6 and 11.1, 1520 13.0 and 11.7.
     if (a.num_tokens >= 8 * device_sm_count() && 2 * kv_bytes <= 48 * 1024) {
         const dim3 block = shape(vec_threads(2), rows, passes);
         return launch_dependent(rope_cache_vec_kernel<T, kQ4, 2>, dim3((a.num_tokens + 1) / 2), block,
