@@ -767,11 +767,12 @@ __global__ void __launch_bounds__(Q4Shape<T, D, NT>::kWarps * 32, 1) q4_decode_k
                         for (int d = 0; d < 8; ++d) most = fmaxf(most, fabsf(x[g][d]));
                     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
                     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                    // Exponent fields: of the factor that brings `most` into [2^14, 2^15) (fp32 calls: [1, 2)), and of
-                    // its inverse, times the 2^24 that the codes carry.  An inverse with the scale past the largest fp32
-                    // leaves 2^24 of itself to the logits (`far`: the q-heads that do, four bits each).
+                    // Exponent fields: of the factor that brings `most` into [2^14, 2^15) (fp32 calls: [2^-9, 2^-8), where a
+                    // group's sum over its codes stays below 1), and of its inverse, times the 2^24 that the codes of bf16
+                    // calls carry.  An inverse with the scale past the largest fp32 leaves 2^24 of itself to the logits
+                    // (`far`: the q-heads that do, four bits each).
                     const int e = (int)(__float_as_uint(most) >> 23);
-                    const int lift_q = S::kF32 ? max(1, min(253, 254 - e)) : min(254, 268 - e);
+                    const int lift_q = S::kF32 ? max(1, 245 - e) : min(254, 268 - e);
                     const int inverse = (S::kF32 ? 254 : 278) - lift_q;
                     float up_q = __uint_as_float((uint32_t)lift_q << 23);
                     float back = __uint_as_float((uint32_t)min(254, inverse) << 23) * p.scale_log2;

@@ -33,6 +33,22 @@ def test_queries_and_keys_of_opposite_size(e, H, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("e", [-124, -110, 0, 110, 123])
+def test_keys_along_the_query(e, dtype):
+    """Keys of the queries' signs: every product of a row adds to the one sum, and the codes are the largest."""
+    c = Case([40, 500], 2, 2, 128, 16, dtype, seed=86)
+    c.q[:] = c.q[0]
+    c.q *= 2.0 ** e
+    g = torch.Generator().manual_seed(87)
+    size = 0.7 + 0.3 * torch.rand(c.nb, 16, 2, 1, generator=g).to(DEV)
+    k = torch.sign(c.q[0].float()) * size * 2.0 ** -e
+    v = torch.randn(c.nb, 16, 2, 128, generator=g).to(DEV)
+    ident = torch.arange(c.nb, dtype=torch.int32, device=DEV)[:, None].repeat(1, 2).contiguous()
+    pa.quantize_blocks_q4(k, v, c.k4, c.v4, ident)
+    check(c, c.run(), what=f"2^{e}")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_heads_of_all_sizes_side_by_side(dtype):
     """Heads of one kv-head whose queries differ by powers of two up to 2^224: logits from nothing to several units."""
     c = Case([300], 8, 1, 128, 16, dtype, seed=82)
