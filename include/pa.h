@@ -288,6 +288,31 @@ PA_API pa_status pa_rope_and_cache(void *q_out, const void *q, const void *key, 
                                    pa_dtype dtype, int32_t *dev_status, pa_stream_t stream);
 
 /*
+ * pa_rope_and_cache for tokens with a position on several axes (time, height
+ * and width of a picture or a video's frames, say): pair i, i < R, of token t
+ * turns by the position of its own axis,
+ *     p = positions[pair_axis[i] * positions_stride_axis + t],
+ * in place of positions[t]; all else is as there.  Any assignment of the pairs
+ * to axes can be given: sections, axes taking turns, or a mixture.
+ *  positions  device int32, num_axes rows of num_tokens, a row every
+ *             positions_stride_axis elements (>= 0; 0: one row for all axes)
+ *  pair_axis  device int32 [R], entries 0 .. num_axes - 1 (unused with rot_dim 0)
+ *  num_axes   1 .. 4 (PA_ERR_UNSUPPORTED above)
+ * A live token with a position outside [0, max_position) on any axis, used or
+ * not, sets PA_ERR_OUT_OF_RANGE and is skipped; a pair_axis entry out of range
+ * does so for every live token.
+ */
+PA_API pa_status pa_mrope_and_cache(void *q_out, const void *q, const void *key, const void *value,
+                                    int64_t q_stride_tok, int64_t key_stride_tok,
+                                    int64_t value_stride_tok, const float *cos_sin,
+                                    const int32_t *positions, int64_t positions_stride_axis,
+                                    const int32_t *pair_axis, int num_axes, int max_position,
+                                    int rot_dim, int interleaved, void *k_cache, void *v_cache,
+                                    const int64_t *slot_mapping, int num_tokens, int num_heads,
+                                    int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                    pa_dtype dtype, int32_t *dev_status, pa_stream_t stream);
+
+/*
  * The cache held in 4 bits.  A 4-bit pool is device memory of num_blocks
  * blocks of pa_q4_block_bytes(...) bytes, 16-byte aligned, laid out
  * [num_blocks][num_kv_heads] slabs; a slab is B = block_size token rows of
@@ -324,6 +349,21 @@ PA_API pa_status pa_rope_and_cache_q4(void *q_out, const void *q, const void *ke
                                       const int64_t *slot_mapping, int num_tokens, int num_heads,
                                       int num_kv_heads, int head_dim, int block_size, int num_blocks,
                                       pa_dtype dtype, int32_t *dev_status, pa_stream_t stream);
+
+/*
+ * pa_mrope_and_cache into 4-bit pools, as pa_rope_and_cache_q4 is
+ * pa_rope_and_cache into them: the result equals pa_mrope_and_cache into
+ * 16/32-bit pools followed by pa_quantize_blocks_q4, bit for bit.
+ */
+PA_API pa_status pa_mrope_and_cache_q4(void *q_out, const void *q, const void *key, const void *value,
+                                       int64_t q_stride_tok, int64_t key_stride_tok,
+                                       int64_t value_stride_tok, const float *cos_sin,
+                                       const int32_t *positions, int64_t positions_stride_axis,
+                                       const int32_t *pair_axis, int num_axes, int max_position,
+                                       int rot_dim, int interleaved, void *k_cache, void *v_cache,
+                                       const int64_t *slot_mapping, int num_tokens, int num_heads,
+                                       int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                       pa_dtype dtype, int32_t *dev_status, pa_stream_t stream);
 
 /*
  * Whole blocks from 16/32-bit pools to 4-bit pools: for each pair i, (src, dst)

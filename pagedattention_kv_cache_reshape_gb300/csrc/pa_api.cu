@@ -319,7 +319,8 @@ pa_status rope_and_cache(const RopeArgs &a, bool q4, pa_stream_t stream) {
     if (!aligned(a.key, eb) || !aligned(a.value, eb) || !aligned(a.k_cache, pool_align) ||
         !aligned(a.v_cache, pool_align) || !aligned(a.slot_mapping, 8))
         return PA_ERR_INVALID_ARG;
-    if (a.rot_dim > 0 && (!aligned(a.cos_sin, 4) || !aligned(a.positions, 4))) return PA_ERR_INVALID_ARG;
+    if (a.rot_dim > 0 && (!aligned(a.cos_sin, 4) || !aligned(a.positions, 4) || !aligned(a.pair_axis, 4)))
+        return PA_ERR_INVALID_ARG;
     if (a.num_heads > 0) {
         if (!aligned(a.q, eb) || !aligned(a.q_out, eb)) return PA_ERR_INVALID_ARG;
         // in place (the same contiguous rows) or apart; nothing between
@@ -332,6 +333,13 @@ pa_status rope_and_cache(const RopeArgs &a, bool q4, pa_stream_t stream) {
             return PA_ERR_INVALID_ARG;
     }
     return from_cuda(launch_rope_and_cache(a, q4, (cudaStream_t)stream));
+}
+
+pa_status mrope_and_cache(const RopeArgs &a, bool q4, pa_stream_t stream) {
+    if (a.num_axes <= 0 || a.axis_stride < 0) return PA_ERR_INVALID_ARG;
+    if (a.num_axes > kMaxAxes) return PA_ERR_UNSUPPORTED;
+    if (a.rot_dim > 0 && a.num_tokens > 0 && !a.pair_axis) return PA_ERR_INVALID_ARG;
+    return rope_and_cache(a, q4, stream);
 }
 
 pa_status q4_blocks(const Q4BlocksArgs &a, bool quantize, pa_stream_t stream) {
@@ -377,6 +385,34 @@ pa_status pa_rope_and_cache_q4(void *q_out, const void *q, const void *key, cons
                      max_position, rot_dim, interleaved, k_cache, v_cache, slot_mapping, num_tokens, num_heads,
                      num_kv_heads, head_dim, block_size, num_blocks, dtype, dev_status};
     return rope_and_cache(a, true, stream);
+}
+
+pa_status pa_mrope_and_cache(void *q_out, const void *q, const void *key, const void *value,
+                             int64_t q_stride_tok, int64_t key_stride_tok, int64_t value_stride_tok,
+                             const float *cos_sin, const int32_t *positions, int64_t positions_stride_axis,
+                             const int32_t *pair_axis, int num_axes, int max_position, int rot_dim,
+                             int interleaved, void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                             int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                             int num_blocks, pa_dtype dtype, int32_t *dev_status, pa_stream_t stream) {
+    const RopeArgs a{q_out, q, key, value, q_stride_tok, key_stride_tok, value_stride_tok, cos_sin, positions,
+                     max_position, rot_dim, interleaved, k_cache, v_cache, slot_mapping, num_tokens, num_heads,
+                     num_kv_heads, head_dim, block_size, num_blocks, dtype, dev_status, pair_axis,
+                     positions_stride_axis, num_axes};
+    return mrope_and_cache(a, false, stream);
+}
+
+pa_status pa_mrope_and_cache_q4(void *q_out, const void *q, const void *key, const void *value,
+                                int64_t q_stride_tok, int64_t key_stride_tok, int64_t value_stride_tok,
+                                const float *cos_sin, const int32_t *positions, int64_t positions_stride_axis,
+                                const int32_t *pair_axis, int num_axes, int max_position, int rot_dim,
+                                int interleaved, void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                                int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                int num_blocks, pa_dtype dtype, int32_t *dev_status, pa_stream_t stream) {
+    const RopeArgs a{q_out, q, key, value, q_stride_tok, key_stride_tok, value_stride_tok, cos_sin, positions,
+                     max_position, rot_dim, interleaved, k_cache, v_cache, slot_mapping, num_tokens, num_heads,
+                     num_kv_heads, head_dim, block_size, num_blocks, dtype, dev_status, pair_axis,
+                     positions_stride_axis, num_axes};
+    return mrope_and_cache(a, true, stream);
 }
 
 pa_status pa_quantize_blocks_q4(const void *src_k, const void *src_v, void *dst_k, void *dst_v, int block_size,

@@ -161,7 +161,12 @@ struct RopeArgs {
     int num_blocks;
     pa_dtype dtype;
     int32_t *status;
+    // several position axes: pair i turns by positions[pair_axis[i] * axis_stride + t]; null: one position a token
+    const int32_t *pair_axis = nullptr;
+    int64_t axis_stride = 0;
+    int num_axes = 1;
 };
+constexpr int kMaxAxes = 4;
 // q4: the pools hold 4-bit rows (q4_format.cuh); head_dim 64 or 128 then.
 cudaError_t launch_rope_and_cache(const RopeArgs &a, bool q4, cudaStream_t stream);
 

@@ -6,7 +6,10 @@
 //     a' = a cos_i - b sin_i,   b' = b cos_i + a sin_i,
 // cos_i = cos_sin[p][i], sin_i = cos_sin[p][R + i]; dims from rot_dim on pass
 // through.  The row is rounded to the inputs' type and stored like
-// reshape_and_cache's, or quantised from there (q4_format.cuh).
+// reshape_and_cache's, or quantised from there (q4_format.cuh).  With several
+// position axes (kAxes) pair i takes p = positions[pair_axis[i]][t], so a token's
+// cosines and sines come from up to four rows of the table: they are gathered
+// once a token into shared memory, where all its heads read them.
 //
 // Bound by HBM: every row is read and written once.  A thread of the fast
 // kernel owns the two vectors of 8 dims whose elements pair up, so it needs 8
@@ -69,8 +72,27 @@ __device__ __forceinline__ void turn(float &a, float &b, float c, float s, bool 
     }
 }
 
-template <typename T, bool kQ4>
-__device__ __forceinline__ float rotated(const RopeArgs &a, const T *row, const float *cs, int d) {
+// Cosine and sine of pair i of token t: from the row `cs` of its position or, with several axes, from the row that
+// the pair's own axis names.
+template <bool kAxes>
+__device__ __forceinline__ float2 angle(const RopeArgs &a, const float *cs, int t, int i) {
+    if (kAxes) cs = a.cos_sin + (int64_t)__ldg(a.positions + __ldg(a.pair_axis + i) * a.axis_stride + t) * a.rot_dim;
+    return make_float2(__ldg(cs + i), __ldg(cs + a.rot_dim / 2 + i));
+}
+
+// Whether token t's position, on every axis, lies in the table.
+template <bool kAxes>
+__device__ __forceinline__ bool positions_in_table(const RopeArgs &a, int t) {
+    bool ok = true;
+    for (int x = 0; x < (kAxes ? a.num_axes : 1); ++x) {
+        const int p = __ldg(a.positions + x * a.axis_stride + t);
+        ok = ok && p >= 0 && p < a.max_position;
+    }
+    return ok;
+}
+
+template <typename T, bool kQ4, bool kAxes>
+__device__ __forceinline__ float rotated(const RopeArgs &a, const T *row, const float *cs, int t, int d) {
     const int R = a.rot_dim / 2;
     const float x = to_float(row[d]);
     if (d >= a.rot_dim) return x;
@@ -79,23 +101,32 @@ __device__ __forceinline__ float rotated(const RopeArgs &a, const T *row, const 
     if (a.interleaved) { i = d >> 1; first = (d & 1) == 0; o = d ^ 1; }
     else { first = d < R; i = first ? d : d - R; o = first ? d + R : d - R; }
     const float y = to_float(row[o]);
-    return rotate_exact<kQ4>(x, cs[i], y, first ? -cs[R + i] : cs[R + i]);
+    const float2 g = angle<kAxes>(a, cs, t, i);
+    return rotate_exact<kQ4>(x, g.x, y, first ? -g.y : g.y);
 }
 
 // Any shape, element by element: one CTA per token.
-template <typename T, bool kQ4>
+template <typename T, bool kQ4, bool kAxes>
 __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) {
     grid_dependency_wait();
     grid_dependents_launch();
     const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t slot = a.slot_mapping[t];
     if (slot < 0) return;   // padding token
-    const int pos = a.rot_dim > 0 ? a.positions[t] : 0;
-    if (slot >= (int64_t)a.num_blocks * a.block_size || pos < 0 || (a.rot_dim > 0 && pos >= a.max_position)) {
+    bool bad = slot >= (int64_t)a.num_blocks * a.block_size || (a.rot_dim > 0 && !positions_in_table<kAxes>(a, t));
+    if (kAxes) {
+        int wrong = 0;
+        for (int i = tid; i < a.rot_dim / 2; i += kThreads) {
+            const int x = __ldg(a.pair_axis + i);
+            wrong |= x < 0 || x >= a.num_axes;
+        }
+        bad = __syncthreads_or(wrong) || bad;
+    }
+    if (bad) {
         if (tid == 0) set_status(a.status, PA_ERR_OUT_OF_RANGE);
         return;
     }
-    const float *cs = a.cos_sin + (int64_t)pos * a.rot_dim;
+    const float *cs = !kAxes && a.rot_dim > 0 ? a.cos_sin + (int64_t)a.positions[t] * a.rot_dim : a.cos_sin;
     const int D = a.head_dim;
     // queries: a thread owns both dims of a pair (q_out may be q)
     for (int64_t e = tid; e < (int64_t)a.num_heads * D; e += kThreads) {
@@ -108,7 +139,8 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) 
         const int o = a.interleaved ? d + 1 : d + R;
         const int i = a.interleaved ? d >> 1 : d;
         float x = to_float(row[d]), y = to_float(row[o]);
-        turn<kQ4>(x, y, cs[i], cs[R + i], true);
+        const float2 g = angle<kAxes>(a, cs, t, i);
+        turn<kQ4>(x, y, g.x, g.y, true);
         out[d] = from_float<T>(x);
         out[o] = from_float<T>(y);
     }
@@ -119,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) 
         T *vd = static_cast<T *>(a.v_cache) + slot * ((int64_t)a.num_kv_heads * D);
         for (int64_t e = tid; e < (int64_t)a.num_kv_heads * D; e += kThreads) {
             const int h = (int)(e / D), d = (int)(e - (int64_t)h * D);
-            kd[e] = from_float<T>(rotated<T, kQ4>(a, key + (int64_t)h * D, cs, d));
+            kd[e] = from_float<T>(rotated<T, kQ4, kAxes>(a, key + (int64_t)h * D, cs, t, d));
             vd[e] = value[e];
         }
         return;
@@ -136,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) 
         Raw8<T> x[2];
         for (int i = 0; i < 16; ++i)
             reinterpret_cast<T *>(x)[i] = is_v ? value[(int64_t)h * D + 16 * k + i]
-                                               : from_float<T>(rotated<T, kQ4>(a, key + (int64_t)h * D, cs, 16 * k + i));
+                                               : from_float<T>(rotated<T, kQ4, kAxes>(a, key + (int64_t)h * D, cs, t, 16 * k + i));
         uint8_t *s = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) + (blk * a.num_kv_heads + h) * slab;
         uint8_t *row = s + off * q4_row_bytes(D);
         uint16_t *scales = reinterpret_cast<uint16_t *>(s + a.block_size * q4_row_bytes(D)) + off * (D / kQ4Group);
@@ -145,11 +177,11 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a) 
     }
 }
 
-// The two vectors of 8 that a thread owns, turned and rounded to T.
+// The two vectors of 8 that a thread owns, turned and rounded to T; `cs` is the token's row of cosines and sines.
 template <typename T, bool kQ4>
-__device__ __forceinline__ void turn_rows(Raw8<T> &rx, Raw8<T> &ry, const RopeArgs &a, int pos, int j, bool is_q) {
+__device__ __forceinline__ void turn_rows(Raw8<T> &rx, Raw8<T> &ry, const RopeArgs &a, const float *cs, int j, bool is_q) {
     float c[8], s[8], x[8], y[8];
-    const float *cs = a.cos_sin + (int64_t)pos * a.rot_dim + 8 * j;
+    cs += 8 * j;
     to_floats(c, load_raw8(cs));
     to_floats(s, load_raw8(cs + a.rot_dim / 2));
     to_floats(x, rx);
@@ -168,6 +200,47 @@ __device__ __forceinline__ void turn_rows(Raw8<T> &rx, Raw8<T> &ry, const RopeAr
     ry = from_floats<T>(y);
 }
 
+// Several axes: the cosines and sines of tokens t0 .. t0 + U - 1, each from its pair's own row of the table, into
+// cs_s [U][rot_dim], by every thread of the CTA.  A token's positions are read by all threads alike, its axes by the
+// threads that use them, both at once, so the table's rows wait on one round trip only.  pos[u] becomes -1 where a
+// position, or an axis of any pair, is out of range (nothing is gathered through it then), else 0.
+template <int U>
+__device__ __forceinline__ void gather_angles(const RopeArgs &a, int t0, const int64_t (&slot)[U], int (&pos)[U], float *cs_s) {
+    int p[U][kMaxAxes];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int x = 0; x < kMaxAxes; ++x)   // (slot -1: padding, or no token)
+            p[u][x] = x < a.num_axes && slot[u] >= 0 ? __ldg(a.positions + x * a.axis_stride + t0 + u) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        pos[u] = 0;
+#pragma unroll
+        for (int x = 0; x < kMaxAxes; ++x)
+            if (p[u][x] < 0 || p[u][x] >= a.max_position) pos[u] = -1;
+    }
+    const int R = a.rot_dim / 2;
+    int wrong = 0;
+    for (int e = threadIdx.x; e < a.rot_dim; e += blockDim.x) {
+        const int x = __ldg(a.pair_axis + (e < R ? e : e - R));
+        const bool ok = x >= 0 && x < a.num_axes;
+        wrong |= !ok;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (ok && slot[u] >= 0 && pos[u] == 0) {
+                int64_t at = p[u][0];
+#pragma unroll
+                for (int k = 1; k < kMaxAxes; ++k) at = x == k ? p[u][k] : at;
+                cs_s[u * a.rot_dim + e] = __ldg(a.cos_sin + at * a.rot_dim + e);
+            }
+    }
+    if (__syncthreads_or(wrong)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) pos[u] = -1;
+    }
+}
+
 // One CTA per U tokens, `passes` x `rows` head rows of a token at a time, D / 16 threads a row.  Rows 0 ..
 // num_heads - 1 are queries, then keys, then values.  Thread j of a row, j < rot_dim / 16: the rotated vectors 8 j
 // and R + 8 j (halves) or 16 j and 16 j + 8 (interleaved); the others: the vectors from rot_dim on.  The rows are
@@ -175,10 +248,11 @@ __device__ __forceinline__ void turn_rows(Raw8<T> &rx, Raw8<T> &ry, const RopeAr
 // as a whole or not at all are quantised by the lanes that hold them (a group is 2 or 4 neighbouring lanes);
 // kQ4 = 2: with rot_dim between, the rotated keys and the values meet in shared memory, where 16 consecutive dims
 // go to a lane.
-template <typename T, int kQ4, int U>
+template <typename T, int kQ4, int U, bool kAxes>
 __global__ void __launch_bounds__(vec_threads(U), U == 1 ? 2 : 16) rope_cache_vec_kernel(const RopeArgs a, int rows, int passes) {
     extern __shared__ __align__(16) uint8_t smem[];
-    T *kv_s = reinterpret_cast<T *>(smem);   // [U][2 num_kv_heads][D], kQ4 = 2 only
+    float *cs_s = reinterpret_cast<float *>(smem);   // [U][rot_dim], kAxes only
+    T *kv_s = reinterpret_cast<T *>(cs_s + (kAxes ? U * a.rot_dim : 0));   // [U][2 num_kv_heads][D], kQ4 = 2 only
     const int D = a.head_dim, lanes = D / 16, tid = threadIdx.x;
     const int row0 = tid / lanes, j = tid - row0 * lanes, R = a.rot_dim / 2;
     const int H = a.num_heads, HK = a.num_kv_heads, all = H + 2 * HK;
@@ -190,8 +264,11 @@ __global__ void __launch_bounds__(vec_threads(U), U == 1 ? 2 : 16) rope_cache_ve
     grid_dependency_wait();
     grid_dependents_launch();
     int64_t slot[U];
-    int pos[U];
+    int pos[U];   // several axes: 0, or -1 for a token with a position or an axis out of range
     bool live[U];
+    auto angles = [&](int u) -> const float * {
+        return kAxes ? cs_s + u * a.rot_dim : a.cos_sin + (int64_t)pos[u] * a.rot_dim;
+    };
     for (int pass = 0; pass < passes; ++pass) {
         const int row = row0 + pass * rows;
         const bool mine = row0 < rows && row < all;
@@ -211,8 +288,9 @@ __global__ void __launch_bounds__(vec_threads(U), U == 1 ? 2 : 16) rope_cache_ve
             for (int u = 0; u < U; ++u) {
                 const bool in = t0 + u < a.num_tokens;
                 slot[u] = in ? __ldg(a.slot_mapping + t0 + u) : -1;
-                pos[u] = in && a.rot_dim > 0 ? __ldg(a.positions + t0 + u) : 0;
+                pos[u] = !kAxes && in && a.rot_dim > 0 ? __ldg(a.positions + t0 + u) : 0;
             }
+            if (kAxes) gather_angles<U>(a, t0, slot, pos, cs_s);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 live[u] = slot[u] >= 0;   // else padding
@@ -229,7 +307,7 @@ __global__ void __launch_bounds__(vec_threads(U), U == 1 ? 2 : 16) rope_cache_ve
         for (int u = 0; u < U; ++u) {
             if (!live[u]) continue;   // the same in every thread
             if (kQ4 == 1) {
-                if (mine && turns && !is_v) turn_rows<T, kQ4 != 0>(rx[u], ry[u], a, pos[u], j, is_q);
+                if (mine && turns && !is_v) turn_rows<T, kQ4 != 0>(rx[u], ry[u], a, angles(u), j, is_q);
                 if (mine && is_q) {
                     T *dst = static_cast<T *>(a.q_out) + ((int64_t)(t0 + u) * H + h) * D;
                     store_raw8(dst + d0, rx[u]);
@@ -257,7 +335,7 @@ __global__ void __launch_bounds__(vec_threads(U), U == 1 ? 2 : 16) rope_cache_ve
             if (is_q) dst = static_cast<T *>(a.q_out) + ((int64_t)(t0 + u) * H + h) * D;
             else if (kQ4 == 2) dst = kv_s + (u * 2 * HK + row - H) * D;
             else dst = static_cast<T *>(is_v ? a.v_cache : a.k_cache) + (slot[u] * HK + h) * D;
-            if (turns && !is_v) turn_rows<T, kQ4 != 0>(rx[u], ry[u], a, pos[u], j, is_q);
+            if (turns && !is_v) turn_rows<T, kQ4 != 0>(rx[u], ry[u], a, angles(u), j, is_q);
             store_raw8(dst + d0, rx[u]);
             store_raw8(dst + d1, ry[u]);
         }
@@ -283,8 +361,9 @@ __global__ void __launch_bounds__(vec_threads(U), U == 1 ? 2 : 16) rope_cache_ve
     }
 }
 
-template <typename T, int kQ4>
+template <typename T, int kQ4, bool kAxes>
 cudaError_t launch_vec(const RopeArgs &a, int64_t kv_bytes, cudaStream_t stream) {
+    const int64_t cs_bytes = kAxes ? (int64_t)a.rot_dim * sizeof(float) : 0;   // a token's cosines and sines
     const int lanes = a.head_dim / 16;
     const int64_t all = (int64_t)a.num_heads + 2 * a.num_kv_heads;
     // whole rows a pass, evened out over the passes: rows <= threads / lanes, so that a CTA, rounded up to whole warps,
@@ -299,39 +378,43 @@ cudaError_t launch_vec(const RopeArgs &a, int64_t kv_bytes, cudaStream_t stream)
     // Two tokens a CTA once one each would fill the GPU several times over: twice the loads in flight.  32 + 8 + 8
     // rows of 128 bf16, one a CTA against two: 608 tokens 4.7 and 7.2 us, 912 6.4 and 7.7, 1216 8.1 and 8.1, 1520 9.9
     // and 8.5, 2432 15.0 and 9.8; into 4-bit pools 912 8.3 and 10.7, 1216 10.6 and 11.1, 1520 13.0 and 11.7.
-    if (a.num_tokens >= 8 * device_sm_count() && 2 * kv_bytes <= 48 * 1024) {
+    if (a.num_tokens >= 8 * device_sm_count() && 2 * (kv_bytes + cs_bytes) <= 48 * 1024) {
         const dim3 block = shape(vec_threads(2), rows, passes);
-        return launch_dependent(rope_cache_vec_kernel<T, kQ4, 2>, dim3((a.num_tokens + 1) / 2), block,
-                                (size_t)(2 * kv_bytes), stream, a, rows, passes);
+        return launch_dependent(rope_cache_vec_kernel<T, kQ4, 2, kAxes>, dim3((a.num_tokens + 1) / 2), block,
+                                (size_t)(2 * (kv_bytes + cs_bytes)), stream, a, rows, passes);
     }
     const dim3 block = shape(vec_threads(1), rows, passes);
-    return launch_dependent(rope_cache_vec_kernel<T, kQ4, 1>, dim3(a.num_tokens), block, (size_t)kv_bytes, stream, a,
-                            rows, passes);
+    return launch_dependent(rope_cache_vec_kernel<T, kQ4, 1, kAxes>, dim3(a.num_tokens), block,
+                            (size_t)(kv_bytes + cs_bytes), stream, a, rows, passes);
 }
 
-template <typename T>
+template <typename T, bool kAxes>
 cudaError_t launch_typed(const RopeArgs &a, bool q4, cudaStream_t stream) {
     // the fast kernel's rows come in 16-byte pieces; a token's keys and values fit shared memory
     const bool whole = a.rot_dim == 0 || a.rot_dim == a.head_dim;
     const int64_t kv_bytes = q4 && !whole ? (int64_t)2 * a.num_kv_heads * a.head_dim * sizeof(T) : 0;
     auto in16 = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
     const int64_t e = sizeof(T);
-    bool vec = a.head_dim % 16 == 0 && a.rot_dim % 16 == 0 && a.head_dim <= 512 && kv_bytes <= 48 * 1024 &&
+    bool vec = a.head_dim % 16 == 0 && a.rot_dim % 16 == 0 && a.head_dim <= 512 &&
+               kv_bytes + (kAxes ? a.rot_dim * (int64_t)sizeof(float) : 0) <= 48 * 1024 &&
                a.key_stride * e % 16 == 0 && a.value_stride * e % 16 == 0 && in16(a.key) && in16(a.value) &&
                in16(a.k_cache) && in16(a.v_cache) && (a.rot_dim == 0 || in16(a.cos_sin));
     if (a.num_heads > 0) vec = vec && a.q_stride * e % 16 == 0 && in16(a.q) && in16(a.q_out);
-    if (vec && q4) return whole ? launch_vec<T, 1>(a, 0, stream) : launch_vec<T, 2>(a, kv_bytes, stream);
-    if (vec) return launch_vec<T, 0>(a, 0, stream);
+    if (vec && q4) return whole ? launch_vec<T, 1, kAxes>(a, 0, stream) : launch_vec<T, 2, kAxes>(a, kv_bytes, stream);
+    if (vec) return launch_vec<T, 0, kAxes>(a, 0, stream);
     const dim3 grid(a.num_tokens), block(kThreads);
-    return q4 ? launch_dependent(rope_cache_kernel<T, true>, grid, block, 0, stream, a)
-              : launch_dependent(rope_cache_kernel<T, false>, grid, block, 0, stream, a);
+    return q4 ? launch_dependent(rope_cache_kernel<T, true, kAxes>, grid, block, 0, stream, a)
+              : launch_dependent(rope_cache_kernel<T, false, kAxes>, grid, block, 0, stream, a);
 }
 
 }  // namespace
 
 cudaError_t launch_rope_and_cache(const RopeArgs &a, bool q4, cudaStream_t stream) {
     if (a.num_tokens == 0) return cudaSuccess;
-    return a.dtype == PA_DTYPE_BF16 ? launch_typed<__nv_bfloat16>(a, q4, stream) : launch_typed<float>(a, q4, stream);
+    const bool axes = a.pair_axis != nullptr && a.rot_dim > 0;
+    if (a.dtype == PA_DTYPE_BF16)
+        return axes ? launch_typed<__nv_bfloat16, true>(a, q4, stream) : launch_typed<__nv_bfloat16, false>(a, q4, stream);
+    return axes ? launch_typed<float, true>(a, q4, stream) : launch_typed<float, false>(a, q4, stream);
 }
 
 }  // namespace pa
