@@ -201,6 +201,51 @@ PA_API pa_status pa_decode_static_scratch(void *out, const void *q, const void *
                                           pa_stream_t stream);
 
 /*
+ * Workspace bytes pa_decode_shared_prefix needs for these sizes (0 is never
+ * returned).
+ */
+PA_API size_t pa_decode_shared_prefix_workspace_size(int num_seqs, int num_groups, int num_heads,
+                                                     int num_kv_heads, int head_dim, int block_size,
+                                                     int max_blocks);
+
+/*
+ * pa_decode of a batch in which neighbouring sequences begin with the same
+ * blocks ([kwkr] §1.3: blocks referenced read-only by several block tables, a
+ * shared system prompt; pa_share_prefix makes such tables).  Sequences
+ * group_starts[g] .. group_starts[g+1]-1 form group g and have their first
+ * prefix_lens[g] tokens in common: what the group's rows see there is read
+ * and computed once, as one product for all of them, and joined with each
+ * sequence's own part by the log-sum-exp rule of pa_decode.  The result is
+ * pa_decode's up to rounding.
+ *  group_starts  device int32 [num_groups + 1], from 0 to num_seqs in order
+ *                (empty groups are allowed; a sequence that shares nothing may
+ *                stand in any group with prefix length 0)
+ *  prefix_lens   device int32 [num_groups], 0 .. max_blocks * block_size.  Only
+ *                whole blocks, and no sequence's last token, are taken as
+ *                shared, so any length up to the true one will do.
+ *  block_tables  as for pa_decode, every row whole: entries of a group's shared
+ *                blocks are read from the row of its first sequence
+ *  workspace     >= pa_decode_shared_prefix_workspace_size(...) bytes, 16-byte
+ *                aligned; its contents on entry do not matter; calls that may
+ *                overlap on the GPU take workspaces of their own
+ * The rest as for pa_decode: a context length out of range leaves its row as
+ * it was.  group_starts that are not in order, or a prefix length out of
+ * range, set PA_ERR_OUT_OF_RANGE in *dev_status, and the call (the group) is
+ * computed as if nothing were shared.  Precondition (not checked on the
+ * device): the blocks that hold a group's shared tokens are the same in all
+ * its tables, or hold the same tokens.  Results are deterministic: they depend
+ * on the inputs and the device's SM count, never on which blocks hold the data.
+ */
+PA_API pa_status pa_decode_shared_prefix(void *out, const void *q, const void *k_cache,
+                                         const void *v_cache, const int32_t *block_tables,
+                                         const int32_t *context_lens, const int32_t *group_starts,
+                                         const int32_t *prefix_lens, int num_seqs, int num_groups,
+                                         int num_heads, int num_kv_heads, int head_dim,
+                                         int block_size, int max_blocks, int num_blocks, float scale,
+                                         pa_dtype dtype, void *workspace, size_t workspace_bytes,
+                                         int32_t *dev_status, pa_stream_t stream);
+
+/*
  * One decode step in one call: exactly pa_compute_slot_mapping, then
  * pa_reshape_and_cache of the step's new tokens, then pa_decode (same
  * arguments, same results; slot_mapping is written as an output).  On the

@@ -1,0 +1,603 @@
+// attn_shared.cu -- decode attention for a batch whose sequences share
+// prefixes: what a group of sequences has in common is read and computed once
+// for all of them.
+//
+// For query row (s, h), kv-head g(h), group c of s with C = C_c shared tokens
+// (shared_plan.cuh), softmax weights of the two parts of the context add up
+// when both are kept as (m, l, o) = (max x, sum 2^{x - m}, sum 2^{x - m} V):
+//     M = max m_i,  out = sum 2^{m_i - M} o_i / sum 2^{m_i - M} l_i
+// over the pieces i of keys 0 .. C-1 (the group's rows together: a matrix
+// product whose K and V come from memory once) and of C .. ctx-1 (the
+// sequence's own rows).
+//
+// shared_plan_kernel   C_c, and the two streams of key tiles
+// shared_cc_kernel     CUDA-core products, any dtype (fp32 in and out of them):
+//                      each persistent CTA takes an equal share of both streams
+// shared_merge_kernel  a warp a row: the row's pieces in stream order
+#include <math.h>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+#include "shared_plan.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanSmemGroups = 4096;   // group starts and smallest contexts kept in shared memory
+constexpr int kMaxCtas = 512;           // partial slots reserved for share boundaries
+
+size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// ------------------------------------------------------------------ plan
+// Exclusive scan of v over the CTA (1024 threads); `total` the sum.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *warp_tot, int64_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+    }
+    __syncthreads();   // the previous scan's totals have been read
+    if (lane == 31) warp_tot[warp] = incl;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        const int64_t t = warp_tot[w];
+        if (w < warp) before += t;
+        total += t;
+    }
+    return before + incl - v;
+}
+
+// One CTA.  Group starts that do not run from 0 to num_seqs in order leave
+// every sequence unshared (and set the status); so does a prefix length out of
+// range for its group.
+__global__ void __launch_bounds__(kPlanThreads)
+    shared_plan_kernel(const SharedGroups g, const SharedPlan plan, int32_t *status) {
+    __shared__ int32_t starts_s[kPlanSmemGroups + 1], min_s[kPlanSmemGroups];
+    __shared__ int64_t warp_tot[kPlanThreads / 32];
+    const int tid = threadIdx.x;
+    const int S = g.num_seqs, NG = g.num_groups;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const bool in_smem = NG <= kPlanSmemGroups;
+    int32_t *min_ctx = in_smem ? min_s : plan.min_ctx;
+    int wrong = 0;
+    for (int i = tid; i < NG; i += kPlanThreads) {
+        const int a = __ldg(g.starts + i), b = __ldg(g.starts + i + 1);
+        wrong |= a < 0 || b < a || b > S || (i == 0 && a != 0) || (i == NG - 1 && b != S);
+        if (in_smem) starts_s[i] = a;
+        min_ctx[i] = INT_MAX;
+    }
+    const bool ok = !__syncthreads_or(wrong);
+    if (!ok && tid == 0) set_status(status, PA_ERR_OUT_OF_RANGE);
+    const int32_t *starts = in_smem ? starts_s : g.starts;
+    for (int s = tid; s < S; s += kPlanThreads) {
+        const int ctx = __ldg(g.context_lens + s);
+        const int grp = ok ? last_at_most(starts, NG, s) : 0;
+        plan.seq_group[s] = grp;
+        if (ctx > 0 && ctx <= g.max_tokens) atomicMin(min_ctx + grp, ctx);
+        else set_status(status, PA_ERR_OUT_OF_RANGE);
+    }
+    __syncthreads();
+    int64_t items = 0, tiles = 0;
+    for (int base = 0; base < NG; base += kPlanThreads) {
+        const int i = base + tid;
+        int C = 0, mine = 0;
+        if (i < NG && ok) {
+            const int n = __ldg(g.starts + i + 1) - __ldg(g.starts + i), P = __ldg(g.prefix_lens + i);
+            const int least = in_smem ? min_s[i] : __ldcg(plan.min_ctx + i);   // (global atomics: not through L1)
+            if (P < 0 || P > g.max_tokens) set_status(status, PA_ERR_OUT_OF_RANGE);
+            else if (n >= 2 && least != INT_MAX) C = min(P, least - 1) / g.block_size * g.block_size;
+            if (C > 0) mine = g.num_kv_heads * ((n + g.seqs_per_item - 1) / g.seqs_per_item);
+        }
+        const int64_t t = (int64_t)mine * ((C + g.keys_per_tile - 1) / g.keys_per_tile);
+        int64_t total;
+        const int64_t item0 = block_scan(mine, warp_tot, total) + items;
+        items += total;
+        const int64_t tile0 = block_scan(t, warp_tot, total) + tiles;
+        tiles += total;
+        if (i < NG) {
+            plan.shared_len[i] = C;
+            plan.item_start[i] = (int32_t)item0;
+            plan.tile_start[i] = tile0;
+        }
+    }
+    if (tid == 0) {
+        plan.item_start[NG] = (int32_t)items;
+        plan.tile_start[NG] = tiles;
+    }
+    __syncthreads();
+    int64_t own = 0;
+    for (int base = 0; base < S; base += kPlanThreads) {
+        const int s = base + tid;
+        int len = 0;
+        if (s < S) {
+            const int ctx = __ldg(g.context_lens + s);
+            if (ctx > 0 && ctx <= g.max_tokens) len = ctx - plan.shared_len[plan.seq_group[s]];
+        }
+        int64_t total;
+        const int64_t own0 = block_scan((len + g.keys_per_tile - 1) / g.keys_per_tile, warp_tot, total) + own;
+        own += total;
+        if (s < S) {
+            plan.own_len[s] = len;
+            plan.own_start[s] = own0;
+        }
+    }
+    if (tid == 0) plan.own_start[S] = own;
+}
+
+// ------------------------------------------------------------------ CUDA-core kernel
+constexpr int kRows = 64;     // rows of an item at most
+constexpr int kKeys = 64;     // keys of a tile
+constexpr int kCcThreads = 256;
+
+struct CcParams {
+    const void *q;
+    const void *k_cache;
+    const void *v_cache;
+    const int32_t *block_tables;
+    const int32_t *group_starts;
+    SharedPlan plan;
+    float *pre_o;      // prefix pieces: [item + share][item_rows][D]
+    float2 *pre_ml;    // [item + share][item_rows]
+    float *own_o;      // own pieces: [sequence * num_kv_heads + kv-head + share][G][D]
+    float2 *own_ml;
+    int item_rows;     // seqs_per_item * G
+    int seqs_per_item;
+    int num_seqs;
+    int num_groups;
+    int num_heads;
+    int num_kv_heads;
+    int block_size;
+    int max_blocks;
+    int num_blocks;
+    int aligned;       // pools and q on 16 bytes
+    float scale_log2;
+    int32_t *status;
+};
+
+// One piece: rows [0, rows) (row r: sequence s0 + r / G, q-head r % G of kv-head kvh) against keys key0 .. key1-1 of
+// the block table `table`.
+struct CcPiece {
+    const int32_t *table;
+    int s0, rows, kvh, key0, key1;
+    float *o;      // [rows][D]
+    float2 *ml;    // [rows]
+};
+
+template <typename T> struct Vec16 { T v[16 / sizeof(T)]; };
+
+// 16 bytes of a row, as floats; element by element where rows need not be aligned.
+template <typename T>
+__device__ __forceinline__ void load_floats(const T *p, bool aligned, float (&x)[16 / sizeof(T)]) {
+    constexpr int n = 16 / sizeof(T);
+    Vec16<T> r;
+    if (aligned) *reinterpret_cast<uint4 *>(&r) = __ldg(reinterpret_cast<const uint4 *>(p));
+    else {
+#pragma unroll
+        for (int i = 0; i < n; ++i) r.v[i] = p[i];
+    }
+#pragma unroll
+    for (int i = 0; i < n; ++i) x[i] = to_float(r.v[i]);
+}
+
+// Shared memory: Q [kRows][D] | K [kKeys][D + 4], whose place the weights [kRows][kKeys + 4] take | V [kKeys][D].
+template <int D> constexpr int cc_smem_floats() { return kRows * D + kKeys * (D + 4) + kKeys * D; }
+
+// Thread (ty, tx) of 16 x 16 holds logits of rows ty * RT + i and keys tx + 16 j, and of the outputs the same rows and
+// dims 4 tx + 64 j + (0..3).  A row's 16 threads are half a warp.  RT = 1, 2 or 4: 16, 32 or 64 rows.
+template <typename T, int D, int RT>
+__device__ void cc_piece(const CcParams &p, const CcPiece &w, float *smem) {
+    constexpr int kVec = 16 / sizeof(T), kKS = D + 4, kPS = kKeys + 4, kDJ = D / 64;
+    static_assert(kRows * kPS <= kKeys * kKS, "the weights fit the keys' place");
+    float *qs = smem, *ks = qs + kRows * D, *ps = ks, *vs = ks + kKeys * kKS;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ty = tid >> 4, tx = tid & 15;
+    const int G = p.num_heads / p.num_kv_heads;
+    const bool al = p.aligned != 0;
+    for (int e = tid; e < 16 * RT * (D / kVec); e += kCcThreads) {
+        const int r = e / (D / kVec), d = (e - r * (D / kVec)) * kVec;
+        float x[kVec] = {};
+        if (r < w.rows)
+            load_floats(static_cast<const T *>(p.q) +
+                            ((int64_t)(w.s0 + r / G) * p.num_heads + w.kvh * G + r % G) * D + d, al, x);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) qs[r * D + d + i] = x[i];
+    }
+    float m[RT], l[RT], o[RT][kDJ][4];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < kDJ; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
+    }
+    const int64_t tok_stride = (int64_t)p.num_kv_heads * D;
+    for (int key = w.key0; key < w.key1; key += kKeys) {
+        // warp w loads keys 8 w .. 8 w + 7, which lie in one block (tiles start at multiples of 8 tokens)
+        const int t0 = key + 8 * warp;
+        int blk = -1;
+        if (t0 < w.key1) {
+            blk = __ldg(w.table + t0 / p.block_size);
+            if (blk < 0 || blk >= p.num_blocks) {
+                if (lane == 0) set_status(p.status, PA_ERR_OUT_OF_RANGE);
+                blk = -1;
+            }
+        }
+        const int64_t base = ((int64_t)max(blk, 0) * p.block_size + t0 % p.block_size) * tok_stride + (int64_t)w.kvh * D;
+        const int live = blk < 0 ? 0 : min(8, w.key1 - t0);   // rows behind them may hold anything: not read
+#pragma unroll
+        for (int e0 = 0; e0 < 8 * (D / kVec); e0 += 32) {
+            const int e = e0 + lane, r = e / (D / kVec), d = (e - r * (D / kVec)) * kVec;
+            float x[kVec] = {}, y[kVec] = {};
+            if (r < live) {
+                load_floats(static_cast<const T *>(p.k_cache) + base + r * tok_stride + d, al, x);
+                load_floats(static_cast<const T *>(p.v_cache) + base + r * tok_stride + d, al, y);
+            }
+#pragma unroll
+            for (int i = 0; i < kVec; i += 4) {
+                *reinterpret_cast<float4 *>(ks + (8 * warp + r) * kKS + d + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                *reinterpret_cast<float4 *>(vs + (8 * warp + r) * D + d + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            }
+        }
+        __syncthreads();
+        float x[RT][4] = {};
+#pragma unroll 4
+        for (int d = 0; d < D; d += 4) {
+            float4 a[RT], b[4];
+#pragma unroll
+            for (int i = 0; i < RT; ++i) a[i] = *reinterpret_cast<const float4 *>(qs + (ty * RT + i) * D + d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(ks + (tx + 16 * j) * kKS + d);
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[i][j] = fmaf(a[i].x, b[j].x, x[i][j]);
+                    x[i][j] = fmaf(a[i].y, b[j].y, x[i][j]);
+                    x[i][j] = fmaf(a[i].z, b[j].z, x[i][j]);
+                    x[i][j] = fmaf(a[i].w, b[j].w, x[i][j]);
+                }
+        }
+        // a key is seen if its block was (the warp that loaded it says so) and it lies before key1
+        unsigned seen = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int kk = tx + 16 * j, t = key + kk;
+            if (t < w.key1) {
+                const int b = __ldg(w.table + t / p.block_size);
+                if (b >= 0 && b < p.num_blocks) seen |= 1u << j;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[i][j] = (seen >> j) & 1 ? x[i][j] * p.scale_log2 : -INFINITY;
+                top = fmaxf(top, x[i][j]);
+            }
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float mn = fmaxf(m[i], top);
+            const float ref = mn == -INFINITY ? 0.f : mn;   // nothing seen yet: weights 0
+            const float alpha = fast_exp2(m[i] - ref);
+            m[i] = mn;
+            l[i] *= alpha;
+#pragma unroll
+            for (int j = 0; j < kDJ; ++j)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) o[i][j][u] *= alpha;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[i][j] = fast_exp2(x[i][j] - ref);
+                l[i] += x[i][j];
+            }
+        }
+        __syncthreads();   // the keys have been read
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ps[(ty * RT + i) * kPS + tx + 16 * j] = x[i][j];
+        __syncwarp();      // a row's weights are written and read by the same half warp
+#pragma unroll 4
+        for (int kk = 0; kk < kKeys; kk += 4) {
+            float4 a[RT];
+#pragma unroll
+            for (int i = 0; i < RT; ++i) a[i] = *reinterpret_cast<const float4 *>(ps + (ty * RT + i) * kPS + kk);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int j = 0; j < kDJ; ++j) {
+                    const float4 b = *reinterpret_cast<const float4 *>(vs + (kk + u) * D + 4 * tx + 64 * j);
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) {
+                        const float c = u == 0 ? a[i].x : u == 1 ? a[i].y : u == 2 ? a[i].z : a[i].w;
+                        o[i][j][0] = fmaf(c, b.x, o[i][j][0]);
+                        o[i][j][1] = fmaf(c, b.y, o[i][j][1]);
+                        o[i][j][2] = fmaf(c, b.z, o[i][j][2]);
+                        o[i][j][3] = fmaf(c, b.w, o[i][j][3]);
+                    }
+                }
+        }
+        __syncthreads();   // weights and values have been read
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        float sum = l[i];
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        const int r = ty * RT + i;
+        if (r >= w.rows) continue;
+#pragma unroll
+        for (int j = 0; j < kDJ; ++j)
+            *reinterpret_cast<float4 *>(w.o + (int64_t)r * D + 4 * tx + 64 * j) =
+                make_float4(o[i][j][0], o[i][j][1], o[i][j][2], o[i][j][3]);
+        if (tx == 0) w.ml[r] = make_float2(m[i], sum);
+    }
+}
+
+template <typename T, int D>
+__device__ __forceinline__ void cc_any_rows(const CcParams &p, const CcPiece &w, float *smem) {
+    if (w.rows <= 16) cc_piece<T, D, 1>(p, w, smem);
+    else if (w.rows <= 32) cc_piece<T, D, 2>(p, w, smem);
+    else cc_piece<T, D, 4>(p, w, smem);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kCcThreads, 2) shared_cc_kernel(const CcParams p) {
+    extern __shared__ __align__(16) float cc_smem[];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int G = p.num_heads / p.num_kv_heads;
+    const int64_t P = gridDim.x, c = blockIdx.x;
+    // the groups' shared tokens
+    const int64_t T0 = p.plan.tile_start[p.num_groups];
+    int64_t t = share_begin(c, T0, P);
+    const int64_t t_end = share_begin(c + 1, T0, P);
+    while (t < t_end) {
+        const int g = last_at_most(p.plan.tile_start, p.num_groups, t);   // (groups without tiles are passed over)
+        const int C = p.plan.shared_len[g], kt = (C + kKeys - 1) / kKeys;
+        const int s0 = __ldg(p.group_starts + g), n = __ldg(p.group_starts + g + 1) - s0;
+        const int64_t local = t - p.plan.tile_start[g];
+        const int item = (int)(local / kt), tile = (int)(local - (int64_t)item * kt);
+        const int per_head = (n + p.seqs_per_item - 1) / p.seqs_per_item;
+        const int kvh = item / per_head, part = item - kvh * per_head;
+        const int tiles = (int)min((int64_t)(kt - tile), t_end - t);
+        const int64_t slot = p.plan.item_start[g] + item + c;
+        CcPiece w;
+        w.table = p.block_tables + (int64_t)s0 * p.max_blocks;
+        w.s0 = s0 + part * p.seqs_per_item;
+        w.rows = min(p.seqs_per_item, n - part * p.seqs_per_item) * G;
+        w.kvh = kvh;
+        w.key0 = tile * kKeys;
+        w.key1 = (int)min((int64_t)C, (int64_t)(tile + tiles) * kKeys);
+        w.o = p.pre_o + slot * p.item_rows * D;
+        w.ml = p.pre_ml + slot * p.item_rows;
+        cc_any_rows<T, D>(p, w, cc_smem);
+        t += tiles;
+    }
+    // the sequences' own: by sequence, then kv-head
+    const int64_t T1 = p.plan.own_start[p.num_seqs] * p.num_kv_heads;
+    t = share_begin(c, T1, P);
+    const int64_t t_last = share_begin(c + 1, T1, P);
+    while (t < t_last) {
+        const int s = last_at_most(p.plan.own_start, p.num_seqs, t / p.num_kv_heads);
+        const int len = p.plan.own_len[s], kt = (len + kKeys - 1) / kKeys;
+        const int64_t local = t - p.plan.own_start[s] * p.num_kv_heads;
+        const int kvh = (int)(local / kt), tile = (int)(local - (int64_t)kvh * kt);
+        const int tiles = (int)min((int64_t)(kt - tile), t_last - t);
+        const int C = p.plan.shared_len[p.plan.seq_group[s]];
+        const int64_t slot = (int64_t)s * p.num_kv_heads + kvh + c;
+        CcPiece w;
+        w.table = p.block_tables + (int64_t)s * p.max_blocks;
+        w.s0 = s;
+        w.rows = G;
+        w.kvh = kvh;
+        w.key0 = C + tile * kKeys;
+        w.key1 = (int)min((int64_t)C + len, (int64_t)w.key0 + (int64_t)tiles * kKeys);
+        w.o = p.own_o + slot * G * D;
+        w.ml = p.own_ml + slot * G;
+        cc_any_rows<T, D>(p, w, cc_smem);
+        t += tiles;
+    }
+}
+
+// ------------------------------------------------------------------ merge
+struct MergeParams {
+    void *out;
+    const int32_t *group_starts;
+    SharedPlan plan;
+    const float *pre_o;
+    const float2 *pre_ml;
+    const float *own_o;
+    const float2 *own_ml;
+    int pre_shares;     // CTAs that cut the prefix stream
+    int own_shares;     // CTAs that cut the own stream
+    int item_rows;
+    int seqs_per_item;
+    int keys_per_tile;
+    int num_seqs;
+    int num_groups;
+    int num_heads;
+    int num_kv_heads;
+};
+
+constexpr int kMergeThreads = 128;
+
+// The running (M, L, acc) of one row; lane: D / 32 consecutive dims.
+template <int D> struct RowSum {
+    float M = -INFINITY, L = 0.f, acc[D / 32] = {};
+    __device__ __forceinline__ void add(float2 ml, const float (&o)[D / 32]) {
+        if (ml.y == 0.f) return;   // nothing seen (a NaN stays)
+        const float Mn = fmaxf(M, ml.x), a = fast_exp2(M - Mn), b = fast_exp2(ml.x - Mn);
+        L = L * a + ml.y * b;
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) acc[u] = acc[u] * a + o[u] * b;
+        M = Mn;
+    }
+};
+
+template <int D>
+__device__ __forceinline__ void load_dims(const float *src, float (&v)[D / 32]) {
+    if constexpr (D == 128) {
+        const float4 t = __ldcg(reinterpret_cast<const float4 *>(src));
+        v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+    } else {
+        const float2 t = __ldcg(reinterpret_cast<const float2 *>(src));
+        v[0] = t.x; v[1] = t.y;
+    }
+}
+
+// Pieces of one item, tiles [t0, t0 + n) of a stream of T tiles cut into P shares, in order; slot0 + share holds a
+// piece of `rows` rows, of which `row` is taken.  Four pieces' loads are in flight at a time.
+template <int D>
+__device__ __forceinline__ void merge_stream(RowSum<D> &sum, const float *o, const float2 *ml, int64_t slot0, int rows,
+                                             int row, int64_t t0, int64_t n, int64_t T, int64_t P) {
+    constexpr int kBatch = 4;
+    const int lane = threadIdx.x & 31;
+    const int64_t c0 = share_of(t0, T, P), c1 = share_of(t0 + n - 1, T, P);
+    for (int64_t cb = c0; cb <= c1; cb += kBatch) {
+        float2 x[kBatch];
+        float v[kBatch][D / 32];
+        bool use[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int64_t c = cb + k;
+            use[k] = c <= c1 && share_begin(c, T, P) < share_begin(c + 1, T, P);   // an empty share holds no piece
+            const int64_t at = (slot0 + (use[k] ? c : c0)) * rows + row;
+            x[k] = __ldcg(ml + at);
+            load_dims<D>(o + at * D + lane * (D / 32), v[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (use[k]) sum.add(x[k], v[k]);
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const MergeParams p) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int lane = threadIdx.x & 31;
+    const int64_t r = (int64_t)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+    if (r >= (int64_t)p.num_seqs * p.num_heads) return;
+    const int s = (int)(r / p.num_heads), h = (int)(r - (int64_t)s * p.num_heads);
+    const int len = p.plan.own_len[s];
+    if (len <= 0) return;   // context length out of range: the row stays as it was
+    const int G = p.num_heads / p.num_kv_heads, kvh = h / G, hh = h - kvh * G;
+    const int g = p.plan.seq_group[s], C = p.plan.shared_len[g];
+    RowSum<D> sum;
+    if (C > 0) {
+        const int s0 = __ldg(p.group_starts + g), n = __ldg(p.group_starts + g + 1) - s0;
+        const int per_head = (n + p.seqs_per_item - 1) / p.seqs_per_item;
+        const int part = (s - s0) / p.seqs_per_item, item = kvh * per_head + part;
+        const int64_t kt = (C + p.keys_per_tile - 1) / p.keys_per_tile;
+        merge_stream<D>(sum, p.pre_o, p.pre_ml, p.plan.item_start[g] + item, p.item_rows,
+                        (s - s0 - part * p.seqs_per_item) * G + hh, p.plan.tile_start[g] + item * kt, kt,
+                        p.plan.tile_start[p.num_groups], p.pre_shares);
+    }
+    const int64_t kt = (len + p.keys_per_tile - 1) / p.keys_per_tile;
+    merge_stream<D>(sum, p.own_o, p.own_ml, (int64_t)s * p.num_kv_heads + kvh, G, hh,
+                    p.plan.own_start[s] * p.num_kv_heads + kvh * kt, kt,
+                    p.plan.own_start[p.num_seqs] * p.num_kv_heads, p.own_shares);
+    T *dst = static_cast<T *>(p.out) + r * D + lane * (D / 32);
+    const float inv = 1.f / sum.L;
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) dst[u] = from_float<T>(sum.acc[u] * inv);
+}
+
+// ------------------------------------------------------------------ host side
+// Workspace: the plan's arrays, then the pieces.
+struct Layout {
+    size_t seq_group, own_len, shared_len, min_ctx, item_start, tile_start, own_start, pre_ml, pre_o, own_ml, own_o, total;
+};
+
+Layout layout(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int head_dim) {
+    Layout w;
+    const size_t S = num_seqs, NG = num_groups, HK = num_kv_heads, G = num_heads / num_kv_heads > 0 ? num_heads / num_kv_heads : 1;
+    size_t at = 0;
+    auto take = [&](size_t bytes) { const size_t a = at; at = align_up(at + bytes, 256); return a; };
+    w.seq_group = take(4 * S);
+    w.own_len = take(4 * S);
+    w.shared_len = take(4 * NG);
+    w.min_ctx = take(4 * NG);
+    w.item_start = take(4 * (NG + 1));
+    w.tile_start = take(8 * (NG + 1));
+    w.own_start = take(8 * (S + 1));
+    const size_t spi = kRows / G > 0 ? kRows / G : 1;
+    // a group's items: its sequences by spi, rounded up
+    const size_t pre_rows = (HK * (S / spi + (NG < S ? NG : S)) + kMaxCtas) * (spi < S ? spi : S) * G;
+    const size_t own_rows = (HK * S + kMaxCtas) * G;
+    w.pre_ml = take(8 * pre_rows);
+    w.pre_o = take(4 * pre_rows * head_dim);
+    w.own_ml = take(8 * own_rows);
+    w.own_o = take(4 * own_rows * head_dim);
+    w.total = at;
+    return w;
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(const CcParams &cc, const MergeParams &mg, int grid, cudaStream_t stream) {
+    auto kern = shared_cc_kernel<T, D>;
+    constexpr size_t smem = cc_smem_floats<D>() * sizeof(float);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(kern, dim3(grid), dim3(kCcThreads), smem, stream, cc);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = (int64_t)mg.num_seqs * mg.num_heads;
+    return launch_dependent(shared_merge_kernel<T, D>, dim3((unsigned)((rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32))),
+                            dim3(kMergeThreads), 0, stream, mg);
+}
+
+}  // namespace
+
+size_t shared_prefix_workspace(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int head_dim) {
+    return layout(num_seqs, num_groups, num_heads, num_kv_heads, head_dim).total;
+}
+
+cudaError_t launch_shared_prefix(const AttnArgs &a, const int32_t *group_starts, const int32_t *prefix_lens, int num_groups,
+                                 void *workspace, cudaStream_t stream) {
+    const Layout w = layout(a.num_seqs, num_groups, a.num_heads, a.num_kv_heads, a.head_dim);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const int G = a.num_heads / a.num_kv_heads, spi = kRows / G;
+    const SharedPlan plan = {reinterpret_cast<int32_t *>(ws + w.seq_group), reinterpret_cast<int32_t *>(ws + w.own_len),
+                             reinterpret_cast<int32_t *>(ws + w.shared_len), reinterpret_cast<int32_t *>(ws + w.min_ctx),
+                             reinterpret_cast<int32_t *>(ws + w.item_start), reinterpret_cast<int64_t *>(ws + w.tile_start),
+                             reinterpret_cast<int64_t *>(ws + w.own_start)};
+    const SharedGroups groups = {a.context_lens, group_starts, prefix_lens, a.num_seqs, num_groups, a.num_kv_heads,
+                                 a.block_size, (int64_t)a.max_blocks * a.block_size, spi, kKeys};
+    cudaError_t e = launch_dependent(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, groups, plan, a.status);
+    if (e != cudaSuccess) return e;
+    auto in16 = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+    const int sms = device_sm_count(), grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+    CcParams cc = {a.q, a.k_cache, a.v_cache, a.block_tables, group_starts, plan};
+    cc.pre_o = reinterpret_cast<float *>(ws + w.pre_o);
+    cc.pre_ml = reinterpret_cast<float2 *>(ws + w.pre_ml);
+    cc.own_o = reinterpret_cast<float *>(ws + w.own_o);
+    cc.own_ml = reinterpret_cast<float2 *>(ws + w.own_ml);
+    cc.item_rows = (spi < a.num_seqs ? spi : a.num_seqs) * G;
+    cc.seqs_per_item = spi;
+    cc.num_seqs = a.num_seqs;
+    cc.num_groups = num_groups;
+    cc.num_heads = a.num_heads;
+    cc.num_kv_heads = a.num_kv_heads;
+    cc.block_size = a.block_size;
+    cc.max_blocks = a.max_blocks;
+    cc.num_blocks = a.num_blocks;
+    cc.aligned = in16(a.q) && in16(a.k_cache) && in16(a.v_cache) ? 1 : 0;
+    cc.scale_log2 = a.scale * 1.4426950408889634f;
+    cc.status = a.status;
+    MergeParams mg = {a.out, group_starts, plan, cc.pre_o, cc.pre_ml, cc.own_o, cc.own_ml, grid, grid, cc.item_rows, spi,
+                      kKeys, a.num_seqs, num_groups, a.num_heads, a.num_kv_heads};
+    if (a.dtype == PA_DTYPE_F32)
+        return a.head_dim == 64 ? launch_typed<float, 64>(cc, mg, grid, stream)
+                                : launch_typed<float, 128>(cc, mg, grid, stream);
+    return a.head_dim == 64 ? launch_typed<__nv_bfloat16, 64>(cc, mg, grid, stream)
+                            : launch_typed<__nv_bfloat16, 128>(cc, mg, grid, stream);
+}
+
+}  // namespace pa

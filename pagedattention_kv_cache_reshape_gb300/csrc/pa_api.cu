@@ -466,6 +466,44 @@ pa_status pa_decode_q4(void *out, const void *q, const void *k_cache, const void
     return from_cuda(launch_decode_q4(a, workspace, workspace_bytes, (cudaStream_t)stream));
 }
 
+size_t pa_decode_shared_prefix_workspace_size(int num_seqs, int num_groups, int num_heads, int num_kv_heads,
+                                              int head_dim, int block_size, int max_blocks) {
+    (void)block_size;
+    (void)max_blocks;
+    if (num_kv_heads < 1) num_kv_heads = 1;
+    if (num_heads < num_kv_heads) num_heads = num_kv_heads;
+    return shared_prefix_workspace(num_seqs < 0 ? 0 : num_seqs, num_groups < 1 ? 1 : num_groups, num_heads,
+                                   num_kv_heads, head_dim < 1 ? 1 : head_dim);
+}
+
+pa_status pa_decode_shared_prefix(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                  const int32_t *block_tables, const int32_t *context_lens,
+                                  const int32_t *group_starts, const int32_t *prefix_lens, int num_seqs,
+                                  int num_groups, int num_heads, int num_kv_heads, int head_dim,
+                                  int block_size, int max_blocks, int num_blocks, float scale, pa_dtype dtype,
+                                  void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                  pa_stream_t stream) {
+    size_t unused = 0;
+    const pa_status st = decode_requirements(out, q, k_cache, v_cache, block_tables, context_lens, num_seqs,
+                                             num_heads, num_kv_heads, head_dim, block_size, max_blocks,
+                                             num_blocks, scale, dtype, &unused);
+    if (st != PA_OK) return st;
+    if (num_groups < 0) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (num_groups == 0 || !group_starts || !prefix_lens) return PA_ERR_INVALID_ARG;
+    if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(group_starts, 4) || !aligned(prefix_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    // pieces are counted in 32 bits
+    if ((int64_t)num_heads * ((int64_t)num_seqs + num_groups) > INT32_MAX / 2) return PA_ERR_UNSUPPORTED;
+    const size_t need = pa_decode_shared_prefix_workspace_size(num_seqs, num_groups, num_heads, num_kv_heads, head_dim,
+                                                               block_size, max_blocks);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return PA_ERR_WORKSPACE;
+    const AttnArgs a{out, q, k_cache, v_cache, block_tables, context_lens, nullptr, num_seqs, num_seqs, 1,
+                     num_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks, scale, dtype,
+                     dev_status};
+    return from_cuda(launch_shared_prefix(a, group_starts, prefix_lens, num_groups, workspace, (cudaStream_t)stream));
+}
+
 size_t pa_varlen_prefill_workspace_size(int num_seqs, int total_q, int num_heads,
                                         int num_kv_heads, int head_dim, int block_size,
                                         int max_blocks) {

@@ -192,6 +192,11 @@ cudaError_t launch_q4_blocks(const Q4BlocksArgs &a, bool quantize, cudaStream_t 
 size_t decode_q4_workspace(int num_seqs, int num_heads, int num_kv_heads, int head_dim);
 cudaError_t launch_decode_q4(const AttnArgs &a, void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
+// Decode of a batch in groups whose sequences share prefixes (a.cu_seqlens_q is not used).
+size_t shared_prefix_workspace(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int head_dim);
+cudaError_t launch_shared_prefix(const AttnArgs &a, const int32_t *group_starts, const int32_t *prefix_lens, int num_groups,
+                                 void *workspace, cudaStream_t stream);
+
 // Launch as a programmatic dependent of the previous kernel in the stream:
 // the kernel calls griddepcontrol.wait before it reads that kernel's output.
 template <typename... KArgs, typename... Args>

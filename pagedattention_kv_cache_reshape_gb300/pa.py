@@ -33,6 +33,7 @@ EXPORTS = (
     "pa_rope_and_cache", "pa_q4_block_bytes", "pa_rope_and_cache_q4", "pa_quantize_blocks_q4",
     "pa_dequantize_blocks_q4", "pa_decode_q4_workspace_size", "pa_decode_q4",
     "pa_mrope_and_cache", "pa_mrope_and_cache_q4",
+    "pa_decode_shared_prefix_workspace_size", "pa_decode_shared_prefix",
 )
 STATIC_SCRATCH_BYTES = 24 << 20
 STALL_NONE, STALL_PRODUCER, STALL_CONSUMER = 0, 1, 2
@@ -139,6 +140,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         L.pa_decode_q4_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
         L.pa_decode_q4.restype = i32
         L.pa_decode_q4.argtypes = L.pa_decode.argtypes
+        L.pa_decode_shared_prefix_workspace_size.restype = sz
+        L.pa_decode_shared_prefix_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+        L.pa_decode_shared_prefix.restype = i32
+        L.pa_decode_shared_prefix.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, f32,
+                                              i32, vp, sz, vp, vp]
         L.pa_validate_inputs.restype = i32
         L.pa_validate_inputs.argtypes = [vp, i32, i32, vp, vp, i32, i32, i32, ctypes.POINTER(ctypes.c_int),
                                          ctypes.POINTER(ctypes.c_int64)]
@@ -670,6 +676,59 @@ def decode_q4(q, k_cache, v_cache, block_tables, context_lens, scale: float, out
         _raw_stream(dev) if stream is None else _stream(stream))
     if rc != OK:
         raise PAError(rc, "pa_decode_q4")
+    return out
+
+
+def decode_shared_prefix_workspace_size(num_seqs, num_groups, num_heads, num_kv_heads, head_dim, block_size,
+                                        max_blocks) -> int:
+    return int(load().pa_decode_shared_prefix_workspace_size(num_seqs, num_groups, num_heads, num_kv_heads, head_dim,
+                                                             block_size, max_blocks))
+
+
+def decode_shared_prefix(q, k_cache, v_cache, block_tables, context_lens, group_starts, prefix_lens, scale: float,
+                         out=None, workspace=None, dev_status=None, stream=None):
+    """pa_decode_shared_prefix: pa.decode of q [num_seqs, H, D] in groups of neighbouring sequences
+    (group_starts int32 [groups + 1]) whose first prefix_lens [groups] tokens are the same and computed once."""
+    num_seqs, H, D = q.shape
+    pool = k_cache.shape
+    if len(pool) != 4 or v_cache.shape != pool or pool[3] != D:
+        raise ValueError("the pools must be [num_blocks, block_size, num_kv_heads, head_dim] with q's head_dim")
+    num_blocks, block_size, hkv, _ = pool
+    n, max_blocks = block_tables.shape
+    if n != num_seqs or context_lens.numel() != num_seqs:
+        raise ValueError("block_tables and context_lens must have a row per sequence")
+    groups = prefix_lens.numel()
+    if group_starts.numel() != groups + 1:
+        raise ValueError("group_starts must have one entry more than prefix_lens")
+    dtype, dev = q.dtype, torch.cuda.current_device()
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    if out is None:
+        out = _empty(q.shape, q.dtype, q.device, stream, result=True)
+    elif out.shape != q.shape or out.dtype != dtype:
+        raise ValueError("out must have q's shape and dtype")
+    if workspace is None:
+        workspace = _ws(None, decode_shared_prefix_workspace_size(num_seqs, groups, H, hkv, D, block_size, max_blocks),
+                        q.device, stream)
+    if not (q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and block_tables.is_contiguous() and context_lens.is_contiguous() and workspace.is_contiguous()
+            and group_starts.is_contiguous() and prefix_lens.is_contiguous() and k_cache.dtype == v_cache.dtype == dtype
+            and block_tables.dtype == context_lens.dtype == group_starts.dtype == prefix_lens.dtype == torch.int32
+            and q.get_device() == out.get_device() == k_cache.get_device() == v_cache.get_device()
+            == block_tables.get_device() == context_lens.get_device() == workspace.get_device()
+            == group_starts.get_device() == prefix_lens.get_device() == dev):
+        _refuse(dev, (q, "q", None), (out, "out", None), (k_cache, "k_cache", dtype), (v_cache, "v_cache", dtype),
+                (block_tables, "block_tables", torch.int32), (context_lens, "context_lens", torch.int32),
+                (group_starts, "group_starts", torch.int32), (prefix_lens, "prefix_lens", torch.int32),
+                (workspace, "workspace", None))
+    rc = (_lib or load()).pa_decode_shared_prefix(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), group_starts.data_ptr(), prefix_lens.data_ptr(), num_seqs, groups, H, hkv, D, block_size,
+        max_blocks, num_blocks, scale, code, workspace.data_ptr(), workspace.nbytes,
+        0 if dev_status is None else _status(dev_status, dev), _raw_stream(dev) if stream is None else _stream(stream))
+    if rc != OK:
+        raise PAError(rc, "pa_decode_shared_prefix")
     return out
 
 
