@@ -644,8 +644,9 @@ PA_API pa_status pa_set_timing_events(void *ev_begin, void *ev_end);
  * limit, records PA_ERR_TIMEOUT in *dev_status and lets its kernel return, so
  * a stuck pipeline never hangs the GPU.  This hook lets a test reach those
  * branches on purpose, without any fault: for every later pa_decode,
- * pa_decode_step, pa_varlen_prefill, pa_varlen_step and pa_varlen_encode call
- * made from the same host thread,
+ * pa_decode_step, pa_decode_shared_prefix, pa_varlen_prefill, pa_varlen_step
+ * and pa_varlen_encode call made from the same host thread (the shared part of
+ * a pa_decode_shared_prefix call counts as prefill below),
  *  limit_ns  bounds each wait (0: the default of one second);
  *  stall     makes one role of each CTA stop early and never give the signal
  *            the others wait for (nobody ever sets it, so their waits run out):

@@ -74,6 +74,8 @@ constexpr int kSmemBudget = 227 * 1024;
 // at its shortest between 58 and 70.
 constexpr double kDecodeBytesPerSmNs = 64.0;
 constexpr double kPrefillFlopsPerSmNs = 6600.0;
+// SM-nanoseconds of a 128-key tile in the prefix kernel: head_dim 64, 128; one M-tile, two
+constexpr double kPrefixTileNs[2][2] = {{700.0, 900.0}, {900.0, 1300.0}};
 
 struct __align__(16) StreamEntry {
     int32_t seq;
@@ -85,7 +87,10 @@ struct __align__(16) StreamEntry {
 struct __align__(16) StageHeader {
     int32_t seq, qrow, hg, lb, ntok, flags, pad0, pad1;
 };
-constexpr int kFirst = 1, kLast = 2, kSeqEnd = 4, kValid = 8;
+constexpr int kFirst = 1, kLast = 2, kSeqEnd = 4, kValid = 8, kShared = 16;
+// packed of a StreamEntry when the batch has shared prefixes: ntok in bits 0..4, bit 5 the sequence shares some tokens
+// (its result here is a piece: (m, l, o))
+constexpr int kSharedBit = 32;
 
 struct DecodeParams {
     const __nv_bfloat16 *q;
@@ -124,6 +129,9 @@ struct DecodeParams {
     int stall;
     int stall_after;
     int32_t *wait_sites;
+    // shared prefixes: where the own parts of sequences that share some tokens go, [num_seqs * num_heads]
+    float *own_o;
+    float2 *own_ml;
 };
 
 // Optional cache write folded into the plan kernel (pa_decode_step): for new
@@ -161,15 +169,61 @@ struct DecodeSplit {
     int causal;
     double block_ns;   // SM-nanoseconds per decode block of all kv-heads
     double pair_ns;    // SM-nanoseconds per causal (query row, key) pair of all heads
+    double tile_ns[2]; // SM-nanoseconds per prefix tile of an item with one and with two M-tiles
+    int32_t *prefix_shares;   // CTAs of the prefix kernel that take a share, of prefix_grid
+    int prefix_grid;
 };
+
+// The planning CTA of a batch with shared prefixes: the groups' plan for the prefix and merge kernels, and the SMs'
+// split between the decode and the prefix kernel by estimated work.
+__device__ void shared_plan_cta(const SharedGroups &g, const SharedPlan &plan, const DecodeSplit &split, int32_t *starts,
+                                int32_t *lens, int32_t *status) {
+    __shared__ int64_t scan_tot[kPlanThreads / 32];
+    __shared__ double work[2][kPlanThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool ok = shared_lens<kPlanThreads>(g, starts, lens, status);
+    const int64_t tiles = shared_write_plan<kPlanThreads>(g, plan, ok, starts, lens, scan_tot);
+    double dec = 0.0, pre = 0.0;
+    for (int s = tid; s < g.num_seqs; s += kPlanThreads) dec += (plan.own_len[s] + kU - 1) / kU;   // (this thread wrote it)
+    for (int i = tid; i < g.num_groups; i += kPlanThreads) {
+        if (lens[i] <= 0) continue;
+        const int n = __ldg(g.starts + i + 1) - __ldg(g.starts + i), pos = g.seqs_per_item / 2;
+        const int pairs = n / g.seqs_per_item, rest = n - pairs * g.seqs_per_item;
+        const double one = rest > 0 && rest <= pos ? 1.0 : 0.0, two = pairs + (rest > pos ? 1.0 : 0.0);
+        pre += (one * split.tile_ns[0] + two * split.tile_ns[1]) * g.num_kv_heads *
+               ((lens[i] + g.keys_per_tile - 1) / g.keys_per_tile);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        dec += __shfl_xor_sync(0xffffffffu, dec, off);
+        pre += __shfl_xor_sync(0xffffffffu, pre, off);
+    }
+    if (lane == 0) { work[0][warp] = dec; work[1][warp] = pre; }
+    __syncthreads();
+    if (tid == 0) {
+        dec = pre = 0.0;
+        for (int w = 0; w < kPlanThreads / 32; ++w) { dec += work[0][w]; pre += work[1][w]; }
+        dec *= split.block_ns;
+        int act = split.grid;
+        if (tiles > 0 && split.grid > 1) {
+            act = (int)llrint(split.grid * dec / (dec + pre));
+            act = act < 1 ? 1 : (act > split.grid - 1 ? split.grid - 1 : act);
+        }
+        *split.active = act;
+        *split.prefix_shares = min(split.grid - act > 0 ? split.grid - act : split.grid, split.prefix_grid);
+    }
+}
 
 // ------------------------------------------------------------------ plan
 // CTAs [0, job.first_cta) build the block stream (CTA 0 also zeroes the
 // arrival counters); the CTAs after them, up to the last, write the step's
 // new tokens into the cache, concurrently.  kShare: the batch also has
 // prefill chunks (the last CTA plans them and CTA 0 sets the SM split);
+// kGroups: it has shared prefixes, which the stream leaves out (every plan CTA
+// finds them itself; the last CTA writes the groups' plan and sets the split);
 // decode-only calls run the plain instantiation.
-template <bool kShare>
+constexpr int kPlain = 0, kMixed = 1, kPrefixes = 2;
+template <int kMode>
 __global__ void __launch_bounds__(kPlanThreads)
     decode_plan_kernel(const int32_t *__restrict__ context_lens,
                        const int32_t *__restrict__ cu_seqlens_q,
@@ -177,7 +231,9 @@ __global__ void __launch_bounds__(kPlanThreads)
                        int num_blocks, int total_q, int log2b, int32_t *__restrict__ prefix,
                        StreamEntry *__restrict__ stream, int32_t *__restrict__ stream_b1, int32_t *status,
                        const KvWriteJob job,
-                       const DecodeSplit split, const PrefillPlanJob prefill) {
+                       const DecodeSplit split, const PrefillPlanJob prefill, const SharedGroups groups,
+                       const SharedPlan shared) {
+    constexpr bool kShare = kMode == kMixed, kGroups = kMode == kPrefixes;
     const int B = 1 << log2b;   // tokens per cache block
     extern __shared__ __align__(16) int32_t pref_s[];  // [num_seqs + 1]
     __shared__ int32_t warp_tot[kPlanThreads / 32];
@@ -186,7 +242,12 @@ __global__ void __launch_bounds__(kPlanThreads)
     grid_dependency_wait();      // inputs may come from the previous kernel
     grid_dependents_launch();    // the decode kernel may start its prologue
     // with prefill chunks in the batch, the last CTA builds their work list
-    const int dgrid = (int)gridDim.x - (kShare ? 1 : 0);   // CTAs of the plan and the cache write
+    const int dgrid = (int)gridDim.x - (kMode != kPlain ? 1 : 0);   // CTAs of the plan and the cache write
+    int32_t *starts_s = pref_s + num_seqs + 1, *lens_s = starts_s + (kGroups ? groups.num_groups : 0);
+    if (kGroups && (int)blockIdx.x == dgrid) {
+        shared_plan_cta(groups, shared, split, starts_s, lens_s, status);
+        return;
+    }
     if (kShare && (int)blockIdx.x == dgrid) {
         prefill_plan_block(prefill, reinterpret_cast<uint8_t *>(pref_s));
         return;
@@ -272,6 +333,9 @@ __global__ void __launch_bounds__(kPlanThreads)
         return;
     }
     const int pgrid = job.first_cta;   // CTAs of the plan proper
+    bool grouped = false;
+    if (kGroups) grouped = shared_lens<kPlanThreads>(groups, starts_s, lens_s, nullptr);
+    auto shared_of = [&](int s) { return kGroups && grouped ? lens_s[last_at_most(starts_s, groups.num_groups, s)] : 0; };
     int running = 0;
     double pairs = 0.0;   // causal (query, key) pairs of this thread's prefill rows
     for (int base = 0; base < num_seqs; base += kPlanThreads) {
@@ -291,7 +355,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                 if (ctx <= 0 || (int64_t)ctx > (int64_t)max_blocks * B) {
                     if (blockIdx.x == 0) set_status(status, PA_ERR_OUT_OF_RANGE);
                 } else {
-                    nb = (ctx + kU - 1) / kU;   // 16-token units
+                    nb = (ctx - shared_of(s) + kU - 1) / kU;   // 16-token units
                 }
             }
         }
@@ -347,8 +411,9 @@ __global__ void __launch_bounds__(kPlanThreads)
         }
         const int s = lo;
         const int lb = b - pref_s[s];            // 16-token unit of the sequence
-        const int ctx = __ldg(context_lens + s);
-        const int32_t *row = block_tables + (int64_t)s * max_blocks;
+        const int skip = shared_of(s);
+        const int ctx = __ldg(context_lens + s) - skip;
+        const int32_t *row = block_tables + (int64_t)s * max_blocks + (skip >> log2b);
         // the unit's physical block(s): B = 16 one, B = 32 half of one, B = 8 two
         // (the second -1 past the sequence end; an invalid entry voids the unit)
         int32_t blk, blk1 = -1;
@@ -375,7 +440,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         e.seq = s;
         e.qrow = cu_seqlens_q ? __ldg(cu_seqlens_q + s) : s;
         e.blk = blk;
-        e.packed = ntok | (seq_end << 6) | (half << 7) | (lb << 8);
+        e.packed = ntok | (skip > 0 ? kSharedBit : 0) | (seq_end << 6) | (half << 7) | (lb << 8);
         stream[b] = e;
         if (log2b == 3) stream_b1[b] = blk1;
     }
@@ -390,16 +455,29 @@ __device__ __forceinline__ int64_t cta_of(int64_t v, int64_t nv, int64_t p) {
 }
 
 // ------------------------------------------------------------------ merge
+// (m, l, o) of one row by a warp (lane: D/32 consecutive dims).
+template <int D>
+__device__ __forceinline__ void store_piece(float *o, float2 *ml, float M, float L, const float (&acc)[D / 32]) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (D == 128)
+        *reinterpret_cast<float4 *>(o + lane * 4) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    else
+        *reinterpret_cast<float2 *>(o + lane * 2) = make_float2(acc[0], acc[1]);
+    if (lane == 0) *ml = make_float2(M, L);
+}
+
 // One warp merges the pieces of a cut sequence for nh <= 4 q-heads h0.. of
 // its kv-head group (lane: D/32 consecutive dims of each), in CTA order
-// c0..c1, with the online rule (M, L, acc) <- (max, L a + l b, acc a + o b),
+// c0..c1 (into `dst`, normalised, or, for the own part of a sequence with
+// shared tokens, as (m, l, o) into own_o / own_ml), with the online rule (M, L, acc) <- (max, L a + l b, acc a + o b),
 // a = 2^{M - M'}, b = 2^{m - M'}, per head.  The loads of two pieces of all
 // nh heads are in flight at a time.  The partials were written by other
 // SMs: they are read through L2.
 template <int D>
 __device__ __forceinline__ void merge_pieces(const DecodeParams &p, int64_t vs, int64_t c0,
                                              int64_t c1, int64_t NV, int64_t P, int h0, int nh,
-                                             __nv_bfloat16 *dst) {
+                                             __nv_bfloat16 *dst, float *own_o = nullptr,
+                                             float2 *own_ml = nullptr) {
     constexpr int kPer = D / 32;
     constexpr int kH = 4;
     constexpr int kBatch = 2;
@@ -452,6 +530,10 @@ __device__ __forceinline__ void merge_pieces(const DecodeParams &p, int64_t vs, 
 #pragma unroll
     for (int hh = 0; hh < kH; ++hh) {
         if (hh >= nh) break;
+        if (own_o) {
+            store_piece<D>(own_o + hh * D, own_ml + hh, M[hh], L[hh], acc[hh]);
+            continue;
+        }
         const float inv = 1.f / L[hh];
 #pragma unroll
         for (int u = 0; u < kPer; u += 2)
@@ -485,7 +567,8 @@ __device__ __forceinline__ int tree_groups(int m, int n) {
 // `dst`, normalised into the output rows.
 template <int D>
 __device__ __forceinline__ void merge_group(const DecodeParams &p, int64_t slot0, int stride, int cnt, int h0,
-                                            int nh, __nv_bfloat16 *dst) {
+                                            int nh, __nv_bfloat16 *dst, float *own_o = nullptr,
+                                            float2 *own_ml = nullptr) {
     constexpr int kPer = D / 32;
     constexpr int kH = 4;
     const int lane = threadIdx.x & 31;
@@ -534,7 +617,9 @@ __device__ __forceinline__ void merge_group(const DecodeParams &p, int64_t slot0
 #pragma unroll
     for (int hh = 0; hh < kH; ++hh) {
         if (hh >= nh) break;
-        if (dst) {
+        if (own_o) {
+            store_piece<D>(own_o + hh * D, own_ml + hh, M[hh], L[hh], acc[hh]);
+        } else if (dst) {
             const float inv = 1.f / L[hh];
 #pragma unroll
             for (int u = 0; u < kPer; u += 2)
@@ -648,7 +733,9 @@ __device__ __forceinline__ void prefetch_first_blocks(const DecodeParams &p, int
 // kTwo: the cache block size is 8, and a unit's K (and V) tile is two 8-row
 // TMA boxes, [box][kv-head][D/64 plane][8 rows][64], the second box kv_tile/2
 // bytes after the first; otherwise one 16-row box, [kv-head][plane][16 rows][64].
-template <int D, bool kTwo>
+// kPart: the batch has shared prefixes; the own part of a sequence that shares
+// some tokens is left as (m, l, o).
+template <int D, bool kTwo, bool kPart>
 __global__ void __launch_bounds__(32 * (kMaxConsumerWarps + 1), 1)
     split_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         const __grid_constant__ CUtensorMap tmap_v, const DecodeParams p) {
@@ -751,9 +838,10 @@ __global__ void __launch_bounds__(32 * (kMaxConsumerWarps + 1), 1)
                         h.qrow = qrow;
                         h.hg = hg;
                         h.lb = packed >> 8;
-                        h.ntok = packed & 63;
+                        h.ntok = packed & (kPart ? kSharedBit - 1 : 63);
                         h.flags = (first ? kFirst : 0) | (last ? kLast : 0) |
-                                  ((packed >> 6) & 1 ? kSeqEnd : 0) | (blk >= 0 ? kValid : 0);
+                                  ((packed >> 6) & 1 ? kSeqEnd : 0) | (blk >= 0 ? kValid : 0) |
+                                  (kPart && (packed & kSharedBit) ? kShared : 0);
                         h.pad0 = h.pad1 = 0;
                         hdr[stage] = h;
                         uint8_t *st = smem + (size_t)stage * stage_bytes;
@@ -959,7 +1047,15 @@ __global__ void __launch_bounds__(32 * (kMaxConsumerWarps + 1), 1)
             if (hh >= gcount) continue;
             const int h_loc = h_first + hh;
             const float l_e = e ? l1 : l0;
-            if (whole) {
+            if (kPart && whole && (h.flags & kShared)) {
+                float *dst = p.own_o + (out_row + h_loc) * D + r;
+#pragma unroll
+                for (int j = 0; j < kMTiles; ++j) {
+                    dst[j * 16] = ot[j][e];
+                    dst[j * 16 + 8] = ot[j][2 + e];
+                }
+                if (r == 0) p.own_ml[out_row + h_loc] = make_float2(m_run[e], l_e);
+            } else if (whole) {
                 const float inv = 1.f / l_e;
                 __nv_bfloat16 *dst = p.out + (out_row + h_loc) * D + r;
 #pragma unroll
@@ -979,6 +1075,7 @@ __global__ void __launch_bounds__(32 * (kMaxConsumerWarps + 1), 1)
             }
         }
         if (whole) continue;
+        const bool to_own = kPart && (h.flags & kShared);
         // a piece of a sequence cut by CTA boundaries, now stored: count it in;
         // the warp that stores the last of the sequence's pieces merges them
         // (the stream's sizes are reloaded here rather than kept in registers)
@@ -1006,7 +1103,9 @@ __global__ void __launch_bounds__(32 * (kMaxConsumerWarps + 1), 1)
                     const bool root = span >= pieces;
                     for (int h = 0; h < gcount; h += 4)
                         merge_group<D>(p, vs + c0 + first, child, cnt, h_first + h, gcount - h < 4 ? gcount - h : 4,
-                                       root ? p.out + (out_row + h_first + h) * D : nullptr);
+                                       root ? p.out + (out_row + h_first + h) * D : nullptr,
+                                       root && to_own ? p.own_o + (out_row + h_first + h) * D : nullptr,
+                                       p.own_ml + out_row + h_first + h);
                     if (root) break;
                 }
                 node = first;
@@ -1026,7 +1125,9 @@ __global__ void __launch_bounds__(32 * (kMaxConsumerWarps + 1), 1)
         if (merge) {
             for (int g = 0; g < gcount; g += 4)
                 merge_pieces<D>(p, vs, c0, c1, NVt, Pt, h_first + g, gcount - g < 4 ? gcount - g : 4,
-                                p.out + (out_row + h_first + g) * D);
+                                p.out + (out_row + h_first + g) * D,
+                                to_own ? p.own_o + (out_row + h_first + g) * D : nullptr,
+                                p.own_ml + out_row + h_first + g);
         }
     }
 }
@@ -1122,13 +1223,13 @@ WorkspaceLayout workspace_layout(int num_seqs, int num_heads, int head_dim, int 
     return w;
 }
 
-template <int D, bool kTwo>
+template <int D, bool kTwo, bool kPart>
 cudaError_t launch_main(const DecodeParams &prm, const CUtensorMap &mk, const CUtensorMap &mv,
                         int grid, cudaStream_t stream, bool timed) {
     const int kv_tile = prm.kvh * kU * D * 2;
     const int stage_bytes = (int)align_up(2 * kv_tile + prm.qh * D * 2, 1024);
     const size_t smem = 1024 + (size_t)prm.num_stages * (stage_bytes + sizeof(StageHeader) + 16);
-    auto kern = split_decode_kernel<D, kTwo>;
+    auto kern = split_decode_kernel<D, kTwo, kPart>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (timed) timing_begin(stream);
@@ -1164,7 +1265,7 @@ size_t split_decode_workspace(int num_seqs, int num_heads, int head_dim, int max
 cudaError_t launch_split_decode(const AttnArgs &a, void *workspace, size_t workspace_bytes,
                                 cudaStream_t stream, bool timed, const KvWriteArgs *write,
                                 const PrefillPlanJob *prefill,
-                                const std::function<cudaError_t()> *between) {
+                                const std::function<cudaError_t()> *between, const SharedJob *shared) {
     const bool share_sms = prefill != nullptr;
     if (a.num_seqs == 0) return cudaSuccess;
     const int B = a.block_size;
@@ -1192,13 +1293,15 @@ cudaError_t launch_split_decode(const AttnArgs &a, void *workspace, size_t works
     prm.nhg = L.nhg;
     prm.active = reinterpret_cast<const int32_t *>(ws + w.active);
     prm.arrivals = reinterpret_cast<int32_t *>(ws + w.arrivals);
-    prm.shared_sms = prefill ? 1 : 0;
+    prm.shared_sms = prefill || shared ? 1 : 0;
+    prm.own_o = shared ? shared->own_o : nullptr;
+    prm.own_ml = shared ? shared->own_ml : nullptr;
     prm.num_stages = stages_for(L.kvh, L.qh, a.head_dim);
     prm.scale_log2 = a.scale * 1.4426950408889634f;
     prm.status = a.status;
     // decode calls (one query row per sequence, all CTAs take a slice): each
     // CTA prefetches its first blocks into L2 while it waits for the plan
-    const bool early = !share_sms && a.cu_seqlens_q == nullptr && a.num_seqs <= kMaxSeqsEarlyPrefetch;
+    const bool early = !share_sms && !shared && a.cu_seqlens_q == nullptr && a.num_seqs <= kMaxSeqsEarlyPrefetch;
     prm.context_lens = early ? a.context_lens : nullptr;
     prm.block_tables = a.block_tables;
     prm.max_blocks = a.max_blocks;
@@ -1243,7 +1346,8 @@ cudaError_t launch_split_decode(const AttnArgs &a, void *workspace, size_t works
     // plan (and the folded cache write)
     size_t plan_smem = sizeof(int32_t) * ((size_t)a.num_seqs + 1);
     if (share_sms && plan_smem < (size_t)kPrefillPlanSmem) plan_smem = kPrefillPlanSmem;
-    auto plan_kern = share_sms ? decode_plan_kernel<true> : decode_plan_kernel<false>;
+    if (shared) plan_smem += 2 * sizeof(int32_t) * (size_t)shared->groups.num_groups;
+    auto plan_kern = share_sms ? decode_plan_kernel<kMixed> : shared ? decode_plan_kernel<kPrefixes> : decode_plan_kernel<kPlain>;
     cudaError_t e = cudaFuncSetAttribute(plan_kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan_smem);
     if (e != cudaSuccess) return e;
     const int64_t max_entries = (int64_t)a.num_seqs * max_units(a.max_blocks, B);
@@ -1259,6 +1363,10 @@ cudaError_t launch_split_decode(const AttnArgs &a, void *workspace, size_t works
     split.causal = a.causal;
     split.block_ns = (double)kU * a.num_kv_heads * a.head_dim * 2 * 2 / kDecodeBytesPerSmNs;
     split.pair_ns = 4.0 * a.num_heads * a.head_dim / kPrefillFlopsPerSmNs;
+    split.tile_ns[0] = kPrefixTileNs[a.head_dim == 64 ? 0 : 1][0];
+    split.tile_ns[1] = kPrefixTileNs[a.head_dim == 64 ? 0 : 1][1];
+    split.prefix_shares = shared ? shared->shares : nullptr;
+    split.prefix_grid = prefix_grid();
     int plan_grid = (int)((max_entries + 4 * kPlanThreads - 1) / (4 * kPlanThreads));
     if (plan_grid > 2 * sms) plan_grid = 2 * sms;
     if (plan_grid < 1) plan_grid = 1;
@@ -1269,20 +1377,26 @@ cudaError_t launch_split_decode(const AttnArgs &a, void *workspace, size_t works
     if (write_grid > 2 * sms) write_grid = 2 * sms;
     job.first_cta = plan_grid;
     plan_grid += write_grid;                    // + the CTAs of the cache write
-    if (share_sms) ++plan_grid;                 // + the CTA that plans the prefill chunks
+    if (share_sms || shared) ++plan_grid;       // + the CTA that plans the prefill chunks or the groups
     const PrefillPlanJob pf = share_sms ? *prefill : PrefillPlanJob{};
     e = launch_dependent(plan_kern, dim3(plan_grid), dim3(kPlanThreads), plan_smem, stream,
                          a.context_lens, a.cu_seqlens_q, a.block_tables, a.num_seqs, a.max_blocks,
                          a.num_blocks, a.total_q, log2_of_block(B), reinterpret_cast<int32_t *>(ws + w.prefix),
                          reinterpret_cast<StreamEntry *>(ws + w.stream), reinterpret_cast<int32_t *>(ws + w.stream_b1),
-                         a.status, job, split, pf);
+                         a.status, job, split, pf, shared ? shared->groups : SharedGroups{},
+                         shared ? shared->plan : SharedPlan{});
     if (e != cudaSuccess) return e;
 
     const bool two = B < kU;   // B = 8: two blocks per unit
-    if (a.head_dim == 64) e = two ? launch_main<64, true>(prm, mk, mv, grid, stream, timed)
-                                  : launch_main<64, false>(prm, mk, mv, grid, stream, timed);
-    else e = two ? launch_main<128, true>(prm, mk, mv, grid, stream, timed)
-                 : launch_main<128, false>(prm, mk, mv, grid, stream, timed);
+    if (shared) {
+        if (a.head_dim == 64) e = two ? launch_main<64, true, true>(prm, mk, mv, grid, stream, timed)
+                                      : launch_main<64, false, true>(prm, mk, mv, grid, stream, timed);
+        else e = two ? launch_main<128, true, true>(prm, mk, mv, grid, stream, timed)
+                     : launch_main<128, false, true>(prm, mk, mv, grid, stream, timed);
+    } else if (a.head_dim == 64) e = two ? launch_main<64, true, false>(prm, mk, mv, grid, stream, timed)
+                                         : launch_main<64, false, false>(prm, mk, mv, grid, stream, timed);
+    else e = two ? launch_main<128, true, false>(prm, mk, mv, grid, stream, timed)
+                 : launch_main<128, false, false>(prm, mk, mv, grid, stream, timed);
     if (e != cudaSuccess) return e;
     return between ? (*between)() : cudaSuccess;
 }

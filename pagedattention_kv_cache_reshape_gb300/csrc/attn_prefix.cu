@@ -1,0 +1,706 @@
+// attn_prefix.cu -- the shared part of pa_decode_shared_prefix on the 5th-gen
+// tensor cores: what all sequences of a group see, for all their query rows.
+//
+// For an item (group, kv-head, up to 2 * POS neighbouring sequences, POS =
+// 128 / G) the rows (sequence, q-head of the kv-head) are the M of
+//     S = Q K^T,  P = 2^(S * scale*log2e - m),  O += P V,  l += rows' sums of P
+// over the group's shared keys, and the result stays (m, l, O) in fp32: the
+// merge kernel joins it with the sequences' own parts.
+//
+// Work: the items' 128-key tiles, one after the other, are one stream
+// (shared_plan.cuh).  Each persistent CTA takes an equal contiguous share, so
+// every CTA has the same number of tiles whatever the group sizes; a share
+// holds a few pieces of items, usually one or two.
+//
+// Bound: a 64 KB tile (K and V, 128 keys x 128 dims) takes an SM's share of
+// HBM 1.5 us; the products of one M-tile of 128 rows take 0.5 us of the tensor
+// pipe, of two 1 us.  So groups of up to 256 rows a kv-head are bound by HBM,
+// larger ones (several items read the same tiles) by the tensor pipe and the
+// softmax beside it.  Items of one M-tile leave the second softmax warpgroup
+// idle.
+//
+// Roles (512 threads): warps 0-7 two softmax warpgroups (thread = row = TMEM
+// lane of its M-tile), warp 8 TMA producer, warp 9 TMEM owner and MMA issuer,
+// warps 12-15 output.  Schedule, layouts and waits as in attn_prefill.cu; no
+// causal mask, and blocks past the shared tokens come in as zeros (TMA
+// out-of-bounds fill) with their logits masked.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include <type_traits>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+#include "shared_plan.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int BM = 128;               // rows per M-tile
+constexpr int kMT = 2;                // M-tiles per item at most, one softmax warpgroup each
+constexpr int BN = kPrefixKeys;       // keys per KV tile
+static_assert(BN == 128, "P is released in two halves of 64 keys");
+constexpr size_t kSmemLimit = 227 * 1024;
+constexpr int kProducerWarp = 4 * kMT;
+constexpr int kMmaWarp = kProducerWarp + 1;
+constexpr int kOutWarp = kProducerWarp + 4;
+constexpr int kThreads = 32 * (4 * kMT + 8);
+// Register split: launched at 128 a thread; the softmax warpgroups' share comes from the others'.
+constexpr int kRegsLaunch = 128;
+constexpr int kRegsSide = 56;
+constexpr int kRegsOut = 56;
+constexpr int kRegsSoftmax = 200;
+static_assert(128 * (kRegsSide + kRegsOut) + 128 * kMT * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
+constexpr int kTmemCols = 512;
+
+struct PrefixParams {
+    SharedPlan plan;
+    const int32_t *starts;
+    const int32_t *block_tables;
+    const int32_t *shares;     // CTAs that take a share
+    float *o;                  // pieces: [rows][D]
+    float2 *ml;                // [rows]
+    int num_seqs;
+    int num_groups;
+    int num_heads;
+    int group;        // q-heads per kv-head
+    int pos;          // sequences per M-tile: 128 / group
+    int item_rows;
+    int max_blocks;
+    int num_blocks;
+    float scale_log2;
+    int32_t *status;
+    // bounded waits: their limit, and the test hook's stall (PA_STALL_*)
+    uint64_t wait_ns;
+    int stall;
+    int stall_after;
+    int32_t *wait_sites;
+};
+
+template <int D> struct Shape {
+    static constexpr int kDH = D / 64;                 // 64-column planes of a head
+    static constexpr int kQBytes = BM * D * 2;         // one M-tile of Q
+    static constexpr int kSlotBytes = BN * D * 2;      // K or V of one KV tile
+    static constexpr int kPlaneQ = BM * 128;           // one 64-column plane of Q
+    static constexpr int kBarBytes = 2816;             // barriers, TMEM address, item slots, (m, l) of the rows
+    static constexpr int kFit = (int)((kSmemLimit - kMT * kQBytes - kBarBytes) / kSlotBytes);
+    static constexpr int kSlots = kFit < 8 ? kFit : 8;  // K/V ring depth
+    static constexpr size_t kSmem = (size_t)kMT * kQBytes + (size_t)kSlots * kSlotBytes + kBarBytes;
+    static_assert(kSlots >= 3, "the K/V ring needs at least three slots");
+    static_assert(kSmem <= kSmemLimit, "shared memory");
+};
+
+// A piece: tiles tile0 .. tile0 + nkv - 1 of an item.  `live` = 0 marks the end.
+struct Piece {
+    int table_seq, kvh, seq0, nseq, mt, tile0, nkv, C, live, pad;
+    int64_t row;      // row of (sequence seq0, q-head 0) in o and ml
+};
+constexpr int kItemSlots = 4;                 // pieces published ahead of their use
+
+template <int D, int kB>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                  const __grid_constant__ CUtensorMap tmap_v, const PrefixParams p) {
+    constexpr int kBlocksPerTile = BN / kB;          // cache blocks per KV tile
+    static_assert(kBlocksPerTile <= 32, "one TMA box per producer lane");
+    using SH = Shape<D>;
+    constexpr int kDH = SH::kDH, kQBytes = SH::kQBytes, kSlotBytes = SH::kSlotBytes;
+    constexpr int kPlaneQ = SH::kPlaneQ, kSlots = SH::kSlots;
+    // V: [block][D/64 plane][B rows][64]; 16-key MMA steps 0..3 of 64 keys start
+    // at 0, kVS1, kVS2 and kVS2 + kVS1
+    constexpr int kVBlockBytes = kDH * kB * 128;                       // one block, all planes
+    constexpr int kVS1 = (16 / kB) * kVBlockBytes + (16 % kB) * 128;
+    constexpr int kVS2 = (32 / kB) * kVBlockBytes + (32 % kB) * 128;
+    static_assert(((48 / kB) * kVBlockBytes + (48 % kB) * 128) == kVS1 + kVS2, "step 3 = s2 + s1");
+    constexpr int kVChunk = 64 / kB * kVBlockBytes;                    // 64 keys
+    constexpr int kVLbo = kB * 128;
+    constexpr int kVSbo = kB < 16 ? kVBlockBytes : 1024;
+    // K: [8-row group][D/64 plane][8 rows][64]
+    constexpr int kKSbo = kDH * 1024;
+    constexpr int kKPlane = 1024;
+    constexpr uint32_t kIdescQK = umma_idesc_bf16(BM, BN, 0);
+    constexpr uint32_t kIdescPV = umma_idesc_bf16(BM, D, 1);
+    constexpr uint32_t kAll = 0xffffffffu;
+
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *q_s = smem;
+    uint8_t *kv_s = smem + kMT * kQBytes;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(kv_s + kSlots * kSlotBytes);
+    uint64_t *q_full = bars;                       // Q of the piece landed
+    uint64_t *q_empty = q_full + 1;                // every QK product of the piece done
+    uint64_t *kv_full = q_empty + 1;               // [kSlots]: slot landed
+    uint64_t *kv_empty = kv_full + kSlots;         // [kSlots]: slot read by its products
+    uint64_t *s_full = kv_empty + kSlots;          // [tile]: S_t written
+    uint64_t *p_full = s_full + kMT;               // [tile]: P_t written (and O_t rescaled)
+    uint64_t *o_full = p_full + kMT;               // [tile]: last product of the piece into O_t done
+    uint64_t *p_half = o_full + kMT;               // [tile]: P_t's first 64 keys written
+    uint64_t *o_empty = p_half + kMT;              // [tile]: O_t read by the output warpgroup
+    uint64_t *l_full = o_empty + kMT;              // [tile]: the rows' (m, l) written
+    uint64_t *item_full = l_full + kMT;            // [kItemSlots]: piece published
+    uint64_t *item_empty = item_full + kItemSlots; // [kItemSlots]: piece read by every consumer
+    uint64_t *drained = item_empty + kItemSlots;   // every product issued has completed
+    uint32_t &tmem_base_s = *reinterpret_cast<uint32_t *>(drained + 1);
+    Piece *items = reinterpret_cast<Piece *>(drained + 2);           // [kItemSlots]
+    float2 *ml_s = reinterpret_cast<float2 *>(items + kItemSlots);   // [tile][row]
+    static_assert((3 + 2 * kSlots + 6 * kMT + 2 * kItemSlots + 2) * 8 + kItemSlots * sizeof(Piece) +
+                          kMT * BM * sizeof(float2) <= SH::kBarBytes,
+                  "barrier area");
+
+    // the warp index broadcast from lane 0 is provably warp-uniform
+    const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31;
+    if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled tiles need 1024-byte alignment
+        if (tid == 0) set_status(p.status, PA_ERR_CUDA);
+        grid_dependency_wait();
+        return;
+    }
+    // This grid starts once every decode CTA has passed its wait for the plan, so
+    // the plan is complete.  Shares for fewer CTAs than the grid has: the others
+    // leave their SMs (but not before the decode grid is done: what waits for
+    // this grid relies on both).
+    const int64_t T = p.plan.tile_start[p.num_groups];   // plain loads: written by the plan grid
+    const int64_t P = p.shares[0], cta = blockIdx.x;
+    const int64_t t_begin = cta < P ? share_begin(cta, T, P) : 0, t_end = cta < P ? share_begin(cta + 1, T, P) : 0;
+    grid_dependents_launch();    // every decode and prefix CTA runs before the merge's take up room
+    if (t_begin >= t_end) {
+        grid_dependency_wait();
+        return;
+    }
+
+    if (tid == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(kv_full + i, 1);
+            mbar_init(kv_empty + i, 1);
+        }
+        for (int t = 0; t < kMT; ++t) {
+            mbar_init(s_full + t, 1);
+            mbar_init(p_full + t, BM);
+            mbar_init(o_full + t, 1);
+            mbar_init(p_half + t, BM);
+            mbar_init(o_empty + t, BM);
+            mbar_init(l_full + t, BM);
+        }
+        for (int i = 0; i < kItemSlots; ++i) {
+            mbar_init(item_full + i, 1);
+            mbar_init(item_empty + i, 1 + 4 * kMT + 4);  // the MMA warp, every softmax and output warp
+        }
+        mbar_init(drained, 1);
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc(&tmem_base_s, kTmemCols);
+    if (warp == kProducerWarp && lane == 0) {
+        prefetch_tmap(&tmap_q);
+        prefetch_tmap(&tmap_k);
+        prefetch_tmap(&tmap_v);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_s;
+    // TMEM columns: S_t at t*BN (fp32); P_t, bf16 pairs, over the first BN/2 columns of S_t; O_t at kMT*BN + t*D
+    auto s_col = [](int t) { return (uint32_t)(t * BN); };
+    auto o_col = [](int t) { return (uint32_t)(kMT * BN + t * D); };
+    auto slot_of = [](int n) { return n % kSlots; };
+    auto phase_of = [](int n) { return (uint32_t)((n / kSlots) & 1); };
+    auto take_item = [&](int it, Piece &I) -> bool {
+        if (!mbar_wait_warp(item_full + it % kItemSlots, (uint32_t)((it / kItemSlots) & 1), p.wait_ns)) return false;
+        I = items[it % kItemSlots];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_empty + it % kItemSlots);
+        return true;
+    };
+
+    if (warp >= kOutWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+        // ================= output warpgroup: thread r writes (m, l, O) of row r of M-tile t after the piece's last
+        // product into O_t; the MMA warp waits for its o_empty before the next piece's first product into O_t
+        const int r = tid & (BM - 1);
+        const int head = r / p.pos, i_pos = r - head * p.pos;
+        const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        bool ok = true;
+        int no[kMT] = {};
+        for (int it = 0; ok; ++it) {
+            Piece I;
+            if (!take_item(it, I)) { ok = false; break; }
+            if (!I.live) break;
+#pragma unroll
+            for (int t = 0; t < kMT; ++t) {
+                if (t >= I.mt || !ok) continue;
+                if (!mbar_wait_warp(o_full + t, (uint32_t)(no[t] & 1), p.wait_ns) ||
+                    !mbar_wait_warp(l_full + t, (uint32_t)(no[t] & 1), p.wait_ns)) {
+                    ok = false;
+                    continue;
+                }
+                tc_fence_after();
+                const float2 ml = ml_s[t * BM + r];
+                const int i = t * p.pos + i_pos;            // sequence within the item
+                const bool row_valid = head < p.group && i < I.nseq;
+                const int64_t row = I.row + (row_valid ? (int64_t)i * p.group + head : 0);
+                float *dst = p.o + row * D;
+                if (row_valid) p.ml[row] = ml;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o0[16], o1[16];
+                    tmem_ld16(lane_addr + o_col(t) + 32 * c, o0);
+                    tmem_ld16(lane_addr + o_col(t) + 32 * c + 16, o1);
+                    tmem_wait_ld();
+                    if (c == D / 32 - 1) {       // O_t read: the next piece's products may overwrite it
+                        tc_fence_before();
+                        mbar_arrive(o_empty + t);
+                    }
+                    if (row_valid) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t a[8], b[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                a[e] = (h ? o1 : o0)[e];
+                                b[e] = (h ? o1 : o0)[8 + e];
+                            }
+                            st_global_v8(dst + 32 * c + 16 * h, a);      // whole 32-byte sectors
+                            st_global_v8(dst + 32 * c + 16 * h + 8, b);
+                        }
+                    }
+                }
+                ++no[t];
+            }
+        }
+        if (!ok && r == 0) {
+            set_status(p.status, PA_ERR_TIMEOUT);
+            note_wait_site(p.wait_sites, PA_WAIT_PREFILL_SOFTMAX);
+        }
+    } else if (warp >= kProducerWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSide));
+    if (warp == kProducerWarp) {
+        // ================= TMA producer
+        bool ok = true, stopped = false;
+        int n = 0, nq = 0, issued_end = 0;   // issued_end: ring entries issued so far
+        int64_t t_next = t_begin;
+        // the next piece of this CTA's share, published one piece ahead of its use
+        auto publish = [&](int it, Piece &I) -> bool {
+            bool okp = true;
+            if (lane == 0 && it >= kItemSlots &&
+                !mbar_wait(item_empty + it % kItemSlots, (uint32_t)(((it / kItemSlots) - 1) & 1), p.wait_ns))
+                okp = false;
+            okp = __shfl_sync(kAll, okp ? 1 : 0, 0) != 0;
+            I = Piece{};
+            if (t_next < t_end) {
+                const int spi = kMT * p.pos;
+                const PrefixItem x = prefix_item(p.plan, p.starts, p.num_groups, spi, BN, t_next);
+                const int i0 = x.part * spi;
+                I.table_seq = x.s0;
+                I.kvh = x.kvh;
+                I.seq0 = x.s0 + i0;
+                I.nseq = min(spi, x.n - i0);
+                I.mt = I.nseq > p.pos ? 2 : 1;
+                I.tile0 = x.tile;
+                I.nkv = (int)min((int64_t)(x.kt - x.tile), t_end - t_next);
+                I.C = x.C;
+                I.live = 1;
+                I.row = x.tile == 0 ? item_row(x.s0, x.n, x.kvh, i0, p.num_heads, p.group)
+                                    : (int64_t)p.num_seqs * p.num_heads + cta * p.item_rows;
+                t_next += I.nkv;
+            }
+            if (lane == 0 && okp) {
+                items[it % kItemSlots] = I;
+                mbar_arrive(item_full + it % kItemSlots);
+            }
+            return okp;
+        };
+        // block ids of piece X, 32 per chunk (lane l holds block 32*chunk + l of the piece); past the shared tokens (or
+        // invalid) the coordinate num_blocks is out of bounds and TMA fills zeros
+        auto load_ids = [&](const Piece &X, int chunk) {
+            const int lb = X.tile0 * kBlocksPerTile + chunk * 32 + lane;
+            int coord = p.num_blocks;
+            if (X.live && chunk * 32 + lane < X.nkv * kBlocksPerTile && lb < X.C / kB) {
+                const int32_t blk = __ldg(p.block_tables + (int64_t)X.table_seq * p.max_blocks + lb);
+                if (blk >= 0 && blk < p.num_blocks) coord = blk;
+                else set_status(p.status, PA_ERR_OUT_OF_RANGE);
+            }
+            return coord;
+        };
+        Piece I, I_next;
+        ok = publish(0, I);
+        int pre_cur = load_ids(I, 0), pre_next = load_ids(I, 1);
+        for (int it = 0; ok && I.live; ++it, I = I_next) {
+            if (!publish(it + 1, I_next)) { ok = false; break; }
+            int ids_cur = pre_cur, ids_next = pre_next, chunk_cur = 0;
+            pre_cur = load_ids(I_next, 0);
+            pre_next = load_ids(I_next, 1);
+            // Q: its buffer is free once every QK product of the previous piece completed
+            if (lane == 0) {
+                if (nq >= 1 && !mbar_wait(q_empty, (uint32_t)((nq - 1) & 1), p.wait_ns)) ok = false;
+                if (ok) {
+                    mbar_arrive_expect_tx(q_full, (uint32_t)(I.mt * kDH * p.pos * p.group * 128));
+                    for (int t = 0; t < I.mt; ++t)
+                        for (int pl = 0; pl < kDH; ++pl)
+                            tma_load_4d(q_s + t * kQBytes + pl * kPlaneQ, &tmap_q, 0, I.seq0 + t * p.pos, I.kvh * p.group,
+                                        pl, q_full);
+                }
+            }
+            ok = __shfl_sync(kAll, ok ? 1 : 0, 0) != 0;
+            if (!ok) break;
+            ++nq;
+            for (int j = 0; ok && j < I.nkv; ++j) {
+                if ((j * kBlocksPerTile) / 32 != chunk_cur) {
+                    ids_cur = ids_next;
+                    ++chunk_cur;
+                    ids_next = load_ids(I, chunk_cur + 1);
+                }
+                const int id0 = (j * kBlocksPerTile) & 31;
+                const int cbv = __shfl_sync(kAll, ids_cur, id0 + (lane & (kBlocksPerTile - 1)));
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int m = n + 2 * j + kv;
+                    if (p.stall == PA_STALL_PRODUCER && m >= p.stall_after) {
+                        stopped = true;   // test hook: entry m and later are never filled
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0 && m >= kSlots && !mbar_wait(kv_empty + slot_of(m), phase_of(m) ^ 1u, p.wait_ns))
+                        ok = false;
+                    ok = __shfl_sync(kAll, ok ? 1 : 0, 0) != 0;
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(kv_full + slot_of(m), kSlotBytes);
+                    __syncwarp();
+                    // lane b < kBlocksPerTile copies block b of K or V
+                    if (lane < kBlocksPerTile) {
+                        uint8_t *dst = kv_s + slot_of(m) * kSlotBytes + lane * kVBlockBytes;
+                        if (kv)
+                            tma_load_5d(dst, &tmap_v, 0, 0, 0, I.kvh, cbv, kv_full + slot_of(m));
+                        else if (kB == 8)
+                            tma_load_5d(dst, &tmap_k, 0, 0, 0, I.kvh, cbv, kv_full + slot_of(m));
+                        else
+                            tma_load_5d(dst, &tmap_k, 0, 0, I.kvh * kDH, 0, cbv, kv_full + slot_of(m));
+                    }
+                    issued_end = m + 1;
+                }
+            }
+            n += 2 * I.nkv;
+        }
+        if (!ok && !stopped && lane == 0) {
+            set_status(p.status, PA_ERR_TIMEOUT);
+            note_wait_site(p.wait_sites, PA_WAIT_PREFILL_PRODUCER);
+        }
+        // every copy this CTA issued has landed before the CTA may exit (default limit)
+        if (lane == 0) {
+            if (nq >= 1) mbar_wait(q_full, (uint32_t)((nq - 1) & 1));
+            for (int m = issued_end > kSlots ? issued_end - kSlots : 0; m < issued_end; ++m)
+                mbar_wait(kv_full + slot_of(m), phase_of(m));
+        }
+    } else if (warp == kMmaWarp) {
+        // ================= MMA issuer: all lanes follow the schedule, one elected lane issues.  Tensor-pipe order, per
+        // KV tile j: PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1), so one M-tile's products run while the other's softmax
+        // turns S into P.  QK_t(j+1) overwrites the TMEM columns that PV_t(j) reads P_t from; the pipe runs one
+        // thread's MMAs in issue order, so the read precedes the overwrite.
+        const uint32_t q_addr = smem_u32(q_s), kv_addr = smem_u32(kv_s);
+        const uint64_t dq = umma_desc_sw128(q_addr, 16, 1024);
+        const uint64_t dk = umma_desc_sw128(kv_addr, 16, kKSbo);
+        const uint64_t dv = umma_desc_sw128(kv_addr, kVLbo, kVSbo);
+        auto issue_qk = [&](int t, int nk) {      // S_t = Q_t K^T, K in ring entry nk
+            const uint32_t ko = (uint32_t)slot_of(nk) * kSlotBytes;
+#pragma unroll
+            for (int pl = 0; pl < D / 64; ++pl)
+                umma_bf16_k64(tmem + s_col(t), dq + ((uint32_t)(t * kQBytes + pl * kPlaneQ) >> 4),
+                              dk + ((ko + pl * kKPlane) >> 4), kIdescQK, pl > 0 ? 1u : 0u);
+        };
+        // O_t (+)= P_t V over keys 64 kq .. 64 kq + 63 (4 MMAs of 16), V in ring entry nv
+        auto issue_pv = [&](int t, int nv, int kq, bool first) {
+            const uint32_t vo = (uint32_t)slot_of(nv) * kSlotBytes;
+            umma_bf16_tmem_a_k64(tmem + o_col(t), tmem + s_col(t) + kq * 32, dv + ((vo + kq * kVChunk) >> 4), kIdescPV,
+                                 kVS1 >> 4, kVS2 >> 4, (!first || kq > 0) ? 1u : 0u);
+        };
+        bool ok = true, stopped = false;
+        int n = 0, nq = 0;
+        int J[kMT] = {}, no[kMT] = {};   // per M-tile: tiles and pieces so far
+        for (int it = 0; ok; ++it) {
+            Piece I;
+            if (!take_item(it, I)) { ok = false; break; }
+            if (!I.live) break;
+            const int nkv = __shfl_sync(kAll, I.nkv, 0), mt = __shfl_sync(kAll, I.mt, 0);
+            if (p.stall == PA_STALL_CONSUMER && n >= p.stall_after) { stopped = true; ok = false; break; }
+            if (!mbar_wait_warp(q_full, (uint32_t)(nq & 1), p.wait_ns) ||
+                !mbar_wait_warp(kv_full + slot_of(n), phase_of(n), p.wait_ns)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int t = 0; t < kMT; ++t)
+                if (t < mt) {
+                    issue_qk(t, n);
+                    umma_commit(s_full + t);
+                }
+            if (nkv == 1) umma_commit(q_empty);
+            umma_commit(kv_empty + slot_of(n));
+            for (int j = 0; j < nkv; ++j) {
+                const bool next = j + 1 < nkv;
+                const int nv = n + 2 * j + 1, nk = n + 2 * j + 2;
+                // test hook: stop, leaving ring entries unreleased, so the producer's wait runs out
+                if (p.stall == PA_STALL_CONSUMER && nv >= p.stall_after) { stopped = true; ok = false; break; }
+                if (!mbar_wait_warp(kv_full + slot_of(nv), phase_of(nv), p.wait_ns)) { ok = false; break; }
+#pragma unroll
+                for (int t = 0; t < kMT; ++t) {
+                    if (t >= mt || !ok) continue;
+                    // the piece's first product into O_t overwrites it: the output warpgroup has read the last piece's
+                    if (j == 0 && no[t] > 0 && !mbar_wait_warp(o_empty + t, (uint32_t)((no[t] - 1) & 1), p.wait_ns)) {
+                        ok = false;
+                        continue;
+                    }
+                    if (!mbar_wait_warp(p_half + t, (uint32_t)((J[t] + j) & 1), p.wait_ns)) { ok = false; continue; }
+                    tc_fence_after();
+                    issue_pv(t, nv, 0, j == 0);
+                    if (!mbar_wait_warp(p_full + t, (uint32_t)((J[t] + j) & 1), p.wait_ns)) { ok = false; continue; }
+                    tc_fence_after();
+                    issue_pv(t, nv, 1, j == 0);
+                    if (next) {
+                        if (t == 0 && !mbar_wait_warp(kv_full + slot_of(nk), phase_of(nk), p.wait_ns)) { ok = false; continue; }
+                        tc_fence_after();
+                        issue_qk(t, nk);
+                        umma_commit(s_full + t);
+                    } else {
+                        umma_commit(o_full + t);
+                    }
+                }
+                if (!ok) break;
+                umma_commit(kv_empty + slot_of(nv));
+                if (next) {
+                    umma_commit(kv_empty + slot_of(nk));
+                    if (j + 2 == nkv) umma_commit(q_empty);    // the piece's last QK products
+                }
+            }
+            n += 2 * nkv;
+            ++nq;
+#pragma unroll
+            for (int t = 0; t < kMT; ++t)
+                if (t < mt) {
+                    J[t] += nkv;
+                    ++no[t];
+                }
+        }
+        if (!ok && !stopped && lane == 0) {
+            set_status(p.status, PA_ERR_TIMEOUT);
+            note_wait_site(p.wait_sites, PA_WAIT_PREFILL_MMA);
+        }
+        // drain (default limit): everything issued must finish before TMEM is released
+        umma_commit(drained);
+        mbar_wait_warp(drained, 0);
+        __syncwarp();
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        // ================= softmax warpgroup t: thread r owns row r of M-tile t
+        const int t = warp >> 2;
+        const int r = tid & (BM - 1);
+        const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const float sl2 = p.scale_log2;
+        bool ok = true;
+        int J = 0, no = 0;
+        for (int it = 0; ok; ++it) {
+            Piece I;
+            if (!take_item(it, I)) { ok = false; break; }
+            if (!I.live) break;
+            if (t >= I.mt) continue;
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < I.nkv; ++j) {
+                if (!mbar_wait_warp(s_full + t, (uint32_t)((J + j) & 1), p.wait_ns)) { ok = false; break; }
+                tc_fence_after();
+                const int lim = I.C - (I.tile0 + j) * BN;     // shared keys from the tile's first on
+                // S is read whole and its max taken first, so P can go out in two halves of 64 keys (the tensor pipe
+                // takes the first while the second is computed).  The piece's first tile takes its own max; later ones
+                // run with the running max m: P stays <= 2^8 unless the tile's max exceeds it by more than 8, and
+                // then (rarely) the row moves its max and rescales O first.
+                uint32_t sr[BN / 32][32];
+                auto mask = [&](int c) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * c + e >= lim) sr[c][e] = __float_as_uint(-INFINITY);
+                };
+                tmem_ld32(lane_addr + s_col(t), sr[0]);
+                tmem_ld32(lane_addr + s_col(t) + 32, sr[1]);
+                tmem_wait_ld_regs(sr[0], sr[1]);
+                tmem_ld32(lane_addr + s_col(t) + 64, sr[2]);
+                tmem_ld32(lane_addr + s_col(t) + 96, sr[3]);
+                if (lim < BN) { mask(0); mask(1); }
+                float a0 = -INFINITY, a1 = -INFINITY;
+                auto max_of = [&](int c) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        a0 = fmax3(a0, __uint_as_float(sr[c][e]), __uint_as_float(sr[c][e + 1]));
+                        a1 = fmax3(a1, __uint_as_float(sr[c][e + 2]), __uint_as_float(sr[c][e + 3]));
+                    }
+                };
+                max_of(0);
+                max_of(1);
+                tmem_wait_ld_regs(sr[2], sr[3]);
+                if (lim < BN) { mask(2); mask(3); }
+                max_of(2);
+                max_of(3);
+                const float m_tile = fmaxf(a0, a1) * sl2;
+                if (j == 0) {
+                    m = m_tile == -INFINITY ? 0.f : m_tile;
+                } else {
+                    const bool need = m_tile > m + 8.f;
+                    if (__any_sync(kAll, need)) {
+                        const float m_new = need ? m_tile : m;
+                        const float alpha = fast_exp2(m - m_new);
+                        l *= alpha;
+                        // PV_t(j-1) completed before S_t(j) was committed, so O_t is final here
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(lane_addr + o_col(t) + 32 * c, o);
+                            tmem_wait_ld();
+                            reg_fence32(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st32(lane_addr + o_col(t) + 32 * c, o);
+                        }
+                        m = m_new;
+                    }
+                }
+                // P for key pairs u0..u0+31 into pk, rounded to bf16 (the products' operand type): independent
+                // roundings of half a step, beside a result rounded to bf16 itself; l sums the unrounded values
+                const float2 sl2x2 = make_float2(sl2, sl2), negm = make_float2(-m, -m);
+                float2 ls = make_float2(0.f, 0.f);
+                uint32_t pk[BN / 4];
+                auto pass = [&](auto u0c) {
+                    constexpr int u0 = decltype(u0c)::value;
+#pragma unroll
+                    for (int u = u0; u < u0 + BN / 4; ++u) {
+                        const float s0 = __uint_as_float(sr[u >> 4][(2 * u) & 31]);
+                        const float s1 = __uint_as_float(sr[u >> 4][(2 * u + 1) & 31]);
+                        const float2 x = fma_f32x2(make_float2(s0, s1), sl2x2, negm);
+                        const float p0 = fast_exp2(x.x);
+                        const float p1 = fast_exp2(x.y);
+                        ls = add_f32x2(ls, make_float2(p0, p1));
+                        pk[u - u0] = pack_bf16x2(p0, p1);
+                    }
+                };
+                pass(std::integral_constant<int, 0>{});
+                tmem_st32(lane_addr + s_col(t), pk);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(p_half + t);
+                pass(std::integral_constant<int, BN / 4>{});
+                tmem_st32(lane_addr + s_col(t) + 32, pk);
+                l += ls.x + ls.y;
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(p_full + t);
+            }
+            if (!ok) break;
+            // (m, l) for the output warpgroup, which read the last piece's before it released O_t
+            if (no > 0 && !mbar_wait_warp(o_empty + t, (uint32_t)((no - 1) & 1), p.wait_ns)) { ok = false; break; }
+            ml_s[t * BM + r] = make_float2(m, l);
+            mbar_arrive(l_full + t);
+            J += I.nkv;
+            ++no;
+        }
+        if (!ok && r == 0) {
+            set_status(p.status, PA_ERR_TIMEOUT);
+            note_wait_site(p.wait_sites, PA_WAIT_PREFILL_SOFTMAX);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+    grid_dependency_wait();
+}
+
+CUresult encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                const cuuint32_t *box) {
+    auto fn = tensor_map_encoder();
+    if (!fn) return CUDA_ERROR_NOT_FOUND;
+    const cuuint32_t step[5] = {1, 1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+// q [num_seqs][num_heads][D]: one plane of `pos` sequences x `group` heads lands as [head][sequence][64]
+CUresult make_q_map(CUtensorMap *map, const void *q, int num_seqs, int num_heads, int D, int pos, int group) {
+    const cuuint64_t dims[4] = {64, (cuuint64_t)num_seqs, (cuuint64_t)num_heads, (cuuint64_t)(D / 64)};
+    const cuuint64_t strides[3] = {(cuuint64_t)num_heads * D * 2, (cuuint64_t)D * 2, 128};
+    const cuuint32_t box[4] = {64, (cuuint32_t)pos, (cuuint32_t)group, 1};
+    return encode(map, q, 4, dims, strides, box);
+}
+
+// One block of one kv-head: [plane][B rows][64]
+CUresult make_v_map(CUtensorMap *map, const void *pool, int num_blocks, int kB, int hkv, int D) {
+    const cuuint64_t dims[5] = {64, (cuuint64_t)kB, (cuuint64_t)(D / 64), (cuuint64_t)hkv, (cuuint64_t)num_blocks};
+    const cuuint64_t strides[4] = {(cuuint64_t)hkv * D * 2, 128, (cuuint64_t)D * 2, (cuuint64_t)kB * hkv * D * 2};
+    const cuuint32_t box[5] = {64, (cuuint32_t)kB, (cuuint32_t)(D / 64), 1, 1};
+    return encode(map, pool, 5, dims, strides, box);
+}
+
+// One block of one kv-head: [8-row group][plane][8 rows][64] (at B = 8 the map above gives the same)
+CUresult make_k_map(CUtensorMap *map, const void *pool, int num_blocks, int kB, int hkv, int D) {
+    const cuuint64_t dims[5] = {64, 8, (cuuint64_t)hkv * (D / 64), (cuuint64_t)(kB / 8), (cuuint64_t)num_blocks};
+    const cuuint64_t strides[4] = {(cuuint64_t)hkv * D * 2, 128, (cuuint64_t)8 * hkv * D * 2, (cuuint64_t)kB * hkv * D * 2};
+    const cuuint32_t box[5] = {64, 8, (cuuint32_t)(D / 64), (cuuint32_t)(kB / 8), 1};
+    return encode(map, pool, 5, dims, strides, box);
+}
+
+template <int D, int B>
+cudaError_t launch_main(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const PrefixParams &prm,
+                        int grid, cudaStream_t stream) {
+    const size_t smem = Shape<D>::kSmem;
+    auto kern = prefix_kernel<D, B>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, dim3(grid), dim3(kThreads), smem, stream, mq, mk, mv, prm);
+}
+
+}  // namespace
+
+int prefix_seqs_per_item(int group) { return kMT * (BM / group); }
+
+cudaError_t launch_prefix(const AttnArgs &a, const SharedJob &job, cudaStream_t stream) {
+    const int G = a.num_heads / a.num_kv_heads;
+    CUtensorMap mq, mk, mv;
+    if (make_q_map(&mq, a.q, a.num_seqs, a.num_heads, a.head_dim, BM / G, G) != CUDA_SUCCESS ||
+        (a.block_size == 8 ? make_v_map(&mk, a.k_cache, a.num_blocks, 8, a.num_kv_heads, a.head_dim)
+                           : make_k_map(&mk, a.k_cache, a.num_blocks, a.block_size, a.num_kv_heads, a.head_dim)) != CUDA_SUCCESS ||
+        make_v_map(&mv, a.v_cache, a.num_blocks, a.block_size, a.num_kv_heads, a.head_dim) != CUDA_SUCCESS)
+        return cudaErrorNotSupported;
+    PrefixParams prm;
+    prm.plan = job.plan;
+    prm.starts = job.groups.starts;
+    prm.block_tables = a.block_tables;
+    prm.shares = job.shares;
+    prm.o = job.pre_o;
+    prm.ml = job.pre_ml;
+    prm.num_seqs = a.num_seqs;
+    prm.num_groups = job.groups.num_groups;
+    prm.num_heads = a.num_heads;
+    prm.group = G;
+    prm.pos = BM / G;
+    prm.item_rows = job.item_rows;
+    prm.max_blocks = a.max_blocks;
+    prm.num_blocks = a.num_blocks;
+    prm.scale_log2 = a.scale * 1.4426950408889634f;
+    prm.status = a.status;
+    const WaitTest &wt = wait_test();
+    prm.wait_ns = wt.limit_ns;
+    prm.stall = wt.stall;
+    prm.stall_after = wt.after;
+    prm.wait_sites = wt.sites;
+    const int grid = prefix_grid();
+    switch (a.head_dim * 100 + a.block_size) {
+        case 6408: return launch_main<64, 8>(mq, mk, mv, prm, grid, stream);
+        case 6416: return launch_main<64, 16>(mq, mk, mv, prm, grid, stream);
+        case 6432: return launch_main<64, 32>(mq, mk, mv, prm, grid, stream);
+        case 12808: return launch_main<128, 8>(mq, mk, mv, prm, grid, stream);
+        case 12816: return launch_main<128, 16>(mq, mk, mv, prm, grid, stream);
+        case 12832: return launch_main<128, 32>(mq, mk, mv, prm, grid, stream);
+        default: return cudaErrorNotSupported;
+    }
+}
+
+}  // namespace pa

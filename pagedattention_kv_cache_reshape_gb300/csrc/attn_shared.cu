@@ -25,109 +25,35 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanSmemGroups = 4096;   // group starts and smallest contexts kept in shared memory
+constexpr int kMaxTcGroups = 16384;
 constexpr int kMaxCtas = 512;           // partial slots reserved for share boundaries
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // ------------------------------------------------------------------ plan
-// Exclusive scan of v over the CTA (1024 threads); `total` the sum.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *warp_tot, int64_t &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t incl = v;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += y;
-    }
-    __syncthreads();   // the previous scan's totals have been read
-    if (lane == 31) warp_tot[warp] = incl;
-    __syncthreads();
-    int64_t before = 0;
-    total = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        const int64_t t = warp_tot[w];
-        if (w < warp) before += t;
-        total += t;
-    }
-    return before + incl - v;
-}
-
-// One CTA.  Group starts that do not run from 0 to num_seqs in order leave
-// every sequence unshared (and set the status); so does a prefix length out of
-// range for its group.
+// One CTA: the groups' plan, and the own stream's starts (own_start[s]: tiles
+// of one kv-head of the sequences before).
 __global__ void __launch_bounds__(kPlanThreads)
-    shared_plan_kernel(const SharedGroups g, const SharedPlan plan, int32_t *status) {
-    __shared__ int32_t starts_s[kPlanSmemGroups + 1], min_s[kPlanSmemGroups];
+    shared_plan_kernel(const SharedGroups g, const SharedPlan plan, int32_t *scratch, int64_t *own_start, int32_t *status) {
+    __shared__ int32_t starts_s[kPlanSmemGroups], lens_s[kPlanSmemGroups];
     __shared__ int64_t warp_tot[kPlanThreads / 32];
     const int tid = threadIdx.x;
-    const int S = g.num_seqs, NG = g.num_groups;
     grid_dependency_wait();
     grid_dependents_launch();
-    const bool in_smem = NG <= kPlanSmemGroups;
-    int32_t *min_ctx = in_smem ? min_s : plan.min_ctx;
-    int wrong = 0;
-    for (int i = tid; i < NG; i += kPlanThreads) {
-        const int a = __ldg(g.starts + i), b = __ldg(g.starts + i + 1);
-        wrong |= a < 0 || b < a || b > S || (i == 0 && a != 0) || (i == NG - 1 && b != S);
-        if (in_smem) starts_s[i] = a;
-        min_ctx[i] = INT_MAX;
-    }
-    const bool ok = !__syncthreads_or(wrong);
-    if (!ok && tid == 0) set_status(status, PA_ERR_OUT_OF_RANGE);
-    const int32_t *starts = in_smem ? starts_s : g.starts;
-    for (int s = tid; s < S; s += kPlanThreads) {
-        const int ctx = __ldg(g.context_lens + s);
-        const int grp = ok ? last_at_most(starts, NG, s) : 0;
-        plan.seq_group[s] = grp;
-        if (ctx > 0 && ctx <= g.max_tokens) atomicMin(min_ctx + grp, ctx);
-        else set_status(status, PA_ERR_OUT_OF_RANGE);
-    }
-    __syncthreads();
-    int64_t items = 0, tiles = 0;
-    for (int base = 0; base < NG; base += kPlanThreads) {
-        const int i = base + tid;
-        int C = 0, mine = 0;
-        if (i < NG && ok) {
-            const int n = __ldg(g.starts + i + 1) - __ldg(g.starts + i), P = __ldg(g.prefix_lens + i);
-            const int least = in_smem ? min_s[i] : __ldcg(plan.min_ctx + i);   // (global atomics: not through L1)
-            if (P < 0 || P > g.max_tokens) set_status(status, PA_ERR_OUT_OF_RANGE);
-            else if (n >= 2 && least != INT_MAX) C = min(P, least - 1) / g.block_size * g.block_size;
-            if (C > 0) mine = g.num_kv_heads * ((n + g.seqs_per_item - 1) / g.seqs_per_item);
-        }
-        const int64_t t = (int64_t)mine * ((C + g.keys_per_tile - 1) / g.keys_per_tile);
-        int64_t total;
-        const int64_t item0 = block_scan(mine, warp_tot, total) + items;
-        items += total;
-        const int64_t tile0 = block_scan(t, warp_tot, total) + tiles;
-        tiles += total;
-        if (i < NG) {
-            plan.shared_len[i] = C;
-            plan.item_start[i] = (int32_t)item0;
-            plan.tile_start[i] = tile0;
-        }
-    }
-    if (tid == 0) {
-        plan.item_start[NG] = (int32_t)items;
-        plan.tile_start[NG] = tiles;
-    }
+    const bool in_smem = g.num_groups <= kPlanSmemGroups;
+    int32_t *lens = in_smem ? lens_s : scratch;
+    const bool ok = shared_lens<kPlanThreads>(g, in_smem ? starts_s : nullptr, lens, status);
+    shared_write_plan<kPlanThreads>(g, plan, ok, in_smem ? starts_s : g.starts, lens, warp_tot);
     __syncthreads();
     int64_t own = 0;
-    for (int base = 0; base < S; base += kPlanThreads) {
-        const int s = base + tid;
-        int len = 0;
-        if (s < S) {
-            const int ctx = __ldg(g.context_lens + s);
-            if (ctx > 0 && ctx <= g.max_tokens) len = ctx - plan.shared_len[plan.seq_group[s]];
-        }
+    for (int base = 0; base < g.num_seqs; base += kPlanThreads) {
+        const int s = base + tid, len = s < g.num_seqs ? plan.own_len[s] : 0;
         int64_t total;
-        const int64_t own0 = block_scan((len + g.keys_per_tile - 1) / g.keys_per_tile, warp_tot, total) + own;
+        const int64_t first = block_scan<kPlanThreads>((len + g.keys_per_tile - 1) / g.keys_per_tile, warp_tot, total) + own;
         own += total;
-        if (s < S) {
-            plan.own_len[s] = len;
-            plan.own_start[s] = own0;
-        }
+        if (s < g.num_seqs) own_start[s] = first;
     }
-    if (tid == 0) plan.own_start[S] = own;
+    if (tid == 0) own_start[g.num_seqs] = own;
 }
 
 // ------------------------------------------------------------------ CUDA-core kernel
@@ -142,9 +68,10 @@ struct CcParams {
     const int32_t *block_tables;
     const int32_t *group_starts;
     SharedPlan plan;
-    float *pre_o;      // prefix pieces: [item + share][item_rows][D]
-    float2 *pre_ml;    // [item + share][item_rows]
-    float *own_o;      // own pieces: [sequence * num_kv_heads + kv-head + share][G][D]
+    const int64_t *own_start;
+    float *pre_o;      // prefix pieces: [rows][D]
+    float2 *pre_ml;    // [rows]
+    float *own_o;      // own pieces: [num_seqs * num_heads + shares * G][D]
     float2 *own_ml;
     int item_rows;     // seqs_per_item * G
     int seqs_per_item;
@@ -358,40 +285,35 @@ __global__ void __launch_bounds__(kCcThreads, 2) shared_cc_kernel(const CcParams
     const int64_t T0 = p.plan.tile_start[p.num_groups];
     int64_t t = share_begin(c, T0, P);
     const int64_t t_end = share_begin(c + 1, T0, P);
+    const int64_t rows0 = (int64_t)p.num_seqs * p.num_heads;
     while (t < t_end) {
-        const int g = last_at_most(p.plan.tile_start, p.num_groups, t);   // (groups without tiles are passed over)
-        const int C = p.plan.shared_len[g], kt = (C + kKeys - 1) / kKeys;
-        const int s0 = __ldg(p.group_starts + g), n = __ldg(p.group_starts + g + 1) - s0;
-        const int64_t local = t - p.plan.tile_start[g];
-        const int item = (int)(local / kt), tile = (int)(local - (int64_t)item * kt);
-        const int per_head = (n + p.seqs_per_item - 1) / p.seqs_per_item;
-        const int kvh = item / per_head, part = item - kvh * per_head;
-        const int tiles = (int)min((int64_t)(kt - tile), t_end - t);
-        const int64_t slot = p.plan.item_start[g] + item + c;
+        const PrefixItem it = prefix_item(p.plan, p.group_starts, p.num_groups, p.seqs_per_item, kKeys, t);
+        const int tiles = (int)min((int64_t)(it.kt - it.tile), t_end - t), i0 = it.part * p.seqs_per_item;
+        const int64_t row = it.tile == 0 ? item_row(it.s0, it.n, it.kvh, i0, p.num_heads, G) : rows0 + c * p.item_rows;
         CcPiece w;
-        w.table = p.block_tables + (int64_t)s0 * p.max_blocks;
-        w.s0 = s0 + part * p.seqs_per_item;
-        w.rows = min(p.seqs_per_item, n - part * p.seqs_per_item) * G;
-        w.kvh = kvh;
-        w.key0 = tile * kKeys;
-        w.key1 = (int)min((int64_t)C, (int64_t)(tile + tiles) * kKeys);
-        w.o = p.pre_o + slot * p.item_rows * D;
-        w.ml = p.pre_ml + slot * p.item_rows;
+        w.table = p.block_tables + (int64_t)it.s0 * p.max_blocks;
+        w.s0 = it.s0 + i0;
+        w.rows = min(p.seqs_per_item, it.n - i0) * G;
+        w.kvh = it.kvh;
+        w.key0 = it.tile * kKeys;
+        w.key1 = (int)min((int64_t)it.C, (int64_t)(it.tile + tiles) * kKeys);
+        w.o = p.pre_o + row * D;
+        w.ml = p.pre_ml + row;
         cc_any_rows<T, D>(p, w, cc_smem);
         t += tiles;
     }
     // the sequences' own: by sequence, then kv-head
-    const int64_t T1 = p.plan.own_start[p.num_seqs] * p.num_kv_heads;
+    const int64_t T1 = p.own_start[p.num_seqs] * p.num_kv_heads;
     t = share_begin(c, T1, P);
     const int64_t t_last = share_begin(c + 1, T1, P);
     while (t < t_last) {
-        const int s = last_at_most(p.plan.own_start, p.num_seqs, t / p.num_kv_heads);
+        const int s = last_at_most(p.own_start, p.num_seqs, t / p.num_kv_heads);
         const int len = p.plan.own_len[s], kt = (len + kKeys - 1) / kKeys;
-        const int64_t local = t - p.plan.own_start[s] * p.num_kv_heads;
+        const int64_t local = t - p.own_start[s] * p.num_kv_heads;
         const int kvh = (int)(local / kt), tile = (int)(local - (int64_t)kvh * kt);
         const int tiles = (int)min((int64_t)(kt - tile), t_last - t);
         const int C = p.plan.shared_len[p.plan.seq_group[s]];
-        const int64_t slot = (int64_t)s * p.num_kv_heads + kvh + c;
+        const int64_t row = tile == 0 ? (int64_t)s * p.num_heads + kvh * G : rows0 + c * G;
         CcPiece w;
         w.table = p.block_tables + (int64_t)s * p.max_blocks;
         w.s0 = s;
@@ -399,8 +321,8 @@ __global__ void __launch_bounds__(kCcThreads, 2) shared_cc_kernel(const CcParams
         w.kvh = kvh;
         w.key0 = C + tile * kKeys;
         w.key1 = (int)min((int64_t)C + len, (int64_t)w.key0 + (int64_t)tiles * kKeys);
-        w.o = p.own_o + slot * G * D;
-        w.ml = p.own_ml + slot * G;
+        w.o = p.own_o + row * D;
+        w.ml = p.own_ml + row;
         cc_any_rows<T, D>(p, w, cc_smem);
         t += tiles;
     }
@@ -411,11 +333,13 @@ struct MergeParams {
     void *out;
     const int32_t *group_starts;
     SharedPlan plan;
+    const int64_t *own_start;   // null: own_o holds the own parts whole, in their first pieces' rows
     const float *pre_o;
     const float2 *pre_ml;
     const float *own_o;
     const float2 *own_ml;
-    int pre_shares;     // CTAs that cut the prefix stream
+    const int32_t *pre_shares_dev;   // CTAs that cut the prefix stream; null: pre_shares
+    int pre_shares;
     int own_shares;     // CTAs that cut the own stream
     int item_rows;
     int seqs_per_item;
@@ -452,11 +376,11 @@ __device__ __forceinline__ void load_dims(const float *src, float (&v)[D / 32]) 
     }
 }
 
-// Pieces of one item, tiles [t0, t0 + n) of a stream of T tiles cut into P shares, in order; slot0 + share holds a
-// piece of `rows` rows, of which `row` is taken.  Four pieces' loads are in flight at a time.
+// Pieces of one item, tiles [t0, t0 + n) of a stream of T tiles cut into P shares, in order: the first in row `row0`,
+// that of share c in row extra + c * rows.  Four pieces' loads are in flight at a time.
 template <int D>
-__device__ __forceinline__ void merge_stream(RowSum<D> &sum, const float *o, const float2 *ml, int64_t slot0, int rows,
-                                             int row, int64_t t0, int64_t n, int64_t T, int64_t P) {
+__device__ __forceinline__ void merge_stream(RowSum<D> &sum, const float *o, const float2 *ml, int64_t row0, int64_t extra,
+                                             int rows, int64_t t0, int64_t n, int64_t T, int64_t P) {
     constexpr int kBatch = 4;
     const int lane = threadIdx.x & 31;
     const int64_t c0 = share_of(t0, T, P), c1 = share_of(t0 + n - 1, T, P);
@@ -468,7 +392,7 @@ __device__ __forceinline__ void merge_stream(RowSum<D> &sum, const float *o, con
         for (int k = 0; k < kBatch; ++k) {
             const int64_t c = cb + k;
             use[k] = c <= c1 && share_begin(c, T, P) < share_begin(c + 1, T, P);   // an empty share holds no piece
-            const int64_t at = (slot0 + (use[k] ? c : c0)) * rows + row;
+            const int64_t at = use[k] && c > c0 ? extra + c * rows : row0;
             x[k] = __ldcg(ml + at);
             load_dims<D>(o + at * D + lane * (D / 32), v[k]);
         }
@@ -490,20 +414,27 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
     if (len <= 0) return;   // context length out of range: the row stays as it was
     const int G = p.num_heads / p.num_kv_heads, kvh = h / G, hh = h - kvh * G;
     const int g = p.plan.seq_group[s], C = p.plan.shared_len[g];
+    if (!p.own_start && C == 0) return;   // the decode kernel wrote the row
+    const int64_t rows0 = (int64_t)p.num_seqs * p.num_heads;
     RowSum<D> sum;
     if (C > 0) {
         const int s0 = __ldg(p.group_starts + g), n = __ldg(p.group_starts + g + 1) - s0;
         const int per_head = (n + p.seqs_per_item - 1) / p.seqs_per_item;
         const int part = (s - s0) / p.seqs_per_item, item = kvh * per_head + part;
         const int64_t kt = (C + p.keys_per_tile - 1) / p.keys_per_tile;
-        merge_stream<D>(sum, p.pre_o, p.pre_ml, p.plan.item_start[g] + item, p.item_rows,
-                        (s - s0 - part * p.seqs_per_item) * G + hh, p.plan.tile_start[g] + item * kt, kt,
-                        p.plan.tile_start[p.num_groups], p.pre_shares);
+        merge_stream<D>(sum, p.pre_o, p.pre_ml, item_row(s0, n, kvh, s - s0, p.num_heads, G) + hh,
+                        rows0 + (s - s0 - part * p.seqs_per_item) * G + hh, p.item_rows, p.plan.tile_start[g] + item * kt,
+                        kt, p.plan.tile_start[p.num_groups], p.pre_shares_dev ? *p.pre_shares_dev : p.pre_shares);
     }
-    const int64_t kt = (len + p.keys_per_tile - 1) / p.keys_per_tile;
-    merge_stream<D>(sum, p.own_o, p.own_ml, (int64_t)s * p.num_kv_heads + kvh, G, hh,
-                    p.plan.own_start[s] * p.num_kv_heads + kvh * kt, kt,
-                    p.plan.own_start[p.num_seqs] * p.num_kv_heads, p.own_shares);
+    if (p.own_start) {
+        const int64_t kt = (len + p.keys_per_tile - 1) / p.keys_per_tile;
+        merge_stream<D>(sum, p.own_o, p.own_ml, r, rows0 + hh, G, p.own_start[s] * p.num_kv_heads + kvh * kt, kt,
+                        p.own_start[p.num_seqs] * p.num_kv_heads, p.own_shares);
+    } else {
+        float v[D / 32];
+        load_dims<D>(p.own_o + r * D + lane * (D / 32), v);
+        sum.add(__ldcg(p.own_ml + r), v);
+    }
     T *dst = static_cast<T *>(p.out) + r * D + lane * (D / 32);
     const float inv = 1.f / sum.L;
 #pragma unroll
@@ -513,31 +444,35 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
 // ------------------------------------------------------------------ host side
 // Workspace: the plan's arrays, then the pieces.
 struct Layout {
-    size_t seq_group, own_len, shared_len, min_ctx, item_start, tile_start, own_start, pre_ml, pre_o, own_ml, own_o, total;
+    size_t seq_group, own_len, shared_len, scratch, tile_start, own_start, pre_ml, pre_o, own_ml, own_o, total;
 };
 
 Layout layout(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int head_dim) {
     Layout w;
-    const size_t S = num_seqs, NG = num_groups, HK = num_kv_heads, G = num_heads / num_kv_heads > 0 ? num_heads / num_kv_heads : 1;
+    const size_t S = num_seqs, NG = num_groups, G = num_heads / num_kv_heads > 0 ? num_heads / num_kv_heads : 1;
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t a = at; at = align_up(at + bytes, 256); return a; };
     w.seq_group = take(4 * S);
     w.own_len = take(4 * S);
     w.shared_len = take(4 * NG);
-    w.min_ctx = take(4 * NG);
-    w.item_start = take(4 * (NG + 1));
+    w.scratch = take(4 * NG);
     w.tile_start = take(8 * (NG + 1));
     w.own_start = take(8 * (S + 1));
     const size_t spi = kRows / G > 0 ? kRows / G : 1;
-    // a group's items: its sequences by spi, rounded up
-    const size_t pre_rows = (HK * (S / spi + (NG < S ? NG : S)) + kMaxCtas) * (spi < S ? spi : S) * G;
-    const size_t own_rows = (HK * S + kMaxCtas) * G;
+    const size_t pre_rows = S * num_heads + kMaxCtas * (spi < S ? spi : S) * G, own_rows = S * num_heads + kMaxCtas * G;
     w.pre_ml = take(8 * pre_rows);
     w.pre_o = take(4 * pre_rows * head_dim);
     w.own_ml = take(8 * own_rows);
     w.own_o = take(4 * own_rows * head_dim);
     w.total = at;
     return w;
+}
+
+template <typename T, int D>
+cudaError_t launch_merge(const MergeParams &mg, cudaStream_t stream) {
+    const int64_t rows = (int64_t)mg.num_seqs * mg.num_heads;
+    return launch_dependent(shared_merge_kernel<T, D>, dim3((unsigned)((rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32))),
+                            dim3(kMergeThreads), 0, stream, mg);
 }
 
 template <typename T, int D>
@@ -548,33 +483,95 @@ cudaError_t launch_typed(const CcParams &cc, const MergeParams &mg, int grid, cu
     if (e != cudaSuccess) return e;
     e = launch_dependent(kern, dim3(grid), dim3(kCcThreads), smem, stream, cc);
     if (e != cudaSuccess) return e;
-    const int64_t rows = (int64_t)mg.num_seqs * mg.num_heads;
-    return launch_dependent(shared_merge_kernel<T, D>, dim3((unsigned)((rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32))),
-                            dim3(kMergeThreads), 0, stream, mg);
+    return launch_merge<T, D>(mg, stream);
+}
+
+// Workspace of the tensor-core path: the plan's arrays, the prefix pieces, the own parts, the decode kernel's.
+struct TcLayout {
+    size_t seq_group, own_len, shared_len, tile_start, shares, pre_ml, pre_o, own_ml, own_o, decode, total;
+    int item_rows;
+};
+
+TcLayout tc_layout(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int head_dim, int max_blocks, int B) {
+    TcLayout w;
+    const size_t S = num_seqs, NG = num_groups;
+    const int G = num_heads / num_kv_heads > 0 ? num_heads / num_kv_heads : 1;
+    const int spi = G <= 128 ? prefix_seqs_per_item(G) : 1;
+    w.item_rows = (spi < num_seqs ? spi : num_seqs) * G;
+    size_t at = 0;
+    auto take = [&](size_t bytes) { const size_t a = at; at = align_up(at + bytes, 256); return a; };
+    w.seq_group = take(4 * S);
+    w.own_len = take(4 * S);
+    w.shared_len = take(4 * NG);
+    w.tile_start = take(8 * (NG + 1));
+    w.shares = take(4);
+    const size_t rows = S * num_heads, pre_rows = rows + (size_t)kMaxPrefixCtas * w.item_rows;
+    w.pre_ml = take(8 * pre_rows);
+    w.pre_o = take(4 * pre_rows * head_dim);
+    w.own_ml = take(8 * rows);
+    w.own_o = take(4 * rows * head_dim);
+    w.decode = take(split_decode_workspace(num_seqs, num_heads, head_dim, max_blocks, B));
+    w.total = at;
+    return w;
+}
+
+// The tensor-core path takes what the split decode takes, rows on 16 bytes, a positive scale (the running maximum is
+// that of the unscaled products) and groups whose starts the plan's CTAs hold in shared memory.
+bool tc_supported(const AttnArgs &a, int num_groups) {
+    return split_decode_supported(a) && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.scale > 0.f &&
+           a.scale < INFINITY && num_groups <= kMaxTcGroups;
+}
+
+cudaError_t launch_tc(const AttnArgs &a, const int32_t *group_starts, const int32_t *prefix_lens, int num_groups,
+                      void *workspace, cudaStream_t stream) {
+    const TcLayout w = tc_layout(a.num_seqs, num_groups, a.num_heads, a.num_kv_heads, a.head_dim, a.max_blocks, a.block_size);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const int spi = prefix_seqs_per_item(a.num_heads / a.num_kv_heads);
+    SharedJob job;
+    job.groups = {a.context_lens, group_starts, prefix_lens, a.num_seqs, num_groups, a.num_kv_heads, a.block_size,
+                  (int64_t)a.max_blocks * a.block_size, spi, kPrefixKeys};
+    job.plan = {reinterpret_cast<int32_t *>(ws + w.seq_group), reinterpret_cast<int32_t *>(ws + w.own_len),
+                reinterpret_cast<int32_t *>(ws + w.shared_len), reinterpret_cast<int64_t *>(ws + w.tile_start)};
+    job.shares = reinterpret_cast<int32_t *>(ws + w.shares);
+    job.pre_o = reinterpret_cast<float *>(ws + w.pre_o);
+    job.pre_ml = reinterpret_cast<float2 *>(ws + w.pre_ml);
+    job.item_rows = w.item_rows;
+    job.own_o = reinterpret_cast<float *>(ws + w.own_o);
+    job.own_ml = reinterpret_cast<float2 *>(ws + w.own_ml);
+    const std::function<cudaError_t()> prefix = [&] { return launch_prefix(a, job, stream); };
+    cudaError_t e = launch_split_decode(a, ws + w.decode, w.total - w.decode, stream, false, nullptr, nullptr, &prefix, &job);
+    if (e != cudaSuccess) return e;
+    MergeParams mg = {a.out, group_starts, job.plan, nullptr, job.pre_o, job.pre_ml, job.own_o, job.own_ml, job.shares, 0, 0,
+                      job.item_rows, spi, kPrefixKeys, a.num_seqs, num_groups, a.num_heads, a.num_kv_heads};
+    return a.head_dim == 64 ? launch_merge<__nv_bfloat16, 64>(mg, stream) : launch_merge<__nv_bfloat16, 128>(mg, stream);
 }
 
 }  // namespace
 
-size_t shared_prefix_workspace(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int head_dim) {
-    return layout(num_seqs, num_groups, num_heads, num_kv_heads, head_dim).total;
+size_t shared_prefix_workspace(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int head_dim, int max_blocks,
+                               int block_size) {
+    const size_t cc = layout(num_seqs, num_groups, num_heads, num_kv_heads, head_dim).total;
+    const size_t tc = tc_layout(num_seqs, num_groups, num_heads, num_kv_heads, head_dim, max_blocks, block_size).total;
+    return cc > tc ? cc : tc;
 }
 
 cudaError_t launch_shared_prefix(const AttnArgs &a, const int32_t *group_starts, const int32_t *prefix_lens, int num_groups,
                                  void *workspace, cudaStream_t stream) {
+    if (tc_supported(a, num_groups)) return launch_tc(a, group_starts, prefix_lens, num_groups, workspace, stream);
     const Layout w = layout(a.num_seqs, num_groups, a.num_heads, a.num_kv_heads, a.head_dim);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const int G = a.num_heads / a.num_kv_heads, spi = kRows / G;
     const SharedPlan plan = {reinterpret_cast<int32_t *>(ws + w.seq_group), reinterpret_cast<int32_t *>(ws + w.own_len),
-                             reinterpret_cast<int32_t *>(ws + w.shared_len), reinterpret_cast<int32_t *>(ws + w.min_ctx),
-                             reinterpret_cast<int32_t *>(ws + w.item_start), reinterpret_cast<int64_t *>(ws + w.tile_start),
-                             reinterpret_cast<int64_t *>(ws + w.own_start)};
+                             reinterpret_cast<int32_t *>(ws + w.shared_len), reinterpret_cast<int64_t *>(ws + w.tile_start)};
+    int64_t *own_start = reinterpret_cast<int64_t *>(ws + w.own_start);
     const SharedGroups groups = {a.context_lens, group_starts, prefix_lens, a.num_seqs, num_groups, a.num_kv_heads,
                                  a.block_size, (int64_t)a.max_blocks * a.block_size, spi, kKeys};
-    cudaError_t e = launch_dependent(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, groups, plan, a.status);
+    cudaError_t e = launch_dependent(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, groups, plan,
+                                     reinterpret_cast<int32_t *>(ws + w.scratch), own_start, a.status);
     if (e != cudaSuccess) return e;
     auto in16 = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
     const int sms = device_sm_count(), grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
-    CcParams cc = {a.q, a.k_cache, a.v_cache, a.block_tables, group_starts, plan};
+    CcParams cc = {a.q, a.k_cache, a.v_cache, a.block_tables, group_starts, plan, own_start};
     cc.pre_o = reinterpret_cast<float *>(ws + w.pre_o);
     cc.pre_ml = reinterpret_cast<float2 *>(ws + w.pre_ml);
     cc.own_o = reinterpret_cast<float *>(ws + w.own_o);
@@ -591,7 +588,7 @@ cudaError_t launch_shared_prefix(const AttnArgs &a, const int32_t *group_starts,
     cc.aligned = in16(a.q) && in16(a.k_cache) && in16(a.v_cache) ? 1 : 0;
     cc.scale_log2 = a.scale * 1.4426950408889634f;
     cc.status = a.status;
-    MergeParams mg = {a.out, group_starts, plan, cc.pre_o, cc.pre_ml, cc.own_o, cc.own_ml, grid, grid, cc.item_rows, spi,
+    MergeParams mg = {a.out, group_starts, plan, own_start, cc.pre_o, cc.pre_ml, cc.own_o, cc.own_ml, nullptr, grid, grid, cc.item_rows, spi,
                       kKeys, a.num_seqs, num_groups, a.num_heads, a.num_kv_heads};
     if (a.dtype == PA_DTYPE_F32)
         return a.head_dim == 64 ? launch_typed<float, 64>(cc, mg, grid, stream)

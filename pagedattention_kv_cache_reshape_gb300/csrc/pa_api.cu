@@ -468,12 +468,11 @@ pa_status pa_decode_q4(void *out, const void *q, const void *k_cache, const void
 
 size_t pa_decode_shared_prefix_workspace_size(int num_seqs, int num_groups, int num_heads, int num_kv_heads,
                                               int head_dim, int block_size, int max_blocks) {
-    (void)block_size;
-    (void)max_blocks;
     if (num_kv_heads < 1) num_kv_heads = 1;
     if (num_heads < num_kv_heads) num_heads = num_kv_heads;
     return shared_prefix_workspace(num_seqs < 0 ? 0 : num_seqs, num_groups < 1 ? 1 : num_groups, num_heads,
-                                   num_kv_heads, head_dim < 1 ? 1 : head_dim);
+                                   num_kv_heads, head_dim < 1 ? 1 : head_dim, max_blocks < 1 ? 1 : max_blocks,
+                                   block_size < 1 ? 1 : block_size);
 }
 
 pa_status pa_decode_shared_prefix(void *out, const void *q, const void *k_cache, const void *v_cache,

@@ -12,6 +12,7 @@
 
 #include "pa.h"
 #include "prefill_plan.cuh"
+#include "shared_plan.cuh"
 
 namespace pa {
 
@@ -111,6 +112,21 @@ struct KvWriteArgs {
     int64_t *slot_mapping;
 };
 
+// A batch in groups with shared prefixes: the decode kernel computes the
+// sequences' own parts, the prefix kernel the shared ones.
+constexpr int kPrefixKeys = 128;        // keys per tile of the prefix kernel
+constexpr int kMaxPrefixCtas = 160;     // rows reserved for shares' first pieces
+struct SharedJob {
+    SharedGroups groups;
+    SharedPlan plan;
+    int32_t *shares;      // CTAs of the prefix kernel that take a share, set by the plan
+    float *pre_o;         // pieces of the prefix items (shared_plan.cuh)
+    float2 *pre_ml;
+    int item_rows;
+    float *own_o;         // (m, l, o) of the own parts, [num_seqs * num_heads]
+    float2 *own_ml;
+};
+
 // With a.cu_seqlens_q set, only sequences with q_len == 1 are processed and
 // their query/output row is cu_seqlens_q[s].  With `write`, the step's cache
 // write runs in the plan kernel, before any cache read of the decode kernel.
@@ -118,11 +134,20 @@ struct KvWriteArgs {
 // plan launch builds the prefill kernel's work list, the decode kernel keeps
 // only the SMs its share of the work needs, and `between` launches the
 // prefill kernel right behind the decode kernel, so it runs on the SMs the
-// decode kernel leaves.
+// decode kernel leaves.  With `shared` (no cu_seqlens_q) only what lies behind
+// the groups' shared tokens is computed, and for sequences that share some it
+// stays (m, l, o); `between` then launches the prefix kernel.
 cudaError_t launch_split_decode(const AttnArgs &a, void *workspace, size_t workspace_bytes,
                                 cudaStream_t stream, bool timed, const KvWriteArgs *write = nullptr,
                                 const PrefillPlanJob *prefill = nullptr,
-                                const std::function<cudaError_t()> *between = nullptr);
+                                const std::function<cudaError_t()> *between = nullptr,
+                                const SharedJob *shared = nullptr);
+
+// The tcgen05 kernel of the shared parts, behind the decode kernel of the same
+// batch (launch_split_decode with the same job, whose plan launch plans both).
+int prefix_seqs_per_item(int group);
+inline int prefix_grid() { return device_sm_count() < kMaxPrefixCtas ? device_sm_count() : kMaxPrefixCtas; }
+cudaError_t launch_prefix(const AttnArgs &a, const SharedJob &job, cudaStream_t stream);
 
 // tcgen05 causal prefill for sequences with q_len >= 2 (bf16, head_dim 64/128,
 // q-heads per kv-head a power of two up to 16).
@@ -193,7 +218,8 @@ size_t decode_q4_workspace(int num_seqs, int num_heads, int num_kv_heads, int he
 cudaError_t launch_decode_q4(const AttnArgs &a, void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 // Decode of a batch in groups whose sequences share prefixes (a.cu_seqlens_q is not used).
-size_t shared_prefix_workspace(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int head_dim);
+size_t shared_prefix_workspace(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int head_dim, int max_blocks,
+                               int block_size);
 cudaError_t launch_shared_prefix(const AttnArgs &a, const int32_t *group_starts, const int32_t *prefix_lens, int num_groups,
                                  void *workspace, cudaStream_t stream);
 

@@ -7,8 +7,13 @@
 // smallest context - 1), so every sequence keeps at least one token of its
 // own, and 0 where sharing does not pay.  A prefix item is (g, kv-head,
 // `seqs_per_item` neighbouring sequences); its tiles are `keys_per_tile` keys
-// of the prefix.  Items are listed by group, kv-head, sequences.  The own
-// stream lists, by sequence and kv-head, the tiles behind C_g.
+// of the prefix.  Items are listed by group, kv-head, sequences.
+//
+// Pieces: a share's tiles of one item.  The piece that begins with the item's
+// first tile is kept in the item's own rows, ordered (group, kv-head, sequence,
+// q-head of the kv-head), num_seqs * num_heads rows in all; any other piece is
+// the first of its share c and is kept in rows num_seqs * num_heads + c *
+// item_rows and on.
 #pragma once
 
 #include <limits.h>
@@ -36,10 +41,7 @@ struct SharedPlan {
     int32_t *seq_group;    // [num_seqs]
     int32_t *own_len;      // [num_seqs]: tokens behind the shared ones; 0: context length out of range
     int32_t *shared_len;   // [num_groups]: C_g
-    int32_t *min_ctx;      // [num_groups], scratch
-    int32_t *item_start;   // [num_groups + 1]
     int64_t *tile_start;   // [num_groups + 1]: tiles of all items of the groups before
-    int64_t *own_start;    // [num_seqs + 1]: own tiles (of one kv-head) of the sequences before
 };
 
 // The c-th of p equal shares of n tiles begins here; share that holds tile t.
@@ -55,6 +57,126 @@ __device__ __forceinline__ int last_at_most(const V *a, int n, X v) {
         if (a[mid] <= v) lo = mid; else hi = mid;
     }
     return lo;
+}
+
+// The prefix item at tile t of the stream (t < the stream's end).
+struct PrefixItem {
+    int g, C, kt;          // group, its shared tokens and their tiles
+    int s0, n;             // the group's first sequence, its sequences
+    int kvh, part;         // kv-head; the item's place among the group's sequences
+    int tile;              // t's tile of the item
+};
+__device__ __forceinline__ PrefixItem prefix_item(const SharedPlan &plan, const int32_t *starts, int num_groups,
+                                                  int seqs_per_item, int keys_per_tile, int64_t t) {
+    PrefixItem it;
+    it.g = last_at_most(plan.tile_start, num_groups, t);   // (groups without tiles are passed over)
+    it.C = plan.shared_len[it.g];
+    it.kt = (it.C + keys_per_tile - 1) / keys_per_tile;
+    it.s0 = __ldg(starts + it.g);
+    it.n = __ldg(starts + it.g + 1) - it.s0;
+    const int64_t local = t - plan.tile_start[it.g];
+    const int item = (int)(local / it.kt), per_head = (it.n + seqs_per_item - 1) / seqs_per_item;
+    it.tile = (int)(local - (int64_t)item * it.kt);
+    it.kvh = item / per_head;
+    it.part = item - it.kvh * per_head;
+    return it;
+}
+
+// Row of sequence s0 + i, q-head 0 of kv-head kvh, among the items' own rows.
+__device__ __forceinline__ int64_t item_row(int s0, int n, int kvh, int i, int num_heads, int group) {
+    return (int64_t)s0 * num_heads + ((int64_t)kvh * n + i) * group;
+}
+
+// Exclusive scan of v over a CTA of kThreads threads; `total` the sum.
+template <int kThreads>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *warp_tot, int64_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+    }
+    __syncthreads();   // the previous scan's totals have been read
+    if (lane == 31) warp_tot[warp] = incl;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        const int64_t t = warp_tot[w];
+        if (w < warp) before += t;
+        total += t;
+    }
+    return before + incl - v;
+}
+
+// C_g of every group into lens[num_groups], by a whole CTA of kThreads threads;
+// `starts` receives a copy of the groups' starts when it is not the input
+// itself.  Both may be shared or global memory.  False, and every C 0: the
+// starts do not run from 0 to num_seqs in order.  `status` (nullable) receives
+// what is out of range.
+template <int kThreads>
+__device__ bool shared_lens(const SharedGroups &g, int32_t *starts, int32_t *lens, int32_t *status) {
+    const int tid = threadIdx.x, S = g.num_seqs, NG = g.num_groups;
+    int wrong = 0;
+    for (int i = tid; i < NG; i += kThreads) {
+        const int a = __ldg(g.starts + i), b = __ldg(g.starts + i + 1);
+        wrong |= a < 0 || b < a || b > S || (i == 0 && a != 0) || (i == NG - 1 && b != S);
+        if (starts) starts[i] = a;
+        lens[i] = INT_MAX;
+    }
+    const bool ok = !__syncthreads_or(wrong);
+    if (!ok && tid == 0) set_status(status, PA_ERR_OUT_OF_RANGE);
+    const int32_t *from = starts ? starts : g.starts;
+    for (int s = tid; s < S; s += kThreads) {   // the smallest context of each group
+        const int ctx = __ldg(g.context_lens + s);
+        if (ctx <= 0 || ctx > g.max_tokens) set_status(status, PA_ERR_OUT_OF_RANGE);
+        else if (ok) atomicMin(lens + last_at_most(from, NG, s), ctx);
+    }
+    __syncthreads();
+    for (int i = tid; i < NG; i += kThreads) {
+        const int n = __ldg(g.starts + i + 1) - __ldg(g.starts + i), P = __ldg(g.prefix_lens + i);
+        const int least = *const_cast<volatile int32_t *>(lens + i);   // (global atomics: not through L1)
+        int C = 0;
+        if (P < 0 || P > g.max_tokens) set_status(status, PA_ERR_OUT_OF_RANGE);
+        else if (ok && n >= 2 && least != INT_MAX) C = min(P, least - 1) / g.block_size * g.block_size;
+        lens[i] = C;
+    }
+    __syncthreads();
+    return ok;
+}
+
+// The plan's arrays from C_g, by a whole CTA.  Returns the tiles of all items.
+template <int kThreads>
+__device__ int64_t shared_write_plan(const SharedGroups &g, const SharedPlan &plan, bool ok, const int32_t *starts,
+                                     const int32_t *lens, int64_t *warp_tot) {
+    const int tid = threadIdx.x;
+    int64_t tiles = 0;
+    for (int base = 0; base < g.num_groups; base += kThreads) {
+        const int i = base + tid;
+        int64_t mine = 0;
+        if (i < g.num_groups) {
+            const int C = lens[i];
+            if (C > 0) {
+                const int n = __ldg(g.starts + i + 1) - __ldg(g.starts + i);
+                mine = (int64_t)g.num_kv_heads * ((n + g.seqs_per_item - 1) / g.seqs_per_item) *
+                       ((C + g.keys_per_tile - 1) / g.keys_per_tile);
+            }
+            plan.shared_len[i] = C;
+        }
+        int64_t total;
+        const int64_t first = block_scan<kThreads>(mine, warp_tot, total) + tiles;
+        tiles += total;
+        if (i < g.num_groups) plan.tile_start[i] = first;
+    }
+    if (tid == 0) plan.tile_start[g.num_groups] = tiles;
+    for (int s = tid; s < g.num_seqs; s += kThreads) {
+        const int ctx = __ldg(g.context_lens + s);
+        const int grp = ok ? last_at_most(starts, g.num_groups, s) : 0;
+        plan.seq_group[s] = grp;
+        plan.own_len[s] = ctx > 0 && ctx <= g.max_tokens ? ctx - lens[grp] : 0;
+    }
+    return tiles;
 }
 
 }  // namespace pa
