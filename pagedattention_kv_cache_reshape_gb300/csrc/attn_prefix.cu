@@ -16,8 +16,7 @@
 // HBM 1.5 us; the products of one M-tile of 128 rows take 0.5 us of the tensor
 // pipe, of two 1 us.  So groups of up to 256 rows a kv-head are bound by HBM,
 // larger ones (several items read the same tiles) by the tensor pipe and the
-// softmax beside it.  Items of one M-tile leave the second softmax warpgroup
-// idle.
+// softmax beside it.
 //
 // Roles (512 threads): warps 0-7 two softmax warpgroups (thread = row = TMEM
 // lane of its M-tile), warp 8 TMA producer, warp 9 TMEM owner and MMA issuer,
@@ -92,9 +91,13 @@ template <int D> struct Shape {
 };
 
 // A piece: tiles tile0 .. tile0 + nkv - 1 of an item.  `live` = 0 marks the end.
+// With more than `pos` sequences (wide) M-tile t holds the t-th `pos` of them
+// and takes every KV tile; with fewer, both M-tiles hold the same rows, t takes
+// KV tiles t, t + 2, ..., and the output warpgroup joins them.
 struct Piece {
-    int table_seq, kvh, seq0, nseq, mt, tile0, nkv, C, live, pad;
+    int table_seq, kvh, seq0, nseq, wide, tile0, nkv, C, live, pad;
     int64_t row;      // row of (sequence seq0, q-head 0) in o and ml
+    __device__ __forceinline__ int tiles(int t) const { return wide ? nkv : (nkv + 1 - t) >> 1; }
 };
 constexpr int kItemSlots = 4;                 // pieces published ahead of their use
 
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // leave their SMs (but not before the decode grid is done: what waits for
     // this grid relies on both).
     const int64_t T = p.plan.tile_start[p.num_groups];   // plain loads: written by the plan grid
-    const int64_t P = p.shares[0], cta = blockIdx.x;
+    const int64_t P = min((int64_t)p.shares[0], T), cta = blockIdx.x;   // no share is empty
     const int64_t t_begin = cta < P ? share_begin(cta, T, P) : 0, t_end = cta < P ? share_begin(cta + 1, T, P) : 0;
     grid_dependents_launch();    // every decode and prefix CTA runs before the merge's take up room
     if (t_begin >= t_end) {
@@ -225,9 +228,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             Piece I;
             if (!take_item(it, I)) { ok = false; break; }
             if (!I.live) break;
+            if (!I.wide && I.nkv > 1) {
+                // both M-tiles hold this row: joined on the way out
+#pragma unroll
+                for (int t = 0; t < kMT; ++t)
+                    ok = ok && mbar_wait_warp(o_full + t, (uint32_t)(no[t] & 1), p.wait_ns) &&
+                         mbar_wait_warp(l_full + t, (uint32_t)(no[t] & 1), p.wait_ns);
+                if (!ok) break;
+                tc_fence_after();
+                const float2 a = ml_s[r], b = ml_s[BM + r];
+                const float M = fmaxf(a.x, b.x), fa = fast_exp2(a.x - M), fb = fast_exp2(b.x - M);
+                const bool row_valid = head < p.group && i_pos < I.nseq;
+                const int64_t row = I.row + (row_valid ? (int64_t)i_pos * p.group + head : 0);
+                float *dst = p.o + row * D;
+                if (row_valid) p.ml[row] = make_float2(M, a.y * fa + b.y * fb);
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t o0[16], o1[16];
+                    tmem_ld16(lane_addr + o_col(0) + 16 * c, o0);
+                    tmem_ld16(lane_addr + o_col(1) + 16 * c, o1);
+                    tmem_wait_ld();
+                    if (c == D / 16 - 1) {
+                        tc_fence_before();
+                        mbar_arrive(o_empty);
+                        mbar_arrive(o_empty + 1);
+                    }
+                    if (row_valid) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t x[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                x[e] = __float_as_uint(__uint_as_float(o0[8 * h + e]) * fa + __uint_as_float(o1[8 * h + e]) * fb);
+                            st_global_v8(dst + 16 * c + 8 * h, x);
+                        }
+                    }
+                }
+                ++no[0];
+                ++no[1];
+                continue;
+            }
 #pragma unroll
             for (int t = 0; t < kMT; ++t) {
-                if (t >= I.mt || !ok) continue;
+                if ((t > 0 && !I.wide) || !ok) continue;
                 if (!mbar_wait_warp(o_full + t, (uint32_t)(no[t] & 1), p.wait_ns) ||
                     !mbar_wait_warp(l_full + t, (uint32_t)(no[t] & 1), p.wait_ns)) {
                     ok = false;
@@ -294,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 I.kvh = x.kvh;
                 I.seq0 = x.s0 + i0;
                 I.nseq = min(spi, x.n - i0);
-                I.mt = I.nseq > p.pos ? 2 : 1;
+                I.wide = I.nseq > p.pos;
                 I.tile0 = x.tile;
                 I.nkv = (int)min((int64_t)(x.kt - x.tile), t_end - t_next);
                 I.C = x.C;
@@ -333,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 if (nq >= 1 && !mbar_wait(q_empty, (uint32_t)((nq - 1) & 1), p.wait_ns)) ok = false;
                 if (ok) {
-                    mbar_arrive_expect_tx(q_full, (uint32_t)(I.mt * kDH * p.pos * p.group * 128));
-                    for (int t = 0; t < I.mt; ++t)
+                    mbar_arrive_expect_tx(q_full, (uint32_t)((I.wide ? kMT : 1) * kDH * p.pos * p.group * 128));
+                    for (int t = 0; t < (I.wide ? kMT : 1); ++t)
                         for (int pl = 0; pl < kDH; ++pl)
                             tma_load_4d(q_s + t * kQBytes + pl * kPlaneQ, &tmap_q, 0, I.seq0 + t * p.pos, I.kvh * p.group,
                                         pl, q_full);
@@ -398,11 +441,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dq = umma_desc_sw128(q_addr, 16, 1024);
         const uint64_t dk = umma_desc_sw128(kv_addr, 16, kKSbo);
         const uint64_t dv = umma_desc_sw128(kv_addr, kVLbo, kVSbo);
-        auto issue_qk = [&](int t, int nk) {      // S_t = Q_t K^T, K in ring entry nk
+        // S_t = Q_tq K^T, K in ring entry nk
+        auto issue_qk = [&](int t, int tq, int nk) {
             const uint32_t ko = (uint32_t)slot_of(nk) * kSlotBytes;
 #pragma unroll
             for (int pl = 0; pl < D / 64; ++pl)
-                umma_bf16_k64(tmem + s_col(t), dq + ((uint32_t)(t * kQBytes + pl * kPlaneQ) >> 4),
+                umma_bf16_k64(tmem + s_col(t), dq + ((uint32_t)(tq * kQBytes + pl * kPlaneQ) >> 4),
                               dk + ((ko + pl * kKPlane) >> 4), kIdescQK, pl > 0 ? 1u : 0u);
         };
         // O_t (+)= P_t V over keys 64 kq .. 64 kq + 63 (4 MMAs of 16), V in ring entry nv
@@ -413,12 +457,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         bool ok = true, stopped = false;
         int n = 0, nq = 0;
-        int J[kMT] = {}, no[kMT] = {};   // per M-tile: tiles and pieces so far
+        int J0 = 0, J1 = 0, no0 = 0, no1 = 0;   // per M-tile: tiles and pieces so far
         for (int it = 0; ok; ++it) {
             Piece I;
             if (!take_item(it, I)) { ok = false; break; }
             if (!I.live) break;
-            const int nkv = __shfl_sync(kAll, I.nkv, 0), mt = __shfl_sync(kAll, I.mt, 0);
+            const int nkv = __shfl_sync(kAll, I.nkv, 0);
+            const bool wide = __shfl_sync(kAll, I.wide, 0) != 0;
             if (p.stall == PA_STALL_CONSUMER && n >= p.stall_after) { stopped = true; ok = false; break; }
             if (!mbar_wait_warp(q_full, (uint32_t)(nq & 1), p.wait_ns) ||
                 !mbar_wait_warp(kv_full + slot_of(n), phase_of(n), p.wait_ns)) {
@@ -426,58 +471,88 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
-#pragma unroll
-            for (int t = 0; t < kMT; ++t)
-                if (t < mt) {
-                    issue_qk(t, n);
-                    umma_commit(s_full + t);
-                }
-            if (nkv == 1) umma_commit(q_empty);
-            umma_commit(kv_empty + slot_of(n));
-            for (int j = 0; j < nkv; ++j) {
-                const bool next = j + 1 < nkv;
-                const int nv = n + 2 * j + 1, nk = n + 2 * j + 2;
-                // test hook: stop, leaving ring entries unreleased, so the producer's wait runs out
-                if (p.stall == PA_STALL_CONSUMER && nv >= p.stall_after) { stopped = true; ok = false; break; }
-                if (!mbar_wait_warp(kv_full + slot_of(nv), phase_of(nv), p.wait_ns)) { ok = false; break; }
+            // O_t's half products with V in ring entry nv, as P_t comes; x: M-tile t's tiles so far in this piece
+            auto pv = [&](int t, int nv, int x) -> bool {
+                // the piece's first product into O_t overwrites it: the output warpgroup has read the last piece's
+                const int no = t ? no1 : no0;
+                const uint32_t ph = (uint32_t)(((t ? J1 : J0) + x) & 1);
+                if (x == 0 && no > 0 && !mbar_wait_warp(o_empty + t, (uint32_t)((no - 1) & 1), p.wait_ns)) return false;
+                if (!mbar_wait_warp(p_half + t, ph, p.wait_ns)) return false;
+                tc_fence_after();
+                issue_pv(t, nv, 0, x == 0);
+                if (!mbar_wait_warp(p_full + t, ph, p.wait_ns)) return false;
+                tc_fence_after();
+                issue_pv(t, nv, 1, x == 0);
+                return true;
+            };
+            if (wide) {
 #pragma unroll
                 for (int t = 0; t < kMT; ++t) {
-                    if (t >= mt || !ok) continue;
-                    // the piece's first product into O_t overwrites it: the output warpgroup has read the last piece's
-                    if (j == 0 && no[t] > 0 && !mbar_wait_warp(o_empty + t, (uint32_t)((no[t] - 1) & 1), p.wait_ns)) {
-                        ok = false;
-                        continue;
+                    issue_qk(t, t, n);
+                    umma_commit(s_full + t);
+                }
+                if (nkv == 1) umma_commit(q_empty);
+                umma_commit(kv_empty + slot_of(n));
+                for (int j = 0; j < nkv; ++j) {
+                    const bool next = j + 1 < nkv;
+                    const int nv = n + 2 * j + 1, nk = n + 2 * j + 2;
+                    // test hook: stop, leaving ring entries unreleased, so the producer's wait runs out
+                    if (p.stall == PA_STALL_CONSUMER && nv >= p.stall_after) { stopped = true; ok = false; break; }
+                    if (!mbar_wait_warp(kv_full + slot_of(nv), phase_of(nv), p.wait_ns)) { ok = false; break; }
+#pragma unroll
+                    for (int t = 0; t < kMT; ++t) {
+                        if (!ok || !pv(t, nv, j)) { ok = false; continue; }
+                        if (next) {
+                            if (t == 0 && !mbar_wait_warp(kv_full + slot_of(nk), phase_of(nk), p.wait_ns)) { ok = false; continue; }
+                            tc_fence_after();
+                            issue_qk(t, t, nk);
+                            umma_commit(s_full + t);
+                        } else {
+                            umma_commit(o_full + t);
+                        }
                     }
-                    if (!mbar_wait_warp(p_half + t, (uint32_t)((J[t] + j) & 1), p.wait_ns)) { ok = false; continue; }
-                    tc_fence_after();
-                    issue_pv(t, nv, 0, j == 0);
-                    if (!mbar_wait_warp(p_full + t, (uint32_t)((J[t] + j) & 1), p.wait_ns)) { ok = false; continue; }
-                    tc_fence_after();
-                    issue_pv(t, nv, 1, j == 0);
+                    if (!ok) break;
+                    umma_commit(kv_empty + slot_of(nv));
                     if (next) {
-                        if (t == 0 && !mbar_wait_warp(kv_full + slot_of(nk), phase_of(nk), p.wait_ns)) { ok = false; continue; }
+                        umma_commit(kv_empty + slot_of(nk));
+                        if (j + 2 == nkv) umma_commit(q_empty);    // the piece's last QK products
+                    }
+                }
+            } else {
+                // M-tile t takes KV tiles t, t + 2, ...: PV_t(x) QK_t(x + 2), t = x & 1
+                for (int x = 0; x < 2 && x < nkv; ++x) {
+                    const int nk = n + 2 * x;
+                    if (x > 0 && p.stall == PA_STALL_CONSUMER && nk >= p.stall_after) { stopped = true; ok = false; break; }
+                    if (x > 0 && !mbar_wait_warp(kv_full + slot_of(nk), phase_of(nk), p.wait_ns)) { ok = false; break; }
+                    tc_fence_after();
+                    issue_qk(x, 0, nk);
+                    umma_commit(s_full + x);
+                    umma_commit(kv_empty + slot_of(nk));
+                }
+                if (ok && nkv <= 2) umma_commit(q_empty);
+                for (int x = 0; ok && x < nkv; ++x) {
+                    const int t = x & 1, nv = n + 2 * x + 1, nk = n + 2 * x + 4;
+                    if (p.stall == PA_STALL_CONSUMER && nv >= p.stall_after) { stopped = true; ok = false; break; }
+                    if (!mbar_wait_warp(kv_full + slot_of(nv), phase_of(nv), p.wait_ns) || !pv(t, nv, x >> 1)) { ok = false; break; }
+                    umma_commit(kv_empty + slot_of(nv));
+                    if (x + 2 < nkv) {
+                        if (!mbar_wait_warp(kv_full + slot_of(nk), phase_of(nk), p.wait_ns)) { ok = false; break; }
                         tc_fence_after();
-                        issue_qk(t, nk);
+                        issue_qk(t, 0, nk);
                         umma_commit(s_full + t);
+                        umma_commit(kv_empty + slot_of(nk));
+                        if (x + 3 == nkv) umma_commit(q_empty);
                     } else {
                         umma_commit(o_full + t);
                     }
                 }
-                if (!ok) break;
-                umma_commit(kv_empty + slot_of(nv));
-                if (next) {
-                    umma_commit(kv_empty + slot_of(nk));
-                    if (j + 2 == nkv) umma_commit(q_empty);    // the piece's last QK products
-                }
             }
             n += 2 * nkv;
             ++nq;
-#pragma unroll
-            for (int t = 0; t < kMT; ++t)
-                if (t < mt) {
-                    J[t] += nkv;
-                    ++no[t];
-                }
+            J0 += wide ? nkv : (nkv + 1) >> 1;
+            J1 += wide ? nkv : nkv >> 1;
+            ++no0;
+            no1 += wide || nkv > 1 ? 1 : 0;
         }
         if (!ok && !stopped && lane == 0) {
             set_status(p.status, PA_ERR_TIMEOUT);
@@ -501,12 +576,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             Piece I;
             if (!take_item(it, I)) { ok = false; break; }
             if (!I.live) break;
-            if (t >= I.mt) continue;
+            const int mine = I.tiles(t);
+            if (mine == 0) continue;
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < I.nkv; ++j) {
+            for (int j = 0; j < mine; ++j) {
                 if (!mbar_wait_warp(s_full + t, (uint32_t)((J + j) & 1), p.wait_ns)) { ok = false; break; }
                 tc_fence_after();
-                const int lim = I.C - (I.tile0 + j) * BN;     // shared keys from the tile's first on
+                const int lim = I.C - (I.tile0 + (I.wide ? j : 2 * j + t)) * BN;     // shared keys from the tile's first on
                 // S is read whole and its max taken first, so P can go out in two halves of 64 keys (the tensor pipe
                 // takes the first while the second is computed).  The piece's first tile takes its own max; later ones
                 // run with the running max m: P stays <= 2^8 unless the tile's max exceeds it by more than 8, and
@@ -595,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (no > 0 && !mbar_wait_warp(o_empty + t, (uint32_t)((no - 1) & 1), p.wait_ns)) { ok = false; break; }
             ml_s[t * BM + r] = make_float2(m, l);
             mbar_arrive(l_full + t);
-            J += I.nkv;
+            J += mine;
             ++no;
         }
         if (!ok && r == 0) {

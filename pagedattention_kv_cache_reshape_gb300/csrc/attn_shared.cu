@@ -13,7 +13,7 @@
 // shared_plan_kernel   C_c, and the two streams of key tiles
 // shared_cc_kernel     CUDA-core products, any dtype (fp32 in and out of them):
 //                      each persistent CTA takes an equal share of both streams
-// shared_merge_kernel  a warp a row: the row's pieces in stream order
+// shared_merge_kernel  one warp or four a row: the row's pieces in a fixed order
 #include <math.h>
 
 #include "pa_device.cuh"
@@ -280,11 +280,11 @@ __global__ void __launch_bounds__(kCcThreads, 2) shared_cc_kernel(const CcParams
     grid_dependency_wait();
     grid_dependents_launch();
     const int G = p.num_heads / p.num_kv_heads;
-    const int64_t P = gridDim.x, c = blockIdx.x;
+    const int64_t c = blockIdx.x;
     // the groups' shared tokens
-    const int64_t T0 = p.plan.tile_start[p.num_groups];
-    int64_t t = share_begin(c, T0, P);
-    const int64_t t_end = share_begin(c + 1, T0, P);
+    const int64_t T0 = p.plan.tile_start[p.num_groups], P0 = min((int64_t)gridDim.x, T0);   // no share is empty
+    int64_t t = c < P0 ? share_begin(c, T0, P0) : 0;
+    const int64_t t_end = c < P0 ? share_begin(c + 1, T0, P0) : 0;
     const int64_t rows0 = (int64_t)p.num_seqs * p.num_heads;
     while (t < t_end) {
         const PrefixItem it = prefix_item(p.plan, p.group_starts, p.num_groups, p.seqs_per_item, kKeys, t);
@@ -304,8 +304,9 @@ __global__ void __launch_bounds__(kCcThreads, 2) shared_cc_kernel(const CcParams
     }
     // the sequences' own: by sequence, then kv-head
     const int64_t T1 = p.own_start[p.num_seqs] * p.num_kv_heads;
-    t = share_begin(c, T1, P);
-    const int64_t t_last = share_begin(c + 1, T1, P);
+    const int64_t P1 = min((int64_t)gridDim.x, T1);
+    t = c < P1 ? share_begin(c, T1, P1) : 0;
+    const int64_t t_last = c < P1 ? share_begin(c + 1, T1, P1) : 0;
     while (t < t_last) {
         const int s = last_at_most(p.own_start, p.num_seqs, t / p.num_kv_heads);
         const int len = p.plan.own_len[s], kt = (len + kKeys - 1) / kKeys;
@@ -348,9 +349,11 @@ struct MergeParams {
     int num_groups;
     int num_heads;
     int num_kv_heads;
+    int out_aligned;    // rows of out on 4 bytes
 };
 
 constexpr int kMergeThreads = 128;
+constexpr int64_t kFewRows = 5000;
 
 // The running (M, L, acc) of one row; lane: D / 32 consecutive dims.
 template <int D> struct RowSum {
@@ -376,69 +379,109 @@ __device__ __forceinline__ void load_dims(const float *src, float (&v)[D / 32]) 
     }
 }
 
-// Pieces of one item, tiles [t0, t0 + n) of a stream of T tiles cut into P shares, in order: the first in row `row0`,
-// that of share c in row extra + c * rows.  Four pieces' loads are in flight at a time.
-template <int D>
-__device__ __forceinline__ void merge_stream(RowSum<D> &sum, const float *o, const float2 *ml, int64_t row0, int64_t extra,
-                                             int rows, int64_t t0, int64_t n, int64_t T, int64_t P) {
-    constexpr int kBatch = 4;
+// Where one row's pieces of a stream lie: the first in row `first`, the others in rows other, other + step, ...
+struct RowPieces {
+    int64_t first = 0, other = 0, step = 0;
+    int n = 0;
+    // tiles [t0, t0 + n) of a stream of T tiles in at most P shares; share c's rows begin at extra + c * rows
+    __device__ __forceinline__ RowPieces(int64_t row0, int64_t extra, int rows, int64_t t0, int64_t count, int64_t T, int64_t P) {
+        P = min(P, T);
+        const int64_t c0 = share_of(t0, T, P), c1 = share_of(t0 + count - 1, T, P);
+        first = row0;
+        other = extra + (c0 + 1) * rows;
+        step = rows;
+        n = (int)(c1 - c0 + 1);
+    }
+    __device__ __forceinline__ RowPieces() {}
+    __device__ __forceinline__ int64_t at(int i) const { return i == 0 ? first : other + (i - 1) * step; }
+};
+
+// Pieces w, w + W, ... of a row, in order; the loads of kBatch of them in flight at a time.
+template <int D, int W>
+__device__ __forceinline__ void add_pieces(RowSum<D> &sum, const float *o, const float2 *ml, const RowPieces &x, int w) {
+    constexpr int kBatch = 8;
     const int lane = threadIdx.x & 31;
-    const int64_t c0 = share_of(t0, T, P), c1 = share_of(t0 + n - 1, T, P);
-    for (int64_t cb = c0; cb <= c1; cb += kBatch) {
-        float2 x[kBatch];
+    for (int i = w; i < x.n; i += W * kBatch) {
+        float2 a[kBatch];
         float v[kBatch][D / 32];
-        bool use[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int64_t c = cb + k;
-            use[k] = c <= c1 && share_begin(c, T, P) < share_begin(c + 1, T, P);   // an empty share holds no piece
-            const int64_t at = use[k] && c > c0 ? extra + c * rows : row0;
-            x[k] = __ldcg(ml + at);
-            load_dims<D>(o + at * D + lane * (D / 32), v[k]);
-        }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
-            if (use[k]) sum.add(x[k], v[k]);
+            if (i + W * k < x.n) {
+                const int64_t at = x.at(i + W * k);
+                a[k] = __ldcg(ml + at);
+                load_dims<D>(o + at * D + lane * (D / 32), v[k]);
+            }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (i + W * k < x.n) sum.add(a[k], v[k]);
     }
 }
 
-template <typename T, int D>
+// W warps a row.  What a row's pieces are is found before the wait for the kernel in front: the plan was complete
+// before that kernel began.
+template <typename T, int D, int W>
 __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const MergeParams p) {
-    grid_dependency_wait();
-    grid_dependents_launch();
-    const int lane = threadIdx.x & 31;
-    const int64_t r = (int64_t)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
-    if (r >= (int64_t)p.num_seqs * p.num_heads) return;
-    const int s = (int)(r / p.num_heads), h = (int)(r - (int64_t)s * p.num_heads);
-    const int len = p.plan.own_len[s];
-    if (len <= 0) return;   // context length out of range: the row stays as it was
+    constexpr int kPer = D / 32, kRowsPerCta = kMergeThreads / 32 / W;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % W;
+    const int64_t r = (int64_t)blockIdx.x * kRowsPerCta + warp / W;
+    const bool in = r < (int64_t)p.num_seqs * p.num_heads;
+    const int s = in ? (int)(r / p.num_heads) : 0, h = in ? (int)(r - (int64_t)s * p.num_heads) : 0;
+    const int len = in ? p.plan.own_len[s] : 0;
+    const int g = in ? p.plan.seq_group[s] : 0, C = p.plan.shared_len[g];
+    // a context length out of range leaves its row as it was; without shared tokens the decode kernel wrote it
+    const bool mine = len > 0 && (p.own_start || C > 0);
     const int G = p.num_heads / p.num_kv_heads, kvh = h / G, hh = h - kvh * G;
-    const int g = p.plan.seq_group[s], C = p.plan.shared_len[g];
-    if (!p.own_start && C == 0) return;   // the decode kernel wrote the row
     const int64_t rows0 = (int64_t)p.num_seqs * p.num_heads;
-    RowSum<D> sum;
-    if (C > 0) {
+    RowPieces pre, own;
+    if (mine && C > 0) {
         const int s0 = __ldg(p.group_starts + g), n = __ldg(p.group_starts + g + 1) - s0;
         const int per_head = (n + p.seqs_per_item - 1) / p.seqs_per_item;
         const int part = (s - s0) / p.seqs_per_item, item = kvh * per_head + part;
         const int64_t kt = (C + p.keys_per_tile - 1) / p.keys_per_tile;
-        merge_stream<D>(sum, p.pre_o, p.pre_ml, item_row(s0, n, kvh, s - s0, p.num_heads, G) + hh,
-                        rows0 + (s - s0 - part * p.seqs_per_item) * G + hh, p.item_rows, p.plan.tile_start[g] + item * kt,
-                        kt, p.plan.tile_start[p.num_groups], p.pre_shares_dev ? *p.pre_shares_dev : p.pre_shares);
+        pre = RowPieces(item_row(s0, n, kvh, s - s0, p.num_heads, G) + hh, rows0 + (s - s0 - part * p.seqs_per_item) * G + hh,
+                        p.item_rows, p.plan.tile_start[g] + item * kt, kt, p.plan.tile_start[p.num_groups],
+                        p.pre_shares_dev ? *p.pre_shares_dev : p.pre_shares);
     }
-    if (p.own_start) {
+    if (mine && p.own_start) {
         const int64_t kt = (len + p.keys_per_tile - 1) / p.keys_per_tile;
-        merge_stream<D>(sum, p.own_o, p.own_ml, r, rows0 + hh, G, p.own_start[s] * p.num_kv_heads + kvh * kt, kt,
+        own = RowPieces(r, rows0 + hh, G, p.own_start[s] * p.num_kv_heads + kvh * kt, kt,
                         p.own_start[p.num_seqs] * p.num_kv_heads, p.own_shares);
-    } else {
-        float v[D / 32];
-        load_dims<D>(p.own_o + r * D + lane * (D / 32), v);
-        sum.add(__ldcg(p.own_ml + r), v);
+    } else if (mine) {
+        own.first = r;
+        own.n = 1;
     }
-    T *dst = static_cast<T *>(p.out) + r * D + lane * (D / 32);
-    const float inv = 1.f / sum.L;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    RowSum<D> sum;
+    add_pieces<D, W>(sum, p.pre_o, p.pre_ml, pre, w);
+    add_pieces<D, W>(sum, p.own_o, p.own_ml, own, (w + W - pre.n % W) % W);   // on from the warp behind the last
+    if (W > 1) {
+        __shared__ float2 ml_s[kRowsPerCta][W];
+        __shared__ float o_s[kRowsPerCta][W][D];
+        if (lane == 0) ml_s[warp / W][w] = make_float2(sum.M, sum.L);
 #pragma unroll
-    for (int u = 0; u < D / 32; ++u) dst[u] = from_float<T>(sum.acc[u] * inv);
+        for (int u = 0; u < kPer; ++u) o_s[warp / W][w][lane * kPer + u] = sum.acc[u];
+        __syncthreads();
+        if (w > 0) return;
+#pragma unroll
+        for (int i = 1; i < W; ++i) {
+            float v[kPer];
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) v[u] = o_s[warp / W][i][lane * kPer + u];
+            sum.add(ml_s[warp / W][i], v);
+        }
+    }
+    if (!mine) return;
+    T *dst = static_cast<T *>(p.out) + r * D + lane * kPer;
+    const float inv = 1.f / sum.L;
+    if (sizeof(T) == 2 && p.out_aligned) {
+#pragma unroll
+        for (int u = 0; u < kPer; u += 2)
+            *reinterpret_cast<uint32_t *>(dst + u) = pack_bf16x2(sum.acc[u] * inv, sum.acc[u + 1] * inv);
+    } else {
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) dst[u] = from_float<T>(sum.acc[u] * inv);
+    }
 }
 
 // ------------------------------------------------------------------ host side
@@ -470,9 +513,14 @@ Layout layout(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int
 
 template <typename T, int D>
 cudaError_t launch_merge(const MergeParams &mg, cudaStream_t stream) {
+    // A row has about P / items pieces and an item at most 256 rows, so with few rows there may be many pieces each:
+    // then four warps share them.
     const int64_t rows = (int64_t)mg.num_seqs * mg.num_heads;
-    return launch_dependent(shared_merge_kernel<T, D>, dim3((unsigned)((rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32))),
-                            dim3(kMergeThreads), 0, stream, mg);
+    constexpr int kWarps = kMergeThreads / 32;
+    if (rows < kFewRows)
+        return launch_dependent(shared_merge_kernel<T, D, kWarps>, dim3((unsigned)rows), dim3(kMergeThreads), 0, stream, mg);
+    return launch_dependent(shared_merge_kernel<T, D, 1>, dim3((unsigned)((rows + kWarps - 1) / kWarps)), dim3(kMergeThreads),
+                            0, stream, mg);
 }
 
 template <typename T, int D>
@@ -542,7 +590,7 @@ cudaError_t launch_tc(const AttnArgs &a, const int32_t *group_starts, const int3
     cudaError_t e = launch_split_decode(a, ws + w.decode, w.total - w.decode, stream, false, nullptr, nullptr, &prefix, &job);
     if (e != cudaSuccess) return e;
     MergeParams mg = {a.out, group_starts, job.plan, nullptr, job.pre_o, job.pre_ml, job.own_o, job.own_ml, job.shares, 0, 0,
-                      job.item_rows, spi, kPrefixKeys, a.num_seqs, num_groups, a.num_heads, a.num_kv_heads};
+                      job.item_rows, spi, kPrefixKeys, a.num_seqs, num_groups, a.num_heads, a.num_kv_heads, 1};
     return a.head_dim == 64 ? launch_merge<__nv_bfloat16, 64>(mg, stream) : launch_merge<__nv_bfloat16, 128>(mg, stream);
 }
 
@@ -589,7 +637,8 @@ cudaError_t launch_shared_prefix(const AttnArgs &a, const int32_t *group_starts,
     cc.scale_log2 = a.scale * 1.4426950408889634f;
     cc.status = a.status;
     MergeParams mg = {a.out, group_starts, plan, own_start, cc.pre_o, cc.pre_ml, cc.own_o, cc.own_ml, nullptr, grid, grid, cc.item_rows, spi,
-                      kKeys, a.num_seqs, num_groups, a.num_heads, a.num_kv_heads};
+                      kKeys, a.num_seqs, num_groups, a.num_heads, a.num_kv_heads,
+                      reinterpret_cast<uintptr_t>(a.out) % 4 == 0};
     if (a.dtype == PA_DTYPE_F32)
         return a.head_dim == 64 ? launch_typed<float, 64>(cc, mg, grid, stream)
                                 : launch_typed<float, 128>(cc, mg, grid, stream);

@@ -118,28 +118,37 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *warp_tot, int6
 template <int kThreads>
 __device__ bool shared_lens(const SharedGroups &g, int32_t *starts, int32_t *lens, int32_t *status) {
     const int tid = threadIdx.x, S = g.num_seqs, NG = g.num_groups;
+    // the first round's loads all at once; later rounds (more groups or sequences than threads) load again
+    int a = 0, b = 0, P = 0, ctx = 0;
+    if (tid < NG) {
+        a = __ldg(g.starts + tid);
+        b = __ldg(g.starts + tid + 1);
+        P = __ldg(g.prefix_lens + tid);
+    }
+    if (tid < S) ctx = __ldg(g.context_lens + tid);
     int wrong = 0;
     for (int i = tid; i < NG; i += kThreads) {
-        const int a = __ldg(g.starts + i), b = __ldg(g.starts + i + 1);
-        wrong |= a < 0 || b < a || b > S || (i == 0 && a != 0) || (i == NG - 1 && b != S);
-        if (starts) starts[i] = a;
+        const int x = i == tid ? a : __ldg(g.starts + i), y = i == tid ? b : __ldg(g.starts + i + 1);
+        wrong |= x < 0 || y < x || y > S || (i == 0 && x != 0) || (i == NG - 1 && y != S);
+        if (starts) starts[i] = x;
         lens[i] = INT_MAX;
     }
     const bool ok = !__syncthreads_or(wrong);
     if (!ok && tid == 0) set_status(status, PA_ERR_OUT_OF_RANGE);
     const int32_t *from = starts ? starts : g.starts;
     for (int s = tid; s < S; s += kThreads) {   // the smallest context of each group
-        const int ctx = __ldg(g.context_lens + s);
-        if (ctx <= 0 || ctx > g.max_tokens) set_status(status, PA_ERR_OUT_OF_RANGE);
-        else if (ok) atomicMin(lens + last_at_most(from, NG, s), ctx);
+        const int c = s == tid ? ctx : __ldg(g.context_lens + s);
+        if (c <= 0 || c > g.max_tokens) set_status(status, PA_ERR_OUT_OF_RANGE);
+        else if (ok) atomicMin(lens + last_at_most(from, NG, s), c);
     }
     __syncthreads();
     for (int i = tid; i < NG; i += kThreads) {
-        const int n = __ldg(g.starts + i + 1) - __ldg(g.starts + i), P = __ldg(g.prefix_lens + i);
+        const int n = i == tid ? b - a : __ldg(g.starts + i + 1) - __ldg(g.starts + i);
+        const int len = i == tid ? P : __ldg(g.prefix_lens + i);
         const int least = *const_cast<volatile int32_t *>(lens + i);   // (global atomics: not through L1)
         int C = 0;
-        if (P < 0 || P > g.max_tokens) set_status(status, PA_ERR_OUT_OF_RANGE);
-        else if (ok && n >= 2 && least != INT_MAX) C = min(P, least - 1) / g.block_size * g.block_size;
+        if (len < 0 || len > g.max_tokens) set_status(status, PA_ERR_OUT_OF_RANGE);
+        else if (ok && n >= 2 && least != INT_MAX) C = min(len, least - 1) / g.block_size * g.block_size;
         lens[i] = C;
     }
     __syncthreads();
