@@ -74,8 +74,8 @@ constexpr int kSmemBudget = 227 * 1024;
 // at its shortest between 58 and 70.
 constexpr double kDecodeBytesPerSmNs = 64.0;
 constexpr double kPrefillFlopsPerSmNs = 6600.0;
-// SM-nanoseconds of a 128-key tile in the prefix kernel: head_dim 64, 128; one M-tile, two
-constexpr double kPrefixTileNs[2][2] = {{700.0, 900.0}, {900.0, 1300.0}};
+// SM-nanoseconds of a tile in the prefix kernel: head_dim 64, 128; 128 keys of one M-tile, of two, 64 keys of two kv-heads
+constexpr double kPrefixTileNs[2][3] = {{700.0, 900.0, 700.0}, {1100.0, 1420.0, 1000.0}};
 
 struct __align__(16) StreamEntry {
     int32_t seq;
@@ -169,7 +169,7 @@ struct DecodeSplit {
     int causal;
     double block_ns;   // SM-nanoseconds per decode block of all kv-heads
     double pair_ns;    // SM-nanoseconds per causal (query row, key) pair of all heads
-    double tile_ns[2]; // SM-nanoseconds per prefix tile of an item with one and with two M-tiles
+    double tile_ns[3]; // SM-nanoseconds per prefix tile of an item with one M-tile, with two, of two kv-heads
     int32_t *prefix_shares;   // CTAs of the prefix kernel that take a share, of prefix_grid
     int prefix_grid;
 };
@@ -188,10 +188,10 @@ __device__ void shared_plan_cta(const SharedGroups &g, const SharedPlan &plan, c
     for (int i = tid; i < g.num_groups; i += kPlanThreads) {
         if (lens[i] <= 0) continue;
         const int n = __ldg(g.starts + i + 1) - __ldg(g.starts + i), pos = g.seqs_per_item / 2;
-        const int pairs = n / g.seqs_per_item, rest = n - pairs * g.seqs_per_item;
-        const double one = rest > 0 && rest <= pos ? 1.0 : 0.0, two = pairs + (rest > pos ? 1.0 : 0.0);
-        pre += (one * split.tile_ns[0] + two * split.tile_ns[1]) * g.num_kv_heads *
-               ((lens[i] + g.keys_per_tile - 1) / g.keys_per_tile);
+        const int full = n / g.seqs_per_item, rest = n - full * g.seqs_per_item;
+        const double one = rest > 0 && rest <= pos ? 1.0 : 0.0, two = full + (rest > pos ? 1.0 : 0.0);
+        const GroupItems x = group_items(n, lens[i], g.num_kv_heads, g.seqs_per_item, g.keys_per_tile, g.pair_seqs);
+        pre += (x.pair ? split.tile_ns[2] : one * split.tile_ns[0] + two * split.tile_ns[1]) * x.heads * x.kt;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
@@ -1363,8 +1363,7 @@ cudaError_t launch_split_decode(const AttnArgs &a, void *workspace, size_t works
     split.causal = a.causal;
     split.block_ns = (double)kU * a.num_kv_heads * a.head_dim * 2 * 2 / kDecodeBytesPerSmNs;
     split.pair_ns = 4.0 * a.num_heads * a.head_dim / kPrefillFlopsPerSmNs;
-    split.tile_ns[0] = kPrefixTileNs[a.head_dim == 64 ? 0 : 1][0];
-    split.tile_ns[1] = kPrefixTileNs[a.head_dim == 64 ? 0 : 1][1];
+    for (int i = 0; i < 3; ++i) split.tile_ns[i] = kPrefixTileNs[a.head_dim == 64 ? 0 : 1][i];
     split.prefix_shares = shared ? shared->shares : nullptr;
     split.prefix_grid = prefix_grid();
     int plan_grid = (int)((max_entries + 4 * kPlanThreads - 1) / (4 * kPlanThreads));

@@ -63,6 +63,8 @@ struct PrefixParams {
     int num_seqs;
     int num_groups;
     int num_heads;
+    int num_kv_heads;
+    int pair_seqs;    // groups of at most this many sequences: items of two kv-heads
     int group;        // q-heads per kv-head
     int pos;          // sequences per M-tile: 128 / group
     int item_rows;
@@ -90,21 +92,28 @@ template <int D> struct Shape {
     static_assert(kSmem <= kSmemLimit, "shared memory");
 };
 
-// A piece: tiles tile0 .. tile0 + nkv - 1 of an item.  `live` = 0 marks the end.
-// With more than `pos` sequences (wide) M-tile t holds the t-th `pos` of them
-// and takes every KV tile; with fewer, both M-tiles hold the same rows, t takes
-// KV tiles t, t + 2, ..., and the output warpgroup joins them.
+// A piece: tiles tile0 .. tile0 + nkv - 1 of an item.  Three kinds:
+//  kWide  more than `pos` sequences: M-tile t holds the t-th `pos` of them; both
+//         take every KV tile of 128 keys
+//  kPair  a small group and two kv-heads: M-tile t holds the rows of kv-head
+//         kvh + t; a KV tile is 64 keys of both, so a TMA box carries both heads
+//         (half the boxes a byte, rows of memory twice as long)
+//  kTurns up to `pos` sequences of one kv-head: both M-tiles hold the same rows, t
+//         takes KV tiles t, t + 2, ..., and the output warpgroup joins them
+// live = 0 marks the end.
+constexpr int kTurns = 0, kWide = 1, kPair = 2;
 struct Piece {
-    int table_seq, kvh, seq0, nseq, wide, tile0, nkv, C, live, pad;
-    int64_t row;      // row of (sequence seq0, q-head 0) in o and ml
-    __device__ __forceinline__ int tiles(int t) const { return wide ? nkv : (nkv + 1 - t) >> 1; }
+    int table_seq, kvh, seq0, nseq, kind, tile0, nkv, C, live, second;
+    int64_t row;      // row of (sequence seq0, q-head 0 of kvh) in o and ml; M-tile 1's rows begin `second` sequences on
+    __device__ __forceinline__ int tiles(int t) const { return kind != kTurns ? nkv : (nkv + 1 - t) >> 1; }
 };
 constexpr int kItemSlots = 4;                 // pieces published ahead of their use
 
 template <int D, int kB>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                  const __grid_constant__ CUtensorMap tmap_v, const PrefixParams p) {
+                  const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_k2,
+                  const __grid_constant__ CUtensorMap tmap_v2, const PrefixParams p) {
     constexpr int kBlocksPerTile = BN / kB;          // cache blocks per KV tile
     static_assert(kBlocksPerTile <= 32, "one TMA box per producer lane");
     using SH = Shape<D>;
@@ -122,6 +131,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // K: [8-row group][D/64 plane][8 rows][64]
     constexpr int kKSbo = kDH * 1024;
     constexpr int kKPlane = 1024;
+    // tiles of two kv-heads: a block's share is twice as long, [..][kv-head][plane][..], the heads kDH planes apart
+    constexpr int kBlock2 = 2 * kVBlockBytes;
+    constexpr int kVS1p = (16 / kB) * kBlock2 + (16 % kB) * 128, kVS2p = (32 / kB) * kBlock2 + (32 % kB) * 128;
+    static_assert(((48 / kB) * kBlock2 + (48 % kB) * 128) == kVS1p + kVS2p, "step 3 = s2 + s1");
+    constexpr int kVSboP = kB < 16 ? kBlock2 : 1024;
+    constexpr int kKSboP = 2 * kDH * 1024;
+    constexpr uint32_t kIdescQK2 = umma_idesc_bf16(BM, BN / 2, 0);
     constexpr uint32_t kIdescQK = umma_idesc_bf16(BM, BN, 0);
     constexpr uint32_t kIdescPV = umma_idesc_bf16(BM, D, 1);
     constexpr uint32_t kAll = 0xffffffffu;
@@ -140,13 +156,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *p_half = o_full + kMT;               // [tile]: P_t's first 64 keys written
     uint64_t *o_empty = p_half + kMT;              // [tile]: O_t read by the output warpgroup
     uint64_t *l_full = o_empty + kMT;              // [tile]: the rows' (m, l) written
-    uint64_t *item_full = l_full + kMT;            // [kItemSlots]: piece published
+    // kPair, [place][tile]: S_t written in its first (even KV tiles) or second place, P_t written there.  The softmax
+    // warpgroups may be a tile ahead of the products, so each place has barriers of its own: the next use of a place
+    // comes after the products that read it, and no barrier gets two phases ahead of who waits for it.
+    uint64_t *s2_full = l_full + kMT;
+    uint64_t *p2_full = s2_full + 2 * kMT;
+    uint64_t *item_full = p2_full + 2 * kMT;       // [kItemSlots]: piece published
     uint64_t *item_empty = item_full + kItemSlots; // [kItemSlots]: piece read by every consumer
     uint64_t *drained = item_empty + kItemSlots;   // every product issued has completed
     uint32_t &tmem_base_s = *reinterpret_cast<uint32_t *>(drained + 1);
     Piece *items = reinterpret_cast<Piece *>(drained + 2);           // [kItemSlots]
     float2 *ml_s = reinterpret_cast<float2 *>(items + kItemSlots);   // [tile][row]
-    static_assert((3 + 2 * kSlots + 6 * kMT + 2 * kItemSlots + 2) * 8 + kItemSlots * sizeof(Piece) +
+    static_assert((3 + 2 * kSlots + 10 * kMT + 2 * kItemSlots + 2) * 8 + kItemSlots * sizeof(Piece) +
                           kMT * BM * sizeof(float2) <= SH::kBarBytes,
                   "barrier area");
 
@@ -184,6 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(p_half + t, BM);
             mbar_init(o_empty + t, BM);
             mbar_init(l_full + t, BM);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(s2_full + b * kMT + t, 1);
+                mbar_init(p2_full + b * kMT + t, BM);
+            }
         }
         for (int i = 0; i < kItemSlots; ++i) {
             mbar_init(item_full + i, 1);
@@ -202,7 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
-    // TMEM columns: S_t at t*BN (fp32); P_t, bf16 pairs, over the first BN/2 columns of S_t; O_t at kMT*BN + t*D
+    // TMEM columns: S_t at t*BN (fp32); P_t, bf16 pairs, over the first BN/2 columns of S_t; O_t at kMT*BN + t*D.
+    // kPair: S_t of 64 columns has two places, for even and odd KV tiles
     auto s_col = [](int t) { return (uint32_t)(t * BN); };
     auto o_col = [](int t) { return (uint32_t)(kMT * BN + t * D); };
     auto slot_of = [](int n) { return n % kSlots; };
@@ -228,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Piece I;
             if (!take_item(it, I)) { ok = false; break; }
             if (!I.live) break;
-            if (!I.wide && I.nkv > 1) {
+            if (I.kind == kTurns && I.nkv > 1) {
                 // both M-tiles hold this row: joined on the way out
 #pragma unroll
                 for (int t = 0; t < kMT; ++t)
@@ -270,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int t = 0; t < kMT; ++t) {
-                if ((t > 0 && !I.wide) || !ok) continue;
+                if ((t > 0 && I.kind == kTurns) || !ok) continue;
                 if (!mbar_wait_warp(o_full + t, (uint32_t)(no[t] & 1), p.wait_ns) ||
                     !mbar_wait_warp(l_full + t, (uint32_t)(no[t] & 1), p.wait_ns)) {
                     ok = false;
@@ -278,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 const float2 ml = ml_s[t * BM + r];
-                const int i = t * p.pos + i_pos;            // sequence within the item
-                const bool row_valid = head < p.group && i < I.nseq;
+                const int i = t * I.second + i_pos;         // sequence within the item (kPair: and kv-head)
+                const bool row_valid = head < p.group && (I.kind == kPair ? i_pos : i) < I.nseq;
                 const int64_t row = I.row + (row_valid ? (int64_t)i * p.group + head : 0);
                 float *dst = p.o + row * D;
                 if (row_valid) p.ml[row] = ml;
@@ -331,15 +357,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             I = Piece{};
             if (t_next < t_end) {
                 const int spi = kMT * p.pos;
-                const PrefixItem x = prefix_item(p.plan, p.starts, p.num_groups, spi, BN, t_next);
+                const PrefixItem x = prefix_item(p.plan, p.starts, p.num_groups, p.num_kv_heads, spi, BN, p.pair_seqs, t_next);
                 const int i0 = x.part * spi;
                 I.table_seq = x.s0;
                 I.kvh = x.kvh;
                 I.seq0 = x.s0 + i0;
                 I.nseq = min(spi, x.n - i0);
-                I.wide = I.nseq > p.pos;
+                I.kind = x.of.pair ? kPair : I.nseq > p.pos ? kWide : kTurns;
+                I.second = x.of.pair ? x.n : p.pos;
                 I.tile0 = x.tile;
-                I.nkv = (int)min((int64_t)(x.kt - x.tile), t_end - t_next);
+                I.nkv = (int)min((int64_t)(x.of.kt - x.tile), t_end - t_next);
                 I.C = x.C;
                 I.live = 1;
                 I.row = x.tile == 0 ? item_row(x.s0, x.n, x.kvh, i0, p.num_heads, p.group)
@@ -355,9 +382,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // block ids of piece X, 32 per chunk (lane l holds block 32*chunk + l of the piece); past the shared tokens (or
         // invalid) the coordinate num_blocks is out of bounds and TMA fills zeros
         auto load_ids = [&](const Piece &X, int chunk) {
-            const int lb = X.tile0 * kBlocksPerTile + chunk * 32 + lane;
+            const int per = X.kind == kPair ? kBlocksPerTile / 2 : kBlocksPerTile, lb = X.tile0 * per + chunk * 32 + lane;
             int coord = p.num_blocks;
-            if (X.live && chunk * 32 + lane < X.nkv * kBlocksPerTile && lb < X.C / kB) {
+            if (X.live && chunk * 32 + lane < X.nkv * per && lb < X.C / kB) {
                 const int32_t blk = __ldg(p.block_tables + (int64_t)X.table_seq * p.max_blocks + lb);
                 if (blk >= 0 && blk < p.num_blocks) coord = blk;
                 else set_status(p.status, PA_ERR_OUT_OF_RANGE);
@@ -376,24 +403,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 if (nq >= 1 && !mbar_wait(q_empty, (uint32_t)((nq - 1) & 1), p.wait_ns)) ok = false;
                 if (ok) {
-                    mbar_arrive_expect_tx(q_full, (uint32_t)((I.wide ? kMT : 1) * kDH * p.pos * p.group * 128));
-                    for (int t = 0; t < (I.wide ? kMT : 1); ++t)
+                    const int mt = I.kind == kTurns ? 1 : kMT;
+                    mbar_arrive_expect_tx(q_full, (uint32_t)(mt * kDH * p.pos * p.group * 128));
+                    for (int t = 0; t < mt; ++t)
                         for (int pl = 0; pl < kDH; ++pl)
-                            tma_load_4d(q_s + t * kQBytes + pl * kPlaneQ, &tmap_q, 0, I.seq0 + t * p.pos, I.kvh * p.group,
-                                        pl, q_full);
+                            tma_load_4d(q_s + t * kQBytes + pl * kPlaneQ, &tmap_q, 0, I.seq0 + (I.kind == kWide ? t * p.pos : 0),
+                                        (I.kvh + (I.kind == kPair ? t : 0)) * p.group, pl, q_full);
                 }
             }
             ok = __shfl_sync(kAll, ok ? 1 : 0, 0) != 0;
             if (!ok) break;
             ++nq;
+            const bool pair = I.kind == kPair;
+            const int per = pair ? kBlocksPerTile / 2 : kBlocksPerTile;
             for (int j = 0; ok && j < I.nkv; ++j) {
-                if ((j * kBlocksPerTile) / 32 != chunk_cur) {
+                if ((j * per) / 32 != chunk_cur) {
                     ids_cur = ids_next;
                     ++chunk_cur;
                     ids_next = load_ids(I, chunk_cur + 1);
                 }
-                const int id0 = (j * kBlocksPerTile) & 31;
-                const int cbv = __shfl_sync(kAll, ids_cur, id0 + (lane & (kBlocksPerTile - 1)));
+                const int id0 = (j * per) & 31;
+                const int cbv = __shfl_sync(kAll, ids_cur, id0 + (lane & (per - 1)));
                 for (int kv = 0; kv < 2; ++kv) {
                     const int m = n + 2 * j + kv;
                     if (p.stall == PA_STALL_PRODUCER && m >= p.stall_after) {
@@ -407,15 +437,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     if (lane == 0) mbar_arrive_expect_tx(kv_full + slot_of(m), kSlotBytes);
                     __syncwarp();
-                    // lane b < kBlocksPerTile copies block b of K or V
-                    if (lane < kBlocksPerTile) {
-                        uint8_t *dst = kv_s + slot_of(m) * kSlotBytes + lane * kVBlockBytes;
-                        if (kv)
-                            tma_load_5d(dst, &tmap_v, 0, 0, 0, I.kvh, cbv, kv_full + slot_of(m));
-                        else if (kB == 8)
-                            tma_load_5d(dst, &tmap_k, 0, 0, 0, I.kvh, cbv, kv_full + slot_of(m));
-                        else
-                            tma_load_5d(dst, &tmap_k, 0, 0, I.kvh * kDH, 0, cbv, kv_full + slot_of(m));
+                    // lane b < per copies block b of K or V
+                    if (lane < per) {
+                        uint8_t *dst = kv_s + slot_of(m) * kSlotBytes + lane * (pair ? kBlock2 : kVBlockBytes);
+                        const CUtensorMap *map = kv ? (pair ? &tmap_v2 : &tmap_v) : (pair ? &tmap_k2 : &tmap_k);
+                        if (kv || kB == 8) tma_load_5d(dst, map, 0, 0, 0, I.kvh, cbv, kv_full + slot_of(m));
+                        else tma_load_5d(dst, map, 0, 0, I.kvh * kDH, 0, cbv, kv_full + slot_of(m));
                     }
                     issued_end = m + 1;
                 }
@@ -455,15 +482,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_bf16_tmem_a_k64(tmem + o_col(t), tmem + s_col(t) + kq * 32, dv + ((vo + kq * kVChunk) >> 4), kIdescPV,
                                  kVS1 >> 4, kVS2 >> 4, (!first || kq > 0) ? 1u : 0u);
         };
+        // tiles of two kv-heads: S_t = Q_t K_t^T and O_t (+)= P_t V_t over 64 keys, head t of ring entry nk / nv; b: S's place
+        const uint64_t dk2 = umma_desc_sw128(kv_addr, 16, kKSboP), dv2 = umma_desc_sw128(kv_addr, kVLbo, kVSboP);
+        auto issue_qk2 = [&](int t, int b, int nk) {
+            const uint32_t ko = (uint32_t)slot_of(nk) * kSlotBytes + t * (kDH * 1024);
+#pragma unroll
+            for (int pl = 0; pl < D / 64; ++pl)
+                umma_bf16_k64(tmem + s_col(t) + b * 64, dq + ((uint32_t)(t * kQBytes + pl * kPlaneQ) >> 4),
+                              dk2 + ((ko + pl * kKPlane) >> 4), kIdescQK2, pl > 0 ? 1u : 0u);
+        };
+        auto issue_pv2 = [&](int t, int b, int nv, bool first) {
+            const uint32_t vo = (uint32_t)slot_of(nv) * kSlotBytes + t * kVBlockBytes;
+            umma_bf16_tmem_a_k64(tmem + o_col(t), tmem + s_col(t) + b * 64, dv2 + (vo >> 4), kIdescPV, kVS1p >> 4, kVS2p >> 4,
+                                 first ? 0u : 1u);
+        };
         bool ok = true, stopped = false;
         int n = 0, nq = 0;
-        int J0 = 0, J1 = 0, no0 = 0, no1 = 0;   // per M-tile: tiles and pieces so far
+        int J0 = 0, J1 = 0, no0 = 0, no1 = 0;   // per M-tile: tiles (other than kPair's) and pieces so far
+        int U0 = 0, U1 = 0;                     // kPair: uses of S's places so far
         for (int it = 0; ok; ++it) {
             Piece I;
             if (!take_item(it, I)) { ok = false; break; }
             if (!I.live) break;
             const int nkv = __shfl_sync(kAll, I.nkv, 0);
-            const bool wide = __shfl_sync(kAll, I.wide, 0) != 0;
+            const int kind = __shfl_sync(kAll, I.kind, 0);
             if (p.stall == PA_STALL_CONSUMER && n >= p.stall_after) { stopped = true; ok = false; break; }
             if (!mbar_wait_warp(q_full, (uint32_t)(nq & 1), p.wait_ns) ||
                 !mbar_wait_warp(kv_full + slot_of(n), phase_of(n), p.wait_ns)) {
@@ -471,12 +513,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
+            // the piece's first product into O_t overwrites it: the output warpgroup has read the last piece's
+            auto o_free = [&](int t) -> bool {
+                const int no = t ? no1 : no0;
+                return no == 0 || mbar_wait_warp(o_empty + t, (uint32_t)((no - 1) & 1), p.wait_ns);
+            };
             // O_t's half products with V in ring entry nv, as P_t comes; x: M-tile t's tiles so far in this piece
             auto pv = [&](int t, int nv, int x) -> bool {
-                // the piece's first product into O_t overwrites it: the output warpgroup has read the last piece's
-                const int no = t ? no1 : no0;
                 const uint32_t ph = (uint32_t)(((t ? J1 : J0) + x) & 1);
-                if (x == 0 && no > 0 && !mbar_wait_warp(o_empty + t, (uint32_t)((no - 1) & 1), p.wait_ns)) return false;
+                if (x == 0 && !o_free(t)) return false;
                 if (!mbar_wait_warp(p_half + t, ph, p.wait_ns)) return false;
                 tc_fence_after();
                 issue_pv(t, nv, 0, x == 0);
@@ -485,7 +530,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                 issue_pv(t, nv, 1, x == 0);
                 return true;
             };
-            if (wide) {
+            if (kind == kPair) {
+                // QK_0(j+1) QK_1(j+1) PV_0(j) PV_1(j): the next tile's logits are under way while the softmax
+                // warpgroups turn this one's into weights
+#pragma unroll
+                for (int t = 0; t < kMT; ++t) {
+                    issue_qk2(t, 0, n);
+                    umma_commit(s2_full + t);
+                }
+                if (nkv == 1) umma_commit(q_empty);
+                umma_commit(kv_empty + slot_of(n));
+                for (int j = 0; j < nkv; ++j) {
+                    const int nv = n + 2 * j + 1, nk = n + 2 * j + 2, b = j & 1;
+                    // test hook: stop, leaving ring entries unreleased, so the producer's wait runs out
+                    if (p.stall == PA_STALL_CONSUMER && nv >= p.stall_after) { stopped = true; ok = false; break; }
+                    if (!mbar_wait_warp(kv_full + slot_of(nv), phase_of(nv), p.wait_ns)) { ok = false; break; }
+                    if (j + 1 < nkv) {
+                        if (!mbar_wait_warp(kv_full + slot_of(nk), phase_of(nk), p.wait_ns)) { ok = false; break; }
+                        tc_fence_after();
+#pragma unroll
+                        for (int t = 0; t < kMT; ++t) {
+                            issue_qk2(t, b ^ 1, nk);
+                            umma_commit(s2_full + (b ^ 1) * kMT + t);
+                        }
+                        umma_commit(kv_empty + slot_of(nk));
+                        if (j + 2 == nkv) umma_commit(q_empty);    // the piece's last QK products
+                    }
+#pragma unroll
+                    for (int t = 0; t < kMT; ++t) {
+                        if (!ok || (j == 0 && !o_free(t)) ||
+                            !mbar_wait_warp(p2_full + b * kMT + t, (uint32_t)(((b ? U1 : U0) + (j >> 1)) & 1), p.wait_ns)) {
+                            ok = false;
+                            continue;
+                        }
+                        tc_fence_after();
+                        issue_pv2(t, b, nv, j == 0);
+                        if (j + 1 == nkv) umma_commit(o_full + t);
+                    }
+                    if (!ok) break;
+                    umma_commit(kv_empty + slot_of(nv));
+                }
+            } else if (kind == kWide) {
 #pragma unroll
                 for (int t = 0; t < kMT; ++t) {
                     issue_qk(t, t, n);
@@ -496,7 +581,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < nkv; ++j) {
                     const bool next = j + 1 < nkv;
                     const int nv = n + 2 * j + 1, nk = n + 2 * j + 2;
-                    // test hook: stop, leaving ring entries unreleased, so the producer's wait runs out
                     if (p.stall == PA_STALL_CONSUMER && nv >= p.stall_after) { stopped = true; ok = false; break; }
                     if (!mbar_wait_warp(kv_full + slot_of(nv), phase_of(nv), p.wait_ns)) { ok = false; break; }
 #pragma unroll
@@ -549,10 +633,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             n += 2 * nkv;
             ++nq;
-            J0 += wide ? nkv : (nkv + 1) >> 1;
-            J1 += wide ? nkv : nkv >> 1;
+            if (kind == kPair) {
+                U0 += (nkv + 1) >> 1;
+                U1 += nkv >> 1;
+            } else {
+                J0 += kind == kWide ? nkv : (nkv + 1) >> 1;
+                J1 += kind == kWide ? nkv : nkv >> 1;
+            }
             ++no0;
-            no1 += wide || nkv > 1 ? 1 : 0;
+            no1 += kind != kTurns || nkv > 1 ? 1 : 0;
         }
         if (!ok && !stopped && lane == 0) {
             set_status(p.status, PA_ERR_TIMEOUT);
@@ -571,34 +660,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float sl2 = p.scale_log2;
         bool ok = true;
-        int J = 0, no = 0;
+        int no = 0, n_next = 0, J = 0, U0 = 0, U1 = 0;    // pieces, ring entries, tiles (kPair: by S_t's place) so far
         for (int it = 0; ok; ++it) {
             Piece I;
             if (!take_item(it, I)) { ok = false; break; }
             if (!I.live) break;
-            const int mine = I.tiles(t);
+            const int mine = I.tiles(t), n = n_next;
+            n_next += 2 * I.nkv;
             if (mine == 0) continue;
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < mine; ++j) {
-                if (!mbar_wait_warp(s_full + t, (uint32_t)((J + j) & 1), p.wait_ns)) { ok = false; break; }
+            // One tile: S to P.  S is read whole and its max taken first; 128 keys of P then go out in two halves (the
+            // tensor pipe takes the first while the second is computed).  The piece's first tile takes its own max;
+            // later ones run with the running max m: P stays <= 2^8 unless the tile's max exceeds it by more than 8,
+            // and then (rarely) the row moves its max and rescales O first.  lim: shared keys from the tile's first on;
+            // nv: ring entry of the last tile's values.  bar, out: S written, P's first half (all 64 keys) written.
+            auto tile = [&](auto keys, uint32_t col, uint64_t *bar, uint64_t *out, uint32_t phase, int lim, bool first,
+                            int nv) -> bool {
+                constexpr int kN = decltype(keys)::value;
+                if (!mbar_wait_warp(bar, phase, p.wait_ns)) return false;
                 tc_fence_after();
-                const int lim = I.C - (I.tile0 + (I.wide ? j : 2 * j + t)) * BN;     // shared keys from the tile's first on
-                // S is read whole and its max taken first, so P can go out in two halves of 64 keys (the tensor pipe
-                // takes the first while the second is computed).  The piece's first tile takes its own max; later ones
-                // run with the running max m: P stays <= 2^8 unless the tile's max exceeds it by more than 8, and
-                // then (rarely) the row moves its max and rescales O first.
-                uint32_t sr[BN / 32][32];
+                uint32_t sr[kN / 32][32];
                 auto mask = [&](int c) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (32 * c + e >= lim) sr[c][e] = __float_as_uint(-INFINITY);
                 };
-                tmem_ld32(lane_addr + s_col(t), sr[0]);
-                tmem_ld32(lane_addr + s_col(t) + 32, sr[1]);
-                tmem_wait_ld_regs(sr[0], sr[1]);
-                tmem_ld32(lane_addr + s_col(t) + 64, sr[2]);
-                tmem_ld32(lane_addr + s_col(t) + 96, sr[3]);
-                if (lim < BN) { mask(0); mask(1); }
                 float a0 = -INFINITY, a1 = -INFINITY;
                 auto max_of = [&](int c) {
 #pragma unroll
@@ -607,14 +693,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                         a1 = fmax3(a1, __uint_as_float(sr[c][e + 2]), __uint_as_float(sr[c][e + 3]));
                     }
                 };
+                tmem_ld32(col, sr[0]);
+                tmem_ld32(col + 32, sr[1]);
+                tmem_wait_ld_regs(sr[0], sr[1]);
+                if constexpr (kN == BN) {
+                    tmem_ld32(col + 64, sr[2]);
+                    tmem_ld32(col + 96, sr[3]);
+                }
+                if (lim < kN) { mask(0); mask(1); }
                 max_of(0);
                 max_of(1);
-                tmem_wait_ld_regs(sr[2], sr[3]);
-                if (lim < BN) { mask(2); mask(3); }
-                max_of(2);
-                max_of(3);
+                if constexpr (kN == BN) {
+                    tmem_wait_ld_regs(sr[2], sr[3]);
+                    if (lim < kN) { mask(2); mask(3); }
+                    max_of(2);
+                    max_of(3);
+                }
                 const float m_tile = fmaxf(a0, a1) * sl2;
-                if (j == 0) {
+                if (first) {
                     m = m_tile == -INFINITY ? 0.f : m_tile;
                 } else {
                     const bool need = m_tile > m + 8.f;
@@ -622,7 +718,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float m_new = need ? m_tile : m;
                         const float alpha = fast_exp2(m - m_new);
                         l *= alpha;
-                        // PV_t(j-1) completed before S_t(j) was committed, so O_t is final here
+                        // O_t's earlier products are done: with 128 keys they completed before this S was committed;
+                        // with 64, whose S comes a tile early, their values' ring entry must have been released (it
+                        // is not used and released again before this tile's P is out)
+                        if (kN != BN && !mbar_wait_warp(kv_empty + slot_of(nv), phase_of(nv), p.wait_ns)) return false;
+                        tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t o[32];
@@ -636,15 +736,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m = m_new;
                     }
                 }
-                // P for key pairs u0..u0+31 into pk, rounded to bf16 (the products' operand type): independent
-                // roundings of half a step, beside a result rounded to bf16 itself; l sums the unrounded values
+                // P for 32 key pairs into pk, rounded to bf16 (the products' operand type): independent roundings of
+                // half a step, beside a result rounded to bf16 itself; l sums the unrounded values
                 const float2 sl2x2 = make_float2(sl2, sl2), negm = make_float2(-m, -m);
                 float2 ls = make_float2(0.f, 0.f);
-                uint32_t pk[BN / 4];
+                uint32_t pk[32];
                 auto pass = [&](auto u0c) {
                     constexpr int u0 = decltype(u0c)::value;
 #pragma unroll
-                    for (int u = u0; u < u0 + BN / 4; ++u) {
+                    for (int u = u0; u < u0 + 32; ++u) {
                         const float s0 = __uint_as_float(sr[u >> 4][(2 * u) & 31]);
                         const float s1 = __uint_as_float(sr[u >> 4][(2 * u + 1) & 31]);
                         const float2 x = fma_f32x2(make_float2(s0, s1), sl2x2, negm);
@@ -655,23 +755,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 };
                 pass(std::integral_constant<int, 0>{});
-                tmem_st32(lane_addr + s_col(t), pk);
+                tmem_st32(col, pk);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(p_half + t);
-                pass(std::integral_constant<int, BN / 4>{});
-                tmem_st32(lane_addr + s_col(t) + 32, pk);
+                mbar_arrive(out);
+                if constexpr (kN == BN) {
+                    pass(std::integral_constant<int, 32>{});
+                    tmem_st32(col + 32, pk);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(p_full + t);
+                }
                 l += ls.x + ls.y;
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(p_full + t);
+                return true;
+            };
+            const uint32_t col = lane_addr + s_col(t);
+            for (int j = 0; j < mine; ++j) {
+                if (I.kind == kPair) {
+                    const int b = j & 1;
+                    ok = tile(std::integral_constant<int, BN / 2>{}, col + b * 64, s2_full + b * kMT + t, p2_full + b * kMT + t,
+                              (uint32_t)((b ? U1++ : U0++) & 1), I.C - (I.tile0 + j) * (BN / 2), j == 0, n + 2 * j - 1);
+                } else {
+                    ok = tile(std::integral_constant<int, BN>{}, col, s_full + t, p_half + t, (uint32_t)(J++ & 1),
+                              I.C - (I.tile0 + (I.kind == kWide ? j : 2 * j + t)) * BN, j == 0, 0);
+                }
+                if (!ok) break;
             }
             if (!ok) break;
             // (m, l) for the output warpgroup, which read the last piece's before it released O_t
             if (no > 0 && !mbar_wait_warp(o_empty + t, (uint32_t)((no - 1) & 1), p.wait_ns)) { ok = false; break; }
             ml_s[t * BM + r] = make_float2(m, l);
             mbar_arrive(l_full + t);
-            J += mine;
             ++no;
         }
         if (!ok && r == 0) {
@@ -705,32 +819,32 @@ CUresult make_q_map(CUtensorMap *map, const void *q, int num_seqs, int num_heads
     return encode(map, q, 4, dims, strides, box);
 }
 
-// One block of one kv-head: [plane][B rows][64]
-CUresult make_v_map(CUtensorMap *map, const void *pool, int num_blocks, int kB, int hkv, int D) {
+// One block of `heads` kv-heads: [kv-head][plane][B rows][64]
+CUresult make_v_map(CUtensorMap *map, const void *pool, int num_blocks, int kB, int hkv, int D, int heads) {
     const cuuint64_t dims[5] = {64, (cuuint64_t)kB, (cuuint64_t)(D / 64), (cuuint64_t)hkv, (cuuint64_t)num_blocks};
     const cuuint64_t strides[4] = {(cuuint64_t)hkv * D * 2, 128, (cuuint64_t)D * 2, (cuuint64_t)kB * hkv * D * 2};
-    const cuuint32_t box[5] = {64, (cuuint32_t)kB, (cuuint32_t)(D / 64), 1, 1};
+    const cuuint32_t box[5] = {64, (cuuint32_t)kB, (cuuint32_t)(D / 64), (cuuint32_t)heads, 1};
     return encode(map, pool, 5, dims, strides, box);
 }
 
-// One block of one kv-head: [8-row group][plane][8 rows][64] (at B = 8 the map above gives the same)
-CUresult make_k_map(CUtensorMap *map, const void *pool, int num_blocks, int kB, int hkv, int D) {
+// One block of `heads` kv-heads: [8-row group][kv-head][plane][8 rows][64] (at B = 8 the map above gives the same)
+CUresult make_k_map(CUtensorMap *map, const void *pool, int num_blocks, int kB, int hkv, int D, int heads) {
+    if (kB == 8) return make_v_map(map, pool, num_blocks, kB, hkv, D, heads);
     const cuuint64_t dims[5] = {64, 8, (cuuint64_t)hkv * (D / 64), (cuuint64_t)(kB / 8), (cuuint64_t)num_blocks};
     const cuuint64_t strides[4] = {(cuuint64_t)hkv * D * 2, 128, (cuuint64_t)8 * hkv * D * 2, (cuuint64_t)kB * hkv * D * 2};
-    const cuuint32_t box[5] = {64, 8, (cuuint32_t)(D / 64), (cuuint32_t)(kB / 8), 1};
+    const cuuint32_t box[5] = {64, 8, (cuuint32_t)(heads * (D / 64)), (cuuint32_t)(kB / 8), 1};
     return encode(map, pool, 5, dims, strides, box);
 }
 
 template <int D, int B>
-cudaError_t launch_main(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const PrefixParams &prm,
-                        int grid, cudaStream_t stream) {
+cudaError_t launch_main(const CUtensorMap (&m)[5], const PrefixParams &prm, int grid, cudaStream_t stream) {
     const size_t smem = Shape<D>::kSmem;
     auto kern = prefix_kernel<D, B>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3(grid), dim3(kThreads), smem, stream, mq, mk, mv, prm);
+    return launch_dependent(kern, dim3(grid), dim3(kThreads), smem, stream, m[0], m[1], m[2], m[3], m[4], prm);
 }
 
 }  // namespace
@@ -739,12 +853,13 @@ int prefix_seqs_per_item(int group) { return kMT * (BM / group); }
 
 cudaError_t launch_prefix(const AttnArgs &a, const SharedJob &job, cudaStream_t stream) {
     const int G = a.num_heads / a.num_kv_heads;
-    CUtensorMap mq, mk, mv;
-    if (make_q_map(&mq, a.q, a.num_seqs, a.num_heads, a.head_dim, BM / G, G) != CUDA_SUCCESS ||
-        (a.block_size == 8 ? make_v_map(&mk, a.k_cache, a.num_blocks, 8, a.num_kv_heads, a.head_dim)
-                           : make_k_map(&mk, a.k_cache, a.num_blocks, a.block_size, a.num_kv_heads, a.head_dim)) != CUDA_SUCCESS ||
-        make_v_map(&mv, a.v_cache, a.num_blocks, a.block_size, a.num_kv_heads, a.head_dim) != CUDA_SUCCESS)
-        return cudaErrorNotSupported;
+    CUtensorMap m[5];   // q, then K and V of one kv-head, of two
+    const int two = a.num_kv_heads > 1 ? 2 : 1;
+    if (make_q_map(&m[0], a.q, a.num_seqs, a.num_heads, a.head_dim, BM / G, G) != CUDA_SUCCESS) return cudaErrorNotSupported;
+    for (int i = 0; i < 2; ++i)
+        if (make_k_map(&m[1 + 2 * i], a.k_cache, a.num_blocks, a.block_size, a.num_kv_heads, a.head_dim, i ? two : 1) != CUDA_SUCCESS ||
+            make_v_map(&m[2 + 2 * i], a.v_cache, a.num_blocks, a.block_size, a.num_kv_heads, a.head_dim, i ? two : 1) != CUDA_SUCCESS)
+            return cudaErrorNotSupported;
     PrefixParams prm;
     prm.plan = job.plan;
     prm.starts = job.groups.starts;
@@ -755,6 +870,8 @@ cudaError_t launch_prefix(const AttnArgs &a, const SharedJob &job, cudaStream_t 
     prm.num_seqs = a.num_seqs;
     prm.num_groups = job.groups.num_groups;
     prm.num_heads = a.num_heads;
+    prm.num_kv_heads = a.num_kv_heads;
+    prm.pair_seqs = job.groups.pair_seqs;
     prm.group = G;
     prm.pos = BM / G;
     prm.item_rows = job.item_rows;
@@ -769,12 +886,12 @@ cudaError_t launch_prefix(const AttnArgs &a, const SharedJob &job, cudaStream_t 
     prm.wait_sites = wt.sites;
     const int grid = prefix_grid();
     switch (a.head_dim * 100 + a.block_size) {
-        case 6408: return launch_main<64, 8>(mq, mk, mv, prm, grid, stream);
-        case 6416: return launch_main<64, 16>(mq, mk, mv, prm, grid, stream);
-        case 6432: return launch_main<64, 32>(mq, mk, mv, prm, grid, stream);
-        case 12808: return launch_main<128, 8>(mq, mk, mv, prm, grid, stream);
-        case 12816: return launch_main<128, 16>(mq, mk, mv, prm, grid, stream);
-        case 12832: return launch_main<128, 32>(mq, mk, mv, prm, grid, stream);
+        case 6408: return launch_main<64, 8>(m, prm, grid, stream);
+        case 6416: return launch_main<64, 16>(m, prm, grid, stream);
+        case 6432: return launch_main<64, 32>(m, prm, grid, stream);
+        case 12808: return launch_main<128, 8>(m, prm, grid, stream);
+        case 12816: return launch_main<128, 16>(m, prm, grid, stream);
+        case 12832: return launch_main<128, 32>(m, prm, grid, stream);
         default: return cudaErrorNotSupported;
     }
 }

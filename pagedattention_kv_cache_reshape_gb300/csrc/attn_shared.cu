@@ -287,8 +287,8 @@ __global__ void __launch_bounds__(kCcThreads, 2) shared_cc_kernel(const CcParams
     const int64_t t_end = c < P0 ? share_begin(c + 1, T0, P0) : 0;
     const int64_t rows0 = (int64_t)p.num_seqs * p.num_heads;
     while (t < t_end) {
-        const PrefixItem it = prefix_item(p.plan, p.group_starts, p.num_groups, p.seqs_per_item, kKeys, t);
-        const int tiles = (int)min((int64_t)(it.kt - it.tile), t_end - t), i0 = it.part * p.seqs_per_item;
+        const PrefixItem it = prefix_item(p.plan, p.group_starts, p.num_groups, p.num_kv_heads, p.seqs_per_item, kKeys, 0, t);
+        const int tiles = (int)min((int64_t)(it.of.kt - it.tile), t_end - t), i0 = it.part * p.seqs_per_item;
         const int64_t row = it.tile == 0 ? item_row(it.s0, it.n, it.kvh, i0, p.num_heads, G) : rows0 + c * p.item_rows;
         CcPiece w;
         w.table = p.block_tables + (int64_t)it.s0 * p.max_blocks;
@@ -345,6 +345,7 @@ struct MergeParams {
     int item_rows;
     int seqs_per_item;
     int keys_per_tile;
+    int pair_seqs;
     int num_seqs;
     int num_groups;
     int num_heads;
@@ -435,11 +436,11 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
     RowPieces pre, own;
     if (mine && C > 0) {
         const int s0 = __ldg(p.group_starts + g), n = __ldg(p.group_starts + g + 1) - s0;
-        const int per_head = (n + p.seqs_per_item - 1) / p.seqs_per_item;
-        const int part = (s - s0) / p.seqs_per_item, item = kvh * per_head + part;
-        const int64_t kt = (C + p.keys_per_tile - 1) / p.keys_per_tile;
-        pre = RowPieces(item_row(s0, n, kvh, s - s0, p.num_heads, G) + hh, rows0 + (s - s0 - part * p.seqs_per_item) * G + hh,
-                        p.item_rows, p.plan.tile_start[g] + item * kt, kt, p.plan.tile_start[p.num_groups],
+        const GroupItems x = group_items(n, C, p.num_kv_heads, p.seqs_per_item, p.keys_per_tile, p.pair_seqs);
+        const int part = x.pair ? 0 : (s - s0) / p.seqs_per_item, item = x.pair ? kvh >> 1 : kvh * x.parts + part;
+        const int i = x.pair ? (kvh & 1) * n + s - s0 : s - s0 - part * p.seqs_per_item;   // row / G in the item
+        pre = RowPieces(item_row(s0, n, kvh, s - s0, p.num_heads, G) + hh, rows0 + i * G + hh, p.item_rows,
+                        p.plan.tile_start[g] + (int64_t)item * x.kt, x.kt, p.plan.tile_start[p.num_groups],
                         p.pre_shares_dev ? *p.pre_shares_dev : p.pre_shares);
     }
     if (mine && p.own_start) {
@@ -545,7 +546,7 @@ TcLayout tc_layout(int num_seqs, int num_groups, int num_heads, int num_kv_heads
     const size_t S = num_seqs, NG = num_groups;
     const int G = num_heads / num_kv_heads > 0 ? num_heads / num_kv_heads : 1;
     const int spi = G <= 128 ? prefix_seqs_per_item(G) : 1;
-    w.item_rows = (spi < num_seqs ? spi : num_seqs) * G;
+    w.item_rows = (spi < 2 * num_seqs ? spi : 2 * num_seqs) * G;   // (two kv-heads of a small group)
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t a = at; at = align_up(at + bytes, 256); return a; };
     w.seq_group = take(4 * S);
@@ -574,10 +575,10 @@ cudaError_t launch_tc(const AttnArgs &a, const int32_t *group_starts, const int3
                       void *workspace, cudaStream_t stream) {
     const TcLayout w = tc_layout(a.num_seqs, num_groups, a.num_heads, a.num_kv_heads, a.head_dim, a.max_blocks, a.block_size);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const int spi = prefix_seqs_per_item(a.num_heads / a.num_kv_heads);
+    const int spi = prefix_seqs_per_item(a.num_heads / a.num_kv_heads), pair = a.num_kv_heads % 2 == 0 ? spi / 2 : 0;
     SharedJob job;
     job.groups = {a.context_lens, group_starts, prefix_lens, a.num_seqs, num_groups, a.num_kv_heads, a.block_size,
-                  (int64_t)a.max_blocks * a.block_size, spi, kPrefixKeys};
+                  (int64_t)a.max_blocks * a.block_size, spi, kPrefixKeys, pair};
     job.plan = {reinterpret_cast<int32_t *>(ws + w.seq_group), reinterpret_cast<int32_t *>(ws + w.own_len),
                 reinterpret_cast<int32_t *>(ws + w.shared_len), reinterpret_cast<int64_t *>(ws + w.tile_start)};
     job.shares = reinterpret_cast<int32_t *>(ws + w.shares);
@@ -590,7 +591,7 @@ cudaError_t launch_tc(const AttnArgs &a, const int32_t *group_starts, const int3
     cudaError_t e = launch_split_decode(a, ws + w.decode, w.total - w.decode, stream, false, nullptr, nullptr, &prefix, &job);
     if (e != cudaSuccess) return e;
     MergeParams mg = {a.out, group_starts, job.plan, nullptr, job.pre_o, job.pre_ml, job.own_o, job.own_ml, job.shares, 0, 0,
-                      job.item_rows, spi, kPrefixKeys, a.num_seqs, num_groups, a.num_heads, a.num_kv_heads, 1};
+                      job.item_rows, spi, kPrefixKeys, pair, a.num_seqs, num_groups, a.num_heads, a.num_kv_heads, 1};
     return a.head_dim == 64 ? launch_merge<__nv_bfloat16, 64>(mg, stream) : launch_merge<__nv_bfloat16, 128>(mg, stream);
 }
 
@@ -613,7 +614,7 @@ cudaError_t launch_shared_prefix(const AttnArgs &a, const int32_t *group_starts,
                              reinterpret_cast<int32_t *>(ws + w.shared_len), reinterpret_cast<int64_t *>(ws + w.tile_start)};
     int64_t *own_start = reinterpret_cast<int64_t *>(ws + w.own_start);
     const SharedGroups groups = {a.context_lens, group_starts, prefix_lens, a.num_seqs, num_groups, a.num_kv_heads,
-                                 a.block_size, (int64_t)a.max_blocks * a.block_size, spi, kKeys};
+                                 a.block_size, (int64_t)a.max_blocks * a.block_size, spi, kKeys, 0};
     cudaError_t e = launch_dependent(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, groups, plan,
                                      reinterpret_cast<int32_t *>(ws + w.scratch), own_start, a.status);
     if (e != cudaSuccess) return e;
@@ -637,7 +638,7 @@ cudaError_t launch_shared_prefix(const AttnArgs &a, const int32_t *group_starts,
     cc.scale_log2 = a.scale * 1.4426950408889634f;
     cc.status = a.status;
     MergeParams mg = {a.out, group_starts, plan, own_start, cc.pre_o, cc.pre_ml, cc.own_o, cc.own_ml, nullptr, grid, grid, cc.item_rows, spi,
-                      kKeys, a.num_seqs, num_groups, a.num_heads, a.num_kv_heads,
+                      kKeys, 0, a.num_seqs, num_groups, a.num_heads, a.num_kv_heads,
                       reinterpret_cast<uintptr_t>(a.out) % 4 == 0};
     if (a.dtype == PA_DTYPE_F32)
         return a.head_dim == 64 ? launch_typed<float, 64>(cc, mg, grid, stream)

@@ -7,7 +7,9 @@
 // smallest context - 1), so every sequence keeps at least one token of its
 // own, and 0 where sharing does not pay.  A prefix item is (g, kv-head,
 // `seqs_per_item` neighbouring sequences); its tiles are `keys_per_tile` keys
-// of the prefix.  Items are listed by group, kv-head, sequences.
+// of the prefix.  Items of a small group (at most `pair_seqs` sequences) are (g,
+// two neighbouring kv-heads) and their tiles half as many keys.  Items are
+// listed by group, kv-head, sequences.
 //
 // Pieces: a share's tiles of one item.  The piece that begins with the item's
 // first tile is kept in the item's own rows, ordered (group, kv-head, sequence,
@@ -34,7 +36,23 @@ struct SharedGroups {
     int64_t max_tokens;            // max_blocks * block_size
     int seqs_per_item;
     int keys_per_tile;
+    int pair_seqs;                 // 0: no items of two kv-heads
 };
+
+// A group's items: heads * parts of them, each of kt tiles of `keys` keys.
+struct GroupItems {
+    int pair, heads, parts, keys, kt;
+};
+__device__ __forceinline__ GroupItems group_items(int n, int C, int num_kv_heads, int seqs_per_item, int keys_per_tile,
+                                                  int pair_seqs) {
+    GroupItems x;
+    x.pair = n <= pair_seqs;
+    x.heads = x.pair ? num_kv_heads >> 1 : num_kv_heads;
+    x.parts = x.pair ? 1 : (n + seqs_per_item - 1) / seqs_per_item;
+    x.keys = x.pair ? keys_per_tile >> 1 : keys_per_tile;
+    x.kt = (C + x.keys - 1) / x.keys;
+    return x;
+}
 
 // The plan, in the workspace.
 struct SharedPlan {
@@ -61,24 +79,27 @@ __device__ __forceinline__ int last_at_most(const V *a, int n, X v) {
 
 // The prefix item at tile t of the stream (t < the stream's end).
 struct PrefixItem {
-    int g, C, kt;          // group, its shared tokens and their tiles
+    int g, C;              // group, its shared tokens
     int s0, n;             // the group's first sequence, its sequences
-    int kvh, part;         // kv-head; the item's place among the group's sequences
+    int kvh, part;         // (first) kv-head; the item's place among the group's sequences
     int tile;              // t's tile of the item
+    GroupItems of;
 };
 __device__ __forceinline__ PrefixItem prefix_item(const SharedPlan &plan, const int32_t *starts, int num_groups,
-                                                  int seqs_per_item, int keys_per_tile, int64_t t) {
+                                                  int num_kv_heads, int seqs_per_item, int keys_per_tile, int pair_seqs,
+                                                  int64_t t) {
     PrefixItem it;
     it.g = last_at_most(plan.tile_start, num_groups, t);   // (groups without tiles are passed over)
     it.C = plan.shared_len[it.g];
-    it.kt = (it.C + keys_per_tile - 1) / keys_per_tile;
     it.s0 = __ldg(starts + it.g);
     it.n = __ldg(starts + it.g + 1) - it.s0;
+    it.of = group_items(it.n, it.C, num_kv_heads, seqs_per_item, keys_per_tile, pair_seqs);
     const int64_t local = t - plan.tile_start[it.g];
-    const int item = (int)(local / it.kt), per_head = (it.n + seqs_per_item - 1) / seqs_per_item;
-    it.tile = (int)(local - (int64_t)item * it.kt);
-    it.kvh = item / per_head;
-    it.part = item - it.kvh * per_head;
+    const int item = (int)(local / it.of.kt);
+    it.tile = (int)(local - (int64_t)item * it.of.kt);
+    it.kvh = item / it.of.parts;
+    it.part = item - it.kvh * it.of.parts;
+    if (it.of.pair) it.kvh *= 2;
     return it;
 }
 
@@ -168,8 +189,8 @@ __device__ int64_t shared_write_plan(const SharedGroups &g, const SharedPlan &pl
             const int C = lens[i];
             if (C > 0) {
                 const int n = __ldg(g.starts + i + 1) - __ldg(g.starts + i);
-                mine = (int64_t)g.num_kv_heads * ((n + g.seqs_per_item - 1) / g.seqs_per_item) *
-                       ((C + g.keys_per_tile - 1) / g.keys_per_tile);
+                const GroupItems x = group_items(n, C, g.num_kv_heads, g.seqs_per_item, g.keys_per_tile, g.pair_seqs);
+                mine = (int64_t)x.heads * x.parts * x.kt;
             }
             plan.shared_len[i] = C;
         }

@@ -63,6 +63,17 @@ def test_many_sequences_and_groups(S, NG, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, **ids)
+@pytest.mark.parametrize("H,Hkv,D,B,n,step", [(32, 32, 128, 16, 8, 16), (32, 32, 64, 8, 3, 8), (32, 8, 128, 32, 40, 64),
+                                              (15, 15, 128, 8, 5, 24), (32, 1, 64, 16, 3, 208), (16, 4, 64, 16, 70, 48)])
+def test_many_pieces(H, Hkv, D, B, n, step, dtype):
+    """Groups of all lengths whose items are cut anywhere: many pieces a CTA, of all kinds, again and again."""
+    c = Case([(n + i % 3, 300 // B * B + step * i) for i in range(12)], [1, 30, 7, 100], H, Hkv, D, B, dtype, seed=n)
+    want = c.run_checked()
+    for _ in range(20):
+        assert torch.equal(c.run(), want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, **ids)
 @pytest.mark.parametrize("H,Hkv,D,B", [(32, 8, 128, 16), (14, 2, 64, 32), (6, 6, 64, 8)])
 def test_a_key_that_stands_out_is_found(H, Hkv, D, B, dtype):
     """One key after another, at the ends of blocks, tiles and parts, holds nearly all the weight of every row."""
