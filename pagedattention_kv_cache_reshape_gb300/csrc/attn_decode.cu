@@ -182,7 +182,7 @@ __device__ void shared_plan_cta(const SharedGroups &g, const SharedPlan &plan, c
     __shared__ double work[2][kPlanThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool ok = shared_lens<kPlanThreads>(g, starts, lens, status);
-    const int64_t tiles = shared_write_plan<kPlanThreads>(g, plan, ok, starts, lens, scan_tot);
+    const bool any = shared_write_plan<kPlanThreads>(g, plan, ok, starts, lens, scan_tot);
     double dec = 0.0, pre = 0.0;
     for (int s = tid; s < g.num_seqs; s += kPlanThreads) dec += (plan.own_len[s] + kU - 1) / kU;   // (this thread wrote it)
     for (int i = tid; i < g.num_groups; i += kPlanThreads) {
@@ -190,7 +190,7 @@ __device__ void shared_plan_cta(const SharedGroups &g, const SharedPlan &plan, c
         const int n = __ldg(g.starts + i + 1) - __ldg(g.starts + i), pos = g.seqs_per_item / 2;
         const int full = n / g.seqs_per_item, rest = n - full * g.seqs_per_item;
         const double one = rest > 0 && rest <= pos ? 1.0 : 0.0, two = full + (rest > pos ? 1.0 : 0.0);
-        const GroupItems x = group_items(n, lens[i], g.num_kv_heads, g.seqs_per_item, g.keys_per_tile, g.pair_seqs);
+        const GroupItems x = group_items(n, lens[i], g.num_kv_heads, g.seqs_per_item, g.keys_per_tile, g.pair_seqs, 1);
         pre += (x.pair ? split.tile_ns[2] : one * split.tile_ns[0] + two * split.tile_ns[1]) * x.heads * x.kt;
     }
 #pragma unroll
@@ -205,9 +205,11 @@ __device__ void shared_plan_cta(const SharedGroups &g, const SharedPlan &plan, c
         for (int w = 0; w < kPlanThreads / 32; ++w) { dec += work[0][w]; pre += work[1][w]; }
         dec *= split.block_ns;
         int act = split.grid;
-        if (tiles > 0 && split.grid > 1) {
+        if (any && split.grid > 1) {
             act = (int)llrint(split.grid * dec / (dec + pre));
             act = act < 1 ? 1 : (act > split.grid - 1 ? split.grid - 1 : act);
+            const int odd = (split.grid - act) % *plan.width;   // (this thread wrote it) whole teams, if there is one
+            if (split.grid - act > odd) act += odd;
         }
         *split.active = act;
         *split.prefix_shares = min(split.grid - act > 0 ? split.grid - act : split.grid, split.prefix_grid);

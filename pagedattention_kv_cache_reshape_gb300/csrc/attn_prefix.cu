@@ -7,10 +7,12 @@
 // over the group's shared keys, and the result stays (m, l, O) in fp32: the
 // merge kernel joins it with the sequences' own parts.
 //
-// Work: the items' 128-key tiles, one after the other, are one stream
-// (shared_plan.cuh).  Each persistent CTA takes an equal contiguous share, so
-// every CTA has the same number of tiles whatever the group sizes; a share
-// holds a few pieces of items, usually one or two.
+// Work: the items' tiles, one after the other, are a stream (shared_plan.cuh).
+// Each persistent CTA takes an equal contiguous share, so every CTA has the same
+// number of tiles whatever the group sizes; a share holds a few pieces of items,
+// usually one or two.  Items that read the same tiles go to teams of CTAs that
+// read them together: 256 sequences (4 items a kv-head) over 32,768 tokens read
+// 137 MB from HBM instead of 406 MB, and the call takes 149 us instead of 179.
 //
 // Bound: a 64 KB tile (K and V, 128 keys x 128 dims) takes an SM's share of
 // HBM 1.5 us; the products of one M-tile of 128 rows take 0.5 us of the tensor
@@ -166,8 +168,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *drained = item_empty + kItemSlots;   // every product issued has completed
     uint32_t &tmem_base_s = *reinterpret_cast<uint32_t *>(drained + 1);
     Piece *items = reinterpret_cast<Piece *>(drained + 2);           // [kItemSlots]
-    float2 *ml_s = reinterpret_cast<float2 *>(items + kItemSlots);   // [tile][row]
-    static_assert((3 + 2 * kSlots + 10 * kMT + 2 * kItemSlots + 2) * 8 + kItemSlots * sizeof(Piece) +
+    int64_t *range_s = reinterpret_cast<int64_t *>(items + kItemSlots);   // this CTA's shares: begin and end, team's and plain
+    float2 *ml_s = reinterpret_cast<float2 *>(range_s + 4);          // [tile][row]
+    static_assert((3 + 2 * kSlots + 10 * kMT + 2 * kItemSlots + 2) * 8 + kItemSlots * sizeof(Piece) + 32 +
                           kMT * BM * sizeof(float2) <= SH::kBarBytes,
                   "barrier area");
 
@@ -182,16 +185,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the plan is complete.  Shares for fewer CTAs than the grid has: the others
     // leave their SMs (but not before the decode grid is done: what waits for
     // this grid relies on both).
-    const int64_t T = p.plan.tile_start[p.num_groups];   // plain loads: written by the plan grid
-    const int64_t P = min((int64_t)p.shares[0], T), cta = blockIdx.x;   // no share is empty
-    const int64_t t_begin = cta < P ? share_begin(cta, T, P) : 0, t_end = cta < P ? share_begin(cta + 1, T, P) : 0;
+    // Plain loads: written by the plan grid.  Teams of `width` CTAs (as many as there are tiles at most, so that no
+    // share is empty) and their place in one; then every CTA by itself.
+    const int cta = blockIdx.x, width = *p.plan.width, shares = p.shares[0];
+    const int64_t T1 = p.plan.team_start[p.num_groups], P1 = min((int64_t)(shares / width), T1);
+    const int64_t T0 = p.plan.tile_start[p.num_groups], P0 = min((int64_t)shares, T0);
+    const bool in_team = cta / width < P1, alone = cta < P0;
+    const int64_t a1 = in_team ? share_begin(cta / width, T1, P1) : 0, b1 = in_team ? share_begin(cta / width + 1, T1, P1) : 0;
+    const int64_t a0 = alone ? share_begin(cta, T0, P0) : 0, b0 = alone ? share_begin(cta + 1, T0, P0) : 0;
     grid_dependents_launch();    // every decode and prefix CTA runs before the merge's take up room
-    if (t_begin >= t_end) {
+    if (a0 >= b0 && a1 >= b1) {
         grid_dependency_wait();
         return;
     }
 
     if (tid == 0) {
+        range_s[0] = a1;
+        range_s[1] = b1;
+        range_s[2] = a0;
+        range_s[3] = b0;
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         for (int i = 0; i < kSlots; ++i) {
@@ -346,7 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ================= TMA producer
         bool ok = true, stopped = false;
         int n = 0, nq = 0, issued_end = 0;   // issued_end: ring entries issued so far
-        int64_t t_next = t_begin;
+        int64_t t_next = range_s[0];
+        int place = (int)blockIdx.x % *p.plan.width;      // in the team, whose share comes first; -1: on its own
         // the next piece of this CTA's share, published one piece ahead of its use
         auto publish = [&](int it, Piece &I) -> bool {
             bool okp = true;
@@ -355,9 +368,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 okp = false;
             okp = __shfl_sync(kAll, okp ? 1 : 0, 0) != 0;
             I = Piece{};
+            if (place >= 0 && t_next >= range_s[1]) {
+                place = -1;
+                t_next = range_s[2];
+            }
+            const int64_t t_end = range_s[place >= 0 ? 1 : 3];
             if (t_next < t_end) {
                 const int spi = kMT * p.pos;
-                const PrefixItem x = prefix_item(p.plan, p.starts, p.num_groups, p.num_kv_heads, spi, BN, p.pair_seqs, t_next);
+                const PrefixItem x = prefix_item(p.plan, p.starts, p.num_groups, p.num_kv_heads, spi, BN, p.pair_seqs,
+                                                 *p.plan.width, place, t_next);
                 const int i0 = x.part * spi;
                 I.table_seq = x.s0;
                 I.kvh = x.kvh;
@@ -370,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 I.C = x.C;
                 I.live = 1;
                 I.row = x.tile == 0 ? item_row(x.s0, x.n, x.kvh, i0, p.num_heads, p.group)
-                                    : (int64_t)p.num_seqs * p.num_heads + cta * p.item_rows;
+                                    : (int64_t)p.num_seqs * p.num_heads + (2 * (int)blockIdx.x + (place >= 0 ? 1 : 0)) * (int64_t)p.item_rows;
                 t_next += I.nkv;
             }
             if (lane == 0 && okp) {

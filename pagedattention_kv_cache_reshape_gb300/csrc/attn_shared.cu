@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kCcThreads, 2) shared_cc_kernel(const CcParams
     const int64_t t_end = c < P0 ? share_begin(c + 1, T0, P0) : 0;
     const int64_t rows0 = (int64_t)p.num_seqs * p.num_heads;
     while (t < t_end) {
-        const PrefixItem it = prefix_item(p.plan, p.group_starts, p.num_groups, p.num_kv_heads, p.seqs_per_item, kKeys, 0, t);
+        const PrefixItem it = prefix_item(p.plan, p.group_starts, p.num_groups, p.num_kv_heads, p.seqs_per_item, kKeys, 0, 1, -1, t);
         const int tiles = (int)min((int64_t)(it.of.kt - it.tile), t_end - t), i0 = it.part * p.seqs_per_item;
         const int64_t row = it.tile == 0 ? item_row(it.s0, it.n, it.kvh, i0, p.num_heads, G) : rows0 + c * p.item_rows;
         CcPiece w;
@@ -436,12 +436,19 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
     RowPieces pre, own;
     if (mine && C > 0) {
         const int s0 = __ldg(p.group_starts + g), n = __ldg(p.group_starts + g + 1) - s0;
-        const GroupItems x = group_items(n, C, p.num_kv_heads, p.seqs_per_item, p.keys_per_tile, p.pair_seqs);
-        const int part = x.pair ? 0 : (s - s0) / p.seqs_per_item, item = x.pair ? kvh >> 1 : kvh * x.parts + part;
+        const int width = p.plan.width ? *p.plan.width : 1;
+        const GroupItems x = group_items(n, C, p.num_kv_heads, p.seqs_per_item, p.keys_per_tile, p.pair_seqs, width);
+        const int part = x.pair ? 0 : (s - s0) / p.seqs_per_item;
         const int i = x.pair ? (kvh & 1) * n + s - s0 : s - s0 - part * p.seqs_per_item;   // row / G in the item
-        pre = RowPieces(item_row(s0, n, kvh, s - s0, p.num_heads, G) + hh, rows0 + i * G + hh, p.item_rows,
-                        p.plan.tile_start[g] + (int64_t)item * x.kt, x.kt, p.plan.tile_start[p.num_groups],
-                        p.pre_shares_dev ? *p.pre_shares_dev : p.pre_shares);
+        const int64_t first = item_row(s0, n, kvh, s - s0, p.num_heads, G) + hh, P = p.pre_shares_dev ? *p.pre_shares_dev : p.pre_shares;
+        if (part < x.blocks * width)
+            pre = RowPieces(first, rows0 + ((part % width) * 2 + 1) * (int64_t)p.item_rows + i * G + hh, 2 * width * p.item_rows,
+                            p.plan.team_start[g] + (int64_t)(kvh * x.blocks + part / width) * x.kt, x.kt,
+                            p.plan.team_start[p.num_groups], P / width);
+        else
+            pre = RowPieces(first, rows0 + i * G + hh, (p.plan.width ? 2 : 1) * p.item_rows,
+                            p.plan.tile_start[g] + (int64_t)(x.pair ? kvh >> 1 : kvh * x.rest + part - x.blocks * width) * x.kt,
+                            x.kt, p.plan.tile_start[p.num_groups], P);
     }
     if (mine && p.own_start) {
         const int64_t kt = (len + p.keys_per_tile - 1) / p.keys_per_tile;
@@ -537,7 +544,7 @@ cudaError_t launch_typed(const CcParams &cc, const MergeParams &mg, int grid, cu
 
 // Workspace of the tensor-core path: the plan's arrays, the prefix pieces, the own parts, the decode kernel's.
 struct TcLayout {
-    size_t seq_group, own_len, shared_len, tile_start, shares, pre_ml, pre_o, own_ml, own_o, decode, total;
+    size_t seq_group, own_len, shared_len, tile_start, team_start, shares, pre_ml, pre_o, own_ml, own_o, decode, total;
     int item_rows;
 };
 
@@ -553,8 +560,9 @@ TcLayout tc_layout(int num_seqs, int num_groups, int num_heads, int num_kv_heads
     w.own_len = take(4 * S);
     w.shared_len = take(4 * NG);
     w.tile_start = take(8 * (NG + 1));
-    w.shares = take(4);
-    const size_t rows = S * num_heads, pre_rows = rows + (size_t)kMaxPrefixCtas * w.item_rows;
+    w.team_start = take(8 * (NG + 1));
+    w.shares = take(8);   // and the teams' width
+    const size_t rows = S * num_heads, pre_rows = rows + (size_t)2 * kMaxPrefixCtas * w.item_rows;
     w.pre_ml = take(8 * pre_rows);
     w.pre_o = take(4 * pre_rows * head_dim);
     w.own_ml = take(8 * rows);
@@ -578,9 +586,10 @@ cudaError_t launch_tc(const AttnArgs &a, const int32_t *group_starts, const int3
     const int spi = prefix_seqs_per_item(a.num_heads / a.num_kv_heads), pair = a.num_kv_heads % 2 == 0 ? spi / 2 : 0;
     SharedJob job;
     job.groups = {a.context_lens, group_starts, prefix_lens, a.num_seqs, num_groups, a.num_kv_heads, a.block_size,
-                  (int64_t)a.max_blocks * a.block_size, spi, kPrefixKeys, pair};
+                  (int64_t)a.max_blocks * a.block_size, spi, kPrefixKeys, pair, kMaxTeam};
     job.plan = {reinterpret_cast<int32_t *>(ws + w.seq_group), reinterpret_cast<int32_t *>(ws + w.own_len),
-                reinterpret_cast<int32_t *>(ws + w.shared_len), reinterpret_cast<int64_t *>(ws + w.tile_start)};
+                reinterpret_cast<int32_t *>(ws + w.shared_len), reinterpret_cast<int64_t *>(ws + w.tile_start),
+                reinterpret_cast<int64_t *>(ws + w.team_start), reinterpret_cast<int32_t *>(ws + w.shares) + 1};
     job.shares = reinterpret_cast<int32_t *>(ws + w.shares);
     job.pre_o = reinterpret_cast<float *>(ws + w.pre_o);
     job.pre_ml = reinterpret_cast<float2 *>(ws + w.pre_ml);
@@ -611,10 +620,11 @@ cudaError_t launch_shared_prefix(const AttnArgs &a, const int32_t *group_starts,
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const int G = a.num_heads / a.num_kv_heads, spi = kRows / G;
     const SharedPlan plan = {reinterpret_cast<int32_t *>(ws + w.seq_group), reinterpret_cast<int32_t *>(ws + w.own_len),
-                             reinterpret_cast<int32_t *>(ws + w.shared_len), reinterpret_cast<int64_t *>(ws + w.tile_start)};
+                             reinterpret_cast<int32_t *>(ws + w.shared_len), reinterpret_cast<int64_t *>(ws + w.tile_start), nullptr,
+                             nullptr};
     int64_t *own_start = reinterpret_cast<int64_t *>(ws + w.own_start);
     const SharedGroups groups = {a.context_lens, group_starts, prefix_lens, a.num_seqs, num_groups, a.num_kv_heads,
-                                 a.block_size, (int64_t)a.max_blocks * a.block_size, spi, kKeys, 0};
+                                 a.block_size, (int64_t)a.max_blocks * a.block_size, spi, kKeys, 0, 1};
     cudaError_t e = launch_dependent(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, groups, plan,
                                      reinterpret_cast<int32_t *>(ws + w.scratch), own_start, a.status);
     if (e != cudaSuccess) return e;

@@ -11,11 +11,18 @@
 // two neighbouring kv-heads) and their tiles half as many keys.  Items are
 // listed by group, kv-head, sequences.
 //
+// Teams: items of one (g, kv-head) read the same tiles, so `width` of them at a
+// time form a block, and blocks have a stream of their own: teams of `width`
+// CTAs, each CTA with one item of a block, take equal shares of it, so that a
+// tile is read by the whole team at about the same time and comes from HBM
+// once.  Items that fill no block are in the plain stream, cut by CTAs alone.
+//
 // Pieces: a share's tiles of one item.  The piece that begins with the item's
 // first tile is kept in the item's own rows, ordered (group, kv-head, sequence,
-// q-head of the kv-head), num_seqs * num_heads rows in all; any other piece is
-// the first of its share c and is kept in rows num_seqs * num_heads + c *
-// item_rows and on.
+// q-head of the kv-head), num_seqs * num_heads rows in all.  Any other piece is
+// the first of its CTA's share of its stream, and is kept in the CTA's rows for
+// that stream: item_rows rows from num_seqs * num_heads + (c * streams + stream)
+// * item_rows on (stream 0 plain, 1 teams).
 #pragma once
 
 #include <limits.h>
@@ -37,20 +44,25 @@ struct SharedGroups {
     int seqs_per_item;
     int keys_per_tile;
     int pair_seqs;                 // 0: no items of two kv-heads
+    int max_width;                 // of a team; 1: no teams
 };
 
-// A group's items: heads * parts of them, each of kt tiles of `keys` keys.
+// A group's items: heads * parts of them, each of kt tiles of `keys` keys; the
+// first blocks * width parts of a kv-head in the teams' stream, the `rest` in the
+// plain one.
 struct GroupItems {
-    int pair, heads, parts, keys, kt;
+    int pair, heads, parts, keys, kt, blocks, rest;
 };
 __device__ __forceinline__ GroupItems group_items(int n, int C, int num_kv_heads, int seqs_per_item, int keys_per_tile,
-                                                  int pair_seqs) {
+                                                  int pair_seqs, int width) {
     GroupItems x;
     x.pair = n <= pair_seqs;
     x.heads = x.pair ? num_kv_heads >> 1 : num_kv_heads;
     x.parts = x.pair ? 1 : (n + seqs_per_item - 1) / seqs_per_item;
     x.keys = x.pair ? keys_per_tile >> 1 : keys_per_tile;
     x.kt = (C + x.keys - 1) / x.keys;
+    x.blocks = width > 1 ? x.parts / width : 0;
+    x.rest = x.parts - x.blocks * width;
     return x;
 }
 
@@ -59,8 +71,11 @@ struct SharedPlan {
     int32_t *seq_group;    // [num_seqs]
     int32_t *own_len;      // [num_seqs]: tokens behind the shared ones; 0: context length out of range
     int32_t *shared_len;   // [num_groups]: C_g
-    int64_t *tile_start;   // [num_groups + 1]: tiles of all items of the groups before
+    int64_t *tile_start;   // [num_groups + 1]: the plain stream's tiles of the groups before
+    int64_t *team_start;   // [num_groups + 1]: the teams' stream's tiles of the groups before
+    int32_t *width;        // of the teams
 };
+constexpr int kMaxTeam = 4;
 
 // The c-th of p equal shares of n tiles begins here; share that holds tile t.
 __host__ __device__ __forceinline__ int64_t share_begin(int64_t c, int64_t n, int64_t p) { return c * n / p; }
@@ -77,7 +92,8 @@ __device__ __forceinline__ int last_at_most(const V *a, int n, X v) {
     return lo;
 }
 
-// The prefix item at tile t of the stream (t < the stream's end).
+// The prefix item at tile t of a stream (t < the stream's end); lane: the CTA's place in its team, or -1: the plain
+// stream.
 struct PrefixItem {
     int g, C;              // group, its shared tokens
     int s0, n;             // the group's first sequence, its sequences
@@ -87,18 +103,20 @@ struct PrefixItem {
 };
 __device__ __forceinline__ PrefixItem prefix_item(const SharedPlan &plan, const int32_t *starts, int num_groups,
                                                   int num_kv_heads, int seqs_per_item, int keys_per_tile, int pair_seqs,
-                                                  int64_t t) {
+                                                  int width, int lane, int64_t t) {
+    const int64_t *start = lane < 0 ? plan.tile_start : plan.team_start;
     PrefixItem it;
-    it.g = last_at_most(plan.tile_start, num_groups, t);   // (groups without tiles are passed over)
+    it.g = last_at_most(start, num_groups, t);   // (groups without tiles are passed over)
     it.C = plan.shared_len[it.g];
     it.s0 = __ldg(starts + it.g);
     it.n = __ldg(starts + it.g + 1) - it.s0;
-    it.of = group_items(it.n, it.C, num_kv_heads, seqs_per_item, keys_per_tile, pair_seqs);
-    const int64_t local = t - plan.tile_start[it.g];
-    const int item = (int)(local / it.of.kt);
+    it.of = group_items(it.n, it.C, num_kv_heads, seqs_per_item, keys_per_tile, pair_seqs, width);
+    const int64_t local = t - start[it.g];
+    const int item = (int)(local / it.of.kt), per_head = lane < 0 ? it.of.rest : it.of.blocks;
     it.tile = (int)(local - (int64_t)item * it.of.kt);
-    it.kvh = item / it.of.parts;
-    it.part = item - it.kvh * it.of.parts;
+    it.kvh = item / per_head;
+    it.part = item - it.kvh * per_head;
+    it.part = lane < 0 ? it.of.blocks * width + it.part : it.part * width + lane;
     if (it.of.pair) it.kvh *= 2;
     return it;
 }
@@ -176,37 +194,69 @@ __device__ bool shared_lens(const SharedGroups &g, int32_t *starts, int32_t *len
     return ok;
 }
 
-// The plan's arrays from C_g, by a whole CTA.  Returns the tiles of all items.
+// The plan's arrays from C_g, by a whole CTA.  Returns whether any tokens are shared.
 template <int kThreads>
-__device__ int64_t shared_write_plan(const SharedGroups &g, const SharedPlan &plan, bool ok, const int32_t *starts,
-                                     const int32_t *lens, int64_t *warp_tot) {
+__device__ bool shared_write_plan(const SharedGroups &g, const SharedPlan &plan, bool ok, const int32_t *starts,
+                                  const int32_t *lens, int64_t *warp_tot) {
     const int tid = threadIdx.x;
-    int64_t tiles = 0;
+    auto items_of = [&](int i, int width) {
+        return group_items(__ldg(g.starts + i + 1) - __ldg(g.starts + i), lens[i], g.num_kv_heads, g.seqs_per_item,
+                           g.keys_per_tile, g.pair_seqs, width);
+    };
+    // the width that leaves the fewest tiles to be read more than once
+    int width = 1;
+    if (g.max_width > 1) {
+        int64_t saved[kMaxTeam + 1] = {};
+        for (int i = tid; i < g.num_groups; i += kThreads)
+            if (lens[i] > 0)
+                for (int w = 2; w <= kMaxTeam; ++w) {
+                    const GroupItems x = items_of(i, w);
+                    if (w <= g.max_width) saved[w] += (int64_t)x.blocks * (w - 1) * x.heads * x.kt;
+                }
+        int64_t best = 0;
+        for (int w = 2; w <= kMaxTeam; ++w) {
+            int64_t total;
+            block_scan<kThreads>(saved[w], warp_tot, total);
+            if (total > best) { best = total; width = w; }
+        }
+    }
+    int64_t plain = 0, team = 0;
     for (int base = 0; base < g.num_groups; base += kThreads) {
         const int i = base + tid;
-        int64_t mine = 0;
+        int64_t a = 0, b = 0;
         if (i < g.num_groups) {
             const int C = lens[i];
             if (C > 0) {
-                const int n = __ldg(g.starts + i + 1) - __ldg(g.starts + i);
-                const GroupItems x = group_items(n, C, g.num_kv_heads, g.seqs_per_item, g.keys_per_tile, g.pair_seqs);
-                mine = (int64_t)x.heads * x.parts * x.kt;
+                const GroupItems x = items_of(i, width);
+                a = (int64_t)x.heads * x.rest * x.kt;
+                b = (int64_t)x.heads * x.blocks * x.kt;
             }
             plan.shared_len[i] = C;
         }
         int64_t total;
-        const int64_t first = block_scan<kThreads>(mine, warp_tot, total) + tiles;
-        tiles += total;
+        const int64_t first = block_scan<kThreads>(a, warp_tot, total) + plain;
+        plain += total;
         if (i < g.num_groups) plan.tile_start[i] = first;
+        if (g.max_width > 1) {
+            const int64_t first_team = block_scan<kThreads>(b, warp_tot, total) + team;
+            team += total;
+            if (i < g.num_groups) plan.team_start[i] = first_team;
+        }
     }
-    if (tid == 0) plan.tile_start[g.num_groups] = tiles;
+    if (tid == 0) {
+        plan.tile_start[g.num_groups] = plain;
+        if (g.max_width > 1) {
+            plan.team_start[g.num_groups] = team;
+            *plan.width = width;
+        }
+    }
     for (int s = tid; s < g.num_seqs; s += kThreads) {
         const int ctx = __ldg(g.context_lens + s);
         const int grp = ok ? last_at_most(starts, g.num_groups, s) : 0;
         plan.seq_group[s] = grp;
         plan.own_len[s] = ctx > 0 && ctx <= g.max_tokens ? ctx - lens[grp] : 0;
     }
-    return tiles;
+    return plain + team > 0;
 }
 
 }  // namespace pa

@@ -62,6 +62,16 @@ def test_many_sequences_and_groups(S, NG, dtype):
     c.check(out, rows=sorted(set(rng.integers(0, S, 200).tolist()) | {0, S - 1}))
 
 
+@pytest.mark.parametrize("H,Hkv,D,B,groups", [
+    (32, 1, 64, 16, [(17, 800), (3, 320), (9, 640), (60, 480)]),      # 5, 1, 3 and 15 items a kv-head
+    (32, 8, 128, 16, [(64 * 4, 2048), (64, 512), (32, 256)]), (32, 8, 128, 32, [(64 * 2 + 1, 1024), (64 * 3, 640), (2, 64)]),
+    (16, 4, 64, 8, [(64 * 7 + 40, 400)]), (33, 3, 128, 16, [(22 * 2, 320), (22 * 3 + 1, 1600), (22 * 6, 48), (5, 3200)]),
+    (8, 8, 64, 16, [(256 * 4 + 3, 64)])])
+def test_teams(H, Hkv, D, B, groups):
+    """Groups of several items a kv-head, which teams of CTAs share, beside others that fill no team."""
+    Case(groups, [1, 3, 17], H, Hkv, D, B, torch.bfloat16, seed=H + D).run_checked()
+
+
 @pytest.mark.parametrize("dtype", DTYPES, **ids)
 @pytest.mark.parametrize("H,Hkv,D,B,n,step", [(32, 32, 128, 16, 8, 16), (32, 32, 64, 8, 3, 8), (32, 8, 128, 32, 40, 64),
                                               (15, 15, 128, 8, 5, 24), (32, 1, 64, 16, 3, 208), (16, 4, 64, 16, 70, 48)])
