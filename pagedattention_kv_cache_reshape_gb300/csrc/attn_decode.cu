@@ -75,7 +75,8 @@ constexpr int kSmemBudget = 227 * 1024;
 constexpr double kDecodeBytesPerSmNs = 64.0;
 constexpr double kPrefillFlopsPerSmNs = 6600.0;
 // SM-nanoseconds of a tile in the prefix kernel: head_dim 64, 128; 128 keys of one M-tile, of two, 64 keys of two kv-heads
-constexpr double kPrefixTileNs[2][3] = {{700.0, 900.0, 700.0}, {1100.0, 1420.0, 1000.0}};
+constexpr int kPrefixTileNs[2][3] = {{800, 1100, 800}, {1500, 1850, 1450}};
+constexpr int kPrefixItemNs = 3000;   // and of an item's begin and end
 
 struct __align__(16) StreamEntry {
     int32_t seq;
@@ -169,7 +170,9 @@ struct DecodeSplit {
     int causal;
     double block_ns;   // SM-nanoseconds per decode block of all kv-heads
     double pair_ns;    // SM-nanoseconds per causal (query row, key) pair of all heads
-    double tile_ns[3]; // SM-nanoseconds per prefix tile of an item with one M-tile, with two, of two kv-heads
+    // shared prefixes, whole SM-nanoseconds: per decode block; per prefix tile of an item with one M-tile, with two, of
+    // two kv-heads; per item
+    int block_ns32, tile_ns[3], item_ns;
     int32_t *prefix_shares;   // CTAs of the prefix kernel that take a share, of prefix_grid
     int prefix_grid;
 };
@@ -178,37 +181,22 @@ struct DecodeSplit {
 // split between the decode and the prefix kernel by estimated work.
 __device__ void shared_plan_cta(const SharedGroups &g, const SharedPlan &plan, const DecodeSplit &split, int32_t *starts,
                                 int32_t *lens, int32_t *status) {
-    __shared__ int64_t scan_tot[kPlanThreads / 32];
-    __shared__ double work[2][kPlanThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool ok = shared_lens<kPlanThreads>(g, starts, lens, status);
-    const bool any = shared_write_plan<kPlanThreads>(g, plan, ok, starts, lens, scan_tot);
-    double dec = 0.0, pre = 0.0;
-    for (int s = tid; s < g.num_seqs; s += kPlanThreads) dec += (plan.own_len[s] + kU - 1) / kU;   // (this thread wrote it)
-    for (int i = tid; i < g.num_groups; i += kPlanThreads) {
-        if (lens[i] <= 0) continue;
-        const int n = __ldg(g.starts + i + 1) - __ldg(g.starts + i), pos = g.seqs_per_item / 2;
-        const int full = n / g.seqs_per_item, rest = n - full * g.seqs_per_item;
-        const double one = rest > 0 && rest <= pos ? 1.0 : 0.0, two = full + (rest > pos ? 1.0 : 0.0);
-        const GroupItems x = group_items(n, lens[i], g.num_kv_heads, g.seqs_per_item, g.keys_per_tile, g.pair_seqs, 1);
-        pre += (x.pair ? split.tile_ns[2] : one * split.tile_ns[0] + two * split.tile_ns[1]) * x.heads * x.kt;
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        dec += __shfl_xor_sync(0xffffffffu, dec, off);
-        pre += __shfl_xor_sync(0xffffffffu, pre, off);
-    }
-    if (lane == 0) { work[0][warp] = dec; work[1][warp] = pre; }
-    __syncthreads();
-    if (tid == 0) {
-        dec = pre = 0.0;
-        for (int w = 0; w < kPlanThreads / 32; ++w) { dec += work[0][w]; pre += work[1][w]; }
-        dec *= split.block_ns;
+    const int pos = g.seqs_per_item / 2;
+    const PlanSums sum = shared_write_plan<kPlanThreads>(
+        g, plan, ok, starts, lens, [&](int own) { return (int64_t)((own + kU - 1) / kU) * split.block_ns32; },
+        [&](const GroupItems &x) {
+            // parts of two M-tiles, and the last one, of one or two
+            const int two = x.pair ? 0 : x.full + (x.last > pos ? 1 : 0), one = x.parts - two;
+            const int64_t tile = x.pair ? split.tile_ns[2] : (int64_t)one * split.tile_ns[0] + (int64_t)two * split.tile_ns[1];
+            return (tile * x.kt + (int64_t)split.item_ns * x.parts) * x.heads;
+        });
+    if (threadIdx.x == 0) {
         int act = split.grid;
-        if (any && split.grid > 1) {
-            act = (int)llrint(split.grid * dec / (dec + pre));
+        if (sum.prefix > 0 && split.grid > 1) {
+            act = (int)llrintf(split.grid * ((float)sum.own / (float)(sum.own + sum.prefix)));
             act = act < 1 ? 1 : (act > split.grid - 1 ? split.grid - 1 : act);
-            const int odd = (split.grid - act) % *plan.width;   // (this thread wrote it) whole teams, if there is one
+            const int odd = (split.grid - act) % sum.width;   // whole teams, if there is one
             if (split.grid - act > odd) act += odd;
         }
         *split.active = act;
@@ -1364,8 +1352,13 @@ cudaError_t launch_split_decode(const AttnArgs &a, void *workspace, size_t works
     split.share = share_sms ? 1 : 0;
     split.causal = a.causal;
     split.block_ns = (double)kU * a.num_kv_heads * a.head_dim * 2 * 2 / kDecodeBytesPerSmNs;
+    {   // units of few heads are bound by their consumers' latency, not by their bytes
+        const int unit_ns = (int)(kU * L.kvh * a.head_dim * 2 * 2 / kDecodeBytesPerSmNs), least = a.head_dim == 64 ? 450 : 600;
+        split.block_ns32 = L.nhg * (unit_ns > least ? unit_ns : least);
+    }
     split.pair_ns = 4.0 * a.num_heads * a.head_dim / kPrefillFlopsPerSmNs;
     for (int i = 0; i < 3; ++i) split.tile_ns[i] = kPrefixTileNs[a.head_dim == 64 ? 0 : 1][i];
+    split.item_ns = kPrefixItemNs;
     split.prefix_shares = shared ? shared->shares : nullptr;
     split.prefix_grid = prefix_grid();
     int plan_grid = (int)((max_entries + 4 * kPlanThreads - 1) / (4 * kPlanThreads));

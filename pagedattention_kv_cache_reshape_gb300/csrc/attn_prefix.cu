@@ -194,16 +194,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t a1 = in_team ? share_begin(cta / width, T1, P1) : 0, b1 = in_team ? share_begin(cta / width + 1, T1, P1) : 0;
     const int64_t a0 = alone ? share_begin(cta, T0, P0) : 0, b0 = alone ? share_begin(cta + 1, T0, P0) : 0;
     grid_dependents_launch();    // every decode and prefix CTA runs before the merge's take up room
-    if (a0 >= b0 && a1 >= b1) {
-        grid_dependency_wait();
-        return;
-    }
 
     if (tid == 0) {
-        range_s[0] = a1;
-        range_s[1] = b1;
-        range_s[2] = a0;
-        range_s[3] = b0;
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         for (int i = 0; i < kSlots; ++i) {
@@ -229,8 +221,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(drained, 1);
         fence_mbar_init();
     }
+    if (cta >= shares) {         // (the same in every thread)
+        grid_dependency_wait();
+        return;
+    }
     if (warp == kMmaWarp) tmem_alloc(&tmem_base_s, kTmemCols);
     if (warp == kProducerWarp && lane == 0) {
+        range_s[0] = a1;
+        range_s[1] = b1;
+        range_s[2] = a0;
+        range_s[3] = b0;
         prefetch_tmap(&tmap_q);
         prefetch_tmap(&tmap_k);
         prefetch_tmap(&tmap_v);

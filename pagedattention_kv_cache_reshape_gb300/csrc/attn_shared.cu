@@ -36,22 +36,22 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 __global__ void __launch_bounds__(kPlanThreads)
     shared_plan_kernel(const SharedGroups g, const SharedPlan plan, int32_t *scratch, int64_t *own_start, int32_t *status) {
     __shared__ int32_t starts_s[kPlanSmemGroups], lens_s[kPlanSmemGroups];
-    __shared__ int64_t warp_tot[kPlanThreads / 32];
+    __shared__ int64_t tot[1][kPlanThreads / 32];
     const int tid = threadIdx.x;
     grid_dependency_wait();
     grid_dependents_launch();
     const bool in_smem = g.num_groups <= kPlanSmemGroups;
     int32_t *lens = in_smem ? lens_s : scratch;
     const bool ok = shared_lens<kPlanThreads>(g, in_smem ? starts_s : nullptr, lens, status);
-    shared_write_plan<kPlanThreads>(g, plan, ok, in_smem ? starts_s : g.starts, lens, warp_tot);
-    __syncthreads();
+    shared_write_plan<kPlanThreads>(g, plan, ok, in_smem ? starts_s : g.starts, lens, [](int) { return 0; },
+                                    [](const GroupItems &) { return 0; });
     int64_t own = 0;
     for (int base = 0; base < g.num_seqs; base += kPlanThreads) {
-        const int s = base + tid, len = s < g.num_seqs ? plan.own_len[s] : 0;
-        int64_t total;
-        const int64_t first = block_scan<kPlanThreads>((len + g.keys_per_tile - 1) / g.keys_per_tile, warp_tot, total) + own;
-        own += total;
-        if (s < g.num_seqs) own_start[s] = first;
+        const int s = base + tid, len = s < g.num_seqs ? plan.own_len[s] : 0;   // (this thread wrote it)
+        int64_t at[1] = {(len + g.keys_per_tile - 1) / g.keys_per_tile}, total[1];
+        block_scan<kPlanThreads, 1>(at, tot, total);
+        if (s < g.num_seqs) own_start[s] = own + at[0];
+        own += total[0];
     }
     if (tid == 0) own_start[g.num_seqs] = own;
 }
@@ -428,27 +428,33 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
     const bool in = r < (int64_t)p.num_seqs * p.num_heads;
     const int s = in ? (int)(r / p.num_heads) : 0, h = in ? (int)(r - (int64_t)s * p.num_heads) : 0;
     const int len = in ? p.plan.own_len[s] : 0;
-    const int g = in ? p.plan.seq_group[s] : 0, C = p.plan.shared_len[g];
+    const int g = in ? p.plan.seq_group[s] : 0;
+    // all that may be needed, in two round trips
+    const bool teams = p.plan.width != nullptr;
+    const int width = teams ? *p.plan.width : 1;
+    const int64_t P = p.pre_shares_dev ? *p.pre_shares_dev : p.pre_shares;
+    const int64_t T0 = p.plan.tile_start[p.num_groups], T1 = teams ? p.plan.team_start[p.num_groups] : 0;
+    const int C = p.plan.shared_len[g], s0 = __ldg(p.group_starts + g), s1 = __ldg(p.group_starts + g + 1);
+    const int64_t begin0 = p.plan.tile_start[g], begin1 = teams ? p.plan.team_start[g] : 0;
     // a context length out of range leaves its row as it was; without shared tokens the decode kernel wrote it
     const bool mine = len > 0 && (p.own_start || C > 0);
     const int G = p.num_heads / p.num_kv_heads, kvh = h / G, hh = h - kvh * G;
     const int64_t rows0 = (int64_t)p.num_seqs * p.num_heads;
     RowPieces pre, own;
     if (mine && C > 0) {
-        const int s0 = __ldg(p.group_starts + g), n = __ldg(p.group_starts + g + 1) - s0;
-        const int width = p.plan.width ? *p.plan.width : 1;
+        const int n = s1 - s0;
         const GroupItems x = group_items(n, C, p.num_kv_heads, p.seqs_per_item, p.keys_per_tile, p.pair_seqs, width);
         const int part = x.pair ? 0 : (s - s0) / p.seqs_per_item;
         const int i = x.pair ? (kvh & 1) * n + s - s0 : s - s0 - part * p.seqs_per_item;   // row / G in the item
-        const int64_t first = item_row(s0, n, kvh, s - s0, p.num_heads, G) + hh, P = p.pre_shares_dev ? *p.pre_shares_dev : p.pre_shares;
+        const int64_t first = item_row(s0, n, kvh, s - s0, p.num_heads, G) + hh;
         if (part < x.blocks * width)
             pre = RowPieces(first, rows0 + ((part % width) * 2 + 1) * (int64_t)p.item_rows + i * G + hh, 2 * width * p.item_rows,
-                            p.plan.team_start[g] + (int64_t)(kvh * x.blocks + part / width) * x.kt, x.kt,
-                            p.plan.team_start[p.num_groups], P / width);
+                            begin1 + (int64_t)(kvh * x.blocks + part / width) * x.kt, x.kt,
+                            T1, P / width);
         else
-            pre = RowPieces(first, rows0 + i * G + hh, (p.plan.width ? 2 : 1) * p.item_rows,
-                            p.plan.tile_start[g] + (int64_t)(x.pair ? kvh >> 1 : kvh * x.rest + part - x.blocks * width) * x.kt,
-                            x.kt, p.plan.tile_start[p.num_groups], P);
+            pre = RowPieces(first, rows0 + i * G + hh, (teams ? 2 : 1) * p.item_rows,
+                            begin0 + (int64_t)(x.pair ? kvh >> 1 : kvh * x.rest + part - x.blocks * width) * x.kt,
+                            x.kt, T0, P);
     }
     if (mine && p.own_start) {
         const int64_t kt = (len + p.keys_per_tile - 1) / p.keys_per_tile;

@@ -52,6 +52,7 @@ struct SharedGroups {
 // plain one.
 struct GroupItems {
     int pair, heads, parts, keys, kt, blocks, rest;
+    int full, last;   // parts of seqs_per_item sequences, and the sequences of one with fewer (0: none)
 };
 __device__ __forceinline__ GroupItems group_items(int n, int C, int num_kv_heads, int seqs_per_item, int keys_per_tile,
                                                   int pair_seqs, int width) {
@@ -61,6 +62,8 @@ __device__ __forceinline__ GroupItems group_items(int n, int C, int num_kv_heads
     x.parts = x.pair ? 1 : (n + seqs_per_item - 1) / seqs_per_item;
     x.keys = x.pair ? keys_per_tile >> 1 : keys_per_tile;
     x.kt = (C + x.keys - 1) / x.keys;
+    x.full = x.pair ? 0 : n / seqs_per_item;
+    x.last = n - x.full * seqs_per_item;
     x.blocks = width > 1 ? x.parts / width : 0;
     x.rest = x.parts - x.blocks * width;
     return x;
@@ -126,27 +129,36 @@ __device__ __forceinline__ int64_t item_row(int s0, int n, int kvh, int i, int n
     return (int64_t)s0 * num_heads + ((int64_t)kvh * n + i) * group;
 }
 
-// Exclusive scan of v over a CTA of kThreads threads; `total` the sum.
-template <int kThreads>
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *warp_tot, int64_t &total) {
+// Exclusive scans of N values over a CTA of kThreads threads, in place; total[k] their sums.  `tot` holds N * kThreads /
+// 32 values that no thread reads or writes meanwhile.
+template <int kThreads, int N>
+__device__ __forceinline__ void block_scan(int64_t (&v)[N], int64_t (*tot)[kThreads / 32], int64_t (&total)[N]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t incl = v;
+    int64_t incl[N];
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += y;
+    for (int k = 0; k < N; ++k) {
+        incl[k] = v[k];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl[k], off);
+            if (lane >= off) incl[k] += y;
+        }
+        if (lane == 31) tot[k][warp] = incl[k];
     }
-    __syncthreads();   // the previous scan's totals have been read
-    if (lane == 31) warp_tot[warp] = incl;
     __syncthreads();
-    int64_t before = 0;
-    total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-        const int64_t t = warp_tot[w];
-        if (w < warp) before += t;
-        total += t;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        int64_t before = 0;
+        total[k] = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            const int64_t x = tot[k][w];
+            if (w < warp) before += x;
+            total[k] += x;
+        }
+        v[k] = before + incl[k] - v[k];
     }
-    return before + incl - v;
+    __syncthreads();
 }
 
 // C_g of every group into lens[num_groups], by a whole CTA of kThreads threads;
@@ -194,69 +206,76 @@ __device__ bool shared_lens(const SharedGroups &g, int32_t *starts, int32_t *len
     return ok;
 }
 
-// The plan's arrays from C_g, by a whole CTA.  Returns whether any tokens are shared.
-template <int kThreads>
-__device__ bool shared_write_plan(const SharedGroups &g, const SharedPlan &plan, bool ok, const int32_t *starts,
-                                  const int32_t *lens, int64_t *warp_tot) {
+// The plan's arrays from C_g, by a whole CTA.  Returns the costs' sums: own_cost(tokens) of every sequence,
+// item_cost(items) of every group with shared tokens (whole nanoseconds), and the teams' width.
+struct PlanSums {
+    int64_t own, prefix;
+    int width;
+};
+template <int kThreads, typename OwnCost, typename ItemCost>
+__device__ __forceinline__ PlanSums shared_write_plan(const SharedGroups &g, const SharedPlan &plan, bool ok,
+                                                      const int32_t *starts, const int32_t *lens, OwnCost own_cost,
+                                                      ItemCost item_cost) {
+    __shared__ int64_t tot[5][kThreads / 32];
     const int tid = threadIdx.x;
     auto items_of = [&](int i, int width) {
         return group_items(__ldg(g.starts + i + 1) - __ldg(g.starts + i), lens[i], g.num_kv_heads, g.seqs_per_item,
                            g.keys_per_tile, g.pair_seqs, width);
     };
-    // the width that leaves the fewest tiles to be read more than once
-    int width = 1;
-    if (g.max_width > 1) {
-        int64_t saved[kMaxTeam + 1] = {};
-        for (int i = tid; i < g.num_groups; i += kThreads)
-            if (lens[i] > 0)
-                for (int w = 2; w <= kMaxTeam; ++w) {
-                    const GroupItems x = items_of(i, w);
-                    if (w <= g.max_width) saved[w] += (int64_t)x.blocks * (w - 1) * x.heads * x.kt;
-                }
-        int64_t best = 0;
-        for (int w = 2; w <= kMaxTeam; ++w) {
-            int64_t total;
-            block_scan<kThreads>(saved[w], warp_tot, total);
-            if (total > best) { best = total; width = w; }
-        }
-    }
-    int64_t plain = 0, team = 0;
-    for (int base = 0; base < g.num_groups; base += kThreads) {
-        const int i = base + tid;
-        int64_t a = 0, b = 0;
-        if (i < g.num_groups) {
-            const int C = lens[i];
-            if (C > 0) {
-                const GroupItems x = items_of(i, width);
-                a = (int64_t)x.heads * x.rest * x.kt;
-                b = (int64_t)x.heads * x.blocks * x.kt;
-            }
-            plan.shared_len[i] = C;
-        }
-        int64_t total;
-        const int64_t first = block_scan<kThreads>(a, warp_tot, total) + plain;
-        plain += total;
-        if (i < g.num_groups) plan.tile_start[i] = first;
-        if (g.max_width > 1) {
-            const int64_t first_team = block_scan<kThreads>(b, warp_tot, total) + team;
-            team += total;
-            if (i < g.num_groups) plan.team_start[i] = first_team;
-        }
-    }
-    if (tid == 0) {
-        plan.tile_start[g.num_groups] = plain;
-        if (g.max_width > 1) {
-            plan.team_start[g.num_groups] = team;
-            *plan.width = width;
-        }
-    }
+    // costs, and the tiles that teams of 2, 3 and 4 leave to be read once only
+    int64_t sum[5] = {}, total[5];
     for (int s = tid; s < g.num_seqs; s += kThreads) {
         const int ctx = __ldg(g.context_lens + s);
         const int grp = ok ? last_at_most(starts, g.num_groups, s) : 0;
+        const int own = ctx > 0 && ctx <= g.max_tokens ? ctx - lens[grp] : 0;
         plan.seq_group[s] = grp;
-        plan.own_len[s] = ctx > 0 && ctx <= g.max_tokens ? ctx - lens[grp] : 0;
+        plan.own_len[s] = own;
+        sum[0] += own_cost(own);
     }
-    return plain + team > 0;
+    for (int i = tid; i < g.num_groups; i += kThreads)
+        if (lens[i] > 0) {
+            const GroupItems x = items_of(i, 1);
+            sum[1] += item_cost(x);
+#pragma unroll
+            for (int w = 2; w <= kMaxTeam; ++w)
+                if (w <= g.max_width) sum[w] += (int64_t)(x.parts / w) * (w - 1) * x.heads * x.kt;
+        }
+    block_scan<kThreads, 5>(sum, tot, total);
+    PlanSums r = {total[0], total[1], 1};
+    int64_t best = 0;
+#pragma unroll
+    for (int w = 2; w <= kMaxTeam; ++w)
+        if (total[w] > best) { best = total[w]; r.width = w; }
+    // where each group's items begin
+    int64_t before[2] = {};
+    for (int base = 0; base < g.num_groups; base += kThreads) {
+        const int i = base + tid;
+        int64_t at[2] = {}, all[2];
+        if (i < g.num_groups) {
+            const int C = lens[i];
+            if (C > 0) {
+                const GroupItems x = items_of(i, r.width);
+                at[0] = (int64_t)x.heads * x.rest * x.kt;
+                at[1] = (int64_t)x.heads * x.blocks * x.kt;
+            }
+            plan.shared_len[i] = C;
+        }
+        block_scan<kThreads, 2>(at, tot, all);
+        if (i < g.num_groups) {
+            plan.tile_start[i] = before[0] + at[0];
+            if (plan.team_start) plan.team_start[i] = before[1] + at[1];
+        }
+        before[0] += all[0];
+        before[1] += all[1];
+    }
+    if (tid == 0) {
+        plan.tile_start[g.num_groups] = before[0];
+        if (plan.team_start) {
+            plan.team_start[g.num_groups] = before[1];
+            *plan.width = r.width;
+        }
+    }
+    return r;
 }
 
 }  // namespace pa
