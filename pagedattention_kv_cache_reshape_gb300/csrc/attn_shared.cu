@@ -355,6 +355,7 @@ struct MergeParams {
 
 constexpr int kMergeThreads = 128;
 constexpr int64_t kFewRows = 5000;
+constexpr int kRowsPerWarp = 4;
 
 // The running (M, L, acc) of one row; lane: D / 32 consecutive dims.
 template <int D> struct RowSum {
@@ -382,51 +383,38 @@ __device__ __forceinline__ void load_dims(const float *src, float (&v)[D / 32]) 
 
 // Where one row's pieces of a stream lie: the first in row `first`, the others in rows other, other + step, ...
 struct RowPieces {
-    int64_t first = 0, other = 0, step = 0;
-    int n = 0;
+    int first = 0, other = 0, step = 0, n = 0;   // (rows are counted in 31 bits)
     // tiles [t0, t0 + n) of a stream of T tiles in at most P shares; share c's rows begin at extra + c * rows
-    __device__ __forceinline__ RowPieces(int64_t row0, int64_t extra, int rows, int64_t t0, int64_t count, int64_t T, int64_t P) {
+    __device__ __forceinline__ RowPieces(int row0, int extra, int rows, int64_t t0, int64_t count, int64_t T, int64_t P) {
         P = min(P, T);
         const int64_t c0 = share_of(t0, T, P), c1 = share_of(t0 + count - 1, T, P);
         first = row0;
-        other = extra + (c0 + 1) * rows;
+        other = extra + ((int)c0 + 1) * rows;
         step = rows;
         n = (int)(c1 - c0 + 1);
     }
     __device__ __forceinline__ RowPieces() {}
-    __device__ __forceinline__ int64_t at(int i) const { return i == 0 ? first : other + (i - 1) * step; }
+    __device__ __forceinline__ RowPieces of_lane(int l) const {
+        RowPieces x;
+        x.first = __shfl_sync(0xffffffffu, first, l);
+        x.other = __shfl_sync(0xffffffffu, other, l);
+        x.step = __shfl_sync(0xffffffffu, step, l);
+        x.n = __shfl_sync(0xffffffffu, n, l);
+        return x;
+    }
+    __device__ __forceinline__ int at(int i) const { return i == 0 ? first : other + (i - 1) * step; }
 };
 
-// Pieces w, w + W, ... of a row, in order; the loads of kBatch of them in flight at a time.
-template <int D, int W>
-__device__ __forceinline__ void add_pieces(RowSum<D> &sum, const float *o, const float2 *ml, const RowPieces &x, int w) {
-    constexpr int kBatch = 8;
-    const int lane = threadIdx.x & 31;
-    for (int i = w; i < x.n; i += W * kBatch) {
-        float2 a[kBatch];
-        float v[kBatch][D / 32];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            if (i + W * k < x.n) {
-                const int64_t at = x.at(i + W * k);
-                a[k] = __ldcg(ml + at);
-                load_dims<D>(o + at * D + lane * (D / 32), v[k]);
-            }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            if (i + W * k < x.n) sum.add(a[k], v[k]);
-    }
-}
-
-// W warps a row.  What a row's pieces are is found before the wait for the kernel in front: the plan was complete
-// before that kernel began.
-template <typename T, int D, int W>
+// R rows a warp or W warps a row (one of them is 1).  Lane l finds what the pieces of row l % R are, before the wait for
+// the kernel in front (the plan was complete before that kernel began); the loads of kBatch pieces of every row are then
+// in flight at a time, the groups' pieces first, the sequence's own behind them.
+template <typename T, int D, int W, int R>
 __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const MergeParams p) {
-    constexpr int kPer = D / 32, kRowsPerCta = kMergeThreads / 32 / W;
+    constexpr int kPer = D / 32, kRowsPerCta = kMergeThreads / 32 / W * R, kBatch = R > 1 ? 3 : 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % W;
-    const int64_t r = (int64_t)blockIdx.x * kRowsPerCta + warp / W;
-    const bool in = r < (int64_t)p.num_seqs * p.num_heads;
-    const int s = in ? (int)(r / p.num_heads) : 0, h = in ? (int)(r - (int64_t)s * p.num_heads) : 0;
+    const int row0 = blockIdx.x * kRowsPerCta + warp / W * R, r = row0 + lane % R;   // (rows are counted in 31 bits)
+    const bool in = r < p.num_seqs * p.num_heads;
+    const int s = in ? r / p.num_heads : 0, h = in ? r - s * p.num_heads : 0;
     const int len = in ? p.plan.own_len[s] : 0;
     const int g = in ? p.plan.seq_group[s] : 0;
     // all that may be needed, in two round trips
@@ -439,16 +427,16 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
     // a context length out of range leaves its row as it was; without shared tokens the decode kernel wrote it
     const bool mine = len > 0 && (p.own_start || C > 0);
     const int G = p.num_heads / p.num_kv_heads, kvh = h / G, hh = h - kvh * G;
-    const int64_t rows0 = (int64_t)p.num_seqs * p.num_heads;
-    RowPieces pre, own;
+    const int rows0 = p.num_seqs * p.num_heads;
+    RowPieces pre, own;   // (of the lane's row)
     if (mine && C > 0) {
         const int n = s1 - s0;
         const GroupItems x = group_items(n, C, p.num_kv_heads, p.seqs_per_item, p.keys_per_tile, p.pair_seqs, width);
         const int part = x.pair ? 0 : (s - s0) / p.seqs_per_item;
         const int i = x.pair ? (kvh & 1) * n + s - s0 : s - s0 - part * p.seqs_per_item;   // row / G in the item
-        const int64_t first = item_row(s0, n, kvh, s - s0, p.num_heads, G) + hh;
+        const int first = (int)item_row(s0, n, kvh, s - s0, p.num_heads, G) + hh;
         if (part < x.blocks * width)
-            pre = RowPieces(first, rows0 + ((part % width) * 2 + 1) * (int64_t)p.item_rows + i * G + hh, 2 * width * p.item_rows,
+            pre = RowPieces(first, rows0 + ((part % width) * 2 + 1) * p.item_rows + i * G + hh, 2 * width * p.item_rows,
                             begin1 + (int64_t)(kvh * x.blocks + part / width) * x.kt, x.kt,
                             T1, P / width);
         else
@@ -466,35 +454,63 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
     }
     grid_dependency_wait();
     grid_dependents_launch();
-    RowSum<D> sum;
-    add_pieces<D, W>(sum, p.pre_o, p.pre_ml, pre, w);
-    add_pieces<D, W>(sum, p.own_o, p.own_ml, own, (w + W - pre.n % W) % W);   // on from the warp behind the last
-    if (W > 1) {
-        __shared__ float2 ml_s[kRowsPerCta][W];
-        __shared__ float o_s[kRowsPerCta][W][D];
-        if (lane == 0) ml_s[warp / W][w] = make_float2(sum.M, sum.L);
+    RowSum<D> sum[R];
+    RowPieces a[R], b[R];   // every row's, in all lanes
+    int most = 0;
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) o_s[warp / W][w][lane * kPer + u] = sum.acc[u];
+    for (int q = 0; q < R; ++q) {
+        a[q] = pre.of_lane(q);
+        b[q] = own.of_lane(q);
+        most = max(most, a[q].n + b[q].n);
+    }
+    for (int i = w; i < most; i += W * kBatch) {
+        float2 ml[R][kBatch];
+        float v[R][kBatch][kPer];
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int x = i + W * k, y = x - a[q].n;
+                if (y >= b[q].n) continue;
+                const int64_t at = y < 0 ? a[q].at(x) : b[q].at(y);   // (times D below)
+                ml[q][k] = __ldcg((y < 0 ? p.pre_ml : p.own_ml) + at);
+                load_dims<D>((y < 0 ? p.pre_o : p.own_o) + at * D + lane * kPer, v[q][k]);
+            }
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (i + W * k < a[q].n + b[q].n) sum[q].add(ml[q][k], v[q][k]);
+    }
+    if (W > 1) {
+        __shared__ float2 ml_s[W];
+        __shared__ float o_s[W][D];
+        if (lane == 0) ml_s[w] = make_float2(sum[0].M, sum[0].L);
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) o_s[w][lane * kPer + u] = sum[0].acc[u];
         __syncthreads();
         if (w > 0) return;
 #pragma unroll
         for (int i = 1; i < W; ++i) {
             float v[kPer];
 #pragma unroll
-            for (int u = 0; u < kPer; ++u) v[u] = o_s[warp / W][i][lane * kPer + u];
-            sum.add(ml_s[warp / W][i], v);
+            for (int u = 0; u < kPer; ++u) v[u] = o_s[i][lane * kPer + u];
+            sum[0].add(ml_s[i], v);
         }
     }
-    if (!mine) return;
-    T *dst = static_cast<T *>(p.out) + r * D + lane * kPer;
-    const float inv = 1.f / sum.L;
-    if (sizeof(T) == 2 && p.out_aligned) {
 #pragma unroll
-        for (int u = 0; u < kPer; u += 2)
-            *reinterpret_cast<uint32_t *>(dst + u) = pack_bf16x2(sum.acc[u] * inv, sum.acc[u + 1] * inv);
-    } else {
+    for (int q = 0; q < R; ++q) {
+        if (a[q].n + b[q].n == 0) continue;   // not this kernel's row
+        T *dst = static_cast<T *>(p.out) + (int64_t)(row0 + q) * D + lane * kPer;
+        const float inv = 1.f / sum[q].L;
+        if (sizeof(T) == 2 && p.out_aligned) {
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) dst[u] = from_float<T>(sum.acc[u] * inv);
+            for (int u = 0; u < kPer; u += 2)
+                *reinterpret_cast<uint32_t *>(dst + u) = pack_bf16x2(sum[q].acc[u] * inv, sum[q].acc[u + 1] * inv);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) dst[u] = from_float<T>(sum[q].acc[u] * inv);
+        }
     }
 }
 
@@ -530,11 +546,12 @@ cudaError_t launch_merge(const MergeParams &mg, cudaStream_t stream) {
     // A row has about P / items pieces and an item at most 256 rows, so with few rows there may be many pieces each:
     // then four warps share them.
     const int64_t rows = (int64_t)mg.num_seqs * mg.num_heads;
-    constexpr int kWarps = kMergeThreads / 32;
+    // Else four rows a warp, so that they all are resident at once.
+    constexpr int kWarps = kMergeThreads / 32, kCta = kWarps * kRowsPerWarp;
     if (rows < kFewRows)
-        return launch_dependent(shared_merge_kernel<T, D, kWarps>, dim3((unsigned)rows), dim3(kMergeThreads), 0, stream, mg);
-    return launch_dependent(shared_merge_kernel<T, D, 1>, dim3((unsigned)((rows + kWarps - 1) / kWarps)), dim3(kMergeThreads),
-                            0, stream, mg);
+        return launch_dependent(shared_merge_kernel<T, D, kWarps, 1>, dim3((unsigned)rows), dim3(kMergeThreads), 0, stream, mg);
+    return launch_dependent(shared_merge_kernel<T, D, 1, kRowsPerWarp>, dim3((unsigned)((rows + kCta - 1) / kCta)),
+                            dim3(kMergeThreads), 0, stream, mg);
 }
 
 template <typename T, int D>
