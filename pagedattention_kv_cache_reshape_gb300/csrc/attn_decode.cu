@@ -77,6 +77,7 @@ constexpr double kPrefillFlopsPerSmNs = 6600.0;
 // SM-nanoseconds of a tile in the prefix kernel: head_dim 64, 128; 128 keys of one M-tile, of two, 64 keys of two kv-heads
 constexpr int kPrefixTileNs[2][3] = {{800, 1100, 800}, {1500, 1850, 1450}};
 constexpr int kPrefixItemNs = 3000;   // and of an item's begin and end
+constexpr int kUnitsPerCta = 4;
 
 struct __align__(16) StreamEntry {
     int32_t seq;
@@ -194,7 +195,12 @@ __device__ void shared_plan_cta(const SharedGroups &g, const SharedPlan &plan, c
     if (threadIdx.x == 0) {
         int act = split.grid;
         if (sum.prefix > 0 && split.grid > 1) {
-            act = (int)llrintf(split.grid * ((float)sum.own / (float)(sum.own + sum.prefix)));
+            // rounded, and down where few CTAs are left to the prefix kernel: one too few there would make it the longer
+            const float x = split.grid * ((float)sum.own / (float)(sum.own + sum.prefix));
+            act = x > split.grid - 8 ? (int)x : (int)llrintf(x);
+            // a CTA for every few units at most: joining a cut sequence costs more than they do
+            const int64_t few = (sum.own / split.block_ns32 + kUnitsPerCta - 1) / kUnitsPerCta;
+            if (act > few) act = (int)few;
             act = act < 1 ? 1 : (act > split.grid - 1 ? split.grid - 1 : act);
             const int odd = (split.grid - act) % sum.width;   // whole teams, if there is one
             if (split.grid - act > odd) act += odd;
