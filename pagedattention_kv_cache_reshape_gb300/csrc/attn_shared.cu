@@ -11,8 +11,9 @@
 // sequence's own rows).
 //
 // shared_plan_kernel   C_c, and the two streams of key tiles
-// shared_cc_kernel     CUDA-core products, any dtype (fp32 in and out of them):
-//                      each persistent CTA takes an equal share of both streams
+// shared_rows_kernel, shared_few_kernel  CUDA-core products, any dtype (fp32 in and
+//                      out of them): each persistent CTA takes equal shares of the
+//                      groups' and the sequences' key tiles
 // shared_merge_kernel  one warp or four a row: the row's pieces in a fixed order
 #include <math.h>
 
@@ -60,6 +61,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 constexpr int kRows = 64;     // rows of an item at most
 constexpr int kKeys = 64;     // keys of a tile
 constexpr int kCcThreads = 256;
+constexpr int kFewHeads = 8;
 
 struct CcParams {
     const void *q;
@@ -80,6 +82,7 @@ struct CcParams {
     int num_heads;
     int num_kv_heads;
     int block_size;
+    int log2b;
     int max_blocks;
     int num_blocks;
     int aligned;       // pools and q on 16 bytes
@@ -112,16 +115,17 @@ __device__ __forceinline__ void load_floats(const T *p, bool aligned, float (&x)
     for (int i = 0; i < n; ++i) x[i] = to_float(r.v[i]);
 }
 
-// Shared memory: Q [kRows][D] | K [kKeys][D + 4], whose place the weights [kRows][kKeys + 4] take | V [kKeys][D].
-template <int D> constexpr int cc_smem_floats() { return kRows * D + kKeys * (D + 4) + kKeys * D; }
+// Shared memory: Q [kRows][D + 4] | K [kKeys][D + 4], whose place the weights [kRows][kKeys + 4] take | V [kKeys][D].
+// (Rows of D + 4: the two rows of a warp's half warps, and the keys of its lanes, lie in different banks.)
+template <int D> constexpr int cc_smem_floats() { return kRows * (D + 4) + kKeys * (D + 4) + kKeys * D; }
 
 // Thread (ty, tx) of 16 x 16 holds logits of rows ty * RT + i and keys tx + 16 j, and of the outputs the same rows and
 // dims 4 tx + 64 j + (0..3).  A row's 16 threads are half a warp.  RT = 1, 2 or 4: 16, 32 or 64 rows.
 template <typename T, int D, int RT>
-__device__ void cc_piece(const CcParams &p, const CcPiece &w, float *smem) {
+__device__ __forceinline__ void cc_piece(const CcParams &p, const CcPiece &w, float *smem) {
     constexpr int kVec = 16 / sizeof(T), kKS = D + 4, kPS = kKeys + 4, kDJ = D / 64;
     static_assert(kRows * kPS <= kKeys * kKS, "the weights fit the keys' place");
-    float *qs = smem, *ks = qs + kRows * D, *ps = ks, *vs = ks + kKeys * kKS;
+    float *qs = smem, *ks = qs + kRows * kKS, *ps = ks, *vs = ks + kKeys * kKS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ty = tid >> 4, tx = tid & 15;
     const int G = p.num_heads / p.num_kv_heads;
     const bool al = p.aligned != 0;
@@ -132,15 +136,16 @@ __device__ void cc_piece(const CcParams &p, const CcPiece &w, float *smem) {
             load_floats(static_cast<const T *>(p.q) +
                             ((int64_t)(w.s0 + r / G) * p.num_heads + w.kvh * G + r % G) * D + d, al, x);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) qs[r * D + d + i] = x[i];
+        for (int i = 0; i < kVec; ++i) qs[r * kKS + d + i] = x[i];
     }
-    float m[RT], l[RT], o[RT][kDJ][4];
+    float m[RT], l[RT];
+    float2 o[RT][kDJ][2];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < kDJ; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
+        for (int j = 0; j < kDJ; ++j) o[i][j][0] = o[i][j][1] = make_float2(0.f, 0.f);
     }
     const int64_t tok_stride = (int64_t)p.num_kv_heads * D;
     for (int key = w.key0; key < w.key1; key += kKeys) {
@@ -176,7 +181,7 @@ __device__ void cc_piece(const CcParams &p, const CcPiece &w, float *smem) {
         for (int d = 0; d < D; d += 4) {
             float4 a[RT], b[4];
 #pragma unroll
-            for (int i = 0; i < RT; ++i) a[i] = *reinterpret_cast<const float4 *>(qs + (ty * RT + i) * D + d);
+            for (int i = 0; i < RT; ++i) a[i] = *reinterpret_cast<const float4 *>(qs + (ty * RT + i) * kKS + d);
 #pragma unroll
             for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(ks + (tx + 16 * j) * kKS + d);
 #pragma unroll
@@ -217,7 +222,7 @@ __device__ void cc_piece(const CcParams &p, const CcPiece &w, float *smem) {
 #pragma unroll
             for (int j = 0; j < kDJ; ++j)
 #pragma unroll
-                for (int u = 0; u < 4; ++u) o[i][j][u] *= alpha;
+                for (int u = 0; u < 2; ++u) o[i][j][u] = make_float2(o[i][j][u].x * alpha, o[i][j][u].y * alpha);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 x[i][j] = fast_exp2(x[i][j] - ref);
@@ -243,10 +248,8 @@ __device__ void cc_piece(const CcParams &p, const CcPiece &w, float *smem) {
 #pragma unroll
                     for (int i = 0; i < RT; ++i) {
                         const float c = u == 0 ? a[i].x : u == 1 ? a[i].y : u == 2 ? a[i].z : a[i].w;
-                        o[i][j][0] = fmaf(c, b.x, o[i][j][0]);
-                        o[i][j][1] = fmaf(c, b.y, o[i][j][1]);
-                        o[i][j][2] = fmaf(c, b.z, o[i][j][2]);
-                        o[i][j][3] = fmaf(c, b.w, o[i][j][3]);
+                        o[i][j][0] = fma_f32x2(make_float2(c, c), make_float2(b.x, b.y), o[i][j][0]);
+                        o[i][j][1] = fma_f32x2(make_float2(c, c), make_float2(b.z, b.w), o[i][j][1]);
                     }
                 }
         }
@@ -262,30 +265,213 @@ __device__ void cc_piece(const CcParams &p, const CcPiece &w, float *smem) {
 #pragma unroll
         for (int j = 0; j < kDJ; ++j)
             *reinterpret_cast<float4 *>(w.o + (int64_t)r * D + 4 * tx + 64 * j) =
-                make_float4(o[i][j][0], o[i][j][1], o[i][j][2], o[i][j][3]);
+                make_float4(o[i][j][0].x, o[i][j][0].y, o[i][j][1].x, o[i][j][1].y);
         if (tx == 0) w.ml[r] = make_float2(m[i], sum);
     }
 }
 
-template <typename T, int D>
-__device__ __forceinline__ void cc_any_rows(const CcParams &p, const CcPiece &w, float *smem) {
-    if (w.rows <= 16) cc_piece<T, D, 1>(p, w, smem);
-    else if (w.rows <= 32) cc_piece<T, D, 2>(p, w, smem);
-    else cc_piece<T, D, 4>(p, w, smem);
+// Four neighbouring elements as floats.
+template <typename T>
+__device__ __forceinline__ float4 load_four(const T *p, bool aligned) {
+    if constexpr (sizeof(T) == 4) {
+        if (aligned) return __ldg(reinterpret_cast<const float4 *>(p));
+    } else {
+        if (aligned) {
+            const uint2 r = __ldg(reinterpret_cast<const uint2 *>(p));
+            return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
+                               __uint_as_float(r.y & 0xffff0000u));
+        }
+    }
+    return make_float4(to_float(p[0]), to_float(p[1]), to_float(p[2]), to_float(p[3]));
 }
 
+// Up to R = 1, 2, 4 or 8 rows: bound by the cache's bytes, which go straight to registers.  L lanes take a key, each
+// the same dims of its K and V rows, of the queries and of the outputs: 4 (i L + lane) + (0..3), so that the L lanes'
+// loads are contiguous.  Every group of L lanes is a stream of its own with its running maximum and sums; the streams
+// of the CTA are joined at the end of the piece.  A warp takes every eighth chunk of 8 keys (which lie in one block), 32 / L
+// keys a step, and requests a step's rows two steps ahead.  A stream moves its maximum only when a logit exceeds it by
+// more than 2^8 (its weights stay below that).
+template <typename T, int D, int R>
+__device__ __forceinline__ void cc_few(const CcParams &p, const CcPiece &w, float *smem) {
+    constexpr int L = (R > 4 ? R : 4) * D / 32, kV = D / 4 / L, kWarps = kCcThreads / 32, kSlots = 32 / L;
+    constexpr int kStreams = kWarps * kSlots, kSteps = 8 / kSlots;
+    static_assert(kSteps >= 2, "rows are requested two steps ahead");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, slot = lane / L, li = lane % L;
+    const int G = p.num_heads / p.num_kv_heads, log2b = p.log2b;
+    const bool al = p.aligned != 0;
+    const int tok_stride = p.num_kv_heads * D;
+    const T *kc = static_cast<const T *>(p.k_cache) + (int64_t)w.kvh * D + 4 * li + (int64_t)slot * tok_stride;
+    const T *vc = static_cast<const T *>(p.v_cache) + (int64_t)w.kvh * D + 4 * li + (int64_t)slot * tok_stride;
+    const int n = w.key1 - w.key0, chunks = (n + 7) >> 3;
+    auto block_of = [&](int c) {   // of chunk c; -1: none
+        if (c >= chunks) return -1;
+        const int blk = __ldg(w.table + ((w.key0 + 8 * c) >> log2b));
+        if (blk >= 0 && blk < p.num_blocks) return blk;
+        set_status(p.status, PA_ERR_OUT_OF_RANGE);
+        return -1;
+    };
+    float4 k[2][kV], v[2][kV];
+    bool seen[2];
+    auto request = [&](int b, int c, int blk, int step) {
+        seen[b] = blk >= 0 && 8 * c + step * kSlots + slot < n;
+        if (!seen[b]) return;
+        const int64_t at = (((int64_t)blk << log2b) + ((w.key0 + 8 * c) & ((1 << log2b) - 1)) + step * kSlots) * tok_stride;
+#pragma unroll
+        for (int u = 0; u < kV; ++u) {
+            k[b][u] = load_four(kc + at + 4 * L * u, al);
+            v[b][u] = load_four(vc + at + 4 * L * u, al);
+        }
+    };
+    float4 q[R][kV], o[R][kV];
+    float m[R], l[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int u = 0; u < kV; ++u) {
+            o[r][u] = q[r][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < w.rows)
+                q[r][u] = load_four(static_cast<const T *>(p.q) +
+                                        ((int64_t)(w.s0 + r / G) * p.num_heads + w.kvh * G + r % G) * D + 4 * (L * u + li), al);
+        }
+    }
+    int blk = block_of(warp), blk1 = block_of(warp + kWarps);
+    request(0, warp, blk, 0);
+    request(1, warp, blk, 1);
+    for (int c = warp; c < chunks; c += kWarps) {
+        const int blk2 = block_of(c + 2 * kWarps);
+#pragma unroll
+        for (int step = 0; step < kSteps; ++step) {
+            const int b = step & 1;
+            const bool here = seen[b];
+            float x[R];
+            bool grow = false;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float2 y = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int u = 0; u < kV; ++u) {
+                    y = fma_f32x2(make_float2(q[r][u].x, q[r][u].y), make_float2(k[b][u].x, k[b][u].y), y);
+                    y = fma_f32x2(make_float2(q[r][u].z, q[r][u].w), make_float2(k[b][u].z, k[b][u].w), y);
+                }
+                x[r] = y.x + y.y;
+#pragma unroll
+                for (int off = L / 2; off > 0; off >>= 1) x[r] += __shfl_xor_sync(0xffffffffu, x[r], off);
+                x[r] *= p.scale_log2;
+                grow = grow || (here && x[r] > m[r] + 8.f);
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const bool up = here && x[r] > m[r] + 8.f;
+                    const float alpha = up ? fast_exp2(m[r] - x[r]) : 1.f;
+                    if (up) m[r] = x[r];
+                    l[r] *= alpha;
+#pragma unroll
+                    for (int u = 0; u < kV; ++u)
+                        o[r][u] = make_float4(o[r][u].x * alpha, o[r][u].y * alpha, o[r][u].z * alpha, o[r][u].w * alpha);
+                }
+            }
+            if (here) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    // (a maximum of -inf: the logit is -inf too, weight 0, or NaN)
+                    const float e = fast_exp2(x[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+                    l[r] += e;
+#pragma unroll
+                    for (int u = 0; u < kV; ++u) {
+                        const float2 f = fma_f32x2(make_float2(e, e), make_float2(v[b][u].x, v[b][u].y), make_float2(o[r][u].x, o[r][u].y));
+                        const float2 g = fma_f32x2(make_float2(e, e), make_float2(v[b][u].z, v[b][u].w), make_float2(o[r][u].z, o[r][u].w));
+                        o[r][u] = make_float4(f.x, f.y, g.x, g.y);
+                    }
+                }
+            }
+            if (step + 2 < kSteps) request(b, c, blk, step + 2);
+            else request(b, c + kWarps, blk1, step + 2 - kSteps);
+        }
+        blk = blk1;
+        blk1 = blk2;
+    }
+    // the streams joined: [stream][R][D] and their (m, l)
+    float *os = smem;
+    float2 *mls = reinterpret_cast<float2 *>(smem + kStreams * R * D);
+    const int stream = warp * kSlots + slot;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int u = 0; u < kV; ++u) *reinterpret_cast<float4 *>(os + (stream * R + r) * D + 4 * (L * u + li)) = o[r][u];
+        if (li == 0) mls[stream * R + r] = make_float2(m[r], l[r]);
+    }
+    __syncthreads();
+    for (int e = tid; e < w.rows * (D / 4); e += kCcThreads) {
+        const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+        for (int s = 0; s < kStreams; ++s) top = fmaxf(top, mls[s * R + r].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int s = 0; s < kStreams; ++s) {
+            const float2 ml = mls[s * R + r];
+            if (ml.y == 0.f) continue;   // nothing seen (a NaN stays)
+            const float f = fast_exp2(ml.x - ref);
+            const float4 y = *reinterpret_cast<const float4 *>(os + (s * R + r) * D + d);
+            sum += ml.y * f;
+            acc = make_float4(acc.x + y.x * f, acc.y + y.y * f, acc.z + y.z * f, acc.w + y.w * f);
+        }
+        *reinterpret_cast<float4 *>(w.o + (int64_t)r * D + d) = acc;
+        if (d == 0) w.ml[r] = make_float2(top, sum);
+    }
+    __syncthreads();   // the streams have been read
+}
+
+// A CTA's share of the sequences' own parts: by sequence, then kv-head.
+template <typename Piece>
+__device__ __forceinline__ void own_share(const CcParams &p, int D, Piece piece) {
+    const int G = p.num_heads / p.num_kv_heads;
+    const int64_t T1 = p.own_start[p.num_seqs] * p.num_kv_heads, P1 = min((int64_t)gridDim.x, T1), c = blockIdx.x;
+    const int64_t rows0 = (int64_t)p.num_seqs * p.num_heads;
+    int64_t t = c < P1 ? share_begin(c, T1, P1) : 0;   // (no share is empty)
+    const int64_t t_end = c < P1 ? share_begin(c + 1, T1, P1) : 0;
+    while (t < t_end) {
+        const int s = last_at_most(p.own_start, p.num_seqs, t / p.num_kv_heads);
+        const int len = p.plan.own_len[s], kt = (len + kKeys - 1) / kKeys;
+        const int64_t local = t - p.own_start[s] * p.num_kv_heads;
+        const int kvh = (int)(local / kt), tile = (int)(local - (int64_t)kvh * kt);
+        const int tiles = (int)min((int64_t)(kt - tile), t_end - t);
+        const int C = p.plan.shared_len[p.plan.seq_group[s]];
+        const int64_t row = tile == 0 ? (int64_t)s * p.num_heads + kvh * G : rows0 + c * G;
+        CcPiece w;
+        w.table = p.block_tables + (int64_t)s * p.max_blocks;
+        w.s0 = s;
+        w.rows = G;
+        w.kvh = kvh;
+        w.key0 = C + tile * kKeys;
+        w.key1 = (int)min((int64_t)C + len, (int64_t)w.key0 + (int64_t)tiles * kKeys);
+        w.o = p.own_o + row * D;
+        w.ml = p.own_ml + row;
+        piece(w);
+        t += tiles;
+    }
+}
+
+// The groups' shared tokens and, with more than kFewHeads q-heads a kv-head, the own parts.
 template <typename T, int D>
-__global__ void __launch_bounds__(kCcThreads, 2) shared_cc_kernel(const CcParams p) {
+__global__ void __launch_bounds__(kCcThreads, 2) shared_rows_kernel(const CcParams p) {
     extern __shared__ __align__(16) float cc_smem[];
     grid_dependency_wait();
     grid_dependents_launch();
     const int G = p.num_heads / p.num_kv_heads;
-    const int64_t c = blockIdx.x;
-    // the groups' shared tokens
-    const int64_t T0 = p.plan.tile_start[p.num_groups], P0 = min((int64_t)gridDim.x, T0);   // no share is empty
-    int64_t t = c < P0 ? share_begin(c, T0, P0) : 0;
-    const int64_t t_end = c < P0 ? share_begin(c + 1, T0, P0) : 0;
+    const int64_t c = blockIdx.x, T0 = p.plan.tile_start[p.num_groups], P0 = min((int64_t)gridDim.x, T0);
     const int64_t rows0 = (int64_t)p.num_seqs * p.num_heads;
+    auto piece = [&](const CcPiece &w) {
+        if (w.rows <= 16) cc_piece<T, D, 1>(p, w, cc_smem);
+        else if (w.rows <= 32) cc_piece<T, D, 2>(p, w, cc_smem);
+        else cc_piece<T, D, 4>(p, w, cc_smem);
+    };
+    int64_t t = c < P0 ? share_begin(c, T0, P0) : 0;   // (no share is empty)
+    const int64_t t_end = c < P0 ? share_begin(c + 1, T0, P0) : 0;
     while (t < t_end) {
         const PrefixItem it = prefix_item(p.plan, p.group_starts, p.num_groups, p.num_kv_heads, p.seqs_per_item, kKeys, 0, 1, -1, t);
         const int tiles = (int)min((int64_t)(it.of.kt - it.tile), t_end - t), i0 = it.part * p.seqs_per_item;
@@ -299,34 +485,21 @@ __global__ void __launch_bounds__(kCcThreads, 2) shared_cc_kernel(const CcParams
         w.key1 = (int)min((int64_t)it.C, (int64_t)(it.tile + tiles) * kKeys);
         w.o = p.pre_o + row * D;
         w.ml = p.pre_ml + row;
-        cc_any_rows<T, D>(p, w, cc_smem);
+        piece(w);
         t += tiles;
     }
-    // the sequences' own: by sequence, then kv-head
-    const int64_t T1 = p.own_start[p.num_seqs] * p.num_kv_heads;
-    const int64_t P1 = min((int64_t)gridDim.x, T1);
-    t = c < P1 ? share_begin(c, T1, P1) : 0;
-    const int64_t t_last = c < P1 ? share_begin(c + 1, T1, P1) : 0;
-    while (t < t_last) {
-        const int s = last_at_most(p.own_start, p.num_seqs, t / p.num_kv_heads);
-        const int len = p.plan.own_len[s], kt = (len + kKeys - 1) / kKeys;
-        const int64_t local = t - p.own_start[s] * p.num_kv_heads;
-        const int kvh = (int)(local / kt), tile = (int)(local - (int64_t)kvh * kt);
-        const int tiles = (int)min((int64_t)(kt - tile), t_last - t);
-        const int C = p.plan.shared_len[p.plan.seq_group[s]];
-        const int64_t row = tile == 0 ? (int64_t)s * p.num_heads + kvh * G : rows0 + c * G;
-        CcPiece w;
-        w.table = p.block_tables + (int64_t)s * p.max_blocks;
-        w.s0 = s;
-        w.rows = G;
-        w.kvh = kvh;
-        w.key0 = C + tile * kKeys;
-        w.key1 = (int)min((int64_t)C + len, (int64_t)w.key0 + (int64_t)tiles * kKeys);
-        w.o = p.own_o + row * D;
-        w.ml = p.own_ml + row;
-        cc_any_rows<T, D>(p, w, cc_smem);
-        t += tiles;
-    }
+    if (G > kFewHeads) own_share(p, D, piece);
+}
+
+// The own parts of at most kFewHeads q-heads a kv-head.  It needs the plan alone, which was complete before the kernel
+// in front began, so it takes the SMs that one leaves; at its end it waits for it, so that what follows may rely on
+// both.
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kCcThreads, 2) shared_few_kernel(const CcParams p) {
+    extern __shared__ __align__(16) float cc_smem[];
+    grid_dependents_launch();
+    own_share(p, D, [&](const CcPiece &w) { cc_few<T, D, R>(p, w, cc_smem); });
+    grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------ merge
@@ -554,14 +727,29 @@ cudaError_t launch_merge(const MergeParams &mg, cudaStream_t stream) {
                             dim3(kMergeThreads), 0, stream, mg);
 }
 
+template <typename T, int D, int R>
+cudaError_t launch_few(const CcParams &cc, int grid, cudaStream_t stream) {
+    constexpr int L = (R > 4 ? R : 4) * D / 32, kStreams = kCcThreads / L;
+    return launch_dependent(shared_few_kernel<T, D, R>, dim3(grid), dim3(kCcThreads), kStreams * R * (D + 2) * sizeof(float),
+                            stream, cc);
+}
+
 template <typename T, int D>
 cudaError_t launch_typed(const CcParams &cc, const MergeParams &mg, int grid, cudaStream_t stream) {
-    auto kern = shared_cc_kernel<T, D>;
+    auto kern = shared_rows_kernel<T, D>;
     constexpr size_t smem = cc_smem_floats<D>() * sizeof(float);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     e = launch_dependent(kern, dim3(grid), dim3(kCcThreads), smem, stream, cc);
     if (e != cudaSuccess) return e;
+    const int G = cc.num_heads / cc.num_kv_heads;
+    if (G <= kFewHeads) {
+        // (bf16 comes here only with unaligned rows or a scale that is not positive: one form will do)
+        if (sizeof(T) == 2 || G > 4) e = launch_few<T, D, 8>(cc, grid, stream);
+        else if (G > 2) e = launch_few<float, D, 4>(cc, grid, stream);
+        else e = launch_few<float, D, 2>(cc, grid, stream);
+        if (e != cudaSuccess) return e;
+    }
     return launch_merge<T, D>(mg, stream);
 }
 
@@ -665,6 +853,7 @@ cudaError_t launch_shared_prefix(const AttnArgs &a, const int32_t *group_starts,
     cc.num_heads = a.num_heads;
     cc.num_kv_heads = a.num_kv_heads;
     cc.block_size = a.block_size;
+    cc.log2b = a.block_size == 8 ? 3 : a.block_size == 16 ? 4 : 5;
     cc.max_blocks = a.max_blocks;
     cc.num_blocks = a.num_blocks;
     cc.aligned = in16(a.q) && in16(a.k_cache) && in16(a.v_cache) ? 1 : 0;
