@@ -24,7 +24,7 @@
 namespace pa {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256;
 constexpr int kPlanSmemGroups = 4096;   // group starts and smallest contexts kept in shared memory
 constexpr int kMaxTcGroups = 16384;
 constexpr int kMaxCtas = 512;           // partial slots reserved for share boundaries
@@ -99,6 +99,12 @@ struct CcPiece {
     float2 *ml;    // [rows]
 };
 
+// 16 bytes from global to shared memory in the background; zeros without `read` (src is any valid address then).
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 template <typename T> struct Vec16 { T v[16 / sizeof(T)]; };
 
 // 16 bytes of a row, as floats; element by element where rows need not be aligned.
@@ -161,18 +167,31 @@ __device__ __forceinline__ void cc_piece(const CcParams &p, const CcPiece &w, fl
         }
         const int64_t base = ((int64_t)max(blk, 0) * p.block_size + t0 % p.block_size) * tok_stride + (int64_t)w.kvh * D;
         const int live = blk < 0 ? 0 : min(8, w.key1 - t0);   // rows behind them may hold anything: not read
+        if (sizeof(T) == 4 && al) {
+            // all of the tile's rows in flight at once, zeros for those that are not read
+            const float *kc = static_cast<const float *>(p.k_cache) + base, *vc = static_cast<const float *>(p.v_cache) + base;
 #pragma unroll
-        for (int e0 = 0; e0 < 8 * (D / kVec); e0 += 32) {
-            const int e = e0 + lane, r = e / (D / kVec), d = (e - r * (D / kVec)) * kVec;
-            float x[kVec] = {}, y[kVec] = {};
-            if (r < live) {
-                load_floats(static_cast<const T *>(p.k_cache) + base + r * tok_stride + d, al, x);
-                load_floats(static_cast<const T *>(p.v_cache) + base + r * tok_stride + d, al, y);
+            for (int e0 = 0; e0 < 8 * (D / 4); e0 += 32) {
+                const int e = e0 + lane, r = e / (D / 4), d = (e - r * (D / 4)) * 4;
+                const int64_t at = r < live ? r * tok_stride + d : 0;
+                cp_async16(ks + (8 * warp + r) * kKS + d, kc + at, r < live);
+                cp_async16(vs + (8 * warp + r) * D + d, vc + at, r < live);
             }
+            cp_async_wait();
+        } else {
 #pragma unroll
-            for (int i = 0; i < kVec; i += 4) {
-                *reinterpret_cast<float4 *>(ks + (8 * warp + r) * kKS + d + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-                *reinterpret_cast<float4 *>(vs + (8 * warp + r) * D + d + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            for (int e0 = 0; e0 < 8 * (D / kVec); e0 += 32) {
+                const int e = e0 + lane, r = e / (D / kVec), d = (e - r * (D / kVec)) * kVec;
+                float x[kVec] = {}, y[kVec] = {};
+                if (r < live) {
+                    load_floats(static_cast<const T *>(p.k_cache) + base + r * tok_stride + d, al, x);
+                    load_floats(static_cast<const T *>(p.v_cache) + base + r * tok_stride + d, al, y);
+                }
+#pragma unroll
+                for (int i = 0; i < kVec; i += 4) {
+                    *reinterpret_cast<float4 *>(ks + (8 * warp + r) * kKS + d + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                    *reinterpret_cast<float4 *>(vs + (8 * warp + r) * D + d + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+                }
             }
         }
         __syncthreads();
