@@ -453,28 +453,24 @@ def _q4_pool_shape(k_cache, v_cache, head_dim: int):
     return num_blocks, slab // row, hkv
 
 
-def _axes(positions, pair_axis, n: int, rot: int, dev: int) -> tuple:
-    """What the calls with several position axes take: (positions, their axis stride, pair_axis, axes)."""
+def _refuse_axes(cos_sin, positions, pair_axis, n: int, dev: int) -> None:
+    """Raises what is wrong with the table, the positions or the pairs' axes of a call with several position axes."""
+    if cos_sin is None or positions is None or pair_axis is None:
+        raise ValueError("cos_sin, positions and pair_axis are needed")
     if positions.dim() != 2:
         raise ValueError("positions must be [axes, tokens]")
-    axes, tokens = positions.shape
-    stride, step = positions.stride()
-    if tokens < n:
+    if positions.shape[1] < n:
         raise ValueError("positions must have an entry per token on every axis")
-    if step != 1 and n > 1:
+    if positions.stride(1) != 1 and n > 1:
         raise ValueError("positions must be contiguous along the tokens")
-    if pair_axis.dim() != 1 or pair_axis.shape[0] != rot // 2:
+    if pair_axis.dim() != 1 or pair_axis.shape[0] != cos_sin.shape[1] // 2:
         raise ValueError("pair_axis must have an entry per pair of rotated dims")
-    if not (positions.dtype == pair_axis.dtype == torch.int32 and pair_axis.is_contiguous()
-            and positions.get_device() == pair_axis.get_device() == dev):
-        _refuse(dev, (positions[0] if n > 1 and axes else pair_axis, "positions", torch.int32),
-                (pair_axis, "pair_axis", torch.int32))
-        raise ValueError(f"positions must be on the current device cuda:{dev}, got {positions.device}")
-    return positions.data_ptr(), stride if axes > 1 else 0, pair_axis.data_ptr(), axes
+    row = positions[0, :n] if positions.shape[0] else pair_axis
+    _refuse(dev, (cos_sin, "cos_sin", torch.float32), (pair_axis, "pair_axis", torch.int32), (row, "positions", torch.int32))
 
 
 def _rope(fn, q, key, value, cos_sin, positions, k_cache, v_cache, pool_dtype, num_blocks, block_size, slot_mapping,
-          interleaved, q_out, dev_status, stream, pair_axis=None):
+          interleaved, q_out, dev_status, stream, axes=False, pair_axis=None):
     shape, dtype, dev = key.shape, key.dtype, torch.cuda.current_device()
     n, hkv, d = shape
     code = _CODES.get(dtype)
@@ -508,13 +504,17 @@ def _rope(fn, q, key, value, cos_sin, positions, k_cache, v_cache, pool_dtype, n
                 (slot_mapping, "slot_mapping", torch.int64))
     rot = max_pos = table_ptr = 0
     where = (0,)                 # positions, or positions of several axes and what names the pairs' axes
-    if fn.startswith("pa_mrope"):
-        if cos_sin is None or positions is None or pair_axis is None:
-            raise ValueError("cos_sin, positions and pair_axis are needed")
-        max_pos, rot = cos_sin.shape
-        if not (cos_sin.is_contiguous() and cos_sin.get_device() == dev and cos_sin.dtype == torch.float32):
-            _refuse(dev, (cos_sin, "cos_sin", torch.float32))
-        table_ptr, where = cos_sin.data_ptr(), _axes(positions, pair_axis, n, rot, dev)
+    if axes:
+        if cos_sin is None or positions is None or pair_axis is None or positions.dim() != 2:
+            _refuse_axes(cos_sin, positions, pair_axis, n, dev)
+        (max_pos, rot), (num_axes, tokens), (stride, step) = cos_sin.shape, positions.shape, positions.stride()
+        if not (tokens >= n and (step == 1 or n <= 1) and pair_axis.shape == (rot // 2,) and pair_axis.is_contiguous()
+                and cos_sin.is_contiguous() and cos_sin.dtype == torch.float32
+                and positions.dtype == pair_axis.dtype == torch.int32
+                and cos_sin.get_device() == positions.get_device() == pair_axis.get_device() == dev):
+            _refuse_axes(cos_sin, positions, pair_axis, n, dev)
+        table_ptr = cos_sin.data_ptr()
+        where = (positions.data_ptr(), stride if num_axes > 1 else 0, pair_axis.data_ptr(), num_axes)
     elif cos_sin is not None:
         if positions is None:
             raise ValueError("positions are needed with cos_sin")
@@ -543,19 +543,13 @@ def rope_and_cache(q, key, value, cos_sin, positions, k_cache, v_cache, slot_map
     """pa_rope_and_cache: q [tokens, H, D] (or None) and key rotated by position, K/V rows written to the pools;
     returns q_out.  q, key and value may be token-strided views; cos_sin is fp32 [max_position, rot_dim] (None: no
     rotation) and positions int32 [tokens]."""
-    return _rope_wide("pa_rope_and_cache", q, key, value, cos_sin, positions, k_cache, v_cache, slot_mapping, interleaved,
-                      q_out, dev_status, stream)
-
-
-def _rope_wide(fn, q, key, value, cos_sin, positions, k_cache, v_cache, slot_mapping, interleaved, q_out, dev_status,
-               stream, pair_axis=None):
     pool, rows, dtype = k_cache.shape, key.shape, key.dtype
     if len(pool) != 4 or v_cache.shape != pool or len(rows) != 3 or rows[1] != pool[2] or rows[2] != pool[3]:
         raise ValueError("key, value and the pools disagree on heads or head_dim")
     if k_cache.dtype != dtype or v_cache.dtype != dtype:
         raise TypeError("q, key, value and the 16/32-bit pools must share one dtype")
-    return _rope(fn, q, key, value, cos_sin, positions, k_cache, v_cache, dtype, pool[0], pool[1], slot_mapping,
-                 interleaved, q_out, dev_status, stream, pair_axis)
+    return _rope("pa_rope_and_cache", q, key, value, cos_sin, positions, k_cache, v_cache, dtype, pool[0],
+                 pool[1], slot_mapping, interleaved, q_out, dev_status, stream)
 
 
 def mrope_and_cache(q, key, value, cos_sin, positions, pair_axis, k_cache, v_cache, slot_mapping,
@@ -563,8 +557,13 @@ def mrope_and_cache(q, key, value, cos_sin, positions, pair_axis, k_cache, v_cac
     """pa_mrope_and_cache: rope_and_cache for tokens with a position on several axes.  positions is int32
     [axes, tokens or more] (rows contiguous; a view, or one row expanded, will do), pair_axis int32 [rot_dim / 2] names
     the axis that turns each pair."""
-    return _rope_wide("pa_mrope_and_cache", q, key, value, cos_sin, positions, k_cache, v_cache, slot_mapping,
-                      interleaved, q_out, dev_status, stream, pair_axis)
+    pool, rows, dtype = k_cache.shape, key.shape, key.dtype
+    if len(pool) != 4 or v_cache.shape != pool or len(rows) != 3 or rows[1] != pool[2] or rows[2] != pool[3]:
+        raise ValueError("key, value and the pools disagree on heads or head_dim")
+    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise TypeError("q, key, value and the 16/32-bit pools must share one dtype")
+    return _rope("pa_mrope_and_cache", q, key, value, cos_sin, positions, k_cache, v_cache, dtype, pool[0], pool[1],
+                 slot_mapping, interleaved, q_out, dev_status, stream, True, pair_axis)
 
 
 def q4_block_bytes(block_size: int, num_kv_heads: int, head_dim: int) -> int:
@@ -575,26 +574,25 @@ def rope_and_cache_q4(q, key, value, cos_sin, positions, k_cache, v_cache, slot_
                       q_out=None, dev_status=None, stream=None):
     """pa_rope_and_cache_q4: rope_and_cache into 4-bit pools (uint8 [num_blocks, num_kv_heads,
     q4_block_bytes(block_size, 1, head_dim)])."""
-    return _rope_q4("pa_rope_and_cache_q4", q, key, value, cos_sin, positions, k_cache, v_cache, slot_mapping,
-                    interleaved, q_out, dev_status, stream)
-
-
-def _rope_q4(fn, q, key, value, cos_sin, positions, k_cache, v_cache, slot_mapping, interleaved, q_out, dev_status,
-             stream, pair_axis=None):
     if key.dim() != 3:
         raise ValueError("key must be [tokens, num_kv_heads, head_dim]")
     num_blocks, block_size, hkv = _q4_pool_shape(k_cache, v_cache, key.shape[2])
     if key.shape[1] != hkv:
         raise ValueError("key and the pools disagree on num_kv_heads")
-    return _rope(fn, q, key, value, cos_sin, positions, k_cache, v_cache, torch.uint8, num_blocks, block_size,
-                 slot_mapping, interleaved, q_out, dev_status, stream, pair_axis)
+    return _rope("pa_rope_and_cache_q4", q, key, value, cos_sin, positions, k_cache, v_cache, torch.uint8, num_blocks,
+                 block_size, slot_mapping, interleaved, q_out, dev_status, stream)
 
 
 def mrope_and_cache_q4(q, key, value, cos_sin, positions, pair_axis, k_cache, v_cache, slot_mapping,
                        interleaved: bool = False, q_out=None, dev_status=None, stream=None):
     """pa_mrope_and_cache_q4: mrope_and_cache into 4-bit pools (as rope_and_cache_q4)."""
-    return _rope_q4("pa_mrope_and_cache_q4", q, key, value, cos_sin, positions, k_cache, v_cache, slot_mapping,
-                    interleaved, q_out, dev_status, stream, pair_axis)
+    if key.dim() != 3:
+        raise ValueError("key must be [tokens, num_kv_heads, head_dim]")
+    num_blocks, block_size, hkv = _q4_pool_shape(k_cache, v_cache, key.shape[2])
+    if key.shape[1] != hkv:
+        raise ValueError("key and the pools disagree on num_kv_heads")
+    return _rope("pa_mrope_and_cache_q4", q, key, value, cos_sin, positions, k_cache, v_cache, torch.uint8, num_blocks,
+                 block_size, slot_mapping, interleaved, q_out, dev_status, stream, True, pair_axis)
 
 
 def _q4_blocks(fn, wide_k, wide_v, q4_k, q4_v, quantize, pairs, dev_status, stream):
