@@ -222,17 +222,19 @@ __device__ __forceinline__ void gather_angles(const RopeArgs &a, int t0, const i
     }
     const int R = a.rot_dim / 2;
     int wrong = 0;
-    for (int e = threadIdx.x; e < a.rot_dim; e += blockDim.x) {
-        const int x = __ldg(a.pair_axis + (e < R ? e : e - R));
+    for (int i = threadIdx.x; i < R; i += blockDim.x) {   // a pair's cosine and sine at a time
+        const int x = __ldg(a.pair_axis + i);
         const bool ok = x >= 0 && x < a.num_axes;
         wrong |= !ok;
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (ok && slot[u] >= 0 && pos[u] == 0) {
-                int64_t at = p[u][0];
+                int at = p[u][0];
 #pragma unroll
                 for (int k = 1; k < kMaxAxes; ++k) at = x == k ? p[u][k] : at;
-                cs_s[u * a.rot_dim + e] = __ldg(a.cos_sin + at * a.rot_dim + e);
+                const float *cs = a.cos_sin + (int64_t)at * a.rot_dim + i;
+                cs_s[u * a.rot_dim + i] = __ldg(cs);
+                cs_s[u * a.rot_dim + R + i] = __ldg(cs + R);
             }
     }
     if (__syncthreads_or(wrong)) {
