@@ -74,9 +74,6 @@ constexpr int kSmemBudget = 227 * 1024;
 // at its shortest between 58 and 70.
 constexpr double kDecodeBytesPerSmNs = 64.0;
 constexpr double kPrefillFlopsPerSmNs = 6600.0;
-// SM-nanoseconds of a tile in the prefix kernel: head_dim 64, 128; 128 keys of one M-tile, of two, 64 keys of two kv-heads
-constexpr int kPrefixTileNs[2][3] = {{800, 1100, 800}, {1500, 1850, 1450}};
-constexpr int kPrefixItemNs = 3000;   // and of an item's begin and end
 constexpr int kUnitsPerCta = 4;
 
 struct __align__(16) StreamEntry {
@@ -171,9 +168,6 @@ struct DecodeSplit {
     int causal;
     double block_ns;   // SM-nanoseconds per decode block of all kv-heads
     double pair_ns;    // SM-nanoseconds per causal (query row, key) pair of all heads
-    // shared prefixes, whole SM-nanoseconds: per decode block; per prefix tile of an item with one M-tile, with two, of
-    // two kv-heads; per item
-    int block_ns32, tile_ns[3], item_ns;
     int32_t *prefix_shares;   // CTAs of the prefix kernel that take a share, of prefix_grid
     int prefix_grid;
 };
@@ -183,28 +177,18 @@ struct DecodeSplit {
 __device__ void shared_plan_cta(const SharedGroups &g, const SharedPlan &plan, const DecodeSplit &split, int32_t *starts,
                                 int32_t *lens, int32_t *status) {
     const bool ok = shared_lens<kPlanThreads>(g, starts, lens, status);
-    const int pos = g.seqs_per_item / 2;
-    const PlanSums sum = shared_write_plan<kPlanThreads>(
-        g, plan, ok, starts, lens, [&](int own) { return (int64_t)((own + kU - 1) / kU) * split.block_ns32; },
-        [&](const GroupItems &x) {
-            // parts of two M-tiles, and the last one, of one or two
-            const int two = x.pair ? 0 : x.full + (x.last > pos ? 1 : 0), one = x.parts - two;
-            const int64_t tile = x.pair ? split.tile_ns[2] : (int64_t)one * split.tile_ns[0] + (int64_t)two * split.tile_ns[1];
-            return (tile * x.kt + (int64_t)split.item_ns * x.parts) * x.heads;
-        });
+    const PlanSums sum = shared_write_plan<kPlanThreads>(g, plan, ok, starts, lens);
     if (threadIdx.x == 0) {
-        int act = split.grid;
-        if (sum.prefix > 0 && split.grid > 1) {
-            // rounded, and down where few CTAs are left to the prefix kernel: one too few there would make it the longer
-            const float x = split.grid * ((float)sum.own / (float)(sum.own + sum.prefix));
-            act = x > split.grid - 8 ? (int)x : (int)llrintf(x);
-            // a CTA for every few units at most: joining a cut sequence costs more than they do
-            const int64_t few = (sum.own / split.block_ns32 + kUnitsPerCta - 1) / kUnitsPerCta;
-            if (act > few) act = (int)few;
-            act = act < 1 ? 1 : (act > split.grid - 1 ? split.grid - 1 : act);
-            const int odd = (split.grid - act) % sum.width;   // whole teams, if there is one
-            if (split.grid - act > odd) act += odd;
-        }
+        // rounded, and down where few CTAs are left to the prefix kernel: one too few there would make it the longer
+        const float x = split.grid * ((float)sum.own / (float)max(sum.own + sum.prefix, (int64_t)1));
+        int act = x > split.grid - 8 ? (int)x : (int)llrintf(x);
+        // a CTA for every few units at most: joining a cut sequence costs more than they do
+        const int64_t few = (sum.own / g.own_ns + kUnitsPerCta - 1) / kUnitsPerCta;
+        if (act > few) act = (int)few;
+        const int most = sum.prefix > 0 && split.grid > 1 ? split.grid - 1 : split.grid;
+        act = act < 1 ? 1 : (act > most ? most : act);
+        const int odd = (split.grid - act) % sum.width;   // whole teams, if there is one
+        if (split.grid - act > odd) act += odd;
         *split.active = act;
         *split.prefix_shares = min(split.grid - act > 0 ? split.grid - act : split.grid, split.prefix_grid);
     }
@@ -1254,6 +1238,13 @@ bool split_decode_supported(const AttnArgs &a) {
     return al(a.q, 16) && al(a.k_cache, 16) && al(a.v_cache, 16) && al(a.out, 4);
 }
 
+int split_decode_unit_ns(int num_heads, int num_kv_heads, int head_dim) {
+    const Layout L = decode_layout(num_heads, num_kv_heads, head_dim);
+    // units of few heads are bound by their consumers' latency, not by their bytes
+    const int ns = (int)(kU * L.kvh * head_dim * 2 * 2 / kDecodeBytesPerSmNs), least = head_dim == 64 ? 450 : 600;
+    return L.nhg * (ns > least ? ns : least);
+}
+
 size_t split_decode_workspace(int num_seqs, int num_heads, int head_dim, int max_blocks, int block_size) {
     return workspace_layout(num_seqs, num_heads, head_dim, max_blocks, block_size).total;
 }
@@ -1358,13 +1349,7 @@ cudaError_t launch_split_decode(const AttnArgs &a, void *workspace, size_t works
     split.share = share_sms ? 1 : 0;
     split.causal = a.causal;
     split.block_ns = (double)kU * a.num_kv_heads * a.head_dim * 2 * 2 / kDecodeBytesPerSmNs;
-    {   // units of few heads are bound by their consumers' latency, not by their bytes
-        const int unit_ns = (int)(kU * L.kvh * a.head_dim * 2 * 2 / kDecodeBytesPerSmNs), least = a.head_dim == 64 ? 450 : 600;
-        split.block_ns32 = L.nhg * (unit_ns > least ? unit_ns : least);
-    }
     split.pair_ns = 4.0 * a.num_heads * a.head_dim / kPrefillFlopsPerSmNs;
-    for (int i = 0; i < 3; ++i) split.tile_ns[i] = kPrefixTileNs[a.head_dim == 64 ? 0 : 1][i];
-    split.item_ns = kPrefixItemNs;
     split.prefix_shares = shared ? shared->shares : nullptr;
     split.prefix_grid = prefix_grid();
     int plan_grid = (int)((max_entries + 4 * kPlanThreads - 1) / (4 * kPlanThreads));

@@ -27,6 +27,12 @@ namespace {
 constexpr int kPlanThreads = 256;
 constexpr int kPlanSmemGroups = 4096;   // group starts and smallest contexts kept in shared memory
 constexpr int kMaxTcGroups = 16384;
+// Nanoseconds of an SM for a tile of the prefix kernel: head_dim 64, 128; 128 keys of one M-tile, of two, 64 keys of two
+// kv-heads; and for an item's begin and end.  The SMs' split follows them, so they were set by sweeps of it.
+constexpr int kTcTileNs[2][3] = {{800, 1100, 800}, {1500, 1850, 1450}};
+constexpr int kTcItemNs = 3000;
+// CUDA cores: 64 keys of up to 16, 32 and 64 rows, of up to 8 rows from memory to registers; an item's begin and end.
+constexpr int kCcTileNs[3] = {2500, 3500, 8000}, kCcOwnNs = 800, kCcItemNs = 2000;
 constexpr int kMaxCtas = 512;           // partial slots reserved for share boundaries
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -44,8 +50,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     const bool in_smem = g.num_groups <= kPlanSmemGroups;
     int32_t *lens = in_smem ? lens_s : scratch;
     const bool ok = shared_lens<kPlanThreads>(g, in_smem ? starts_s : nullptr, lens, status);
-    shared_write_plan<kPlanThreads>(g, plan, ok, in_smem ? starts_s : g.starts, lens, [](int) { return 0; },
-                                    [](const GroupItems &) { return 0; });
+    shared_write_plan<kPlanThreads>(g, plan, ok, in_smem ? starts_s : g.starts, lens);
     int64_t own = 0;
     for (int base = 0; base < g.num_seqs; base += kPlanThreads) {
         const int s = base + tid, len = s < g.num_seqs ? plan.own_len[s] : 0;   // (this thread wrote it)
@@ -814,9 +819,12 @@ cudaError_t launch_tc(const AttnArgs &a, const int32_t *group_starts, const int3
     const TcLayout w = tc_layout(a.num_seqs, num_groups, a.num_heads, a.num_kv_heads, a.head_dim, a.max_blocks, a.block_size);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const int spi = prefix_seqs_per_item(a.num_heads / a.num_kv_heads), pair = a.num_kv_heads % 2 == 0 ? spi / 2 : 0;
+    const int (&tile_ns)[3] = kTcTileNs[a.head_dim == 64 ? 0 : 1];
     SharedJob job;
     job.groups = {a.context_lens, group_starts, prefix_lens, a.num_seqs, num_groups, a.num_kv_heads, a.block_size,
-                  (int64_t)a.max_blocks * a.block_size, spi, kPrefixKeys, pair, kMaxTeam};
+                  (int64_t)a.max_blocks * a.block_size, spi, kPrefixKeys, pair, kMaxTeam, 16,
+                  split_decode_unit_ns(a.num_heads, a.num_kv_heads, a.head_dim), {spi / 2, spi / 2},
+                  {tile_ns[0], tile_ns[0], tile_ns[1], tile_ns[2]}, kTcItemNs};
     job.plan = {reinterpret_cast<int32_t *>(ws + w.seq_group), reinterpret_cast<int32_t *>(ws + w.own_len),
                 reinterpret_cast<int32_t *>(ws + w.shared_len), reinterpret_cast<int64_t *>(ws + w.tile_start),
                 reinterpret_cast<int64_t *>(ws + w.team_start), reinterpret_cast<int32_t *>(ws + w.shares) + 1};
@@ -854,7 +862,9 @@ cudaError_t launch_shared_prefix(const AttnArgs &a, const int32_t *group_starts,
                              nullptr};
     int64_t *own_start = reinterpret_cast<int64_t *>(ws + w.own_start);
     const SharedGroups groups = {a.context_lens, group_starts, prefix_lens, a.num_seqs, num_groups, a.num_kv_heads,
-                                 a.block_size, (int64_t)a.max_blocks * a.block_size, spi, kKeys, 0, 1};
+                                 a.block_size, (int64_t)a.max_blocks * a.block_size, spi, kKeys, 0, 1, kKeys,
+                                 a.num_kv_heads * (G <= kFewHeads ? kCcOwnNs : G <= 16 ? kCcTileNs[0] : kCcTileNs[1]),
+                                 {16 / G, 32 / G}, {kCcTileNs[0], kCcTileNs[1], kCcTileNs[2], 0}, kCcItemNs};
     cudaError_t e = launch_dependent(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, groups, plan,
                                      reinterpret_cast<int32_t *>(ws + w.scratch), own_start, a.status);
     if (e != cudaSuccess) return e;

@@ -45,6 +45,10 @@ struct SharedGroups {
     int keys_per_tile;
     int pair_seqs;                 // 0: no items of two kv-heads
     int max_width;                 // of a team; 1: no teams
+    // Estimated work, in nanoseconds of an SM: `own_keys` tokens of one sequence (all kv-heads) on their own; a tile of
+    // an item of up to small_seqs[0], up to small_seqs[1] and more sequences, and of one of two kv-heads; an item beside
+    // its tiles.
+    int own_keys, own_ns, small_seqs[2], tile_ns[4], item_ns;
 };
 
 // A group's items: heads * parts of them, each of kt tiles of `keys` keys; the
@@ -67,6 +71,13 @@ __device__ __forceinline__ GroupItems group_items(int n, int C, int num_kv_heads
     x.blocks = width > 1 ? x.parts / width : 0;
     x.rest = x.parts - x.blocks * width;
     return x;
+}
+
+// Estimated work of a group's shared tokens.
+__device__ __forceinline__ int64_t items_ns(const SharedGroups &g, const GroupItems &x) {
+    auto tile = [&](int seqs) { return g.tile_ns[seqs <= g.small_seqs[0] ? 0 : seqs <= g.small_seqs[1] ? 1 : 2]; };
+    const int64_t tiles = x.pair ? g.tile_ns[3] : (int64_t)x.full * tile(g.seqs_per_item) + (x.last > 0 ? tile(x.last) : 0);
+    return (tiles * x.kt + (int64_t)x.parts * g.item_ns) * x.heads;
 }
 
 // The plan, in the workspace.
@@ -200,22 +211,25 @@ __device__ bool shared_lens(const SharedGroups &g, int32_t *starts, int32_t *len
         int C = 0;
         if (len < 0 || len > g.max_tokens) set_status(status, PA_ERR_OUT_OF_RANGE);
         else if (ok && n >= 2 && least != INT_MAX) C = min(len, least - 1) / g.block_size * g.block_size;
+        // shared only where that is less work than every sequence reading these tokens for itself
+        if (C > 0 && items_ns(g, group_items(n, C, g.num_kv_heads, g.seqs_per_item, g.keys_per_tile, g.pair_seqs, 1)) >
+                         (int64_t)n * ((C + g.own_keys - 1) / g.own_keys) * g.own_ns)
+            C = 0;
         lens[i] = C;
     }
     __syncthreads();
     return ok;
 }
 
-// The plan's arrays from C_g, by a whole CTA.  Returns the costs' sums: own_cost(tokens) of every sequence,
-// item_cost(items) of every group with shared tokens (whole nanoseconds), and the teams' width.
+// The plan's arrays from C_g, by a whole CTA.  Returns the estimated work of the own and of the shared parts, and the
+// teams' width.
 struct PlanSums {
     int64_t own, prefix;
     int width;
 };
-template <int kThreads, typename OwnCost, typename ItemCost>
+template <int kThreads>
 __device__ __forceinline__ PlanSums shared_write_plan(const SharedGroups &g, const SharedPlan &plan, bool ok,
-                                                      const int32_t *starts, const int32_t *lens, OwnCost own_cost,
-                                                      ItemCost item_cost) {
+                                                      const int32_t *starts, const int32_t *lens) {
     __shared__ int64_t tot[5][kThreads / 32];
     const int tid = threadIdx.x;
     auto items_of = [&](int i, int width) {
@@ -230,12 +244,12 @@ __device__ __forceinline__ PlanSums shared_write_plan(const SharedGroups &g, con
         const int own = ctx > 0 && ctx <= g.max_tokens ? ctx - lens[grp] : 0;
         plan.seq_group[s] = grp;
         plan.own_len[s] = own;
-        sum[0] += own_cost(own);
+        sum[0] += (int64_t)((own + g.own_keys - 1) / g.own_keys) * g.own_ns;
     }
     for (int i = tid; i < g.num_groups; i += kThreads)
         if (lens[i] > 0) {
             const GroupItems x = items_of(i, 1);
-            sum[1] += item_cost(x);
+            sum[1] += items_ns(g, x);
 #pragma unroll
             for (int w = 2; w <= kMaxTeam; ++w)
                 if (w <= g.max_width) sum[w] += (int64_t)(x.parts / w) * (w - 1) * x.heads * x.kt;
