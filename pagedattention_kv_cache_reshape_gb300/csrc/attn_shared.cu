@@ -31,6 +31,11 @@ constexpr int kMaxTcGroups = 16384;
 // kv-heads; and for an item's begin and end.  The SMs' split follows them, so they were set by sweeps of it.
 constexpr int kTcTileNs[2][3] = {{800, 1100, 800}, {1500, 1850, 1450}};
 constexpr int kTcItemNs = 3000;
+// Two parts to a sequence mean a longer way to its result, about 4 us.  Short prefixes have to save that: 189 sequences in 7
+// groups of 16-64 shared tokens 38.0 us shared and 31.9 not, 49 in 10 of 32 27.7 and 23.7.  Long ones are quicker
+// shared however few the sequences: 4 over 512 tokens 25.7 and 31.9 us, 2 over 4416-20,064 29.8 and 42.1 (flushed L2).
+constexpr int64_t kLeastSavedNs = 1000;   // of every SM
+constexpr int kLongPrefix = 256;
 // CUDA cores: 64 keys of up to 16, 32 and 64 rows, of up to 8 rows from memory to registers; an item's begin and end.
 constexpr int kCcTileNs[3] = {2500, 3500, 8000}, kCcOwnNs = 800, kCcItemNs = 2000;
 constexpr int kMaxCtas = 512;           // partial slots reserved for share boundaries
@@ -621,6 +626,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
     const int64_t T0 = p.plan.tile_start[p.num_groups], T1 = teams ? p.plan.team_start[p.num_groups] : 0;
     const int C = p.plan.shared_len[g], s0 = __ldg(p.group_starts + g), s1 = __ldg(p.group_starts + g + 1);
     const int64_t begin0 = p.plan.tile_start[g], begin1 = teams ? p.plan.team_start[g] : 0;
+    if (!p.own_start && T0 + T1 == 0) return;   // nothing is shared: the decode kernel has written all rows
     // a context length out of range leaves its row as it was; without shared tokens the decode kernel wrote it
     const bool mine = len > 0 && (p.own_start || C > 0);
     const int G = p.num_heads / p.num_kv_heads, kvh = h / G, hh = h - kvh * G;
@@ -824,7 +830,8 @@ cudaError_t launch_tc(const AttnArgs &a, const int32_t *group_starts, const int3
     job.groups = {a.context_lens, group_starts, prefix_lens, a.num_seqs, num_groups, a.num_kv_heads, a.block_size,
                   (int64_t)a.max_blocks * a.block_size, spi, kPrefixKeys, pair, kMaxTeam, 16,
                   split_decode_unit_ns(a.num_heads, a.num_kv_heads, a.head_dim), {spi / 2, spi / 2},
-                  {tile_ns[0], tile_ns[0], tile_ns[1], tile_ns[2]}, kTcItemNs};
+                  {tile_ns[0], tile_ns[0], tile_ns[1], tile_ns[2]}, kTcItemNs, kLeastSavedNs * device_sm_count(),
+                  kLongPrefix};
     job.plan = {reinterpret_cast<int32_t *>(ws + w.seq_group), reinterpret_cast<int32_t *>(ws + w.own_len),
                 reinterpret_cast<int32_t *>(ws + w.shared_len), reinterpret_cast<int64_t *>(ws + w.tile_start),
                 reinterpret_cast<int64_t *>(ws + w.team_start), reinterpret_cast<int32_t *>(ws + w.shares) + 1};
@@ -864,7 +871,7 @@ cudaError_t launch_shared_prefix(const AttnArgs &a, const int32_t *group_starts,
     const SharedGroups groups = {a.context_lens, group_starts, prefix_lens, a.num_seqs, num_groups, a.num_kv_heads,
                                  a.block_size, (int64_t)a.max_blocks * a.block_size, spi, kKeys, 0, 1, kKeys,
                                  a.num_kv_heads * (G <= kFewHeads ? kCcOwnNs : G <= 16 ? kCcTileNs[0] : kCcTileNs[1]),
-                                 {16 / G, 32 / G}, {kCcTileNs[0], kCcTileNs[1], kCcTileNs[2], 0}, kCcItemNs};
+                                 {16 / G, 32 / G}, {kCcTileNs[0], kCcTileNs[1], kCcTileNs[2], 0}, kCcItemNs, 0, 0};
     cudaError_t e = launch_dependent(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, groups, plan,
                                      reinterpret_cast<int32_t *>(ws + w.scratch), own_start, a.status);
     if (e != cudaSuccess) return e;

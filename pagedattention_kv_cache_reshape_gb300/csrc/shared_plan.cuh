@@ -49,6 +49,9 @@ struct SharedGroups {
     // an item of up to small_seqs[0], up to small_seqs[1] and more sequences, and of one of two kv-heads; an item beside
     // its tiles.
     int own_keys, own_ns, small_seqs[2], tile_ns[4], item_ns;
+    // Nothing is shared unless that saves this much, or some group has this many shared tokens.
+    int64_t least_ns;
+    int long_prefix;
 };
 
 // A group's items: heads * parts of them, each of kt tiles of `keys` keys; the
@@ -204,6 +207,7 @@ __device__ bool shared_lens(const SharedGroups &g, int32_t *starts, int32_t *len
         else if (ok) atomicMin(lens + last_at_most(from, NG, s), c);
     }
     __syncthreads();
+    int64_t saved[2] = {}, all[2];   // and the groups with long prefixes
     for (int i = tid; i < NG; i += kThreads) {
         const int n = i == tid ? b - a : __ldg(g.starts + i + 1) - __ldg(g.starts + i);
         const int len = i == tid ? P : __ldg(g.prefix_lens + i);
@@ -212,12 +216,24 @@ __device__ bool shared_lens(const SharedGroups &g, int32_t *starts, int32_t *len
         if (len < 0 || len > g.max_tokens) set_status(status, PA_ERR_OUT_OF_RANGE);
         else if (ok && n >= 2 && least != INT_MAX) C = min(len, least - 1) / g.block_size * g.block_size;
         // shared only where that is less work than every sequence reading these tokens for itself
-        if (C > 0 && items_ns(g, group_items(n, C, g.num_kv_heads, g.seqs_per_item, g.keys_per_tile, g.pair_seqs, 1)) >
-                         (int64_t)n * ((C + g.own_keys - 1) / g.own_keys) * g.own_ns)
-            C = 0;
+        if (C > 0) {
+            const int64_t less = (int64_t)n * ((C + g.own_keys - 1) / g.own_keys) * g.own_ns -
+                                 items_ns(g, group_items(n, C, g.num_kv_heads, g.seqs_per_item, g.keys_per_tile, g.pair_seqs, 1));
+            if (less > 0) {
+                saved[0] += less;
+                saved[1] += C >= g.long_prefix;
+            } else {
+                C = 0;
+            }
+        }
         lens[i] = C;
     }
-    __syncthreads();
+    __shared__ int64_t tot[2][kThreads / 32];
+    block_scan<kThreads, 2>(saved, tot, all);
+    if (all[0] < g.least_ns && all[1] == 0) {
+        for (int i = tid; i < NG; i += kThreads) lens[i] = 0;
+        __syncthreads();
+    }
     return ok;
 }
 

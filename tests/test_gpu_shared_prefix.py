@@ -30,7 +30,9 @@ def test_groups_of_all_kinds(H, Hkv, D, B, dtype):
 @pytest.mark.parametrize("H,Hkv,D,B", HEADS[:4])
 @pytest.mark.parametrize("tokens", [1, 7, 8, 15, 16, 31, 32, 63, 64, 65, 127, 128, 129, 200, 256, 257, 1000])
 def test_every_length(tokens, H, Hkv, D, B, dtype):
-    """Shared lengths of any kind: only whole blocks, and no sequence's last token, are computed once."""
+    """Shared lengths of any kind: only whole blocks, and no sequence's last token, are computed once.  (So many sequences
+    that sharing pays at every length, and a long group beside them.)"""
+    Case([(40, tokens), (2, 32 * B)], [0, 1, 2, 40, 9] if tokens > 1 else [1], H, Hkv, D, B, dtype, seed=tokens).run_checked()
     Case([(5, tokens)], [0, 1, 2, 40, 9] if tokens > 1 else [1], H, Hkv, D, B, dtype, seed=tokens).run_checked()
 
 
