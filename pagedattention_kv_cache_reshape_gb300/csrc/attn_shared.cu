@@ -36,8 +36,10 @@ constexpr int kTcItemNs = 3000;
 // shared however few the sequences: 4 over 512 tokens 25.7 and 31.9 us, 2 over 4416-20,064 29.8 and 42.1 (flushed L2).
 constexpr int64_t kLeastSavedNs = 1000;   // of every SM
 constexpr int kLongPrefix = 256;
-// CUDA cores: 64 keys of up to 16, 32 and 64 rows, of up to 8 rows from memory to registers; an item's begin and end.
-constexpr int kCcTileNs[3] = {2500, 3500, 8000}, kCcOwnNs = 800, kCcItemNs = 2000;
+// CUDA cores: head_dim 64, 128; 64 keys of up to 8, 32 and 64 rows; an item's begin and end; and what sharing has to save,
+// since a tile of many rows takes its CTA long (9 sequences over 64-1056 tokens, 32 / 1 heads x 64: 40 us shared, 24 not).
+constexpr int kCcTileNs[2][3] = {{1000, 3300, 4500}, {2000, 6500, 9000}}, kCcItemNs = 2000;
+constexpr int64_t kCcLeastSavedNs = 4000;   // of every SM
 constexpr int kMaxCtas = 512;           // partial slots reserved for share boundaries
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -317,7 +319,9 @@ __device__ __forceinline__ float4 load_four(const T *p, bool aligned) {
 // Up to R = 1, 2, 4 or 8 rows: bound by the cache's bytes, which go straight to registers.  L lanes take a key, each
 // the same dims of its K and V rows, of the queries and of the outputs: 4 (i L + lane) + (0..3), so that the L lanes'
 // loads are contiguous.  Every group of L lanes is a stream of its own with its running maximum and sums; the streams
-// of the CTA are joined at the end of the piece.  A warp takes every eighth chunk of 8 keys (which lie in one block), 32 / L
+// of the CTA are joined at the end of the piece.  A logit's parts are added up so that the lanes share the rows out among
+// themselves (R / 2 values exchanged, then R / 4, ...): li / (L / R) is the row whose logit, maximum and sum a lane ends
+// up with, and it hands the weight to the others.  A warp takes every eighth chunk of 8 keys (which lie in one block), 32 / L
 // keys a step, and requests a step's rows two steps ahead.  A stream moves its maximum only when a logit exceeds it by
 // more than 2^8 (its weights stay below that).
 template <typename T, int D, int R>
@@ -352,11 +356,11 @@ __device__ __forceinline__ void cc_few(const CcParams &p, const CcPiece &w, floa
         }
     };
     float4 q[R][kV], o[R][kV];
-    float m[R], l[R];
+    float m = -INFINITY, l = 0.f;      // of the lane's row
+    constexpr int kShare = L / R;
+    auto of_row = [&](float x, int r) { return __shfl_sync(0xffffffffu, x, (lane & ~(L - 1)) + r * kShare); };
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
 #pragma unroll
         for (int u = 0; u < kV; ++u) {
             o[r][u] = q[r][u] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -375,7 +379,6 @@ __device__ __forceinline__ void cc_few(const CcParams &p, const CcPiece &w, floa
             const int b = step & 1;
             const bool here = seen[b];
             float x[R];
-            bool grow = false;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 float2 y = make_float2(0.f, 0.f);
@@ -385,29 +388,39 @@ __device__ __forceinline__ void cc_few(const CcParams &p, const CcPiece &w, floa
                     y = fma_f32x2(make_float2(q[r][u].z, q[r][u].w), make_float2(k[b][u].z, k[b][u].w), y);
                 }
                 x[r] = y.x + y.y;
-#pragma unroll
-                for (int off = L / 2; off > 0; off >>= 1) x[r] += __shfl_xor_sync(0xffffffffu, x[r], off);
-                x[r] *= p.scale_log2;
-                grow = grow || (here && x[r] > m[r] + 8.f);
             }
-            if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const bool up = here && x[r] > m[r] + 8.f;
-                    const float alpha = up ? fast_exp2(m[r] - x[r]) : 1.f;
-                    if (up) m[r] = x[r];
-                    l[r] *= alpha;
+            for (int h = R / 2, off = L / 2; h > 0; h >>= 1, off >>= 1) {
+                const bool upper = (li & off) != 0;
 #pragma unroll
-                    for (int u = 0; u < kV; ++u)
-                        o[r][u] = make_float4(o[r][u].x * alpha, o[r][u].y * alpha, o[r][u].z * alpha, o[r][u].w * alpha);
+                for (int r = 0; r < h; ++r) {
+                    const float give = upper ? x[r] : x[r + h], keep = upper ? x[r + h] : x[r];
+                    x[r] = keep + __shfl_xor_sync(0xffffffffu, give, off);
                 }
             }
-            if (here) {
+#pragma unroll
+            for (int off = kShare / 2; off > 0; off >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], off);
+            const float y = x[0] * p.scale_log2;
+            const bool up = here && y > m + 8.f;
+            if (__any_sync(0xffffffffu, up)) {
+                const float alpha = up ? fast_exp2(m - y) : 1.f;
+                if (up) m = y;
+                l *= alpha;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    // (a maximum of -inf: the logit is -inf too, weight 0, or NaN)
-                    const float e = fast_exp2(x[r] - (m[r] == -INFINITY ? 0.f : m[r]));
-                    l[r] += e;
+                    const float f = of_row(alpha, r);
+#pragma unroll
+                    for (int u = 0; u < kV; ++u)
+                        o[r][u] = make_float4(o[r][u].x * f, o[r][u].y * f, o[r][u].z * f, o[r][u].w * f);
+                }
+            }
+            // (a maximum of -inf: the logit is -inf too, weight 0, or NaN)
+            const float weight = fast_exp2(y - (m == -INFINITY ? 0.f : m));
+            if (here) l += weight;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float e = of_row(weight, r);
+                if (here) {
 #pragma unroll
                     for (int u = 0; u < kV; ++u) {
                         const float2 f = fma_f32x2(make_float2(e, e), make_float2(v[b][u].x, v[b][u].y), make_float2(o[r][u].x, o[r][u].y));
@@ -430,8 +443,8 @@ __device__ __forceinline__ void cc_few(const CcParams &p, const CcPiece &w, floa
     for (int r = 0; r < R; ++r) {
 #pragma unroll
         for (int u = 0; u < kV; ++u) *reinterpret_cast<float4 *>(os + (stream * R + r) * D + 4 * (L * u + li)) = o[r][u];
-        if (li == 0) mls[stream * R + r] = make_float2(m[r], l[r]);
     }
+    if (li % kShare == 0) mls[stream * R + li / kShare] = make_float2(m, l);
     __syncthreads();
     for (int e = tid; e < w.rows * (D / 4); e += kCcThreads) {
         const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
@@ -495,7 +508,8 @@ __global__ void __launch_bounds__(kCcThreads, 2) shared_rows_kernel(const CcPara
     const int64_t c = blockIdx.x, T0 = p.plan.tile_start[p.num_groups], P0 = min((int64_t)gridDim.x, T0);
     const int64_t rows0 = (int64_t)p.num_seqs * p.num_heads;
     auto piece = [&](const CcPiece &w) {
-        if (w.rows <= 16) cc_piece<T, D, 1>(p, w, cc_smem);
+        if (w.rows <= 8) cc_few<T, D, 8>(p, w, cc_smem);
+        else if (w.rows <= 16) cc_piece<T, D, 1>(p, w, cc_smem);
         else if (w.rows <= 32) cc_piece<T, D, 2>(p, w, cc_smem);
         else cc_piece<T, D, 4>(p, w, cc_smem);
     };
@@ -868,10 +882,12 @@ cudaError_t launch_shared_prefix(const AttnArgs &a, const int32_t *group_starts,
                              reinterpret_cast<int32_t *>(ws + w.shared_len), reinterpret_cast<int64_t *>(ws + w.tile_start), nullptr,
                              nullptr};
     int64_t *own_start = reinterpret_cast<int64_t *>(ws + w.own_start);
+    const int (&tile_ns)[3] = kCcTileNs[a.head_dim == 64 ? 0 : 1];
     const SharedGroups groups = {a.context_lens, group_starts, prefix_lens, a.num_seqs, num_groups, a.num_kv_heads,
                                  a.block_size, (int64_t)a.max_blocks * a.block_size, spi, kKeys, 0, 1, kKeys,
-                                 a.num_kv_heads * (G <= kFewHeads ? kCcOwnNs : G <= 16 ? kCcTileNs[0] : kCcTileNs[1]),
-                                 {16 / G, 32 / G}, {kCcTileNs[0], kCcTileNs[1], kCcTileNs[2], 0}, kCcItemNs, 0, 0};
+                                 a.num_kv_heads * tile_ns[G <= 8 ? 0 : 1], {8 / G, 32 / G},
+                                 {tile_ns[0], tile_ns[1], tile_ns[2], 0}, kCcItemNs, kCcLeastSavedNs * device_sm_count(),
+                                 INT_MAX};
     cudaError_t e = launch_dependent(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, groups, plan,
                                      reinterpret_cast<int32_t *>(ws + w.scratch), own_start, a.status);
     if (e != cudaSuccess) return e;

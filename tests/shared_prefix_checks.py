@@ -11,9 +11,16 @@ HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}   # half a step, r
 class Case:
     """A batch in groups: `groups` is [(sequences, shared tokens)], `own` the tokens each sequence has beside them.
     Blocks of the shared tokens are the group's; where they end inside a block, each sequence holds a copy of that
-    block's shared part.  Whatever no sequence may read is NaN."""
+    block's shared part.  Whatever no sequence may read is NaN.  anchor: one more group of 64 sequences over so many
+    tokens that the call shares what it can (it shares nothing where all groups together would gain little)."""
 
-    def __init__(self, groups, own, H, Hkv, D, B, dtype, seed=0, prefix=None, spare=3, nan=True):
+    def __init__(self, groups, own, H, Hkv, D, B, dtype, seed=0, prefix=None, spare=3, nan=True, anchor=False):
+        self.rows = None
+        if anchor:
+            first = sum(n for n, _ in groups)
+            groups = list(groups) + [(64, -(-max(1300 // Hkv, 320) // B) * B)]
+            own = np.concatenate([np.resize(np.asarray(own), first), np.arange(64) % 19 + 1])
+            self.rows = list(range(first)) + [first, first + 31, first + 63]
         g = torch.Generator().manual_seed(seed)
         rng = np.random.default_rng(seed)
         self.H, self.Hkv, self.D, self.B, self.dtype, self.groups = H, Hkv, D, B, dtype, groups
@@ -71,7 +78,7 @@ class Case:
         st = torch.zeros(1, dtype=torch.int32, device=DEV)
         out = self.run(dev_status=st, **kw)
         assert pa.get_device_status(st) == pa.OK
-        self.check(out)
+        self.check(out, self.rows)
         return out
 
     def workspace(self, fill=0xFF):

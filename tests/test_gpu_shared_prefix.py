@@ -23,6 +23,7 @@ HEADS = [(32, 8, 128, 16), (14, 2, 64, 32), (4, 4, 128, 8), (16, 1, 64, 16), (32
 def test_groups_of_all_kinds(H, Hkv, D, B, dtype):
     """A long prefix for many, a short one, a single sequence, none shared, a pair; own parts from one token on."""
     groups = [(19, 40 * B), (3, B), (1, 3 * B), (7, 0), (2, 11 * B)]
+    Case(groups, [1, 2, B, B + 1, 130, 17, 63, 64, 65, 300], H, Hkv, D, B, dtype, seed=H, anchor=True).run_checked()
     Case(groups, [1, 2, B, B + 1, 130, 17, 63, 64, 65, 300], H, Hkv, D, B, dtype, seed=H).run_checked()
 
 
@@ -31,8 +32,9 @@ def test_groups_of_all_kinds(H, Hkv, D, B, dtype):
 @pytest.mark.parametrize("tokens", [1, 7, 8, 15, 16, 31, 32, 63, 64, 65, 127, 128, 129, 200, 256, 257, 1000])
 def test_every_length(tokens, H, Hkv, D, B, dtype):
     """Shared lengths of any kind: only whole blocks, and no sequence's last token, are computed once.  (So many sequences
-    that sharing pays at every length, and a long group beside them.)"""
-    Case([(40, tokens), (2, 32 * B)], [0, 1, 2, 40, 9] if tokens > 1 else [1], H, Hkv, D, B, dtype, seed=tokens).run_checked()
+    that sharing pays at every length.)"""
+    own = [0, 1, 2, 40, 9] if tokens > 1 else [1]
+    Case([(40, tokens), (5, tokens)], own, H, Hkv, D, B, dtype, seed=tokens, anchor=True).run_checked()
     Case([(5, tokens)], [0, 1, 2, 40, 9] if tokens > 1 else [1], H, Hkv, D, B, dtype, seed=tokens).run_checked()
 
 
@@ -40,7 +42,7 @@ def test_every_length(tokens, H, Hkv, D, B, dtype):
 @pytest.mark.parametrize("n", [1, 2, 3, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 130, 257])
 @pytest.mark.parametrize("H,Hkv,D", [(8, 2, 128), (3, 1, 64), (2, 2, 64)])
 def test_every_group_size(n, H, Hkv, D, dtype):
-    Case([(n, 320)], [1, 30, 16, 33], H, Hkv, D, 16, dtype, seed=n).run_checked()
+    Case([(n, 320)], [1, 30, 16, 33], H, Hkv, D, 16, dtype, seed=n, anchor=True).run_checked()
 
 
 @pytest.mark.parametrize("dtype", DTYPES, **ids)
@@ -90,7 +92,7 @@ def test_many_pieces(H, Hkv, D, B, n, step, dtype):
 def test_a_key_that_stands_out_is_found(H, Hkv, D, B, dtype):
     """One key after another, at the ends of blocks, tiles and parts, holds nearly all the weight of every row."""
     P, own = 16 * B + 2 * B, 2 * B + 3
-    c = Case([(3, P), (2, 5 * B)], [own], H, Hkv, D, B, dtype, seed=5)
+    c = Case([(3, P), (2, 5 * B)], [own], H, Hkv, D, B, dtype, seed=5, anchor=True)
     c.q = torch.ones_like(c.q)
     c.k = torch.where(torch.isnan(c.k), c.k, 0.01 * c.k)
     plain = c.k.clone()
@@ -100,7 +102,7 @@ def test_a_key_that_stands_out_is_found(H, Hkv, D, B, dtype):
         blk = c.bt[:3, t // B].long()
         c.k[blk, t % B] = 4.0
         out = c.run()
-        c.check(out)
+        c.check(out, c.rows)
         want = c.v[blk, t % B].float().repeat_interleave(H // Hkv, 1)
         w = float(np.exp(-3.9 * np.sqrt(D)))                  # the other keys' weight, each, at most
         err = (out[:3].float() - want).abs()
@@ -111,12 +113,11 @@ def test_a_key_that_stands_out_is_found(H, Hkv, D, B, dtype):
 def test_lengths_that_do_not_go_together(dtype):
     """A prefix length beyond some sequence's context, or short of what is shared: never a wrong result."""
     for prefix in ([500, 48], [64, 40], [4096, 4096], [1, 0], [63, 65]):
-        Case([(6, 64), (4, 48)], [1, 5, 40, 0], 8, 2, 128, 16, dtype, prefix=None, seed=3)
-        c = Case([(6, 64), (4, 48)], [1, 5, 40, 0], 8, 2, 128, 16, dtype, seed=3)
+        c = Case([(6, 64), (4, 48)], [1, 5, 40, 0], 8, 2, 128, 16, dtype, seed=3, anchor=True)
         c.bt = torch.cat([c.bt, torch.full((c.S, 256), -1, dtype=torch.int32, device=DEV)], 1).contiguous()
-        c.prefix.copy_(torch.tensor(prefix))
+        c.prefix[:2] = torch.tensor(prefix, dtype=torch.int32)
         # tokens 64.. of the first group differ by sequence: they may only be called shared where none has them
-        c.prefix.clamp_(max=64)
+        c.prefix[:2].clamp_(max=64)
         c.run_checked()
     c = Case([(5, 96)], [0], 8, 2, 128, 16, dtype, seed=4)        # everything shared, contexts alike
     c.prefix.fill_(96)
@@ -149,7 +150,7 @@ def test_a_prefix_length_out_of_range_shares_nothing(bad, dtype):
 @pytest.mark.parametrize("dtype", DTYPES, **ids)
 @pytest.mark.parametrize("bad", [0, -5, 10 ** 6, -2 ** 31, 2 ** 31 - 1])
 def test_a_context_out_of_range_leaves_its_row(bad, dtype):
-    c = Case([(4, 64), (2, 32)], [5, 40, 1], 8, 2, 128, 16, dtype, seed=8)
+    c = Case([(4, 64), (2, 32)], [5, 40, 1], 8, 2, 128, 16, dtype, seed=8, anchor=True)
     rows = [0, 5]
     c.ctx[rows] = bad
     st = torch.zeros(1, dtype=torch.int32, device=DEV)
@@ -168,13 +169,13 @@ def test_a_context_out_of_range_leaves_its_row(bad, dtype):
 @pytest.mark.parametrize("bad", [-1, 10 ** 6])
 def test_bad_table_entries_are_reported(bad, dtype):
     """In the shared part, and in one sequence's own: other groups, and other sequences, keep their results."""
-    c = Case([(4, 64), (3, 160)], [5, 40, 20], 8, 2, 128, 16, dtype, seed=9)
+    c = Case([(4, 64), (3, 160)], [5, 40, 20], 8, 2, 128, 16, dtype, seed=9, anchor=True)
     st = torch.zeros(1, dtype=torch.int32, device=DEV)
     c.bt[0, 2] = bad
     c.run(dev_status=st)
     assert pa.get_device_status(st) == pa.ERR_OUT_OF_RANGE
     c.check(c.run(), rows=[4, 5, 6])
-    c = Case([(4, 64), (3, 160)], [5, 40, 20], 8, 2, 128, 16, dtype, seed=9)
+    c = Case([(4, 64), (3, 160)], [5, 40, 20], 8, 2, 128, 16, dtype, seed=9, anchor=True)
     c.bt[1, 5] = bad
     st.zero_()
     out = c.run(dev_status=st)
@@ -184,13 +185,13 @@ def test_bad_table_entries_are_reported(bad, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES, **ids)
 def test_nan_and_infinities_stay_in_their_rows(dtype):
-    c = Case([(6, 320), (3, 0)], [5, 40, 20], 8, 2, 128, 16, dtype, seed=10)
+    c = Case([(6, 320), (3, 0)], [5, 40, 20], 8, 2, 128, 16, dtype, seed=10, anchor=True)
     q = c.q.clone()
     q[2, 3, 7] = float("nan")
     q[4, 0] = float("inf")
     out = c.run(q=q)
     assert torch.isnan(out[2, 3]).all() and torch.isnan(out[4, 0]).all()
-    keep = torch.ones(9, 8, dtype=torch.bool, device=DEV)
+    keep = torch.ones(c.S, 8, dtype=torch.bool, device=DEV)
     keep[2, 3] = keep[4, 0] = False
     want = c.run()
     assert torch.equal(out[keep], want[keep])
@@ -207,7 +208,7 @@ def test_nan_and_infinities_stay_in_their_rows(dtype):
 @pytest.mark.parametrize("scale", [0.0, -0.3, 30.0, 1e-30])
 def test_any_scale(scale, dtype):
     """Equal weights, the smallest logits on top, one key alone on top."""
-    c = Case([(5, 192), (2, 64)], [5, 40, 20], 8, 2, 64, 16, dtype, seed=11)
+    c = Case([(5, 192), (2, 64)], [5, 40, 20], 8, 2, 64, 16, dtype, seed=11, anchor=True)
     c.scale = scale
     c.run_checked()
 
@@ -215,7 +216,7 @@ def test_any_scale(scale, dtype):
 @pytest.mark.parametrize("dtype", DTYPES, **ids)
 def test_logits_that_grow_along_the_keys(dtype):
     """Every tile has a new largest logit, so all that was summed before is scaled down."""
-    c = Case([(9, 1024)], [200, 3], 8, 2, 128, 16, dtype, seed=12)
+    c = Case([(70, 1024)], [200, 3], 8, 2, 128, 16, dtype, seed=12)
     for s in range(c.S):
         n = c.lens[s]
         t = torch.arange(n, device=DEV)
@@ -228,7 +229,7 @@ def test_logits_that_grow_along_the_keys(dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES, **ids)
 def test_results_do_not_depend_on_blocks_workspace_or_run(dtype):
-    c = Case([(20, 640), (5, 0), (9, 96)], [5, 40, 200], 32, 8, 128, 16, dtype, seed=13)
+    c = Case([(20, 640), (5, 0), (9, 96)], [5, 40, 200], 32, 8, 128, 16, dtype, seed=13, anchor=True)
     want = c.run()
     ws = c.workspace()
     for _ in range(3):
@@ -243,23 +244,23 @@ def test_results_do_not_depend_on_blocks_workspace_or_run(dtype):
 @pytest.mark.parametrize("dtype", DTYPES, **ids)
 def test_rows_that_start_anywhere(dtype):
     """q, out and the pools one element off the 16-byte grid."""
-    c = Case([(6, 192), (2, 64)], [5, 40, 20], 8, 2, 64, 16, dtype, seed=14)
+    c = Case([(6, 192), (2, 64)], [5, 40, 20], 8, 2, 64, 16, dtype, seed=14, anchor=True)
     want = c.run_checked()
 
     def off(t):
         flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)[1:]
         return flat.copy_(t.flatten()).view(t.shape)
     for name, t in (("q", c.q), ("k_cache", c.k), ("v_cache", c.v)):
-        c.check(c.run(**{name: off(t)}))
+        c.check(c.run(**{name: off(t)}), c.rows)
     out = off(torch.zeros_like(c.q))
-    c.check(c.run(out=out))
+    c.check(c.run(out=out), c.rows)
     assert out.data_ptr() % 16 and want.shape == out.shape
 
 
 @pytest.mark.parametrize("dtype", DTYPES, **ids)
 def test_far_blocks_past_32_bits(dtype):
     """Blocks whose offsets in elements pass 2^32."""
-    c = Case([(3, 64)], [5, 40], 8, 2, 128, 16, dtype, seed=15)
+    c = Case([(3, 64)], [5, 40], 8, 2, 128, 16, dtype, seed=15, anchor=True)
     per = c.k[0].numel()
     far = (2 ** 32) // per + 3
     k = torch.zeros(far + c.nb, 16, 2, 128, dtype=dtype, device=DEV)
@@ -273,12 +274,12 @@ def test_far_blocks_past_32_bits(dtype):
 def test_a_captured_call_follows_its_buffers(dtype):
     """Lengths, groups and prefixes change between replays; two graphs with workspaces of their own, one after the
     other on streams of their own."""
-    c = Case([(12, 640)], [33], 8, 2, 128, 16, dtype, seed=16)
+    c = Case([(12, 640)], [33], 32, 8, 128, 16, dtype, seed=16)
     starts, prefix = torch.tensor([0, 12, 12, 12], device=DEV).int(), torch.tensor([640, 0, 0], device=DEV).int()
     graphs = []
     for _ in range(2):
         s, g, out = torch.cuda.Stream(), torch.cuda.CUDAGraph(), torch.zeros_like(c.q)
-        ws = torch.full((pa.decode_shared_prefix_workspace_size(12, 3, 8, 2, 128, 16, c.mb),), 0xFF, dtype=torch.uint8, device=DEV)
+        ws = torch.full((pa.decode_shared_prefix_workspace_size(12, 3, 32, 8, 128, 16, c.mb),), 0xFF, dtype=torch.uint8, device=DEV)
         s.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
             c.run(group_starts=starts, prefix_lens=prefix, out=out, workspace=ws)
