@@ -228,8 +228,10 @@ PA_API size_t pa_decode_shared_prefix_workspace_size(int num_seqs, int num_group
  *  workspace     >= pa_decode_shared_prefix_workspace_size(...) bytes, 16-byte
  *                aligned; its contents on entry do not matter; calls that may
  *                overlap on the GPU take workspaces of their own
- * The rest as for pa_decode: a context length out of range leaves its row as
- * it was.  group_starts that are not in order, or a prefix length out of
+ * The rest as for pa_decode, but max_blocks * block_size ends 256 tokens
+ * short of 2^31 and num_heads * (num_seqs + num_groups) at 2^30
+ * (PA_ERR_UNSUPPORTED): a context length out of range leaves its row as it
+ * was.  group_starts that are not in order, or a prefix length out of
  * range, set PA_ERR_OUT_OF_RANGE in *dev_status, and the call (the group) is
  * computed as if nothing were shared.  Precondition (not checked on the
  * device): the blocks that hold a group's shared tokens are the same in all

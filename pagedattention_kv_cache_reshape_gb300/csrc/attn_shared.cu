@@ -42,6 +42,8 @@ constexpr int kCcTileNs[2][3] = {{1000, 3300, 4500}, {2000, 6500, 9000}}, kCcIte
 constexpr int64_t kCcLeastSavedNs = 4000;   // of every SM
 constexpr int kMaxCtas = 512;           // partial slots reserved for share boundaries
 
+constexpr size_t kAlign = 32;           // of the pieces' rows (32-byte stores); a caller's workspace lies on 16 bytes
+
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // ------------------------------------------------------------------ plan
@@ -869,11 +871,12 @@ size_t shared_prefix_workspace(int num_seqs, int num_groups, int num_heads, int 
                                int block_size) {
     const size_t cc = layout(num_seqs, num_groups, num_heads, num_kv_heads, head_dim).total;
     const size_t tc = tc_layout(num_seqs, num_groups, num_heads, num_kv_heads, head_dim, max_blocks, block_size).total;
-    return cc > tc ? cc : tc;
+    return (cc > tc ? cc : tc) + kAlign - 16;
 }
 
 cudaError_t launch_shared_prefix(const AttnArgs &a, const int32_t *group_starts, const int32_t *prefix_lens, int num_groups,
                                  void *workspace, cudaStream_t stream) {
+    workspace = reinterpret_cast<void *>(align_up(reinterpret_cast<uintptr_t>(workspace), kAlign));
     if (tc_supported(a, num_groups)) return launch_tc(a, group_starts, prefix_lens, num_groups, workspace, stream);
     const Layout w = layout(a.num_seqs, num_groups, a.num_heads, a.num_kv_heads, a.head_dim);
     uint8_t *ws = static_cast<uint8_t *>(workspace);

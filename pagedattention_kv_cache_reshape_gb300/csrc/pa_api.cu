@@ -492,7 +492,8 @@ pa_status pa_decode_shared_prefix(void *out, const void *q, const void *k_cache,
     if (num_groups == 0 || !group_starts || !prefix_lens) return PA_ERR_INVALID_ARG;
     if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(group_starts, 4) || !aligned(prefix_lens, 4))
         return PA_ERR_INVALID_ARG;
-    // pieces are counted in 32 bits
+    // pieces, and the keys of whole tiles, are counted in 32 bits
+    if ((int64_t)max_blocks * block_size > INT32_MAX - 256) return PA_ERR_UNSUPPORTED;
     if ((int64_t)num_heads * ((int64_t)num_seqs + num_groups) > INT32_MAX / 2) return PA_ERR_UNSUPPORTED;
     const size_t need = pa_decode_shared_prefix_workspace_size(num_seqs, num_groups, num_heads, num_kv_heads, head_dim,
                                                                block_size, max_blocks);

@@ -258,6 +258,18 @@ def test_rows_that_start_anywhere(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, **ids)
+def test_a_workspace_that_starts_on_any_16_bytes(dtype):
+    """Its end too: what lies behind the bytes asked for stays as it was."""
+    c = Case([(6, 192), (2, 64), (20, 48)], [5, 40, 20], 8, 2, 128, 16, dtype, seed=17, anchor=True)
+    want, n = c.run_checked(), c.workspace().numel()
+    for start in (0, 16, 32, 48, 240):
+        raw = torch.full((n + 512,), 0xA5, dtype=torch.uint8, device=DEV)
+        assert raw.data_ptr() % 256 == 0
+        assert torch.equal(c.run(workspace=raw[start:start + n]), want)
+        assert (raw[:start] == 0xA5).all() and (raw[start + n:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, **ids)
 def test_far_blocks_past_32_bits(dtype):
     """Blocks whose offsets in elements pass 2^32."""
     c = Case([(3, 64)], [5, 40], 8, 2, 128, 16, dtype, seed=15, anchor=True)

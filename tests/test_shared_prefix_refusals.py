@@ -30,7 +30,7 @@ ARGS = dict(out=1 << 30, q=2 << 30, k=3 << 30, v=4 << 30, bt=5 << 30, ctx=6 << 3
     (dict(starts=None), INV), (dict(prefix=None), INV), (dict(q=(2 << 30) + 1), INV), (dict(k=(3 << 30) + 1), INV),
     (dict(bt=(5 << 30) + 1), INV), (dict(ctx=(6 << 30) + 2), INV), (dict(starts=(7 << 30) + 2), INV),
     (dict(prefix=(8 << 30) + 3), INV), (dict(ws=None), WS), (dict(ws=(9 << 30) + 8), WS), (dict(wsb=0), WS),
-    (dict(mb=1 << 28), INV), (dict(n=1 << 28), UNS), (dict(groups=1 << 28), UNS),
+    (dict(mb=1 << 28), INV), (dict(mb=(1 << 27) - 8), UNS), (dict(n=1 << 28), UNS), (dict(groups=1 << 28), UNS),
     (dict(n=0, groups=0, out=None, q=None, k=None, v=None, bt=None, ctx=None, starts=None, prefix=None, ws=None, wsb=0), pa.OK),
     (dict(n=0, groups=-1), INV),
 ])
