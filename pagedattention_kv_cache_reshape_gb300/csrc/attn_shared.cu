@@ -642,7 +642,10 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
     const int64_t T0 = p.plan.tile_start[p.num_groups], T1 = teams ? p.plan.team_start[p.num_groups] : 0;
     const int C = p.plan.shared_len[g], s0 = __ldg(p.group_starts + g), s1 = __ldg(p.group_starts + g + 1);
     const int64_t begin0 = p.plan.tile_start[g], begin1 = teams ? p.plan.team_start[g] : 0;
-    if (!p.own_start && T0 + T1 == 0) return;   // nothing is shared: the decode kernel has written all rows
+    if (!p.own_start && T0 + T1 == 0) {   // nothing is shared: the decode kernel writes all rows
+        grid_dependency_wait();           // (and has written them when this grid, the call's last, is done)
+        return;
+    }
     // a context length out of range leaves its row as it was; without shared tokens the decode kernel wrote it
     const bool mine = len > 0 && (p.own_start || C > 0);
     const int G = p.num_heads / p.num_kv_heads, kvh = h / G, hh = h - kvh * G;

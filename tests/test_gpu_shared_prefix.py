@@ -258,6 +258,21 @@ def test_rows_that_start_anywhere(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, **ids)
+@pytest.mark.parametrize("prefix", [0, 2048])
+def test_what_comes_behind_a_call_sees_its_rows(prefix, dtype):
+    """The next operation on the stream starts when all rows are written, whether or not anything was shared."""
+    c = Case([(7, prefix), (3, 0)], [30000, 3, 9000], 8, 2, 128, 16, dtype, seed=18)
+    want, seen = c.run(), []
+    torch.cuda.synchronize()
+    for _ in range(5):
+        out = torch.zeros_like(c.q)
+        torch.cuda.synchronize()
+        seen.append(c.run(out=out).clone())
+    torch.cuda.synchronize()
+    assert all(torch.equal(s, want) for s in seen)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, **ids)
 def test_a_workspace_that_starts_on_any_16_bytes(dtype):
     """Its end too: what lies behind the bytes asked for stays as it was."""
     c = Case([(6, 192), (2, 64), (20, 48)], [5, 40, 20], 8, 2, 128, 16, dtype, seed=17, anchor=True)
