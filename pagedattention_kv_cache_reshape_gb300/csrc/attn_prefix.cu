@@ -12,13 +12,18 @@
 // number of tiles whatever the group sizes; a share holds a few pieces of items,
 // usually one or two.  Items that read the same tiles go to teams of CTAs that
 // read them together: 256 sequences (4 items a kv-head) over 32,768 tokens read
-// 137 MB from HBM instead of 406 MB, and the call takes 149 us instead of 179.
+// 137 MB from HBM instead of 406 MB, and the call takes 130 us instead of 149
+// (teams of at most two: 136).
 //
 // Bound: a 64 KB tile (K and V, 128 keys x 128 dims) takes an SM's share of
 // HBM 1.5 us; the products of one M-tile of 128 rows take 0.5 us of the tensor
 // pipe, of two 1 us.  So groups of up to 256 rows a kv-head are bound by HBM,
 // larger ones (several items read the same tiles) by the tensor pipe and the
-// softmax beside it.
+// softmax beside it.  Measured (32 / 8 heads x 128): 16 sequences over one prefix
+// of 131,072 tokens 91 us, 5.9 TB/s; 256 over 32,768 107 us, the tensor pipe 73 %
+// busy (a tile of two M-tiles takes about 2780 cycles, its products 2048); 24
+// groups of 8 over up to 4096 tokens, 32 heads, 167 us beside the decode kernel,
+// 5.2 TB/s: there an SM waits for its ring of tiles, 56-58 GB/s a SM.
 //
 // Roles (512 threads): warps 0-7 two softmax warpgroups (thread = row = TMEM
 // lane of its M-tile), warp 8 TMA producer, warp 9 TMEM owner and MMA issuer,
@@ -99,9 +104,12 @@ template <int D> struct Shape {
 //         take every KV tile of 128 keys
 //  kPair  a small group and two kv-heads: M-tile t holds the rows of kv-head
 //         kvh + t; a KV tile is 64 keys of both, so a TMA box carries both heads
-//         (half the boxes a byte, rows of memory twice as long)
-//  kTurns up to `pos` sequences of one kv-head: both M-tiles hold the same rows, t
-//         takes KV tiles t, t + 2, ..., and the output warpgroup joins them
+//         (half the boxes a byte, rows of memory twice as long: the 24 groups of 8
+//         222 us against 237 one head at a time, one of 16 over 131,072 tokens 110
+//         against 114, the whole call with a flushed L2)
+//  kTurns up to `pos` sequences of one kv-head (an odd number of kv-heads, or the last
+//         few of a larger group): both M-tiles hold the same rows, t takes KV tiles t,
+//         t + 2, ..., and the output warpgroup joins them
 // live = 0 marks the end.
 constexpr int kTurns = 0, kWide = 1, kPair = 2;
 struct Piece {

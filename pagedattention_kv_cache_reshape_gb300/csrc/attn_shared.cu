@@ -139,8 +139,10 @@ __device__ __forceinline__ void load_floats(const T *p, bool aligned, float (&x)
 // (Rows of D + 4: the two rows of a warp's half warps, and the keys of its lanes, lie in different banks.)
 template <int D> constexpr int cc_smem_floats() { return kRows * (D + 4) + kKeys * (D + 4) + kKeys * D; }
 
-// Thread (ty, tx) of 16 x 16 holds logits of rows ty * RT + i and keys tx + 16 j, and of the outputs the same rows and
-// dims 4 tx + 64 j + (0..3).  A row's 16 threads are half a warp.  RT = 1, 2 or 4: 16, 32 or 64 rows.
+// Bound by what shared memory delivers (64 rows: 34 TFLOP/s, L1 76 % and FMA 53 % busy; 4 x 4 logits of a thread take 8
+// loads of 16 bytes for 64 products).  Thread (ty, tx) of 16 x 16 holds logits of rows ty * RT + i and keys tx + 16 j, and
+// of the outputs the same rows and dims 4 tx + 64 j + (0..3).  A row's 16 threads are half a warp.  RT = 1, 2 or 4: 16, 32
+// or 64 rows.
 template <typename T, int D, int RT>
 __device__ __forceinline__ void cc_piece(const CcParams &p, const CcPiece &w, float *smem) {
     constexpr int kVec = 16 / sizeof(T), kKS = D + 4, kPS = kKeys + 4, kDJ = D / 64;
@@ -325,7 +327,8 @@ __device__ __forceinline__ float4 load_four(const T *p, bool aligned) {
 // themselves (R / 2 values exchanged, then R / 4, ...): li / (L / R) is the row whose logit, maximum and sum a lane ends
 // up with, and it hands the weight to the others.  A warp takes every eighth chunk of 8 keys (which lie in one block), 32 / L
 // keys a step, and requests a step's rows two steps ahead.  A stream moves its maximum only when a logit exceeds it by
-// more than 2^8 (its weights stay below that).
+// more than 2^8 (its weights stay below that).  60 sequences of 1000-2000 tokens, fp32, 32 / 8 heads x 128, 187 us, 4.1
+// TB/s; through shared memory, as the rows kernel has it, 483.
 template <typename T, int D, int R>
 __device__ __forceinline__ void cc_few(const CcParams &p, const CcPiece &w, float *smem) {
     constexpr int L = (R > 4 ? R : 4) * D / 32, kV = D / 4 / L, kWarps = kCcThreads / 32, kSlots = 32 / L;
@@ -572,7 +575,7 @@ struct MergeParams {
 };
 
 constexpr int kMergeThreads = 128;
-constexpr int64_t kFewRows = 5000;
+constexpr int64_t kFewRows = 2100;
 constexpr int kRowsPerWarp = 4;
 
 // The running (M, L, acc) of one row; lane: D / 32 consecutive dims.
@@ -766,9 +769,10 @@ Layout layout(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int
 template <typename T, int D>
 cudaError_t launch_merge(const MergeParams &mg, cudaStream_t stream) {
     // A row has about P / items pieces and an item at most 256 rows, so with few rows there may be many pieces each:
-    // then four warps share them.
+    // then four warps share them.  Else four rows a warp, so that they all are resident at once.  Both ways, 32 / 8 heads x
+    // 128, the whole call with a flushed L2: 64 sequences over 32,768 tokens 68.7 and 72.8 us, 72 79.0 and 74.2, 128 97.4
+    // and 87.1; 64 over 131,072 136.3 and 140.4, 80 187.5 and 183.4; 128 over up to 5120 74.2 and 66.7.
     const int64_t rows = (int64_t)mg.num_seqs * mg.num_heads;
-    // Else four rows a warp, so that they all are resident at once.
     constexpr int kWarps = kMergeThreads / 32, kCta = kWarps * kRowsPerWarp;
     if (rows < kFewRows)
         return launch_dependent(shared_merge_kernel<T, D, kWarps, 1>, dim3((unsigned)rows), dim3(kMergeThreads), 0, stream, mg);

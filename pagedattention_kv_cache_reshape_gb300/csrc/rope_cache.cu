@@ -9,7 +9,8 @@
 // reshape_and_cache's, or quantised from there (q4_format.cuh).  With several
 // position axes (kAxes) pair i takes p = positions[pair_axis[i]][t], so a token's
 // cosines and sines come from up to four rows of the table: they are gathered
-// once a token into shared memory, where all its heads read them.
+// once a token into shared memory, where all its heads read them (8192 tokens 35.8
+// us against 34.6 with one axis, 256 tokens 3.1 against 2.6).
 //
 // Bound by HBM: every row is read and written once.  A thread of the fast
 // kernel owns the two vectors of 8 dims whose elements pair up, so it needs 8
