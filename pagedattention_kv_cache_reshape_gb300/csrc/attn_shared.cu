@@ -482,7 +482,7 @@ __device__ __forceinline__ void own_share(const CcParams &p, int D, Piece piece)
     int64_t t = c < P1 ? share_begin(c, T1, P1) : 0;   // (no share is empty)
     const int64_t t_end = c < P1 ? share_begin(c + 1, T1, P1) : 0;
     while (t < t_end) {
-        const int s = last_at_most(p.own_start, p.num_seqs, t / p.num_kv_heads);
+        const int s = last_at_most_warp(p.own_start, p.num_seqs, t / p.num_kv_heads);
         const int len = p.plan.own_len[s], kt = (len + kKeys - 1) / kKeys;
         const int64_t local = t - p.own_start[s] * p.num_kv_heads;
         const int kvh = (int)(local / kt), tile = (int)(local - (int64_t)kvh * kt);

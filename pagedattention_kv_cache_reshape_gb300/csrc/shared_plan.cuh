@@ -109,8 +109,21 @@ __device__ __forceinline__ int last_at_most(const V *a, int n, X v) {
     return lo;
 }
 
-// The prefix item at tile t of a stream (t < the stream's end); lane: the CTA's place in its team, or -1: the plain
-// stream.
+// The same by a whole warp with the same arguments in every lane: a load for every factor of 32, not of 2.
+template <typename V, typename X>
+__device__ __forceinline__ int last_at_most_warp(const V *a, int n, X v) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
+        lo += (31 - __clz(__ballot_sync(0xffffffffu, i < hi && a[i < hi ? i : lo] <= v))) * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
+}
+
+// The prefix item at tile t of a stream (t < the stream's end), by a whole warp; lane: the CTA's place in its team, or
+// -1: the plain stream.
 struct PrefixItem {
     int g, C;              // group, its shared tokens
     int s0, n;             // the group's first sequence, its sequences
@@ -123,7 +136,7 @@ __device__ __forceinline__ PrefixItem prefix_item(const SharedPlan &plan, const 
                                                   int width, int lane, int64_t t) {
     const int64_t *start = lane < 0 ? plan.tile_start : plan.team_start;
     PrefixItem it;
-    it.g = last_at_most(start, num_groups, t);   // (groups without tiles are passed over)
+    it.g = last_at_most_warp(start, num_groups, t);   // (groups without tiles are passed over)
     it.C = plan.shared_len[it.g];
     it.s0 = __ldg(starts + it.g);
     it.n = __ldg(starts + it.g + 1) - it.s0;
