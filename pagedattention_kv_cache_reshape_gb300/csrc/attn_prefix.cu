@@ -54,9 +54,9 @@ constexpr int kOutWarp = kProducerWarp + 4;
 constexpr int kThreads = 32 * (4 * kMT + 8);
 // Register split: launched at 128 a thread; the softmax warpgroups' share comes from the others'.
 constexpr int kRegsLaunch = 128;
-constexpr int kRegsSide = 56;
-constexpr int kRegsOut = 56;
-constexpr int kRegsSoftmax = 200;
+constexpr int kRegsSide = 64;
+constexpr int kRegsOut = 64;
+constexpr int kRegsSoftmax = 192;
 static_assert(128 * (kRegsSide + kRegsOut) + 128 * kMT * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
 constexpr int kTmemCols = 512;
 
@@ -85,6 +85,19 @@ struct PrefixParams {
     int stall_after;
     int32_t *wait_sites;
 };
+
+// Whether the phase has completed already, in a register that may be used later: the answer travels while products are
+// issued, and a wait is left out where it is yes.
+__device__ __forceinline__ uint32_t peek(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return done;
+}
+__device__ __forceinline__ bool wait_unless(uint32_t done, uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, done != 0) || mbar_wait_warp(bar, parity, limit_ns);
+}
 
 template <int D> struct Shape {
     static constexpr int kDH = D / 64;                 // 64-column planes of a head
@@ -253,6 +266,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto o_col = [](int t) { return (uint32_t)(kMT * BN + t * D); };
     auto slot_of = [](int n) { return n % kSlots; };
     auto phase_of = [](int n) { return (uint32_t)((n / kSlots) & 1); };
+    // a place in the K/V ring
+    struct Ring {
+        int slot;
+        uint32_t phase;
+        __device__ __forceinline__ Ring next() const {
+            Ring r;
+            r.slot = slot + 1 == kSlots ? 0 : slot + 1;
+            r.phase = slot + 1 == kSlots ? phase ^ 1u : phase;
+            return r;
+        }
+    };
     auto take_item = [&](int it, Piece &I) -> bool {
         if (!mbar_wait_warp(item_full + it % kItemSlots, (uint32_t)((it / kItemSlots) & 1), p.wait_ns)) return false;
         I = items[it % kItemSlots];
@@ -366,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ================= TMA producer
         bool ok = true, stopped = false;
         int n = 0, nq = 0, issued_end = 0;   // issued_end: ring entries issued so far
+        Ring at = {0, 0};
         int64_t t_next = range_s[0];
         int place = (int)blockIdx.x % *p.plan.width;      // in the team, whose share comes first; -1: on its own
         // the next piece of this CTA's share, published one piece ahead of its use
@@ -458,20 +483,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    if (lane == 0 && m >= kSlots && !mbar_wait(kv_empty + slot_of(m), phase_of(m) ^ 1u, p.wait_ns))
+                    if (lane == 0 && m >= kSlots && !mbar_wait(kv_empty + at.slot, at.phase ^ 1u, p.wait_ns))
                         ok = false;
                     ok = __shfl_sync(kAll, ok ? 1 : 0, 0) != 0;
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(kv_full + slot_of(m), kSlotBytes);
+                    if (lane == 0) mbar_arrive_expect_tx(kv_full + at.slot, kSlotBytes);
                     __syncwarp();
                     // lane b < per copies block b of K or V
                     if (lane < per) {
-                        uint8_t *dst = kv_s + slot_of(m) * kSlotBytes + lane * (pair ? kBlock2 : kVBlockBytes);
+                        uint8_t *dst = kv_s + at.slot * kSlotBytes + lane * (pair ? kBlock2 : kVBlockBytes);
                         const CUtensorMap *map = kv ? (pair ? &tmap_v2 : &tmap_v) : (pair ? &tmap_k2 : &tmap_k);
-                        if (kv || kB == 8) tma_load_5d(dst, map, 0, 0, 0, I.kvh, cbv, kv_full + slot_of(m));
-                        else tma_load_5d(dst, map, 0, 0, I.kvh * kDH, 0, cbv, kv_full + slot_of(m));
+                        if (kv || kB == 8) tma_load_5d(dst, map, 0, 0, 0, I.kvh, cbv, kv_full + at.slot);
+                        else tma_load_5d(dst, map, 0, 0, I.kvh * kDH, 0, cbv, kv_full + at.slot);
                     }
                     issued_end = m + 1;
+                    at = at.next();
                 }
             }
             n += 2 * I.nkv;
@@ -496,30 +522,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dk = umma_desc_sw128(kv_addr, 16, kKSbo);
         const uint64_t dv = umma_desc_sw128(kv_addr, kVLbo, kVSbo);
         // S_t = Q_tq K^T, K in ring entry nk
-        auto issue_qk = [&](int t, int tq, int nk) {
-            const uint32_t ko = (uint32_t)slot_of(nk) * kSlotBytes;
+        auto issue_qk = [&](int t, int tq, int slot) {
+            const uint32_t ko = (uint32_t)slot * kSlotBytes;
 #pragma unroll
             for (int pl = 0; pl < D / 64; ++pl)
                 umma_bf16_k64(tmem + s_col(t), dq + ((uint32_t)(tq * kQBytes + pl * kPlaneQ) >> 4),
                               dk + ((ko + pl * kKPlane) >> 4), kIdescQK, pl > 0 ? 1u : 0u);
         };
         // O_t (+)= P_t V over keys 64 kq .. 64 kq + 63 (4 MMAs of 16), V in ring entry nv
-        auto issue_pv = [&](int t, int nv, int kq, bool first) {
-            const uint32_t vo = (uint32_t)slot_of(nv) * kSlotBytes;
+        auto issue_pv = [&](int t, int slot, int kq, bool first) {
+            const uint32_t vo = (uint32_t)slot * kSlotBytes;
             umma_bf16_tmem_a_k64(tmem + o_col(t), tmem + s_col(t) + kq * 32, dv + ((vo + kq * kVChunk) >> 4), kIdescPV,
                                  kVS1 >> 4, kVS2 >> 4, (!first || kq > 0) ? 1u : 0u);
         };
         // tiles of two kv-heads: S_t = Q_t K_t^T and O_t (+)= P_t V_t over 64 keys, head t of ring entry nk / nv; b: S's place
         const uint64_t dk2 = umma_desc_sw128(kv_addr, 16, kKSboP), dv2 = umma_desc_sw128(kv_addr, kVLbo, kVSboP);
-        auto issue_qk2 = [&](int t, int b, int nk) {
-            const uint32_t ko = (uint32_t)slot_of(nk) * kSlotBytes + t * (kDH * 1024);
+        auto issue_qk2 = [&](int t, int b, int slot) {
+            const uint32_t ko = (uint32_t)slot * kSlotBytes + t * (kDH * 1024);
 #pragma unroll
             for (int pl = 0; pl < D / 64; ++pl)
                 umma_bf16_k64(tmem + s_col(t) + b * 64, dq + ((uint32_t)(t * kQBytes + pl * kPlaneQ) >> 4),
                               dk2 + ((ko + pl * kKPlane) >> 4), kIdescQK2, pl > 0 ? 1u : 0u);
         };
-        auto issue_pv2 = [&](int t, int b, int nv, bool first) {
-            const uint32_t vo = (uint32_t)slot_of(nv) * kSlotBytes + t * kVBlockBytes;
+        auto issue_pv2 = [&](int t, int b, int slot, bool first) {
+            const uint32_t vo = (uint32_t)slot * kSlotBytes + t * kVBlockBytes;
             umma_bf16_tmem_a_k64(tmem + o_col(t), tmem + s_col(t) + b * 64, dv2 + (vo >> 4), kIdescPV, kVS1p >> 4, kVS2p >> 4,
                                  first ? 0u : 1u);
         };
@@ -545,42 +571,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int no = t ? no1 : no0;
                 return no == 0 || mbar_wait_warp(o_empty + t, (uint32_t)((no - 1) & 1), p.wait_ns);
             };
-            // O_t's half products with V in ring entry nv, as P_t comes; x: M-tile t's tiles so far in this piece
-            auto pv = [&](int t, int nv, int x) -> bool {
+            // O_t's half products with V in the ring's `slot`, as P_t comes; x: M-tile t's tiles so far in this piece; half:
+            // whether its first half was seen to be there
+            auto pv = [&](int t, int slot, int x, uint32_t half) -> bool {
                 const uint32_t ph = (uint32_t)(((t ? J1 : J0) + x) & 1);
                 if (x == 0 && !o_free(t)) return false;
-                if (!mbar_wait_warp(p_half + t, ph, p.wait_ns)) return false;
+                if (!wait_unless(half, p_half + t, ph, p.wait_ns)) return false;
                 tc_fence_after();
-                issue_pv(t, nv, 0, x == 0);
-                if (!mbar_wait_warp(p_full + t, ph, p.wait_ns)) return false;
+                const uint32_t rest = peek(p_full + t, ph);
+                issue_pv(t, slot, 0, x == 0);
+                if (!wait_unless(rest, p_full + t, ph, p.wait_ns)) return false;
                 tc_fence_after();
-                issue_pv(t, nv, 1, x == 0);
+                issue_pv(t, slot, 1, x == 0);
                 return true;
             };
+            auto peek_half = [&](int t, int x) { return peek(p_half + t, (uint32_t)(((t ? J1 : J0) + x) & 1)); };
+            Ring rk = {slot_of(n), phase_of(n)};     // K of the tile at hand
             if (kind == kPair) {
                 // QK_0(j+1) QK_1(j+1) PV_0(j) PV_1(j): the next tile's logits are under way while the softmax
                 // warpgroups turn this one's into weights
 #pragma unroll
                 for (int t = 0; t < kMT; ++t) {
-                    issue_qk2(t, 0, n);
+                    issue_qk2(t, 0, rk.slot);
                     umma_commit(s2_full + t);
                 }
                 if (nkv == 1) umma_commit(q_empty);
-                umma_commit(kv_empty + slot_of(n));
+                umma_commit(kv_empty + rk.slot);
                 for (int j = 0; j < nkv; ++j) {
-                    const int nv = n + 2 * j + 1, nk = n + 2 * j + 2, b = j & 1;
+                    const int nv = n + 2 * j + 1, b = j & 1;
+                    const Ring rv = rk.next();
+                    rk = rv.next();
                     // test hook: stop, leaving ring entries unreleased, so the producer's wait runs out
                     if (p.stall == PA_STALL_CONSUMER && nv >= p.stall_after) { stopped = true; ok = false; break; }
-                    if (!mbar_wait_warp(kv_full + slot_of(nv), phase_of(nv), p.wait_ns)) { ok = false; break; }
+                    if (!mbar_wait_warp(kv_full + rv.slot, rv.phase, p.wait_ns)) { ok = false; break; }
                     if (j + 1 < nkv) {
-                        if (!mbar_wait_warp(kv_full + slot_of(nk), phase_of(nk), p.wait_ns)) { ok = false; break; }
+                        if (!mbar_wait_warp(kv_full + rk.slot, rk.phase, p.wait_ns)) { ok = false; break; }
                         tc_fence_after();
 #pragma unroll
                         for (int t = 0; t < kMT; ++t) {
-                            issue_qk2(t, b ^ 1, nk);
+                            issue_qk2(t, b ^ 1, rk.slot);
                             umma_commit(s2_full + (b ^ 1) * kMT + t);
                         }
-                        umma_commit(kv_empty + slot_of(nk));
+                        umma_commit(kv_empty + rk.slot);
                         if (j + 2 == nkv) umma_commit(q_empty);    // the piece's last QK products
                     }
 #pragma unroll
@@ -591,41 +623,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                             continue;
                         }
                         tc_fence_after();
-                        issue_pv2(t, b, nv, j == 0);
+                        issue_pv2(t, b, rv.slot, j == 0);
                         if (j + 1 == nkv) umma_commit(o_full + t);
                     }
                     if (!ok) break;
-                    umma_commit(kv_empty + slot_of(nv));
+                    umma_commit(kv_empty + rv.slot);
                 }
             } else if (kind == kWide) {
 #pragma unroll
                 for (int t = 0; t < kMT; ++t) {
-                    issue_qk(t, t, n);
+                    issue_qk(t, t, rk.slot);
                     umma_commit(s_full + t);
                 }
                 if (nkv == 1) umma_commit(q_empty);
-                umma_commit(kv_empty + slot_of(n));
+                umma_commit(kv_empty + rk.slot);
+                uint32_t half = 0, v_in = 0, k_in = 0;
                 for (int j = 0; j < nkv; ++j) {
                     const bool next = j + 1 < nkv;
-                    const int nv = n + 2 * j + 1, nk = n + 2 * j + 2;
+                    const int nv = n + 2 * j + 1;
+                    const Ring rv = rk.next();
+                    rk = rv.next();
                     if (p.stall == PA_STALL_CONSUMER && nv >= p.stall_after) { stopped = true; ok = false; break; }
-                    if (!mbar_wait_warp(kv_full + slot_of(nv), phase_of(nv), p.wait_ns)) { ok = false; break; }
+                    if (!wait_unless(v_in, kv_full + rv.slot, rv.phase, p.wait_ns)) { ok = false; break; }
 #pragma unroll
                     for (int t = 0; t < kMT; ++t) {
-                        if (!ok || !pv(t, nv, j)) { ok = false; continue; }
+                        if (t == 0) k_in = peek(kv_full + rk.slot, rk.phase);
+                        if (!ok || !pv(t, rv.slot, j, half)) { ok = false; continue; }
                         if (next) {
-                            if (t == 0 && !mbar_wait_warp(kv_full + slot_of(nk), phase_of(nk), p.wait_ns)) { ok = false; continue; }
+                            if (t == 0 && !wait_unless(k_in, kv_full + rk.slot, rk.phase, p.wait_ns)) { ok = false; continue; }
                             tc_fence_after();
-                            issue_qk(t, t, nk);
+                            if (t == 1) v_in = peek(kv_full + rk.next().slot, rk.next().phase);
+                            half = peek_half(t ^ 1, j + t);
+                            issue_qk(t, t, rk.slot);
                             umma_commit(s_full + t);
                         } else {
+                            half = peek_half(1, j);
                             umma_commit(o_full + t);
                         }
                     }
                     if (!ok) break;
-                    umma_commit(kv_empty + slot_of(nv));
+                    umma_commit(kv_empty + rv.slot);
                     if (next) {
-                        umma_commit(kv_empty + slot_of(nk));
+                        umma_commit(kv_empty + rk.slot);
                         if (j + 2 == nkv) umma_commit(q_empty);    // the piece's last QK products
                     }
                 }
@@ -636,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (x > 0 && p.stall == PA_STALL_CONSUMER && nk >= p.stall_after) { stopped = true; ok = false; break; }
                     if (x > 0 && !mbar_wait_warp(kv_full + slot_of(nk), phase_of(nk), p.wait_ns)) { ok = false; break; }
                     tc_fence_after();
-                    issue_qk(x, 0, nk);
+                    issue_qk(x, 0, slot_of(nk));
                     umma_commit(s_full + x);
                     umma_commit(kv_empty + slot_of(nk));
                 }
@@ -644,12 +683,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int x = 0; ok && x < nkv; ++x) {
                     const int t = x & 1, nv = n + 2 * x + 1, nk = n + 2 * x + 4;
                     if (p.stall == PA_STALL_CONSUMER && nv >= p.stall_after) { stopped = true; ok = false; break; }
-                    if (!mbar_wait_warp(kv_full + slot_of(nv), phase_of(nv), p.wait_ns) || !pv(t, nv, x >> 1)) { ok = false; break; }
+                    if (!mbar_wait_warp(kv_full + slot_of(nv), phase_of(nv), p.wait_ns) || !pv(t, slot_of(nv), x >> 1, 0)) { ok = false; break; }
                     umma_commit(kv_empty + slot_of(nv));
                     if (x + 2 < nkv) {
                         if (!mbar_wait_warp(kv_full + slot_of(nk), phase_of(nk), p.wait_ns)) { ok = false; break; }
                         tc_fence_after();
-                        issue_qk(t, 0, nk);
+                        issue_qk(t, 0, slot_of(nk));
                         umma_commit(s_full + t);
                         umma_commit(kv_empty + slot_of(nk));
                         if (x + 3 == nkv) umma_commit(q_empty);
