@@ -20,9 +20,9 @@
 // pipe, of two 1 us.  So groups of up to 256 rows a kv-head are bound by HBM,
 // larger ones (several items read the same tiles) by the tensor pipe and the
 // softmax beside it.  Measured (32 / 8 heads x 128): 16 sequences over one prefix
-// of 131,072 tokens 91 us, 5.9 TB/s; 256 over 32,768 107 us, the tensor pipe 73 %
-// busy (a tile of two M-tiles takes about 2780 cycles, its products 2048); 24
-// groups of 8 over up to 4096 tokens, 32 heads, 167 us beside the decode kernel,
+// of 131,072 tokens 89 us, 6.0 TB/s; 256 over 32,768 104 us, the tensor pipe 75 %
+// busy (a tile of two M-tiles takes about 2700 cycles, its products 2048); 24
+// groups of 8 over up to 4096 tokens, 32 heads, 165 us beside the decode kernel,
 // 5.2 TB/s: there an SM waits for its ring of tiles, 56-58 GB/s a SM.
 //
 // Roles (512 threads): warps 0-7 two softmax warpgroups (thread = row = TMEM
