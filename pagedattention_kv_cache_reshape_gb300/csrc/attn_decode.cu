@@ -188,8 +188,8 @@ __device__ void shared_plan_cta(const SharedGroups &g, const SharedPlan &plan, c
         if (act > few) act = (int)few;
         const int most = sum.prefix > 0 && split.grid > 1 ? split.grid - 1 : split.grid;
         act = act < 1 ? 1 : (act > most ? most : act);
-        const int odd = (split.grid - act) % sum.width;   // whole teams, if there is one
-        if (split.grid - act > odd) act += odd;
+        const int left = split.grid - act;   // whole teams; one at least, or nobody would take the teams' stream
+        if (left > 0) act += left > sum.width ? left % sum.width : left - sum.width;
         *split.active = act;
         *split.prefix_shares = min(split.grid - act > 0 ? split.grid - act : split.grid, split.prefix_grid);
     }

@@ -851,7 +851,7 @@ cudaError_t launch_tc(const AttnArgs &a, const int32_t *group_starts, const int3
     const int (&tile_ns)[3] = kTcTileNs[a.head_dim == 64 ? 0 : 1];
     SharedJob job;
     job.groups = {a.context_lens, group_starts, prefix_lens, a.num_seqs, num_groups, a.num_kv_heads, a.block_size,
-                  (int64_t)a.max_blocks * a.block_size, spi, kPrefixKeys, pair, kMaxTeam, 16,
+                  (int64_t)a.max_blocks * a.block_size, spi, kPrefixKeys, pair, device_sm_count() > 2 * kMaxTeam ? kMaxTeam : 1, 16,
                   split_decode_unit_ns(a.num_heads, a.num_kv_heads, a.head_dim), {spi / 2, spi / 2},
                   {tile_ns[0], tile_ns[0], tile_ns[1], tile_ns[2]}, kTcItemNs, kLeastSavedNs * device_sm_count(),
                   kLongPrefix};

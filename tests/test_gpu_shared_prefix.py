@@ -257,6 +257,18 @@ def test_rows_that_start_anywhere(dtype):
     assert out.data_ptr() % 16 and want.shape == out.shape
 
 
+@pytest.mark.parametrize("sequences", [129, 176, 257, 300, 385, 512])
+@pytest.mark.parametrize("own", [1, 300, 2000])
+def test_teams_whose_part_is_little_work(sequences, own):
+    """A group of several items, which take a team of as many CTAs, beside so much other work that the team's own
+    share of the SMs would be less than one CTA each."""
+    groups = [(40, 0), (2, 90), (sequences, 83), (1, 2040), (9, 35)]
+    c = Case(groups, [own, 32, 32, 1, 2, own], 2, 1, 64, 32, torch.bfloat16, seed=sequences)
+    c.rows = [0, 41, 42, 43, 44, 42 + 127, 42 + 128, 42 + sequences - 1, c.S - 1]
+    for ws in (c.workspace(0xFF), c.workspace(0)):
+        c.run_checked(workspace=ws)
+
+
 @pytest.mark.parametrize("dtype", DTYPES, **ids)
 @pytest.mark.parametrize("prefix", [0, 2048])
 def test_what_comes_behind_a_call_sees_its_rows(prefix, dtype):
