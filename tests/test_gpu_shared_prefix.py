@@ -257,6 +257,22 @@ def test_rows_that_start_anywhere(dtype):
     assert out.data_ptr() % 16 and want.shape == out.shape
 
 
+@pytest.mark.parametrize("dtype", DTYPES, **ids)
+def test_two_calls_at_once(dtype):
+    """On two streams, each with a workspace and an output of its own, several calls in flight on both."""
+    cases = [Case([(20, 640), (5, 0), (9, 96)], [5, 40, 200], 32, 8, 128, 16, dtype, seed=19),
+             Case([(70, 1024), (3, 64)], [200, 3], 8, 2, 128, 16, dtype, seed=20)]
+    want = [c.run() for c in cases]
+    ws, out = [c.workspace() for c in cases], [[torch.zeros_like(c.q) for _ in range(8)] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for j, c in enumerate(cases):
+            c.run(out=out[j][i], workspace=ws[j], stream=streams[j])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[j]) for j in range(2) for o in out[j])
+
+
 @pytest.mark.parametrize("sequences", [129, 176, 257, 300, 385, 512])
 @pytest.mark.parametrize("own", [1, 300, 2000])
 def test_teams_whose_part_is_little_work(sequences, own):
