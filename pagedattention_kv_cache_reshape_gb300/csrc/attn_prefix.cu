@@ -307,7 +307,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const float2 a = ml_s[r], b = ml_s[BM + r];
-                const float M = fmaxf(a.x, b.x), fa = fast_exp2(a.x - M), fb = fast_exp2(b.x - M);
+                const float M = fmaxf(a.x, b.x), ref = M == -INFINITY ? 0.f : M;   // (-inf: only logits of -inf)
+                const float fa = fast_exp2(a.x - ref), fb = fast_exp2(b.x - ref);
                 const bool row_valid = head < p.group && i_pos < I.nseq;
                 const int64_t row = I.row + (row_valid ? (int64_t)i_pos * p.group + head : 0);
                 float *dst = p.o + row * D;
@@ -738,8 +739,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // One tile: S to P.  S is read whole and its max taken first; 128 keys of P then go out in two halves (the
             // tensor pipe takes the first while the second is computed).  The piece's first tile takes its own max;
             // later ones run with the running max m: P stays <= 2^8 unless the tile's max exceeds it by more than 8,
-            // and then (rarely) the row moves its max and rescales O first.  lim: shared keys from the tile's first on;
-            // nv: ring entry of the last tile's values.  bar, out: S written, P's first half (all 64 keys) written.
+            // and then (rarely) the row moves its max and rescales O first.  While all logits were -inf the max stays
+            // -inf, the weights 0 (taken against 0), and the first finite tile moves it, however low it lies.  lim: shared
+            // keys from the tile's first on; nv: ring entry of the last tile's values.  bar, out: S written, P's first
+            // half (all 64 keys) written.
             auto tile = [&](auto keys, uint32_t col, uint64_t *bar, uint64_t *out, uint32_t phase, int lim, bool first,
                             int nv) -> bool {
                 constexpr int kN = decltype(keys)::value;
@@ -777,12 +780,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float m_tile = fmaxf(a0, a1) * sl2;
                 if (first) {
-                    m = m_tile == -INFINITY ? 0.f : m_tile;
+                    m = m_tile;
                 } else {
                     const bool need = m_tile > m + 8.f;
                     if (__any_sync(kAll, need)) {
-                        const float m_new = need ? m_tile : m;
-                        const float alpha = fast_exp2(m - m_new);
+                        const float alpha = need ? fast_exp2(m - m_tile) : 1.f;
                         l *= alpha;
                         // O_t's earlier products are done: with 128 keys they completed before this S was committed;
                         // with 64, whose S comes a tile early, their values' ring entry must have been released (it
@@ -799,12 +801,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
                             tmem_st32(lane_addr + o_col(t) + 32 * c, o);
                         }
-                        m = m_new;
+                        if (need) m = m_tile;
                     }
                 }
                 // P for 32 key pairs into pk, rounded to bf16 (the products' operand type): independent roundings of
                 // half a step, beside a result rounded to bf16 itself; l sums the unrounded values
-                const float2 sl2x2 = make_float2(sl2, sl2), negm = make_float2(-m, -m);
+                const float neg = m == -INFINITY ? 0.f : -m;
+                const float2 sl2x2 = make_float2(sl2, sl2), negm = make_float2(neg, neg);
                 float2 ls = make_float2(0.f, 0.f);
                 uint32_t pk[32];
                 auto pass = [&](auto u0c) {

@@ -1,0 +1,71 @@
+"""Keys with infinities, whose logits are minus infinity over whole tiles, units or pieces: such keys have weight 0 and
+take no part in the maximum, however small the other logits are; where no key is left the result is NaN."""
+import pytest
+import torch
+
+from shared_prefix_checks import DEV, HALF, Case
+from test_gpu_rope_q4 import _lib  # noqa: F401  (builds and loads the library)
+
+pytestmark = pytest.mark.gpu
+DTYPES = [torch.bfloat16, torch.float32]
+ids = dict(ids=lambda v: str(v).replace("torch.", ""))
+INF = float("inf")
+
+
+def lowered(c, low=-2000.0):
+    """Dim 0 of the queries is positive, so that a key's dim 0 of -inf makes its logit -inf; dim 1 is 1 and every key's
+    dim 1 is `low`: all logits lie about low / sqrt(D) * log2(e) below 0, -255 in powers of two at 128 dims."""
+    c.q[..., 0] = c.q[..., 0].abs() + 0.25
+    c.q[..., 1] = 1.0
+    c.k[..., 1] = torch.where(torch.isnan(c.k[..., 1]), c.k[..., 1], torch.full_like(c.k[..., 1], low))
+    return c
+
+
+def drop(c, s, first, last, head):
+    """Tokens first .. last - 1 of sequence s: keys of kv-head `head` with -inf in dim 0."""
+    t = torch.arange(first, last, device=DEV)
+    c.k[c.bt[s].long()[t // c.B], t % c.B, head, 0] = -INF
+
+
+def check(c, out, rows):
+    """out against the definition in 64 bits over the keys whose logit is not -inf.
+
+    As shared_prefix_checks states it: a logit's error is 2 (D + 8) 2^-24 mag, mag the largest sum of |scale q k| of
+    those keys; the exponential's 2^-21, sums and joins (2 n + 600) 2^-24; one rounding of the weights to bf16, one of
+    the result."""
+    half, bf, G = HALF[c.dtype], c.dtype == torch.bfloat16, c.H // c.Hkv
+    for s in rows:
+        n = c.lens[s]
+        blocks = c.bt[s, :-(-n // c.B)].long()
+        k, v = (t[blocks].reshape(-1, c.Hkv, c.D)[:n].double().transpose(0, 1) for t in (c.k, c.v))
+        q = c.q[s].double().view(c.Hkv, G, c.D)
+        for h in range(c.Hkv):
+            keep = torch.isfinite(k[h]).all(-1)
+            got = out[s].double().view(c.Hkv, G, c.D)[h]
+            if not bool(keep.any()):
+                assert torch.isnan(got).all(), f"row {s}, kv-head {h}: no key is left"
+                continue
+            kk, vv = k[h][keep], v[h][keep]
+            w = torch.softmax(q[h] @ kk.T * c.scale, -1)
+            mag = (q[h].abs() @ kk.abs().T * abs(c.scale)).amax(-1, keepdim=True)
+            ref, spread = w @ vv, w @ vv.abs()
+            e_w = 2 * (c.D + 8) * 2.0 ** -24 * mag + 2.0 ** -21 + (2 * n + 600) * 2.0 ** -24
+            tol = 2 * e_w * spread + half * ref.abs() + (half * spread if bf else 0.0) + 1e-30
+            err = (got - ref).abs()
+            assert bool((err <= tol).all()), f"row {s}, kv-head {h} ({n} tokens): {float((err / tol).max()):.3g} of the bound"
+
+
+# H, Hkv, D, B, sequences of the group: two kv-heads at a time, an odd number of kv-heads, more rows than an M-tile,
+# a group over several items
+SHARED = [(8, 2, 128, 16, 20), (6, 3, 64, 8, 9), (32, 8, 128, 16, 48), (16, 1, 64, 32, 70), (5, 5, 128, 32, 200)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, **ids)
+@pytest.mark.parametrize("H,Hkv,D,B,n", SHARED)
+@pytest.mark.parametrize("first,last", [(0, 64), (0, 128), (0, 300), (128, 384), (0, 2047), (0, 2048), (1, 2048), (640, 2048)])
+def test_shared_keys(first, last, H, Hkv, D, B, n, dtype):
+    """The shared part's first tile, several, tiles in its middle, all of its keys but one, all of them."""
+    c = lowered(Case([(n, 2048)], [30, 7, 200], H, Hkv, D, B, dtype, seed=D + n, anchor=True))
+    head = Hkv - 1
+    drop(c, 0, first, last, head)
+    check(c, c.run(), sorted({0, 1, n // 2, n - 1}))
