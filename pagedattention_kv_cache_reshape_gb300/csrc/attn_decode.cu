@@ -968,11 +968,12 @@ __global__ void __launch_bounds__(32 * (kMaxConsumerWarps + 1), 1)
                     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
                     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
                 }
-                // ntok >= 1, so every column has a finite max
+                // (a unit of keys whose logits are all -inf: the max stays -inf, the weights, taken against 0, are 0)
                 const float mn0 = fmaxf(m_run[0], mx0), mn1 = fmaxf(m_run[1], mx1);
-                const float al0 = fast_exp2(m_run[0] - mn0), al1 = fast_exp2(m_run[1] - mn1);
-                const float p0 = fast_exp2(x[0] - mn0), p1 = fast_exp2(x[1] - mn1);
-                const float p2 = fast_exp2(x[2] - mn0), p3 = fast_exp2(x[3] - mn1);
+                const float r0 = mn0 == -INFINITY ? 0.f : mn0, r1 = mn1 == -INFINITY ? 0.f : mn1;
+                const float al0 = fast_exp2(m_run[0] - r0), al1 = fast_exp2(m_run[1] - r1);
+                const float p0 = fast_exp2(x[0] - r0), p1 = fast_exp2(x[1] - r1);
+                const float p2 = fast_exp2(x[2] - r0), p3 = fast_exp2(x[3] - r1);
                 l_part[0] = l_part[0] * al0 + (p0 + p2);
                 l_part[1] = l_part[1] * al1 + (p1 + p3);
                 m_run[0] = mn0;

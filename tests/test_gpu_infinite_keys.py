@@ -3,6 +3,8 @@ take no part in the maximum, however small the other logits are; where no key is
 import pytest
 import torch
 
+from pagedattention_kv_cache_reshape_gb300 import pa
+
 from shared_prefix_checks import DEV, HALF, Case
 from test_gpu_rope_q4 import _lib  # noqa: F401  (builds and loads the library)
 
@@ -69,3 +71,30 @@ def test_shared_keys(first, last, H, Hkv, D, B, n, dtype):
     head = Hkv - 1
     drop(c, 0, first, last, head)
     check(c, c.run(), sorted({0, 1, n // 2, n - 1}))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, **ids)
+@pytest.mark.parametrize("H,Hkv,D,B", [(8, 2, 128, 16), (33, 3, 64, 8), (32, 8, 128, 32), (4, 4, 64, 16)])
+def test_own_keys(H, Hkv, D, B, dtype):
+    """A sequence's own part: its first keys, its last, all of them; with the shared ones gone too, no key is left."""
+    c = lowered(Case([(20, 2048)], [30, 700, 1500], H, Hkv, D, B, dtype, seed=3, anchor=True))
+    for s, (a, b) in ((0, (0, 16)), (1, (0, 200)), (2, (0, 1500)), (3, (0, 30)), (4, (16, 700)), (5, (1, 1500))):
+        drop(c, s, 2048 + a, 2048 + b, 0)
+    check(c, c.run(), range(8))
+    drop(c, 0, 0, 2048, 0)
+    check(c, c.run(), range(8))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, **ids)
+@pytest.mark.parametrize("H,Hkv,D,B", [(8, 2, 128, 16), (33, 3, 64, 8), (32, 8, 128, 32), (4, 4, 64, 16)])
+@pytest.mark.parametrize("own", [[16, 17, 40], [700, 5000, 33], [20000, 40]])
+def test_decode(own, H, Hkv, D, B, dtype):
+    """pa.decode: sequences in one piece and in many; units of 16 keys and whole pieces without a finite logit."""
+    c = lowered(Case([(2 * len(own), 0)], own, H, Hkv, D, B, dtype, seed=4))
+    for i, n in enumerate(own):
+        drop(c, i, 0, 16, 0)                         # the first unit
+        drop(c, i, n * 2 // 3 // 16 * 16, n - 1, 0)  # whole pieces, up to the last key
+        drop(c, len(own) + i, 0, n - 1, Hkv - 1)     # all but the last key
+    check(c, pa.decode(c.q, c.k, c.v, c.bt, c.ctx, c.scale), range(c.S))
+    drop(c, 0, 0, own[0], 0)
+    check(c, pa.decode(c.q, c.k, c.v, c.bt, c.ctx, c.scale), range(c.S))
