@@ -499,7 +499,7 @@ __device__ __forceinline__ void merge_pieces(const DecodeParams &p, int64_t vs, 
         for (int k = 0; k < kBatch; ++k)
 #pragma unroll
             for (int hh = 0; hh < kH; ++hh) {
-                if (!use[k] || ml[k][hh].x == -INFINITY) continue;
+                if (!use[k] || ml[k][hh].y == 0.f) continue;   // nothing seen (a NaN stays)
                 const float Mn = fmaxf(M[hh], ml[k][hh].x);
                 const float a = fast_exp2(M[hh] - Mn), b = fast_exp2(ml[k][hh].x - Mn);
                 L[hh] = L[hh] * a + ml[k][hh].y * b;
@@ -585,7 +585,7 @@ __device__ __forceinline__ void merge_group(const DecodeParams &p, int64_t slot0
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int hh = 0; hh < kH; ++hh) {
-                if (k0 + k >= cnt || ml[k][hh].x == -INFINITY) continue;
+                if (k0 + k >= cnt || ml[k][hh].y == 0.f) continue;   // nothing seen (a NaN stays)
                 const float Mn = fmaxf(M[hh], ml[k][hh].x);
                 const float a = fast_exp2(M[hh] - Mn), b = fast_exp2(ml[k][hh].x - Mn);
                 L[hh] = L[hh] * a + ml[k][hh].y * b;

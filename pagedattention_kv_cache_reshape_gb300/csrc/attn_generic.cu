@@ -124,17 +124,13 @@ __global__ void __launch_bounds__(kThreads)
                 tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, off));
             const float m_old = m_s[h];
             const float m_new = fmaxf(m_old, tmax);
-            float alpha, sum = 0.f;
-            if (m_new == -INFINITY) {
-                alpha = 1.f;
-                for (int jj = lane; jj < kTile; jj += 32) p_s[h * kTile + jj] = 0.f;
-            } else {
-                alpha = expf(m_old - m_new);
-                for (int jj = lane; jj < kTile; jj += 32) {
-                    const float p = jj < jn ? expf(p_s[h * kTile + jj] - m_new) : 0.f;
-                    p_s[h * kTile + jj] = p;
-                    sum += p;
-                }
+            const float ref = m_new == -INFINITY ? 0.f : m_new;   // no logit above -inf yet: weights 0 (a NaN stays)
+            const float alpha = expf(m_old - ref);
+            float sum = 0.f;
+            for (int jj = lane; jj < kTile; jj += 32) {
+                const float p = jj < jn ? expf(p_s[h * kTile + jj] - ref) : 0.f;
+                p_s[h * kTile + jj] = p;
+                sum += p;
             }
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);

@@ -98,3 +98,35 @@ def test_decode(own, H, Hkv, D, B, dtype):
     check(c, pa.decode(c.q, c.k, c.v, c.bt, c.ctx, c.scale), range(c.S))
     drop(c, 0, 0, own[0], 0)
     check(c, pa.decode(c.q, c.k, c.v, c.bt, c.ctx, c.scale), range(c.S))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, **ids)
+@pytest.mark.parametrize("own", [[40], [5000], [20000, 40]])
+def test_a_piece_of_nan_logits_stays_nan(own, dtype):
+    """Keys that are NaN over whole units and pieces, or everywhere: their rows are NaN, the other kv-head's are not."""
+    c = Case([(2 * len(own), 0)], own, 8, 2, 128, 16, dtype, seed=5)
+    want = pa.decode(c.q, c.k, c.v, c.bt, c.ctx, c.scale)
+    n = own[0]
+    for first, last in ((0, 16), (0, n // 2 // 16 * 16), (n // 2 // 16 * 16, n), (0, n)):
+        k = c.k.clone()
+        t = torch.arange(first, last, device=DEV)
+        k[c.bt[0].long()[t // 16], t % 16, 1, 5] = float("nan")
+        for out in (pa.decode(c.q, k, c.v, c.bt, c.ctx, c.scale), c.run(k_cache=k)):
+            assert torch.isnan(out[0, 4:]).all(), (first, last)
+            assert not torch.isnan(out[0, :4]).any() and not torch.isnan(out[1:]).any()
+    assert not torch.isnan(want).any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, **ids)
+@pytest.mark.parametrize("H,Hkv,D,B,n", SHARED)
+def test_shared_keys_that_are_nan(H, Hkv, D, B, n, dtype):
+    """Over one tile, several or all: every row of the group is NaN at that kv-head, all others are not."""
+    c = Case([(n, 2048), (3, 0)], [30, 7, 200], H, Hkv, D, B, dtype, seed=D + n, anchor=True)
+    G = H // Hkv
+    for first, last in ((0, 128), (256, 900), (0, 2048)):
+        k = c.k.clone()
+        t = torch.arange(first, last, device=DEV)
+        k[c.bt[0].long()[t // B], t % B, Hkv - 1, 5] = float("nan")
+        out = torch.isnan(c.run(k_cache=k))
+        assert out[:n, H - G:].all(), (first, last)
+        assert not out[:n, :H - G].any() and not out[n:].any()
