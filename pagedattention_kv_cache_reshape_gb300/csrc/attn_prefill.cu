@@ -626,13 +626,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 max_of(2);
                 max_of(3);
                 const float m_tile = fmaxf(a0, a1) * sl2;
-                if (j == 0 && m == -INFINITY) {
-                    m = m_tile == -INFINITY ? 0.f : m_tile;   // the item's first tile: its own max
+                // (while all logits were -inf the max stays -inf, the weights, taken against 0, are 0, and the first
+                // finite tile moves it, however low it lies)
+                if (j == 0) {
+                    m = m_tile;   // the item's first tile: its own max
                 } else {
                     const bool need = m_tile > m + 8.f;
                     if (__any_sync(kFull, need)) {
-                        const float m_new = need ? m_tile : m;
-                        const float alpha = fast_exp2(m - m_new);
+                        const float alpha = need ? fast_exp2(m - m_tile) : 1.f;
                         l *= alpha;
                         // PV_t(j-1) completed before S_t(j) was committed, so O_t is final here
 #pragma unroll 1
@@ -644,12 +645,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
                             tmem_st32(lane_addr + o_col(t) + 32 * c, o);
                         }
-                        m = m_new;
+                        if (need) m = m_tile;
                     }
                 }
                 // P = 2^(S * scale*log2e - m) for key pairs u0..u0+31 into pk; the
                 // exponent's FMA and the sums as packed fp32 pairs
-                const float2 sl2x2 = make_float2(sl2, sl2), negm = make_float2(-m, -m);
+                const float neg = m == -INFINITY ? 0.f : -m;
+                const float2 sl2x2 = make_float2(sl2, sl2), negm = make_float2(neg, neg);
                 float2 ls = make_float2(0.f, 0.f);
                 uint32_t pk[BN / 4];
                 auto pass = [&](auto u0c) {

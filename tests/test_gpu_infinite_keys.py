@@ -130,3 +130,22 @@ def test_shared_keys_that_are_nan(H, Hkv, D, B, n, dtype):
         out = torch.isnan(c.run(k_cache=k))
         assert out[:n, H - G:].all(), (first, last)
         assert not out[:n, :H - G].any() and not out[n:].any()
+
+
+@pytest.mark.parametrize("H,Hkv,D,B", [(8, 2, 128, 16), (16, 1, 64, 32), (4, 4, 64, 8)])
+@pytest.mark.parametrize("cached,rows", [(0, 300), (700, 40), (2000, 257)])
+def test_prefill(cached, rows, H, Hkv, D, B):
+    """pa.varlen_prefill of one chunk behind `cached` tokens, its first keys without a finite logit."""
+    dtype, n = torch.bfloat16, cached + rows
+    c = lowered(Case([(1, 0)], [n], H, Hkv, D, B, dtype, seed=6))
+    q = torch.randn(rows, H, D, generator=torch.Generator().manual_seed(7)).to(dtype).to(DEV)
+    q[..., 0] = q[..., 0].abs() + 0.25
+    q[..., 1] = 1.0
+    cu = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    for last in (128, 256, 301):
+        drop(c, 0, 0, min(last, n), 0)
+        out = pa.varlen_prefill(q, cu, c.k, c.v, c.bt, c.ctx, c.scale, rows)
+        for r in sorted({0, 1, 127, 128, rows - 1} & set(range(rows))):
+            row = Case.__new__(Case)
+            row.__dict__.update(c.__dict__, q=q[r:r + 1], lens=[cached + r + 1])
+            check(row, out[r:r + 1], [0])
