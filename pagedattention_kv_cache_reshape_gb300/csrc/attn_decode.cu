@@ -65,6 +65,17 @@ constexpr int kMaxSeqsEarlyPrefetch = 4096;   // the early prefetch reads every 
 constexpr int kPartialCtas = 512;   // partial slots reserved for CTA boundaries
 constexpr int kPlanThreads = 256;
 constexpr int kSmemBudget = 227 * 1024;
+// what a plan launch plans beside the block stream: nothing, prefill chunks, groups with shared prefixes
+constexpr int kPlain = 0, kMixed = 1, kPrefixes = 2;
+// Most dynamic shared memory of any call's decode kernel (stages_for: 1024 bytes and up to 8 stages, multiples of 1024
+// with a header and two barriers each) and of any call's plan: what the kernels' attributes are set to, always the same,
+// so that host threads with calls of different sizes never lower each other's limit.
+constexpr int kSmemMost = kSmemBudget - 1024 + 8 * 48;
+template <int kMode> constexpr int plan_smem_most() {
+    const int prefix = 4 * (kMaxSeqs + 1);
+    if (kMode == kPrefixes) return prefix + 2 * 4 * kMaxPrefixGroups;
+    return kMode == kMixed && prefix < kPrefillPlanSmem ? kPrefillPlanSmem : prefix;
+}
 // Per-SM rates for splitting the SMs between the decode rows and a concurrent
 // prefill kernel (GB300): the tcgen05 prefill kernel sustains about 7.6
 // TFLOP/s per SM on causal chunks alone, but beside the decode kernel the
@@ -203,7 +214,6 @@ __device__ void shared_plan_cta(const SharedGroups &g, const SharedPlan &plan, c
 // kGroups: it has shared prefixes, which the stream leaves out (every plan CTA
 // finds them itself; the last CTA writes the groups' plan and sets the split);
 // decode-only calls run the plain instantiation.
-constexpr int kPlain = 0, kMixed = 1, kPrefixes = 2;
 template <int kMode>
 __global__ void __launch_bounds__(kPlanThreads)
     decode_plan_kernel(const int32_t *__restrict__ context_lens,
@@ -1212,7 +1222,8 @@ cudaError_t launch_main(const DecodeParams &prm, const CUtensorMap &mk, const CU
     const int stage_bytes = (int)align_up(2 * kv_tile + prm.qh * D * 2, 1024);
     const size_t smem = 1024 + (size_t)prm.num_stages * (stage_bytes + sizeof(StageHeader) + 16);
     auto kern = split_decode_kernel<D, kTwo, kPart>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > kSmemMost) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
     if (e != cudaSuccess) return e;
     if (timed) timing_begin(stream);
     e = launch_dependent(kern, dim3(grid), dim3(32 * (prm.kvh * prm.wpk + 1)), smem, stream, mk, mv, prm);
@@ -1337,7 +1348,9 @@ cudaError_t launch_split_decode(const AttnArgs &a, void *workspace, size_t works
     if (share_sms && plan_smem < (size_t)kPrefillPlanSmem) plan_smem = kPrefillPlanSmem;
     if (shared) plan_smem += 2 * sizeof(int32_t) * (size_t)shared->groups.num_groups;
     auto plan_kern = share_sms ? decode_plan_kernel<kMixed> : shared ? decode_plan_kernel<kPrefixes> : decode_plan_kernel<kPlain>;
-    cudaError_t e = cudaFuncSetAttribute(plan_kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan_smem);
+    const int plan_most = share_sms ? plan_smem_most<kMixed>() : shared ? plan_smem_most<kPrefixes>() : plan_smem_most<kPlain>();
+    if (plan_smem > (size_t)plan_most) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(plan_kern, cudaFuncAttributeMaxDynamicSharedMemorySize, plan_most);
     if (e != cudaSuccess) return e;
     const int64_t max_entries = (int64_t)a.num_seqs * max_units(a.max_blocks, B);
     const int sms = device_sm_count();

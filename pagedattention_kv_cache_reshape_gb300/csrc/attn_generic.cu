@@ -175,12 +175,13 @@ __global__ void __launch_bounds__(kThreads)
 template <typename T, int D>
 cudaError_t launch_typed(const AttnArgs &a, int row_filter, cudaStream_t stream) {
     const int G = a.num_heads / a.num_kv_heads;
-    const size_t smem = sizeof(float) * (2 * G * D + G * kTile + 3 * G) + sizeof(int) * kTile;
+    auto bytes = [](int g) { return (int)(sizeof(float) * (2 * g * D + g * kTile + 3 * g) + sizeof(int) * kTile); };
     auto kern = generic_attention_kernel<T, D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the largest size always, so that host threads with calls of different sizes never lower each other's limit
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(kMaxGroup));
     if (e != cudaSuccess) return e;
     dim3 grid(a.total_q, a.num_kv_heads);
-    kern<<<grid, kThreads, smem, stream>>>(a, row_filter);
+    kern<<<grid, kThreads, bytes(G), stream>>>(a, row_filter);
     return cudaGetLastError();
 }
 

@@ -26,7 +26,6 @@ namespace {
 
 constexpr int kPlanThreads = 256;
 constexpr int kPlanSmemGroups = 4096;   // group starts and smallest contexts kept in shared memory
-constexpr int kMaxTcGroups = 16384;
 // Nanoseconds of an SM for a tile of the prefix kernel: head_dim 64, 128; 128 keys of one M-tile, of two, 64 keys of two
 // kv-heads; and for an item's begin and end.  The SMs' split follows them, so they were set by sweeps of it.
 constexpr int kTcTileNs[2][3] = {{800, 1100, 800}, {1500, 1850, 1450}};
@@ -840,7 +839,7 @@ TcLayout tc_layout(int num_seqs, int num_groups, int num_heads, int num_kv_heads
 // that of the unscaled products) and groups whose starts the plan's CTAs hold in shared memory.
 bool tc_supported(const AttnArgs &a, int num_groups) {
     return split_decode_supported(a) && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.scale > 0.f &&
-           a.scale < INFINITY && num_groups <= kMaxTcGroups;
+           a.scale < INFINITY && num_groups <= kMaxPrefixGroups;
 }
 
 cudaError_t launch_tc(const AttnArgs &a, const int32_t *group_starts, const int32_t *prefix_lens, int num_groups,

@@ -117,6 +117,7 @@ struct KvWriteArgs {
 // A batch in groups with shared prefixes: the decode kernel computes the
 // sequences' own parts, the prefix kernel the shared ones.
 constexpr int kPrefixKeys = 128;        // keys per tile of the prefix kernel
+constexpr int kMaxPrefixGroups = 16384; // whose starts and lengths the plan's CTAs hold in shared memory
 constexpr int kMaxPrefixCtas = 160;     // rows reserved for shares' first pieces
 struct SharedJob {
     SharedGroups groups;
