@@ -835,11 +835,10 @@ TcLayout tc_layout(int num_seqs, int num_groups, int num_heads, int num_kv_heads
     return w;
 }
 
-// The tensor-core path takes what the split decode takes, rows on 16 bytes, a positive scale (the running maximum is
-// that of the unscaled products) and groups whose starts the plan's CTAs hold in shared memory.
+// The tensor-core path takes what the split decode takes (out on 4 bytes: no kernel stores wider to it), a positive scale
+// (the running maximum is that of the unscaled products) and groups whose starts the plan's CTAs hold in shared memory.
 bool tc_supported(const AttnArgs &a, int num_groups) {
-    return split_decode_supported(a) && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.scale > 0.f &&
-           a.scale < INFINITY && num_groups <= kMaxPrefixGroups;
+    return split_decode_supported(a) && a.scale > 0.f && a.scale < INFINITY && num_groups <= kMaxPrefixGroups;
 }
 
 cudaError_t launch_tc(const AttnArgs &a, const int32_t *group_starts, const int32_t *prefix_lens, int num_groups,
