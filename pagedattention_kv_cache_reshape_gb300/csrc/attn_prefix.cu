@@ -108,7 +108,10 @@ template <int D> struct Shape {
     static constexpr int kFit = (int)((kSmemLimit - kMT * kQBytes - kBarBytes) / kSlotBytes);
     static constexpr int kSlots = kFit < 8 ? kFit : 8;  // K/V ring depth
     static constexpr size_t kSmem = (size_t)kMT * kQBytes + (size_t)kSlots * kSlotBytes + kBarBytes;
-    static_assert(kSlots >= 3, "the K/V ring needs at least three slots");
+    // kPair's softmax looks at the phase of V's entry of tile j - 1 until its own weights of tile j are out.  The same slot
+    // must not be released again before that: with three slots it would be by tile j + 1's K, whose product waits for no
+    // weights; with four it is by tile j + 1's V, whose product waits for them.
+    static_assert(kSlots >= 4, "the K/V ring needs at least four slots");
     static_assert(kSmem <= kSmemLimit, "shared memory");
 };
 
