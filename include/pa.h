@@ -224,7 +224,10 @@ PA_API size_t pa_decode_shared_prefix_workspace_size(int num_seqs, int num_group
  *                whole blocks, and no sequence's last token, are taken as
  *                shared, so any length up to the true one will do.
  *  block_tables  as for pa_decode, every row whole: entries of a group's shared
- *                blocks are read from the row of its first sequence
+ *                blocks are read from the row of its first sequence (also
+ *                where that sequence's context length is out of range); one
+ *                out of range there leaves the rows of the whole group
+ *                unspecified
  *  workspace     >= pa_decode_shared_prefix_workspace_size(...) bytes, 16-byte
  *                aligned; its contents on entry do not matter; calls that may
  *                overlap on the GPU take workspaces of their own
@@ -235,7 +238,9 @@ PA_API size_t pa_decode_shared_prefix_workspace_size(int num_seqs, int num_group
  * range, set PA_ERR_OUT_OF_RANGE in *dev_status, and the call (the group) is
  * computed as if nothing were shared.  Precondition (not checked on the
  * device): the blocks that hold a group's shared tokens are the same in all
- * its tables, or hold the same tokens.  Results are deterministic: they depend
+ * its tables, or hold the same tokens.  A batch that shares little is served
+ * quicker by pa_decode (256 sequences of 16-4096 tokens that share nothing 88 us,
+ * by this call 94).  Results are deterministic: they depend
  * on the inputs and the device's SM count, never on which blocks hold the data.
  */
 PA_API pa_status pa_decode_shared_prefix(void *out, const void *q, const void *k_cache,

@@ -12,8 +12,8 @@
 // number of tiles whatever the group sizes; a share holds a few pieces of items,
 // usually one or two.  Items that read the same tiles go to teams of CTAs that
 // read them together: 256 sequences (4 items a kv-head) over 32,768 tokens read
-// 137 MB from HBM instead of 406 MB, and the call takes 130 us instead of 149
-// (teams of at most two: 136).
+// 137 MB from HBM instead of 406 MB, and the call took 130 us instead of 149
+// (teams of at most two: 136) when they were introduced; it takes 128-130 now.
 //
 // Bound: a 64 KB tile (K and V, 128 keys x 128 dims) takes an SM's share of
 // HBM 1.5 us; the products of one M-tile of 128 rows take 0.5 us of the tensor

@@ -31,8 +31,12 @@ constexpr int kPlanSmemGroups = 4096;   // group starts and smallest contexts ke
 constexpr int kTcTileNs[2][3] = {{800, 1100, 800}, {1500, 1850, 1450}};
 constexpr int kTcItemNs = 3000;
 // Two parts to a sequence mean a longer way to its result, about 4 us.  Short prefixes have to save that: 189 sequences in 7
-// groups of 16-64 shared tokens 38.0 us shared and 31.9 not, 49 in 10 of 32 27.7 and 23.7.  Long ones are quicker
-// shared however few the sequences: 4 over 512 tokens 25.7 and 31.9 us, 2 over 4416-20,064 29.8 and 42.1 (flushed L2).
+// groups of 16-64 shared tokens 38.0 us shared and 31.9 not, 49 in 10 of 32 27.7 and 23.7 (flushed L2).  Long ones are
+// shared however little they save, which pays for groups by themselves from about 256 tokens on (32 / 8 heads x 128, the
+// call replayed with and without prefix lengths; 100-300 own tokens): 4 sequences over 256 20.7 and 21.1 us, 8 over 256
+// 20.9 and 20.7, 2 over 512 17.4 and 20.5, 8 over 512 20.6 and 23.5, 8 over 1024 21.6 and 25.5.  It does not pay where such a
+// group stands among many sequences that share nothing, whose blocks keep HBM busy while shared ones come from L2: 2 over
+// 512 and 60 alone 29.3 and 27.0, 8 over 512 and 250 alone 73.4 and 71.2, 128 of 256 over 256 99.0 and 95.0.
 constexpr int64_t kLeastSavedNs = 1000;   // of every SM
 constexpr int kLongPrefix = 256;
 // CUDA cores: head_dim 64, 128; 64 keys of up to 8, 32 and 64 rows; an item's begin and end; and what sharing has to save,
@@ -138,8 +142,9 @@ __device__ __forceinline__ void load_floats(const T *p, bool aligned, float (&x)
 // (Rows of D + 4: the two rows of a warp's half warps, and the keys of its lanes, lie in different banks.)
 template <int D> constexpr int cc_smem_floats() { return kRows * (D + 4) + kKeys * (D + 4) + kKeys * D; }
 
-// Bound by what shared memory delivers (64 rows: 34 TFLOP/s, L1 76 % and FMA 53 % busy; 4 x 4 logits of a thread take 8
-// loads of 16 bytes for 64 products).  Thread (ty, tx) of 16 x 16 holds logits of rows ty * RT + i and keys tx + 16 j, and
+// Bound by what shared memory delivers (L1 76 % and FMA 53 % busy; 4 x 4 logits of a thread take 8 loads of 16 bytes for 64
+// products).  fp32, items of 64 rows, 32 / 8 heads x 128, sequences behind 8192 tokens, this kernel alone: 64 of them 213
+// us, 256 776, 40 and 44 TFLOP/s; 16 74 us; x 64, 64 of them 126 us, 34 TFLOP/s.  Thread (ty, tx) of 16 x 16 holds logits of rows ty * RT + i and keys tx + 16 j, and
 // of the outputs the same rows and dims 4 tx + 64 j + (0..3).  A row's 16 threads are half a warp.  RT = 1, 2 or 4: 16, 32
 // or 64 rows.
 template <typename T, int D, int RT>
@@ -502,7 +507,8 @@ __device__ __forceinline__ void own_share(const CcParams &p, int D, Piece piece)
     }
 }
 
-// The groups' shared tokens and, with more than kFewHeads q-heads a kv-head, the own parts.
+// The groups' shared tokens and, with more than kFewHeads q-heads a kv-head, the own parts.  The four forms of a piece under
+// the 128 registers of two CTAs an SM spill 76-132 bytes a thread in fp32 (36-160 in bf16).
 template <typename T, int D>
 __global__ void __launch_bounds__(kCcThreads, 2) shared_rows_kernel(const CcParams p) {
     extern __shared__ __align__(16) float cc_smem[];

@@ -8,9 +8,11 @@
 // through.  The row is rounded to the inputs' type and stored like
 // reshape_and_cache's, or quantised from there (q4_format.cuh).  With several
 // position axes (kAxes) pair i takes p = positions[pair_axis[i]][t], so a token's
-// cosines and sines come from up to four rows of the table: they are gathered
-// once a token into shared memory, where all its heads read them (8192 tokens 35.8
-// us against 34.6 with one axis, 256 tokens 3.1 against 2.6).
+// cosines and sines come from up to four rows of the table.  The fast kernel
+// gathers them once a token into shared memory, where all its heads read them
+// (8192 tokens 35.9-36.5 us against 34.6 with one position, 256 tokens 3.2 against
+// 2.6); the element-wise kernel looks axis, position, cosine and sine up for
+// every pair of every head.
 //
 // Bound by HBM: every row is read and written once.  A thread of the fast
 // kernel owns the two vectors of 8 dims whose elements pair up, so it needs 8
@@ -23,9 +25,9 @@
 // us from cold caches at 63 % of the issue slots: the keys' exact rotation and
 // the codes cost it half as many instructions again (29.1 M against 19.5 M);
 // fp32 69 us.  Head sizes of other lanes: 32 + 8 + 8 rows of 96 30.0 us, of 192
-// 55.4.  The element-wise kernel is far slower: with 72 or 36 of the dims turned
-// the 8192 tokens take 165 us (neighbouring pairs 171-175), into 4-bit pools
-// 440-470.
+// 55.4.  The element-wise kernel is far slower: with 36 or 72 of the 128 dims turned
+// the 8192 tokens take 163-169 us (neighbouring pairs 171-175), with three axes
+// 174-188 (190-197); into 4-bit pools 336-361 (358), with three axes 361-404.
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "q4_format.cuh"
