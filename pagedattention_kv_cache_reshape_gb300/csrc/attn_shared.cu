@@ -144,9 +144,9 @@ template <int D> constexpr int cc_smem_floats() { return kRows * (D + 4) + kKeys
 
 // Bound by what shared memory delivers (L1 76 % and FMA 53 % busy; 4 x 4 logits of a thread take 8 loads of 16 bytes for 64
 // products).  fp32, items of 64 rows, 32 / 8 heads x 128, sequences behind 8192 tokens, this kernel alone: 64 of them 213
-// us, 256 776, 40 and 44 TFLOP/s; 16 74 us; x 64, 64 of them 126 us, 34 TFLOP/s.  Thread (ty, tx) of 16 x 16 holds logits of rows ty * RT + i and keys tx + 16 j, and
-// of the outputs the same rows and dims 4 tx + 64 j + (0..3).  A row's 16 threads are half a warp.  RT = 1, 2 or 4: 16, 32
-// or 64 rows.
+// us, 256 776, 40 and 44 TFLOP/s; 16 74 us; x 64, 64 of them 126 us, 34 TFLOP/s.  Thread (ty, tx) of 16 x 16 holds logits
+// of rows ty * RT + i and keys tx + 16 j, and of the outputs the same rows and dims 4 tx + 64 j + (0..3).  A row's 16
+// threads are half a warp.  RT = 1, 2 or 4: 16, 32 or 64 rows.
 template <typename T, int D, int RT>
 __device__ __forceinline__ void cc_piece(const CcParams &p, const CcPiece &w, float *smem) {
     constexpr int kVec = 16 / sizeof(T), kKS = D + 4, kPS = kKeys + 4, kDJ = D / 64;
